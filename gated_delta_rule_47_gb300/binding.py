@@ -8,6 +8,7 @@ fallback: if ``libgdn.so`` is missing or fails to load, ``load()`` raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -21,6 +22,7 @@ GDN_F32, GDN_BF16 = 0, 1
 GDN_QK_L2NORM = 1
 GDN_PATH_SIMT = 2
 GDN_CAM_REVERSE = 4
+GDN_G_PER_HEAD = 8
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARG", 2: "GDN_ERR_UNSUPPORTED", 3: "GDN_ERR_MISALIGNED",
           4: "GDN_ERR_WORKSPACE", 5: "GDN_ERR_CUDA", 6: "GDN_ERR_TIMEOUT"}
 
@@ -31,7 +33,11 @@ EXPORTS = ("gdn_status_string", "gdn_version", "gdn_chunk_fwd_workspace_bytes", 
            "cam_prep_scan_fwd_workspace_bytes", "cam_prep_scan_fwd",
            "cam_prep_bwd", "cam_scan_bwd_workspace_bytes", "cam_scan_bwd", "gdn_chunk_bwd_workspace_bytes",
            "gdn_chunk_bwd", "deltaproduct_chunk_bwd", "masked_deltaproduct_chunk_bwd_workspace_bytes",
-           "masked_deltaproduct_chunk_bwd")
+           "masked_deltaproduct_chunk_bwd",
+           "linattn_chunk_fwd_workspace_bytes", "linattn_chunk_fwd", "linattn_chunk_bwd_workspace_bytes",
+           "linattn_chunk_bwd", "linattn_step", "gdn_step", "rms_norm_fwd", "rms_norm_bwd_workspace_bytes",
+           "rms_norm_bwd", "state_pool_copy", "state_pool_fork_workspace_bytes", "state_pool_fork", "state_pool_free",
+           "state_pool_compact_workspace_bytes", "state_pool_compact")
 
 _lock = threading.Lock()
 _lib = None
@@ -97,6 +103,29 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.cam_scan_fwd.restype = i
         lib.cam_prep_fwd.argtypes = [vp] * 9 + [f] + [vp] * 5 + [i] * 4 + [f, f, i, vp]
         lib.cam_prep_fwd.restype = i
+        ll = ctypes.c_longlong
+        for name in ("linattn_chunk_fwd_workspace_bytes", "linattn_chunk_bwd_workspace_bytes"):
+            getattr(lib, name).argtypes = [i] * 8 + [u, i]
+            getattr(lib, name).restype = sz
+        lib.linattn_chunk_fwd.argtypes = [vp] * 9 + [i] * 7 + [f, u, i, vp, sz, vp]
+        lib.linattn_chunk_bwd.argtypes = [vp] * 14 + [i] * 7 + [f, u, i, vp, sz, vp]
+        lib.linattn_step.argtypes = [vp] * 8 + [i] * 6 + [f, u, i, vp]
+        lib.gdn_step.argtypes = [vp] * 9 + [i] * 6 + [f, u, i, vp]
+        lib.rms_norm_fwd.argtypes = [vp] * 6 + [ll, i, i, f, i, i, vp]
+        lib.rms_norm_bwd_workspace_bytes.argtypes = [ll, i]
+        lib.rms_norm_bwd.argtypes = [vp] * 6 + [ll, i, f, i, vp, sz, vp]
+        lib.state_pool_copy.argtypes = [vp, i, i, ll, vp, vp, i, vp]
+        lib.state_pool_fork_workspace_bytes.argtypes = [i, i]
+        lib.state_pool_fork.argtypes = [vp, i, i, ll, vp, vp, vp, i, vp, sz, vp]
+        lib.state_pool_free.argtypes = [vp, i, vp, i, vp]
+        lib.state_pool_compact_workspace_bytes.argtypes = [i]
+        lib.state_pool_compact.argtypes = [vp, i, i, ll, vp, vp, vp, vp, sz, vp]
+        for name in ("rms_norm_bwd_workspace_bytes", "state_pool_fork_workspace_bytes",
+                     "state_pool_compact_workspace_bytes"):
+            getattr(lib, name).restype = sz
+        for name in ("linattn_chunk_fwd", "linattn_chunk_bwd", "linattn_step", "gdn_step", "rms_norm_fwd",
+                     "rms_norm_bwd", "state_pool_copy", "state_pool_fork", "state_pool_free", "state_pool_compact"):
+            getattr(lib, name).restype = i
         lib.gdn_get_device_error.argtypes = [vp]
         lib.gdn_get_device_error.restype = i
         lib.gdn_set_wait_limit.argtypes = [ctypes.c_ulonglong]
@@ -583,6 +612,334 @@ def cam_prep_bwd(q_raw, k_raw, proj_q, proj_kv, dq_out, dk_out, dv_out, dk_pre_s
                              _ptr(outs[2]), B, N, H, D, float(k_scale), float(eps), code, _stream(stream))
     _raise("cam_prep_bwd", st)
     return outs
+
+
+# ------------------------------------------------- around a linear-attention layer
+_NO_BYTES = ctypes.c_size_t(-1).value
+
+
+def _strided(t, name, shape, dtype):
+    """As _check for a tensor whose last dimension is contiguous and whose
+    other strides are multiples of 16 bytes."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    size = t.element_size()
+    for n, s in zip(t.shape[:-1], t.stride()[:-1]):
+        if n > 1 and s * size % 16 != 0:
+            raise ValueError(f"{name}'s strides {t.stride()} must be multiples of 16 bytes")
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t
+
+
+def _gates(g, shape):
+    """Checks log-decays [B,H,T] (any strides) or [H]; whether they are per head."""
+    per_head = isinstance(g, torch.Tensor) and g.dim() == 1
+    if per_head:
+        _check(g, "g", (shape[1],), torch.float32)
+    else:
+        if not isinstance(g, torch.Tensor) or not g.is_cuda:
+            raise TypeError("g must be a CUDA tensor")
+        if tuple(g.shape) != shape:
+            raise ValueError(f"g has shape {tuple(g.shape)}, expected {shape} or ({shape[1]},)")
+        if g.dtype != torch.float32:
+            raise TypeError(f"g must be torch.float32, got {g.dtype}")
+    return per_head
+
+
+def _steps(*tensors):
+    """The strides array of linattn_chunk_*: (batch, head, token) of each; a
+    dimension of one element has none that matters."""
+    out = []
+    for t in tensors:
+        if t.dim() == 1:
+            out += (0, 0, 0)
+        else:
+            out += [s if n > 1 else 0 for n, s in zip(t.shape[:3], t.stride())]
+    return (ctypes.c_longlong * 15)(*out)
+
+
+def _on(stream):
+    """Allocations of a call belong to the stream that it runs on."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def _linattn_sizes(q, k, v, g, cu_seqlens, initial_state):
+    if not isinstance(q, torch.Tensor) or not isinstance(v, torch.Tensor) or q.dim() != 4 or v.dim() != 4:
+        raise TypeError("q, k and v must be [B,heads,T,D] CUDA tensors")
+    B, Hk, T, Dk = q.shape
+    H, Dv = v.shape[1], v.shape[3]
+    code = _dtype_code(q)
+    _strided(q, "q", (B, Hk, T, Dk), q.dtype)
+    _strided(k, "k", (B, Hk, T, Dk), q.dtype)
+    _strided(v, "v", (B, H, T, Dv), q.dtype)
+    per_head = _gates(g, (B, H, T))
+    if Hk == 0 or H % Hk != 0:
+        raise ValueError(f"{Hk} query / key heads do not divide {H} value heads")
+    n_seq = B
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must hold at least two offsets")
+        _check(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32)
+        if B != 1:
+            raise ValueError("packed sequences (cu_seqlens) lie in one row: B must be 1")
+        n_seq = cu_seqlens.numel() - 1
+    if initial_state is not None:
+        _check(initial_state, "initial_state", (n_seq, H, Dk, Dv), torch.float32)
+    return B, H, Hk, T, Dk, Dv, n_seq, code, per_head
+
+
+def _scratch(fn, need, workspace, device):
+    """The caller's workspace or a new one of `need` bytes."""
+    if need == _NO_BYTES:
+        raise ValueError(f"sizes rejected by {fn}")
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def linattn_chunk_fwd(q, k, v, g, initial_state=None, output_final_state=False, cu_seqlens=None, scale=1.0, o=None,
+                      workspace=None, stream=None, simt=False):
+    """Linear attention with a decay for each head over prompts.  q, k
+    [B,Hk,T,Dk]; v [B,H,T,Dv] (all bf16 or all fp32, last dimension
+    contiguous); g [B,H,T] or [H] fp32 log-decays.  cu_seqlens: int32 CUDA
+    offsets of sequences packed into one row (a token-major [T,H,D] tensor x
+    goes in as x.unsqueeze(0).transpose(1, 2)).  initial_state
+    [sequences,H,Dk,Dv] fp32.  Returns (o, final_state or None); o has v's
+    strides unless it is given."""
+    B, H, Hk, T, Dk, Dv, n_seq, code, per_head = _linattn_sizes(q, k, v, g, cu_seqlens, initial_state)
+    lib = load()
+    flags = (GDN_G_PER_HEAD if per_head else 0) | (GDN_PATH_SIMT if simt else 0)
+    with _on(stream):
+        if o is None:
+            o = torch.empty_like(v) if not _overlaps(v) else torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        _strided(o, "o", (B, H, T, Dv), q.dtype)
+        sf = torch.empty(n_seq, H, Dk, Dv, dtype=torch.float32, device=q.device) if output_final_state else None
+        need = lib.linattn_chunk_fwd_workspace_bytes(B, H, Hk, T, Dk, Dv, n_seq, cu_seqlens is not None, flags, code)
+        workspace, ws_bytes = _scratch("linattn_chunk_fwd", need, workspace, q.device)
+    st = lib.linattn_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(initial_state), _ptr(o), _ptr(sf),
+                               _ptr(cu_seqlens), _steps(q, k, v, o, g), n_seq, B, H, Hk, T, Dk, Dv, float(scale), flags,
+                               code, _ptr(workspace), ws_bytes, _stream(stream))
+    _raise("linattn_chunk_fwd", st)
+    return o, sf
+
+
+def _overlaps(t):
+    """Whether elements share memory (an expanded tensor)."""
+    return any(s == 0 and n > 1 for n, s in zip(t.shape, t.stride()))
+
+
+def linattn_chunk_bwd(q, k, v, g, dout, initial_state=None, dfinal_state=None, cu_seqlens=None, scale=1.0,
+                      workspace=None, stream=None, simt=False):
+    """Backward of linattn_chunk_fwd.  dout [B,H,T,Dv], dfinal_state
+    [sequences,H,Dk,Dv] fp32.  Returns (dq, dk, dv, dg, dinitial_state or
+    None): the first three in the tensors' type, dg fp32 in g's shape (its sum
+    over batch and tokens for g [H])."""
+    B, H, Hk, T, Dk, Dv, n_seq, code, per_head = _linattn_sizes(q, k, v, g, cu_seqlens, initial_state)
+    _strided(dout, "dout", (B, H, T, Dv), q.dtype)
+    if dfinal_state is not None:
+        _check(dfinal_state, "dfinal_state", (n_seq, H, Dk, Dv), torch.float32)
+    lib = load()
+    flags = (GDN_G_PER_HEAD if per_head else 0) | (GDN_PATH_SIMT if simt else 0)
+    with _on(stream):
+        # gradients take their tensors' strides, so those may not overlap
+        q, k, v, g = (t.contiguous() if _overlaps(t) else t for t in (q, k, v, g))
+        dq, dk, dv, dg = (torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device) for t in (q, k, v, g))
+        ds0 = torch.empty_like(initial_state) if initial_state is not None else None
+        need = lib.linattn_chunk_bwd_workspace_bytes(B, H, Hk, T, Dk, Dv, n_seq, cu_seqlens is not None, flags, code)
+        workspace, ws_bytes = _scratch("linattn_chunk_bwd", need, workspace, q.device)
+    st = lib.linattn_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(initial_state), _ptr(dout), _ptr(dfinal_state),
+                               _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(ds0), _ptr(cu_seqlens),
+                               _steps(q, k, v, dout, g), n_seq, B, H, Hk, T, Dk, Dv, float(scale), flags, code,
+                               _ptr(workspace), ws_bytes, _stream(stream))
+    _raise("linattn_chunk_bwd", st)
+    return dq, dk, dv, dg, ds0
+
+
+def _step(fn_name, q, k, v, beta, g, state, slots, state_out, scale, l2norm, o, stream):
+    B, Hk, Dk = q.shape
+    H, Dv = v.shape[1], v.shape[2]
+    n_slots = state.shape[0]
+    dt = q.dtype
+    code = _dtype_code(q)
+    _check(q, "q", (B, Hk, Dk), dt)
+    _check(k, "k", (B, Hk, Dk), dt)
+    _check(v, "v", (B, H, Dv), dt)
+    if Hk == 0 or H % Hk != 0:
+        raise ValueError(f"{Hk} query / key heads do not divide {H} value heads")
+    per_head = g.dim() == 1
+    _check(g, "g", (H,) if per_head else (B, H), torch.float32)
+    _check(state, "state", (n_slots, H, Dk, Dv), torch.float32)
+    if state_out is None:
+        state_out = state
+    elif state_out is not state:
+        _check(state_out, "state_out", (n_slots, H, Dk, Dv), torch.float32)
+    if slots is not None:
+        _check(slots, "slots", (B,), torch.int32)
+    elif B > n_slots:
+        raise ValueError(f"{B} rows but {n_slots} pages")
+    if o is None:
+        with _on(stream):
+            o = torch.empty_like(v)
+    else:
+        _check(o, "o", (B, H, Dv), dt)
+    flags = (GDN_G_PER_HEAD if per_head else 0) | (GDN_QK_L2NORM if l2norm else 0)
+    rest = (g.data_ptr(), state.data_ptr(), state_out.data_ptr(), _ptr(slots), o.data_ptr(), B, H, Hk, Dk, Dv, n_slots,
+            float(scale), flags, code, _stream(stream))
+    if beta is None:
+        st = load().linattn_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), *rest)
+    else:
+        _check(beta, "beta", (B, H), dt)
+        st = load().gdn_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), beta.data_ptr(), *rest)
+    _raise(fn_name, st)
+    return o
+
+
+def linattn_step(q, k, v, g, state, slots=None, state_out=None, scale=1.0, o=None, stream=None):
+    """One token of linear attention with a decay for each head.  q, k
+    [B,Hk,Dk]; v [B,H,Dv]; g [B,H] or [H] fp32; state [slots,H,Dk,Dv] fp32,
+    updated in place unless state_out is given; slots int32 [B]: each row's
+    page, -1 for an idle row (o = 0).  Returns o [B,H,Dv]."""
+    return _step("linattn_step", q, k, v, None, g, state, slots, state_out, scale, False, o, stream)
+
+
+def gdn_step(q, k, v, beta, g, state, slots=None, state_out=None, scale=1.0, l2norm=False, o=None, stream=None):
+    """One token of the gated delta rule (gdn_chunk_fwd's recurrence) against a
+    pool of states; beta [B,H], the rest as linattn_step."""
+    return _step("gdn_step", q, k, v, beta, g, state, slots, state_out, scale, l2norm, o, stream)
+
+
+def rms_norm_fwd(x, weight=None, residual=None, eps=1e-6, out_dtype=None, group=0, stream=None):
+    """h = x + residual and its root-mean-square norm over the last dimension.
+    out_dtype: None (x's) or torch.float8_e4m3fn, then with scales [...,C/group]
+    (group 32, 64 or 128) or [...,1] (group 0: one a row).  Returns (y, scales or
+    None, h); h is x itself without a residual."""
+    C = x.shape[-1]
+    code = _dtype_code(x)
+    _check(x, "x", x.shape)
+    if residual is not None:
+        _check(residual, "residual", x.shape, x.dtype)
+    if weight is not None:
+        _check(weight, "weight", (C,), torch.float32)
+    e4m3 = out_dtype is torch.float8_e4m3fn
+    if not e4m3 and out_dtype not in (None, x.dtype):
+        raise TypeError(f"out_dtype must be {x.dtype} or torch.float8_e4m3fn, got {out_dtype}")
+    if group and (not e4m3 or group not in (32, 64, 128) or C % group):
+        raise ValueError(f"group {group}: 32, 64 or 128 dividing the last dimension, with an e4m3 output")
+    scales = None
+    with _on(stream):
+        y = torch.empty_like(x, dtype=out_dtype)
+        if e4m3:
+            scales = torch.empty((*x.shape[:-1], C // group if group else 1), dtype=torch.float32, device=x.device)
+        h = torch.empty_like(x) if residual is not None else x
+    rows = x.numel() // C if C else 0
+    st = load().rms_norm_fwd(x.data_ptr(), _ptr(residual), _ptr(weight), y.data_ptr(), _ptr(scales),
+                             h.data_ptr() if residual is not None else None, rows, C, group, float(eps), int(e4m3),
+                             code, _stream(stream))
+    _raise("rms_norm_fwd", st)
+    return y, scales, h
+
+
+def rms_norm_bwd(dy, h, weight=None, dresidual=None, eps=1e-6, workspace=None, stream=None):
+    """Backward of rms_norm_fwd at the h that it returned: (dx, dweight [C]
+    fp32).  dresidual: the gradient that reaches h past the norm; dx is also
+    the residual's gradient."""
+    C = h.shape[-1]
+    code = _dtype_code(h)
+    _check(h, "h", h.shape)
+    _check(dy, "dy", h.shape, h.dtype)
+    if dresidual is not None:
+        _check(dresidual, "dresidual", h.shape, h.dtype)
+    if weight is not None:
+        _check(weight, "weight", (C,), torch.float32)
+    rows = h.numel() // C if C else 0
+    lib = load()
+    with _on(stream):
+        dx = torch.empty_like(h)
+        dw = torch.empty(C, dtype=torch.float32, device=h.device)
+        workspace, ws_bytes = _scratch("rms_norm_bwd", lib.rms_norm_bwd_workspace_bytes(rows, C), workspace, h.device)
+    st = lib.rms_norm_bwd(dy.data_ptr(), h.data_ptr(), _ptr(weight), _ptr(dresidual), dx.data_ptr(), dw.data_ptr(), rows,
+                          C, float(eps), code, _ptr(workspace), ws_bytes, _stream(stream))
+    _raise("rms_norm_bwd", st)
+    return dx, dw
+
+
+def _pool(pool):
+    """(layers, slots, page bytes) of a contiguous [layers,slots,...] pool."""
+    if not isinstance(pool, torch.Tensor) or not pool.is_cuda:
+        raise TypeError("pool must be a CUDA tensor")
+    if pool.dim() < 2 or not pool.is_contiguous():
+        raise ValueError("pool must be a contiguous [layers,slots,...] tensor")
+    layers, n_slots = pool.shape[:2]
+    page = pool[0, 0].numel() * pool.element_size() if layers and n_slots else 0
+    if page % 16:
+        raise ValueError(f"a page of {page} bytes is not a multiple of 16")
+    return layers, n_slots, page
+
+
+def _slots(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        raise TypeError(f"{name} must be a one-dimensional CUDA tensor")
+    _check(t, name, t.shape, torch.int32)
+    return t.numel()
+
+
+def state_pool_copy(pool, src, dst, stream=None):
+    """pool[:, dst[i]] = pool[:, src[i]] (zeros for src -1); indices out of
+    range are skipped.  Destinations are distinct and no one's source."""
+    layers, n_slots, page = _pool(pool)
+    n = _slots(src, "src")
+    if _slots(dst, "dst") != n:
+        raise ValueError(f"{n} sources but {dst.numel()} destinations")
+    _raise("state_pool_copy", load().state_pool_copy(pool.data_ptr(), layers, n_slots, page, src.data_ptr(),
+                                                     dst.data_ptr(), n, _stream(stream)))
+
+
+def state_pool_fork(pool, live, parents, stream=None):
+    """Gives each parent (a live slot, or -1 for a new request's page of zeros)
+    the lowest free slot, with a copy of its page in every layer of pool
+    [layers,slots,...].  live uint8 [slots] is updated.  Returns the children,
+    int32, -1 where the parent is not live or no slot is left."""
+    layers, n_slots, page = _pool(pool)
+    _check(live, "live", (n_slots,), torch.uint8)
+    n = _slots(parents, "parents")
+    lib = load()
+    with _on(stream):
+        children = torch.empty_like(parents)
+        ws, ws_bytes = _scratch("state_pool_fork", lib.state_pool_fork_workspace_bytes(n_slots, n), None, pool.device)
+    _raise("state_pool_fork", lib.state_pool_fork(pool.data_ptr(), layers, n_slots, page, live.data_ptr(),
+                                                  parents.data_ptr(), children.data_ptr(), n, _ptr(ws), ws_bytes,
+                                                  _stream(stream)))
+    return children
+
+
+def state_pool_free(live, slots, stream=None):
+    """Marks slots (int32; out-of-range ones are skipped) free in live uint8."""
+    _check(live, "live", live.shape, torch.uint8)
+    n = _slots(slots, "slots")
+    _raise("state_pool_free", load().state_pool_free(live.data_ptr(), live.numel(), slots.data_ptr(), n,
+                                                     _stream(stream)))
+
+
+def state_pool_compact(pool, live, stream=None):
+    """Moves the live pages of pool [layers,slots,...] into its first slots and
+    updates live.  Returns (remap, n_live): int32 [slots], each slot's new
+    place or -1, and the count, int32 [1], on the device."""
+    layers, n_slots, page = _pool(pool)
+    _check(live, "live", (n_slots,), torch.uint8)
+    lib = load()
+    with _on(stream):
+        remap = torch.empty(n_slots, dtype=torch.int32, device=pool.device)
+        n_live = torch.empty(1, dtype=torch.int32, device=pool.device)
+        ws, ws_bytes = _scratch("state_pool_compact", lib.state_pool_compact_workspace_bytes(n_slots), None, pool.device)
+    _raise("state_pool_compact", lib.state_pool_compact(pool.data_ptr(), layers, n_slots, page, live.data_ptr(),
+                                                        remap.data_ptr(), n_live.data_ptr(), _ptr(ws), ws_bytes,
+                                                        _stream(stream)))
+    return remap, n_live
 
 
 def device_error(stream=None) -> int:

@@ -6,11 +6,9 @@
 // Nsight Compute or Nsight Systems is attached), so a profiler can select a
 // call's kernels by range (ncu --nvtx --nvtx-include "gdn_chunk_fwd/").
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
-#include <stdint.h>
-
 #include <atomic>
 
+#include "api_util.h"
 #include "gdn_internal.h"
 
 namespace gdn {
@@ -22,15 +20,8 @@ void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
 namespace {
 
-// An NVTX range over the enclosing scope.
-struct Range {
-    explicit Range(const char *name) { nvtxRangePushA(name); }
-    ~Range() { nvtxRangePop(); }
-    Range(const Range &) = delete;
-    Range &operator=(const Range &) = delete;
-};
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+using gdn::Range;
+using gdn::aligned16;
 
 int check_scan(const gdn::ScanArgs &a) {
     if (a.B < 0 || a.H < 0 || a.T < 0 || a.r < 1) return GDN_ERR_INVALID_ARG;

@@ -1,0 +1,619 @@
+// linattn.cu -- linear attention with a decay for each head over whole
+// prompts, forward and backward, on the CUDA cores in fp32.
+//
+//   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+//
+// Chunks of 64 tokens.  With c_t the sum of a chunk's log-decays up to token
+// t, S the state that enters the chunk and G = c_63:
+//
+//   o_t  = scale (e^{c_t} S^T q_t + sum_{s<=t} e^{c_t - c_s} (q_t . k_s) v_s)
+//   S'   = e^G S + sum_t e^{G - c_t} k_t v_t^T
+//
+// so a call is three launches: every chunk's own share of the state (a product
+// over its tokens), the scan of these over a sequence's chunks, and every
+// chunk's outputs.  The backward has the same shape twice, forwards for S and
+// backwards for R, the gradient of the state that leaves a chunk,
+//
+//   R_before = e^G R + scale sum_t e^{c_t} q_t do_t^T,
+//
+// and then, with P_ts = scale e^{c_t-c_s} (q_t . k_s), N_ts = scale e^{c_t-c_s}
+// (do_t . v_s) for s <= t,
+//
+//   dq_t = scale e^{c_t} S do_t + sum_s N_ts k_s
+//   dk_s = e^{G-c_s} R v_s + sum_t N_ts q_t
+//   dv_s = e^{G-c_s} R^T k_s + sum_t P_ts do_t
+//   dg_u = sum_{t>=u} (q_t . dq_t - k_t . dk_t) + sum_t k_t . (R's part of dk_t) + e^G <R, S>
+//
+// (the last line's sums of R's part over t >= u cancel and are left out).
+#include <cuda_bf16.h>
+
+#include "gdn_internal.h"
+#include "linattn.cuh"
+#include "simt_tile.cuh"
+
+namespace gdn {
+namespace la {
+namespace {
+
+constexpr int kC = 64;
+constexpr int kTableThreads = 1024;
+
+// One CTA: sequence s's first chunk from the running count, then every chunk's
+// entry by a search for its sequence.  Bad offsets are cut to [0, T] and to
+// the tables' room, so that no entry leads outside the tensors.
+__global__ void __launch_bounds__(kTableThreads) table_kernel(const int *cu, int n_seq, int T, int C, int4 *chunks,
+                                                              int4 *seqs, int bound) {
+    __shared__ int sums[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int first = 0;
+    for (int s0 = 0; s0 < n_seq; s0 += kTableThreads) {
+        const int s = s0 + threadIdx.x;
+        int start = 0, len = 0;
+        if (s < n_seq) {
+            start = min(max(cu[s], 0), T);
+            len = max(min(cu[s + 1], T) - start, 0);
+        }
+        const int n = (int)(((long long)len + C - 1) / C);
+        int y = n;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int t = __shfl_up_sync(~0u, y, m);
+            if (lane >= m) y += t;
+        }
+        __syncthreads();
+        if (lane == 31) sums[warp] = y;
+        __syncthreads();
+        if (warp == 0) {
+            int z = sums[lane];
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int t = __shfl_up_sync(~0u, z, m);
+                if (lane >= m) z += t;
+            }
+            sums[lane] = z;
+        }
+        __syncthreads();
+        const int at = first + y - n + (warp ? sums[warp - 1] : 0);
+        first += sums[31];
+        if (s < n_seq) seqs[s] = make_int4(min(at, bound), max(min(n, bound - at), 0), start, len);
+    }
+    __syncthreads();
+    const int count = min(first, bound);
+    const int head = min(max(cu[0], 0), T), tail = min(max(cu[n_seq], 0), T);
+    const int fill0 = (head + C - 1) / C;
+    for (int ci = threadIdx.x; ci < bound; ci += kTableThreads) {
+        int4 e = make_int4(0, 0, 0, -1);
+        if (ci >= count) {  // fillers, as far as there are any
+            const int f = ci - count;
+            const long long t = f < fill0 ? (long long)f * C : tail + (long long)(f - fill0) * C;
+            const int end = f < fill0 ? head : T;
+            if (t < end) e = make_int4(0, (int)t, min(C, end - (int)t), -1);
+        } else {
+            int lo = 0, hi = n_seq - 1;  // the last sequence whose first chunk is not after ci
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (seqs[mid].x <= ci) lo = mid;
+                else hi = mid - 1;
+            }
+            const int4 q = seqs[lo];
+            const int t = (ci - q.x) * C;
+            e = make_int4(0, q.z + t, max(min(C, q.w - t), 0), lo);
+        }
+        chunks[ci] = e;
+    }
+}
+
+// dst[b,hk,t,:] = sum of src[b,h,t,:] over hk's value heads, in their order.
+template <typename T>
+__global__ void group_sum_kernel(const float4 *src, T *dst, Strides s, int H, int Hk, int T_len, int D) {
+    const int per = D / 4, rep = H / Hk;
+    const long long n = (long long)T_len * per;
+    const int hk = blockIdx.y, b = blockIdx.z;
+    for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
+        const int t = (int)(i / per), c = (int)(i - (long long)t * per);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = 0; r < rep; ++r) {
+            const float4 y = src[(((long long)b * H + hk * rep + r) * T_len + t) * per + c];
+            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        }
+        T *p = at(dst, s, b, hk, t) + 4 * c;
+        tile::st_f(p, x.x), tile::st_f(p + 1, x.y), tile::st_f(p + 2, x.z), tile::st_f(p + 3, x.w);
+    }
+}
+
+__global__ void __launch_bounds__(1024) head_sum_kernel(const float *src, float *dg, int B, int H, int T) {
+    __shared__ double s[32];
+    const int h = blockIdx.x;
+    double x = 0.;
+    for (int b = 0; b < B; ++b) {
+        const float *p = src + ((long long)b * H + h) * T;
+        float part = 0.f;
+        int n = 0;
+        for (int t = threadIdx.x; t < T; t += 1024) {
+            part += p[t];
+            if (++n == 16) x += part, part = 0.f, n = 0;
+        }
+        x += part;
+    }
+#pragma unroll
+    for (int m = 16; m; m >>= 1) x += __shfl_xor_sync(~0u, x, m);
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        x = s[threadIdx.x];
+#pragma unroll
+        for (int m = 16; m; m >>= 1) x += __shfl_xor_sync(~0u, x, m);
+        if (threadIdx.x == 0) dg[h] = (float)x;
+    }
+}
+
+// ------------------------------------------------------------ chunk kernels
+template <int D>
+constexpr int ld() { return D + 1; }
+
+// Rows t < len of a strided [T][D] slice into a [64][D + 1] fp32 tile, zeros after them.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void load_tile(float *dst, const T *src, long long step, int len) {
+    for (int i = threadIdx.x; i < kC * D; i += NT) {
+        const int t = i / D, d = i % D;
+        dst[t * ld<D>() + d] = t < len ? tile::ld_f(src + t * step + d) : 0.f;
+    }
+}
+
+// Zeros in rows t < len of a strided [T][D] slice (tokens of no sequence).
+template <typename T, int D, int NT>
+__device__ __forceinline__ void zero_rows(T *dst, long long step, int len) {
+    for (int i = threadIdx.x; i < len * D; i += NT) tile::st_f(dst + (i / D) * step + i % D, 0.f);
+}
+
+__device__ __forceinline__ const float *gate_ptr(const LinAttnArgs &a, const Chunk &c, int h) {
+    return (a.flags & GDN_G_PER_HEAD) ? a.g + h : at(a.g, a.sg, c.row, h, c.t0);
+}
+
+// A chunk's share of the state that leaves it, sum_t e^{G-c_t} k_t v_t^T, or
+// (REV) of the gradient before it, scale sum_t e^{c_t} q_t do_t^T.
+// Grid (chunks, H); U [chunk][H][DK][DV], decay [chunk][H] = e^G.
+template <typename T, int DK, int DV, bool REV>
+__global__ void __launch_bounds__(256) share_kernel(LinAttnArgs a, View v, float *U, float *decay) {
+    extern __shared__ float sm[];
+    float *X = sm, *Y = X + kC * ld<DK>(), *hi = Y + kC * ld<DV>(), *lo = hi + kC, *te = lo + kC;
+    const int ci = blockIdx.x, h = blockIdx.y;
+    const Chunk c = chunk_at<kC>(v, a.T, ci);
+    if (c.len <= 0 || c.seq < 0) return;
+    const int hk = h / (a.H / a.Hk);
+    if (threadIdx.x < 32)
+        gates<kC>(gate_ptr(a, c, h), a.sg.t, c.len, a.flags & GDN_G_PER_HEAD, hi, lo, te);
+    const T *xp = REV ? at(static_cast<const T *>(a.q), a.sq, c.row, hk, c.t0) : at(static_cast<const T *>(a.k), a.sk, c.row, hk, c.t0);
+    const T *yp = REV ? at(static_cast<const T *>(a.dout), a.sdo, c.row, h, c.t0) : at(static_cast<const T *>(a.v), a.sv, c.row, h, c.t0);
+    load_tile<T, DK, 256>(X, xp, REV ? a.sq.t : a.sk.t, c.len);
+    load_tile<T, DV, 256>(Y, yp, REV ? a.sdo.t : a.sv.t, c.len);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kC * DK; i += 256) {
+        const int t = i / DK;
+        X[t * ld<DK>() + i % DK] *= REV ? a.scale * expf(hi[t]) : expf(te[t]);
+    }
+    __syncthreads();
+    float acc[DK / 16][DV / 16];
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < DV / 16; ++j) acc[i][j] = 0.f;
+    tile::mm<256, DK / 16, DV / 16>(acc, X, 1, ld<DK>(), Y, ld<DV>(), 1, kC);
+    float *u = U + ((long long)ci * a.H + h) * DK * DV;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < DV / 16; ++j) u[(ty + 16 * i) * DV + tx + 16 * j] = acc[i][j];
+    if (threadIdx.x == 0) decay[(long long)ci * a.H + h] = expf(hi[c.len - 1]);
+}
+
+// Turns the shares of a sequence's chunks into the states that enter them
+// (forwards, from s0; the last one to sf), or (REV) into the gradients of the
+// states that leave them (backwards, from dsf; the last one to ds0).
+// Grid (page / 1024, H, n_seq), a thread for four elements.
+template <bool REV>
+__global__ void __launch_bounds__(256) scan_kernel(View v, float *U, const float *decay, const float *start,
+                                                   float *end, int H, int page) {
+    const int e = (blockIdx.x * 256 + threadIdx.x) * 4, h = blockIdx.y, s = blockIdx.z;
+    if (e >= page) return;
+    const int2 q = seq_at(v, s);
+    const long long mine = ((long long)s * H + h) * page + e;
+    float4 x = start ? *reinterpret_cast<const float4 *>(start + mine) : make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int A = 4;  // chunks read ahead
+    float4 u[A];
+    float d[A];
+    auto slot = [&](int i) { return ((long long)(q.x + (REV ? q.y - 1 - i : i)) * H + h); };
+#pragma unroll
+    for (int j = 0; j < A; ++j)
+        if (j < q.y) {
+            u[j] = *reinterpret_cast<const float4 *>(U + slot(j) * page + e);
+            d[j] = decay[slot(j)];
+        }
+    for (int i0 = 0; i0 < q.y; i0 += A) {
+#pragma unroll
+        for (int j = 0; j < A; ++j) {
+            if (i0 + j >= q.y) break;
+            const float4 w = u[j];
+            const float f = d[j];
+            if (i0 + j + A < q.y) {
+                u[j] = *reinterpret_cast<const float4 *>(U + slot(i0 + j + A) * page + e);
+                d[j] = decay[slot(i0 + j + A)];
+            }
+            *reinterpret_cast<float4 *>(U + slot(i0 + j) * page + e) = x;
+            x.x = fmaf(f, x.x, w.x), x.y = fmaf(f, x.y, w.y), x.z = fmaf(f, x.z, w.z), x.w = fmaf(f, x.w, w.w);
+        }
+    }
+    if (end) *reinterpret_cast<float4 *>(end + mine) = x;
+}
+
+constexpr int kT = tile::kThr;  // 512
+
+// A chunk's outputs.  Grid (chunks, H); S as scan_kernel left it.
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(kT) out_kernel(LinAttnArgs a, View v, const float *S) {
+    extern __shared__ float sm[];
+    float *Q = sm, *K = Q + kC * ld<DK>(), *V = K + kC * ld<DK>(), *P = V + kC * ld<DV>();
+    float *hi = P + kC * (kC + 1), *lo = hi + kC, *te = lo + kC;
+    const int ci = blockIdx.x, h = blockIdx.y;
+    const Chunk c = chunk_at<kC>(v, a.T, ci);
+    if (c.len <= 0) return;
+    if (c.seq < 0) {
+        zero_rows<T, DV, kT>(at(static_cast<T *>(a.o), a.so, c.row, h, c.t0), a.so.t, c.len);
+        return;
+    }
+    const int hk = h / (a.H / a.Hk);
+    if (threadIdx.x < 32)
+        gates<kC>(gate_ptr(a, c, h), a.sg.t, c.len, a.flags & GDN_G_PER_HEAD, hi, lo, te);
+    load_tile<T, DK, kT>(Q, at(static_cast<const T *>(a.q), a.sq, c.row, hk, c.t0), a.sq.t, c.len);
+    load_tile<T, DK, kT>(K, at(static_cast<const T *>(a.k), a.sk, c.row, hk, c.t0), a.sk.t, c.len);
+    load_tile<T, DV, kT>(V, at(static_cast<const T *>(a.v), a.sv, c.row, h, c.t0), a.sv.t, c.len);
+    __syncthreads();
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    float p[2][4] = {};
+    tile::mm<kT, 2, 4>(p, Q, ld<DK>(), 1, K, 1, ld<DK>(), DK);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int t = ty + 32 * i, s = tx + 16 * j;
+            P[t * (kC + 1) + s] = s <= t ? p[i][j] * decay_between(hi[t], lo[t], hi[s], lo[s]) : 0.f;
+        }
+    float o[2][DV / 16];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < DV / 16; ++j) o[i][j] = 0.f;
+    tile::mm<kT, 2, DV / 16>(o, Q, ld<DK>(), 1, S + ((long long)ci * a.H + h) * DK * DV, DV, 1, DK);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < DV / 16; ++j) o[i][j] *= expf(hi[ty + 32 * i]);
+    __syncthreads();
+    tile::mm<kT, 2, DV / 16>(o, P, kC + 1, 1, V, ld<DV>(), 1, kC);
+    T *out = at(static_cast<T *>(a.o), a.so, c.row, h, c.t0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < DV / 16; ++j)
+            if (ty + 32 * i < c.len) tile::st_f(out + (ty + 32 * i) * a.so.t + tx + 16 * j, a.scale * o[i][j]);
+}
+
+// Sum over the 16 threads of a tile row; every one of them gets it.
+__device__ __forceinline__ float row16(float x) {
+#pragma unroll
+    for (int m = 8; m; m >>= 1) x += __shfl_xor_sync(~0u, x, m);
+    return x;
+}
+
+// A chunk's gradients.  Grid (chunks, H); S and R as the scans left them.
+// dq and dk go to dqh, dkh [B,H,T,DK] fp32 where value heads share them.
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(kT) grad_kernel(LinAttnArgs a, View v, const float *S, const float *R, float *dqh,
+                                                  float *dkh, float *dgt, Strides sdg) {
+    extern __shared__ float sm[];
+    float *Q = sm, *K = Q + kC * ld<DK>(), *V = K + kC * ld<DK>(), *O = V + kC * ld<DV>();
+    float *P = O + kC * ld<DV>(), *N = P + kC * (kC + 1), *slab = N + kC * (kC + 1);  // slab [DK][65]
+    float *hi = slab + DK * 65, *lo = hi + kC, *te = lo + kC, *xq = te + kC, *xk = xq + kC, *xr = xk + kC, *red = xr + kC;
+    const int ci = blockIdx.x, h = blockIdx.y;
+    const Chunk c = chunk_at<kC>(v, a.T, ci);
+    if (c.len <= 0) return;
+    const int hk = h / (a.H / a.Hk);
+    const bool shared = a.H != a.Hk;
+    const long long out_row = (((long long)c.row * a.H + h) * a.T + c.t0) * DK;
+    if (c.seq < 0) {
+        if (shared) {
+            zero_rows<float, DK, kT>(dqh + out_row, DK, c.len);
+            zero_rows<float, DK, kT>(dkh + out_row, DK, c.len);
+        } else {
+            zero_rows<T, DK, kT>(at(static_cast<T *>(a.dq), a.sq, c.row, hk, c.t0), a.sq.t, c.len);
+            zero_rows<T, DK, kT>(at(static_cast<T *>(a.dk), a.sk, c.row, hk, c.t0), a.sk.t, c.len);
+        }
+        zero_rows<T, DV, kT>(at(static_cast<T *>(a.dv), a.sv, c.row, h, c.t0), a.sv.t, c.len);
+        zero_rows<float, 1, kT>(at(dgt, sdg, c.row, h, c.t0), sdg.t, c.len);
+        return;
+    }
+    if (threadIdx.x < 32)
+        gates<kC>(gate_ptr(a, c, h), a.sg.t, c.len, a.flags & GDN_G_PER_HEAD, hi, lo, te);
+    load_tile<T, DK, kT>(Q, at(static_cast<const T *>(a.q), a.sq, c.row, hk, c.t0), a.sq.t, c.len);
+    load_tile<T, DK, kT>(K, at(static_cast<const T *>(a.k), a.sk, c.row, hk, c.t0), a.sk.t, c.len);
+    load_tile<T, DV, kT>(V, at(static_cast<const T *>(a.v), a.sv, c.row, h, c.t0), a.sv.t, c.len);
+    load_tile<T, DV, kT>(O, at(static_cast<const T *>(a.dout), a.sdo, c.row, h, c.t0), a.sdo.t, c.len);
+    const float *Sc = S + ((long long)ci * a.H + h) * DK * DV, *Rc = R + ((long long)ci * a.H + h) * DK * DV;
+    __syncthreads();
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    {
+        float p[2][4] = {}, n[2][4] = {};
+        tile::mm<kT, 2, 4>(p, Q, ld<DK>(), 1, K, 1, ld<DK>(), DK);
+        tile::mm<kT, 2, 4>(n, O, ld<DV>(), 1, V, 1, ld<DV>(), DV);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = ty + 32 * i, s = tx + 16 * j;
+                const float f = s <= t ? a.scale * decay_between(hi[t], lo[t], hi[s], lo[s]) : 0.f;
+                P[t * (kC + 1) + s] = s <= t ? p[i][j] * f : 0.f;
+                N[t * (kC + 1) + s] = s <= t ? n[i][j] * f : 0.f;
+            }
+    }
+    // dq: the part through S over its columns in slabs of 64, then the chunk's own
+    {
+        float acc[2][DK / 16];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < DK / 16; ++j) acc[i][j] = 0.f;
+        for (int j0 = 0; j0 < DV; j0 += 64) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < DK * 64; i += kT) slab[(i >> 6) * 65 + (i & 63)] = Sc[(i >> 6) * DV + j0 + (i & 63)];
+            __syncthreads();
+            tile::mm<kT, 2, DK / 16>(acc, O + j0, ld<DV>(), 1, slab, 1, 65, 64);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < DK / 16; ++j) acc[i][j] *= a.scale * expf(hi[ty + 32 * i]);
+        tile::mm<kT, 2, DK / 16>(acc, N, kC + 1, 1, K, ld<DK>(), 1, kC);
+        T *dq = at(static_cast<T *>(a.dq), a.sq, c.row, hk, c.t0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = ty + 32 * i;
+            float x = 0.f;
+#pragma unroll
+            for (int j = 0; j < DK / 16; ++j) {
+                const int d = tx + 16 * j;
+                x = fmaf(Q[t * ld<DK>() + d], acc[i][j], x);
+                if (t < c.len) {
+                    if (shared) dqh[out_row + (long long)t * DK + d] = acc[i][j];
+                    else tile::st_f(dq + t * a.sq.t + d, acc[i][j]);
+                }
+            }
+            x = row16(x);
+            if (tx == 0) xq[t] = x;
+        }
+    }
+    // dk and dv, with R in the same slabs; <R, S> on the way
+    float dot = 0.f;
+    {
+        float acc[2][DK / 16];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < DK / 16; ++j) acc[i][j] = 0.f;
+        T *dv = at(static_cast<T *>(a.dv), a.sv, c.row, h, c.t0);
+        for (int j0 = 0; j0 < DV; j0 += 64) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < DK * 64; i += kT) {
+                const float r = Rc[(i >> 6) * DV + j0 + (i & 63)];
+                slab[(i >> 6) * 65 + (i & 63)] = r;
+                dot = fmaf(r, Sc[(i >> 6) * DV + j0 + (i & 63)], dot);
+            }
+            __syncthreads();
+            tile::mm<kT, 2, DK / 16>(acc, V + j0, ld<DV>(), 1, slab, 1, 65, 64);
+            float w[2][4] = {};
+            tile::mm<kT, 2, 4>(w, K, ld<DK>(), 1, slab, 65, 1, DK);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[i][j] *= expf(te[ty + 32 * i]);
+            tile::mm<kT, 2, 4>(w, P, 1, kC + 1, O + j0, ld<DV>(), 1, kC);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (ty + 32 * i < c.len) tile::st_f(dv + (ty + 32 * i) * a.sv.t + j0 + tx + 16 * j, w[i][j]);
+        }
+        float own[2][DK / 16];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = ty + 32 * i;
+            float x = 0.f;
+#pragma unroll
+            for (int j = 0; j < DK / 16; ++j) {
+                own[i][j] = 0.f;
+                acc[i][j] *= expf(te[t]);
+                x = fmaf(K[t * ld<DK>() + tx + 16 * j], acc[i][j], x);
+            }
+            x = row16(x);
+            if (tx == 0) xr[t] = x;
+        }
+        tile::mm<kT, 2, DK / 16>(own, N, 1, kC + 1, Q, ld<DK>(), 1, kC);
+        T *dk = at(static_cast<T *>(a.dk), a.sk, c.row, hk, c.t0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = ty + 32 * i;
+            float x = 0.f;
+#pragma unroll
+            for (int j = 0; j < DK / 16; ++j) {
+                const int d = tx + 16 * j;
+                x = fmaf(K[t * ld<DK>() + d], own[i][j], x);
+                if (t < c.len) {
+                    if (shared) dkh[out_row + (long long)t * DK + d] = acc[i][j] + own[i][j];
+                    else tile::st_f(dk + t * a.sk.t + d, acc[i][j] + own[i][j]);
+                }
+            }
+            x = row16(x);
+            if (tx == 0) xk[t] = x;
+        }
+    }
+#pragma unroll
+    for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(~0u, dot, m);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = dot;
+    __syncthreads();
+    if (threadIdx.x < kC) {  // each token's own sums, in order
+        const int u = threadIdx.x;
+        if (u < c.len) {
+            float x = 0.f, d = 0.f;
+            for (int w = 0; w < kT / 32; ++w) d += red[w];
+            for (int t = 0; t < kC; ++t) x += t < u ? xr[t] : xq[t] - xk[t];
+            at(dgt, sdg, c.row, h, c.t0)[u * sdg.t] = fmaf(expf(hi[c.len - 1]), d, x);
+        }
+    }
+}
+
+size_t page_bytes(const LinAttnArgs &a) { return 4 * (size_t)a.H * a.Dk * a.Dv; }
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+template <class F>
+int smem_limit(F f, int bytes) {
+    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+int launched() {
+    if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+    note_launch();
+    return GDN_OK;
+}
+
+#define LA_TRY(x)                       \
+    do {                                \
+        const int st_ = (x);            \
+        if (st_ != GDN_OK) return st_;  \
+    } while (0)
+
+template <typename T, int DK, int DV, bool REV>
+int run_states(const LinAttnArgs &a, const View &v, float *U, float *decay, cudaStream_t stream) {
+    const int smem = 4 * (kC * (ld<DK>() + ld<DV>()) + 3 * kC);
+    LA_TRY(smem_limit(share_kernel<T, DK, DV, REV>, smem));
+    share_kernel<T, DK, DV, REV><<<dim3(v.n_chunks, a.H), 256, smem, stream>>>(a, v, U, decay);
+    LA_TRY(launched());
+    scan_kernel<REV><<<dim3((DK * DV + 1023) / 1024, a.H, a.n_seq), 256, 0, stream>>>(
+        v, U, decay, REV ? a.dsf : a.s0, REV ? a.ds0 : a.sf, a.H, DK * DV);
+    return launched();
+}
+
+template <typename T, int DK, int DV>
+int run_fwd(const LinAttnArgs &a, const View &v, float *U, float *decay, cudaStream_t stream) {
+    LA_TRY((run_states<T, DK, DV, false>(a, v, U, decay, stream)));
+    const int smem = 4 * (kC * (2 * ld<DK>() + ld<DV>() + kC + 1) + 3 * kC);
+    LA_TRY(smem_limit(out_kernel<T, DK, DV>, smem));
+    out_kernel<T, DK, DV><<<dim3(v.n_chunks, a.H), kT, smem, stream>>>(a, v, U);
+    return launched();
+}
+
+struct BwdWs {
+    float *U, *R, *decay, *dqh, *dkh, *dgt;
+    size_t bytes;
+};
+
+BwdWs bwd_ws(const LinAttnArgs &a, void *ws) {
+    const size_t tab = table_bytes(a, kC), n = chunk_bound(a, kC);
+    const size_t heads = a.H != a.Hk ? up(4 * (size_t)a.B * a.H * a.T * a.Dk) : 0;
+    const size_t gates = (a.flags & GDN_G_PER_HEAD) ? up(4 * (size_t)a.B * a.H * a.T) : 0;
+    char *p = static_cast<char *>(ws) + tab;
+    BwdWs w;
+    w.U = reinterpret_cast<float *>(p), p += n * page_bytes(a);
+    w.R = reinterpret_cast<float *>(p), p += n * page_bytes(a);
+    w.decay = reinterpret_cast<float *>(p), p += up(4 * n * a.H);
+    w.dqh = reinterpret_cast<float *>(p), p += heads;
+    w.dkh = reinterpret_cast<float *>(p), p += heads;
+    w.dgt = reinterpret_cast<float *>(p), p += gates;
+    w.bytes = p - static_cast<char *>(ws);
+    return w;
+}
+
+template <typename T, int DK, int DV>
+int run_bwd(const LinAttnArgs &a, const View &v, const BwdWs &w, cudaStream_t stream) {
+    LA_TRY((run_states<T, DK, DV, false>(a, v, w.U, w.decay, stream)));
+    LA_TRY((run_states<T, DK, DV, true>(a, v, w.R, w.decay, stream)));
+    const int smem = 4 * (kC * (2 * ld<DK>() + 2 * ld<DV>() + 2 * (kC + 1)) + DK * 65 + 6 * kC + 32);
+    LA_TRY(smem_limit(grad_kernel<T, DK, DV>, smem));
+    const bool per_head = a.flags & GDN_G_PER_HEAD;
+    const Strides whole{(long long)a.H * a.T, a.T, 1};
+    grad_kernel<T, DK, DV><<<dim3(v.n_chunks, a.H), kT, smem, stream>>>(a, v, w.U, w.R, w.dqh, w.dkh,
+                                                                        per_head ? w.dgt : a.dg, per_head ? whole : a.sg);
+    return launched();
+}
+
+template <typename T>
+int fwd_t(const LinAttnArgs &a, const View &v, float *U, float *decay, cudaStream_t s) {
+    if (a.Dk == 128) return a.Dv == 128 ? run_fwd<T, 128, 128>(a, v, U, decay, s) : run_fwd<T, 128, 64>(a, v, U, decay, s);
+    return a.Dv == 128 ? run_fwd<T, 64, 128>(a, v, U, decay, s) : run_fwd<T, 64, 64>(a, v, U, decay, s);
+}
+
+template <typename T>
+int bwd_t(const LinAttnArgs &a, const View &v, const BwdWs &w, cudaStream_t s) {
+    if (a.Dk == 128) return a.Dv == 128 ? run_bwd<T, 128, 128>(a, v, w, s) : run_bwd<T, 128, 64>(a, v, w, s);
+    return a.Dv == 128 ? run_bwd<T, 64, 128>(a, v, w, s) : run_bwd<T, 64, 64>(a, v, w, s);
+}
+
+}  // namespace
+
+int make_view(const LinAttnArgs &a, int C, void *ws, View *v, cudaStream_t stream) {
+    v->n_chunks = chunk_bound(a, C);
+    v->per_row = (a.T + C - 1) / C;
+    v->chunks = v->seqs = nullptr;
+    if (!a.cu) return GDN_OK;
+    int4 *chunks = static_cast<int4 *>(ws), *seqs = chunks + v->n_chunks;
+    table_kernel<<<1, kTableThreads, 0, stream>>>(a.cu, a.n_seq, a.T, C, chunks, seqs, v->n_chunks);
+    v->chunks = chunks, v->seqs = seqs;
+    return launched();
+}
+
+int launch_group_sum(const float *src, void *dst, const Strides &s, int B, int H, int Hk, int T, int D, int dtype,
+                     cudaStream_t stream) {
+    const long long n = (long long)T * D / 4;
+    const dim3 grid((unsigned)(n < 256 * 1024 ? (n + 255) / 256 : 1024), Hk, B);
+    if (dtype == GDN_BF16) group_sum_kernel<<<grid, 256, 0, stream>>>(reinterpret_cast<const float4 *>(src), static_cast<__nv_bfloat16 *>(dst), s, H, Hk, T, D);
+    else group_sum_kernel<<<grid, 256, 0, stream>>>(reinterpret_cast<const float4 *>(src), static_cast<float *>(dst), s, H, Hk, T, D);
+    return launched();
+}
+
+int launch_head_sum(const float *src, float *dg, int B, int H, int T, cudaStream_t stream) {
+    head_sum_kernel<<<H, 1024, 0, stream>>>(src, dg, B, H, T);
+    return launched();
+}
+
+}  // namespace la
+
+using namespace la;
+
+size_t linattn_fwd_workspace(const LinAttnArgs &a) {
+    return table_bytes(a, kC) + (size_t)chunk_bound(a, kC) * page_bytes(a) + up(4 * (size_t)chunk_bound(a, kC) * a.H);
+}
+
+int launch_linattn_fwd(const LinAttnArgs &a, cudaStream_t stream) {
+    View v;
+    LA_TRY(make_view(a, kC, a.ws, &v, stream));
+    float *U = reinterpret_cast<float *>(static_cast<char *>(a.ws) + table_bytes(a, kC));
+    float *decay = U + (size_t)v.n_chunks * page_bytes(a) / 4;
+    return a.dtype == GDN_BF16 ? fwd_t<__nv_bfloat16>(a, v, U, decay, stream) : fwd_t<float>(a, v, U, decay, stream);
+}
+
+size_t linattn_bwd_workspace(const LinAttnArgs &a) { return bwd_ws(a, nullptr).bytes; }
+
+int launch_linattn_bwd(const LinAttnArgs &a, cudaStream_t stream) {
+    View v;
+    LA_TRY(make_view(a, kC, a.ws, &v, stream));
+    const bool shared = a.H != a.Hk, per_head = a.flags & GDN_G_PER_HEAD;
+    const BwdWs w = bwd_ws(a, a.ws);
+    LA_TRY(a.dtype == GDN_BF16 ? bwd_t<__nv_bfloat16>(a, v, w, stream) : bwd_t<float>(a, v, w, stream));
+    if (shared) {
+        LA_TRY(launch_group_sum(w.dqh, a.dq, a.sq, a.B, a.H, a.Hk, a.T, a.Dk, a.dtype, stream));
+        LA_TRY(launch_group_sum(w.dkh, a.dk, a.sk, a.B, a.H, a.Hk, a.T, a.Dk, a.dtype, stream));
+    }
+    if (per_head) LA_TRY(launch_head_sum(w.dgt, a.dg, a.B, a.H, a.T, stream));
+    return GDN_OK;
+}
+
+}  // namespace gdn

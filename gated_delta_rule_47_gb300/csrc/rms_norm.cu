@@ -1,0 +1,426 @@
+// rms_norm.cu -- root-mean-square norm of a row after the residual's addition,
+// with an output in the tensors' type or in e4m3 with scales; and its backward.
+//
+//   h = x + res;   y = w h / sqrt(mean(h^2) + eps)
+//   e4m3: per group, scale = max(max|y| / 448, 1e-12) and y is stored as y / scale
+//
+// backward, for the row h that the forward stored (r = 1 / sqrt(...), C columns):
+//   dh = r (w dy - h r^2 mean(h w dy)) + dres;   dw = sum over rows of dy h r
+//
+// One pass over the data: a CTA holds its row in registers between the sum of
+// squares and the output.  The bytes of the rows bound both directions.
+// Sums are in fp32; h enters the norm before it is rounded for the store.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "gdn_internal.h"
+#include "layer_ops.h"
+
+namespace gdn {
+namespace {
+
+constexpr float kTop = 448.f;  // the largest e4m3 value
+
+// Vectors of 16 bytes: 8 bf16 or 4 fp32.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void unpack(uint4 p, float (&x)[8]) {
+        const uint32_t u[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(u[i] << 16);
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t *>(&t);
+        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+};
+template <>
+struct Vec<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void unpack(uint4 p, float (&x)[4]) {
+        x[0] = __uint_as_float(p.x), x[1] = __uint_as_float(p.y);
+        x[2] = __uint_as_float(p.z), x[3] = __uint_as_float(p.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
+};
+
+__device__ __forceinline__ float ldf(const float *p) { return *p; }
+__device__ __forceinline__ float ldf(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void stf(float *p, float x) { *p = x; }
+__device__ __forceinline__ void stf(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+
+// max that keeps a NaN, so that a bad row shows in its scale
+__device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a != a) ? a : b; }
+
+// Sum / maximum over the CTA; every thread gets it.  `s` has room for 32.
+template <int NT, bool MAX>
+__device__ __forceinline__ float block_all(float x, float *s) {
+#pragma unroll
+    for (int m = 16; m; m >>= 1) {
+        const float y = __shfl_xor_sync(~0u, x, m);
+        x = MAX ? max_nan(x, y) : x + y;
+    }
+    if (NT == 32) return x;
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = s[0];
+#pragma unroll
+    for (int w = 1; w < NT / 32; ++w) x = MAX ? max_nan(x, s[w]) : x + s[w];
+    return x;
+}
+
+template <int N>
+__device__ __forceinline__ void store_e4m3(void *p, const float (&y)[N], float inv) {
+    uint32_t u[N / 4];
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * i] * inv, y[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * i + 2] * inv, y[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+        u[i] = lo | hi << 16;
+    }
+    if (N == 8) *static_cast<uint2 *>(p) = make_uint2(u[0], u[N / 4 - 1]);
+    else *static_cast<uint32_t *>(p) = u[0];
+}
+
+// One row a CTA of NT threads, V vectors a thread (vector j of thread t is
+// number j NT + t, so a group's vectors are consecutive lanes of one warp).
+// C is a multiple of the vector's width; rows are 16-byte aligned.
+template <typename T, int NT, int V>
+__global__ void __launch_bounds__(NT) norm_kernel(NormArgs a) {
+    constexpr int N = Vec<T>::N;
+    __shared__ float red[32];
+    const long long row = blockIdx.x;
+    const int nv = a.C / N;
+    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + row * a.C);
+    const uint4 *res = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.res) + row * a.C);
+    uint4 px[V], pr[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int i = j * NT + threadIdx.x;
+        px[j] = pr[j] = make_uint4(0, 0, 0, 0);
+        if (i < nv) {
+            px[j] = __ldcs(x + i);
+            if (a.res) pr[j] = __ldcs(res + i);
+        }
+    }
+    float h[V][N];
+    float sum = 0.f;
+    uint4 *ho = a.h ? reinterpret_cast<uint4 *>(static_cast<T *>(a.h) + row * a.C) : nullptr;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int i = j * NT + threadIdx.x;
+        Vec<T>::unpack(px[j], h[j]);
+        if (a.res) {
+            float r[N];
+            Vec<T>::unpack(pr[j], r);
+#pragma unroll
+            for (int e = 0; e < N; ++e) h[j][e] += r[e];
+        }
+        if (ho && i < nv) ho[i] = Vec<T>::pack(h[j]);
+#pragma unroll
+        for (int e = 0; e < N; ++e) sum = fmaf(h[j][e], h[j][e], sum);
+    }
+    sum = block_all<NT, false>(sum, red);
+    const float r = rsqrtf(sum / a.C + a.eps);
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int i = j * NT + threadIdx.x;
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+            float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
+            if (a.w && i < nv) w = __ldg(reinterpret_cast<const float4 *>(a.w) + (i * N + e) / 4);
+            h[j][e] *= r * w.x, h[j][e + 1] *= r * w.y, h[j][e + 2] *= r * w.z, h[j][e + 3] *= r * w.w;
+        }
+        if (a.out_e4m3 && a.group == 0)
+#pragma unroll
+            for (int e = 0; e < N; ++e) top = max_nan(top, fabsf(h[j][e]));
+    }
+    if (!a.out_e4m3) {
+        uint4 *y = reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + row * a.C);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j * NT + threadIdx.x < nv) y[j * NT + threadIdx.x] = Vec<T>::pack(h[j]);
+        return;
+    }
+    unsigned char *y = static_cast<unsigned char *>(a.y) + row * a.C;
+    if (a.group == 0) {
+        top = block_all<NT, true>(top, red);
+        const float scale = max_nan(top / kTop, 1e-12f);
+        if (threadIdx.x == 0) a.scales[row] = scale;
+        const float inv = 1.f / scale;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j * NT + threadIdx.x < nv) store_e4m3<N>(y + (size_t)(j * NT + threadIdx.x) * N, h[j], inv);
+        return;
+    }
+    const int lanes = a.group / N;  // a power of two, at most 32
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int i = j * NT + threadIdx.x;
+        float t = 0.f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) t = max_nan(t, fabsf(h[j][e]));
+        for (int m = lanes >> 1; m; m >>= 1) t = max_nan(t, __shfl_xor_sync(~0u, t, m));
+        const float scale = max_nan(t / kTop, 1e-12f);
+        if (i < nv) {
+            if ((i & (lanes - 1)) == 0) a.scales[row * (a.C / a.group) + i / lanes] = scale;
+            store_e4m3<N>(y + (size_t)i * N, h[j], 1.f / scale);
+        }
+    }
+}
+
+// Any C: the row is read again after its sum of squares (and again for its
+// maximum), element by element.  Groups are not offered here.
+template <typename T>
+__global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
+    __shared__ float red[32];
+    const long long row = blockIdx.x;
+    const T *x = static_cast<const T *>(a.x) + row * a.C;
+    const T *res = a.res ? static_cast<const T *>(a.res) + row * a.C : nullptr;
+    T *ho = a.h ? static_cast<T *>(a.h) + row * a.C : nullptr;
+    float sum = 0.f, top = 0.f;
+    for (int i = threadIdx.x; i < a.C; i += 256) {
+        const float h = ldf(x + i) + (res ? ldf(res + i) : 0.f);
+        sum = fmaf(h, h, sum);
+    }
+    sum = block_all<256, false>(sum, red);
+    const float r = rsqrtf(sum / a.C + a.eps);
+    float inv = 1.f;
+    if (a.out_e4m3) {
+        for (int i = threadIdx.x; i < a.C; i += 256) {
+            const float h = ldf(x + i) + (res ? ldf(res + i) : 0.f);
+            top = max_nan(top, fabsf(h * (r * (a.w ? a.w[i] : 1.f))));
+        }
+        top = block_all<256, true>(top, red);
+        const float scale = max_nan(top / kTop, 1e-12f);
+        if (threadIdx.x == 0) a.scales[row] = scale;
+        inv = 1.f / scale;
+    }
+    for (int i = threadIdx.x; i < a.C; i += 256) {
+        const float h = ldf(x + i) + (res ? ldf(res + i) : 0.f);
+        const float y = h * (r * (a.w ? a.w[i] : 1.f));
+        // h after every read of x and res at this place, which it may overwrite
+        if (ho) stf(ho + i, h);
+        if (a.out_e4m3)
+            static_cast<unsigned char *>(a.y)[row * a.C + i] = __nv_cvt_float_to_fp8(y * inv, __NV_SATFINITE, __NV_E4M3);
+        else
+            stf(static_cast<T *>(a.y) + row * a.C + i, y);
+    }
+}
+
+template <typename T, int NT, int V>
+void launch_v(const NormArgs &a, cudaStream_t stream) {
+    norm_kernel<T, NT, V><<<(unsigned)a.rows, NT, 0, stream>>>(a);
+}
+
+template <typename T>
+void launch_t(const NormArgs &a, cudaStream_t stream) {
+    constexpr int N = Vec<T>::N;
+    const int nv = a.C / N;
+    if (a.C % N != 0 || nv > 4096) {
+        norm_any_kernel<T><<<(unsigned)a.rows, 256, 0, stream>>>(a);
+    } else if (nv <= 32) {
+        launch_v<T, 32, 1>(a, stream);
+    } else if (nv <= 64) {
+        launch_v<T, 64, 1>(a, stream);
+    } else if (nv <= 128) {
+        launch_v<T, 128, 1>(a, stream);
+    } else if (nv <= 256) {
+        launch_v<T, 256, 1>(a, stream);
+    } else if (nv <= 512) {
+        launch_v<T, 256, 2>(a, stream);
+    } else if (nv <= 1024) {
+        launch_v<T, 256, 4>(a, stream);
+    } else if (nv <= 2048) {
+        launch_v<T, 512, 4>(a, stream);
+    } else {
+        launch_v<T, 1024, 4>(a, stream);
+    }
+}
+
+// ------------------------------------------------------------------ backward
+constexpr int kBwdThreads = 256;
+
+// Rows blockIdx.x, + gridDim.x, ... ; each thread's columns are the same in
+// every row, so its share of dw stays in registers until the CTA's rows are
+// done.  part[blockIdx.x][C].  V vectors a thread, as norm_kernel.
+template <typename T, int V>
+__global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(NormBwdArgs a, float *part) {
+    constexpr int N = Vec<T>::N, NT = kBwdThreads;
+    __shared__ float red[2][2][NT / 32];
+    const int nv = a.C / N, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float dw[V][N];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int e = 0; e < N; ++e) dw[j][e] = 0.f;
+    int buf = 0;
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
+        const uint4 *h4 = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.h) + row * a.C);
+        const uint4 *dy4 = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.dy) + row * a.C);
+        const uint4 *dr4 = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.dres) + row * a.C);
+        uint4 ph[V], pd[V], pr[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int i = j * NT + threadIdx.x;
+            ph[j] = pd[j] = pr[j] = make_uint4(0, 0, 0, 0);
+            if (i < nv) {
+                ph[j] = __ldcs(h4 + i);
+                pd[j] = __ldcs(dy4 + i);
+                if (a.dres) pr[j] = __ldcs(dr4 + i);
+            }
+        }
+        float ss = 0.f, sp = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float h[N], d[N];
+            Vec<T>::unpack(ph[j], h);
+            Vec<T>::unpack(pd[j], d);
+            const int i = j * NT + threadIdx.x;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float w = a.w && i < nv ? __ldg(a.w + i * N + e) : 1.f;
+                ss = fmaf(h[e], h[e], ss);
+                sp = fmaf(h[e], d[e] * w, sp);
+            }
+        }
+#pragma unroll
+        for (int m = 16; m; m >>= 1) {
+            ss += __shfl_xor_sync(~0u, ss, m);
+            sp += __shfl_xor_sync(~0u, sp, m);
+        }
+        if (lane == 0) red[buf][0][warp] = ss, red[buf][1][warp] = sp;
+        __syncthreads();  // one a row: the buffers alternate
+        ss = sp = 0.f;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) ss += red[buf][0][w], sp += red[buf][1][w];
+        const float r = rsqrtf(ss / a.C + a.eps);
+        const float m = r * r * (sp / a.C);
+        uint4 *dx = reinterpret_cast<uint4 *>(static_cast<T *>(a.dx) + row * a.C);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int i = j * NT + threadIdx.x;
+            float h[N], d[N], g[N];
+            Vec<T>::unpack(ph[j], h);
+            Vec<T>::unpack(pd[j], d);
+            Vec<T>::unpack(pr[j], g);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float w = a.w && i < nv ? __ldg(a.w + i * N + e) : 1.f;
+                g[e] = fmaf(r, fmaf(d[e], w, -h[e] * m), g[e]);
+                dw[j][e] = fmaf(d[e], h[e] * r, dw[j][e]);
+            }
+            if (i < nv) dx[i] = Vec<T>::pack(g);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int i = j * NT + threadIdx.x;
+        if (i < nv)
+#pragma unroll
+            for (int e = 0; e < N; e += 4)
+                reinterpret_cast<float4 *>(part + (size_t)blockIdx.x * a.C)[(i * N + e) / 4] =
+                    make_float4(dw[j][e], dw[j][e + 1], dw[j][e + 2], dw[j][e + 3]);
+    }
+}
+
+// Any C: rows are read twice; dw's share of a column is summed in `part`.
+template <typename T>
+__global__ void __launch_bounds__(kBwdThreads) norm_bwd_any_kernel(NormBwdArgs a, float *part) {
+    constexpr int NT = kBwdThreads;
+    __shared__ float red[32];
+    float *mine = part + (size_t)blockIdx.x * a.C;
+    for (int i = threadIdx.x; i < a.C; i += NT) mine[i] = 0.f;
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T *h = static_cast<const T *>(a.h) + row * a.C, *dy = static_cast<const T *>(a.dy) + row * a.C;
+        const T *dres = a.dres ? static_cast<const T *>(a.dres) + row * a.C : nullptr;
+        float ss = 0.f, sp = 0.f;
+        for (int i = threadIdx.x; i < a.C; i += NT) {
+            const float x = ldf(h + i);
+            ss = fmaf(x, x, ss);
+            sp = fmaf(x, ldf(dy + i) * (a.w ? a.w[i] : 1.f), sp);
+        }
+        ss = block_all<NT, false>(ss, red);
+        sp = block_all<NT, false>(sp, red);
+        const float r = rsqrtf(ss / a.C + a.eps);
+        const float m = r * r * (sp / a.C);
+        for (int i = threadIdx.x; i < a.C; i += NT) {
+            const float x = ldf(h + i), d = ldf(dy + i);
+            mine[i] = fmaf(d, x * r, mine[i]);
+            stf(static_cast<T *>(a.dx) + row * a.C + i,
+                fmaf(r, fmaf(d, a.w ? a.w[i] : 1.f, -x * m), dres ? ldf(dres + i) : 0.f));
+        }
+    }
+}
+
+// dw[c] = the CTAs' shares, in order: 32 columns and 8 strands of shares a CTA.
+__global__ void __launch_bounds__(256) norm_dw_kernel(const float *part, float *dw, int n, int C) {
+    __shared__ float s[8][33];
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), strand = threadIdx.x >> 5;
+    float x = 0.f;
+    if (c < C)
+        for (int i = strand; i < n; i += 8) x += part[(size_t)i * C + c];
+    s[strand][threadIdx.x & 31] = x;
+    __syncthreads();
+    if (strand == 0 && c < C) {
+#pragma unroll
+        for (int j = 1; j < 8; ++j) x += s[j][threadIdx.x & 31];
+        dw[c] = x;
+    }
+}
+
+int bwd_ctas(long long rows) {
+    const long long full = 4LL * device_sm_count();
+    return (int)(rows < full ? rows : full);
+}
+
+template <typename T>
+void launch_bwd_t(const NormBwdArgs &a, int ctas, float *part, cudaStream_t stream) {
+    const int nv = a.C / Vec<T>::N;
+    if (a.C % Vec<T>::N != 0 || nv > 4 * kBwdThreads) norm_bwd_any_kernel<T><<<ctas, kBwdThreads, 0, stream>>>(a, part);
+    else if (nv <= kBwdThreads) norm_bwd_kernel<T, 1><<<ctas, kBwdThreads, 0, stream>>>(a, part);
+    else if (nv <= 2 * kBwdThreads) norm_bwd_kernel<T, 2><<<ctas, kBwdThreads, 0, stream>>>(a, part);
+    else norm_bwd_kernel<T, 4><<<ctas, kBwdThreads, 0, stream>>>(a, part);
+}
+
+}  // namespace
+
+int launch_rms_norm(const NormArgs &a, cudaStream_t stream) {
+    if (a.dtype == GDN_BF16) launch_t<__nv_bfloat16>(a, stream);
+    else launch_t<float>(a, stream);
+    if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+    note_launch();
+    return GDN_OK;
+}
+
+size_t rms_norm_bwd_workspace(long long rows, int C) { return 4 * (size_t)bwd_ctas(rows) * C; }
+
+int launch_rms_norm_bwd(const NormBwdArgs &a, cudaStream_t stream) {
+    float *part = static_cast<float *>(a.ws);
+    const int ctas = bwd_ctas(a.rows);
+    if (a.dtype == GDN_BF16) launch_bwd_t<__nv_bfloat16>(a, ctas, part, stream);
+    else launch_bwd_t<float>(a, ctas, part, stream);
+    if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+    note_launch();
+    norm_dw_kernel<<<(a.C + 31) / 32, 256, 0, stream>>>(part, a.dw, ctas, a.C);
+    if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+    note_launch();
+    return GDN_OK;
+}
+
+}  // namespace gdn

@@ -61,6 +61,8 @@ typedef enum {
                             path applies (bf16, Dk = Dv = 128, chunk 64,
                             r in {1, 2, 4})                                */
 #define GDN_CAM_REVERSE 4u /* cam_scan_fwd only: the anti-causal mode        */
+#define GDN_G_PER_HEAD 8u  /* linattn_* and gdn_step: g is [H], one fixed
+                              log-decay for each head                        */
 
 /* Human-readable name of a status code; never NULL. */
 const char *gdn_status_string(int status);
@@ -473,6 +475,161 @@ int cam_prep_bwd(const void *q_raw, const void *k_raw, const float *q_norm_w, co
                  float rope_base, const void *dq_out, const void *dk_out, const void *dv_out,
                  const float *dk_pre_sq, const float *dk_post_sq, void *dq_raw, void *dk_raw, void *dv_raw, int B,
                  int N, int H, int D, float k_scale, float eps, int dtype, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Operators around a linear-attention layer: prompts, single-token steps, the
+ * norm in front of the projections, and the pool that keeps the states.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * linattn_chunk_fwd -- linear attention with a decay for each head (the gated
+ * delta rule without its correction) over whole prompts:
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,      o_t = scale * S_t^T q_t
+ *
+ *   q, k    [B,Hk,T,Dk] dtype; value head h uses query / key head h / (H / Hk)
+ *           (Hk divides H)
+ *   v, o    [B,H,T,Dv]  dtype (o may not alias an input)
+ *   g       [B,H,T] fp32 log-decays, or [H] with GDN_G_PER_HEAD.  Values below
+ *           -100 (also -inf) count as -100: exp(-100) leaves nothing of a
+ *           state in fp32.
+ *   cu_seqlens  NULL: every row is one sequence of T tokens (n_seq = B).
+ *           Else B = 1 and device int32 [n_seq + 1] offsets, not decreasing:
+ *           sequence s holds tokens cu_seqlens[s] .. cu_seqlens[s+1] - 1 (none
+ *           is allowed).  Offsets outside 0..T are cut to it.  Tokens before
+ *           the first and after the last offset belong to no sequence and get
+ *           o = 0.
+ *   initial_state / final_state [n_seq,H,Dk,Dv] fp32 or NULL; a sequence of no
+ *           tokens passes its state on
+ *   strides host array of 15 element strides or NULL for contiguous tensors:
+ *           (batch, head, token) of q, k, v, o, g; the last dimension is
+ *           contiguous.  Those of q, k, v, o are multiples of 16 bytes
+ *           (GDN_ERR_MISALIGNED).  A token-major [T,H,D] tensor is a
+ *           [1,H,T,D] one with strides (0, D, H*D).
+ *   flags   0 or GDN_G_PER_HEAD, GDN_PATH_SIMT
+ *   Dk, Dv  64 or 128 each; n_seq, B and H up to 65535
+ *   workspace / workspace_bytes: linattn_chunk_fwd_workspace_bytes(...) bytes
+ *           (packed: 1 where cu_seqlens is given), 16-byte aligned; no
+ *           initialisation needed, contents not meaningful afterwards.
+ * T = 0 or B*H = 0 is valid and passes the state on.
+ */
+size_t linattn_chunk_fwd_workspace_bytes(int B, int H, int Hk, int T, int Dk, int Dv, int n_seq, int packed,
+                                         unsigned flags, int dtype);
+int linattn_chunk_fwd(const void *q, const void *k, const void *v, const float *g, const float *initial_state,
+                      void *o, float *final_state, const int *cu_seqlens, const long long *strides, int n_seq, int B,
+                      int H, int Hk, int T, int Dk, int Dv, float scale, unsigned flags, int dtype, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/*
+ * linattn_chunk_bwd -- backward of linattn_chunk_fwd.  With R_t the gradient
+ * of S_t (R_t = scale q_t do_t^T + exp(g_{t+1}) R_{t+1}):
+ *     dq_t = scale S_t do_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,
+ *     dg_t = exp(g_t) <R_t, S_{t-1}>
+ *   q, k, v, g, initial_state, cu_seqlens, sizes, scale, flags: as given to
+ *           linattn_chunk_fwd
+ *   dout    as o;  dfinal_state [n_seq,H,Dk,Dv] fp32 or NULL (= zero)
+ *   dq, dk, dv  the shapes, type and strides of q, k, v (shared query and key
+ *           heads get the sum over their value heads); dg those of g, fp32
+ *           (with GDN_G_PER_HEAD the sum over batch and tokens)
+ *   dinitial_state [n_seq,H,Dk,Dv] fp32 or NULL (not wanted)
+ *   strides those of q, k, v, dout, g, or NULL
+ * Tokens of no sequence get zeros.  Every sum has a fixed order: equal calls
+ * give equal bits.
+ */
+size_t linattn_chunk_bwd_workspace_bytes(int B, int H, int Hk, int T, int Dk, int Dv, int n_seq, int packed,
+                                         unsigned flags, int dtype);
+int linattn_chunk_bwd(const void *q, const void *k, const void *v, const float *g, const float *initial_state,
+                      const void *dout, const float *dfinal_state, void *dq, void *dk, void *dv, float *dg,
+                      float *dinitial_state, const int *cu_seqlens, const long long *strides, int n_seq, int B, int H,
+                      int Hk, int T, int Dk, int Dv, float scale, unsigned flags, int dtype, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/*
+ * linattn_step, gdn_step -- one token of each of B requests against a pool of
+ * states, for decoding: with D = exp(g) S,
+ *     S' = D + k u^T,   o = scale * S'^T q,
+ *     u = v (linattn_step)   or   beta (v - D^T k) (gdn_step)
+ *   q, k [B,Hk,Dk]; v, o [B,H,Dv]; beta [B,H] dtype; g [B,H] fp32 (or [H]
+ *           with GDN_G_PER_HEAD), all contiguous
+ *   state, state_out [n_slots,H,Dk,Dv] fp32; state_out may be state itself
+ *           (updated in place) but not overlap it otherwise
+ *   slots   int32 [B]: row b's page, or NULL (page b).  A slot outside
+ *           0..n_slots-1 (-1 by custom) marks an idle row: o = 0 and no page
+ *           is read or written.  Rows may not share a page.
+ *   flags   0, GDN_G_PER_HEAD; gdn_step also GDN_QK_L2NORM
+ */
+int linattn_step(const void *q, const void *k, const void *v, const float *g, const float *state, float *state_out,
+                 const int *slots, void *o, int B, int H, int Hk, int Dk, int Dv, int n_slots, float scale,
+                 unsigned flags, int dtype, void *stream);
+int gdn_step(const void *q, const void *k, const void *v, const void *beta, const float *g, const float *state,
+             float *state_out, const int *slots, void *o, int B, int H, int Hk, int Dk, int Dv, int n_slots,
+             float scale, unsigned flags, int dtype, void *stream);
+
+/*
+ * rms_norm_fwd -- h = x + residual, y = weight * h / sqrt(mean(h^2) + eps) over
+ * rows of C, with y in the tensors' type or in e4m3 with scales.
+ *   x, residual, h  [rows,C] dtype, contiguous; residual NULL: h = x;
+ *           h NULL: not written; h may be x or residual (in place)
+ *   weight  [C] fp32 or NULL (ones)
+ *   y       [rows,C] dtype, or e4m3 bytes with out_e4m3 (it may be x or
+ *           residual only in the tensors' type, and not where h is too)
+ *   scales  out_e4m3: fp32 [rows,C/group], group 32, 64 or 128 dividing C, or
+ *           [rows] with group 0.  scale = max(max|y| / 448, 1e-12) over the
+ *           group; what is stored is y / scale
+ * The norm uses h before its rounding to dtype.  C up to 32768 bf16 or 16384
+ * fp32 with groups; any C >= 1 without.
+ */
+int rms_norm_fwd(const void *x, const void *residual, const float *weight, void *y, float *scales, void *h,
+                 long long rows, int C, int group, float eps, int out_e4m3, int dtype, void *stream);
+
+/*
+ * rms_norm_bwd -- backward of rms_norm_fwd (y in the tensors' type) at the h
+ * that it wrote: with r = 1 / sqrt(mean(h^2) + eps),
+ *     dx = r (weight dy - h r^2 mean(h weight dy)) + dresidual
+ *     dweight = sum over rows of dy h r
+ *   dy, h, dx [rows,C] dtype; dresidual [rows,C] dtype or NULL: the gradient
+ *   that reaches h past the norm; dx is also the residual's gradient and may be
+ *   dy or dresidual; dweight [C] fp32; workspace of
+ *   rms_norm_bwd_workspace_bytes(rows, C) bytes, 16-byte aligned.
+ * dweight is summed in a fixed order.
+ */
+size_t rms_norm_bwd_workspace_bytes(long long rows, int C);
+int rms_norm_bwd(const void *dy, const void *h, const float *weight, const void *dresidual, void *dx, float *dweight,
+                 long long rows, int C, float eps, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * state_pool_* -- the pages of a pool [layers][n_slots][page_bytes] (the
+ * states of one request in every layer; page_bytes a multiple of 16, base
+ * 16-byte aligned).  `live` is a byte per slot, 0 = free; it is the only
+ * bookkeeping, lives on the device and is updated there, so no call waits for
+ * the host.
+ *
+ * copy:    page dst[i] <- page src[i] in every layer, i < n (device int32);
+ *          src -1 writes zeros; a pair with an index out of range is skipped.
+ *          The destinations are distinct and no one's source.
+ * fork:    the i-th valid parent gets the i-th lowest free slot as its child:
+ *          children[i] = that slot, now live, with a copy of the parent's page.
+ *          Parent -1 is a new request (a page of zeros).  A parent that is not
+ *          live or out of range, or one for which no slot is left, gets
+ *          child -1.
+ * free:    marks the slots free (out-of-range ones are skipped; pages keep
+ *          their bytes).
+ * compact: the live pages move into slots 0 .. n_live-1: those past them, in
+ *          order, into the free slots before, in order; the others stay.
+ *          remap[s] is slot s's new place (-1: was free), *n_live (device)
+ *          the count; live is updated.
+ * workspace: the matching *_workspace_bytes, 16-byte aligned.
+ */
+int state_pool_copy(void *pool, int layers, int n_slots, long long page_bytes, const int *src, const int *dst, int n,
+                    void *stream);
+size_t state_pool_fork_workspace_bytes(int n_slots, int n);
+int state_pool_fork(void *pool, int layers, int n_slots, long long page_bytes, unsigned char *live,
+                    const int *parents, int *children, int n, void *workspace, size_t workspace_bytes, void *stream);
+int state_pool_free(unsigned char *live, int n_slots, const int *slots, int n, void *stream);
+size_t state_pool_compact_workspace_bytes(int n_slots);
+int state_pool_compact(void *pool, int layers, int n_slots, long long page_bytes, unsigned char *live, int *remap,
+                       int *n_live, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Reads and clears the device error word of the current device after
