@@ -715,8 +715,9 @@ def linattn_chunk_fwd(q, k, v, g, initial_state=None, output_final_state=False, 
     lib = load()
     flags = (GDN_G_PER_HEAD if per_head else 0) | (GDN_PATH_SIMT if simt else 0)
     with _on(stream):
+        q, k, v = (t.contiguous() if _overlaps(t) else t for t in (q, k, v))
         if o is None:
-            o = torch.empty_like(v) if not _overlaps(v) else torch.empty(v.shape, dtype=v.dtype, device=v.device)
+            o = torch.empty_like(v)
         _strided(o, "o", (B, H, T, Dv), q.dtype)
         sf = torch.empty(n_seq, H, Dk, Dv, dtype=torch.float32, device=q.device) if output_final_state else None
         need = lib.linattn_chunk_fwd_workspace_bytes(B, H, Hk, T, Dk, Dv, n_seq, cu_seqlens is not None, flags, code)
@@ -747,7 +748,7 @@ def linattn_chunk_bwd(q, k, v, g, dout, initial_state=None, dfinal_state=None, c
     flags = (GDN_G_PER_HEAD if per_head else 0) | (GDN_PATH_SIMT if simt else 0)
     with _on(stream):
         # gradients take their tensors' strides, so those may not overlap
-        q, k, v, g = (t.contiguous() if _overlaps(t) else t for t in (q, k, v, g))
+        q, k, v, g, dout = (t.contiguous() if _overlaps(t) else t for t in (q, k, v, g, dout))
         dq, dk, dv, dg = (torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device) for t in (q, k, v, g))
         ds0 = torch.empty_like(initial_state) if initial_state is not None else None
         need = lib.linattn_chunk_bwd_workspace_bytes(B, H, Hk, T, Dk, Dv, n_seq, cu_seqlens is not None, flags, code)

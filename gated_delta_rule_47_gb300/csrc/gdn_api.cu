@@ -10,6 +10,7 @@
 
 #include "api_util.h"
 #include "gdn_internal.h"
+#include "linattn.cuh"
 
 namespace gdn {
 namespace {
@@ -506,7 +507,8 @@ int gdn_get_device_error(void *stream) {
     const int c = gdn::cam_scan_read_clear_error();
     const int d = gdn::cam_scan_bwd_read_clear_error();
     const int e = gdn::wy_chain_tc_read_clear_error();
-    const int r[] = {a, b, c, d, e};
+    const int f = gdn::linattn_tc_read_clear_error();
+    const int r[] = {a, b, c, d, e, f};
     for (int x : r)
         if (x != GDN_OK) return x;
     return GDN_OK;

@@ -22,9 +22,10 @@
 //   dq_t = scale e^{c_t} S do_t + sum_s N_ts k_s
 //   dk_s = e^{G-c_s} R v_s + sum_t N_ts q_t
 //   dv_s = e^{G-c_s} R^T k_s + sum_t P_ts do_t
-//   dg_u = sum_{t>=u} (q_t . dq_t - k_t . dk_t) + sum_t k_t . (R's part of dk_t) + e^G <R, S>
+//   dg_u = sum_{t>=u} (x_t + sum_{s<t} A_ts - sum_{r>t} A_rt) + sum_{t<u} y_t + e^G <R, S>
 //
-// (the last line's sums of R's part over t >= u cancel and are left out).
+// with A_ts = (q_t . k_s) N_ts, x_t = q_t . (S's part of dq_t) and y_t = k_t .
+// (R's part of dk_t): what passes over the decay of token u, pair by pair.
 #include <cuda_bf16.h>
 
 #include "gdn_internal.h"
@@ -164,10 +165,6 @@ __device__ __forceinline__ void load_tile(float *dst, const T *src, long long st
 template <typename T, int D, int NT>
 __device__ __forceinline__ void zero_rows(T *dst, long long step, int len) {
     for (int i = threadIdx.x; i < len * D; i += NT) tile::st_f(dst + (i / D) * step + i % D, 0.f);
-}
-
-__device__ __forceinline__ const float *gate_ptr(const LinAttnArgs &a, const Chunk &c, int h) {
-    return (a.flags & GDN_G_PER_HEAD) ? a.g + h : at(a.g, a.sg, c.row, h, c.t0);
 }
 
 // A chunk's share of the state that leaves it, sum_t e^{G-c_t} k_t v_t^T, or
@@ -314,7 +311,7 @@ __global__ void __launch_bounds__(kT) grad_kernel(LinAttnArgs a, View v, const f
     extern __shared__ float sm[];
     float *Q = sm, *K = Q + kC * ld<DK>(), *V = K + kC * ld<DK>(), *O = V + kC * ld<DV>();
     float *P = O + kC * ld<DV>(), *N = P + kC * (kC + 1), *slab = N + kC * (kC + 1);  // slab [DK][65]
-    float *hi = slab + DK * 65, *lo = hi + kC, *te = lo + kC, *xq = te + kC, *xk = xq + kC, *xr = xk + kC, *red = xr + kC;
+    float *hi = slab + DK * 65, *lo = hi + kC, *te = lo + kC, *xq = te + kC, *xk = xq + kC, *xr = xk + kC, *xa = xr + kC, *red = xa + kC;
     const int ci = blockIdx.x, h = blockIdx.y;
     const Chunk c = chunk_at<kC>(v, a.T, ci);
     if (c.len <= 0) return;
@@ -354,7 +351,16 @@ __global__ void __launch_bounds__(kT) grad_kernel(LinAttnArgs a, View v, const f
                 const float f = s <= t ? a.scale * decay_between(hi[t], lo[t], hi[s], lo[s]) : 0.f;
                 P[t * (kC + 1) + s] = s <= t ? p[i][j] * f : 0.f;
                 N[t * (kC + 1) + s] = s <= t ? n[i][j] * f : 0.f;
+                slab[t * 65 + s] = s < t ? p[i][j] * (n[i][j] * f) : 0.f;  // A
             }
+    }
+    __syncthreads();
+    if (threadIdx.x < 2 * kC) {  // A's sums: rows, then columns
+        const int t = threadIdx.x & (kC - 1);
+        const bool rows = threadIdx.x < kC;
+        float x = 0.f;
+        for (int s = 0; s < kC; ++s) x += rows ? slab[t * 65 + s] : slab[s * 65 + t];
+        (rows ? xa : xk)[t] = x;
     }
     // dq: the part through S over its columns in slabs of 64, then the chunk's own
     {
@@ -373,23 +379,27 @@ __global__ void __launch_bounds__(kT) grad_kernel(LinAttnArgs a, View v, const f
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < DK / 16; ++j) acc[i][j] *= a.scale * expf(hi[ty + 32 * i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float x = 0.f;
+#pragma unroll
+            for (int j = 0; j < DK / 16; ++j) x = fmaf(Q[(ty + 32 * i) * ld<DK>() + tx + 16 * j], acc[i][j], x);
+            x = row16(x);
+            if (tx == 0) xq[ty + 32 * i] = x;
+        }
         tile::mm<kT, 2, DK / 16>(acc, N, kC + 1, 1, K, ld<DK>(), 1, kC);
         T *dq = at(static_cast<T *>(a.dq), a.sq, c.row, hk, c.t0);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int t = ty + 32 * i;
-            float x = 0.f;
 #pragma unroll
             for (int j = 0; j < DK / 16; ++j) {
                 const int d = tx + 16 * j;
-                x = fmaf(Q[t * ld<DK>() + d], acc[i][j], x);
                 if (t < c.len) {
                     if (shared) dqh[out_row + (long long)t * DK + d] = acc[i][j];
                     else tile::st_f(dq + t * a.sq.t + d, acc[i][j]);
                 }
             }
-            x = row16(x);
-            if (tx == 0) xq[t] = x;
         }
     }
     // dk and dv, with R in the same slabs; <R, S> on the way
@@ -442,18 +452,14 @@ __global__ void __launch_bounds__(kT) grad_kernel(LinAttnArgs a, View v, const f
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int t = ty + 32 * i;
-            float x = 0.f;
 #pragma unroll
             for (int j = 0; j < DK / 16; ++j) {
                 const int d = tx + 16 * j;
-                x = fmaf(K[t * ld<DK>() + d], own[i][j], x);
                 if (t < c.len) {
                     if (shared) dkh[out_row + (long long)t * DK + d] = acc[i][j] + own[i][j];
                     else tile::st_f(dk + t * a.sk.t + d, acc[i][j] + own[i][j]);
                 }
             }
-            x = row16(x);
-            if (tx == 0) xk[t] = x;
         }
     }
 #pragma unroll
@@ -465,7 +471,7 @@ __global__ void __launch_bounds__(kT) grad_kernel(LinAttnArgs a, View v, const f
         if (u < c.len) {
             float x = 0.f, d = 0.f;
             for (int w = 0; w < kT / 32; ++w) d += red[w];
-            for (int t = 0; t < kC; ++t) x += t < u ? xr[t] : xq[t] - xk[t];
+            for (int t = 0; t < kC; ++t) x += t < u ? xr[t] : xq[t] + (xa[t] - xk[t]);
             at(dgt, sdg, c.row, h, c.t0)[u * sdg.t] = fmaf(expf(hi[c.len - 1]), d, x);
         }
     }
@@ -536,7 +542,7 @@ template <typename T, int DK, int DV>
 int run_bwd(const LinAttnArgs &a, const View &v, const BwdWs &w, cudaStream_t stream) {
     LA_TRY((run_states<T, DK, DV, false>(a, v, w.U, w.decay, stream)));
     LA_TRY((run_states<T, DK, DV, true>(a, v, w.R, w.decay, stream)));
-    const int smem = 4 * (kC * (2 * ld<DK>() + 2 * ld<DV>() + 2 * (kC + 1)) + DK * 65 + 6 * kC + 32);
+    const int smem = 4 * (kC * (2 * ld<DK>() + 2 * ld<DV>() + 2 * (kC + 1)) + DK * 65 + 7 * kC + 32);
     LA_TRY(smem_limit(grad_kernel<T, DK, DV>, smem));
     const bool per_head = a.flags & GDN_G_PER_HEAD;
     const Strides whole{(long long)a.H * a.T, a.T, 1};

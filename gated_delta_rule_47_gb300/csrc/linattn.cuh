@@ -71,17 +71,27 @@ __device__ __forceinline__ float clamp_g(float g) { return g < -100.f ? -100.f :
 // difference alone, not of its two large terms), and to_end[t] = g_{t+1} + ..
 // The sums are made in 64 bits.  Tokens past len count 0.
 template <int C>
-__device__ __forceinline__ void gates(const float *g, long long step, int len, bool per_head, float *cum_hi,
-                                      float *cum_lo, float *to_end) {
-    constexpr int P = C / 32;
+struct Gates {
+    static constexpr int P = C / 32;  // lane's tokens: lane P .. lane P + P - 1
+    double cum[P], all;
+};
+
+template <int C>
+__device__ __forceinline__ Gates<C> warp_gates(const float *g, long long step, int len, bool per_head) {
+    constexpr int P = Gates<C>::P;
     const int lane = threadIdx.x & 31;
-    double x[P], sum = 0.;
+    Gates<C> r;
+    float gt[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         const int t = lane * P + i;
-        const float gt = t < len ? clamp_g(per_head ? g[0] : g[t * step]) : 0.f;
-        sum += gt;
-        x[i] = sum;
+        gt[i] = t < len ? clamp_g(per_head ? g[0] : g[t * step]) : 0.f;
+    }
+    double sum = 0.;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        sum += gt[i];
+        r.cum[i] = sum;
     }
     double run = sum;
 #pragma unroll
@@ -89,20 +99,34 @@ __device__ __forceinline__ void gates(const float *g, long long step, int len, b
         const double y = __shfl_up_sync(~0u, run, m);
         if (lane >= m) run += y;
     }
-    const double all = __shfl_sync(~0u, run, 31);
+    r.all = __shfl_sync(~0u, run, 31);
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const double c = run - sum + x[i];
-        const float hi = (float)c;
-        cum_hi[lane * P + i] = hi;
-        cum_lo[lane * P + i] = (float)(c - (double)hi);
-        to_end[lane * P + i] = (float)(all - c);
+    for (int i = 0; i < P; ++i) r.cum[i] += run - sum;
+    return r;
+}
+
+template <int C>
+__device__ __forceinline__ void gates(const float *g, long long step, int len, bool per_head, float *cum_hi,
+                                      float *cum_lo, float *to_end) {
+    const Gates<C> r = warp_gates<C>(g, step, len, per_head);
+#pragma unroll
+    for (int i = 0; i < Gates<C>::P; ++i) {
+        const int t = (threadIdx.x & 31) * Gates<C>::P + i;
+        const float hi = (float)r.cum[i];
+        cum_hi[t] = hi;
+        cum_lo[t] = (float)(r.cum[i] - (double)hi);
+        to_end[t] = (float)(r.all - r.cum[i]);
     }
 }
 
 // exp(cum[t] - cum[s]) from the pairs.
 __device__ __forceinline__ float decay_between(float hi_t, float lo_t, float hi_s, float lo_s) {
     return expf((hi_t - hi_s) + (lo_t - lo_s));
+}
+
+// Where head h's log-decays of a chunk start.
+__device__ __forceinline__ const float *gate_ptr(const LinAttnArgs &a, const Chunk &c, int h) {
+    return (a.flags & GDN_G_PER_HEAD) ? a.g + h : a.g + c.row * a.sg.b + h * a.sg.h + c.t0 * a.sg.t;
 }
 
 // First element of head h of token t of a strided tensor.

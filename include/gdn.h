@@ -505,7 +505,9 @@ int cam_prep_bwd(const void *q_raw, const void *k_raw, const float *q_norm_w, co
  *   strides host array of 15 element strides or NULL for contiguous tensors:
  *           (batch, head, token) of q, k, v, o, g; the last dimension is
  *           contiguous.  Those of q, k, v, o are multiples of 16 bytes
- *           (GDN_ERR_MISALIGNED).  A token-major [T,H,D] tensor is a
+ *           (GDN_ERR_MISALIGNED), not negative and, for bf16 q, k, v without
+ *           GDN_PATH_SIMT, not 0 over more than one element
+ *           (GDN_ERR_UNSUPPORTED).  A token-major [T,H,D] tensor is a
  *           [1,H,T,D] one with strides (0, D, H*D).
  *   flags   0 or GDN_G_PER_HEAD, GDN_PATH_SIMT
  *   Dk, Dv  64 or 128 each; n_seq, B and H up to 65535
