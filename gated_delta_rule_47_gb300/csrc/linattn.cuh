@@ -76,17 +76,23 @@ struct Gates {
     double cum[P], all;
 };
 
+// The lane's gates, as loaded ..
 template <int C>
-__device__ __forceinline__ Gates<C> warp_gates(const float *g, long long step, int len, bool per_head) {
+__device__ __forceinline__ void load_gates(const float *g, long long step, int len, bool per_head,
+                                           float (&gt)[C / 32]) {
+#pragma unroll
+    for (int i = 0; i < C / 32; ++i) {
+        const int t = (threadIdx.x & 31) * (C / 32) + i;
+        gt[i] = t < len ? clamp_g(per_head ? g[0] : g[t * step]) : 0.f;
+    }
+}
+
+// .. and their sums over the warp.
+template <int C>
+__device__ __forceinline__ Gates<C> scan_gates(const float (&gt)[C / 32]) {
     constexpr int P = Gates<C>::P;
     const int lane = threadIdx.x & 31;
     Gates<C> r;
-    float gt[P];
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const int t = lane * P + i;
-        gt[i] = t < len ? clamp_g(per_head ? g[0] : g[t * step]) : 0.f;
-    }
     double sum = 0.;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -108,7 +114,9 @@ __device__ __forceinline__ Gates<C> warp_gates(const float *g, long long step, i
 template <int C>
 __device__ __forceinline__ void gates(const float *g, long long step, int len, bool per_head, float *cum_hi,
                                       float *cum_lo, float *to_end) {
-    const Gates<C> r = warp_gates<C>(g, step, len, per_head);
+    float gt[C / 32];
+    load_gates<C>(g, step, len, per_head, gt);
+    const Gates<C> r = scan_gates<C>(gt);
 #pragma unroll
     for (int i = 0; i < Gates<C>::P; ++i) {
         const int t = (threadIdx.x & 31) * Gates<C>::P + i;

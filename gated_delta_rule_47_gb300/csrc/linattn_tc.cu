@@ -1,24 +1,22 @@
 // linattn_tc.cu -- linear attention with a decay for each head over whole
 // prompts on the tensor cores (bf16, tcgen05), in chunks of 128 tokens.  The
-// formulas are linattn.cu's.  Two launches:
+// formulas are linattn.cu's.
 //
-// state_kernel walks a sequence's chunks with the state in registers and
-// writes the state that enters each chunk as a bf16 operand.  A CTA owns 64
-// value columns of one head (columns are independent, and only the value
-// tile is weighted, so nothing is computed twice).  The chunk's own share
-// K^T diag(w) V is one product that does not depend on the state, so the walk
-// itself costs one multiply-add an element and chunk.  The weighted values
-// w v go in as three bf16 terms (x = hi + mid + lo to 2^-24): with one, the
-// state would carry 2^-9 of rounding in every term, against inputs that are
-// exact; sums and state stay in fp32.
-//
-// out_kernel takes every chunk by itself: O = e^c (Q S) + (Q K^T o D) V with
-// the decay mask D applied in fp32 between the two products.  P and S enter
-// the products rounded to bf16: each adds about as much as the output's own
+// prompt_kernel is the forward in one launch.  A CTA owns 64 value columns of
+// one head (columns are independent) and walks a sequence's chunks with the
+// state in registers, so q, k, v and o cross the memory once (a head's two
+// CTAs run side by side and share q and k in L2).  A chunk is four products:
+// T = Q K^T; P V with P = T under the decay mask, in tensor memory; Q S; and
+// the chunk's own share of the state K^T diag(w) V, which does not depend on
+// the state, so the walk itself costs one multiply-add an element.
+// The weighted values w v go in as two or three bf16 terms (x = hi + mid + lo
+// to 2^-24): with one, the state would carry 2^-9 of rounding in every term,
+// against inputs that are exact; sums and state stay in fp32.  P and S enter
+// their products rounded to bf16: each adds about as much as the output's own
 // rounding does.
 //
-// Both are bound by the bytes of q, k, v, o and the states (k and v are read
-// twice, a state is 32 KB a chunk and head written and read).
+// state_kernel is the walk alone, for the backward, which wants the state that
+// enters each chunk and (backwards) the gradient of the one that leaves it.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
@@ -91,7 +89,7 @@ struct TcArgs {
 
 // ================================================================ state kernel
 constexpr int kStages = 3;
-constexpr int kStateThreads = 480;  // warp 0 TMA, 1 MMA, 2..9 weighting, 10..13 state, 14 gates
+constexpr int kStateThreads = 512;  // warp 0 TMA, 1 MMA, 2..9 weighting, 10..13 state, 14..15 decays
 constexpr int kConv = 256, kSt = 128;
 constexpr int kWRing = 4;
 
@@ -318,12 +316,21 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             for (int e = 0; e < 64; e += 4)
                 *reinterpret_cast<float4 *>(to + page + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
     } else {
-        // the weights: e^{G - c_t}, or (REV) scale e^{c_t}
-        for (int i = 0; i < n; ++i) {
-            const int w = i % kWRing;
-            if (i >= kWRing && !la_wait(&bars[L::WEMPTY + w], ((i / kWRing) - 1) & 1, 16u, lim)) break;
+        // the weights of every other chunk: e^{G - c_t}, or (REV) scale e^{c_t};
+        // the next chunk's gates are on their way meanwhile
+        const bool per_head = p.a.flags & GDN_G_PER_HEAD;
+        float next[4];
+        auto fetch = [&](int i) {
+            if (i >= n) return;
             const Chunk c = chunk_at<kC>(p.v, p.a.T, chunk_of(i));
-            const Gates<kC> g = warp_gates<kC>(gate_ptr(p.a, c, h), p.a.sg.t, c.len, p.a.flags & GDN_G_PER_HEAD);
+            load_gates<kC>(gate_ptr(p.a, c, h), p.a.sg.t, c.len, per_head, next);
+        };
+        fetch(warp - 14);
+        for (int i = warp - 14; i < n; i += 2) {
+            const int w = i % kWRing;
+            const Gates<kC> g = scan_gates<kC>(next);
+            fetch(i + 2);
+            if (i >= kWRing && !la_wait(&bars[L::WEMPTY + w], ((i / kWRing) - 1) & 1, 16u, lim)) break;
             float4 x;
             if (REV) x = make_float4(expf((float)g.cum[0]), expf((float)g.cum[1]), expf((float)g.cum[2]), expf((float)g.cum[3]));
             else x = make_float4(expf((float)(g.all - g.cum[0])), expf((float)(g.all - g.cum[1])),
@@ -343,53 +350,109 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     }
 }
 
-// ================================================================== out kernel
-constexpr int kOutThreads = 256;
+// ================================================================ prompt kernel
+// Warps: 0 TMA, 1 MMA, 2..3 decays, 4..7 state and outputs, 8..11 P, 12..15 weighting.
+constexpr int kFwdThreads = 512;
+constexpr int kQKStages = 2, kVStages = 3, kGRing = 4;
+constexpr float kLog2e = 1.44269504088896341f;
 
-template <int DK, int DV>
-struct OutSmem {
-    static constexpr uint32_t Q = 0;              // later the rows of O
-    static constexpr uint32_t K = 32768;          // later P
-    static constexpr uint32_t S = 65536;          // later V
-    static constexpr uint32_t G = 98304;          // [2][128] decays
-    static constexpr uint32_t BAR = G + 1536;
-    enum { QK = 0, ST, VL, DQK, DQS, DPV, DRAIN, NUM };
+template <int DK>
+struct FwdSmem {
+    static constexpr uint32_t TB = DK * 256;                 // a chunk's Q or K
+    static constexpr uint32_t QK = 0;                        // [stage] K | Q
+    static constexpr uint32_t V = kQKStages * 2 * TB;        // [stage] 64 columns of V
+    static constexpr uint32_t X = V + kVStages * 16384;      // [2][3][32 tokens][128 B] weighted values
+    static constexpr uint32_t S = X + 2 * 3 * 4096;          // [DK][128 B] the state as an operand
+    static constexpr uint32_t G = S + DK * 128;              // [ring] weights [128] | log2 decays [128]
+    static constexpr uint32_t D = G + kGRing * 1024;         // [ring] chunk decays
+    static constexpr uint32_t BAR = D + 64;
+    enum { QKFULL = 0, QKEMPTY = 2, VFULL = 4, VEMPTY = 7, XREADY = 10, XEMPTY = 12, UFULL = 14, UEMPTY, SREADY, SEMPTY,
+           TFULL, TEMPTY = TFULL + 2, PREADY = TEMPTY + 2, PEMPTY, OFULL, OEMPTY, GFULL, GEMPTY = GFULL + kGRing,
+           DRAIN = GEMPTY + kGRing, NUM };
     static constexpr uint32_t TSLOT = BAR + 8 * NUM;
     static constexpr uint32_t BYTES = TSLOT + 16 + 1024;
 };
-static_assert(2 * (OutSmem<128, 128>::BYTES + 1024) <= 233472, "two CTAs of the out kernel share an SM");
+static_assert(FwdSmem<128>::BYTES <= 232448, "prompt kernel fits the shared memory of one CTA");
+// TMEM columns: Q K^T twice, P (two bf16 a column), Q S, P V, the chunk's share of the state
+constexpr uint32_t TM_T = 0, TM_P = 256, TM_OS = 320, TM_OP = 384, TM_U = 448;
 
-// A chunk's outputs.  Grid (chunks, H), two CTAs an SM: one's loads and
-// stores run under the other's products.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A's rows are lanes, two bf16 of a row a column.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Grid (DV / 64, H, n_seq, and one more for the tokens of no sequence).  A CTA walks the chunks of
+// one sequence for 64 value columns of one head.
 template <int DK, int DV>
-__global__ void __launch_bounds__(kOutThreads, 2)
-    out_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
-               const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mS, TcArgs p) {
-    using L = OutSmem<DK, DV>;
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
+                  const __grid_constant__ CUtensorMap mV, TcArgs p) {
+    using L = FwdSmem<DK>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::TSLOT);
-    float *hi = reinterpret_cast<float *>(sm + L::G), *lo = hi + 128, *te = lo + 128;
+    float *gring = reinterpret_cast<float *>(sm + L::G), *dring = reinterpret_cast<float *>(sm + L::D);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int ci = blockIdx.x, h = blockIdx.y;
-    const Chunk c = chunk_at<kC>(p.v, p.a.T, ci);
-    __nv_bfloat16 *out = at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, c.row, h, c.t0);
-    if (c.len <= 0) return;
-    if (c.seq < 0) {  // tokens of no sequence
-        for (int e = threadIdx.x; e < c.len * (DV / 8); e += kOutThreads)
-            *reinterpret_cast<uint4 *>(out + (e / (DV / 8)) * p.a.so.t + (e % (DV / 8)) * 8) = make_uint4(0, 0, 0, 0);
+    const int slice = blockIdx.x, h = blockIdx.y, seq = blockIdx.z;
+    const unsigned long long lim = p.timeout_ns;
+    if (seq >= p.a.n_seq) {  // packed: zeros for the tokens of no sequence
+        const int T = p.a.T, head = min(max(p.a.cu[0], 0), T), tail = min(max(p.a.cu[p.a.n_seq], 0), T);
+        for (int e = threadIdx.x; e < (head + T - tail) * 8; e += kFwdThreads) {
+            const int i = e >> 3, t = i < head ? i : tail + i - head;
+            *reinterpret_cast<uint4 *>(at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, 0, h, t) + 64 * slice + (e & 7) * 8) =
+                make_uint4(0, 0, 0, 0);
+        }
         return;
     }
-    // a first chunk without an initial state has nothing to read
-    const bool with_state = p.a.s0 != nullptr || seq_at(p.v, c.seq).x != ci;
-    const unsigned long long lim = p.timeout_ns;
+    const int2 sq = seq_at(p.v, seq);
+    const int n = sq.y;
+    // the final state is an fp32 output: three bf16 terms a weighted value; for
+    // bf16 outputs alone two (2^-16) are far below their rounding
+    const int terms = p.a.sf ? 3 : 2;
+
     if (threadIdx.x == 0) {
-        for (int b = 0; b < L::NUM; ++b) mbar_init(&bars[b], 1);
+        for (int s = 0; s < kQKStages; ++s) {
+            mbar_init(&bars[L::QKFULL + s], 1);
+            mbar_init(&bars[L::QKEMPTY + s], 1);
+            mbar_init(&bars[L::XREADY + s], 128);
+            mbar_init(&bars[L::XEMPTY + s], 1);
+            mbar_init(&bars[L::TFULL + s], 1);
+            mbar_init(&bars[L::TEMPTY + s], 128);
+        }
+        for (int s = 0; s < kVStages; ++s) {
+            mbar_init(&bars[L::VFULL + s], 1);
+            mbar_init(&bars[L::VEMPTY + s], 1);
+        }
+        for (int s = 0; s < kGRing; ++s) {
+            mbar_init(&bars[L::GFULL + s], 32);
+            mbar_init(&bars[L::GEMPTY + s], 384);
+        }
+        mbar_init(&bars[L::UFULL], 1);
+        mbar_init(&bars[L::UEMPTY], 128);
+        mbar_init(&bars[L::SREADY], 128);
+        mbar_init(&bars[L::SEMPTY], 1);
+        mbar_init(&bars[L::PREADY], 128);
+        mbar_init(&bars[L::PEMPTY], 1);
+        mbar_init(&bars[L::OFULL], 1);
+        mbar_init(&bars[L::OEMPTY], 128);
+        mbar_init(&bars[L::DRAIN], 1);
         fence_mbar_init();
     }
     if (warp == 1) {
-        tmem_alloc(tslot, 256);
+        tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
     tc_fence_before_sync();
@@ -397,159 +460,301 @@ __global__ void __launch_bounds__(kOutThreads, 2)
     tc_fence_after_sync();
     const uint32_t tmem = *tslot;
     const uint32_t sbase = smem_u32(sm);
-    const int hk = h / (p.a.H / p.a.Hk);
-    bool ok = true, v_armed = false;
-    auto load_v = [&] {
-        v_armed = true;
-        mbar_arrive_expect_tx(&bars[L::VL], DV * 256);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const int hk = h / (p.a.H / p.a.Hk);
+            int iq = 0, iv = 0;
+            for (int i = 0; i < n; ++i) {
+                const Chunk c = chunk_at<kC>(p.v, p.a.T, sq.x + i);
+                const int s = i % kQKStages, v = i % kVStages;
+                if (i >= kQKStages && !la_wait(&bars[L::QKEMPTY + s], (i / kQKStages - 1) & 1, 1u, lim)) break;
+                uint8_t *st = sm + L::QK + s * 2 * L::TB;
+                mbar_arrive_expect_tx(&bars[L::QKFULL + s], 2 * L::TB);
 #pragma unroll
-        for (int x = 0; x < DV / 64; ++x) tma_load_4d(sm + L::S + x * 16384, &mV, &bars[L::VL], 64 * x, c.t0, h, c.row);
-    };
-    if (warp == 0 && lane == 0) {
-        mbar_arrive_expect_tx(&bars[L::QK], 2 * DK * 256);
-#pragma unroll
-        for (int x = 0; x < DK / 64; ++x) {
-            tma_load_4d(sm + L::Q + x * 16384, &mQ, &bars[L::QK], 64 * x, c.t0, hk, c.row);
-            tma_load_4d(sm + L::K + x * 16384, &mK, &bars[L::QK], 64 * x, c.t0, hk, c.row);
+                for (int x = 0; x < DK / 64; ++x) {
+                    tma_load_4d(st + x * 16384, &mK, &bars[L::QKFULL + s], 64 * x, c.t0, hk, c.row);
+                    tma_load_4d(st + L::TB + x * 16384, &mQ, &bars[L::QKFULL + s], 64 * x, c.t0, hk, c.row);
+                }
+                ++iq;
+                if (i >= kVStages && !la_wait(&bars[L::VEMPTY + v], (i / kVStages - 1) & 1, 1u, lim)) break;
+                mbar_arrive_expect_tx(&bars[L::VFULL + v], 16384);
+                tma_load_4d(sm + L::V + v * 16384, &mV, &bars[L::VFULL + v], 64 * slice, c.t0, h, c.row);
+                ++iv;
+            }
+            // no copy is in flight when the CTA ends
+            for (int j = iq > kQKStages ? iq - kQKStages : 0; j < iq; ++j)
+                mbar_wait(&bars[L::QKFULL + j % kQKStages], (j / kQKStages) & 1, kDrainNs);
+            for (int j = iv > kVStages ? iv - kVStages : 0; j < iv; ++j)
+                mbar_wait(&bars[L::VFULL + j % kVStages], (j / kVStages) & 1, kDrainNs);
         }
-        if (with_state) {
-            mbar_arrive_expect_tx(&bars[L::ST], DK * DV * 2);
-#pragma unroll
-            for (int x = 0; x < DV / 64; ++x)
-                tma_load_3d(sm + L::S + x * (DK * 128), &mS, &bars[L::ST], 64 * x, 0, ci * p.a.H + h);
-        } else {
-            load_v();
-        }
-        ok = la_wait(&bars[L::QK], 0, 32u, lim);
-        if (ok) {
-            const uint32_t id = idesc_bf16(128, 128, false, false);
-#pragma unroll
-            for (int ks = 0; ks < DK / 16; ++ks)
-                mma_bf16_ss(tmem, smem_desc(sbase + L::Q + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
-                            smem_desc(sbase + L::K + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024), id, ks > 0);
-            mma_commit(&bars[L::DQK]);
-        }
-        if (with_state) {
-            ok = la_wait(&bars[L::ST], 0, 32u, lim) && ok;
-            if (ok) {
-                const uint32_t id = idesc_bf16(128, DV, false, true);
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idT = idesc_bf16(128, 128, false, false), idU = idesc_bf16(128, 64, true, true),
+                           idO = idesc_bf16(128, 64, false, true);
+            auto stage = [&](int i) { return sbase + L::QK + (i % kQKStages) * 2 * L::TB; };
+            auto qk = [&](int i) {
+                bool ok = la_wait(&bars[L::QKFULL + i % kQKStages], (i / kQKStages) & 1, 2u, lim);
+                if (i >= 2) ok = ok && la_wait(&bars[L::TEMPTY + (i & 1)], (i / 2 - 1) & 1, 2u, lim);
+                if (!ok) return false;
+                tc_fence_after_sync();
+                const uint32_t k = stage(i), q = k + L::TB;
 #pragma unroll
                 for (int ks = 0; ks < DK / 16; ++ks)
-                    mma_bf16_ss(tmem + 128, smem_desc(sbase + L::Q + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
-                                smem_desc(sbase + L::S + ks * 2048, DK * 128, 1024), id, ks > 0);
-                mma_commit(&bars[L::DQS]);
-                ok = la_wait(&bars[L::DQS], 0, 32u, lim);  // S's place is V's now
-                if (ok) load_v();
-            }
-        }
-    } else if (warp == 2) {
-        gates<kC>(gate_ptr(p.a, c, h), p.a.sg.t, c.len, p.a.flags & GDN_G_PER_HEAD, hi, lo, te);
-    }
-    __syncwarp();
-    __syncthreads();  // the decays are there
-    // P: thread's row t, columns s of its half
-    const int t = 32 * (warp & 3) + lane, s0 = 64 * (warp >> 2);
-    if (!warp_ok(la_wait(&bars[L::DQK], 0, 64u, lim))) ok = false;
-    if (warp_ok(ok)) {
-        tc_fence_after_sync();
-        const float ht = hi[t], lt = lo[t];
+                    mma_bf16_ss(tmem + TM_T + 128u * (i & 1), smem_desc(q + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
+                                smem_desc(k + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024), idT, ks > 0);
+                mma_commit(&bars[L::TFULL + (i & 1)]);
+                return true;
+            };
+            bool ok = n > 0 && qk(0);
+            for (int i = 0; i < n && ok; ++i) {
+                const uint32_t k = stage(i), q = k + L::TB;
+                if (i >= 1) ok = la_wait(&bars[L::UEMPTY], (i - 1) & 1, 2u, lim);
+                for (int qd = 0; qd < 4 && ok; ++qd) {
+                    const int b = qd & 1, use = 2 * i + (qd >> 1);
+                    ok = la_wait(&bars[L::XREADY + b], use & 1, 2u, lim);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint32_t xb = sbase + L::X + b * 3 * 4096;
+                    for (int t = 0; t < terms; ++t)
 #pragma unroll
-        for (int e = 0; e < 64; e += 16) {
-            uint32_t u[16];
-            float x[16];
-            if (32 * (warp & 3) + 31 >= s0 + e) {  // some row of the warp reaches these columns
-                tmem_ld16(tmem + lane_base(warp) + s0 + e, u);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int s = s0 + e + j;
-                    x[j] = s <= t ? __uint_as_float(u[j]) * __expf((ht - hi[s]) + (lt - lo[s])) : 0.f;
+                        for (int ks = 0; ks < 2; ++ks)
+                            mma_bf16_ss(tmem + TM_U, smem_desc(k + (2 * qd + ks) * 2048, 16384, 1024),
+                                        smem_desc(xb + t * 4096 + ks * 2048, 8192, 1024), idU, (qd | t | ks) ? 1u : 0u);
+                    mma_commit(&bars[L::XEMPTY + b]);
                 }
-            } else {
+                if (ok) mma_commit(&bars[L::UFULL]);
+                ok = ok && la_wait(&bars[L::SREADY], i & 1, 2u, lim);
+                if (i >= 1) ok = ok && la_wait(&bars[L::OEMPTY], (i - 1) & 1, 2u, lim);
+                if (!ok) break;
+                tc_fence_after_sync();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = 0.f;
+                for (int ks = 0; ks < DK / 16; ++ks)
+                    mma_bf16_ss(tmem + TM_OS, smem_desc(q + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
+                                smem_desc(sbase + L::S + ks * 2048, 8192, 1024), idO, ks > 0);
+                mma_commit(&bars[L::SEMPTY]);
+                mma_commit(&bars[L::QKEMPTY + i % kQKStages]);
+                if (i + 1 < n) ok = qk(i + 1);
+                ok = ok && la_wait(&bars[L::PREADY], i & 1, 2u, lim);
+                ok = ok && la_wait(&bars[L::VFULL + i % kVStages], (i / kVStages) & 1, 2u, lim);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint32_t v = sbase + L::V + (i % kVStages) * 16384;
+#pragma unroll
+                for (int ks = 0; ks < kC / 16; ++ks)
+                    mma_bf16_ts(tmem + TM_OP, tmem + TM_P + 8 * ks, smem_desc(v + ks * 2048, 8192, 1024), idO, ks > 0);
+                mma_commit(&bars[L::PEMPTY]);
+                mma_commit(&bars[L::VEMPTY + i % kVStages]);
+                mma_commit(&bars[L::OFULL]);
             }
-#pragma unroll
-            for (int j = 0; j < 16; j += 8)
-                *reinterpret_cast<uint4 *>(sm + L::K + (s0 >> 6) * 16384 + sw128_offset(t, e + j)) =
-                    make_uint4(pack_bf16(x[j], x[j + 1]), pack_bf16(x[j + 2], x[j + 3]), pack_bf16(x[j + 4], x[j + 5]),
-                               pack_bf16(x[j + 6], x[j + 7]));
-        }
-    }
-    ok = warp_ok(la_wait(&bars[L::VL], 0, 64u, lim)) && ok;
-    if (c.len < kC && ok) {  // another sequence's rows: zeros, as in state_kernel
-        for (int e = threadIdx.x; e < (kC - c.len) * (DV / 8); e += kOutThreads) {
-            const int row = c.len + e / (DV / 8), col = (e % (DV / 8)) * 8;
-            *reinterpret_cast<uint4 *>(sm + L::S + (col >> 6) * 16384 + sw128_offset(row, col & 63)) = make_uint4(0, 0, 0, 0);
-        }
-    }
-    fence_proxy_async_smem();
-    tc_fence_before_sync();
-    ok = __syncthreads_and(ok);
-    if (ok) {
-        if (warp == 0 && lane == 0) {
-            tc_fence_after_sync();
-            const uint32_t id = idesc_bf16(128, DV, false, true);
-#pragma unroll
-            for (int ks = 0; ks < kC / 16; ++ks)
-                mma_bf16_ss(tmem, smem_desc(sbase + L::K + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
-                            smem_desc(sbase + L::S + ks * 2048, 16384, 1024), id, ks > 0);
-            mma_commit(&bars[L::DPV]);
-        }
-        __syncwarp();
-        ok = warp_ok(la_wait(&bars[L::DPV], 0, 128u, lim));
-    }
-    if (ok) {
-        // the rows of O: scale (e^c (Q S) + P V), through Q's place, so that
-        // the stores are whole rows
-        tc_fence_after_sync();
-        const float f = __expf(hi[t]) * p.a.scale;
-        constexpr int W = DV / 2;  // columns of a thread
-        const int w0 = W * (warp >> 2);
-#pragma unroll
-        for (int e = 0; e < W; e += 16) {
-            uint32_t u[16], y[16];
-            tmem_ld16(tmem + lane_base(warp) + w0 + e, u);
-            if (with_state) tmem_ld16(tmem + 128 + lane_base(warp) + w0 + e, y);
-            tmem_wait_ld();
-            float x[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                x[j] = p.a.scale * __uint_as_float(u[j]);
-                if (with_state) x[j] = fmaf(f, __uint_as_float(y[j]), x[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < 16; j += 8) {
-                const int ch = (w0 + e + j) >> 3;
-                *reinterpret_cast<uint4 *>(sm + L::Q + t * (DV * 2) + ((ch ^ (t & 7)) << 4)) =
-                    make_uint4(pack_bf16(x[j], x[j + 1]), pack_bf16(x[j + 2], x[j + 3]), pack_bf16(x[j + 4], x[j + 5]),
-                               pack_bf16(x[j + 6], x[j + 7]));
-            }
-        }
-    }
-    tc_fence_before_sync();
-    ok = __syncthreads_and(ok);
-    if (ok)
-        for (int e = threadIdx.x; e < c.len * (DV / 8); e += kOutThreads) {
-            const int row = e / (DV / 8), ch = e % (DV / 8);
-            *reinterpret_cast<uint4 *>(out + row * p.a.so.t + ch * 8) =
-                *reinterpret_cast<const uint4 *>(sm + L::Q + row * (DV * 2) + ((ch ^ (row & 7)) << 4));
-        }
-    if (!ok) {  // a wait gave up: no copy and no product is in flight when the CTA ends
-        if (threadIdx.x == 0) {
+            // every MMA issued here is complete before TMEM is released
             mma_commit(&bars[L::DRAIN]);
             mbar_wait(&bars[L::DRAIN], 0, kDrainNs);
-            mbar_wait(&bars[L::QK], 0, kDrainNs);
-            if (with_state) mbar_wait(&bars[L::ST], 0, kDrainNs);
-            if (v_armed) mbar_wait(&bars[L::VL], 0, kDrainNs);
         }
-        __syncwarp();
-        tc_fence_before_sync();
-        __syncthreads();
+    } else if (warp < 4) {
+        // decays of every other chunk: e^{G - c_t}, log2(e) c_t and e^G; the
+        // next chunk's gates are on their way meanwhile
+        const bool per_head = p.a.flags & GDN_G_PER_HEAD;
+        float next[4];
+        auto fetch = [&](int i) {
+            if (i >= n) return;
+            const Chunk c = chunk_at<kC>(p.v, p.a.T, sq.x + i);
+            load_gates<kC>(gate_ptr(p.a, c, h), p.a.sg.t, c.len, per_head, next);
+        };
+        fetch(warp - 2);
+        for (int i = warp - 2; i < n; i += 2) {
+            const int w = i % kGRing;
+            const Gates<kC> g = scan_gates<kC>(next);
+            fetch(i + 2);
+            if (i >= kGRing && !la_wait(&bars[L::GEMPTY + w], (i / kGRing - 1) & 1, 16u, lim)) break;
+            float4 x, y;
+            x = make_float4(expf((float)(g.all - g.cum[0])), expf((float)(g.all - g.cum[1])),
+                            expf((float)(g.all - g.cum[2])), expf((float)(g.all - g.cum[3])));
+            y = make_float4((float)g.cum[0] * kLog2e, (float)g.cum[1] * kLog2e, (float)g.cum[2] * kLog2e, (float)g.cum[3] * kLog2e);
+            reinterpret_cast<float4 *>(gring + w * 256)[lane] = x;
+            reinterpret_cast<float4 *>(gring + w * 256 + 128)[lane] = y;
+            if (lane == 0) dring[w] = expf((float)g.all);
+            mbar_arrive(&bars[L::GFULL + w]);
+        }
+    } else if (warp < 8) {
+        // the state, one row of 64 columns a thread; and the rows of O
+        const int row = 32 * (warp & 3) + lane;
+        const bool mine = row < DK;
+        float S[64];
+        const size_t page = (((size_t)seq * p.a.H + h) * DK + row) * DV + 64 * slice;
+#pragma unroll
+        for (int e = 0; e < 64; e += 4) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (mine && p.a.s0) x = *reinterpret_cast<const float4 *>(p.a.s0 + page + e);
+            S[e] = x.x, S[e + 1] = x.y, S[e + 2] = x.z, S[e + 3] = x.w;
+        }
+        auto rows_out = [&](int i) {
+            const int w = i % kGRing;
+            if (!warp_ok(la_wait(&bars[L::OFULL], i & 1, 8u, lim))) return false;
+            tc_fence_after_sync();
+            const Chunk c = chunk_at<kC>(p.v, p.a.T, sq.x + i);
+            const float f = exp2_fast(gring[w * 256 + 128 + row]) * p.a.scale;
+            uint4 *out = reinterpret_cast<uint4 *>(at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, c.row, h, c.t0 + row) + 64 * slice);
+#pragma unroll
+            for (int e = 0; e < 64; e += 16) {
+                uint32_t u[16], y[16];
+                tmem_ld16(tmem + lane_base(warp) + TM_OS + e, u);
+                tmem_ld16(tmem + lane_base(warp) + TM_OP + e, y);
+                tmem_wait_ld();
+                float x[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = fmaf(f, __uint_as_float(u[j]), p.a.scale * __uint_as_float(y[j]));
+                if (row < c.len) {
+                    out[e / 8] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+                    out[e / 8 + 1] = make_uint4(pack_bf16(x[8], x[9]), pack_bf16(x[10], x[11]), pack_bf16(x[12], x[13]),
+                                                pack_bf16(x[14], x[15]));
+                }
+            }
+            tc_fence_before_sync();
+            mbar_arrive(&bars[L::OEMPTY]);
+            mbar_arrive(&bars[L::GEMPTY + w]);
+            return true;
+        };
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const int w = i % kGRing;
+            if (i >= 1) ok = la_wait(&bars[L::SEMPTY], (i - 1) & 1, 8u, lim);
+            if (!warp_ok(ok)) break;
+            if (mine)
+#pragma unroll
+                for (int e = 0; e < 64; e += 8)
+                    *reinterpret_cast<uint4 *>(sm + L::S + sw128_offset(row, e)) =
+                        make_uint4(pack_bf16(S[e], S[e + 1]), pack_bf16(S[e + 2], S[e + 3]), pack_bf16(S[e + 4], S[e + 5]),
+                                   pack_bf16(S[e + 6], S[e + 7]));
+            fence_proxy_async_smem();
+            mbar_arrive(&bars[L::SREADY]);
+            if (i >= 1) ok = rows_out(i - 1);
+            ok = ok && la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, 8u, lim);
+            const float d = ok ? dring[w] : 0.f;
+            ok = ok && la_wait(&bars[L::UFULL], i & 1, 8u, lim);
+            if (!warp_ok(ok)) break;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int e = 0; e < 64; e += 16) {
+                uint32_t u[16];
+                tmem_ld16(tmem + lane_base(warp) + TM_U + e, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) S[e + j] = fmaf(d, S[e + j], __uint_as_float(u[j]));
+            }
+            tc_fence_before_sync();
+            mbar_arrive(&bars[L::UEMPTY]);
+        }
+        if (warp_ok(ok) && n > 0) ok = rows_out(n - 1);
+        if (p.a.sf && mine && ok)
+#pragma unroll
+            for (int e = 0; e < 64; e += 4)
+                *reinterpret_cast<float4 *>(p.a.sf + page + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+    } else if (warp < 12) {
+        // P: thread's row t; columns past the warp's last row are zeros for good
+        const int t = 32 * (warp & 3) + lane, cols = 32 * (warp & 3) + 32;
+        {
+            uint32_t z[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) z[j] = 0u;
+            for (int s = cols; s < kC; s += 32) tmem_st16(tmem + lane_base(warp) + TM_P + s / 2, z);
+        }
+        for (int i = 0; i < n; ++i) {
+            const int w = i % kGRing;
+            bool ok = la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, 32u, lim);
+            ok = ok && la_wait(&bars[L::TFULL + (i & 1)], (i / 2) & 1, 32u, lim);
+            if (i >= 1) ok = ok && la_wait(&bars[L::PEMPTY], (i - 1) & 1, 32u, lim);
+            if (!warp_ok(ok)) break;
+            tc_fence_after_sync();
+            const float *c2 = gring + w * 256 + 128;
+            const float ct = c2[t];
+            for (int s = 0; s < cols; s += 32) {
+                uint32_t u[32], y[16];
+                tmem_ld16(tmem + lane_base(warp) + TM_T + 128u * (i & 1) + s, *reinterpret_cast<uint32_t(*)[16]>(u));
+                tmem_ld16(tmem + lane_base(warp) + TM_T + 128u * (i & 1) + s + 16, *reinterpret_cast<uint32_t(*)[16]>(u + 16));
+                tmem_wait_ld();
+                const bool edge = s + 32 == cols;  // the block on the diagonal
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 cs = *reinterpret_cast<const float4 *>(c2 + s + j);
+                    float x[4] = {__uint_as_float(u[j]) * exp2_fast(ct - cs.x), __uint_as_float(u[j + 1]) * exp2_fast(ct - cs.y),
+                                  __uint_as_float(u[j + 2]) * exp2_fast(ct - cs.z), __uint_as_float(u[j + 3]) * exp2_fast(ct - cs.w)};
+                    if (edge)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[k] = s + j + k <= t ? x[k] : 0.f;
+                    y[j / 2] = pack_bf16(x[0], x[1]);
+                    y[j / 2 + 1] = pack_bf16(x[2], x[3]);
+                }
+                tmem_st16(tmem + lane_base(warp) + TM_P + s / 2, y);
+            }
+            tmem_wait_st();
+            tc_fence_before_sync();
+            mbar_arrive(&bars[L::TEMPTY + (i & 1)]);
+            mbar_arrive(&bars[L::PREADY]);
+            mbar_arrive(&bars[L::GEMPTY + w]);
+        }
+    } else {
+        // the weighted values, in quarters of 32 tokens: row r, 16 columns
+        const int ct = threadIdx.x - 384, r = ct >> 2, c0 = (ct & 3) * 16;
+        for (int i = 0; i < n; ++i) {
+            const int v = i % kVStages, w = i % kGRing;
+            const Chunk c = chunk_at<kC>(p.v, p.a.T, sq.x + i);
+            bool ok = la_wait(&bars[L::VFULL + v], (i / kVStages) & 1, 4u, lim);
+            ok = ok && la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, 4u, lim);
+            uint8_t *vt = sm + L::V + v * 16384;
+            if (ok && c.len < kC) {
+                // rows past the chunk's tokens are another sequence's: zeros, so
+                // that nothing of theirs (an infinity, say) meets a zero weight
+                ok = la_wait(&bars[L::QKFULL + i % kQKStages], (i / kQKStages) & 1, 4u, lim);
+                uint8_t *k = sm + L::QK + (i % kQKStages) * 2 * L::TB;
+                if (ok)
+                    for (int e = ct; e < (kC - c.len) * (DK / 8); e += 128) {
+                        const int row = c.len + e / (DK / 8), col = (e % (DK / 8)) * 8;
+                        *reinterpret_cast<uint4 *>(k + (col >> 6) * 16384 + sw128_offset(row, col & 63)) = make_uint4(0, 0, 0, 0);
+                    }
+                if (ok)
+                    for (int e = ct; e < (kC - c.len) * 8; e += 128)
+                        *reinterpret_cast<uint4 *>(vt + sw128_offset(c.len + (e >> 3), (e & 7) * 8)) = make_uint4(0, 0, 0, 0);
+            }
+            if (!warp_ok(ok)) break;
+#pragma unroll 1
+            for (int qd = 0; qd < 4; ++qd) {
+                const int b = qd & 1, use = 2 * i + (qd >> 1), t = 32 * qd + r;
+                const float wt = gring[w * 256 + t];
+                float x[2][8];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    unpack8(*reinterpret_cast<const uint4 *>(vt + sw128_offset(t, c0 + 8 * u)), x[u]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[u][e] = t < c.len ? x[u][e] * wt : 0.f;
+                }
+                if (use >= 1 && !la_wait(&bars[L::XEMPTY + b], (use - 1) & 1, 4u, lim)) ok = false;
+                if (!warp_ok(ok)) break;
+                uint8_t *xb = sm + L::X + b * 3 * 4096;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t off = sw128_offset(r, c0 + 8 * u);
+                    *reinterpret_cast<uint4 *>(xb + off) = take8(x[u]);
+                    if (terms == 3) {
+                        *reinterpret_cast<uint4 *>(xb + 4096 + off) = take8(x[u]);
+                        *reinterpret_cast<uint4 *>(xb + 8192 + off) = pack8(x[u]);
+                    } else {
+                        *reinterpret_cast<uint4 *>(xb + 4096 + off) = pack8(x[u]);
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&bars[L::XREADY + b]);
+            }
+            if (!warp_ok(ok)) break;
+            mbar_arrive(&bars[L::GEMPTY + w]);
+        }
     }
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
     if (warp == 1) {
         tc_fence_after_sync();
-        tmem_dealloc(tmem, 256);
+        tmem_dealloc(tmem, 512);
     }
 }
 
@@ -625,20 +830,13 @@ int run_fwd(const TcArgs &p, cudaStream_t stream) {
     const LinAttnArgs &a = p.a;
     if (!mappable(a.sq, a.B, a.Hk, a.T) || !mappable(a.sk, a.B, a.Hk, a.T) || !mappable(a.sv, a.B, a.H, a.T))
         return GDN_ERR_UNSUPPORTED;
-    CUtensorMap mQ, mK, mV, mS;
+    CUtensorMap mQ, mK, mV;
     if (!strided_map(&mQ, a.q, a.sq, a.B, a.Hk, a.T, DK, kC) || !strided_map(&mK, a.k, a.sk, a.B, a.Hk, a.T, DK, kC) ||
-        !strided_map(&mV, a.v, a.sv, a.B, a.H, a.T, DV, kC) ||
-        !state_map(&mS, p.Shi, (long long)p.v.n_chunks * a.H, DK, DV))
+        !strided_map(&mV, a.v, a.sv, a.B, a.H, a.T, DV, kC))
         return GDN_ERR_CUDA;
-    // one chunk a sequence, no state in or out: the outputs are all
-    if (a.cu || a.T > kC || a.s0 || a.sf) {
-        const int st = run_state<DK, DV, false, false>(mK, mV, p, stream);
-        if (st != GDN_OK) return st;
-    }
-    using L = OutSmem<DK, DV>;
-    auto kern = out_kernel<DK, DV>;
-    if (!smem_limit(kern, L::BYTES)) return GDN_ERR_CUDA;
-    kern<<<dim3(p.v.n_chunks, a.H), kOutThreads, L::BYTES, stream>>>(mQ, mK, mV, mS, p);
+    auto kern = prompt_kernel<DK, DV>;
+    if (!smem_limit(kern, FwdSmem<DK>::BYTES)) return GDN_ERR_CUDA;
+    kern<<<dim3(DV / 64, a.H, a.n_seq + (a.cu ? 1 : 0)), kFwdThreads, FwdSmem<DK>::BYTES, stream>>>(mQ, mK, mV, p);
     return launched();
 }
 
@@ -651,7 +849,7 @@ bool linattn_tc_supported(const LinAttnArgs &a) {
     return a.dtype == GDN_BF16 && !(a.flags & GDN_PATH_SIMT) && sm100_family();
 }
 
-size_t linattn_tc_fwd_workspace(const LinAttnArgs &a) { return up(table_bytes(a, kC)) + state_bytes(a) + 1024; }
+size_t linattn_tc_fwd_workspace(const LinAttnArgs &a) { return table_bytes(a, kC); }
 
 int launch_linattn_tc_fwd(const LinAttnArgs &a, cudaStream_t stream) {
     TcArgs p{};
@@ -659,7 +857,6 @@ int launch_linattn_tc_fwd(const LinAttnArgs &a, cudaStream_t stream) {
     p.timeout_ns = wait_limit_ns();
     const int st = make_view(a, kC, a.ws, &p.v, stream);
     if (st != GDN_OK) return st;
-    p.Shi = reinterpret_cast<uint16_t *>(static_cast<char *>(a.ws) + up(table_bytes(a, kC)));
     if (a.Dk == 128) return a.Dv == 128 ? run_fwd<128, 128>(p, stream) : run_fwd<128, 64>(p, stream);
     return a.Dv == 128 ? run_fwd<64, 128>(p, stream) : run_fwd<64, 64>(p, stream);
 }

@@ -510,7 +510,7 @@ int cam_prep_bwd(const void *q_raw, const void *k_raw, const float *q_norm_w, co
  *           (GDN_ERR_UNSUPPORTED).  A token-major [T,H,D] tensor is a
  *           [1,H,T,D] one with strides (0, D, H*D).
  *   flags   0 or GDN_G_PER_HEAD, GDN_PATH_SIMT
- *   Dk, Dv  64 or 128 each; n_seq, B and H up to 65535
+ *   Dk, Dv  64 or 128 each; n_seq and B up to 65534, H up to 65535
  *   workspace / workspace_bytes: linattn_chunk_fwd_workspace_bytes(...) bytes
  *           (packed: 1 where cu_seqlens is given), 16-byte aligned; no
  *           initialisation needed, contents not meaningful afterwards.

@@ -271,4 +271,4 @@ def test_refusals():
         three = inputs(1, 3, 3, 16, 64, 64, "bf16", 1)
         f(d["q"], d["k"], three["v"], three["g"])
     with pytest.raises(binding.GdnError):
-        f(d["q"], d["k"], d["v"], d["g"], workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        f(d["q"], d["k"], d["v"], d["g"], workspace=torch.empty(16, dtype=torch.uint8, device="cuda"), simt=True)
