@@ -66,14 +66,27 @@ int make_view(const LinAttnArgs &a, int C, void *ws, View *v, cudaStream_t strea
 // state).  A NaN stays one.
 __device__ __forceinline__ float clamp_g(float g) { return g < -100.f ? -100.f : g; }
 
+// A sum carried as hi + lo, to about 2^-45 (64-bit arithmetic is slow on this
+// GPU: a chunk's sums took a warp 4,300 cycles in it, and take 700 so).
+struct Pair {
+    float hi, lo;
+};
+__device__ __forceinline__ Pair add(const Pair &a, const Pair &b) {
+    const float s = a.hi + b.hi, bb = s - a.hi;
+    const float e = ((a.hi - (s - bb)) + (b.hi - bb)) + (a.lo + b.lo);
+    const float hi = s + e;
+    return {hi, e - (hi - s)};
+}
+
 // The running sums of a chunk's log-decays, by one warp: cum[t] = g_0 + .. +
-// g_t as a pair hi + lo (so that cum[t] - cum[s] carries the error of the
-// difference alone, not of its two large terms), and to_end[t] = g_{t+1} + ..
-// The sums are made in 64 bits.  Tokens past len count 0.
+// g_t, and all of them.  Differences of two sums, (a.hi - b.hi) + (a.lo -
+// b.lo), carry the error of the difference alone, not of its two large terms.
+// Tokens past len count 0.
 template <int C>
 struct Gates {
     static constexpr int P = C / 32;  // lane's tokens: lane P .. lane P + P - 1
-    double cum[P], all;
+    Pair cum[P], all;
+    __device__ __forceinline__ float to_end(int i) const { return (all.hi - cum[i].hi) + (all.lo - cum[i].lo); }
 };
 
 // The lane's gates, as loaded ..
@@ -93,21 +106,21 @@ __device__ __forceinline__ Gates<C> scan_gates(const float (&gt)[C / 32]) {
     constexpr int P = Gates<C>::P;
     const int lane = threadIdx.x & 31;
     Gates<C> r;
-    double sum = 0.;
+    r.cum[0] = {gt[0], 0.f};
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        sum += gt[i];
-        r.cum[i] = sum;
-    }
-    double run = sum;
+    for (int i = 1; i < P; ++i) r.cum[i] = add(r.cum[i - 1], {gt[i], 0.f});
+    Pair run = r.cum[P - 1];
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const double y = __shfl_up_sync(~0u, run, m);
-        if (lane >= m) run += y;
+        const Pair y = {__shfl_up_sync(~0u, run.hi, m), __shfl_up_sync(~0u, run.lo, m)};
+        const Pair z = add(run, y);
+        if (lane >= m) run = z;
     }
-    r.all = __shfl_sync(~0u, run, 31);
+    r.all = {__shfl_sync(~0u, run.hi, 31), __shfl_sync(~0u, run.lo, 31)};
+    Pair before = {__shfl_up_sync(~0u, run.hi, 1), __shfl_up_sync(~0u, run.lo, 1)};
+    if (lane == 0) before = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < P; ++i) r.cum[i] += run - sum;
+    for (int i = 0; i < P; ++i) r.cum[i] = add(before, r.cum[i]);
     return r;
 }
 
@@ -120,10 +133,9 @@ __device__ __forceinline__ void gates(const float *g, long long step, int len, b
 #pragma unroll
     for (int i = 0; i < Gates<C>::P; ++i) {
         const int t = (threadIdx.x & 31) * Gates<C>::P + i;
-        const float hi = (float)r.cum[i];
-        cum_hi[t] = hi;
-        cum_lo[t] = (float)(r.cum[i] - (double)hi);
-        to_end[t] = (float)(r.all - r.cum[i]);
+        cum_hi[t] = r.cum[i].hi;
+        cum_lo[t] = r.cum[i].lo;
+        to_end[t] = r.to_end(i);
     }
 }
 

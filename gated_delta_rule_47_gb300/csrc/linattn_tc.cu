@@ -36,19 +36,22 @@ constexpr int kC = 128;
 __device__ unsigned int g_la_error = 0;  // set when a bounded wait gives up
 constexpr unsigned long long kDrainNs = 200000000ull;
 
-// Waits for the phase of the given parity for at most limit ns; gives up at
-// once when another wait has.
-__device__ __forceinline__ bool la_wait(uint64_t *bar, uint32_t parity, unsigned code, unsigned long long limit) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-        if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
-        if (*reinterpret_cast<volatile unsigned *>(&g_la_error) != 0u) return false;
-        if (global_timer_ns() - t0 > limit) {
-            atomicOr(&g_la_error, code);
+// Waits for the phase of the given parity, until the CTA's deadline at most.
+// Small on purpose: the roles' loops share the instruction cache.
+__device__ __forceinline__ bool la_wait(uint64_t *bar, uint32_t parity, uint64_t deadline) {
+#pragma unroll 1
+    while (!mbar_try_wait_sleep(bar, parity, 20000u))
+        if (global_timer_ns() > deadline) {
+            *reinterpret_cast<volatile unsigned *>(&g_la_error) = 1u;
             return false;
         }
-    }
+    return true;
+}
+
+// When a CTA that walks n chunks gives up: the wait limit, and 50 us a chunk
+// for the work itself.
+__device__ __forceinline__ uint64_t deadline_after(unsigned long long limit, int n) {
+    return global_timer_ns() + limit + 50000ull * n;
 }
 
 // A wait's outcome made uniform across the warp, so that the warp's
@@ -77,6 +80,53 @@ __device__ __forceinline__ uint4 take8(float (&x)[8]) {
     return p;
 }
 
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// A weight as bf16 terms, each twice in a word: w = h + m + l to 2^-24.
+struct Weight {
+    uint32_t h, m, l;
+};
+__device__ __forceinline__ Weight split_weight(float w) {
+    Weight r;
+    r.h = pack_bf16(w, w);
+    w -= __uint_as_float(r.h & 0xffff0000u);
+    r.m = pack_bf16(w, w);
+    w -= __uint_as_float(r.m & 0xffff0000u);
+    r.l = pack_bf16(w, w);
+    return r;
+}
+
+// Two values times a weight as a sum of bf16 terms, in packed bf16 arithmetic.
+// hi is the rounded product with the weight's first term and r what that
+// rounding left, exactly (a product of two 8-bit mantissas has 16 bits).
+// Two terms: lo = v m + r, 2^-17 of the product off.  Three: mid = v m + r
+// rounded, and lo picks up what is left of it and v l; r - mid is exact
+// unless the two nearly cancel, so the sum is 2^-22 off or so.
+__device__ __forceinline__ void weigh2(uint32_t v, const Weight &w, uint32_t &hi, uint32_t &lo) {
+    hi = mul2(v, w.h);
+    lo = fma2(v, w.m, fma2(v, w.h, hi ^ 0x80008000u));
+}
+__device__ __forceinline__ void weigh3(uint32_t v, const Weight &w, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+    hi = mul2(v, w.h);
+    const uint32_t r = fma2(v, w.h, hi ^ 0x80008000u);
+    mid = fma2(v, w.m, r);
+    lo = fma2(v, w.l, fma2(v, w.m, sub2(r, mid)));
+}
+
 // What the tensor-core kernels take besides their maps.
 struct TcArgs {
     LinAttnArgs a;
@@ -85,6 +135,7 @@ struct TcArgs {
     uint16_t *Rhi, *Rlo;  // gradients of the states that leave them
     float *dot;           // [chunk][H][DV / 64][4] shares of <R, S>
     unsigned long long timeout_ns;
+    int wide;             // o's rows are 32-byte aligned
 };
 
 // ================================================================ state kernel
@@ -100,8 +151,8 @@ struct StateSmem {
     // with DK = 64 the product's rows 64..127 read the bytes after K, in the
     // stage's own V tile: rows that nobody looks at
     static constexpr uint32_t X = kStages * STAGE;        // [half][3][64 tokens][128 B] weighted values
-    static constexpr uint32_t W = X + 2 * 3 * 8192;       // [ring][128] weights, then [ring] chunk decays
-    static constexpr uint32_t BAR = W + kWRing * 512 + 64;
+    static constexpr uint32_t W = X + 2 * 3 * 8192;       // [ring][3][128] weights, then [ring] chunk decays
+    static constexpr uint32_t BAR = W + kWRing * 1536 + 64;
     enum { FULL = 0, EMPTY = 3, XREADY = 6, XEMPTY = 8, UFULL = 10, UEMPTY = 12, WFULL = 14, WEMPTY = 18, DRAIN = 22, NUM = 23 };
     static constexpr uint32_t TSLOT = BAR + 8 * NUM;
     static constexpr uint32_t BYTES = TSLOT + 16 + 1024;
@@ -119,12 +170,13 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::TSLOT);
-    float *wring = reinterpret_cast<float *>(sm + L::W), *dring = wring + kWRing * 128;
+    uint32_t *wring = reinterpret_cast<uint32_t *>(sm + L::W);
+    float *dring = reinterpret_cast<float *>(wring + kWRing * 384);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slice = blockIdx.x, h = blockIdx.y, seq = blockIdx.z;
     const int2 sq = seq_at(p.v, seq);
     const int n = sq.y;
-    const unsigned long long lim = p.timeout_ns;
+    const uint64_t end = deadline_after(p.timeout_ns, n);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -161,7 +213,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             int i = 0;
             for (; i < n; ++i) {
                 const int s = i % kStages;
-                if (i >= kStages && !la_wait(&bars[L::EMPTY + s], ((i / kStages) - 1) & 1, 1u, lim)) break;
+                if (i >= kStages && !la_wait(&bars[L::EMPTY + s], ((i / kStages) - 1) & 1, end)) break;
                 const Chunk c = chunk_at<kC>(p.v, p.a.T, chunk_of(i));
                 uint8_t *st = sm + s * L::STAGE;
                 mbar_arrive_expect_tx(&bars[L::FULL + s], L::STAGE);
@@ -171,6 +223,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 tma_load_4d(st + L::KB, &mV, &bars[L::FULL + s], 64 * slice, c.t0, h, c.row);
             }
             // no copy is in flight when the CTA ends
+#pragma unroll 1
             for (int j = i > kStages ? i - kStages : 0; j < i; ++j)
                 mbar_wait(&bars[L::FULL + j % kStages], (j / kStages) & 1, kDrainNs);
         }
@@ -178,12 +231,13 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         if (lane == 0) {
             const uint32_t id = idesc_bf16(128, 64, true, true);
             bool ok = true;
+#pragma unroll 1
             for (int i = 0; i < n && ok; ++i) {
                 const int s = i % kStages, acc = i & 1;
-                ok = la_wait(&bars[L::FULL + s], (i / kStages) & 1, 2u, lim);
-                if (ok && i >= 2) ok = la_wait(&bars[L::UEMPTY + acc], ((i >> 1) - 1) & 1, 2u, lim);
+                ok = la_wait(&bars[L::FULL + s], (i / kStages) & 1, end);
+                if (ok && i >= 2) ok = la_wait(&bars[L::UEMPTY + acc], ((i >> 1) - 1) & 1, end);
                 for (int half = 0; half < 2 && ok; ++half) {
-                    ok = la_wait(&bars[L::XREADY + half], i & 1, 2u, lim);
+                    ok = la_wait(&bars[L::XREADY + half], i & 1, end);
                     if (!ok) break;
                     tc_fence_after_sync();
                     const uint32_t ka = sbase + s * L::STAGE, xb = sbase + L::X + half * 3 * 8192;
@@ -208,16 +262,18 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     } else if (warp < 10) {
         // the weighted values, in two halves of 64 tokens: row r, 16 columns
         const int ct = threadIdx.x - 64, r = ct >> 2, c0 = (ct & 3) * 16;
+#pragma unroll 1
         for (int i = 0; i < n; ++i) {
             const int s = i % kStages, w = i % kWRing;
-            bool ok = la_wait(&bars[L::FULL + s], (i / kStages) & 1, 4u, lim);
-            ok = ok && la_wait(&bars[L::WFULL + w], (i / kWRing) & 1, 4u, lim);
+            bool ok = la_wait(&bars[L::FULL + s], (i / kStages) & 1, end);
+            ok = ok && la_wait(&bars[L::WFULL + w], (i / kWRing) & 1, end);
             if (!warp_ok(ok)) break;
             uint8_t *st = sm + s * L::STAGE;
             const Chunk c = chunk_at<kC>(p.v, p.a.T, chunk_of(i));
             if (c.len < kC) {
                 // rows past the chunk's tokens are another sequence's: zeros, so
                 // that nothing of theirs (an infinity, say) meets a zero weight
+#pragma unroll 1
                 for (int e = ct; e < (kC - c.len) * (DK / 8); e += kConv) {
                     const int row = c.len + e / (DK / 8), col = (e % (DK / 8)) * 8;
                     *reinterpret_cast<uint4 *>(st + (col >> 6) * 16384 + sw128_offset(row, col & 63)) = make_uint4(0, 0, 0, 0);
@@ -226,23 +282,26 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int t = half * 64 + r;
-                const float wt = wring[w * 128 + t];
-                float x[2][8];
+                const uint32_t *wr = wring + w * 384 + t;
+                const Weight wt = {wr[0], wr[128], wr[256]};
+                uint4 v[2];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    unpack8(*reinterpret_cast<const uint4 *>(st + L::KB + sw128_offset(t, c0 + 8 * u)), x[u]);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[u][e] = t < c.len ? x[u][e] * wt : 0.f;
+                    v[u] = *reinterpret_cast<const uint4 *>(st + L::KB + sw128_offset(t, c0 + 8 * u));
+                    if (t >= c.len) v[u] = make_uint4(0, 0, 0, 0);
                 }
-                if (i >= 1 && !la_wait(&bars[L::XEMPTY + half], (i - 1) & 1, 4u, lim)) ok = false;
+                if (i >= 1 && !la_wait(&bars[L::XEMPTY + half], (i - 1) & 1, end)) ok = false;
                 if (!warp_ok(ok)) break;
                 uint8_t *xb = sm + L::X + half * 3 * 8192;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const uint32_t off = sw128_offset(r, c0 + 8 * u);
-                    *reinterpret_cast<uint4 *>(xb + off) = take8(x[u]);
-                    *reinterpret_cast<uint4 *>(xb + 8192 + off) = take8(x[u]);
-                    *reinterpret_cast<uint4 *>(xb + 16384 + off) = pack8(x[u]);
+                    uint4 x, y, z;
+                    weigh3(v[u].x, wt, x.x, y.x, z.x), weigh3(v[u].y, wt, x.y, y.y, z.y);
+                    weigh3(v[u].z, wt, x.z, y.z, z.z), weigh3(v[u].w, wt, x.w, y.w, z.w);
+                    *reinterpret_cast<uint4 *>(xb + off) = x;
+                    *reinterpret_cast<uint4 *>(xb + 8192 + off) = y;
+                    *reinterpret_cast<uint4 *>(xb + 16384 + off) = z;
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&bars[L::XREADY + half]);
@@ -264,6 +323,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             S[e] = x.x, S[e + 1] = x.y, S[e + 2] = x.z, S[e + 3] = x.w;
         }
         bool ok = true;
+#pragma unroll 1
         for (int i = 0; i < n; ++i) {
             const int acc = i & 1, w = i % kWRing;
             const size_t ci = (size_t)chunk_of(i) * p.a.H + h;
@@ -293,9 +353,9 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(~0u, dot, m);
                 if (lane == 0) p.dot[(ci * (DV / 64) + slice) * 4 + (warp & 3)] = dot;
             }
-            ok = la_wait(&bars[L::WFULL + w], (i / kWRing) & 1, 8u, lim);
+            ok = la_wait(&bars[L::WFULL + w], (i / kWRing) & 1, end);
             const float d = ok ? dring[w] : 0.f;
-            ok = ok && la_wait(&bars[L::UFULL + acc], (i >> 1) & 1, 8u, lim);
+            ok = ok && la_wait(&bars[L::UFULL + acc], (i >> 1) & 1, end);
             if (!warp_ok(ok)) break;
             tc_fence_after_sync();
 #pragma unroll
@@ -326,18 +386,23 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             load_gates<kC>(gate_ptr(p.a, c, h), p.a.sg.t, c.len, per_head, next);
         };
         fetch(warp - 14);
+#pragma unroll 1
         for (int i = warp - 14; i < n; i += 2) {
             const int w = i % kWRing;
             const Gates<kC> g = scan_gates<kC>(next);
             fetch(i + 2);
-            if (i >= kWRing && !la_wait(&bars[L::WEMPTY + w], ((i / kWRing) - 1) & 1, 16u, lim)) break;
+            if (i >= kWRing && !la_wait(&bars[L::WEMPTY + w], ((i / kWRing) - 1) & 1, end)) break;
             float4 x;
-            if (REV) x = make_float4(expf((float)g.cum[0]), expf((float)g.cum[1]), expf((float)g.cum[2]), expf((float)g.cum[3]));
-            else x = make_float4(expf((float)(g.all - g.cum[0])), expf((float)(g.all - g.cum[1])),
-                                 expf((float)(g.all - g.cum[2])), expf((float)(g.all - g.cum[3])));
+            if (REV) x = make_float4(expf(g.cum[0].hi), expf(g.cum[1].hi), expf(g.cum[2].hi), expf(g.cum[3].hi));
+            else x = make_float4(expf(g.to_end(0)), expf(g.to_end(1)),
+                                 expf(g.to_end(2)), expf(g.to_end(3)));
             if (REV) x.x *= p.a.scale, x.y *= p.a.scale, x.z *= p.a.scale, x.w *= p.a.scale;
-            reinterpret_cast<float4 *>(wring + w * 128)[lane] = x;
-            if (lane == 0) dring[w] = expf((float)g.all);
+            uint4 *ws = reinterpret_cast<uint4 *>(wring + w * 384);
+            const Weight wa = split_weight(x.x), wb = split_weight(x.y), wc = split_weight(x.z), wd = split_weight(x.w);
+            ws[lane] = make_uint4(wa.h, wb.h, wc.h, wd.h);
+            ws[lane + 32] = make_uint4(wa.m, wb.m, wc.m, wd.m);
+            ws[lane + 64] = make_uint4(wa.l, wb.l, wc.l, wd.l);
+            if (lane == 0) dring[w] = expf(g.all.hi);
             mbar_arrive(&bars[L::WFULL + w]);
         }
     }
@@ -351,9 +416,9 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 }
 
 // ================================================================ prompt kernel
-// Warps: 0 TMA, 1 MMA, 2..3 decays, 4..7 state and outputs, 8..11 P, 12..15 weighting.
+// Warps: 0 TMA, 1 and 2 MMA, 3 decays, 4..7 state and outputs, 8..11 P, 12..15 weighting.
 constexpr int kFwdThreads = 512;
-constexpr int kQKStages = 2, kVStages = 3, kGRing = 4;
+constexpr int kQKStages = 2, kVStages = 2, kXRing = 3, kGRing = 4;
 constexpr float kLog2e = 1.44269504088896341f;
 
 template <int DK>
@@ -361,25 +426,34 @@ struct FwdSmem {
     static constexpr uint32_t TB = DK * 256;                 // a chunk's Q or K
     static constexpr uint32_t QK = 0;                        // [stage] K | Q
     static constexpr uint32_t V = kQKStages * 2 * TB;        // [stage] 64 columns of V
-    static constexpr uint32_t X = V + kVStages * 16384;      // [2][3][32 tokens][128 B] weighted values
-    static constexpr uint32_t S = X + 2 * 3 * 4096;          // [DK][128 B] the state as an operand
-    static constexpr uint32_t G = S + DK * 128;              // [ring] weights [128] | log2 decays [128]
+    static constexpr uint32_t X = V + kVStages * 16384;      // [ring][3][32 tokens][128 B] weighted values
+    static constexpr uint32_t S = X + kXRing * 3 * 4096;     // [DK][128 B] the state as an operand
+    static constexpr uint32_t W = S + DK * 128;              // [ring][3][128] weights
+    static constexpr uint32_t G = W + kGRing * 1536;         // [ring] log2 decays | block factors, 128 each
     static constexpr uint32_t D = G + kGRing * 1024;         // [ring] chunk decays
     static constexpr uint32_t BAR = D + 64;
-    enum { QKFULL = 0, QKEMPTY = 2, VFULL = 4, VEMPTY = 7, XREADY = 10, XEMPTY = 12, UFULL = 14, UEMPTY, SREADY, SEMPTY,
-           TFULL, TEMPTY = TFULL + 2, PREADY = TEMPTY + 2, PEMPTY, OFULL, OEMPTY, GFULL, GEMPTY = GFULL + kGRing,
-           DRAIN = GEMPTY + kGRing, NUM };
+    enum { QKFULL = 0, QKEMPTY = 2, VFULL = 4, VREADY = 6, VEMPTY = 8, XREADY = 10, XEMPTY = XREADY + kXRing, UFULL = XEMPTY + kXRing,
+           UEMPTY, SREADY, SEMPTY, TFULL, PREADY = TFULL + 2, OFULL = PREADY + 2, OEMPTY, OSFULL, OSEMPTY = OSFULL + 2, GFULL = OSEMPTY + 2, GEMPTY = GFULL + kGRing,
+           DRAIN = GEMPTY + kGRing, NUM = DRAIN + 2 };
     static constexpr uint32_t TSLOT = BAR + 8 * NUM;
     static constexpr uint32_t BYTES = TSLOT + 16 + 1024;
 };
 static_assert(FwdSmem<128>::BYTES <= 232448, "prompt kernel fits the shared memory of one CTA");
-// TMEM columns: Q K^T twice, P (two bf16 a column), Q S, P V, the chunk's share of the state
-constexpr uint32_t TM_T = 0, TM_P = 256, TM_OS = 320, TM_OP = 384, TM_U = 448;
+// TMEM columns: Q K^T twice (P, two bf16 a column, takes its first half), Q S
+// twice, P V, the chunk's share of the state
+constexpr uint32_t TM_T = 0, TM_OS = 256, TM_OP = 384, TM_U = 448;
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// 32 bytes to a 32-byte aligned address: whole sectors.
+__device__ __forceinline__ void st_global_32(void *p, const uint32_t (&x)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+                 "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]: A's rows are lanes, two bf16 of a row a column.
@@ -405,11 +479,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::TSLOT);
     float *gring = reinterpret_cast<float *>(sm + L::G), *dring = reinterpret_cast<float *>(sm + L::D);
+    uint32_t *wring = reinterpret_cast<uint32_t *>(sm + L::W);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slice = blockIdx.x, h = blockIdx.y, seq = blockIdx.z;
-    const unsigned long long lim = p.timeout_ns;
     if (seq >= p.a.n_seq) {  // packed: zeros for the tokens of no sequence
         const int T = p.a.T, head = min(max(p.a.cu[0], 0), T), tail = min(max(p.a.cu[p.a.n_seq], 0), T);
+#pragma unroll 1
         for (int e = threadIdx.x; e < (head + T - tail) * 8; e += kFwdThreads) {
             const int i = e >> 3, t = i < head ? i : tail + i - head;
             *reinterpret_cast<uint4 *>(at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, 0, h, t) + 64 * slice + (e & 7) * 8) =
@@ -422,19 +497,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     // the final state is an fp32 output: three bf16 terms a weighted value; for
     // bf16 outputs alone two (2^-16) are far below their rounding
     const int terms = p.a.sf ? 3 : 2;
+    const uint64_t end = deadline_after(p.timeout_ns, n);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kQKStages; ++s) {
             mbar_init(&bars[L::QKFULL + s], 1);
-            mbar_init(&bars[L::QKEMPTY + s], 1);
+            mbar_init(&bars[L::QKEMPTY + s], 2);
+            mbar_init(&bars[L::OSFULL + s], 1);
+            mbar_init(&bars[L::OSEMPTY + s], 128);
+            mbar_init(&bars[L::DRAIN + s], 1);
+            mbar_init(&bars[L::TFULL + s], 1);
+            mbar_init(&bars[L::PREADY + s], 128);
+        }
+        for (int s = 0; s < kXRing; ++s) {
             mbar_init(&bars[L::XREADY + s], 128);
             mbar_init(&bars[L::XEMPTY + s], 1);
-            mbar_init(&bars[L::TFULL + s], 1);
-            mbar_init(&bars[L::TEMPTY + s], 128);
         }
         for (int s = 0; s < kVStages; ++s) {
             mbar_init(&bars[L::VFULL + s], 1);
-            mbar_init(&bars[L::VEMPTY + s], 1);
+            mbar_init(&bars[L::VREADY + s], 128);
+            mbar_init(&bars[L::VEMPTY + s], 129);
         }
         for (int s = 0; s < kGRing; ++s) {
             mbar_init(&bars[L::GFULL + s], 32);
@@ -444,11 +526,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         mbar_init(&bars[L::UEMPTY], 128);
         mbar_init(&bars[L::SREADY], 128);
         mbar_init(&bars[L::SEMPTY], 1);
-        mbar_init(&bars[L::PREADY], 128);
-        mbar_init(&bars[L::PEMPTY], 1);
         mbar_init(&bars[L::OFULL], 1);
         mbar_init(&bars[L::OEMPTY], 128);
-        mbar_init(&bars[L::DRAIN], 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -465,10 +544,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (lane == 0) {
             const int hk = h / (p.a.H / p.a.Hk);
             int iq = 0, iv = 0;
+#pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 const Chunk c = chunk_at<kC>(p.v, p.a.T, sq.x + i);
                 const int s = i % kQKStages, v = i % kVStages;
-                if (i >= kQKStages && !la_wait(&bars[L::QKEMPTY + s], (i / kQKStages - 1) & 1, 1u, lim)) break;
+                if (i >= kQKStages && !la_wait(&bars[L::QKEMPTY + s], (i / kQKStages - 1) & 1, end)) break;
                 uint8_t *st = sm + L::QK + s * 2 * L::TB;
                 mbar_arrive_expect_tx(&bars[L::QKFULL + s], 2 * L::TB);
 #pragma unroll
@@ -477,45 +557,76 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     tma_load_4d(st + L::TB + x * 16384, &mQ, &bars[L::QKFULL + s], 64 * x, c.t0, hk, c.row);
                 }
                 ++iq;
-                if (i >= kVStages && !la_wait(&bars[L::VEMPTY + v], (i / kVStages - 1) & 1, 1u, lim)) break;
+                if (i >= kVStages && !la_wait(&bars[L::VEMPTY + v], (i / kVStages - 1) & 1, end)) break;
                 mbar_arrive_expect_tx(&bars[L::VFULL + v], 16384);
                 tma_load_4d(sm + L::V + v * 16384, &mV, &bars[L::VFULL + v], 64 * slice, c.t0, h, c.row);
                 ++iv;
             }
             // no copy is in flight when the CTA ends
+#pragma unroll 1
             for (int j = iq > kQKStages ? iq - kQKStages : 0; j < iq; ++j)
                 mbar_wait(&bars[L::QKFULL + j % kQKStages], (j / kQKStages) & 1, kDrainNs);
+#pragma unroll 1
             for (int j = iv > kVStages ? iv - kVStages : 0; j < iv; ++j)
                 mbar_wait(&bars[L::VFULL + j % kVStages], (j / kVStages) & 1, kDrainNs);
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            const uint32_t idT = idesc_bf16(128, 128, false, false), idU = idesc_bf16(128, 64, true, true),
-                           idO = idesc_bf16(128, 64, false, true);
+            const uint32_t idT = idesc_bf16(128, 128, false, false), idO = idesc_bf16(128, 64, false, true);
             auto stage = [&](int i) { return sbase + L::QK + (i % kQKStages) * 2 * L::TB; };
+            // T's place is free: P V of two chunks before, the last to read it,
+            // was issued before (products run in the order of their issue)
             auto qk = [&](int i) {
-                bool ok = la_wait(&bars[L::QKFULL + i % kQKStages], (i / kQKStages) & 1, 2u, lim);
-                if (i >= 2) ok = ok && la_wait(&bars[L::TEMPTY + (i & 1)], (i / 2 - 1) & 1, 2u, lim);
-                if (!ok) return false;
+                if (!la_wait(&bars[L::QKFULL + i % kQKStages], (i / kQKStages) & 1, end)) return false;
                 tc_fence_after_sync();
                 const uint32_t k = stage(i), q = k + L::TB;
-#pragma unroll
+#pragma unroll 2
                 for (int ks = 0; ks < DK / 16; ++ks)
                     mma_bf16_ss(tmem + TM_T + 128u * (i & 1), smem_desc(q + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
                                 smem_desc(k + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024), idT, ks > 0);
+                mma_commit(&bars[L::QKEMPTY + i % kQKStages]);
                 mma_commit(&bars[L::TFULL + (i & 1)]);
                 return true;
             };
             bool ok = n > 0 && qk(0);
+#pragma unroll 1
             for (int i = 0; i < n && ok; ++i) {
-                const uint32_t k = stage(i), q = k + L::TB;
-                if (i >= 1) ok = la_wait(&bars[L::UEMPTY], (i - 1) & 1, 2u, lim);
+                if (i + 1 < n) ok = qk(i + 1);
+                ok = ok && la_wait(&bars[L::PREADY + (i & 1)], (i / 2) & 1, end);
+                ok = ok && la_wait(&bars[L::VREADY + i % kVStages], (i / kVStages) & 1, end);
+                if (i >= 1) ok = ok && la_wait(&bars[L::OEMPTY], (i - 1) & 1, end);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint32_t v = sbase + L::V + (i % kVStages) * 16384;
+#pragma unroll 2
+                for (int ks = 0; ks < kC / 16; ++ks)
+                    mma_bf16_ts(tmem + TM_OP, tmem + TM_T + 128u * (i & 1) + 8 * ks, smem_desc(v + ks * 2048, 8192, 1024), idO,
+                                ks > 0);
+                mma_commit(&bars[L::VEMPTY + i % kVStages]);
+                mma_commit(&bars[L::OFULL]);
+            }
+            // every MMA issued here is complete before TMEM is released
+            mma_commit(&bars[L::DRAIN]);
+            mbar_wait(&bars[L::DRAIN], 0, kDrainNs);
+        }
+    } else if (warp == 2) {
+        // the products of the state's walk: the chunk's share of it, and Q S
+        if (lane == 0) {
+            const uint32_t idU = idesc_bf16(128, 64, true, true), idO = idesc_bf16(128, 64, false, true);
+            bool ok = true;
+#pragma unroll 1
+            for (int i = 0; i < n && ok; ++i) {
+                const uint32_t k = sbase + L::QK + (i % kQKStages) * 2 * L::TB, q = k + L::TB;
+                ok = la_wait(&bars[L::QKFULL + i % kQKStages], (i / kQKStages) & 1, end);
+                if (i >= 1) ok = ok && la_wait(&bars[L::UEMPTY], (i - 1) & 1, end);
+#pragma unroll 1
                 for (int qd = 0; qd < 4 && ok; ++qd) {
-                    const int b = qd & 1, use = 2 * i + (qd >> 1);
-                    ok = la_wait(&bars[L::XREADY + b], use & 1, 2u, lim);
+                    const int x = 4 * i + qd, b = x % kXRing;
+                    ok = la_wait(&bars[L::XREADY + b], (x / kXRing) & 1, end);
                     if (!ok) break;
                     tc_fence_after_sync();
                     const uint32_t xb = sbase + L::X + b * 3 * 4096;
+#pragma unroll 1
                     for (int t = 0; t < terms; ++t)
 #pragma unroll
                         for (int ks = 0; ks < 2; ++ks)
@@ -524,36 +635,25 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     mma_commit(&bars[L::XEMPTY + b]);
                 }
                 if (ok) mma_commit(&bars[L::UFULL]);
-                ok = ok && la_wait(&bars[L::SREADY], i & 1, 2u, lim);
-                if (i >= 1) ok = ok && la_wait(&bars[L::OEMPTY], (i - 1) & 1, 2u, lim);
+                ok = ok && la_wait(&bars[L::SREADY], i & 1, end);
+                if (i >= 2) ok = ok && la_wait(&bars[L::OSEMPTY + (i & 1)], (i / 2 - 1) & 1, end);
                 if (!ok) break;
                 tc_fence_after_sync();
-#pragma unroll
+#pragma unroll 2
                 for (int ks = 0; ks < DK / 16; ++ks)
-                    mma_bf16_ss(tmem + TM_OS, smem_desc(q + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
+                    mma_bf16_ss(tmem + TM_OS + 64u * (i & 1), smem_desc(q + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
                                 smem_desc(sbase + L::S + ks * 2048, 8192, 1024), idO, ks > 0);
                 mma_commit(&bars[L::SEMPTY]);
                 mma_commit(&bars[L::QKEMPTY + i % kQKStages]);
-                if (i + 1 < n) ok = qk(i + 1);
-                ok = ok && la_wait(&bars[L::PREADY], i & 1, 2u, lim);
-                ok = ok && la_wait(&bars[L::VFULL + i % kVStages], (i / kVStages) & 1, 2u, lim);
-                if (!ok) break;
-                tc_fence_after_sync();
-                const uint32_t v = sbase + L::V + (i % kVStages) * 16384;
-#pragma unroll
-                for (int ks = 0; ks < kC / 16; ++ks)
-                    mma_bf16_ts(tmem + TM_OP, tmem + TM_P + 8 * ks, smem_desc(v + ks * 2048, 8192, 1024), idO, ks > 0);
-                mma_commit(&bars[L::PEMPTY]);
-                mma_commit(&bars[L::VEMPTY + i % kVStages]);
-                mma_commit(&bars[L::OFULL]);
+                mma_commit(&bars[L::OSFULL + (i & 1)]);
             }
-            // every MMA issued here is complete before TMEM is released
-            mma_commit(&bars[L::DRAIN]);
-            mbar_wait(&bars[L::DRAIN], 0, kDrainNs);
+            mma_commit(&bars[L::DRAIN + 1]);
+            mbar_wait(&bars[L::DRAIN + 1], 0, kDrainNs);
         }
-    } else if (warp < 4) {
-        // decays of every other chunk: e^{G - c_t}, log2(e) c_t and e^G; the
-        // next chunk's gates are on their way meanwhile
+    } else if (warp == 3) {
+        // a chunk's decays: e^{G - c_t}, log2(e) c_t, e^{c_r - c_t} with r the last
+        // token of t's block of 32, and e^G; the next chunk's gates are on their
+        // way meanwhile
         const bool per_head = p.a.flags & GDN_G_PER_HEAD;
         float next[4];
         auto fetch = [&](int i) {
@@ -561,19 +661,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const Chunk c = chunk_at<kC>(p.v, p.a.T, sq.x + i);
             load_gates<kC>(gate_ptr(p.a, c, h), p.a.sg.t, c.len, per_head, next);
         };
-        fetch(warp - 2);
-        for (int i = warp - 2; i < n; i += 2) {
+        fetch(0);
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
             const int w = i % kGRing;
             const Gates<kC> g = scan_gates<kC>(next);
-            fetch(i + 2);
-            if (i >= kGRing && !la_wait(&bars[L::GEMPTY + w], (i / kGRing - 1) & 1, 16u, lim)) break;
+            fetch(i + 1);
+            if (i >= kGRing && !la_wait(&bars[L::GEMPTY + w], (i / kGRing - 1) & 1, end)) break;
             float4 x, y;
-            x = make_float4(expf((float)(g.all - g.cum[0])), expf((float)(g.all - g.cum[1])),
-                            expf((float)(g.all - g.cum[2])), expf((float)(g.all - g.cum[3])));
-            y = make_float4((float)g.cum[0] * kLog2e, (float)g.cum[1] * kLog2e, (float)g.cum[2] * kLog2e, (float)g.cum[3] * kLog2e);
-            reinterpret_cast<float4 *>(gring + w * 256)[lane] = x;
-            reinterpret_cast<float4 *>(gring + w * 256 + 128)[lane] = y;
-            if (lane == 0) dring[w] = expf((float)g.all);
+            x = make_float4(expf(g.to_end(0)), expf(g.to_end(1)),
+                            expf(g.to_end(2)), expf(g.to_end(3)));
+            y = make_float4(g.cum[0].hi * kLog2e, g.cum[1].hi * kLog2e, g.cum[2].hi * kLog2e, g.cum[3].hi * kLog2e);
+            uint4 *ws = reinterpret_cast<uint4 *>(wring + w * 384);
+            const Weight wa = split_weight(x.x), wb = split_weight(x.y), wc = split_weight(x.z), wd = split_weight(x.w);
+            ws[lane] = make_uint4(wa.h, wb.h, wc.h, wd.h);
+            ws[lane + 32] = make_uint4(wa.m, wb.m, wc.m, wd.m);
+            ws[lane + 64] = make_uint4(wa.l, wb.l, wc.l, wd.l);
+            float4 *slot = reinterpret_cast<float4 *>(gring + w * 256);
+            slot[lane] = y;
+            const float r = __shfl_sync(~0u, y.w, lane | 7);
+            slot[lane + 32] = make_float4(exp2_fast(r - y.x), exp2_fast(r - y.y), exp2_fast(r - y.z), exp2_fast(r - y.w));
+            if (lane == 0) dring[w] = expf(g.all.hi);
             mbar_arrive(&bars[L::GFULL + w]);
         }
     } else if (warp < 8) {
@@ -588,164 +696,191 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (mine && p.a.s0) x = *reinterpret_cast<const float4 *>(p.a.s0 + page + e);
             S[e] = x.x, S[e + 1] = x.y, S[e + 2] = x.z, S[e + 3] = x.w;
         }
-        auto rows_out = [&](int i) {
-            const int w = i % kGRing;
-            if (!warp_ok(la_wait(&bars[L::OFULL], i & 1, 8u, lim))) return false;
-            tc_fence_after_sync();
-            const Chunk c = chunk_at<kC>(p.v, p.a.T, sq.x + i);
-            const float f = exp2_fast(gring[w * 256 + 128 + row]) * p.a.scale;
-            uint4 *out = reinterpret_cast<uint4 *>(at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, c.row, h, c.t0 + row) + 64 * slice);
+        bool ok = true;
+#pragma unroll 1
+        for (int i = 0; i <= n; ++i) {  // the outputs are a chunk behind the state
+            if (i < n) {
+                const int w = i % kGRing;
+                if (i >= 1) ok = la_wait(&bars[L::SEMPTY], (i - 1) & 1, end);
+                if (!warp_ok(ok)) break;
+                if (mine)
 #pragma unroll
+                    for (int e = 0; e < 64; e += 8)
+                        *reinterpret_cast<uint4 *>(sm + L::S + sw128_offset(row, e)) =
+                            make_uint4(pack_bf16(S[e], S[e + 1]), pack_bf16(S[e + 2], S[e + 3]), pack_bf16(S[e + 4], S[e + 5]),
+                                       pack_bf16(S[e + 6], S[e + 7]));
+                fence_proxy_async_smem();
+                mbar_arrive(&bars[L::SREADY]);
+                ok = la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, end) && la_wait(&bars[L::UFULL], i & 1, end);
+                if (!warp_ok(ok)) break;
+                const float d = dring[w];
+                tc_fence_after_sync();
+#pragma unroll
+                for (int e = 0; e < 64; e += 32) {
+                    uint32_t u[32];
+                    tmem_ld32(tmem + lane_base(warp) + TM_U + e, u);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) S[e + j] = fmaf(d, S[e + j], __uint_as_float(u[j]));
+                }
+                tc_fence_before_sync();
+                mbar_arrive(&bars[L::UEMPTY]);
+            }
+            if (i == 0) continue;
+            const int j = i - 1, w = j % kGRing;
+            ok = la_wait(&bars[L::OSFULL + (j & 1)], (j / 2) & 1, end) && la_wait(&bars[L::OFULL], j & 1, end);
+            if (!warp_ok(ok)) break;
+            tc_fence_after_sync();
+            const Chunk c = chunk_at<kC>(p.v, p.a.T, sq.x + j);
+            const float f = exp2_fast(gring[w * 256 + row]) * p.a.scale;
+            __nv_bfloat16 *out = at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, c.row, h, c.t0 + row) + 64 * slice;
+#pragma unroll 1
             for (int e = 0; e < 64; e += 16) {
-                uint32_t u[16], y[16];
-                tmem_ld16(tmem + lane_base(warp) + TM_OS + e, u);
+                uint32_t x[16], y[16];
+                tmem_ld16(tmem + lane_base(warp) + TM_OS + 64u * (j & 1) + e, x);
                 tmem_ld16(tmem + lane_base(warp) + TM_OP + e, y);
                 tmem_wait_ld();
-                float x[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = fmaf(f, __uint_as_float(u[j]), p.a.scale * __uint_as_float(y[j]));
                 if (row < c.len) {
-                    out[e / 8] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-                    out[e / 8 + 1] = make_uint4(pack_bf16(x[8], x[9]), pack_bf16(x[10], x[11]), pack_bf16(x[12], x[13]),
-                                                pack_bf16(x[14], x[15]));
+                    uint32_t w8[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        w8[k] = pack_bf16(fmaf(f, __uint_as_float(x[2 * k]), p.a.scale * __uint_as_float(y[2 * k])),
+                                          fmaf(f, __uint_as_float(x[2 * k + 1]), p.a.scale * __uint_as_float(y[2 * k + 1])));
+                    if (p.wide) {
+                        st_global_32(out + e, w8);
+                    } else {
+                        reinterpret_cast<uint4 *>(out + e)[0] = make_uint4(w8[0], w8[1], w8[2], w8[3]);
+                        reinterpret_cast<uint4 *>(out + e)[1] = make_uint4(w8[4], w8[5], w8[6], w8[7]);
+                    }
                 }
             }
             tc_fence_before_sync();
             mbar_arrive(&bars[L::OEMPTY]);
+            mbar_arrive(&bars[L::OSEMPTY + (j & 1)]);
             mbar_arrive(&bars[L::GEMPTY + w]);
-            return true;
-        };
-        bool ok = true;
-        for (int i = 0; i < n; ++i) {
-            const int w = i % kGRing;
-            if (i >= 1) ok = la_wait(&bars[L::SEMPTY], (i - 1) & 1, 8u, lim);
-            if (!warp_ok(ok)) break;
-            if (mine)
-#pragma unroll
-                for (int e = 0; e < 64; e += 8)
-                    *reinterpret_cast<uint4 *>(sm + L::S + sw128_offset(row, e)) =
-                        make_uint4(pack_bf16(S[e], S[e + 1]), pack_bf16(S[e + 2], S[e + 3]), pack_bf16(S[e + 4], S[e + 5]),
-                                   pack_bf16(S[e + 6], S[e + 7]));
-            fence_proxy_async_smem();
-            mbar_arrive(&bars[L::SREADY]);
-            if (i >= 1) ok = rows_out(i - 1);
-            ok = ok && la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, 8u, lim);
-            const float d = ok ? dring[w] : 0.f;
-            ok = ok && la_wait(&bars[L::UFULL], i & 1, 8u, lim);
-            if (!warp_ok(ok)) break;
-            tc_fence_after_sync();
-#pragma unroll
-            for (int e = 0; e < 64; e += 16) {
-                uint32_t u[16];
-                tmem_ld16(tmem + lane_base(warp) + TM_U + e, u);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) S[e + j] = fmaf(d, S[e + j], __uint_as_float(u[j]));
-            }
-            tc_fence_before_sync();
-            mbar_arrive(&bars[L::UEMPTY]);
         }
-        if (warp_ok(ok) && n > 0) ok = rows_out(n - 1);
         if (p.a.sf && mine && ok)
 #pragma unroll
             for (int e = 0; e < 64; e += 4)
                 *reinterpret_cast<float4 *>(p.a.sf + page + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
     } else if (warp < 12) {
-        // P: thread's row t; columns past the warp's last row are zeros for good
-        const int t = 32 * (warp & 3) + lane, cols = 32 * (warp & 3) + 32;
-        {
-            uint32_t z[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) z[j] = 0u;
-            for (int s = cols; s < kC; s += 32) tmem_st16(tmem + lane_base(warp) + TM_P + s / 2, z);
-        }
+        // P in blocks of 32 columns, thread's row t.  On the warp's diagonal the
+        // decay is e^{c_t - c_s}; in a block before it e^{c_t - c_r} e^{c_r - c_s}
+        // with r the block's last token, whose factors are both at most 1 for
+        // decays, so that a row costs one exponential a block.
+        const int t = 32 * (warp & 3) + lane, diag = 32 * (warp & 3);
+#pragma unroll 1
         for (int i = 0; i < n; ++i) {
             const int w = i % kGRing;
-            bool ok = la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, 32u, lim);
-            ok = ok && la_wait(&bars[L::TFULL + (i & 1)], (i / 2) & 1, 32u, lim);
-            if (i >= 1) ok = ok && la_wait(&bars[L::PEMPTY], (i - 1) & 1, 32u, lim);
+            bool ok = la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, end);
+            ok = ok && la_wait(&bars[L::TFULL + (i & 1)], (i / 2) & 1, end);
             if (!warp_ok(ok)) break;
             tc_fence_after_sync();
-            const float *c2 = gring + w * 256 + 128;
+            const float *c2 = gring + w * 256, *cf = c2 + 128;
             const float ct = c2[t];
-            for (int s = 0; s < cols; s += 32) {
+            const uint32_t tt = tmem + lane_base(warp) + TM_T + 128u * (i & 1);
+#pragma unroll 1
+            for (int s = 0; s <= diag; s += 32) {
                 uint32_t u[32], y[16];
-                tmem_ld16(tmem + lane_base(warp) + TM_T + 128u * (i & 1) + s, *reinterpret_cast<uint32_t(*)[16]>(u));
-                tmem_ld16(tmem + lane_base(warp) + TM_T + 128u * (i & 1) + s + 16, *reinterpret_cast<uint32_t(*)[16]>(u + 16));
+                tmem_ld32(tt + s, u);
+                const float rf = exp2_fast(ct - c2[s + 31]);
                 tmem_wait_ld();
-                const bool edge = s + 32 == cols;  // the block on the diagonal
+                if (s < diag) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 cs = *reinterpret_cast<const float4 *>(c2 + s + j);
-                    float x[4] = {__uint_as_float(u[j]) * exp2_fast(ct - cs.x), __uint_as_float(u[j + 1]) * exp2_fast(ct - cs.y),
-                                  __uint_as_float(u[j + 2]) * exp2_fast(ct - cs.z), __uint_as_float(u[j + 3]) * exp2_fast(ct - cs.w)};
-                    if (edge)
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(cf + s + j);
+                        y[j / 2] = pack_bf16(__uint_as_float(u[j]) * (rf * f.x), __uint_as_float(u[j + 1]) * (rf * f.y));
+                        y[j / 2 + 1] = pack_bf16(__uint_as_float(u[j + 2]) * (rf * f.z), __uint_as_float(u[j + 3]) * (rf * f.w));
+                    }
+                } else {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) x[k] = s + j + k <= t ? x[k] : 0.f;
-                    y[j / 2] = pack_bf16(x[0], x[1]);
-                    y[j / 2 + 1] = pack_bf16(x[2], x[3]);
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 cs = *reinterpret_cast<const float4 *>(c2 + s + j);
+                        const float x0 = j + 0 <= lane ? __uint_as_float(u[j]) * exp2_fast(ct - cs.x) : 0.f;
+                        const float x1 = j + 1 <= lane ? __uint_as_float(u[j + 1]) * exp2_fast(ct - cs.y) : 0.f;
+                        const float x2 = j + 2 <= lane ? __uint_as_float(u[j + 2]) * exp2_fast(ct - cs.z) : 0.f;
+                        const float x3 = j + 3 <= lane ? __uint_as_float(u[j + 3]) * exp2_fast(ct - cs.w) : 0.f;
+                        y[j / 2] = pack_bf16(x0, x1);
+                        y[j / 2 + 1] = pack_bf16(x2, x3);
+                    }
                 }
-                tmem_st16(tmem + lane_base(warp) + TM_P + s / 2, y);
+                tmem_st16(tt + s / 2, y);
+            }
+#pragma unroll 1
+            for (int s = diag + 32; s < kC; s += 32) {  // P's columns s / 2.. hold what T's have been read for
+                uint32_t z[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) z[j] = 0u;
+                tmem_st16(tt + s / 2, z);
             }
             tmem_wait_st();
             tc_fence_before_sync();
-            mbar_arrive(&bars[L::TEMPTY + (i & 1)]);
-            mbar_arrive(&bars[L::PREADY]);
+            mbar_arrive(&bars[L::PREADY + (i & 1)]);
             mbar_arrive(&bars[L::GEMPTY + w]);
         }
     } else {
         // the weighted values, in quarters of 32 tokens: row r, 16 columns
         const int ct = threadIdx.x - 384, r = ct >> 2, c0 = (ct & 3) * 16;
+#pragma unroll 1
         for (int i = 0; i < n; ++i) {
             const int v = i % kVStages, w = i % kGRing;
             const Chunk c = chunk_at<kC>(p.v, p.a.T, sq.x + i);
-            bool ok = la_wait(&bars[L::VFULL + v], (i / kVStages) & 1, 4u, lim);
-            ok = ok && la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, 4u, lim);
+            bool ok = la_wait(&bars[L::VFULL + v], (i / kVStages) & 1, end);
+            ok = ok && la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, end);
             uint8_t *vt = sm + L::V + v * 16384;
             if (ok && c.len < kC) {
                 // rows past the chunk's tokens are another sequence's: zeros, so
                 // that nothing of theirs (an infinity, say) meets a zero weight
-                ok = la_wait(&bars[L::QKFULL + i % kQKStages], (i / kQKStages) & 1, 4u, lim);
+                ok = la_wait(&bars[L::QKFULL + i % kQKStages], (i / kQKStages) & 1, end);
                 uint8_t *k = sm + L::QK + (i % kQKStages) * 2 * L::TB;
                 if (ok)
+#pragma unroll 1
                     for (int e = ct; e < (kC - c.len) * (DK / 8); e += 128) {
                         const int row = c.len + e / (DK / 8), col = (e % (DK / 8)) * 8;
                         *reinterpret_cast<uint4 *>(k + (col >> 6) * 16384 + sw128_offset(row, col & 63)) = make_uint4(0, 0, 0, 0);
                     }
                 if (ok)
+#pragma unroll 1
                     for (int e = ct; e < (kC - c.len) * 8; e += 128)
                         *reinterpret_cast<uint4 *>(vt + sw128_offset(c.len + (e >> 3), (e & 7) * 8)) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
             }
             if (!warp_ok(ok)) break;
+            mbar_arrive(&bars[L::VREADY + v]);
 #pragma unroll 1
             for (int qd = 0; qd < 4; ++qd) {
-                const int b = qd & 1, use = 2 * i + (qd >> 1), t = 32 * qd + r;
-                const float wt = gring[w * 256 + t];
-                float x[2][8];
+                const int xn = 4 * i + qd, b = xn % kXRing, t = 32 * qd + r;
+                const uint32_t *wr = wring + w * 384 + t;
+                const Weight wt = {wr[0], wr[128], wr[256]};
+                uint4 v[2];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    unpack8(*reinterpret_cast<const uint4 *>(vt + sw128_offset(t, c0 + 8 * u)), x[u]);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[u][e] = t < c.len ? x[u][e] * wt : 0.f;
+                    v[u] = *reinterpret_cast<const uint4 *>(vt + sw128_offset(t, c0 + 8 * u));
+                    if (t >= c.len) v[u] = make_uint4(0, 0, 0, 0);
                 }
-                if (use >= 1 && !la_wait(&bars[L::XEMPTY + b], (use - 1) & 1, 4u, lim)) ok = false;
+                if (xn >= kXRing && !la_wait(&bars[L::XEMPTY + b], (xn / kXRing - 1) & 1, end)) ok = false;
                 if (!warp_ok(ok)) break;
                 uint8_t *xb = sm + L::X + b * 3 * 4096;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const uint32_t off = sw128_offset(r, c0 + 8 * u);
-                    *reinterpret_cast<uint4 *>(xb + off) = take8(x[u]);
+                    uint4 x, y, z;
                     if (terms == 3) {
-                        *reinterpret_cast<uint4 *>(xb + 4096 + off) = take8(x[u]);
-                        *reinterpret_cast<uint4 *>(xb + 8192 + off) = pack8(x[u]);
+                        weigh3(v[u].x, wt, x.x, y.x, z.x), weigh3(v[u].y, wt, x.y, y.y, z.y);
+                        weigh3(v[u].z, wt, x.z, y.z, z.z), weigh3(v[u].w, wt, x.w, y.w, z.w);
+                        *reinterpret_cast<uint4 *>(xb + 8192 + off) = z;
                     } else {
-                        *reinterpret_cast<uint4 *>(xb + 4096 + off) = pack8(x[u]);
+                        weigh2(v[u].x, wt, x.x, y.x), weigh2(v[u].y, wt, x.y, y.y);
+                        weigh2(v[u].z, wt, x.z, y.z), weigh2(v[u].w, wt, x.w, y.w);
                     }
+                    *reinterpret_cast<uint4 *>(xb + off) = x;
+                    *reinterpret_cast<uint4 *>(xb + 4096 + off) = y;
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&bars[L::XREADY + b]);
             }
             if (!warp_ok(ok)) break;
+            mbar_arrive(&bars[L::VEMPTY + v]);
             mbar_arrive(&bars[L::GEMPTY + w]);
         }
     }
@@ -834,9 +969,11 @@ int run_fwd(const TcArgs &p, cudaStream_t stream) {
     if (!strided_map(&mQ, a.q, a.sq, a.B, a.Hk, a.T, DK, kC) || !strided_map(&mK, a.k, a.sk, a.B, a.Hk, a.T, DK, kC) ||
         !strided_map(&mV, a.v, a.sv, a.B, a.H, a.T, DV, kC))
         return GDN_ERR_CUDA;
+    TcArgs w = p;
+    w.wide = ((reinterpret_cast<uintptr_t>(a.o) | 2 * a.so.b | 2 * a.so.h | 2 * a.so.t) & 31) == 0;
     auto kern = prompt_kernel<DK, DV>;
     if (!smem_limit(kern, FwdSmem<DK>::BYTES)) return GDN_ERR_CUDA;
-    kern<<<dim3(DV / 64, a.H, a.n_seq + (a.cu ? 1 : 0)), kFwdThreads, FwdSmem<DK>::BYTES, stream>>>(mQ, mK, mV, p);
+    kern<<<dim3(DV / 64, a.H, a.n_seq + (a.cu ? 1 : 0)), kFwdThreads, FwdSmem<DK>::BYTES, stream>>>(mQ, mK, mV, w);
     return launched();
 }
 
