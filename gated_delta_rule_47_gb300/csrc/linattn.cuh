@@ -46,6 +46,16 @@ __device__ __forceinline__ int2 seq_at(const View &v, int s) {
     return make_int2(s * v.per_row, v.per_row);
 }
 
+// A sequence's tokens, cut to the row: also for offsets out of order or range.
+struct Span {
+    int start, len;
+};
+__device__ __forceinline__ Span span_of(const LinAttnArgs &a, int s) {
+    if (!a.cu) return {0, a.T};
+    const int start = min(max(a.cu[s], 0), a.T);
+    return {start, max(min(a.cu[s + 1], a.T) - start, 0)};
+}
+
 inline int chunk_bound(const LinAttnArgs &a, int C) {
     if (a.cu) return a.T / C + a.n_seq + 2;
     return (int)((long long)a.B * ((a.T + C - 1) / C));

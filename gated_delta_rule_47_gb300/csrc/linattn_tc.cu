@@ -4,11 +4,11 @@
 //
 // prompt_kernel is the forward in one launch.  A CTA owns 64 value columns of
 // one head (columns are independent) and walks a sequence's chunks with the
-// state in registers, so q, k, v and o cross the memory once (a head's two
+// fp32 state in tensor memory, so q, k, v and o cross the memory once (a head's two
 // CTAs run side by side and share q and k in L2).  A chunk is four products:
 // T = Q K^T; P V with P = T under the decay mask, in tensor memory; Q S; and
-// the chunk's own share of the state K^T diag(w) V, which does not depend on
-// the state, so the walk itself costs one multiply-add an element.
+// the chunk's own share of the state K^T diag(w) V, added to the state after
+// it has been scaled by the chunk's decay.
 // The weighted values w v go in as two or three bf16 terms (x = hi + mid + lo
 // to 2^-24): with one, the state would carry 2^-9 of rounding in every term,
 // against inputs that are exact; sums and state stay in fp32.  P and S enter
@@ -155,7 +155,7 @@ struct StateSmem {
     static constexpr uint32_t BAR = W + kWRing * 1536 + 64;
     enum { FULL = 0, EMPTY = 3, XREADY = 6, XEMPTY = 8, UFULL = 10, UEMPTY = 12, WFULL = 14, WEMPTY = 18, DRAIN = 22, NUM = 23 };
     static constexpr uint32_t TSLOT = BAR + 8 * NUM;
-    static constexpr uint32_t BYTES = TSLOT + 16 + 1024;
+    static constexpr uint32_t BYTES = TSLOT + 16;
 };
 static_assert(StateSmem<128>::BYTES <= 232448, "state kernel fits the shared memory of one CTA");
 
@@ -166,8 +166,7 @@ template <int DK, int DV, bool REV, bool LO>
 __global__ void __launch_bounds__(kStateThreads, 1)
     state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV, TcArgs p) {
     using L = StateSmem<DK>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::TSLOT);
     uint32_t *wring = reinterpret_cast<uint32_t *>(sm + L::W);
@@ -416,9 +415,13 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 }
 
 // ================================================================ prompt kernel
-// Warps: 0 TMA, 1 and 2 MMA, 3 decays, 4..7 state and outputs, 8..11 P, 12..15 weighting.
-constexpr int kFwdThreads = 512;
-constexpr int kQKStages = 2, kVStages = 2, kXRing = 3, kGRing = 4;
+// Warps: 0 TMA, 1 and 2 products, 3 decays, 4..7 state, 8..11 P, 12..15
+// weighting, 16..19 outputs.  One warp of each on each of the SM's four
+// schedulers, so every instruction is fetched for one warp alone, and
+// straight-line code is bound by its fetching (a third of an instruction a
+// cycle here): the roles' bodies are short loops.
+constexpr int kFwdThreads = 640;
+constexpr int kQKStages = 2, kVStages = 3, kXMax = 3, kGRing = 4;
 constexpr float kLog2e = 1.44269504088896341f;
 
 template <int DK>
@@ -426,27 +429,44 @@ struct FwdSmem {
     static constexpr uint32_t TB = DK * 256;                 // a chunk's Q or K
     static constexpr uint32_t QK = 0;                        // [stage] K | Q
     static constexpr uint32_t V = kQKStages * 2 * TB;        // [stage] 64 columns of V
-    static constexpr uint32_t X = V + kVStages * 16384;      // [ring][3][32 tokens][128 B] weighted values
-    static constexpr uint32_t S = X + kXRing * 3 * 4096;     // [DK][128 B] the state as an operand
+    static constexpr uint32_t X = V + kVStages * 16384;      // [slot][term][32 tokens][128 B] weighted values
+    static constexpr uint32_t S = X + 6 * 4096;              // [DK][128 B] the state as an operand
     static constexpr uint32_t W = S + DK * 128;              // [ring][3][128] weights
     static constexpr uint32_t G = W + kGRing * 1536;         // [ring] log2 decays | block factors, 128 each
     static constexpr uint32_t D = G + kGRing * 1024;         // [ring] chunk decays
     static constexpr uint32_t BAR = D + 64;
-    enum { QKFULL = 0, QKEMPTY = 2, VFULL = 4, VREADY = 6, VEMPTY = 8, XREADY = 10, XEMPTY = XREADY + kXRing, UFULL = XEMPTY + kXRing,
-           UEMPTY, SREADY, SEMPTY, TFULL, PREADY = TFULL + 2, OFULL = PREADY + 2, OEMPTY, OSFULL, OSEMPTY = OSFULL + 2, GFULL = OSEMPTY + 2, GEMPTY = GFULL + kGRing,
+    enum { KFULL = 0, KEMPTY = 2, QFULL = 4, QEMPTY = 6, VFULL = 8, VREADY = 11, VEMPTY = 14, XREADY = 17,
+           XEMPTY = XREADY + kXMax, UFULL = XEMPTY + kXMax,
+           SREADY, SEMPTY, TFULL, PREADY = TFULL + 2, OFULL = PREADY + 2, OEMPTY, OSFULL, OSEMPTY = OSFULL + 2, GFULL = OSEMPTY + 2, GEMPTY = GFULL + kGRing,
            DRAIN = GEMPTY + kGRing, NUM = DRAIN + 2 };
     static constexpr uint32_t TSLOT = BAR + 8 * NUM;
-    static constexpr uint32_t BYTES = TSLOT + 16 + 1024;
+    static constexpr uint32_t BYTES = TSLOT + 16;
 };
 static_assert(FwdSmem<128>::BYTES <= 232448, "prompt kernel fits the shared memory of one CTA");
 // TMEM columns: Q K^T twice (P, two bf16 a column, takes its first half), Q S
-// twice, P V, the chunk's share of the state
-constexpr uint32_t TM_T = 0, TM_OS = 256, TM_OP = 384, TM_U = 448;
+// twice, P V, the state
+constexpr uint32_t TM_T = 0, TM_OS = 256, TM_OP = 384, TM_S = 448;
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// smem_desc in two halves: what varies is the low one, an address (and the
+// leading stride) in 16-byte units, to which a product's steps add constants.
+// The warps that issue products run converged, so that all of this stays in
+// uniform registers; a step is then two instructions.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) { return (saddr >> 4) | (lbo_bytes >> 4) << 16; }
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+    return (uint64_t)((1024u >> 4) | 1u << 14 | 2u << 29) << 32 | lo;
 }
 
 // 32 bytes to a 32-byte aligned address: whole sectors.
@@ -456,15 +476,34 @@ __device__ __forceinline__ void st_global_32(void *p, const uint32_t (&x)[8]) {
                  : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]: A's rows are lanes, two bf16 of a row a column.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// D[tmem] (+)= A * B[smem]^T with A in shared memory, or (ts) in tensor memory:
+// rows are lanes, two bf16 of a row a column.  ADD is a constant: as a run-time
+// operand it costs more instructions than all the rest of a product.
+template <int ADD>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(ADD)
+        : "memory");
+}
+template <int ADD>
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "n"(ADD)
         : "memory");
+}
+
+// KS steps of 16; a(ks) and b(ks) are the operands' low descriptor words.
+template <int KS, class A, class B>
+__device__ __forceinline__ void mma_steps(uint32_t d, uint32_t idesc, const A &a, const B &b) {
+    mma_ss<0>(d, desc_of(a(0)), desc_of(b(0)), idesc);
+#pragma unroll
+    for (int ks = 1; ks < KS; ++ks) mma_ss<1>(d, desc_of(a(ks)), desc_of(b(ks)), idesc);
 }
 
 // Grid (DV / 64, H, n_seq, and one more for the tokens of no sequence).  A CTA walks the chunks of
@@ -474,8 +513,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                   const __grid_constant__ CUtensorMap mV, TcArgs p) {
     using L = FwdSmem<DK>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::TSLOT);
     float *gring = reinterpret_cast<float *>(sm + L::G), *dring = reinterpret_cast<float *>(sm + L::D);
@@ -492,24 +530,28 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         return;
     }
-    const int2 sq = seq_at(p.v, seq);
-    const int n = sq.y;
+    const int row = p.a.cu ? 0 : seq;
+    const Span sp = span_of(p.a, seq);
+    const int n = (sp.len + kC - 1) / kC;
+    auto chunk = [&](int i) { return Chunk{row, sp.start + i * kC, min(kC, sp.len - i * kC), seq}; };
     // the final state is an fp32 output: three bf16 terms a weighted value; for
     // bf16 outputs alone two (2^-16) are far below their rounding
-    const int terms = p.a.sf ? 3 : 2;
+    const int terms = p.a.sf ? 3 : 2, xring = p.a.sf ? 2 : 3;  // slots of X: 24 KB in all
     const uint64_t end = deadline_after(p.timeout_ns, n);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kQKStages; ++s) {
-            mbar_init(&bars[L::QKFULL + s], 1);
-            mbar_init(&bars[L::QKEMPTY + s], 2);
+            mbar_init(&bars[L::KFULL + s], 1);
+            mbar_init(&bars[L::KEMPTY + s], 2);
+            mbar_init(&bars[L::QFULL + s], 1);
+            mbar_init(&bars[L::QEMPTY + s], 2);
             mbar_init(&bars[L::OSFULL + s], 1);
             mbar_init(&bars[L::OSEMPTY + s], 128);
             mbar_init(&bars[L::DRAIN + s], 1);
             mbar_init(&bars[L::TFULL + s], 1);
             mbar_init(&bars[L::PREADY + s], 128);
         }
-        for (int s = 0; s < kXRing; ++s) {
+        for (int s = 0; s < kXMax; ++s) {
             mbar_init(&bars[L::XREADY + s], 128);
             mbar_init(&bars[L::XEMPTY + s], 1);
         }
@@ -520,10 +562,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         for (int s = 0; s < kGRing; ++s) {
             mbar_init(&bars[L::GFULL + s], 32);
-            mbar_init(&bars[L::GEMPTY + s], 384);
+            mbar_init(&bars[L::GEMPTY + s], 512);
         }
         mbar_init(&bars[L::UFULL], 1);
-        mbar_init(&bars[L::UEMPTY], 128);
         mbar_init(&bars[L::SREADY], 128);
         mbar_init(&bars[L::SEMPTY], 1);
         mbar_init(&bars[L::OFULL], 1);
@@ -537,119 +578,140 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tmem = *tslot;
+    constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
     const uint32_t sbase = smem_u32(sm);
 
     if (warp == 0) {
         if (lane == 0) {
             const int hk = h / (p.a.H / p.a.Hk);
-            int iq = 0, iv = 0;
+            int ik = 0, iq = 0, iv = 0;
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
-                const Chunk c = chunk_at<kC>(p.v, p.a.T, sq.x + i);
+                const Chunk c = chunk(i);
                 const int s = i % kQKStages, v = i % kVStages;
-                if (i >= kQKStages && !la_wait(&bars[L::QKEMPTY + s], (i / kQKStages - 1) & 1, end)) break;
                 uint8_t *st = sm + L::QK + s * 2 * L::TB;
-                mbar_arrive_expect_tx(&bars[L::QKFULL + s], 2 * L::TB);
-#pragma unroll
-                for (int x = 0; x < DK / 64; ++x) {
-                    tma_load_4d(st + x * 16384, &mK, &bars[L::QKFULL + s], 64 * x, c.t0, hk, c.row);
-                    tma_load_4d(st + L::TB + x * 16384, &mQ, &bars[L::QKFULL + s], 64 * x, c.t0, hk, c.row);
-                }
-                ++iq;
                 if (i >= kVStages && !la_wait(&bars[L::VEMPTY + v], (i / kVStages - 1) & 1, end)) break;
                 mbar_arrive_expect_tx(&bars[L::VFULL + v], 16384);
                 tma_load_4d(sm + L::V + v * 16384, &mV, &bars[L::VFULL + v], 64 * slice, c.t0, h, c.row);
                 ++iv;
+                if (i >= kQKStages && !la_wait(&bars[L::KEMPTY + s], (i / kQKStages - 1) & 1, end)) break;
+                mbar_arrive_expect_tx(&bars[L::KFULL + s], L::TB);
+#pragma unroll
+                for (int x = 0; x < DK / 64; ++x) tma_load_4d(st + x * 16384, &mK, &bars[L::KFULL + s], 64 * x, c.t0, hk, c.row);
+                ++ik;
+                if (i >= kQKStages && !la_wait(&bars[L::QEMPTY + s], (i / kQKStages - 1) & 1, end)) break;
+                mbar_arrive_expect_tx(&bars[L::QFULL + s], L::TB);
+#pragma unroll
+                for (int x = 0; x < DK / 64; ++x)
+                    tma_load_4d(st + L::TB + x * 16384, &mQ, &bars[L::QFULL + s], 64 * x, c.t0, hk, c.row);
+                ++iq;
             }
             // no copy is in flight when the CTA ends
+            auto drain = [&](int full, int stages, int count) {
 #pragma unroll 1
-            for (int j = iq > kQKStages ? iq - kQKStages : 0; j < iq; ++j)
-                mbar_wait(&bars[L::QKFULL + j % kQKStages], (j / kQKStages) & 1, kDrainNs);
-#pragma unroll 1
-            for (int j = iv > kVStages ? iv - kVStages : 0; j < iv; ++j)
-                mbar_wait(&bars[L::VFULL + j % kVStages], (j / kVStages) & 1, kDrainNs);
+                for (int j = count > stages ? count - stages : 0; j < count; ++j)
+                    mbar_wait(&bars[full + j % stages], (j / stages) & 1, kDrainNs);
+            };
+            drain(L::KFULL, kQKStages, ik);
+            drain(L::QFULL, kQKStages, iq);
+            drain(L::VFULL, kVStages, iv);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idT = idesc_bf16(128, 128, false, false), idO = idesc_bf16(128, 64, false, true);
-            auto stage = [&](int i) { return sbase + L::QK + (i % kQKStages) * 2 * L::TB; };
-            // T's place is free: P V of two chunks before, the last to read it,
-            // was issued before (products run in the order of their issue)
-            auto qk = [&](int i) {
-                if (!la_wait(&bars[L::QKFULL + i % kQKStages], (i / kQKStages) & 1, end)) return false;
-                tc_fence_after_sync();
-                const uint32_t k = stage(i), q = k + L::TB;
-#pragma unroll 2
-                for (int ks = 0; ks < DK / 16; ++ks)
-                    mma_bf16_ss(tmem + TM_T + 128u * (i & 1), smem_desc(q + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
-                                smem_desc(k + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024), idT, ks > 0);
-                mma_commit(&bars[L::QKEMPTY + i % kQKStages]);
-                mma_commit(&bars[L::TFULL + (i & 1)]);
-                return true;
-            };
-            bool ok = n > 0 && qk(0);
+        // the products around P: Q K^T a chunk ahead, and P V
+        constexpr uint32_t idT = idesc_bf16(128, 128, false, false), idO = idesc_bf16(128, 64, false, true);
+        const bool leader = elect_one();
+        // T's place is free: P V of two chunks before, the last to read it,
+        // was issued before (products run in the order of their issue)
+        bool ok = true;
 #pragma unroll 1
-            for (int i = 0; i < n && ok; ++i) {
-                if (i + 1 < n) ok = qk(i + 1);
-                ok = ok && la_wait(&bars[L::PREADY + (i & 1)], (i / 2) & 1, end);
-                ok = ok && la_wait(&bars[L::VREADY + i % kVStages], (i / kVStages) & 1, end);
-                if (i >= 1) ok = ok && la_wait(&bars[L::OEMPTY], (i - 1) & 1, end);
-                if (!ok) break;
+        for (int i = -1; i < n; ++i) {
+            if (i + 1 < n) {
+                const int j = i + 1, st = j % kQKStages;
+                ok = la_wait(&bars[L::KFULL + st], (j / kQKStages) & 1, end) && la_wait(&bars[L::QFULL + st], (j / kQKStages) & 1, end);
+                if (!warp_ok(ok)) break;
                 tc_fence_after_sync();
-                const uint32_t v = sbase + L::V + (i % kVStages) * 16384;
-#pragma unroll 2
-                for (int ks = 0; ks < kC / 16; ++ks)
-                    mma_bf16_ts(tmem + TM_OP, tmem + TM_T + 128u * (i & 1) + 8 * ks, smem_desc(v + ks * 2048, 8192, 1024), idO,
-                                ks > 0);
+                const uint32_t k = desc_lo(sbase + L::QK + st * 2 * L::TB, 16), q = k + (L::TB >> 4), d = TM_T + 128u * (j & 1);
+                if (leader) {
+                    mma_steps<DK / 16>(d, idT, [&](int ks) { return q + (ks >> 2) * 1024 + (ks & 3) * 2; },
+                                       [&](int ks) { return k + (ks >> 2) * 1024 + (ks & 3) * 2; });
+                    mma_commit(&bars[L::KEMPTY + st]);
+                    mma_commit(&bars[L::QEMPTY + st]);
+                    mma_commit(&bars[L::TFULL + (j & 1)]);
+                }
+                __syncwarp();
+            }
+            if (i < 0) continue;
+            ok = la_wait(&bars[L::PREADY + (i & 1)], (i / 2) & 1, end) && la_wait(&bars[L::VREADY + i % kVStages], (i / kVStages) & 1, end);
+            if (i >= 1) ok = ok && la_wait(&bars[L::OEMPTY], (i - 1) & 1, end);
+            if (!warp_ok(ok)) break;
+            tc_fence_after_sync();
+            const uint32_t v = desc_lo(sbase + L::V + (i % kVStages) * 16384, 8192), t = TM_T + 128u * (i & 1);
+            if (leader) {
+                mma_ts<0>(TM_OP, t, desc_of(v), idO);
+#pragma unroll
+                for (int ks = 1; ks < kC / 16; ++ks) mma_ts<1>(TM_OP, t + 8 * ks, desc_of(v + ks * 128), idO);
                 mma_commit(&bars[L::VEMPTY + i % kVStages]);
                 mma_commit(&bars[L::OFULL]);
             }
-            // every MMA issued here is complete before TMEM is released
-            mma_commit(&bars[L::DRAIN]);
-            mbar_wait(&bars[L::DRAIN], 0, kDrainNs);
+            __syncwarp();
         }
+        // every MMA issued here is complete before TMEM is released
+        if (leader) mma_commit(&bars[L::DRAIN]);
+        mbar_wait(&bars[L::DRAIN], 0, kDrainNs);
     } else if (warp == 2) {
-        // the products of the state's walk: the chunk's share of it, and Q S
-        if (lane == 0) {
-            const uint32_t idU = idesc_bf16(128, 64, true, true), idO = idesc_bf16(128, 64, false, true);
-            bool ok = true;
+        // the products of the state's walk: the chunk's share, added to it, and Q S
+        constexpr uint32_t idU = idesc_bf16(128, 64, true, true), idO = idesc_bf16(128, 64, false, true);
+        const bool leader = elect_one();
+        bool ok = true;
+        int xs = 0, xp = 0;  // slot of X, and its phase
 #pragma unroll 1
-            for (int i = 0; i < n && ok; ++i) {
-                const uint32_t k = sbase + L::QK + (i % kQKStages) * 2 * L::TB, q = k + L::TB;
-                ok = la_wait(&bars[L::QKFULL + i % kQKStages], (i / kQKStages) & 1, end);
-                if (i >= 1) ok = ok && la_wait(&bars[L::UEMPTY], (i - 1) & 1, end);
+        for (int i = 0; i < n; ++i) {
+            const int st = i % kQKStages;
+            const uint32_t kb = sbase + L::QK + st * 2 * L::TB, k = desc_lo(kb, 16384), q = desc_lo(kb + L::TB, 16);
+            // the state has been scaled, and is there as an operand
+            ok = la_wait(&bars[L::KFULL + st], (i / kQKStages) & 1, end) && la_wait(&bars[L::SREADY], i & 1, end);
 #pragma unroll 1
-                for (int qd = 0; qd < 4 && ok; ++qd) {
-                    const int x = 4 * i + qd, b = x % kXRing;
-                    ok = la_wait(&bars[L::XREADY + b], (x / kXRing) & 1, end);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    const uint32_t xb = sbase + L::X + b * 3 * 4096;
-#pragma unroll 1
-                    for (int t = 0; t < terms; ++t)
-#pragma unroll
-                        for (int ks = 0; ks < 2; ++ks)
-                            mma_bf16_ss(tmem + TM_U, smem_desc(k + (2 * qd + ks) * 2048, 16384, 1024),
-                                        smem_desc(xb + t * 4096 + ks * 2048, 8192, 1024), idU, (qd | t | ks) ? 1u : 0u);
-                    mma_commit(&bars[L::XEMPTY + b]);
-                }
-                if (ok) mma_commit(&bars[L::UFULL]);
-                ok = ok && la_wait(&bars[L::SREADY], i & 1, end);
-                if (i >= 2) ok = ok && la_wait(&bars[L::OSEMPTY + (i & 1)], (i / 2 - 1) & 1, end);
-                if (!ok) break;
+            for (int qd = 0; qd < 4; ++qd) {
+                ok = ok && la_wait(&bars[L::XREADY + xs], xp, end);
+                if (!warp_ok(ok)) break;
                 tc_fence_after_sync();
-#pragma unroll 2
-                for (int ks = 0; ks < DK / 16; ++ks)
-                    mma_bf16_ss(tmem + TM_OS + 64u * (i & 1), smem_desc(q + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
-                                smem_desc(sbase + L::S + ks * 2048, 8192, 1024), idO, ks > 0);
+                const uint32_t x = desc_lo(sbase + L::X + xs * terms * 4096, 8192), kq = k + qd * 256;
+                if (leader) {
+                    mma_ss<1>(TM_S, desc_of(kq), desc_of(x), idU);
+                    mma_ss<1>(TM_S, desc_of(kq + 128), desc_of(x + 128), idU);
+                    mma_ss<1>(TM_S, desc_of(kq), desc_of(x + 256), idU);
+                    mma_ss<1>(TM_S, desc_of(kq + 128), desc_of(x + 384), idU);
+                    if (terms == 3) {
+                        mma_ss<1>(TM_S, desc_of(kq), desc_of(x + 512), idU);
+                        mma_ss<1>(TM_S, desc_of(kq + 128), desc_of(x + 640), idU);
+                    }
+                    mma_commit(&bars[L::XEMPTY + xs]);
+                }
+                __syncwarp();
+                if (++xs == xring) xs = 0, xp ^= 1;
+            }
+            if (!warp_ok(ok)) break;
+            if (leader) {
+                mma_commit(&bars[L::UFULL]);
+                mma_commit(&bars[L::KEMPTY + st]);
+            }
+            __syncwarp();
+            ok = la_wait(&bars[L::QFULL + st], (i / kQKStages) & 1, end);
+            if (i >= 2) ok = ok && la_wait(&bars[L::OSEMPTY + (i & 1)], (i / 2 - 1) & 1, end);
+            if (!warp_ok(ok)) break;
+            tc_fence_after_sync();
+            const uint32_t sd = desc_lo(sbase + L::S, 8192), d = TM_OS + 64u * (i & 1);
+            if (leader) {
+                mma_steps<DK / 16>(d, idO, [&](int ks) { return q + (ks >> 2) * 1024 + (ks & 3) * 2; },
+                                   [&](int ks) { return sd + ks * 128; });
                 mma_commit(&bars[L::SEMPTY]);
-                mma_commit(&bars[L::QKEMPTY + i % kQKStages]);
+                mma_commit(&bars[L::QEMPTY + st]);
                 mma_commit(&bars[L::OSFULL + (i & 1)]);
             }
-            mma_commit(&bars[L::DRAIN + 1]);
-            mbar_wait(&bars[L::DRAIN + 1], 0, kDrainNs);
+            __syncwarp();
         }
+        if (leader) mma_commit(&bars[L::DRAIN + 1]);
+        mbar_wait(&bars[L::DRAIN + 1], 0, kDrainNs);
     } else if (warp == 3) {
         // a chunk's decays: e^{G - c_t}, log2(e) c_t, e^{c_r - c_t} with r the last
         // token of t's block of 32, and e^G; the next chunk's gates are on their
@@ -658,8 +720,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         float next[4];
         auto fetch = [&](int i) {
             if (i >= n) return;
-            const Chunk c = chunk_at<kC>(p.v, p.a.T, sq.x + i);
-            load_gates<kC>(gate_ptr(p.a, c, h), p.a.sg.t, c.len, per_head, next);
+            load_gates<kC>(gate_ptr(p.a, chunk(i), h), p.a.sg.t, chunk(i).len, per_head, next);
         };
         fetch(0);
 #pragma unroll 1
@@ -668,219 +729,253 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const Gates<kC> g = scan_gates<kC>(next);
             fetch(i + 1);
             if (i >= kGRing && !la_wait(&bars[L::GEMPTY + w], (i / kGRing - 1) & 1, end)) break;
-            float4 x, y;
-            x = make_float4(expf(g.to_end(0)), expf(g.to_end(1)),
-                            expf(g.to_end(2)), expf(g.to_end(3)));
-            y = make_float4(g.cum[0].hi * kLog2e, g.cum[1].hi * kLog2e, g.cum[2].hi * kLog2e, g.cum[3].hi * kLog2e);
+            Weight wt[4];
+            float c2[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                wt[j] = split_weight(exp2_fast(g.to_end(j) * kLog2e));
+                c2[j] = g.cum[j].hi * kLog2e;
+            }
             uint4 *ws = reinterpret_cast<uint4 *>(wring + w * 384);
-            const Weight wa = split_weight(x.x), wb = split_weight(x.y), wc = split_weight(x.z), wd = split_weight(x.w);
-            ws[lane] = make_uint4(wa.h, wb.h, wc.h, wd.h);
-            ws[lane + 32] = make_uint4(wa.m, wb.m, wc.m, wd.m);
-            ws[lane + 64] = make_uint4(wa.l, wb.l, wc.l, wd.l);
+            ws[lane] = make_uint4(wt[0].h, wt[1].h, wt[2].h, wt[3].h);
+            ws[lane + 32] = make_uint4(wt[0].m, wt[1].m, wt[2].m, wt[3].m);
+            ws[lane + 64] = make_uint4(wt[0].l, wt[1].l, wt[2].l, wt[3].l);
             float4 *slot = reinterpret_cast<float4 *>(gring + w * 256);
-            slot[lane] = y;
-            const float r = __shfl_sync(~0u, y.w, lane | 7);
-            slot[lane + 32] = make_float4(exp2_fast(r - y.x), exp2_fast(r - y.y), exp2_fast(r - y.z), exp2_fast(r - y.w));
+            slot[lane] = make_float4(c2[0], c2[1], c2[2], c2[3]);
+            const float r = __shfl_sync(~0u, c2[3], lane | 7);
+            slot[lane + 32] = make_float4(exp2_fast(r - c2[0]), exp2_fast(r - c2[1]), exp2_fast(r - c2[2]), exp2_fast(r - c2[3]));
             if (lane == 0) dring[w] = expf(g.all.hi);
             mbar_arrive(&bars[L::GFULL + w]);
         }
     } else if (warp < 8) {
-        // the state, one row of 64 columns a thread; and the rows of O
+        // the state, in tensor memory: a row of 64 columns a thread.  Before a
+        // chunk it goes out as an operand and is scaled by the chunk's decay.
         const int row = 32 * (warp & 3) + lane;
         const bool mine = row < DK;
-        float S[64];
+        const uint32_t ts = tmem + lane_base(warp) + TM_S;
         const size_t page = (((size_t)seq * p.a.H + h) * DK + row) * DV + 64 * slice;
+        auto state_in = [&](int e, uint32_t (&x)[16]) {
 #pragma unroll
-        for (int e = 0; e < 64; e += 4) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (mine && p.a.s0) x = *reinterpret_cast<const float4 *>(p.a.s0 + page + e);
-            S[e] = x.x, S[e + 1] = x.y, S[e + 2] = x.z, S[e + 3] = x.w;
-        }
+            for (int j = 0; j < 16; j += 4) {
+                uint4 y = make_uint4(0, 0, 0, 0);
+                if (mine && p.a.s0) y = *reinterpret_cast<const uint4 *>(p.a.s0 + page + e + j);
+                x[j] = y.x, x[j + 1] = y.y, x[j + 2] = y.z, x[j + 3] = y.w;
+            }
+        };
         bool ok = true;
 #pragma unroll 1
-        for (int i = 0; i <= n; ++i) {  // the outputs are a chunk behind the state
-            if (i < n) {
-                const int w = i % kGRing;
-                if (i >= 1) ok = la_wait(&bars[L::SEMPTY], (i - 1) & 1, end);
-                if (!warp_ok(ok)) break;
-                if (mine)
-#pragma unroll
-                    for (int e = 0; e < 64; e += 8)
-                        *reinterpret_cast<uint4 *>(sm + L::S + sw128_offset(row, e)) =
-                            make_uint4(pack_bf16(S[e], S[e + 1]), pack_bf16(S[e + 2], S[e + 3]), pack_bf16(S[e + 4], S[e + 5]),
-                                       pack_bf16(S[e + 6], S[e + 7]));
-                fence_proxy_async_smem();
-                mbar_arrive(&bars[L::SREADY]);
-                ok = la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, end) && la_wait(&bars[L::UFULL], i & 1, end);
-                if (!warp_ok(ok)) break;
-                const float d = dring[w];
-                tc_fence_after_sync();
-#pragma unroll
-                for (int e = 0; e < 64; e += 32) {
-                    uint32_t u[32];
-                    tmem_ld32(tmem + lane_base(warp) + TM_U + e, u);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) S[e + j] = fmaf(d, S[e + j], __uint_as_float(u[j]));
-                }
-                tc_fence_before_sync();
-                mbar_arrive(&bars[L::UEMPTY]);
-            }
-            if (i == 0) continue;
-            const int j = i - 1, w = j % kGRing;
-            ok = la_wait(&bars[L::OSFULL + (j & 1)], (j / 2) & 1, end) && la_wait(&bars[L::OFULL], j & 1, end);
+        for (int i = 0; i < n; ++i) {
+            const int w = i % kGRing;
+            ok = la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, end);
+            if (i >= 1) ok = ok && la_wait(&bars[L::SEMPTY], (i - 1) & 1, end) && la_wait(&bars[L::UFULL], (i - 1) & 1, end);
             if (!warp_ok(ok)) break;
             tc_fence_after_sync();
-            const Chunk c = chunk_at<kC>(p.v, p.a.T, sq.x + j);
-            const float f = exp2_fast(gring[w * 256 + row]) * p.a.scale;
-            __nv_bfloat16 *out = at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, c.row, h, c.t0 + row) + 64 * slice;
+            const float d = dring[w];
+            uint8_t *op = sm + L::S + row * 128;
 #pragma unroll 1
             for (int e = 0; e < 64; e += 16) {
-                uint32_t x[16], y[16];
-                tmem_ld16(tmem + lane_base(warp) + TM_OS + 64u * (j & 1) + e, x);
-                tmem_ld16(tmem + lane_base(warp) + TM_OP + e, y);
-                tmem_wait_ld();
-                if (row < c.len) {
-                    uint32_t w8[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        w8[k] = pack_bf16(fmaf(f, __uint_as_float(x[2 * k]), p.a.scale * __uint_as_float(y[2 * k])),
-                                          fmaf(f, __uint_as_float(x[2 * k + 1]), p.a.scale * __uint_as_float(y[2 * k + 1])));
-                    if (p.wide) {
-                        st_global_32(out + e, w8);
-                    } else {
-                        reinterpret_cast<uint4 *>(out + e)[0] = make_uint4(w8[0], w8[1], w8[2], w8[3]);
-                        reinterpret_cast<uint4 *>(out + e)[1] = make_uint4(w8[4], w8[5], w8[6], w8[7]);
-                    }
+                uint32_t x[16];
+                if (i == 0) {
+                    state_in(e, x);
+                } else {
+                    tmem_ld16(ts + e, x);
+                    tmem_wait_ld();
                 }
+                if (mine)
+#pragma unroll
+                    for (int j = 0; j < 16; j += 8) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) y[k] = pack_bf16(__uint_as_float(x[j + 2 * k]), __uint_as_float(x[j + 2 * k + 1]));
+                        *reinterpret_cast<uint4 *>(op + ((((e + j) >> 3) ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(d * __uint_as_float(x[j]));
+                tmem_st16(ts + e, x);
             }
+            tmem_wait_st();
+            fence_proxy_async_smem();
             tc_fence_before_sync();
-            mbar_arrive(&bars[L::OEMPTY]);
-            mbar_arrive(&bars[L::OSEMPTY + (j & 1)]);
+            mbar_arrive(&bars[L::SREADY]);
             mbar_arrive(&bars[L::GEMPTY + w]);
         }
-        if (p.a.sf && mine && ok)
+        if (p.a.sf && warp_ok(ok)) {
+            if (n > 0) ok = warp_ok(la_wait(&bars[L::UFULL], (n - 1) & 1, end));
+            tc_fence_after_sync();
+#pragma unroll 1
+            for (int e = 0; e < 64 && ok; e += 16) {
+                uint32_t x[16];
+                if (n == 0) {
+                    state_in(e, x);
+                } else {
+                    tmem_ld16(ts + e, x);
+                    tmem_wait_ld();
+                }
+                if (mine)
 #pragma unroll
-            for (int e = 0; e < 64; e += 4)
-                *reinterpret_cast<float4 *>(p.a.sf + page + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+                    for (int j = 0; j < 16; j += 4)
+                        *reinterpret_cast<uint4 *>(p.a.sf + page + e + j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+            }
+        }
     } else if (warp < 12) {
-        // P in blocks of 32 columns, thread's row t.  On the warp's diagonal the
-        // decay is e^{c_t - c_s}; in a block before it e^{c_t - c_r} e^{c_r - c_s}
-        // with r the block's last token, whose factors are both at most 1 for
-        // decays, so that a row costs one exponential a block.
+        // P in blocks of 16 columns, thread's row t.  On the warp's diagonal (32
+        // columns) the decay is e^{c_t - c_s}; before it e^{c_t - c_r} e^{c_r - c_s}
+        // with r the last token of s's block of 32, whose factors are both at most
+        // 1 for decays, so that a row costs one exponential a block.
         const int t = 32 * (warp & 3) + lane, diag = 32 * (warp & 3);
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
             const int w = i % kGRing;
-            bool ok = la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, end);
-            ok = ok && la_wait(&bars[L::TFULL + (i & 1)], (i / 2) & 1, end);
+            const bool ok = la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, end) && la_wait(&bars[L::TFULL + (i & 1)], (i / 2) & 1, end);
             if (!warp_ok(ok)) break;
             tc_fence_after_sync();
             const float *c2 = gring + w * 256, *cf = c2 + 128;
             const float ct = c2[t];
             const uint32_t tt = tmem + lane_base(warp) + TM_T + 128u * (i & 1);
+            uint32_t u[16], y[8];
 #pragma unroll 1
-            for (int s = 0; s <= diag; s += 32) {
-                uint32_t u[32], y[16];
-                tmem_ld32(tt + s, u);
-                const float rf = exp2_fast(ct - c2[s + 31]);
+            for (int s = 0; s < diag; s += 16) {
+                tmem_ld16(tt + s, u);
+                const float rf = exp2_fast(ct - c2[s | 31]);
                 tmem_wait_ld();
-                if (s < diag) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(cf + s + j);
-                        y[j / 2] = pack_bf16(__uint_as_float(u[j]) * (rf * f.x), __uint_as_float(u[j + 1]) * (rf * f.y));
-                        y[j / 2 + 1] = pack_bf16(__uint_as_float(u[j + 2]) * (rf * f.z), __uint_as_float(u[j + 3]) * (rf * f.w));
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 cs = *reinterpret_cast<const float4 *>(c2 + s + j);
-                        const float x0 = j + 0 <= lane ? __uint_as_float(u[j]) * exp2_fast(ct - cs.x) : 0.f;
-                        const float x1 = j + 1 <= lane ? __uint_as_float(u[j + 1]) * exp2_fast(ct - cs.y) : 0.f;
-                        const float x2 = j + 2 <= lane ? __uint_as_float(u[j + 2]) * exp2_fast(ct - cs.z) : 0.f;
-                        const float x3 = j + 3 <= lane ? __uint_as_float(u[j + 3]) * exp2_fast(ct - cs.w) : 0.f;
-                        y[j / 2] = pack_bf16(x0, x1);
-                        y[j / 2 + 1] = pack_bf16(x2, x3);
-                    }
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(cf + s + j);
+                    y[j / 2] = pack_bf16(__uint_as_float(u[j]) * (rf * f.x), __uint_as_float(u[j + 1]) * (rf * f.y));
+                    y[j / 2 + 1] = pack_bf16(__uint_as_float(u[j + 2]) * (rf * f.z), __uint_as_float(u[j + 3]) * (rf * f.w));
                 }
-                tmem_st16(tt + s / 2, y);
+                tmem_st8(tt + s / 2, y);
             }
 #pragma unroll 1
-            for (int s = diag + 32; s < kC; s += 32) {  // P's columns s / 2.. hold what T's have been read for
-                uint32_t z[16];
+            for (int s = diag; s < diag + 32; s += 16) {
+                tmem_ld16(tt + s, u);
+                tmem_wait_ld();
+                const int last = t - s;  // the row's last column of the block
 #pragma unroll
-                for (int j = 0; j < 16; ++j) z[j] = 0u;
-                tmem_st16(tt + s / 2, z);
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 cs = *reinterpret_cast<const float4 *>(c2 + s + j);
+                    const float x0 = j + 0 <= last ? __uint_as_float(u[j]) * exp2_fast(ct - cs.x) : 0.f;
+                    const float x1 = j + 1 <= last ? __uint_as_float(u[j + 1]) * exp2_fast(ct - cs.y) : 0.f;
+                    const float x2 = j + 2 <= last ? __uint_as_float(u[j + 2]) * exp2_fast(ct - cs.z) : 0.f;
+                    const float x3 = j + 3 <= last ? __uint_as_float(u[j + 3]) * exp2_fast(ct - cs.w) : 0.f;
+                    y[j / 2] = pack_bf16(x0, x1);
+                    y[j / 2 + 1] = pack_bf16(x2, x3);
+                }
+                tmem_st8(tt + s / 2, y);
             }
+            // P's columns past the diagonal take the place of T's that have been read
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = 0u;
+#pragma unroll 1
+            for (int s = diag + 32; s < kC; s += 16) tmem_st8(tt + s / 2, y);
             tmem_wait_st();
             tc_fence_before_sync();
             mbar_arrive(&bars[L::PREADY + (i & 1)]);
             mbar_arrive(&bars[L::GEMPTY + w]);
         }
-    } else {
-        // the weighted values, in quarters of 32 tokens: row r, 16 columns
+    } else if (warp < 16) {
+        // the weighted values, in quarters of 32 tokens: row r of each, 16 columns
         const int ct = threadIdx.x - 384, r = ct >> 2, c0 = (ct & 3) * 16;
+        const uint32_t off[2] = {sw128_offset(r, c0), sw128_offset(r, c0 + 8)};
+        int xs = 0, xp = 1;  // slot of X, and the phase of its last release
+        bool ok = true;
 #pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-            const int v = i % kVStages, w = i % kGRing;
-            const Chunk c = chunk_at<kC>(p.v, p.a.T, sq.x + i);
-            bool ok = la_wait(&bars[L::VFULL + v], (i / kVStages) & 1, end);
-            ok = ok && la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, end);
+        for (int i = 0; i < n && ok; ++i) {
+            const int v = i % kVStages, w = i % kGRing, len = chunk(i).len;
+            ok = la_wait(&bars[L::VFULL + v], (i / kVStages) & 1, end) && la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, end);
             uint8_t *vt = sm + L::V + v * 16384;
-            if (ok && c.len < kC) {
+            if (len < kC) {
                 // rows past the chunk's tokens are another sequence's: zeros, so
                 // that nothing of theirs (an infinity, say) meets a zero weight
-                ok = la_wait(&bars[L::QKFULL + i % kQKStages], (i / kQKStages) & 1, end);
+                ok = ok && la_wait(&bars[L::KFULL + i % kQKStages], (i / kQKStages) & 1, end);
                 uint8_t *k = sm + L::QK + (i % kQKStages) * 2 * L::TB;
-                if (ok)
+                if (ok) {
 #pragma unroll 1
-                    for (int e = ct; e < (kC - c.len) * (DK / 8); e += 128) {
-                        const int row = c.len + e / (DK / 8), col = (e % (DK / 8)) * 8;
+                    for (int row = r; row < kC; row += 32)
+                        if (row >= len) {
+                            *reinterpret_cast<uint4 *>(vt + (row - r) * 128 + off[0]) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(vt + (row - r) * 128 + off[1]) = make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll 1
+                    for (int e = ct; e < (kC - len) * (DK / 8); e += 128) {
+                        const int row = len + e / (DK / 8), col = (e % (DK / 8)) * 8;
                         *reinterpret_cast<uint4 *>(k + (col >> 6) * 16384 + sw128_offset(row, col & 63)) = make_uint4(0, 0, 0, 0);
                     }
-                if (ok)
-#pragma unroll 1
-                    for (int e = ct; e < (kC - c.len) * 8; e += 128)
-                        *reinterpret_cast<uint4 *>(vt + sw128_offset(c.len + (e >> 3), (e & 7) * 8)) = make_uint4(0, 0, 0, 0);
+                }
                 fence_proxy_async_smem();
             }
-            if (!warp_ok(ok)) break;
-            mbar_arrive(&bars[L::VREADY + v]);
+            if (ok) mbar_arrive(&bars[L::VREADY + v]);
+            const uint32_t *wr = wring + w * 384 + r;
 #pragma unroll 1
-            for (int qd = 0; qd < 4; ++qd) {
-                const int xn = 4 * i + qd, b = xn % kXRing, t = 32 * qd + r;
-                const uint32_t *wr = wring + w * 384 + t;
+            for (int qd = 0; qd < 4; ++qd, wr += 32, vt += 4096) {
+                const uint4 x[2] = {*reinterpret_cast<const uint4 *>(vt + off[0]), *reinterpret_cast<const uint4 *>(vt + off[1])};
                 const Weight wt = {wr[0], wr[128], wr[256]};
-                uint4 v[2];
+                ok = ok && la_wait(&bars[L::XEMPTY + xs], xp, end);
+                if (!ok) break;
+                uint8_t *xb = sm + L::X + xs * terms * 4096;
+                if (terms == 3) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    v[u] = *reinterpret_cast<const uint4 *>(vt + sw128_offset(t, c0 + 8 * u));
-                    if (t >= c.len) v[u] = make_uint4(0, 0, 0, 0);
-                }
-                if (xn >= kXRing && !la_wait(&bars[L::XEMPTY + b], (xn / kXRing - 1) & 1, end)) ok = false;
-                if (!warp_ok(ok)) break;
-                uint8_t *xb = sm + L::X + b * 3 * 4096;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const uint32_t off = sw128_offset(r, c0 + 8 * u);
-                    uint4 x, y, z;
-                    if (terms == 3) {
-                        weigh3(v[u].x, wt, x.x, y.x, z.x), weigh3(v[u].y, wt, x.y, y.y, z.y);
-                        weigh3(v[u].z, wt, x.z, y.z, z.z), weigh3(v[u].w, wt, x.w, y.w, z.w);
-                        *reinterpret_cast<uint4 *>(xb + 8192 + off) = z;
-                    } else {
-                        weigh2(v[u].x, wt, x.x, y.x), weigh2(v[u].y, wt, x.y, y.y);
-                        weigh2(v[u].z, wt, x.z, y.z), weigh2(v[u].w, wt, x.w, y.w);
+                    for (int u = 0; u < 2; ++u) {
+                        uint4 a, b, d;
+                        weigh3(x[u].x, wt, a.x, b.x, d.x), weigh3(x[u].y, wt, a.y, b.y, d.y);
+                        weigh3(x[u].z, wt, a.z, b.z, d.z), weigh3(x[u].w, wt, a.w, b.w, d.w);
+                        *reinterpret_cast<uint4 *>(xb + off[u]) = a;
+                        *reinterpret_cast<uint4 *>(xb + 4096 + off[u]) = b;
+                        *reinterpret_cast<uint4 *>(xb + 8192 + off[u]) = d;
                     }
-                    *reinterpret_cast<uint4 *>(xb + off) = x;
-                    *reinterpret_cast<uint4 *>(xb + 4096 + off) = y;
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        uint4 a, b;
+                        weigh2(x[u].x, wt, a.x, b.x), weigh2(x[u].y, wt, a.y, b.y);
+                        weigh2(x[u].z, wt, a.z, b.z), weigh2(x[u].w, wt, a.w, b.w);
+                        *reinterpret_cast<uint4 *>(xb + off[u]) = a;
+                        *reinterpret_cast<uint4 *>(xb + 4096 + off[u]) = b;
+                    }
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(&bars[L::XREADY + b]);
+                mbar_arrive(&bars[L::XREADY + xs]);
+                if (++xs == xring) xs = 0, xp ^= 1;
             }
-            if (!warp_ok(ok)) break;
+            if (!ok) break;
             mbar_arrive(&bars[L::VEMPTY + v]);
+            mbar_arrive(&bars[L::GEMPTY + w]);
+        }
+    } else {
+        // the rows of O: scale (e^c (Q S) + P V)
+        const int t = 32 * (warp & 3) + lane;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            const int w = i % kGRing;
+            const bool ok = la_wait(&bars[L::OSFULL + (i & 1)], (i / 2) & 1, end) && la_wait(&bars[L::OFULL], i & 1, end);
+            if (!warp_ok(ok)) break;
+            tc_fence_after_sync();
+            const Chunk c = chunk(i);
+            const float f = exp2_fast(gring[w * 256 + t]) * p.a.scale;
+            __nv_bfloat16 *out = at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, c.row, h, c.t0 + t) + 64 * slice;
+            const uint32_t ts = tmem + lane_base(warp) + TM_OS + 64u * (i & 1), tp = tmem + lane_base(warp) + TM_OP;
+#pragma unroll 1
+            for (int e = 0; e < 64; e += 16) {
+                uint32_t x[16], y[16], z[8];
+                tmem_ld16(ts + e, x);
+                tmem_ld16(tp + e, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    z[j] = pack_bf16(fmaf(f, __uint_as_float(x[2 * j]), p.a.scale * __uint_as_float(y[2 * j])),
+                                     fmaf(f, __uint_as_float(x[2 * j + 1]), p.a.scale * __uint_as_float(y[2 * j + 1])));
+                if (t < c.len) {
+                    if (p.wide) {
+                        st_global_32(out + e, z);
+                    } else {
+                        reinterpret_cast<uint4 *>(out + e)[0] = make_uint4(z[0], z[1], z[2], z[3]);
+                        reinterpret_cast<uint4 *>(out + e)[1] = make_uint4(z[4], z[5], z[6], z[7]);
+                    }
+                }
+            }
+            tc_fence_before_sync();
+            mbar_arrive(&bars[L::OEMPTY]);
+            mbar_arrive(&bars[L::OSEMPTY + (i & 1)]);
             mbar_arrive(&bars[L::GEMPTY + w]);
         }
     }
@@ -986,14 +1081,12 @@ bool linattn_tc_supported(const LinAttnArgs &a) {
     return a.dtype == GDN_BF16 && !(a.flags & GDN_PATH_SIMT) && sm100_family();
 }
 
-size_t linattn_tc_fwd_workspace(const LinAttnArgs &a) { return table_bytes(a, kC); }
+size_t linattn_tc_fwd_workspace(const LinAttnArgs &) { return 0; }
 
 int launch_linattn_tc_fwd(const LinAttnArgs &a, cudaStream_t stream) {
     TcArgs p{};
     p.a = a;
     p.timeout_ns = wait_limit_ns();
-    const int st = make_view(a, kC, a.ws, &p.v, stream);
-    if (st != GDN_OK) return st;
     if (a.Dk == 128) return a.Dv == 128 ? run_fwd<128, 128>(p, stream) : run_fwd<128, 64>(p, stream);
     return a.Dv == 128 ? run_fwd<64, 128>(p, stream) : run_fwd<64, 64>(p, stream);
 }
