@@ -4,11 +4,11 @@
 //
 // prompt_kernel is the forward in one launch.  A CTA owns 64 value columns of
 // one head (columns are independent) and walks a sequence's chunks with the
-// fp32 state in tensor memory, so q, k, v and o cross the memory once (a head's two
+// fp32 state in registers, so q, k, v and o cross the memory once (a head's two
 // CTAs run side by side and share q and k in L2).  A chunk is four products:
 // T = Q K^T; P V with P = T under the decay mask, in tensor memory; Q S; and
-// the chunk's own share of the state K^T diag(w) V, added to the state after
-// it has been scaled by the chunk's decay.
+// the chunk's own share of the state K^T diag(w) V, which does not depend on
+// the state, so the walk itself costs one multiply-add an element.
 // The weighted values w v go in as two or three bf16 terms (x = hi + mid + lo
 // to 2^-24): with one, the state would carry 2^-9 of rounding in every term,
 // against inputs that are exact; sums and state stay in fp32.  P and S enter
@@ -437,15 +437,15 @@ struct FwdSmem {
     static constexpr uint32_t BAR = D + 64;
     enum { KFULL = 0, KEMPTY = 2, QFULL = 4, QEMPTY = 6, VFULL = 8, VREADY = 11, VEMPTY = 14, XREADY = 17,
            XEMPTY = XREADY + kXMax, UFULL = XEMPTY + kXMax,
-           SREADY, SEMPTY, TFULL, PREADY = TFULL + 2, OFULL = PREADY + 2, OEMPTY, OSFULL, OSEMPTY = OSFULL + 2, GFULL = OSEMPTY + 2, GEMPTY = GFULL + kGRing,
+           UEMPTY, SREADY, SEMPTY, TFULL, PREADY = TFULL + 2, OFULL = PREADY + 2, OEMPTY, GFULL, GEMPTY = GFULL + kGRing,
            DRAIN = GEMPTY + kGRing, NUM = DRAIN + 2 };
     static constexpr uint32_t TSLOT = BAR + 8 * NUM;
     static constexpr uint32_t BYTES = TSLOT + 16;
 };
 static_assert(FwdSmem<128>::BYTES <= 232448, "prompt kernel fits the shared memory of one CTA");
 // TMEM columns: Q K^T twice (P, two bf16 a column, takes its first half), Q S
-// twice, P V, the state
-constexpr uint32_t TM_T = 0, TM_OS = 256, TM_OP = 384, TM_S = 448;
+// twice, P V, the chunk's share of the state
+constexpr uint32_t TM_T = 0, TM_OS = 256, TM_OP = 384, TM_U = 448;
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -467,6 +467,35 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) { return (saddr >> 4) | (lbo_bytes >> 4) << 16; }
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
     return (uint64_t)((1024u >> 4) | 1u << 14 | 2u << 29) << 32 | lo;
+}
+
+// A chunk's log-decays, lane's tokens 4 lane ..: summed up to each from the
+// chunk's start, and after it to the end, each way by itself: weights near the
+// end are made from few terms, not from the difference of two large sums.
+struct Sums {
+    float cum[4], to_end[4], all;
+};
+__device__ __forceinline__ Sums scan_sums(const float (&g)[4]) {
+    const int lane = threadIdx.x & 31;
+    Sums r;
+    r.cum[0] = g[0], r.cum[1] = g[0] + g[1], r.cum[2] = r.cum[1] + g[2], r.cum[3] = r.cum[2] + g[3];
+    r.to_end[3] = 0.f, r.to_end[2] = g[3], r.to_end[1] = g[3] + g[2], r.to_end[0] = r.to_end[1] + g[1];
+    float up = r.cum[3], down = r.cum[3];
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const float x = __shfl_up_sync(~0u, up, m), y = __shfl_down_sync(~0u, down, m);
+        if (lane >= m) up += x;
+        if (lane + m < 32) down += y;
+    }
+    r.all = __shfl_sync(~0u, up, 31);
+    up = __shfl_up_sync(~0u, up, 1);
+    down = __shfl_down_sync(~0u, down, 1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (lane > 0) r.cum[j] += up;
+        if (lane < 31) r.to_end[j] += down;
+    }
+    return r;
 }
 
 // 32 bytes to a 32-byte aligned address: whole sectors.
@@ -544,9 +573,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             mbar_init(&bars[L::KFULL + s], 1);
             mbar_init(&bars[L::KEMPTY + s], 2);
             mbar_init(&bars[L::QFULL + s], 1);
-            mbar_init(&bars[L::QEMPTY + s], 2);
-            mbar_init(&bars[L::OSFULL + s], 1);
-            mbar_init(&bars[L::OSEMPTY + s], 128);
+            mbar_init(&bars[L::QEMPTY + s], 1);
             mbar_init(&bars[L::DRAIN + s], 1);
             mbar_init(&bars[L::TFULL + s], 1);
             mbar_init(&bars[L::PREADY + s], 128);
@@ -565,6 +592,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             mbar_init(&bars[L::GEMPTY + s], 512);
         }
         mbar_init(&bars[L::UFULL], 1);
+        mbar_init(&bars[L::UEMPTY], 128);
         mbar_init(&bars[L::SREADY], 128);
         mbar_init(&bars[L::SEMPTY], 1);
         mbar_init(&bars[L::OFULL], 1);
@@ -617,98 +645,87 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             drain(L::VFULL, kVStages, iv);
         }
     } else if (warp == 1) {
-        // the products around P: Q K^T a chunk ahead, and P V
+        // the products of the outputs: Q K^T a chunk ahead, Q S and P V.  All
+        // lanes wait, one issues.
         constexpr uint32_t idT = idesc_bf16(128, 128, false, false), idO = idesc_bf16(128, 64, false, true);
         const bool leader = elect_one();
-        // T's place is free: P V of two chunks before, the last to read it,
-        // was issued before (products run in the order of their issue)
-        bool ok = true;
 #pragma unroll 1
         for (int i = -1; i < n; ++i) {
             if (i + 1 < n) {
+                // T's place is free: P V of two chunks before, the last to read
+                // it, was issued before (products run in the order of their issue)
                 const int j = i + 1, st = j % kQKStages;
-                ok = la_wait(&bars[L::KFULL + st], (j / kQKStages) & 1, end) && la_wait(&bars[L::QFULL + st], (j / kQKStages) & 1, end);
-                if (!warp_ok(ok)) break;
-                tc_fence_after_sync();
+                if (!la_wait(&bars[L::KFULL + st], (j / kQKStages) & 1, end)) break;
+                if (!la_wait(&bars[L::QFULL + st], (j / kQKStages) & 1, end)) break;
                 const uint32_t k = desc_lo(sbase + L::QK + st * 2 * L::TB, 16), q = k + (L::TB >> 4), d = TM_T + 128u * (j & 1);
                 if (leader) {
                     mma_steps<DK / 16>(d, idT, [&](int ks) { return q + (ks >> 2) * 1024 + (ks & 3) * 2; },
                                        [&](int ks) { return k + (ks >> 2) * 1024 + (ks & 3) * 2; });
-                    mma_commit(&bars[L::KEMPTY + st]);
-                    mma_commit(&bars[L::QEMPTY + st]);
                     mma_commit(&bars[L::TFULL + (j & 1)]);
+                    mma_commit(&bars[L::KEMPTY + st]);
                 }
-                __syncwarp();
             }
             if (i < 0) continue;
-            ok = la_wait(&bars[L::PREADY + (i & 1)], (i / 2) & 1, end) && la_wait(&bars[L::VREADY + i % kVStages], (i / kVStages) & 1, end);
-            if (i >= 1) ok = ok && la_wait(&bars[L::OEMPTY], (i - 1) & 1, end);
-            if (!warp_ok(ok)) break;
+            if (!la_wait(&bars[L::SREADY], i & 1, end)) break;
+            if (leader) {  // into the place that P V of one chunk before has waited for
+                const uint32_t q = desc_lo(sbase + L::QK + (i % kQKStages) * 2 * L::TB + L::TB, 16), x = desc_lo(sbase + L::S, 8192);
+                mma_steps<DK / 16>(TM_OS + 64u * (i & 1), idO, [&](int ks) { return q + (ks >> 2) * 1024 + (ks & 3) * 2; },
+                                   [&](int ks) { return x + ks * 128; });
+                mma_commit(&bars[L::SEMPTY]);
+                mma_commit(&bars[L::QEMPTY + i % kQKStages]);
+            }
+            if (!la_wait(&bars[L::PREADY + (i & 1)], (i / 2) & 1, end)) break;
+            if (!la_wait(&bars[L::VREADY + i % kVStages], (i / kVStages) & 1, end)) break;
+            if (i >= 1 && !la_wait(&bars[L::OEMPTY], (i - 1) & 1, end)) break;
             tc_fence_after_sync();
             const uint32_t v = desc_lo(sbase + L::V + (i % kVStages) * 16384, 8192), t = TM_T + 128u * (i & 1);
             if (leader) {
                 mma_ts<0>(TM_OP, t, desc_of(v), idO);
 #pragma unroll
                 for (int ks = 1; ks < kC / 16; ++ks) mma_ts<1>(TM_OP, t + 8 * ks, desc_of(v + ks * 128), idO);
-                mma_commit(&bars[L::VEMPTY + i % kVStages]);
                 mma_commit(&bars[L::OFULL]);
+                mma_commit(&bars[L::VEMPTY + i % kVStages]);
             }
-            __syncwarp();
         }
         // every MMA issued here is complete before TMEM is released
         if (leader) mma_commit(&bars[L::DRAIN]);
         mbar_wait(&bars[L::DRAIN], 0, kDrainNs);
     } else if (warp == 2) {
-        // the products of the state's walk: the chunk's share, added to it, and Q S
-        constexpr uint32_t idU = idesc_bf16(128, 64, true, true), idO = idesc_bf16(128, 64, false, true);
+        // the chunk's share of the state, as far as the weighted values are there
+        constexpr uint32_t idU = idesc_bf16(128, 64, true, true);
         const bool leader = elect_one();
+        int xs = 0;  // slot of X, and its phase
+        uint32_t xp = 0;
         bool ok = true;
-        int xs = 0, xp = 0;  // slot of X, and its phase
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
             const int st = i % kQKStages;
-            const uint32_t kb = sbase + L::QK + st * 2 * L::TB, k = desc_lo(kb, 16384), q = desc_lo(kb + L::TB, 16);
-            // the state has been scaled, and is there as an operand
-            ok = la_wait(&bars[L::KFULL + st], (i / kQKStages) & 1, end) && la_wait(&bars[L::SREADY], i & 1, end);
+            uint32_t k = desc_lo(sbase + L::QK + st * 2 * L::TB, 16384);
+            ok = la_wait(&bars[L::KFULL + st], (i / kQKStages) & 1, end);
+            if (i >= 1) ok = ok && la_wait(&bars[L::UEMPTY], (i - 1) & 1, end);
+            tc_fence_after_sync();
 #pragma unroll 1
-            for (int qd = 0; qd < 4; ++qd) {
+            for (int qd = 0; qd < 4; ++qd, k += 256) {
                 ok = ok && la_wait(&bars[L::XREADY + xs], xp, end);
-                if (!warp_ok(ok)) break;
-                tc_fence_after_sync();
-                const uint32_t x = desc_lo(sbase + L::X + xs * terms * 4096, 8192), kq = k + qd * 256;
+                if (!ok) break;
+                const uint32_t x = desc_lo(sbase + L::X + xs * terms * 4096, 8192);
                 if (leader) {
-                    mma_ss<1>(TM_S, desc_of(kq), desc_of(x), idU);
-                    mma_ss<1>(TM_S, desc_of(kq + 128), desc_of(x + 128), idU);
-                    mma_ss<1>(TM_S, desc_of(kq), desc_of(x + 256), idU);
-                    mma_ss<1>(TM_S, desc_of(kq + 128), desc_of(x + 384), idU);
+                    if (qd == 0) mma_ss<0>(TM_U, desc_of(k), desc_of(x), idU);
+                    else mma_ss<1>(TM_U, desc_of(k), desc_of(x), idU);
+                    mma_ss<1>(TM_U, desc_of(k + 128), desc_of(x + 128), idU);
+                    mma_ss<1>(TM_U, desc_of(k), desc_of(x + 256), idU);
+                    mma_ss<1>(TM_U, desc_of(k + 128), desc_of(x + 384), idU);
                     if (terms == 3) {
-                        mma_ss<1>(TM_S, desc_of(kq), desc_of(x + 512), idU);
-                        mma_ss<1>(TM_S, desc_of(kq + 128), desc_of(x + 640), idU);
+                        mma_ss<1>(TM_U, desc_of(k), desc_of(x + 512), idU);
+                        mma_ss<1>(TM_U, desc_of(k + 128), desc_of(x + 640), idU);
                     }
+                    if (qd == 3) mma_commit(&bars[L::UFULL]);
                     mma_commit(&bars[L::XEMPTY + xs]);
+                    if (qd == 3) mma_commit(&bars[L::KEMPTY + st]);
                 }
-                __syncwarp();
                 if (++xs == xring) xs = 0, xp ^= 1;
             }
-            if (!warp_ok(ok)) break;
-            if (leader) {
-                mma_commit(&bars[L::UFULL]);
-                mma_commit(&bars[L::KEMPTY + st]);
-            }
-            __syncwarp();
-            ok = la_wait(&bars[L::QFULL + st], (i / kQKStages) & 1, end);
-            if (i >= 2) ok = ok && la_wait(&bars[L::OSEMPTY + (i & 1)], (i / 2 - 1) & 1, end);
-            if (!warp_ok(ok)) break;
-            tc_fence_after_sync();
-            const uint32_t sd = desc_lo(sbase + L::S, 8192), d = TM_OS + 64u * (i & 1);
-            if (leader) {
-                mma_steps<DK / 16>(d, idO, [&](int ks) { return q + (ks >> 2) * 1024 + (ks & 3) * 2; },
-                                   [&](int ks) { return sd + ks * 128; });
-                mma_commit(&bars[L::SEMPTY]);
-                mma_commit(&bars[L::QEMPTY + st]);
-                mma_commit(&bars[L::OSFULL + (i & 1)]);
-            }
-            __syncwarp();
+            if (!ok) break;
         }
         if (leader) mma_commit(&bars[L::DRAIN + 1]);
         mbar_wait(&bars[L::DRAIN + 1], 0, kDrainNs);
@@ -726,15 +743,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
             const int w = i % kGRing;
-            const Gates<kC> g = scan_gates<kC>(next);
+            const Sums g = scan_sums(next);
             fetch(i + 1);
             if (i >= kGRing && !la_wait(&bars[L::GEMPTY + w], (i / kGRing - 1) & 1, end)) break;
             Weight wt[4];
             float c2[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                wt[j] = split_weight(exp2_fast(g.to_end(j) * kLog2e));
-                c2[j] = g.cum[j].hi * kLog2e;
+                wt[j] = split_weight(exp2_fast(g.to_end[j] * kLog2e));
+                c2[j] = g.cum[j] * kLog2e;
             }
             uint4 *ws = reinterpret_cast<uint4 *>(wring + w * 384);
             ws[lane] = make_uint4(wt[0].h, wt[1].h, wt[2].h, wt[3].h);
@@ -744,79 +761,54 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             slot[lane] = make_float4(c2[0], c2[1], c2[2], c2[3]);
             const float r = __shfl_sync(~0u, c2[3], lane | 7);
             slot[lane + 32] = make_float4(exp2_fast(r - c2[0]), exp2_fast(r - c2[1]), exp2_fast(r - c2[2]), exp2_fast(r - c2[3]));
-            if (lane == 0) dring[w] = expf(g.all.hi);
+            if (lane == 0) dring[w] = expf(g.all);
             mbar_arrive(&bars[L::GFULL + w]);
         }
     } else if (warp < 8) {
-        // the state, in tensor memory: a row of 64 columns a thread.  Before a
-        // chunk it goes out as an operand and is scaled by the chunk's decay.
+        // the state: a row of 64 columns a thread, in registers
         const int row = 32 * (warp & 3) + lane;
         const bool mine = row < DK;
-        const uint32_t ts = tmem + lane_base(warp) + TM_S;
+        float S[64];
         const size_t page = (((size_t)seq * p.a.H + h) * DK + row) * DV + 64 * slice;
-        auto state_in = [&](int e, uint32_t (&x)[16]) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-                uint4 y = make_uint4(0, 0, 0, 0);
-                if (mine && p.a.s0) y = *reinterpret_cast<const uint4 *>(p.a.s0 + page + e + j);
-                x[j] = y.x, x[j + 1] = y.y, x[j + 2] = y.z, x[j + 3] = y.w;
-            }
-        };
+        for (int e = 0; e < 64; e += 4) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (mine && p.a.s0) x = *reinterpret_cast<const float4 *>(p.a.s0 + page + e);
+            S[e] = x.x, S[e + 1] = x.y, S[e + 2] = x.z, S[e + 3] = x.w;
+        }
         bool ok = true;
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
             const int w = i % kGRing;
-            ok = la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, end);
-            if (i >= 1) ok = ok && la_wait(&bars[L::SEMPTY], (i - 1) & 1, end) && la_wait(&bars[L::UFULL], (i - 1) & 1, end);
-            if (!warp_ok(ok)) break;
-            tc_fence_after_sync();
-            const float d = dring[w];
-            uint8_t *op = sm + L::S + row * 128;
-#pragma unroll 1
-            for (int e = 0; e < 64; e += 16) {
-                uint32_t x[16];
-                if (i == 0) {
-                    state_in(e, x);
-                } else {
-                    tmem_ld16(ts + e, x);
-                    tmem_wait_ld();
-                }
-                if (mine)
+            if (i >= 1) ok = la_wait(&bars[L::SEMPTY], (i - 1) & 1, end);
+            if (mine)
 #pragma unroll
-                    for (int j = 0; j < 16; j += 8) {
-                        uint32_t y[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) y[k] = pack_bf16(__uint_as_float(x[j + 2 * k]), __uint_as_float(x[j + 2 * k + 1]));
-                        *reinterpret_cast<uint4 *>(op + ((((e + j) >> 3) ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-                    }
-#pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(d * __uint_as_float(x[j]));
-                tmem_st16(ts + e, x);
-            }
-            tmem_wait_st();
+                for (int e = 0; e < 64; e += 8)
+                    *reinterpret_cast<uint4 *>(sm + L::S + sw128_offset(row, e)) =
+                        make_uint4(pack_bf16(S[e], S[e + 1]), pack_bf16(S[e + 2], S[e + 3]), pack_bf16(S[e + 4], S[e + 5]),
+                                   pack_bf16(S[e + 6], S[e + 7]));
             fence_proxy_async_smem();
-            tc_fence_before_sync();
             mbar_arrive(&bars[L::SREADY]);
+            ok = ok && la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, end) && la_wait(&bars[L::UFULL], i & 1, end);
+            if (!warp_ok(ok)) break;
+            const float d = dring[w];
+            tc_fence_after_sync();
+#pragma unroll
+            for (int e = 0; e < 64; e += 16) {
+                uint32_t u[16];
+                tmem_ld16(tmem + lane_base(warp) + TM_U + e, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) S[e + j] = fmaf(d, S[e + j], __uint_as_float(u[j]));
+            }
+            tc_fence_before_sync();
+            mbar_arrive(&bars[L::UEMPTY]);
             mbar_arrive(&bars[L::GEMPTY + w]);
         }
-        if (p.a.sf && warp_ok(ok)) {
-            if (n > 0) ok = warp_ok(la_wait(&bars[L::UFULL], (n - 1) & 1, end));
-            tc_fence_after_sync();
-#pragma unroll 1
-            for (int e = 0; e < 64 && ok; e += 16) {
-                uint32_t x[16];
-                if (n == 0) {
-                    state_in(e, x);
-                } else {
-                    tmem_ld16(ts + e, x);
-                    tmem_wait_ld();
-                }
-                if (mine)
+        if (p.a.sf && mine && ok)
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4)
-                        *reinterpret_cast<uint4 *>(p.a.sf + page + e + j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-            }
-        }
+            for (int e = 0; e < 64; e += 4)
+                *reinterpret_cast<float4 *>(p.a.sf + page + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
     } else if (warp < 12) {
         // P in blocks of 16 columns, thread's row t.  On the warp's diagonal (32
         // columns) the decay is e^{c_t - c_s}; before it e^{c_t - c_r} e^{c_r - c_s}
@@ -947,36 +939,38 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
             const int w = i % kGRing;
-            const bool ok = la_wait(&bars[L::OSFULL + (i & 1)], (i / 2) & 1, end) && la_wait(&bars[L::OFULL], i & 1, end);
-            if (!warp_ok(ok)) break;
+            if (!warp_ok(la_wait(&bars[L::OFULL], i & 1, end))) break;
             tc_fence_after_sync();
             const Chunk c = chunk(i);
             const float f = exp2_fast(gring[w * 256 + t]) * p.a.scale;
-            __nv_bfloat16 *out = at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, c.row, h, c.t0 + t) + 64 * slice;
             const uint32_t ts = tmem + lane_base(warp) + TM_OS + 64u * (i & 1), tp = tmem + lane_base(warp) + TM_OP;
-#pragma unroll 1
-            for (int e = 0; e < 64; e += 16) {
-                uint32_t x[16], y[16], z[8];
-                tmem_ld16(ts + e, x);
-                tmem_ld16(tp + e, y);
+            uint32_t z[4][8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t x[16], y[16];
+                tmem_ld16(ts + 16 * e, x);
+                tmem_ld16(tp + 16 * e, y);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    z[j] = pack_bf16(fmaf(f, __uint_as_float(x[2 * j]), p.a.scale * __uint_as_float(y[2 * j])),
-                                     fmaf(f, __uint_as_float(x[2 * j + 1]), p.a.scale * __uint_as_float(y[2 * j + 1])));
-                if (t < c.len) {
-                    if (p.wide) {
-                        st_global_32(out + e, z);
-                    } else {
-                        reinterpret_cast<uint4 *>(out + e)[0] = make_uint4(z[0], z[1], z[2], z[3]);
-                        reinterpret_cast<uint4 *>(out + e)[1] = make_uint4(z[4], z[5], z[6], z[7]);
-                    }
-                }
+                    z[e][j] = pack_bf16(fmaf(f, __uint_as_float(x[2 * j]), p.a.scale * __uint_as_float(y[2 * j])),
+                                        fmaf(f, __uint_as_float(x[2 * j + 1]), p.a.scale * __uint_as_float(y[2 * j + 1])));
             }
             tc_fence_before_sync();
             mbar_arrive(&bars[L::OEMPTY]);
-            mbar_arrive(&bars[L::OSEMPTY + (i & 1)]);
             mbar_arrive(&bars[L::GEMPTY + w]);
+            __nv_bfloat16 *out = at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, c.row, h, c.t0 + t) + 64 * slice;
+            if (t < c.len) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (p.wide) {
+                        st_global_32(out + 16 * e, z[e]);
+                    } else {
+                        reinterpret_cast<uint4 *>(out)[2 * e] = make_uint4(z[e][0], z[e][1], z[e][2], z[e][3]);
+                        reinterpret_cast<uint4 *>(out)[2 * e + 1] = make_uint4(z[e][4], z[e][5], z[e][6], z[e][7]);
+                    }
+                }
+            }
         }
     }
     __syncwarp();
