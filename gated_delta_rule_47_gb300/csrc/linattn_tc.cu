@@ -67,19 +67,6 @@ __device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
         x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
     }
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-}
-// x[0..7] -> bf16(x), leaving x - bf16(x)
-__device__ __forceinline__ uint4 take8(float (&x)[8]) {
-    const uint4 p = pack8(x);
-    float h[8];
-    unpack8(p, h);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] -= h[e];
-    return p;
-}
-
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -131,321 +118,16 @@ __device__ __forceinline__ void weigh3(uint32_t v, const Weight &w, uint32_t &hi
 struct TcArgs {
     LinAttnArgs a;
     View v;
-    uint16_t *Shi, *Slo;  // [chunk][H][DK][DV] bf16: the states that enter the chunks (lo: the backward's)
-    uint16_t *Rhi, *Rlo;  // gradients of the states that leave them
-    float *dot;           // [chunk][H][DV / 64][4] shares of <R, S>
+    uint16_t *Shi, *Slo;  // [chunk][H][DK][DV] bf16 hi + lo: the states that enter the chunks
+    uint16_t *Rhi, *Rlo;  // and the gradients of the states that leave them
+    float *dqh, *dkh;     // [B,H,T,DK] fp32, where value heads share dq and dk
+    float *dgt;           // dg by token, with its strides
+    Strides sdg;
     unsigned long long timeout_ns;
     int wide;             // o's rows are 32-byte aligned
 };
 
-// ================================================================ state kernel
-constexpr int kStages = 3;
-constexpr int kStateThreads = 512;  // warp 0 TMA, 1 MMA, 2..9 weighting, 10..13 state, 14..15 decays
-constexpr int kConv = 256, kSt = 128;
-constexpr int kWRing = 4;
-
-template <int DK>
-struct StateSmem {
-    static constexpr uint32_t KB = DK * 256, VB = 16384;  // a chunk's K (or Q) and 64 columns of V (or dO)
-    static constexpr uint32_t STAGE = KB + VB;
-    // with DK = 64 the product's rows 64..127 read the bytes after K, in the
-    // stage's own V tile: rows that nobody looks at
-    static constexpr uint32_t X = kStages * STAGE;        // [half][3][64 tokens][128 B] weighted values
-    static constexpr uint32_t W = X + 2 * 3 * 8192;       // [ring][3][128] weights, then [ring] chunk decays
-    static constexpr uint32_t BAR = W + kWRing * 1536 + 64;
-    enum { FULL = 0, EMPTY = 3, XREADY = 6, XEMPTY = 8, UFULL = 10, UEMPTY = 12, WFULL = 14, WEMPTY = 18, DRAIN = 22, NUM = 23 };
-    static constexpr uint32_t TSLOT = BAR + 8 * NUM;
-    static constexpr uint32_t BYTES = TSLOT + 16;
-};
-static_assert(StateSmem<128>::BYTES <= 232448, "state kernel fits the shared memory of one CTA");
-
-// Grid (DV / 64, H, n_seq).  REV: the gradient's walk, backwards over the
-// chunks, with Q and dO in the places of K and V.  LO: also the states' lower
-// bf16 halves (the backward's products take both).
-template <int DK, int DV, bool REV, bool LO>
-__global__ void __launch_bounds__(kStateThreads, 1)
-    state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV, TcArgs p) {
-    using L = StateSmem<DK>;
-    extern __shared__ __align__(1024) uint8_t sm[];
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::TSLOT);
-    uint32_t *wring = reinterpret_cast<uint32_t *>(sm + L::W);
-    float *dring = reinterpret_cast<float *>(wring + kWRing * 384);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int slice = blockIdx.x, h = blockIdx.y, seq = blockIdx.z;
-    const int2 sq = seq_at(p.v, seq);
-    const int n = sq.y;
-    const uint64_t end = deadline_after(p.timeout_ns, n);
-
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&bars[L::FULL + s], 1);
-            mbar_init(&bars[L::EMPTY + s], 1);
-        }
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(&bars[L::XREADY + x], kConv);
-            mbar_init(&bars[L::XEMPTY + x], 1);
-            mbar_init(&bars[L::UFULL + x], 1);
-            mbar_init(&bars[L::UEMPTY + x], kSt);
-        }
-        for (int w = 0; w < kWRing; ++w) {
-            mbar_init(&bars[L::WFULL + w], 32);
-            mbar_init(&bars[L::WEMPTY + w], kConv + kSt);
-        }
-        mbar_init(&bars[L::DRAIN], 1);
-        fence_mbar_init();
-    }
-    if (warp == 1) {
-        tmem_alloc(tslot, 128);
-        tmem_relinquish();
-    }
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
-    const uint32_t tmem = *tslot;
-    const uint32_t sbase = smem_u32(sm);
-    auto chunk_of = [&](int i) { return sq.x + (REV ? n - 1 - i : i); };
-
-    if (warp == 0) {
-        if (lane == 0) {
-            const int hk = h / (p.a.H / p.a.Hk);
-            int i = 0;
-            for (; i < n; ++i) {
-                const int s = i % kStages;
-                if (i >= kStages && !la_wait(&bars[L::EMPTY + s], ((i / kStages) - 1) & 1, end)) break;
-                const Chunk c = chunk_at<kC>(p.v, p.a.T, chunk_of(i));
-                uint8_t *st = sm + s * L::STAGE;
-                mbar_arrive_expect_tx(&bars[L::FULL + s], L::STAGE);
-#pragma unroll
-                for (int x = 0; x < DK / 64; ++x)
-                    tma_load_4d(st + x * 16384, &mK, &bars[L::FULL + s], 64 * x, c.t0, hk, c.row);
-                tma_load_4d(st + L::KB, &mV, &bars[L::FULL + s], 64 * slice, c.t0, h, c.row);
-            }
-            // no copy is in flight when the CTA ends
-#pragma unroll 1
-            for (int j = i > kStages ? i - kStages : 0; j < i; ++j)
-                mbar_wait(&bars[L::FULL + j % kStages], (j / kStages) & 1, kDrainNs);
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t id = idesc_bf16(128, 64, true, true);
-            bool ok = true;
-#pragma unroll 1
-            for (int i = 0; i < n && ok; ++i) {
-                const int s = i % kStages, acc = i & 1;
-                ok = la_wait(&bars[L::FULL + s], (i / kStages) & 1, end);
-                if (ok && i >= 2) ok = la_wait(&bars[L::UEMPTY + acc], ((i >> 1) - 1) & 1, end);
-                for (int half = 0; half < 2 && ok; ++half) {
-                    ok = la_wait(&bars[L::XREADY + half], i & 1, end);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    const uint32_t ka = sbase + s * L::STAGE, xb = sbase + L::X + half * 3 * 8192;
-#pragma unroll
-                    for (int t = 0; t < 3; ++t)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_bf16_ss(tmem + 64u * acc, smem_desc(ka + (half * 4 + ks) * 2048, 16384, 1024),
-                                        smem_desc(xb + t * 8192 + ks * 2048, 8192, 1024), id,
-                                        (half | t | ks) ? 1u : 0u);
-                    mma_commit(&bars[L::XEMPTY + half]);
-                }
-                if (ok) {
-                    mma_commit(&bars[L::EMPTY + s]);
-                    mma_commit(&bars[L::UFULL + acc]);
-                }
-            }
-            // every MMA issued here is complete before TMEM is released
-            mma_commit(&bars[L::DRAIN]);
-            mbar_wait(&bars[L::DRAIN], 0, kDrainNs);
-        }
-    } else if (warp < 10) {
-        // the weighted values, in two halves of 64 tokens: row r, 16 columns
-        const int ct = threadIdx.x - 64, r = ct >> 2, c0 = (ct & 3) * 16;
-#pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-            const int s = i % kStages, w = i % kWRing;
-            bool ok = la_wait(&bars[L::FULL + s], (i / kStages) & 1, end);
-            ok = ok && la_wait(&bars[L::WFULL + w], (i / kWRing) & 1, end);
-            if (!warp_ok(ok)) break;
-            uint8_t *st = sm + s * L::STAGE;
-            const Chunk c = chunk_at<kC>(p.v, p.a.T, chunk_of(i));
-            if (c.len < kC) {
-                // rows past the chunk's tokens are another sequence's: zeros, so
-                // that nothing of theirs (an infinity, say) meets a zero weight
-#pragma unroll 1
-                for (int e = ct; e < (kC - c.len) * (DK / 8); e += kConv) {
-                    const int row = c.len + e / (DK / 8), col = (e % (DK / 8)) * 8;
-                    *reinterpret_cast<uint4 *>(st + (col >> 6) * 16384 + sw128_offset(row, col & 63)) = make_uint4(0, 0, 0, 0);
-                }
-            }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int t = half * 64 + r;
-                const uint32_t *wr = wring + w * 384 + t;
-                const Weight wt = {wr[0], wr[128], wr[256]};
-                uint4 v[2];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    v[u] = *reinterpret_cast<const uint4 *>(st + L::KB + sw128_offset(t, c0 + 8 * u));
-                    if (t >= c.len) v[u] = make_uint4(0, 0, 0, 0);
-                }
-                if (i >= 1 && !la_wait(&bars[L::XEMPTY + half], (i - 1) & 1, end)) ok = false;
-                if (!warp_ok(ok)) break;
-                uint8_t *xb = sm + L::X + half * 3 * 8192;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const uint32_t off = sw128_offset(r, c0 + 8 * u);
-                    uint4 x, y, z;
-                    weigh3(v[u].x, wt, x.x, y.x, z.x), weigh3(v[u].y, wt, x.y, y.y, z.y);
-                    weigh3(v[u].z, wt, x.z, y.z, z.z), weigh3(v[u].w, wt, x.w, y.w, z.w);
-                    *reinterpret_cast<uint4 *>(xb + off) = x;
-                    *reinterpret_cast<uint4 *>(xb + 8192 + off) = y;
-                    *reinterpret_cast<uint4 *>(xb + 16384 + off) = z;
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(&bars[L::XREADY + half]);
-            }
-            if (!warp_ok(ok)) break;
-            mbar_arrive(&bars[L::WEMPTY + w]);
-        }
-    } else if (warp < 14) {
-        // the state: one row of 64 columns a thread
-        const int row = 32 * (warp & 3) + lane;
-        const bool mine = row < DK;
-        float S[64];
-        const float *from = REV ? p.a.dsf : p.a.s0;
-        const size_t page = (((size_t)seq * p.a.H + h) * DK + row) * DV + 64 * slice;
-#pragma unroll
-        for (int e = 0; e < 64; e += 4) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (mine && from) x = *reinterpret_cast<const float4 *>(from + page + e);
-            S[e] = x.x, S[e + 1] = x.y, S[e + 2] = x.z, S[e + 3] = x.w;
-        }
-        bool ok = true;
-#pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-            const int acc = i & 1, w = i % kWRing;
-            const size_t ci = (size_t)chunk_of(i) * p.a.H + h;
-            const size_t at = (ci * DK + row) * DV + 64 * slice;
-            uint16_t *hi = (REV ? p.Rhi : p.Shi) + at, *lo = (REV ? p.Rlo : p.Slo) + at;
-            float dot = 0.f;
-#pragma unroll
-            for (int e = 0; e < 64; e += 8) {
-                float x[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = S[e + j];
-                if (REV && mine) {
-                    float a[8], b[8];
-                    unpack8(*reinterpret_cast<const uint4 *>(p.Shi + at + e), a);
-                    unpack8(*reinterpret_cast<const uint4 *>(p.Slo + at + e), b);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) dot = fmaf(x[j], a[j] + b[j], dot);
-                }
-                const uint4 top = take8(x);
-                if (mine) {
-                    *reinterpret_cast<uint4 *>(hi + e) = top;
-                    if (LO) *reinterpret_cast<uint4 *>(lo + e) = pack8(x);
-                }
-            }
-            if (REV) {
-#pragma unroll
-                for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(~0u, dot, m);
-                if (lane == 0) p.dot[(ci * (DV / 64) + slice) * 4 + (warp & 3)] = dot;
-            }
-            ok = la_wait(&bars[L::WFULL + w], (i / kWRing) & 1, end);
-            const float d = ok ? dring[w] : 0.f;
-            ok = ok && la_wait(&bars[L::UFULL + acc], (i >> 1) & 1, end);
-            if (!warp_ok(ok)) break;
-            tc_fence_after_sync();
-#pragma unroll
-            for (int e = 0; e < 64; e += 16) {
-                uint32_t u[16];
-                tmem_ld16(tmem + lane_base(warp) + 64u * acc + e, u);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) S[e + j] = fmaf(d, S[e + j], __uint_as_float(u[j]));
-            }
-            tc_fence_before_sync();
-            mbar_arrive(&bars[L::UEMPTY + acc]);
-            mbar_arrive(&bars[L::WEMPTY + w]);
-        }
-        float *to = REV ? p.a.ds0 : p.a.sf;
-        if (to && mine && warp_ok(ok))
-#pragma unroll
-            for (int e = 0; e < 64; e += 4)
-                *reinterpret_cast<float4 *>(to + page + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
-    } else {
-        // the weights of every other chunk: e^{G - c_t}, or (REV) scale e^{c_t};
-        // the next chunk's gates are on their way meanwhile
-        const bool per_head = p.a.flags & GDN_G_PER_HEAD;
-        float next[4];
-        auto fetch = [&](int i) {
-            if (i >= n) return;
-            const Chunk c = chunk_at<kC>(p.v, p.a.T, chunk_of(i));
-            load_gates<kC>(gate_ptr(p.a, c, h), p.a.sg.t, c.len, per_head, next);
-        };
-        fetch(warp - 14);
-#pragma unroll 1
-        for (int i = warp - 14; i < n; i += 2) {
-            const int w = i % kWRing;
-            const Gates<kC> g = scan_gates<kC>(next);
-            fetch(i + 2);
-            if (i >= kWRing && !la_wait(&bars[L::WEMPTY + w], ((i / kWRing) - 1) & 1, end)) break;
-            float4 x;
-            if (REV) x = make_float4(expf(g.cum[0].hi), expf(g.cum[1].hi), expf(g.cum[2].hi), expf(g.cum[3].hi));
-            else x = make_float4(expf(g.to_end(0)), expf(g.to_end(1)),
-                                 expf(g.to_end(2)), expf(g.to_end(3)));
-            if (REV) x.x *= p.a.scale, x.y *= p.a.scale, x.z *= p.a.scale, x.w *= p.a.scale;
-            uint4 *ws = reinterpret_cast<uint4 *>(wring + w * 384);
-            const Weight wa = split_weight(x.x), wb = split_weight(x.y), wc = split_weight(x.z), wd = split_weight(x.w);
-            ws[lane] = make_uint4(wa.h, wb.h, wc.h, wd.h);
-            ws[lane + 32] = make_uint4(wa.m, wb.m, wc.m, wd.m);
-            ws[lane + 64] = make_uint4(wa.l, wb.l, wc.l, wd.l);
-            if (lane == 0) dring[w] = expf(g.all.hi);
-            mbar_arrive(&bars[L::WFULL + w]);
-        }
-    }
-    __syncwarp();
-    tc_fence_before_sync();
-    __syncthreads();
-    if (warp == 1) {
-        tc_fence_after_sync();
-        tmem_dealloc(tmem, 128);
-    }
-}
-
-// ================================================================ prompt kernel
-// Warps: 0 TMA, 1 and 2 products, 3 decays, 4..7 state, 8..11 P, 12..15
-// weighting, 16..19 outputs.  One warp of each on each of the SM's four
-// schedulers, so every instruction is fetched for one warp alone, and
-// straight-line code is bound by its fetching (a third of an instruction a
-// cycle here): the roles' bodies are short loops.
-constexpr int kFwdThreads = 640;
-constexpr int kQKStages = 2, kVStages = 3, kXMax = 3, kGRing = 4;
 constexpr float kLog2e = 1.44269504088896341f;
-
-template <int DK>
-struct FwdSmem {
-    static constexpr uint32_t TB = DK * 256;                 // a chunk's Q or K
-    static constexpr uint32_t QK = 0;                        // [stage] K | Q
-    static constexpr uint32_t V = kQKStages * 2 * TB;        // [stage] 64 columns of V
-    static constexpr uint32_t X = V + kVStages * 16384;      // [slot][term][32 tokens][128 B] weighted values
-    static constexpr uint32_t S = X + 6 * 4096;              // [DK][128 B] the state as an operand
-    static constexpr uint32_t W = S + DK * 128;              // [ring][3][128] weights
-    static constexpr uint32_t G = W + kGRing * 1536;         // [ring] log2 decays | block factors, 128 each
-    static constexpr uint32_t D = G + kGRing * 1024;         // [ring] chunk decays
-    static constexpr uint32_t BAR = D + 64;
-    enum { KFULL = 0, KEMPTY = 2, QFULL = 4, QEMPTY = 6, VFULL = 8, VREADY = 11, VEMPTY = 14, XREADY = 17,
-           XEMPTY = XREADY + kXMax, UFULL = XEMPTY + kXMax,
-           UEMPTY, SREADY, SEMPTY, TFULL, PREADY = TFULL + 2, OFULL = PREADY + 2, OEMPTY, GFULL, GEMPTY = GFULL + kGRing,
-           DRAIN = GEMPTY + kGRing, NUM = DRAIN + 2 };
-    static constexpr uint32_t TSLOT = BAR + 8 * NUM;
-    static constexpr uint32_t BYTES = TSLOT + 16;
-};
-static_assert(FwdSmem<128>::BYTES <= 232448, "prompt kernel fits the shared memory of one CTA");
-// TMEM columns: Q K^T twice (P, two bf16 a column, takes its first half), Q S
-// twice, P V, the chunk's share of the state
-constexpr uint32_t TM_T = 0, TM_OS = 256, TM_OP = 384, TM_U = 448;
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -528,12 +210,314 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
 }
 
 // KS steps of 16; a(ks) and b(ks) are the operands' low descriptor words.
+// mma_more adds to what is there.
 template <int KS, class A, class B>
 __device__ __forceinline__ void mma_steps(uint32_t d, uint32_t idesc, const A &a, const B &b) {
     mma_ss<0>(d, desc_of(a(0)), desc_of(b(0)), idesc);
 #pragma unroll
     for (int ks = 1; ks < KS; ++ks) mma_ss<1>(d, desc_of(a(ks)), desc_of(b(ks)), idesc);
 }
+template <int KS, class A, class B>
+__device__ __forceinline__ void mma_more(uint32_t d, uint32_t idesc, const A &a, const B &b) {
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) mma_ss<1>(d, desc_of(a(ks)), desc_of(b(ks)), idesc);
+}
+
+// ================================================================ state kernel
+// Warps: 0 TMA, 1 products, 2 decays, 4..7 state, 8..15 weighting.
+constexpr int kStateThreads = 512;
+constexpr int kStages = 3, kWRing = 4;
+
+template <int DK>
+struct StateSmem {
+    static constexpr uint32_t KB = DK * 256, VB = 16384;  // a chunk's K (or Q) and 64 columns of V (or dO)
+    static constexpr uint32_t STAGE = KB + VB;
+    // with DK = 64 the product's rows 64..127 read the bytes after K, in the
+    // stage's own V tile: rows that nobody looks at
+    static constexpr uint32_t X = kStages * STAGE;        // [half][3][64 tokens][128 B] weighted values
+    static constexpr uint32_t W = X + 2 * 3 * 8192;       // [ring][3][128] weights, then [ring] chunk decays
+    static constexpr uint32_t BAR = W + kWRing * 1536 + 64;
+    enum { FULL = 0, EMPTY = 3, XREADY = 6, XEMPTY = 8, UFULL = 10, UEMPTY = 12, WFULL = 14, WEMPTY = 18, DRAIN = 22, NUM = 23 };
+    static constexpr uint32_t TSLOT = BAR + 8 * NUM;
+    static constexpr uint32_t BYTES = TSLOT + 16;
+};
+static_assert(StateSmem<128>::BYTES <= 232448, "state kernel fits the shared memory of one CTA");
+
+// Grid (2 DV / 64, H, n_seq): the states that enter a sequence's chunks, and
+// (the second half of x) backwards over them the gradients of the states that
+// leave them, with Q and dO in the places of K and V.  Both go out as bf16
+// pairs hi + lo (2^-17), which the gradients' products take as operands.
+template <int DK, int DV>
+__global__ void __launch_bounds__(kStateThreads, 1)
+    state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
+                 const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mO, TcArgs p) {
+    using L = StateSmem<DK>;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::TSLOT);
+    uint32_t *wring = reinterpret_cast<uint32_t *>(sm + L::W);
+    float *dring = reinterpret_cast<float *>(wring + kWRing * 384);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool rev = blockIdx.x >= DV / 64;
+    const int slice = blockIdx.x % (DV / 64), h = blockIdx.y, seq = blockIdx.z;
+    const Span sp = span_of(p.a, seq);
+    const int2 sq = seq_at(p.v, seq);
+    const int n = sq.y, row0 = p.a.cu ? 0 : seq;
+    const uint64_t end = deadline_after(p.timeout_ns, n);
+    auto number = [&](int i) { return rev ? n - 1 - i : i; };
+    auto chunk = [&](int i) { return Chunk{row0, sp.start + number(i) * kC, min(kC, sp.len - number(i) * kC), seq}; };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&bars[L::FULL + s], 1);
+            mbar_init(&bars[L::EMPTY + s], 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&bars[L::XREADY + x], 256);
+            mbar_init(&bars[L::XEMPTY + x], 1);
+            mbar_init(&bars[L::UFULL + x], 1);
+            mbar_init(&bars[L::UEMPTY + x], 128);
+        }
+        for (int w = 0; w < kWRing; ++w) {
+            mbar_init(&bars[L::WFULL + w], 32);
+            mbar_init(&bars[L::WEMPTY + w], 256 + 128);
+        }
+        mbar_init(&bars[L::DRAIN], 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tslot, 128);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tslot;
+    const uint32_t sbase = smem_u32(sm);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const int hk = h / (p.a.H / p.a.Hk);
+            const CUtensorMap *m1 = rev ? &mQ : &mK, *m2 = rev ? &mO : &mV;
+            int i = 0;
+#pragma unroll 1
+            for (; i < n; ++i) {
+                const int s = i % kStages;
+                if (i >= kStages && !la_wait(&bars[L::EMPTY + s], ((i / kStages) - 1) & 1, end)) break;
+                const Chunk c = chunk(i);
+                uint8_t *st = sm + s * L::STAGE;
+                mbar_arrive_expect_tx(&bars[L::FULL + s], L::STAGE);
+#pragma unroll
+                for (int x = 0; x < DK / 64; ++x) tma_load_4d(st + x * 16384, m1, &bars[L::FULL + s], 64 * x, c.t0, hk, c.row);
+                tma_load_4d(st + L::KB, m2, &bars[L::FULL + s], 64 * slice, c.t0, h, c.row);
+            }
+            // no copy is in flight when the CTA ends
+#pragma unroll 1
+            for (int j = i > kStages ? i - kStages : 0; j < i; ++j)
+                mbar_wait(&bars[L::FULL + j % kStages], (j / kStages) & 1, kDrainNs);
+        }
+    } else if (warp == 1) {
+        constexpr uint32_t id = idesc_bf16(128, 64, true, true);
+        const bool leader = elect_one();
+        bool ok = true;
+#pragma unroll 1
+        for (int i = 0; i < n && ok; ++i) {
+            const int s = i % kStages, acc = i & 1;
+            ok = la_wait(&bars[L::FULL + s], (i / kStages) & 1, end);
+            if (i >= 2) ok = ok && la_wait(&bars[L::UEMPTY + acc], ((i >> 1) - 1) & 1, end);
+            tc_fence_after_sync();
+            const uint32_t d = tmem + 64u * acc;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                ok = ok && la_wait(&bars[L::XREADY + half], i & 1, end);
+                if (!ok) break;
+                const uint32_t k = desc_lo(sbase + s * L::STAGE, 16384) + half * 512, x = desc_lo(sbase + L::X + half * 3 * 8192, 8192);
+                if (leader) {
+                    if (half == 0) mma_ss<0>(d, desc_of(k), desc_of(x), id);
+                    else mma_ss<1>(d, desc_of(k), desc_of(x), id);
+#pragma unroll
+                    for (int e = 1; e < 12; ++e) mma_ss<1>(d, desc_of(k + (e & 3) * 128), desc_of(x + (e >> 2) * 512 + (e & 3) * 128), id);
+                    if (half == 1) mma_commit(&bars[L::UFULL + acc]);
+                    mma_commit(&bars[L::XEMPTY + half]);
+                    if (half == 1) mma_commit(&bars[L::EMPTY + s]);
+                }
+            }
+        }
+        // every MMA issued here is complete before TMEM is released
+        if (leader) mma_commit(&bars[L::DRAIN]);
+        mbar_wait(&bars[L::DRAIN], 0, kDrainNs);
+    } else if (warp == 2) {
+        // the weights: e^{G - c_t}, or backwards scale e^{c_t}; the next chunk's
+        // gates are on their way meanwhile
+        const bool per_head = p.a.flags & GDN_G_PER_HEAD;
+        float next[4];
+        auto fetch = [&](int i) {
+            if (i >= n) return;
+            load_gates<kC>(gate_ptr(p.a, chunk(i), h), p.a.sg.t, chunk(i).len, per_head, next);
+        };
+        fetch(0);
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            const int w = i % kWRing;
+            const Sums g = scan_sums(next);
+            fetch(i + 1);
+            if (i >= kWRing && !la_wait(&bars[L::WEMPTY + w], ((i / kWRing) - 1) & 1, end)) break;
+            Weight wt[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                wt[j] = split_weight(rev ? p.a.scale * exp2_fast(g.cum[j] * kLog2e) : exp2_fast(g.to_end[j] * kLog2e));
+            uint4 *ws = reinterpret_cast<uint4 *>(wring + w * 384);
+            ws[lane] = make_uint4(wt[0].h, wt[1].h, wt[2].h, wt[3].h);
+            ws[lane + 32] = make_uint4(wt[0].m, wt[1].m, wt[2].m, wt[3].m);
+            ws[lane + 64] = make_uint4(wt[0].l, wt[1].l, wt[2].l, wt[3].l);
+            if (lane == 0) dring[w] = expf(g.all);
+            mbar_arrive(&bars[L::WFULL + w]);
+        }
+    } else if (warp >= 8) {
+        // the weighted values, in two halves of 64 tokens: row r, 16 columns
+        const int ct = threadIdx.x - 256, r = ct >> 2, c0 = (ct & 3) * 16;
+        const uint32_t off[2] = {sw128_offset(r, c0), sw128_offset(r, c0 + 8)};
+        bool ok = true;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            const int s = i % kStages, w = i % kWRing, len = chunk(i).len;
+            ok = la_wait(&bars[L::FULL + s], (i / kStages) & 1, end) && la_wait(&bars[L::WFULL + w], (i / kWRing) & 1, end);
+            if (!ok) break;
+            uint8_t *st = sm + s * L::STAGE;
+            if (len < kC) {
+                // rows past the chunk's tokens are another sequence's: zeros, so
+                // that nothing of theirs (an infinity, say) meets a zero weight
+#pragma unroll 1
+                for (int e = ct; e < (kC - len) * (DK / 8); e += 256) {
+                    const int row = len + e / (DK / 8), col = (e % (DK / 8)) * 8;
+                    *reinterpret_cast<uint4 *>(st + (col >> 6) * 16384 + sw128_offset(row, col & 63)) = make_uint4(0, 0, 0, 0);
+                }
+            }
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                const int t = half * 64 + r;
+                const uint32_t *wr = wring + w * 384 + t;
+                const Weight wt = {wr[0], wr[128], wr[256]};
+                uint4 v[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    v[u] = *reinterpret_cast<const uint4 *>(st + L::KB + half * 8192 + off[u]);
+                    if (t >= len) v[u] = make_uint4(0, 0, 0, 0);
+                }
+                if (i >= 1 && !la_wait(&bars[L::XEMPTY + half], (i - 1) & 1, end)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *xb = sm + L::X + half * 3 * 8192;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint4 x, y, z;
+                    weigh3(v[u].x, wt, x.x, y.x, z.x), weigh3(v[u].y, wt, x.y, y.y, z.y);
+                    weigh3(v[u].z, wt, x.z, y.z, z.z), weigh3(v[u].w, wt, x.w, y.w, z.w);
+                    *reinterpret_cast<uint4 *>(xb + off[u]) = x;
+                    *reinterpret_cast<uint4 *>(xb + 8192 + off[u]) = y;
+                    *reinterpret_cast<uint4 *>(xb + 16384 + off[u]) = z;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&bars[L::XREADY + half]);
+            }
+            if (!ok) break;
+            mbar_arrive(&bars[L::WEMPTY + w]);
+        }
+    } else if (warp >= 4) {
+        // the state: one row of 64 columns a thread
+        const int row = 32 * (warp & 3) + lane;
+        const bool mine = row < DK;
+        float S[64];
+        const float *from = rev ? p.a.dsf : p.a.s0;
+        const size_t page = (((size_t)seq * p.a.H + h) * DK + row) * DV + 64 * slice;
+#pragma unroll
+        for (int e = 0; e < 64; e += 4) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (mine && from) x = *reinterpret_cast<const float4 *>(from + page + e);
+            S[e] = x.x, S[e + 1] = x.y, S[e + 2] = x.z, S[e + 3] = x.w;
+        }
+        bool ok = true;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            const int acc = i & 1, w = i % kWRing;
+            const size_t at = (((size_t)(sq.x + number(i)) * p.a.H + h) * DK + row) * DV + 64 * slice;
+            uint16_t *hi = (rev ? p.Rhi : p.Shi) + at, *lo = (rev ? p.Rlo : p.Slo) + at;
+            if (mine)
+#pragma unroll
+                for (int e = 0; e < 64; e += 16) {
+                    uint32_t a[8], b[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float x = S[e + 2 * j], y = S[e + 2 * j + 1];
+                        a[j] = pack_bf16(x, y);
+                        b[j] = pack_bf16(x - __uint_as_float(a[j] << 16), y - __uint_as_float(a[j] & 0xffff0000u));
+                    }
+                    st_global_32(hi + e, a);
+                    st_global_32(lo + e, b);
+                }
+            ok = warp_ok(la_wait(&bars[L::WFULL + w], (i / kWRing) & 1, end) && la_wait(&bars[L::UFULL + acc], (i >> 1) & 1, end));
+            if (!ok) break;
+            const float d = dring[w];
+            tc_fence_after_sync();
+#pragma unroll
+            for (int e = 0; e < 64; e += 16) {
+                uint32_t u[16];
+                tmem_ld16(tmem + lane_base(warp) + 64u * acc + e, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) S[e + j] = fmaf(d, S[e + j], __uint_as_float(u[j]));
+            }
+            tc_fence_before_sync();
+            mbar_arrive(&bars[L::UEMPTY + acc]);
+            mbar_arrive(&bars[L::WEMPTY + w]);
+        }
+        float *to = rev ? p.a.ds0 : p.a.sf;
+        if (to && mine && ok)
+#pragma unroll
+            for (int e = 0; e < 64; e += 4)
+                *reinterpret_cast<float4 *>(to + page + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+    }
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 128);
+    }
+}
+
+// ================================================================ prompt kernel
+// Warps: 0 TMA, 1 and 2 products, 3 decays, 4..7 state, 8..11 P, 12..15
+// weighting, 16..19 outputs.  One warp of each on each of the SM's four
+// schedulers, so every instruction is fetched for one warp alone, and
+// straight-line code is bound by its fetching (a third of an instruction a
+// cycle here): the roles' bodies are short loops.
+constexpr int kFwdThreads = 640;
+constexpr int kQKStages = 2, kVStages = 3, kXMax = 3, kGRing = 4;
+
+template <int DK>
+struct FwdSmem {
+    static constexpr uint32_t TB = DK * 256;                 // a chunk's Q or K
+    static constexpr uint32_t QK = 0;                        // [stage] K | Q
+    static constexpr uint32_t V = kQKStages * 2 * TB;        // [stage] 64 columns of V
+    static constexpr uint32_t X = V + kVStages * 16384;      // [slot][term][32 tokens][128 B] weighted values
+    static constexpr uint32_t S = X + 6 * 4096;              // [DK][128 B] the state as an operand
+    static constexpr uint32_t W = S + DK * 128;              // [ring][3][128] weights
+    static constexpr uint32_t G = W + kGRing * 1536;         // [ring] log2 decays | block factors, 128 each
+    static constexpr uint32_t D = G + kGRing * 1024;         // [ring] chunk decays
+    static constexpr uint32_t BAR = D + 64;
+    enum { KFULL = 0, KEMPTY = 2, QFULL = 4, QEMPTY = 6, VFULL = 8, VREADY = 11, VEMPTY = 14, XREADY = 17,
+           XEMPTY = XREADY + kXMax, UFULL = XEMPTY + kXMax,
+           UEMPTY, SREADY, SEMPTY, TFULL, PREADY = TFULL + 2, OFULL = PREADY + 2, OEMPTY, GFULL, GEMPTY = GFULL + kGRing,
+           DRAIN = GEMPTY + kGRing, NUM = DRAIN + 2 };
+    static constexpr uint32_t TSLOT = BAR + 8 * NUM;
+    static constexpr uint32_t BYTES = TSLOT + 16;
+};
+static_assert(FwdSmem<128>::BYTES <= 232448, "prompt kernel fits the shared memory of one CTA");
+// TMEM columns: Q K^T twice (P, two bf16 a column, takes its first half), Q S
+// twice, P V, the chunk's share of the state
+constexpr uint32_t TM_T = 0, TM_OS = 256, TM_OP = 384, TM_U = 448;
 
 // Grid (DV / 64, H, n_seq, and one more for the tokens of no sequence).  A CTA walks the chunks of
 // one sequence for 64 value columns of one head.
@@ -982,6 +966,443 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
 }
 
+// ================================================================ grad kernel
+// Warps: 0..7 arithmetic (rows by lane quarter, columns in two halves), 8 loads
+// and products.
+constexpr int kGradThreads = 288;
+
+struct GradSmem {
+    static constexpr uint32_t Q = 0, K = 32768, V = 65536, O = 98304;  // V: later P
+    static constexpr uint32_t X = 131072, Y = 163840, Z = 196608;      // S hi, later R lo; S lo, later N; R hi
+    static constexpr uint32_t G = 229376;                              // decays: cum hi, lo, to_end
+    static constexpr uint32_t RED = G + 1536;                          // sums of a chunk's dg, see kernel
+    static constexpr uint32_t BAR = RED + 512;
+    enum { QK = 0, OV, SS, RH, RL, CT, CN, CQ, CK, XREAD, READY, DONE, DRAIN, NUM };
+    static constexpr uint32_t TSLOT = BAR + 8 * NUM;
+    static constexpr uint32_t BYTES = TSLOT + 16;
+};
+static_assert(GradSmem::BYTES <= 232448, "grad kernel fits the shared memory of one CTA");
+// TMEM columns: Q K^T, later K R; dO V^T, later P^T dO; dQ; dK
+constexpr uint32_t TM_A = 0, TM_B = 128, TM_Q = 256, TM_K = 384;
+
+// Sum over the warp's lanes (rows) of x[j], to lane j.
+__device__ __forceinline__ float column_sums(float (&x)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int m = 16; m; m >>= 1) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int j = 0; j < m; ++j) {
+            const float keep = up ? x[j + m] : x[j], give = up ? x[j] : x[j + m];
+            x[j] = keep + __shfl_xor_sync(~0u, give, m);
+        }
+    }
+    return x[0];
+}
+
+__device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float x) {
+    float u[8], v[8];
+    unpack8(a, u);
+    unpack8(b, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x = fmaf(u[e], v[e], x);
+    return x;
+}
+
+// A chunk's gradients (the formulas are linattn.cu's).  Grid (chunks, H).
+// Products: T = Q K^T and dO V^T; dO S^T and V R^T with S and R as hi + lo;
+// then, with P and N = dO V^T under the decay mask rounded to bf16, N K, N^T Q,
+// P^T dO and K R.  What dg is made of never passes through a rounded operand:
+// the pairs' terms A come from the fp32 products, the terms through S and R
+// from the split ones.  Bound by the bytes: 256 KB in, 96 KB out a chunk.
+template <int DK, int DV>
+__global__ void __launch_bounds__(kGradThreads, 1)
+    grad_kernel_tc(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
+                   const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mO,
+                   const __grid_constant__ CUtensorMap mSh, const __grid_constant__ CUtensorMap mSl,
+                   const __grid_constant__ CUtensorMap mRh, const __grid_constant__ CUtensorMap mRl, TcArgs p) {
+    using L = GradSmem;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::TSLOT);
+    float *hi = reinterpret_cast<float *>(sm + L::G), *lo = hi + 128, *te = lo + 128;
+    float *red = reinterpret_cast<float *>(sm + L::RED);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ci = blockIdx.x, h = blockIdx.y, hk = h / (p.a.H / p.a.Hk);
+    const Chunk c = chunk_at<kC>(p.v, p.a.T, ci);
+    if (c.len <= 0) return;
+    const bool shared = p.a.H != p.a.Hk;
+    using T = __nv_bfloat16;
+    T *dq = at(static_cast<T *>(p.a.dq), p.a.sq, c.row, hk, c.t0), *dk = at(static_cast<T *>(p.a.dk), p.a.sk, c.row, hk, c.t0);
+    T *dv = at(static_cast<T *>(p.a.dv), p.a.sv, c.row, h, c.t0);
+    float *dg = at(p.dgt, p.sdg, c.row, h, c.t0);
+    const size_t wide_row = (((size_t)c.row * p.a.H + h) * p.a.T + c.t0) * DK;
+    if (c.seq < 0) {  // tokens of no sequence
+        auto zeros = [&](T *x, long long step, int d) {
+            for (int e = threadIdx.x; e < c.len * (d / 8); e += kGradThreads)
+                *reinterpret_cast<uint4 *>(x + (e / (d / 8)) * step + (e % (d / 8)) * 8) = make_uint4(0, 0, 0, 0);
+        };
+        if (shared) {
+            for (int e = threadIdx.x; e < c.len * DK; e += kGradThreads) p.dqh[wide_row + e] = p.dkh[wide_row + e] = 0.f;
+        } else {
+            zeros(dq, p.a.sq.t, DK);
+            zeros(dk, p.a.sk.t, DK);
+        }
+        zeros(dv, p.a.sv.t, DV);
+        for (int e = threadIdx.x; e < c.len; e += kGradThreads) dg[e * p.sdg.t] = 0.f;
+        return;
+    }
+    const uint64_t end = deadline_after(p.timeout_ns, 1);
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < L::NUM; ++b) mbar_init(&bars[b], b == L::XREAD || b == L::READY ? 256 : 1);
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(tslot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
+    const uint32_t sbase = smem_u32(sm);
+    bool ok = true;
+
+    if (warp == 8) {
+        const bool leader = elect_one();
+        auto tile = [&](const CUtensorMap *m, uint32_t at_, int bar, int d, int head) {
+#pragma unroll
+            for (int x = 0; x < d / 64; ++x) tma_load_4d(sm + at_ + x * 16384, m, &bars[bar], 64 * x, c.t0, head, c.row);
+        };
+        auto state = [&](const CUtensorMap *m, uint32_t at_, int bar) {
+#pragma unroll
+            for (int x = 0; x < DV / 64; ++x) tma_load_3d(sm + at_ + x * (DK * 128), m, &bars[bar], 64 * x, 0, ci * p.a.H + h);
+        };
+        if (leader) {
+            mbar_arrive_expect_tx(&bars[L::QK], 2 * DK * 256);
+            tile(&mQ, L::Q, L::QK, DK, hk);
+            tile(&mK, L::K, L::QK, DK, hk);
+            mbar_arrive_expect_tx(&bars[L::OV], 2 * DV * 256);
+            tile(&mO, L::O, L::OV, DV, h);
+            tile(&mV, L::V, L::OV, DV, h);
+            mbar_arrive_expect_tx(&bars[L::SS], 2 * DK * DV * 2);
+            state(&mSh, L::X, L::SS);
+            state(&mSl, L::Y, L::SS);
+            mbar_arrive_expect_tx(&bars[L::RH], DK * DV * 2);
+            state(&mRh, L::Z, L::RH);
+        }
+        // operands' low descriptor words: K-major tiles step by 32 bytes in a
+        // block of 64 columns, MN-major ones by 16 rows
+        auto km = [&](uint32_t at_, int rows) { return [=](int ks) { return desc_lo(sbase + at_, 16) + (ks >> 2) * (rows * 8) + (ks & 3) * 2; }; };
+        auto mn = [&](uint32_t at_, uint32_t stride) { return [=](int ks) { return desc_lo(sbase + at_, stride) + ks * 128; }; };
+        bool rl = false;
+        do {
+            ok = la_wait(&bars[L::QK], 0, end);
+            if (!ok) break;
+            if (leader) {
+                mma_steps<DK / 16>(TM_A, idesc_bf16(128, 128, false, false), km(L::Q, 128), km(L::K, 128));
+                mma_commit(&bars[L::CT]);
+            }
+            ok = la_wait(&bars[L::OV], 0, end);
+            if (!ok) break;
+            if (leader) {
+                mma_steps<DV / 16>(TM_B, idesc_bf16(128, 128, false, false), km(L::O, 128), km(L::V, 128));
+                mma_commit(&bars[L::CN]);
+            }
+            constexpr uint32_t idk = idesc_bf16(128, DK, false, false);
+            ok = la_wait(&bars[L::SS], 0, end);
+            if (!ok) break;
+            if (leader) {
+                mma_steps<DV / 16>(TM_Q, idk, km(L::O, 128), km(L::X, DK));
+                mma_more<DV / 16>(TM_Q, idk, km(L::O, 128), km(L::Y, DK));
+                mma_commit(&bars[L::CQ]);
+            }
+            ok = la_wait(&bars[L::RH], 0, end);
+            if (!ok) break;
+            if (leader) mma_steps<DV / 16>(TM_K, idk, km(L::V, 128), km(L::Z, DK));
+            // R lo in S hi's place, which has been multiplied and read
+            ok = la_wait(&bars[L::CQ], 0, end) && la_wait(&bars[L::XREAD], 0, end);
+            if (!ok) break;
+            if (leader) {
+                mbar_arrive_expect_tx(&bars[L::RL], DK * DV * 2);
+                state(&mRl, L::X, L::RL);
+            }
+            rl = true;
+            ok = la_wait(&bars[L::RL], 0, end);
+            if (!ok) break;
+            if (leader) {
+                mma_more<DV / 16>(TM_K, idk, km(L::V, 128), km(L::X, DK));
+                mma_commit(&bars[L::CK]);
+            }
+            ok = la_wait(&bars[L::READY], 0, end);
+            if (!ok) break;
+            tc_fence_after_sync();
+            if (leader) {
+                mma_more<kC / 16>(TM_Q, idesc_bf16(128, DK, false, true), km(L::Y, 128), mn(L::K, 16384));
+                mma_more<kC / 16>(TM_K, idesc_bf16(128, DK, true, true), mn(L::Y, 16384), mn(L::Q, 16384));
+                mma_steps<kC / 16>(TM_B, idesc_bf16(128, DV, true, true), mn(L::V, 16384), mn(L::O, 16384));
+                mma_steps<DK / 16>(TM_A, idesc_bf16(128, DV, false, true), km(L::K, 128), mn(L::Z, DK * 128));
+                mma_commit(&bars[L::DONE]);
+            }
+            ok = la_wait(&bars[L::DONE], 0, end);
+        } while (false);
+        if (!warp_ok(ok)) {  // no copy and no product is in flight when the CTA ends
+            if (leader) mma_commit(&bars[L::DRAIN]);
+            mbar_wait(&bars[L::DRAIN], 0, kDrainNs);
+            mbar_wait(&bars[L::QK], 0, kDrainNs);
+            mbar_wait(&bars[L::OV], 0, kDrainNs);
+            mbar_wait(&bars[L::SS], 0, kDrainNs);
+            mbar_wait(&bars[L::RH], 0, kDrainNs);
+            if (rl) mbar_wait(&bars[L::RL], 0, kDrainNs);
+        }
+    } else {
+        const int t = 32 * (warp & 3) + lane, half = warp >> 2, s0 = 64 * half, tid = threadIdx.x;
+        const uint32_t lanes = tmem + lane_base(warp);
+        // [quantity][..] partial sums by token: A's rows (2 halves), its columns (4
+        // quarters of rows), x (2), y (2), in the places of tiles that are done;
+        // until then in registers
+        float rowa = 0.f, cola[2] = {0.f, 0.f}, xt = 0.f, yt = 0.f, dot = 0.f;
+        uint32_t P[32], N[32];
+        // the eight warps' barrier.  A warp whose wait gave up comes to it all the
+        // same, and none of them goes on.
+        auto meet = [&] {
+            uint32_t all;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                : "=r"(all)
+                : "r"(ok ? 1u : 0u)
+                : "memory");
+            ok = all != 0;
+        };
+        auto wait = [&](int bar) { ok = warp_ok(ok && la_wait(&bars[bar], 0, end)); };
+        {
+            if (warp == 0) gates<kC>(gate_ptr(p.a, c, h), p.a.sg.t, c.len, p.a.flags & GDN_G_PER_HEAD, hi, lo, te);
+            meet();
+            wait(L::CT);
+            wait(L::CN);
+            tc_fence_after_sync();
+            const float ht = hi[t], lt = lo[t];
+#pragma unroll
+            for (int b = 0; b < 2 && ok; ++b) {
+                const int sb = s0 + 32 * b;  // the block's first column
+                if (sb > t - lane + 31) {    // past the diagonal for every row of the warp
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) P[16 * b + j] = N[16 * b + j] = 0u;
+                    continue;
+                }
+                uint32_t u[32], w[32];
+                float a[32];
+                tmem_ld32(lanes + TM_A + sb, u);
+                tmem_ld32(lanes + TM_B + sb, w);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const int s = sb + j;
+                    const bool in = s <= t && t < c.len;
+                    const float f = in ? p.a.scale * exp2_fast(((ht - hi[s]) + (lt - lo[s])) * kLog2e) : 0.f;
+                    const float qk = in ? __uint_as_float(u[j]) : 0.f, nn = in ? __uint_as_float(w[j]) * f : 0.f;
+                    a[j] = s < t ? qk * nn : 0.f;
+                    rowa += a[j];
+                    u[j] = __float_as_uint(qk * f);
+                    w[j] = __float_as_uint(nn);
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    P[16 * b + j] = pack_bf16(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+                    N[16 * b + j] = pack_bf16(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+                }
+                cola[b] = column_sums(a);
+            }
+            // <R, S>: (S hi + S lo) . R hi now, S hi . R lo when that is there
+            constexpr int NV = DK * DV / 8 / 256;  // 16-byte words of a state a thread
+            wait(L::SS);
+            wait(L::RH);
+            uint4 sh[NV];
+#pragma unroll
+            for (int e = 0; e < NV; ++e) {
+                const uint32_t o = (tid + 256 * e) * 16;
+                sh[e] = *reinterpret_cast<const uint4 *>(sm + L::X + o);
+                const uint4 r = *reinterpret_cast<const uint4 *>(sm + L::Z + o);
+                dot = dot8(sh[e], r, dot8(*reinterpret_cast<const uint4 *>(sm + L::Y + o), r, dot));
+            }
+            mbar_arrive(&bars[L::XREAD]);
+            // dQ's part through S: scaled by its row, and x_t = q_t . it
+            wait(L::CQ);
+            tc_fence_after_sync();
+            const float ft = p.a.scale * exp2_fast(ht * kLog2e), fe = exp2_fast(te[t] * kLog2e);
+            auto scale_rows = [&](uint32_t col, float f, uint32_t tile_at) {
+                float x = 0.f;
+#pragma unroll 1
+                for (int e = 0; e < DK / 2; e += 16) {
+                    const int d0 = half * (DK / 2) + e;
+                    uint32_t u[16];
+                    tmem_ld16(lanes + col + d0, u);
+                    float q[16];
+#pragma unroll
+                    for (int j = 0; j < 16; j += 8) {
+                        float y[8];
+                        unpack8(*reinterpret_cast<const uint4 *>(sm + tile_at + ((d0 + j) >> 6) * 16384 + sw128_offset(t, (d0 + j) & 63)), y);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) q[j + k] = y[k];
+                    }
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float y = f * __uint_as_float(u[j]);
+                        x = fmaf(q[j], y, x);
+                        u[j] = __float_as_uint(y);
+                    }
+                    tmem_st16(lanes + col + d0, u);
+                }
+                return t < c.len ? x : 0.f;
+            };
+            if (ok) xt = scale_rows(TM_Q, ft, L::Q);
+            meet();  // S lo has been read: N takes its place
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+                *reinterpret_cast<uint4 *>(sm + L::Y + half * 16384 + sw128_offset(t, 2 * j)) = make_uint4(N[j], N[j + 1], N[j + 2], N[j + 3]);
+            wait(L::RL);
+#pragma unroll
+            for (int e = 0; e < NV; ++e) dot = dot8(sh[e], *reinterpret_cast<const uint4 *>(sm + L::X + (tid + 256 * e) * 16), dot);
+            wait(L::CK);
+            tc_fence_after_sync();
+            if (ok) yt = scale_rows(TM_K, fe, L::K);
+            // V has been multiplied: P takes its place
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+                *reinterpret_cast<uint4 *>(sm + L::V + half * 16384 + sw128_offset(t, 2 * j)) = make_uint4(P[j], P[j + 1], P[j + 2], P[j + 3]);
+            if (c.len < kC) {
+                // another sequence's rows: zeros, so that nothing of theirs (an
+                // infinity, say) meets the zeros of N and P
+                meet();  // x and y have been made
+#pragma unroll 1
+                for (int e = tid; e < (kC - c.len) * 16; e += 256) {
+                    const int row = c.len + (e >> 4), col = (e & 15) * 8;
+                    const uint32_t o = (col >> 6) * 16384 + sw128_offset(row, col & 63);
+                    if (col < DK) *reinterpret_cast<uint4 *>(sm + L::Q + o) = make_uint4(0, 0, 0, 0);
+                    if (col < DK) *reinterpret_cast<uint4 *>(sm + L::K + o) = make_uint4(0, 0, 0, 0);
+                    if (col < DV) *reinterpret_cast<uint4 *>(sm + L::O + o) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            tmem_wait_st();
+            fence_proxy_async_smem();
+            tc_fence_before_sync();
+            if (ok) mbar_arrive(&bars[L::READY]);
+            // dg meanwhile, through R lo's place
+            float *part = reinterpret_cast<float *>(sm + L::X);
+            meet();
+            part[half * 128 + t] = rowa;
+            part[256 + half * 128 + t] = xt;
+            part[512 + half * 128 + t] = yt;
+            part[768 + (warp & 3) * 128 + s0 + lane] = cola[0];
+            part[768 + (warp & 3) * 128 + s0 + 32 + lane] = cola[1];
+#pragma unroll
+            for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(~0u, dot, m);
+            if (lane == 0) red[warp] = dot;
+            meet();
+            if (warp == 0 && ok) {
+                // dg_u = sum_{t >= u} (x_t + A's row t - A's column t) + sum_{t < u} y_t + e^G <R, S>
+                float x[4], y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int u = 4 * lane + j;
+                    const float *q = part + u;
+                    x[j] = (q[256] + q[384]) + ((q[0] + q[128]) - ((q[768] + q[896]) + (q[1024] + q[1152])));
+                    y[j] = q[512] + q[640];
+                }
+                x[2] += x[3], x[1] += x[2], x[0] += x[1];
+                float from = x[0], before = (y[0] + y[1]) + (y[2] + y[3]);
+#pragma unroll
+                for (int m = 1; m < 32; m <<= 1) {
+                    const float a = __shfl_down_sync(~0u, from, m), b = __shfl_up_sync(~0u, before, m);
+                    if (lane + m < 32) from += a;
+                    if (lane >= m) before += b;
+                }
+                const float after = __shfl_down_sync(~0u, from, 1);
+                const float prior = __shfl_up_sync(~0u, before, 1);
+                float d = 0.f;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) d += red[w];
+                d *= expf(hi[c.len - 1]);
+                float low = lane > 0 ? prior : 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int u = 4 * lane + j;
+                    if (u < c.len) dg[u * p.sdg.t] = (x[j] + (lane < 31 ? after : 0.f)) + (low + d);
+                    low += y[j];
+                }
+            }
+            wait(L::DONE);
+            tc_fence_after_sync();
+            // the rows of the gradients: bf16 through tiles that are done, so that
+            // the stores are whole rows; fp32 (shared heads) straight
+            auto rows = [&](uint32_t col, uint32_t tile_at, int d, float *wide, auto value) {
+                const int n = d / 2;
+#pragma unroll 1
+                for (int e = 0; e < n; e += 16) {
+                    const int d0 = half * n + e;
+                    float x[16];
+                    value(col + d0, x);
+                    if (wide) {
+                        if (t < c.len)
+#pragma unroll
+                            for (int j = 0; j < 16; j += 8) {
+                                uint32_t y[8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(x[j + k]);
+                                st_global_32(wide + (size_t)t * d + d0 + j, y);
+                            }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 8)
+                            *reinterpret_cast<uint4 *>(sm + tile_at + ((d0 + j) >> 6) * 16384 + sw128_offset(t, (d0 + j) & 63)) =
+                                make_uint4(pack_bf16(x[j], x[j + 1]), pack_bf16(x[j + 2], x[j + 3]),
+                                           pack_bf16(x[j + 4], x[j + 5]), pack_bf16(x[j + 6], x[j + 7]));
+                    }
+                }
+            };
+            auto plain = [&](uint32_t col, float (&x)[16]) {
+                uint32_t u[16];
+                tmem_ld16(lanes + col, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(u[j]);
+            };
+            if (ok) rows(TM_Q, L::Q, DK, shared ? p.dqh + wide_row : nullptr, plain);
+            if (ok) rows(TM_K, L::K, DK, shared ? p.dkh + wide_row : nullptr, plain);
+            if (ok) rows(TM_A, L::V, DV, nullptr, [&](uint32_t col, float (&x)[16]) {
+                uint32_t u[16], w[16];
+                tmem_ld16(lanes + col, u);
+                tmem_ld16(lanes + col + (TM_B - TM_A), w);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = fmaf(fe, __uint_as_float(u[j]), __uint_as_float(w[j]));
+            });
+            meet();
+            auto store = [&](T *x, long long step, int d, uint32_t tile_at) {
+#pragma unroll 4
+                for (int e = tid; e < c.len * (d / 8); e += 256) {
+                    const int row = e / (d / 8), col = (e % (d / 8)) * 8;
+                    *reinterpret_cast<uint4 *>(x + row * step + col) =
+                        *reinterpret_cast<const uint4 *>(sm + tile_at + (col >> 6) * 16384 + sw128_offset(row, col & 63));
+                }
+            };
+            if (!shared && ok) {
+                store(dq, p.a.sq.t, DK, L::Q);
+                store(dk, p.a.sk.t, DK, L::K);
+            }
+            if (ok) store(dv, p.a.sv.t, DV, L::V);
+        }
+    }
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
 // ==================================================================== host side
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -1028,7 +1449,6 @@ bool state_map(CUtensorMap *m, const void *base, long long n, int DK, int DV) {
 }
 
 size_t up(size_t x) { return (x + 1023) / 1024 * 1024; }
-size_t state_bytes(const LinAttnArgs &a) { return up(2 * (size_t)chunk_bound(a, kC) * a.H * a.Dk * a.Dv); }
 
 int launched() {
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
@@ -1039,14 +1459,6 @@ int launched() {
 template <class F>
 bool smem_limit(F f, uint32_t bytes) {
     return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
-}
-
-template <int DK, int DV, bool REV, bool LO>
-int run_state(const CUtensorMap &mK, const CUtensorMap &mV, const TcArgs &p, cudaStream_t stream) {
-    auto kern = state_kernel<DK, DV, REV, LO>;
-    if (!smem_limit(kern, StateSmem<DK>::BYTES)) return GDN_ERR_CUDA;
-    kern<<<dim3(DV / 64, p.a.H, p.a.n_seq), kStateThreads, StateSmem<DK>::BYTES, stream>>>(mK, mV, p);
-    return launched();
 }
 
 template <int DK, int DV>
@@ -1063,6 +1475,48 @@ int run_fwd(const TcArgs &p, cudaStream_t stream) {
     auto kern = prompt_kernel<DK, DV>;
     if (!smem_limit(kern, FwdSmem<DK>::BYTES)) return GDN_ERR_CUDA;
     kern<<<dim3(DV / 64, a.H, a.n_seq + (a.cu ? 1 : 0)), kFwdThreads, FwdSmem<DK>::BYTES, stream>>>(mQ, mK, mV, w);
+    return launched();
+}
+
+struct BwdWs {
+    char *S[4];  // S hi, lo, R hi, lo
+    float *dqh, *dkh, *dgt;
+    size_t bytes;
+};
+
+BwdWs bwd_ws(const LinAttnArgs &a, void *ws) {
+    const size_t states = up(2 * (size_t)chunk_bound(a, kC) * a.H * a.Dk * a.Dv);
+    const size_t heads = a.H != a.Hk ? up(4 * (size_t)a.B * a.H * a.T * a.Dk) : 0;
+    // 1024-byte alignment for the kernels' wide stores, whatever the caller's
+    char *p = reinterpret_cast<char *>(up(reinterpret_cast<uintptr_t>(ws) + table_bytes(a, kC)));
+    BwdWs w;
+    for (char *&s : w.S) s = p, p += states;
+    w.dqh = reinterpret_cast<float *>(p), p += heads;
+    w.dkh = reinterpret_cast<float *>(p), p += heads;
+    w.dgt = reinterpret_cast<float *>(p), p += (a.flags & GDN_G_PER_HEAD) ? up(4 * (size_t)a.B * a.H * a.T) : 0;
+    w.bytes = p - static_cast<char *>(ws) + 1024;
+    return w;
+}
+
+template <int DK, int DV>
+int run_bwd(const TcArgs &p, cudaStream_t stream) {
+    const LinAttnArgs &a = p.a;
+    if (!mappable(a.sq, a.B, a.Hk, a.T) || !mappable(a.sk, a.B, a.Hk, a.T) || !mappable(a.sv, a.B, a.H, a.T) ||
+        !mappable(a.sdo, a.B, a.H, a.T))
+        return GDN_ERR_UNSUPPORTED;
+    CUtensorMap mQ, mK, mV, mO, mS[4];
+    const uint16_t *states[4] = {p.Shi, p.Slo, p.Rhi, p.Rlo};
+    for (int i = 0; i < 4; ++i)
+        if (!state_map(&mS[i], states[i], (long long)p.v.n_chunks * a.H, DK, DV)) return GDN_ERR_CUDA;
+    if (!strided_map(&mQ, a.q, a.sq, a.B, a.Hk, a.T, DK, kC) || !strided_map(&mK, a.k, a.sk, a.B, a.Hk, a.T, DK, kC) ||
+        !strided_map(&mV, a.v, a.sv, a.B, a.H, a.T, DV, kC) || !strided_map(&mO, a.dout, a.sdo, a.B, a.H, a.T, DV, kC))
+        return GDN_ERR_CUDA;
+    if (!smem_limit(state_kernel<DK, DV>, StateSmem<DK>::BYTES) || !smem_limit(grad_kernel_tc<DK, DV>, GradSmem::BYTES))
+        return GDN_ERR_CUDA;
+    state_kernel<DK, DV><<<dim3(2 * DV / 64, a.H, a.n_seq), kStateThreads, StateSmem<DK>::BYTES, stream>>>(mK, mV, mQ, mO, p);
+    const int st = launched();
+    if (st != GDN_OK) return st;
+    grad_kernel_tc<DK, DV><<<dim3(p.v.n_chunks, a.H), kGradThreads, GradSmem::BYTES, stream>>>(mQ, mK, mV, mO, mS[0], mS[1], mS[2], mS[3], p);
     return launched();
 }
 
@@ -1085,8 +1539,30 @@ int launch_linattn_tc_fwd(const LinAttnArgs &a, cudaStream_t stream) {
     return a.Dv == 128 ? run_fwd<64, 128>(p, stream) : run_fwd<64, 64>(p, stream);
 }
 
-size_t linattn_tc_bwd_workspace(const LinAttnArgs &a) { return linattn_bwd_workspace(a); }
-int launch_linattn_tc_bwd(const LinAttnArgs &a, cudaStream_t stream) { return launch_linattn_bwd(a, stream); }
+size_t linattn_tc_bwd_workspace(const LinAttnArgs &a) { return bwd_ws(a, nullptr).bytes; }
+
+int launch_linattn_tc_bwd(const LinAttnArgs &a, cudaStream_t stream) {
+    TcArgs p{};
+    p.a = a;
+    p.timeout_ns = wait_limit_ns();
+    const BwdWs w = bwd_ws(a, a.ws);
+    int st = make_view(a, kC, a.ws, &p.v, stream);
+    if (st != GDN_OK) return st;
+    p.Shi = reinterpret_cast<uint16_t *>(w.S[0]), p.Slo = reinterpret_cast<uint16_t *>(w.S[1]);
+    p.Rhi = reinterpret_cast<uint16_t *>(w.S[2]), p.Rlo = reinterpret_cast<uint16_t *>(w.S[3]);
+    p.dqh = w.dqh, p.dkh = w.dkh;
+    const bool per_head = a.flags & GDN_G_PER_HEAD;
+    p.dgt = per_head ? w.dgt : a.dg;
+    p.sdg = per_head ? Strides{(long long)a.H * a.T, a.T, 1} : a.sg;
+    if (a.Dk == 128) st = a.Dv == 128 ? run_bwd<128, 128>(p, stream) : run_bwd<128, 64>(p, stream);
+    else st = a.Dv == 128 ? run_bwd<64, 128>(p, stream) : run_bwd<64, 64>(p, stream);
+    if (st == GDN_OK && a.H != a.Hk) {
+        st = launch_group_sum(w.dqh, a.dq, a.sq, a.B, a.H, a.Hk, a.T, a.Dk, a.dtype, stream);
+        if (st == GDN_OK) st = launch_group_sum(w.dkh, a.dk, a.sk, a.B, a.H, a.Hk, a.T, a.Dk, a.dtype, stream);
+    }
+    if (st == GDN_OK && per_head) st = launch_head_sum(w.dgt, a.dg, a.B, a.H, a.T, stream);
+    return st;
+}
 
 int linattn_tc_read_clear_error() {
     unsigned int v = 0, zero = 0;
