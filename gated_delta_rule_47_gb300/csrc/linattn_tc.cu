@@ -83,6 +83,12 @@ __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // A weight as bf16 terms, each twice in a word: w = h + m + l to 2^-24.
 struct Weight {
     uint32_t h, m, l;
@@ -100,9 +106,10 @@ __device__ __forceinline__ Weight split_weight(float w) {
 // Two values times a weight as a sum of bf16 terms, in packed bf16 arithmetic.
 // hi is the rounded product with the weight's first term and r what that
 // rounding left, exactly (a product of two 8-bit mantissas has 16 bits).
-// Two terms: lo = v m + r, 2^-17 of the product off.  Three: mid = v m + r
-// rounded, and lo picks up what is left of it and v l; r - mid is exact
-// unless the two nearly cancel, so the sum is 2^-22 off or so.
+// Two terms: lo = v m + r, 2^-17 of the product off.  Three: the product with
+// the second term is split in the same way, the two parts of that size are
+// added with the sum's own rounding error kept (exact in any order of size),
+// and what is left goes into lo: 2^-24 or so off.
 __device__ __forceinline__ void weigh2(uint32_t v, const Weight &w, uint32_t &hi, uint32_t &lo) {
     hi = mul2(v, w.h);
     lo = fma2(v, w.m, fma2(v, w.h, hi ^ 0x80008000u));
@@ -110,8 +117,11 @@ __device__ __forceinline__ void weigh2(uint32_t v, const Weight &w, uint32_t &hi
 __device__ __forceinline__ void weigh3(uint32_t v, const Weight &w, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
     hi = mul2(v, w.h);
     const uint32_t r = fma2(v, w.h, hi ^ 0x80008000u);
-    mid = fma2(v, w.m, r);
-    lo = fma2(v, w.l, fma2(v, w.m, sub2(r, mid)));
+    const uint32_t m = mul2(v, w.m), mr = fma2(v, w.m, m ^ 0x80008000u);
+    mid = add2(r, m);
+    const uint32_t b = sub2(mid, r);
+    const uint32_t e = add2(sub2(r, sub2(mid, b)), sub2(m, b));
+    lo = fma2(v, w.l, add2(mr, e));
 }
 
 // What the tensor-core kernels take besides their maps.
@@ -119,7 +129,7 @@ struct TcArgs {
     LinAttnArgs a;
     View v;
     uint16_t *Shi, *Slo;  // [chunk][H][DK][DV] bf16 hi + lo: the states that enter the chunks
-    uint16_t *Rhi, *Rlo;  // and the gradients of the states that leave them
+    uint16_t *Rhi, *Rlo, *Rend;  // and, in three terms, the gradients of the states that leave them
     float *dqh, *dkh;     // [B,H,T,DK] fp32, where value heads share dq and dk
     float *dgt;           // dg by token, with its strides
     Strides sdg;
@@ -245,8 +255,9 @@ static_assert(StateSmem<128>::BYTES <= 232448, "state kernel fits the shared mem
 
 // Grid (2 DV / 64, H, n_seq): the states that enter a sequence's chunks, and
 // (the second half of x) backwards over them the gradients of the states that
-// leave them, with Q and dO in the places of K and V.  Both go out as bf16
-// pairs hi + lo (2^-17), which the gradients' products take as operands.
+// leave them, with Q and dO in the places of K and V.  They go out as bf16
+// terms, which the gradients' products take as operands: S in two (2^-17), R,
+// on which more of dg's error hangs, in three.
 template <int DK, int DV>
 __global__ void __launch_bounds__(kStateThreads, 1)
     state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
@@ -327,19 +338,24 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             if (i >= 2) ok = ok && la_wait(&bars[L::UEMPTY + acc], ((i >> 1) - 1) & 1, end);
             tc_fence_after_sync();
             const uint32_t d = tmem + 64u * acc;
+            // sums in the tensor core are cut off, not rounded, and what is added
+            // to little loses little: the half of smaller weights first, and in
+            // it the smallest terms
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
+            for (int j = 0; j < 2; ++j) {
+                const int half = rev ? 1 - j : j;
                 ok = ok && la_wait(&bars[L::XREADY + half], i & 1, end);
                 if (!ok) break;
                 const uint32_t k = desc_lo(sbase + s * L::STAGE, 16384) + half * 512, x = desc_lo(sbase + L::X + half * 3 * 8192, 8192);
                 if (leader) {
-                    if (half == 0) mma_ss<0>(d, desc_of(k), desc_of(x), id);
-                    else mma_ss<1>(d, desc_of(k), desc_of(x), id);
+                    if (j == 0) mma_ss<0>(d, desc_of(k), desc_of(x + 1024), id);
+                    else mma_ss<1>(d, desc_of(k), desc_of(x + 1024), id);
 #pragma unroll
-                    for (int e = 1; e < 12; ++e) mma_ss<1>(d, desc_of(k + (e & 3) * 128), desc_of(x + (e >> 2) * 512 + (e & 3) * 128), id);
-                    if (half == 1) mma_commit(&bars[L::UFULL + acc]);
+                    for (int e = 1; e < 12; ++e)
+                        mma_ss<1>(d, desc_of(k + (e & 3) * 128), desc_of(x + (2 - (e >> 2)) * 512 + (e & 3) * 128), id);
+                    if (j == 1) mma_commit(&bars[L::UFULL + acc]);
                     mma_commit(&bars[L::XEMPTY + half]);
-                    if (half == 1) mma_commit(&bars[L::EMPTY + s]);
+                    if (j == 1) mma_commit(&bars[L::EMPTY + s]);
                 }
             }
         }
@@ -394,8 +410,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 }
             }
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                const int t = half * 64 + r;
+            for (int j = 0; j < 2; ++j) {
+                const int half = rev ? 1 - j : j, t = half * 64 + r;
                 const uint32_t *wr = wring + w * 384 + t;
                 const Weight wt = {wr[0], wr[128], wr[256]};
                 uint4 v[2];
@@ -442,19 +458,23 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         for (int i = 0; i < n; ++i) {
             const int acc = i & 1, w = i % kWRing;
             const size_t at = (((size_t)(sq.x + number(i)) * p.a.H + h) * DK + row) * DV + 64 * slice;
-            uint16_t *hi = (rev ? p.Rhi : p.Shi) + at, *lo = (rev ? p.Rlo : p.Slo) + at;
+            uint16_t *hi = (rev ? p.Rhi : p.Shi) + at, *lo = (rev ? p.Rlo : p.Slo) + at, *last = rev ? p.Rend + at : nullptr;
             if (mine)
 #pragma unroll
                 for (int e = 0; e < 64; e += 16) {
-                    uint32_t a[8], b[8];
+                    uint32_t a[8], b[8], c[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const float x = S[e + 2 * j], y = S[e + 2 * j + 1];
+                        float x = S[e + 2 * j], y = S[e + 2 * j + 1];
                         a[j] = pack_bf16(x, y);
-                        b[j] = pack_bf16(x - __uint_as_float(a[j] << 16), y - __uint_as_float(a[j] & 0xffff0000u));
+                        x -= __uint_as_float(a[j] << 16), y -= __uint_as_float(a[j] & 0xffff0000u);
+                        b[j] = pack_bf16(x, y);
+                        x -= __uint_as_float(b[j] << 16), y -= __uint_as_float(b[j] & 0xffff0000u);
+                        c[j] = pack_bf16(x, y);
                     }
                     st_global_32(hi + e, a);
                     st_global_32(lo + e, b);
+                    if (last) st_global_32(last + e, c);
                 }
             ok = warp_ok(la_wait(&bars[L::WFULL + w], (i / kWRing) & 1, end) && la_wait(&bars[L::UFULL + acc], (i >> 1) & 1, end));
             if (!ok) break;
@@ -973,7 +993,7 @@ constexpr int kGradThreads = 288;
 
 struct GradSmem {
     static constexpr uint32_t Q = 0, K = 32768, V = 65536, O = 98304;  // V: later P
-    static constexpr uint32_t X = 131072, Y = 163840, Z = 196608;      // S hi, later R lo; S lo, later N; R hi
+    static constexpr uint32_t X = 131072, Y = 163840, Z = 196608;      // S hi, then R lo; S lo, then R's last term, then N; R hi
     static constexpr uint32_t G = 229376;                              // decays: cum hi, lo, to_end
     static constexpr uint32_t RED = G + 1536;                          // sums of a chunk's dg, see kernel
     static constexpr uint32_t BAR = RED + 512;
@@ -1020,7 +1040,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     grad_kernel_tc(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                    const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mO,
                    const __grid_constant__ CUtensorMap mSh, const __grid_constant__ CUtensorMap mSl,
-                   const __grid_constant__ CUtensorMap mRh, const __grid_constant__ CUtensorMap mRl, TcArgs p) {
+                   const __grid_constant__ CUtensorMap mRh, const __grid_constant__ CUtensorMap mRl,
+                   const __grid_constant__ CUtensorMap mRe, TcArgs p) {
     using L = GradSmem;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
@@ -1113,25 +1134,25 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             ok = la_wait(&bars[L::SS], 0, end);
             if (!ok) break;
             if (leader) {
-                mma_steps<DV / 16>(TM_Q, idk, km(L::O, 128), km(L::X, DK));
-                mma_more<DV / 16>(TM_Q, idk, km(L::O, 128), km(L::Y, DK));
+                mma_steps<DV / 16>(TM_Q, idk, km(L::O, 128), km(L::Y, DK));  // the smaller term first, as in state_kernel
+                mma_more<DV / 16>(TM_Q, idk, km(L::O, 128), km(L::X, DK));
                 mma_commit(&bars[L::CQ]);
             }
-            ok = la_wait(&bars[L::RH], 0, end);
-            if (!ok) break;
-            if (leader) mma_steps<DV / 16>(TM_K, idk, km(L::V, 128), km(L::Z, DK));
-            // R lo in S hi's place, which has been multiplied and read
+            // R's lower terms in S's places, which have been multiplied and read
             ok = la_wait(&bars[L::CQ], 0, end) && la_wait(&bars[L::XREAD], 0, end);
             if (!ok) break;
             if (leader) {
-                mbar_arrive_expect_tx(&bars[L::RL], DK * DV * 2);
+                mbar_arrive_expect_tx(&bars[L::RL], 2 * DK * DV * 2);
                 state(&mRl, L::X, L::RL);
+                state(&mRe, L::Y, L::RL);
             }
             rl = true;
-            ok = la_wait(&bars[L::RL], 0, end);
+            ok = la_wait(&bars[L::RL], 0, end) && la_wait(&bars[L::RH], 0, end);
             if (!ok) break;
             if (leader) {
+                mma_steps<DV / 16>(TM_K, idk, km(L::V, 128), km(L::Y, DK));
                 mma_more<DV / 16>(TM_K, idk, km(L::V, 128), km(L::X, DK));
+                mma_more<DV / 16>(TM_K, idk, km(L::V, 128), km(L::Z, DK));
                 mma_commit(&bars[L::CK]);
             }
             ok = la_wait(&bars[L::READY], 0, end);
@@ -1257,20 +1278,18 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 return t < c.len ? x : 0.f;
             };
             if (ok) xt = scale_rows(TM_Q, ft, L::Q);
-            meet();  // S lo has been read: N takes its place
-#pragma unroll
-            for (int j = 0; j < 32; j += 4)
-                *reinterpret_cast<uint4 *>(sm + L::Y + half * 16384 + sw128_offset(t, 2 * j)) = make_uint4(N[j], N[j + 1], N[j + 2], N[j + 3]);
             wait(L::RL);
 #pragma unroll
             for (int e = 0; e < NV; ++e) dot = dot8(sh[e], *reinterpret_cast<const uint4 *>(sm + L::X + (tid + 256 * e) * 16), dot);
             wait(L::CK);
             tc_fence_after_sync();
             if (ok) yt = scale_rows(TM_K, fe, L::K);
-            // V has been multiplied: P takes its place
+            // R's last term and V have been multiplied: N and P take their places
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
+            for (int j = 0; j < 32; j += 4) {
+                *reinterpret_cast<uint4 *>(sm + L::Y + half * 16384 + sw128_offset(t, 2 * j)) = make_uint4(N[j], N[j + 1], N[j + 2], N[j + 3]);
                 *reinterpret_cast<uint4 *>(sm + L::V + half * 16384 + sw128_offset(t, 2 * j)) = make_uint4(P[j], P[j + 1], P[j + 2], P[j + 3]);
+            }
             if (c.len < kC) {
                 // another sequence's rows: zeros, so that nothing of theirs (an
                 // infinity, say) meets the zeros of N and P
@@ -1479,7 +1498,7 @@ int run_fwd(const TcArgs &p, cudaStream_t stream) {
 }
 
 struct BwdWs {
-    char *S[4];  // S hi, lo, R hi, lo
+    char *S[5];  // S hi, lo, R hi, lo, last
     float *dqh, *dkh, *dgt;
     size_t bytes;
 };
@@ -1504,9 +1523,9 @@ int run_bwd(const TcArgs &p, cudaStream_t stream) {
     if (!mappable(a.sq, a.B, a.Hk, a.T) || !mappable(a.sk, a.B, a.Hk, a.T) || !mappable(a.sv, a.B, a.H, a.T) ||
         !mappable(a.sdo, a.B, a.H, a.T))
         return GDN_ERR_UNSUPPORTED;
-    CUtensorMap mQ, mK, mV, mO, mS[4];
-    const uint16_t *states[4] = {p.Shi, p.Slo, p.Rhi, p.Rlo};
-    for (int i = 0; i < 4; ++i)
+    CUtensorMap mQ, mK, mV, mO, mS[5];
+    const uint16_t *states[5] = {p.Shi, p.Slo, p.Rhi, p.Rlo, p.Rend};
+    for (int i = 0; i < 5; ++i)
         if (!state_map(&mS[i], states[i], (long long)p.v.n_chunks * a.H, DK, DV)) return GDN_ERR_CUDA;
     if (!strided_map(&mQ, a.q, a.sq, a.B, a.Hk, a.T, DK, kC) || !strided_map(&mK, a.k, a.sk, a.B, a.Hk, a.T, DK, kC) ||
         !strided_map(&mV, a.v, a.sv, a.B, a.H, a.T, DV, kC) || !strided_map(&mO, a.dout, a.sdo, a.B, a.H, a.T, DV, kC))
@@ -1516,7 +1535,7 @@ int run_bwd(const TcArgs &p, cudaStream_t stream) {
     state_kernel<DK, DV><<<dim3(2 * DV / 64, a.H, a.n_seq), kStateThreads, StateSmem<DK>::BYTES, stream>>>(mK, mV, mQ, mO, p);
     const int st = launched();
     if (st != GDN_OK) return st;
-    grad_kernel_tc<DK, DV><<<dim3(p.v.n_chunks, a.H), kGradThreads, GradSmem::BYTES, stream>>>(mQ, mK, mV, mO, mS[0], mS[1], mS[2], mS[3], p);
+    grad_kernel_tc<DK, DV><<<dim3(p.v.n_chunks, a.H), kGradThreads, GradSmem::BYTES, stream>>>(mQ, mK, mV, mO, mS[0], mS[1], mS[2], mS[3], mS[4], p);
     return launched();
 }
 
@@ -1550,6 +1569,7 @@ int launch_linattn_tc_bwd(const LinAttnArgs &a, cudaStream_t stream) {
     if (st != GDN_OK) return st;
     p.Shi = reinterpret_cast<uint16_t *>(w.S[0]), p.Slo = reinterpret_cast<uint16_t *>(w.S[1]);
     p.Rhi = reinterpret_cast<uint16_t *>(w.S[2]), p.Rlo = reinterpret_cast<uint16_t *>(w.S[3]);
+    p.Rend = reinterpret_cast<uint16_t *>(w.S[4]);
     p.dqh = w.dqh, p.dkh = w.dkh;
     const bool per_head = a.flags & GDN_G_PER_HEAD;
     p.dgt = per_head ? w.dgt : a.dg;
