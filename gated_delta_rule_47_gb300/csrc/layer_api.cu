@@ -37,7 +37,7 @@ int check_sizes(const LinAttnArgs &a) {
     if (!a.cu && a.n_seq != a.B) return GDN_ERR_INVALID_ARG;
     if (bad_dims(a.Dk, a.Dv)) return GDN_ERR_UNSUPPORTED;
     if (a.H > 65535 || a.B > 65534 || a.n_seq > 65534 || a.T > (1 << 30)) return GDN_ERR_UNSUPPORTED;
-    if ((long long)a.B * ((a.T + 63) / 64) + a.n_seq > 0x3fffffffLL) return GDN_ERR_UNSUPPORTED;
+    if (((long long)a.B * ((a.T + 63) / 64) + a.n_seq + 2) * (a.H ? a.H : 1) > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 

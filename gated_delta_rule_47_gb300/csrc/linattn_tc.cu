@@ -130,6 +130,7 @@ struct TcArgs {
     View v;
     uint16_t *Shi, *Slo;  // [chunk][H][DK][DV] bf16 hi + lo: the states that enter the chunks
     uint16_t *Rhi, *Rlo, *Rend;  // and, in three terms, the gradients of the states that leave them
+    float *gates;         // [chunk][H][4][128] decays for the gradients, see state_kernel
     float *dqh, *dkh;     // [B,H,T,DK] fp32, where value heads share dq and dk
     float *dgt;           // dg by token, with its strides
     Strides sdg;
@@ -375,18 +376,31 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
             const int w = i % kWRing;
-            const Sums g = scan_sums(next);
+            const Gates<kC> g = scan_gates<kC>(next);
             fetch(i + 1);
             if (i >= kWRing && !la_wait(&bars[L::WEMPTY + w], ((i / kWRing) - 1) & 1, end)) break;
             Weight wt[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                wt[j] = split_weight(rev ? p.a.scale * exp2_fast(g.cum[j] * kLog2e) : exp2_fast(g.to_end[j] * kLog2e));
+                wt[j] = split_weight(rev ? p.a.scale * exp2_fast(g.cum[j].hi * kLog2e) : exp2_fast(g.to_end(j) * kLog2e));
+            if (blockIdx.x == 0) {
+                // the gradient kernel's decays: c_t as a pair, G - c_t, and
+                // e^{c_r - c_t} with r the last token of t's block of 32
+                const float rh = __shfl_sync(~0u, g.cum[3].hi, lane | 7), rl = __shfl_sync(~0u, g.cum[3].lo, lane | 7);
+                float4 *out = reinterpret_cast<float4 *>(p.gates + ((size_t)(sq.x + i) * p.a.H + h) * 512) + lane;
+                float cf[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) cf[j] = exp2_fast(((rh - g.cum[j].hi) + (rl - g.cum[j].lo)) * kLog2e);
+                out[0] = make_float4(g.cum[0].hi, g.cum[1].hi, g.cum[2].hi, g.cum[3].hi);
+                out[32] = make_float4(g.cum[0].lo, g.cum[1].lo, g.cum[2].lo, g.cum[3].lo);
+                out[64] = make_float4(g.to_end(0), g.to_end(1), g.to_end(2), g.to_end(3));
+                out[96] = make_float4(cf[0], cf[1], cf[2], cf[3]);
+            }
             uint4 *ws = reinterpret_cast<uint4 *>(wring + w * 384);
             ws[lane] = make_uint4(wt[0].h, wt[1].h, wt[2].h, wt[3].h);
             ws[lane + 32] = make_uint4(wt[0].m, wt[1].m, wt[2].m, wt[3].m);
             ws[lane + 64] = make_uint4(wt[0].l, wt[1].l, wt[2].l, wt[3].l);
-            if (lane == 0) dring[w] = expf(g.all);
+            if (lane == 0) dring[w] = expf(g.all.hi);
             mbar_arrive(&bars[L::WFULL + w]);
         }
     } else if (warp >= 8) {
@@ -987,37 +1001,37 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 }
 
 // ================================================================ grad kernel
-// Warps: 0..7 arithmetic (rows by lane quarter, columns in two halves), 8 loads
-// and products.
+// Warps: 0..7 arithmetic (rows by lane quarter, blocks of 16 columns in turn),
+// 8 loads and products.
 constexpr int kGradThreads = 288;
 
 struct GradSmem {
-    static constexpr uint32_t Q = 0, K = 32768, V = 65536, O = 98304;  // V: later P
+    static constexpr uint32_t Q = 0, K = 32768, V = 65536, O = 98304;  // V: later P; Q, K, V: last dq, dk, dv
     static constexpr uint32_t X = 131072, Y = 163840, Z = 196608;      // S hi, then R lo; S lo, then R's last term, then N; R hi
-    static constexpr uint32_t G = 229376;                              // decays: cum hi, lo, to_end
-    static constexpr uint32_t RED = G + 1536;                          // sums of a chunk's dg, see kernel
-    static constexpr uint32_t BAR = RED + 512;
-    enum { QK = 0, OV, SS, RH, RL, CT, CN, CQ, CK, XREAD, READY, DONE, DRAIN, NUM };
+    static constexpr uint32_t G = 229376;                              // the chunk's decays, as state_kernel wrote them
+    static constexpr uint32_t RED = G + 2048;
+    static constexpr uint32_t BAR = RED + 64;
+    enum { QK = 0, OV, SS, RH, RL, GT, LOADS = 6, CT = 6, CN, CQ, CK, DONE, TAIL, XREAD, READY, XFREE, STORED, DRAIN, NUM };
     static constexpr uint32_t TSLOT = BAR + 8 * NUM;
     static constexpr uint32_t BYTES = TSLOT + 16;
 };
 static_assert(GradSmem::BYTES <= 232448, "grad kernel fits the shared memory of one CTA");
-// TMEM columns: Q K^T, later K R; dO V^T, later P^T dO; dQ; dK
+// TMEM columns: Q K^T, then P | N by blocks, then K R; dO V^T, then P^T dO; dQ; dK
 constexpr uint32_t TM_A = 0, TM_B = 128, TM_Q = 256, TM_K = 384;
 
-// Sum over the warp's lanes (rows) of x[j], to lane j.
-__device__ __forceinline__ float column_sums(float (&x)[32]) {
+// Sums of x[j] over the warp's lanes (rows): lane's is column lane / 2.
+__device__ __forceinline__ float column_sums(float (&x)[16]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int m = 16; m; m >>= 1) {
-        const bool up = lane & m;
+    for (int m = 8; m; m >>= 1) {
+        const bool up = lane & (2 * m);
 #pragma unroll
         for (int j = 0; j < m; ++j) {
             const float keep = up ? x[j + m] : x[j], give = up ? x[j] : x[j + m];
-            x[j] = keep + __shfl_xor_sync(~0u, give, m);
+            x[j] = keep + __shfl_xor_sync(~0u, give, 2 * m);
         }
     }
-    return x[0];
+    return x[0] + __shfl_xor_sync(~0u, x[0], 1);
 }
 
 __device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float x) {
@@ -1029,53 +1043,34 @@ __device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float x) {
     return x;
 }
 
-// A chunk's gradients (the formulas are linattn.cu's).  Grid (chunks, H).
-// Products: T = Q K^T and dO V^T; dO S^T and V R^T with S and R as hi + lo;
-// then, with P and N = dO V^T under the decay mask rounded to bf16, N K, N^T Q,
-// P^T dO and K R.  What dg is made of never passes through a rounded operand:
-// the pairs' terms A come from the fp32 products, the terms through S and R
-// from the split ones.  Bound by the bytes: 256 KB in, 96 KB out a chunk.
+struct GradMaps {
+    CUtensorMap q, k, v, o, s_hi, s_lo, r_hi, r_lo, r_last, dq, dk, dv;
+};
+
+// The chunks' gradients (the formulas are linattn.cu's): one CTA an SM takes
+// (chunk, head) items in turn, the next item's tiles coming in as this one's
+// places get free.
+// Products: T = Q K^T and dO V^T; dO S^T and V R^T with S and R in terms; then,
+// with P and N = dO V^T under the decay mask rounded to bf16, N K, N^T Q, P^T dO
+// and K R.  What dg is made of never passes through a rounded operand: the
+// pairs' terms A come from the fp32 products, the terms through S and R from
+// the split ones.  Bound by the bytes: 288 KB in, 96 KB out a chunk.
 template <int DK, int DV>
-__global__ void __launch_bounds__(kGradThreads, 1)
-    grad_kernel_tc(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
-                   const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mO,
-                   const __grid_constant__ CUtensorMap mSh, const __grid_constant__ CUtensorMap mSl,
-                   const __grid_constant__ CUtensorMap mRh, const __grid_constant__ CUtensorMap mRl,
-                   const __grid_constant__ CUtensorMap mRe, TcArgs p) {
+__global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_constant__ GradMaps m, TcArgs p) {
     using L = GradSmem;
+    using T = __nv_bfloat16;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + L::TSLOT);
-    float *hi = reinterpret_cast<float *>(sm + L::G), *lo = hi + 128, *te = lo + 128;
+    const float *hi = reinterpret_cast<const float *>(sm + L::G), *lo = hi + 128, *te = lo + 128, *cf = te + 128;
     float *red = reinterpret_cast<float *>(sm + L::RED);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int ci = blockIdx.x, h = blockIdx.y, hk = h / (p.a.H / p.a.Hk);
-    const Chunk c = chunk_at<kC>(p.v, p.a.T, ci);
-    if (c.len <= 0) return;
+    const int items = p.v.n_chunks * p.a.H;
     const bool shared = p.a.H != p.a.Hk;
-    using T = __nv_bfloat16;
-    T *dq = at(static_cast<T *>(p.a.dq), p.a.sq, c.row, hk, c.t0), *dk = at(static_cast<T *>(p.a.dk), p.a.sk, c.row, hk, c.t0);
-    T *dv = at(static_cast<T *>(p.a.dv), p.a.sv, c.row, h, c.t0);
-    float *dg = at(p.dgt, p.sdg, c.row, h, c.t0);
-    const size_t wide_row = (((size_t)c.row * p.a.H + h) * p.a.T + c.t0) * DK;
-    if (c.seq < 0) {  // tokens of no sequence
-        auto zeros = [&](T *x, long long step, int d) {
-            for (int e = threadIdx.x; e < c.len * (d / 8); e += kGradThreads)
-                *reinterpret_cast<uint4 *>(x + (e / (d / 8)) * step + (e % (d / 8)) * 8) = make_uint4(0, 0, 0, 0);
-        };
-        if (shared) {
-            for (int e = threadIdx.x; e < c.len * DK; e += kGradThreads) p.dqh[wide_row + e] = p.dkh[wide_row + e] = 0.f;
-        } else {
-            zeros(dq, p.a.sq.t, DK);
-            zeros(dk, p.a.sk.t, DK);
-        }
-        zeros(dv, p.a.sv.t, DV);
-        for (int e = threadIdx.x; e < c.len; e += kGradThreads) dg[e * p.sdg.t] = 0.f;
-        return;
-    }
-    const uint64_t end = deadline_after(p.timeout_ns, 1);
+    const uint64_t end = deadline_after(p.timeout_ns, items / (int)gridDim.x + 1);
     if (threadIdx.x == 0) {
-        for (int b = 0; b < L::NUM; ++b) mbar_init(&bars[b], b == L::XREAD || b == L::READY ? 256 : 1);
+        for (int b = 0; b < L::NUM; ++b)
+            mbar_init(&bars[b], b == L::XREAD || b == L::READY || b == L::TAIL ? 256 : b == L::XFREE ? 32 : 1);
         fence_mbar_init();
     }
     if (warp == 8) {
@@ -1087,51 +1082,72 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     tc_fence_after_sync();
     constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
     const uint32_t sbase = smem_u32(sm);
-    bool ok = true;
 
     if (warp == 8) {
         const bool leader = elect_one();
-        auto tile = [&](const CUtensorMap *m, uint32_t at_, int bar, int d, int head) {
-#pragma unroll
-            for (int x = 0; x < d / 64; ++x) tma_load_4d(sm + at_ + x * 16384, m, &bars[bar], 64 * x, c.t0, head, c.row);
+        int loads[L::LOADS] = {0, 0, 0, 0, 0, 0};  // arrivals ordered on each of the loads' barriers
+        auto order = [&](int bar, uint32_t bytes) {
+            ++loads[bar];
+            if (leader) mbar_arrive_expect_tx(&bars[bar], bytes);
         };
-        auto state = [&](const CUtensorMap *m, uint32_t at_, int bar) {
+        auto tile = [&](const CUtensorMap *map, uint32_t to, int bar, int d, int head, const Chunk &c) {
+            if (leader)
 #pragma unroll
-            for (int x = 0; x < DV / 64; ++x) tma_load_3d(sm + at_ + x * (DK * 128), m, &bars[bar], 64 * x, 0, ci * p.a.H + h);
+                for (int x = 0; x < d / 64; ++x) tma_load_4d(sm + to + x * 16384, map, &bars[bar], 64 * x, c.t0, head, c.row);
         };
-        if (leader) {
-            mbar_arrive_expect_tx(&bars[L::QK], 2 * DK * 256);
-            tile(&mQ, L::Q, L::QK, DK, hk);
-            tile(&mK, L::K, L::QK, DK, hk);
-            mbar_arrive_expect_tx(&bars[L::OV], 2 * DV * 256);
-            tile(&mO, L::O, L::OV, DV, h);
-            tile(&mV, L::V, L::OV, DV, h);
-            mbar_arrive_expect_tx(&bars[L::SS], 2 * DK * DV * 2);
-            state(&mSh, L::X, L::SS);
-            state(&mSl, L::Y, L::SS);
-            mbar_arrive_expect_tx(&bars[L::RH], DK * DV * 2);
-            state(&mRh, L::Z, L::RH);
-        }
+        auto state = [&](const CUtensorMap *map, uint32_t to, int bar, int item) {
+            if (leader)
+#pragma unroll
+                for (int x = 0; x < DV / 64; ++x) tma_load_3d(sm + to + x * (DK * 128), map, &bars[bar], 64 * x, 0, item);
+        };
         // operands' low descriptor words: K-major tiles step by 32 bytes in a
         // block of 64 columns, MN-major ones by 16 rows
         auto km = [&](uint32_t at_, int rows) { return [=](int ks) { return desc_lo(sbase + at_, 16) + (ks >> 2) * (rows * 8) + (ks & 3) * 2; }; };
         auto mn = [&](uint32_t at_, uint32_t stride) { return [=](int ks) { return desc_lo(sbase + at_, stride) + ks * 128; }; };
-        bool rl = false;
-        do {
-            ok = la_wait(&bars[L::QK], 0, end);
+        bool ok = true;
+        uint32_t ph = 0, tails = 0;
+        bool first = true;
+#pragma unroll 1
+        for (int it = blockIdx.x; it < items; it += gridDim.x) {
+            const int ci = it / p.a.H, h = it - ci * p.a.H, hk = h / (p.a.H / p.a.Hk);
+            const Chunk c = chunk_at<kC>(p.v, p.a.T, ci);
+            if (c.len <= 0 || c.seq < 0) continue;
+            // the item before this one: its products are done; its dg has left X
+            // and the decays, its rows Q, K and V
+            order(L::SS, 2 * DK * DV * 2);
+            state(&m.s_lo, L::Y, L::SS, it);
+            order(L::RH, DK * DV * 2);
+            state(&m.r_hi, L::Z, L::RH, it);
+            if (!first) ok = la_wait(&bars[L::XFREE], ph ^ 1, end);
             if (!ok) break;
+            order(L::GT, 2048);
+            if (leader) bulk_load_global(sm + L::G, p.gates + (size_t)it * 512, 2048, &bars[L::GT]);
+            state(&m.s_hi, L::X, L::SS, it);
+            if (!first) ok = la_wait(&bars[L::STORED], ph ^ 1, end);
+            if (!ok) break;
+            order(L::QK, 2 * DK * 256);
+            tile(&m.q, L::Q, L::QK, DK, hk, c);
+            tile(&m.k, L::K, L::QK, DK, hk, c);
+            order(L::OV, 2 * DV * 256);
+            tile(&m.o, L::O, L::OV, DV, h, c);
+            tile(&m.v, L::V, L::OV, DV, h, c);
+            first = false;
+            ok = la_wait(&bars[L::QK], ph, end);
+            if (ok && c.len < kC) ok = la_wait(&bars[L::TAIL], tails++ & 1, end);
+            if (!ok) break;
+            tc_fence_after_sync();
             if (leader) {
                 mma_steps<DK / 16>(TM_A, idesc_bf16(128, 128, false, false), km(L::Q, 128), km(L::K, 128));
                 mma_commit(&bars[L::CT]);
             }
-            ok = la_wait(&bars[L::OV], 0, end);
+            ok = la_wait(&bars[L::OV], ph, end);
             if (!ok) break;
             if (leader) {
                 mma_steps<DV / 16>(TM_B, idesc_bf16(128, 128, false, false), km(L::O, 128), km(L::V, 128));
                 mma_commit(&bars[L::CN]);
             }
             constexpr uint32_t idk = idesc_bf16(128, DK, false, false);
-            ok = la_wait(&bars[L::SS], 0, end);
+            ok = la_wait(&bars[L::SS], ph, end);
             if (!ok) break;
             if (leader) {
                 mma_steps<DV / 16>(TM_Q, idk, km(L::O, 128), km(L::Y, DK));  // the smaller term first, as in state_kernel
@@ -1139,15 +1155,12 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 mma_commit(&bars[L::CQ]);
             }
             // R's lower terms in S's places, which have been multiplied and read
-            ok = la_wait(&bars[L::CQ], 0, end) && la_wait(&bars[L::XREAD], 0, end);
+            ok = la_wait(&bars[L::CQ], ph, end) && la_wait(&bars[L::XREAD], ph, end);
             if (!ok) break;
-            if (leader) {
-                mbar_arrive_expect_tx(&bars[L::RL], 2 * DK * DV * 2);
-                state(&mRl, L::X, L::RL);
-                state(&mRe, L::Y, L::RL);
-            }
-            rl = true;
-            ok = la_wait(&bars[L::RL], 0, end) && la_wait(&bars[L::RH], 0, end);
+            order(L::RL, 2 * DK * DV * 2);
+            state(&m.r_lo, L::X, L::RL, it);
+            state(&m.r_last, L::Y, L::RL, it);
+            ok = la_wait(&bars[L::RL], ph, end) && la_wait(&bars[L::RH], ph, end);
             if (!ok) break;
             if (leader) {
                 mma_steps<DV / 16>(TM_K, idk, km(L::V, 128), km(L::Y, DK));
@@ -1155,7 +1168,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 mma_more<DV / 16>(TM_K, idk, km(L::V, 128), km(L::Z, DK));
                 mma_commit(&bars[L::CK]);
             }
-            ok = la_wait(&bars[L::READY], 0, end);
+            ok = la_wait(&bars[L::READY], ph, end);
             if (!ok) break;
             tc_fence_after_sync();
             if (leader) {
@@ -1165,25 +1178,22 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 mma_steps<DK / 16>(TM_A, idesc_bf16(128, DV, false, true), km(L::K, 128), mn(L::Z, DK * 128));
                 mma_commit(&bars[L::DONE]);
             }
-            ok = la_wait(&bars[L::DONE], 0, end);
-        } while (false);
+            ok = la_wait(&bars[L::DONE], ph, end);
+            if (!ok) break;
+            ph ^= 1;
+        }
         if (!warp_ok(ok)) {  // no copy and no product is in flight when the CTA ends
             if (leader) mma_commit(&bars[L::DRAIN]);
             mbar_wait(&bars[L::DRAIN], 0, kDrainNs);
-            mbar_wait(&bars[L::QK], 0, kDrainNs);
-            mbar_wait(&bars[L::OV], 0, kDrainNs);
-            mbar_wait(&bars[L::SS], 0, kDrainNs);
-            mbar_wait(&bars[L::RH], 0, kDrainNs);
-            if (rl) mbar_wait(&bars[L::RL], 0, kDrainNs);
+#pragma unroll
+            for (int b = 0; b < L::LOADS; ++b)
+                if (loads[b]) mbar_wait(&bars[b], (loads[b] - 1) & 1, kDrainNs);
         }
     } else {
-        const int t = 32 * (warp & 3) + lane, half = warp >> 2, s0 = 64 * half, tid = threadIdx.x;
+        const int t = 32 * (warp & 3) + lane, half = warp >> 2, tid = threadIdx.x;
         const uint32_t lanes = tmem + lane_base(warp);
-        // [quantity][..] partial sums by token: A's rows (2 halves), its columns (4
-        // quarters of rows), x (2), y (2), in the places of tiles that are done;
-        // until then in registers
-        float rowa = 0.f, cola[2] = {0.f, 0.f}, xt = 0.f, yt = 0.f, dot = 0.f;
-        uint32_t P[32], N[32];
+        bool ok = true;
+        uint32_t ph = 0;
         // the eight warps' barrier.  A warp whose wait gave up comes to it all the
         // same, and none of them goes on.
         auto meet = [&] {
@@ -1195,47 +1205,81 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 : "memory");
             ok = all != 0;
         };
-        auto wait = [&](int bar) { ok = warp_ok(ok && la_wait(&bars[bar], 0, end)); };
-        {
-            if (warp == 0) gates<kC>(gate_ptr(p.a, c, h), p.a.sg.t, c.len, p.a.flags & GDN_G_PER_HEAD, hi, lo, te);
-            meet();
-            wait(L::CT);
-            wait(L::CN);
-            tc_fence_after_sync();
-            const float ht = hi[t], lt = lo[t];
+        auto wait = [&](int bar) { ok = warp_ok(ok && la_wait(&bars[bar], ph, end)); };
+        // Scales the thread's part of its row of dQ or dK and gives its product
+        // with the row of Q or K.
+        auto scale_rows = [&](uint32_t col, float f, uint32_t tile_at) {
+            float x = 0.f;
+#pragma unroll 1
+            for (int e = 0; e < DK / 2; e += 16) {
+                const int d0 = half * (DK / 2) + e;
+                uint32_t u[16];
+                tmem_ld16(lanes + col + d0, u);
+                float q[16];
 #pragma unroll
-            for (int b = 0; b < 2 && ok; ++b) {
-                const int sb = s0 + 32 * b;  // the block's first column
-                if (sb > t - lane + 31) {    // past the diagonal for every row of the warp
+                for (int j = 0; j < 16; j += 8) {
+                    float y[8];
+                    unpack8(*reinterpret_cast<const uint4 *>(sm + tile_at + ((d0 + j) >> 6) * 16384 + sw128_offset(t, (d0 + j) & 63)), y);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) P[16 * b + j] = N[16 * b + j] = 0u;
-                    continue;
+                    for (int k = 0; k < 8; ++k) q[j + k] = y[k];
                 }
-                uint32_t u[32], w[32];
-                float a[32];
-                tmem_ld32(lanes + TM_A + sb, u);
-                tmem_ld32(lanes + TM_B + sb, w);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int s = sb + j;
-                    const bool in = s <= t && t < c.len;
-                    const float f = in ? p.a.scale * exp2_fast(((ht - hi[s]) + (lt - lo[s])) * kLog2e) : 0.f;
-                    const float qk = in ? __uint_as_float(u[j]) : 0.f, nn = in ? __uint_as_float(w[j]) * f : 0.f;
-                    a[j] = s < t ? qk * nn : 0.f;
-                    rowa += a[j];
-                    u[j] = __float_as_uint(qk * f);
-                    w[j] = __float_as_uint(nn);
-                }
-#pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    P[16 * b + j] = pack_bf16(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
-                    N[16 * b + j] = pack_bf16(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+                    const float y = f * __uint_as_float(u[j]);
+                    x = fmaf(q[j], y, x);
+                    u[j] = __float_as_uint(y);
                 }
-                cola[b] = column_sums(a);
+                tmem_st16(lanes + col + d0, u);
+            }
+            return x;
+        };
+#pragma unroll 1
+        for (int it = blockIdx.x; it < items; it += gridDim.x) {
+            const int ci = it / p.a.H, h = it - ci * p.a.H, hk = h / (p.a.H / p.a.Hk);
+            const Chunk c = chunk_at<kC>(p.v, p.a.T, ci);
+            if (c.len <= 0) continue;
+            T *dq = at(static_cast<T *>(p.a.dq), p.a.sq, c.row, hk, c.t0), *dk = at(static_cast<T *>(p.a.dk), p.a.sk, c.row, hk, c.t0);
+            T *dv = at(static_cast<T *>(p.a.dv), p.a.sv, c.row, h, c.t0);
+            float *dg = at(p.dgt, p.sdg, c.row, h, c.t0);
+            const size_t wide_row = (((size_t)c.row * p.a.H + h) * p.a.T + c.t0) * DK;
+            if (c.seq < 0) {  // tokens of no sequence
+                auto zeros = [&](T *x, long long step, int d) {
+#pragma unroll 1
+                    for (int e = tid; e < c.len * (d / 8); e += 256)
+                        *reinterpret_cast<uint4 *>(x + (e / (d / 8)) * step + (e % (d / 8)) * 8) = make_uint4(0, 0, 0, 0);
+                };
+                if (shared) {
+#pragma unroll 1
+                    for (int e = tid; e < c.len * DK; e += 256) p.dqh[wide_row + e] = p.dkh[wide_row + e] = 0.f;
+                } else {
+                    zeros(dq, p.a.sq.t, DK);
+                    zeros(dk, p.a.sk.t, DK);
+                }
+                zeros(dv, p.a.sv.t, DV);
+                for (int e = tid; e < c.len; e += 256) dg[e * p.sdg.t] = 0.f;
+                continue;
+            }
+            if (c.len < kC) {
+                // another sequence's rows: zeros, so that nothing of theirs (an
+                // infinity, say) reaches this one, and zeros come out of them
+                wait(L::QK);
+                wait(L::OV);
+#pragma unroll 1
+                for (int e = tid; e < (kC - c.len) * 16; e += 256) {
+                    const int row = c.len + (e >> 4), col = (e & 15) * 8;
+                    const uint32_t o = (col >> 6) * 16384 + sw128_offset(row, col & 63);
+                    if (col < DK) *reinterpret_cast<uint4 *>(sm + L::Q + o) = make_uint4(0, 0, 0, 0);
+                    if (col < DK) *reinterpret_cast<uint4 *>(sm + L::K + o) = make_uint4(0, 0, 0, 0);
+                    if (col < DV) *reinterpret_cast<uint4 *>(sm + L::O + o) = make_uint4(0, 0, 0, 0);
+                    if (col < DV) *reinterpret_cast<uint4 *>(sm + L::V + o) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                if (ok) mbar_arrive(&bars[L::TAIL]);
             }
             // <R, S>: (S hi + S lo) . R hi now, S hi . R lo when that is there
             constexpr int NV = DK * DV / 8 / 256;  // 16-byte words of a state a thread
+            float rowa = 0.f, cola[4] = {0.f, 0.f, 0.f, 0.f}, dot = 0.f, xt = 0.f, yt = 0.f;
             wait(L::SS);
             wait(L::RH);
             uint4 sh[NV];
@@ -1246,77 +1290,110 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 const uint4 r = *reinterpret_cast<const uint4 *>(sm + L::Z + o);
                 dot = dot8(sh[e], r, dot8(*reinterpret_cast<const uint4 *>(sm + L::Y + o), r, dot));
             }
-            mbar_arrive(&bars[L::XREAD]);
-            // dQ's part through S: scaled by its row, and x_t = q_t . it
-            wait(L::CQ);
+            if (ok) mbar_arrive(&bars[L::XREAD]);
+            wait(L::GT);
+            wait(L::CT);
+            wait(L::CN);
             tc_fence_after_sync();
-            const float ft = p.a.scale * exp2_fast(ht * kLog2e), fe = exp2_fast(te[t] * kLog2e);
-            auto scale_rows = [&](uint32_t col, float f, uint32_t tile_at) {
-                float x = 0.f;
+            // P, N and A of the thread's row, a block of 16 columns at a time (this
+            // half of the warps' are every other one).  The decays as in
+            // prompt_kernel, with c_t - c_s from the pairs.
+            const float ht = hi[t], lt = lo[t];
 #pragma unroll 1
-                for (int e = 0; e < DK / 2; e += 16) {
-                    const int d0 = half * (DK / 2) + e;
-                    uint32_t u[16];
-                    tmem_ld16(lanes + col + d0, u);
-                    float q[16];
+            for (int k = 0; k < 4 && ok; ++k) {
+                const int sb = 16 * (2 * k + half), diag = 32 * (warp & 3);
+                uint32_t u[16];
+                if (sb >= diag + 32) {  // past the diagonal for every row of the warp
 #pragma unroll
-                    for (int j = 0; j < 16; j += 8) {
-                        float y[8];
-                        unpack8(*reinterpret_cast<const uint4 *>(sm + tile_at + ((d0 + j) >> 6) * 16384 + sw128_offset(t, (d0 + j) & 63)), y);
+                    for (int j = 0; j < 16; ++j) u[j] = 0u;
+                    tmem_st16(lanes + TM_A + sb, u);
+                    continue;
+                }
+                uint32_t w[16];
+                float a[16];
+                tmem_ld16(lanes + TM_A + sb, u);
+                tmem_ld16(lanes + TM_B + sb, w);
+                const int r = sb | 31;
+                const float rf = p.a.scale * exp2_fast(((ht - hi[r]) + (lt - lo[r])) * kLog2e);
+                tmem_wait_ld();
+                if (sb < diag) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) q[j + k] = y[k];
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 f4 = *reinterpret_cast<const float4 *>(cf + sb + j);
+                        const float f[4] = {rf * f4.x, rf * f4.y, rf * f4.z, rf * f4.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float qk = __uint_as_float(u[j + e]), nn = __uint_as_float(w[j + e]) * f[e];
+                            a[j + e] = qk * nn;
+                            u[j + e] = __float_as_uint(qk * f[e]);
+                            w[j + e] = __float_as_uint(nn);
+                        }
                     }
-                    tmem_wait_ld();
+                } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float y = f * __uint_as_float(u[j]);
-                        x = fmaf(q[j], y, x);
-                        u[j] = __float_as_uint(y);
+                        const int s = sb + j;
+                        const float f = s <= t ? p.a.scale * exp2_fast(((ht - hi[s]) + (lt - lo[s])) * kLog2e) : 0.f;
+                        const float qk = __uint_as_float(u[j]), nn = __uint_as_float(w[j]) * f;
+                        a[j] = s < t ? qk * nn : 0.f;
+                        u[j] = __float_as_uint(qk * f);
+                        w[j] = __float_as_uint(nn);
                     }
-                    tmem_st16(lanes + col + d0, u);
                 }
-                return t < c.len ? x : 0.f;
-            };
-            if (ok) xt = scale_rows(TM_Q, ft, L::Q);
+                uint32_t pn[16];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    pn[j] = pack_bf16(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+                    pn[j + 8] = pack_bf16(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+                    rowa += a[2 * j] + a[2 * j + 1];
+                }
+                tmem_st16(lanes + TM_A + sb, pn);  // until their tiles' places are free
+                const float sum = column_sums(a);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) cola[j] = j == k ? sum : cola[j];
+            }
+            // dQ's part through S: scaled by its row, and x_t = q_t . it
+            const float fe = exp2_fast(te[t] * kLog2e), whole = expf(hi[c.len - 1]);
+            wait(L::CQ);
+            tc_fence_after_sync();
+            if (ok) xt = scale_rows(TM_Q, p.a.scale * exp2_fast(ht * kLog2e), L::Q);
             wait(L::RL);
 #pragma unroll
             for (int e = 0; e < NV; ++e) dot = dot8(sh[e], *reinterpret_cast<const uint4 *>(sm + L::X + (tid + 256 * e) * 16), dot);
             wait(L::CK);
             tc_fence_after_sync();
-            if (ok) yt = scale_rows(TM_K, fe, L::K);
-            // R's last term and V have been multiplied: N and P take their places
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                *reinterpret_cast<uint4 *>(sm + L::Y + half * 16384 + sw128_offset(t, 2 * j)) = make_uint4(N[j], N[j + 1], N[j + 2], N[j + 3]);
-                *reinterpret_cast<uint4 *>(sm + L::V + half * 16384 + sw128_offset(t, 2 * j)) = make_uint4(P[j], P[j + 1], P[j + 2], P[j + 3]);
-            }
-            if (c.len < kC) {
-                // another sequence's rows: zeros, so that nothing of theirs (an
-                // infinity, say) meets the zeros of N and P
-                meet();  // x and y have been made
+            if (ok) {
+                yt = scale_rows(TM_K, fe, L::K);
+                // R's last term and V have been multiplied: N and P take their places
+                tmem_wait_st();
 #pragma unroll 1
-                for (int e = tid; e < (kC - c.len) * 16; e += 256) {
-                    const int row = c.len + (e >> 4), col = (e & 15) * 8;
-                    const uint32_t o = (col >> 6) * 16384 + sw128_offset(row, col & 63);
-                    if (col < DK) *reinterpret_cast<uint4 *>(sm + L::Q + o) = make_uint4(0, 0, 0, 0);
-                    if (col < DK) *reinterpret_cast<uint4 *>(sm + L::K + o) = make_uint4(0, 0, 0, 0);
-                    if (col < DV) *reinterpret_cast<uint4 *>(sm + L::O + o) = make_uint4(0, 0, 0, 0);
+                for (int k = 0; k < 4; ++k) {
+                    const int sb = 16 * (2 * k + half);
+                    uint32_t pn[16];
+                    tmem_ld16(lanes + TM_A + sb, pn);
+                    tmem_wait_ld();
+                    const uint32_t o = (sb >> 6) * 16384, o0 = o + sw128_offset(t, sb & 63), o1 = o + sw128_offset(t, (sb & 63) + 8);
+                    *reinterpret_cast<uint4 *>(sm + L::V + o0) = make_uint4(pn[0], pn[1], pn[2], pn[3]);
+                    *reinterpret_cast<uint4 *>(sm + L::V + o1) = make_uint4(pn[4], pn[5], pn[6], pn[7]);
+                    *reinterpret_cast<uint4 *>(sm + L::Y + o0) = make_uint4(pn[8], pn[9], pn[10], pn[11]);
+                    *reinterpret_cast<uint4 *>(sm + L::Y + o1) = make_uint4(pn[12], pn[13], pn[14], pn[15]);
                 }
+                fence_proxy_async_smem();
+                tc_fence_before_sync();
+                mbar_arrive(&bars[L::READY]);
             }
-            tmem_wait_st();
-            fence_proxy_async_smem();
-            tc_fence_before_sync();
-            if (ok) mbar_arrive(&bars[L::READY]);
-            // dg meanwhile, through R lo's place
+            // dg meanwhile, through R lo's place: partial sums by token, A's rows (2
+            // halves of the warps), x, y, A's columns (4 quarters of rows)
             float *part = reinterpret_cast<float *>(sm + L::X);
             meet();
             part[half * 128 + t] = rowa;
             part[256 + half * 128 + t] = xt;
             part[512 + half * 128 + t] = yt;
-            part[768 + (warp & 3) * 128 + s0 + lane] = cola[0];
-            part[768 + (warp & 3) * 128 + s0 + 32 + lane] = cola[1];
+            if (!(lane & 1))
 #pragma unroll
-            for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(~0u, dot, m);
+                for (int k = 0; k < 4; ++k) part[768 + (warp & 3) * 128 + 16 * (2 * k + half) + lane / 2] = cola[k];
+#pragma unroll
+            for (int i = 16; i; i >>= 1) dot += __shfl_xor_sync(~0u, dot, i);
             if (lane == 0) red[warp] = dot;
             meet();
             if (warp == 0 && ok) {
@@ -1324,25 +1401,24 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 float x[4], y[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int u = 4 * lane + j;
-                    const float *q = part + u;
+                    const float *q = part + 4 * lane + j;
                     x[j] = (q[256] + q[384]) + ((q[0] + q[128]) - ((q[768] + q[896]) + (q[1024] + q[1152])));
                     y[j] = q[512] + q[640];
                 }
-                x[2] += x[3], x[1] += x[2], x[0] += x[1];
-                float from = x[0], before = (y[0] + y[1]) + (y[2] + y[3]);
-#pragma unroll
-                for (int m = 1; m < 32; m <<= 1) {
-                    const float a = __shfl_down_sync(~0u, from, m), b = __shfl_up_sync(~0u, before, m);
-                    if (lane + m < 32) from += a;
-                    if (lane >= m) before += b;
-                }
-                const float after = __shfl_down_sync(~0u, from, 1);
-                const float prior = __shfl_up_sync(~0u, before, 1);
                 float d = 0.f;
 #pragma unroll
                 for (int w = 0; w < 8; ++w) d += red[w];
-                d *= expf(hi[c.len - 1]);
+                d *= whole;
+                mbar_arrive(&bars[L::XFREE]);
+                x[2] += x[3], x[1] += x[2], x[0] += x[1];
+                float from = x[0], before = (y[0] + y[1]) + (y[2] + y[3]);
+#pragma unroll
+                for (int i = 1; i < 32; i <<= 1) {
+                    const float a = __shfl_down_sync(~0u, from, i), b = __shfl_up_sync(~0u, before, i);
+                    if (lane + i < 32) from += a;
+                    if (lane >= i) before += b;
+                }
+                const float after = __shfl_down_sync(~0u, from, 1), prior = __shfl_up_sync(~0u, before, 1);
                 float low = lane > 0 ? prior : 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -1353,65 +1429,82 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             }
             wait(L::DONE);
             tc_fence_after_sync();
-            // the rows of the gradients: bf16 through tiles that are done, so that
+            // the rows of the gradients: bf16 through the tiles Q, K and V, so that
             // the stores are whole rows; fp32 (shared heads) straight
-            auto rows = [&](uint32_t col, uint32_t tile_at, int d, float *wide, auto value) {
-                const int n = d / 2;
+            auto rows = [&](uint32_t col, uint32_t tile_at, int d, float *wide, bool both) {
 #pragma unroll 1
-                for (int e = 0; e < n; e += 16) {
-                    const int d0 = half * n + e;
-                    float x[16];
-                    value(col + d0, x);
+                for (int e = 0; e < d / 2; e += 16) {
+                    const int d0 = half * (d / 2) + e;
+                    uint32_t u[16], w[16];
+                    tmem_ld16(lanes + col + d0, u);
+                    if (both) tmem_ld16(lanes + TM_B + d0, w);
+                    tmem_wait_ld();
+                    if (both)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(fmaf(fe, __uint_as_float(u[j]), __uint_as_float(w[j])));
                     if (wide) {
                         if (t < c.len)
 #pragma unroll
                             for (int j = 0; j < 16; j += 8) {
-                                uint32_t y[8];
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(x[j + k]);
+                                const uint32_t y[8] = {u[j], u[j + 1], u[j + 2], u[j + 3], u[j + 4], u[j + 5], u[j + 6], u[j + 7]};
                                 st_global_32(wide + (size_t)t * d + d0 + j, y);
                             }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 16; j += 8)
+                        for (int j = 0; j < 16; j += 8) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) y[k] = pack_bf16(__uint_as_float(u[j + 2 * k]), __uint_as_float(u[j + 2 * k + 1]));
                             *reinterpret_cast<uint4 *>(sm + tile_at + ((d0 + j) >> 6) * 16384 + sw128_offset(t, (d0 + j) & 63)) =
-                                make_uint4(pack_bf16(x[j], x[j + 1]), pack_bf16(x[j + 2], x[j + 3]),
-                                           pack_bf16(x[j + 4], x[j + 5]), pack_bf16(x[j + 6], x[j + 7]));
+                                make_uint4(y[0], y[1], y[2], y[3]);
+                        }
                     }
                 }
             };
-            auto plain = [&](uint32_t col, float (&x)[16]) {
-                uint32_t u[16];
-                tmem_ld16(lanes + col, u);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(u[j]);
-            };
-            if (ok) rows(TM_Q, L::Q, DK, shared ? p.dqh + wide_row : nullptr, plain);
-            if (ok) rows(TM_K, L::K, DK, shared ? p.dkh + wide_row : nullptr, plain);
-            if (ok) rows(TM_A, L::V, DV, nullptr, [&](uint32_t col, float (&x)[16]) {
-                uint32_t u[16], w[16];
-                tmem_ld16(lanes + col, u);
-                tmem_ld16(lanes + col + (TM_B - TM_A), w);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = fmaf(fe, __uint_as_float(u[j]), __uint_as_float(w[j]));
-            });
-            meet();
-            auto store = [&](T *x, long long step, int d, uint32_t tile_at) {
-#pragma unroll 4
-                for (int e = tid; e < c.len * (d / 8); e += 256) {
-                    const int row = e / (d / 8), col = (e % (d / 8)) * 8;
-                    *reinterpret_cast<uint4 *>(x + row * step + col) =
-                        *reinterpret_cast<const uint4 *>(sm + tile_at + (col >> 6) * 16384 + sw128_offset(row, col & 63));
-                }
-            };
-            if (!shared && ok) {
-                store(dq, p.a.sq.t, DK, L::Q);
-                store(dk, p.a.sk.t, DK, L::K);
+            if (ok) {
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k)
+                    rows(k ? TM_K : TM_Q, k ? L::K : L::Q, DK, shared ? (k ? p.dkh : p.dqh) + wide_row : nullptr, false);
+                rows(TM_A, L::V, DV, nullptr, true);
             }
-            if (ok) store(dv, p.a.sv.t, DV, L::V);
+            fence_proxy_async_smem();
+            tc_fence_before_sync();
+            meet();
+            if (!ok) break;
+            if (c.len == kC) {
+                if (tid == 0) {
+#pragma unroll
+                    for (int x = 0; x < DK / 64; ++x) {
+                        if (shared) break;
+                        tma_store_4d(&m.dq, sm + L::Q + x * 16384, 64 * x, c.t0, hk, c.row);
+                        tma_store_4d(&m.dk, sm + L::K + x * 16384, 64 * x, c.t0, hk, c.row);
+                    }
+#pragma unroll
+                    for (int x = 0; x < DV / 64; ++x) tma_store_4d(&m.dv, sm + L::V + x * 16384, 64 * x, c.t0, h, c.row);
+                    tma_store_commit();
+                    tma_store_wait_read<0>();
+                    mbar_arrive(&bars[L::STORED]);
+                }
+            } else {
+                auto store = [&](T *x, long long step, int d, uint32_t tile_at) {
+#pragma unroll 1
+                    for (int e = tid; e < c.len * (d / 8); e += 256) {
+                        const int row = e / (d / 8), col = (e % (d / 8)) * 8;
+                        *reinterpret_cast<uint4 *>(x + row * step + col) =
+                            *reinterpret_cast<const uint4 *>(sm + tile_at + (col >> 6) * 16384 + sw128_offset(row, col & 63));
+                    }
+                };
+                if (!shared) {
+                    store(dq, p.a.sq.t, DK, L::Q);
+                    store(dk, p.a.sk.t, DK, L::K);
+                }
+                store(dv, p.a.sv.t, DV, L::V);
+                meet();
+                if (tid == 0) mbar_arrive(&bars[L::STORED]);
+            }
+            ph ^= 1;
         }
+        if (tid == 0) tma_store_wait_all<0>();
     }
     __syncwarp();
     tc_fence_before_sync();
@@ -1499,7 +1592,7 @@ int run_fwd(const TcArgs &p, cudaStream_t stream) {
 
 struct BwdWs {
     char *S[5];  // S hi, lo, R hi, lo, last
-    float *dqh, *dkh, *dgt;
+    float *gates, *dqh, *dkh, *dgt;
     size_t bytes;
 };
 
@@ -1510,6 +1603,7 @@ BwdWs bwd_ws(const LinAttnArgs &a, void *ws) {
     char *p = reinterpret_cast<char *>(up(reinterpret_cast<uintptr_t>(ws) + table_bytes(a, kC)));
     BwdWs w;
     for (char *&s : w.S) s = p, p += states;
+    w.gates = reinterpret_cast<float *>(p), p += up(2048 * (size_t)chunk_bound(a, kC) * a.H);
     w.dqh = reinterpret_cast<float *>(p), p += heads;
     w.dkh = reinterpret_cast<float *>(p), p += heads;
     w.dgt = reinterpret_cast<float *>(p), p += (a.flags & GDN_G_PER_HEAD) ? up(4 * (size_t)a.B * a.H * a.T) : 0;
@@ -1523,19 +1617,24 @@ int run_bwd(const TcArgs &p, cudaStream_t stream) {
     if (!mappable(a.sq, a.B, a.Hk, a.T) || !mappable(a.sk, a.B, a.Hk, a.T) || !mappable(a.sv, a.B, a.H, a.T) ||
         !mappable(a.sdo, a.B, a.H, a.T))
         return GDN_ERR_UNSUPPORTED;
-    CUtensorMap mQ, mK, mV, mO, mS[5];
+    GradMaps m;
     const uint16_t *states[5] = {p.Shi, p.Slo, p.Rhi, p.Rlo, p.Rend};
+    CUtensorMap *maps[5] = {&m.s_hi, &m.s_lo, &m.r_hi, &m.r_lo, &m.r_last};
     for (int i = 0; i < 5; ++i)
-        if (!state_map(&mS[i], states[i], (long long)p.v.n_chunks * a.H, DK, DV)) return GDN_ERR_CUDA;
-    if (!strided_map(&mQ, a.q, a.sq, a.B, a.Hk, a.T, DK, kC) || !strided_map(&mK, a.k, a.sk, a.B, a.Hk, a.T, DK, kC) ||
-        !strided_map(&mV, a.v, a.sv, a.B, a.H, a.T, DV, kC) || !strided_map(&mO, a.dout, a.sdo, a.B, a.H, a.T, DV, kC))
+        if (!state_map(maps[i], states[i], (long long)p.v.n_chunks * a.H, DK, DV)) return GDN_ERR_CUDA;
+    if (!strided_map(&m.q, a.q, a.sq, a.B, a.Hk, a.T, DK, kC) || !strided_map(&m.k, a.k, a.sk, a.B, a.Hk, a.T, DK, kC) ||
+        !strided_map(&m.v, a.v, a.sv, a.B, a.H, a.T, DV, kC) || !strided_map(&m.o, a.dout, a.sdo, a.B, a.H, a.T, DV, kC) ||
+        !strided_map(&m.dq, a.dq, a.sq, a.B, a.Hk, a.T, DK, kC) || !strided_map(&m.dk, a.dk, a.sk, a.B, a.Hk, a.T, DK, kC) ||
+        !strided_map(&m.dv, a.dv, a.sv, a.B, a.H, a.T, DV, kC))
         return GDN_ERR_CUDA;
     if (!smem_limit(state_kernel<DK, DV>, StateSmem<DK>::BYTES) || !smem_limit(grad_kernel_tc<DK, DV>, GradSmem::BYTES))
         return GDN_ERR_CUDA;
-    state_kernel<DK, DV><<<dim3(2 * DV / 64, a.H, a.n_seq), kStateThreads, StateSmem<DK>::BYTES, stream>>>(mK, mV, mQ, mO, p);
+    state_kernel<DK, DV><<<dim3(2 * DV / 64, a.H, a.n_seq), kStateThreads, StateSmem<DK>::BYTES, stream>>>(m.k, m.v, m.q, m.o, p);
     const int st = launched();
     if (st != GDN_OK) return st;
-    grad_kernel_tc<DK, DV><<<dim3(p.v.n_chunks, a.H), kGradThreads, GradSmem::BYTES, stream>>>(mQ, mK, mV, mO, mS[0], mS[1], mS[2], mS[3], mS[4], p);
+    const long long items = (long long)p.v.n_chunks * a.H;
+    const int sms = device_sm_count();
+    grad_kernel_tc<DK, DV><<<(unsigned)(items < sms ? items : sms), kGradThreads, GradSmem::BYTES, stream>>>(m, p);
     return launched();
 }
 
@@ -1570,7 +1669,7 @@ int launch_linattn_tc_bwd(const LinAttnArgs &a, cudaStream_t stream) {
     p.Shi = reinterpret_cast<uint16_t *>(w.S[0]), p.Slo = reinterpret_cast<uint16_t *>(w.S[1]);
     p.Rhi = reinterpret_cast<uint16_t *>(w.S[2]), p.Rlo = reinterpret_cast<uint16_t *>(w.S[3]);
     p.Rend = reinterpret_cast<uint16_t *>(w.S[4]);
-    p.dqh = w.dqh, p.dkh = w.dkh;
+    p.gates = w.gates, p.dqh = w.dqh, p.dkh = w.dkh;
     const bool per_head = a.flags & GDN_G_PER_HEAD;
     p.dgt = per_head ? w.dgt : a.dg;
     p.sdg = per_head ? Strides{(long long)a.H * a.T, a.T, 1} : a.sg;
