@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -53,6 +54,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     """Load libgdn.so (built by ``gated_delta_rule_47_gb300.build``) and declare
     the signatures of its entry points."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -615,40 +618,75 @@ def cam_prep_bwd(q_raw, k_raw, proj_q, proj_kv, dq_out, dk_out, dv_out, dk_pre_s
 
 
 # ------------------------------------------------- around a linear-attention layer
+# (a decoding step's kernels take a few microseconds: these calls keep to plain
+# attribute reads, and ask for a workspace's size once for each set of sizes)
 _NO_BYTES = ctypes.c_size_t(-1).value
+
+
+def _dense(t, name, shape, dtype):
+    """_check, for the case that all is well."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
+        _check(t, name, shape, dtype)
+
+
+def _at(stream, t):
+    """The raw stream of a call: the given one or the current one of t's device."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index) if stream is None else stream.cuda_stream
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=4096)
+def _bytes(fn, *sizes):
+    """A workspace query's answer."""
+    need = getattr(load(), fn)(*sizes)
+    if need == _NO_BYTES:
+        raise ValueError(f"sizes rejected by {fn}")
+    return int(need)
+
+
+def _scratch(need, device):
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+def _room(workspace):
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
 def _strided(t, name, shape, dtype):
     """As _check for a tensor whose last dimension is contiguous and whose
-    other strides are multiples of 16 bytes."""
+    other strides are multiples of 16 bytes; whether it is contiguous."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.is_contiguous():
+        return True
     size = t.element_size()
     for n, s in zip(t.shape[:-1], t.stride()[:-1]):
         if n > 1 and s * size % 16 != 0:
             raise ValueError(f"{name}'s strides {t.stride()} must be multiples of 16 bytes")
     if t.stride(-1) != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return t
+    return False
 
 
 def _gates(g, shape):
-    """Checks log-decays [B,H,T] (any strides) or [H]; whether they are per head."""
-    per_head = isinstance(g, torch.Tensor) and g.dim() == 1
-    if per_head:
-        _check(g, "g", (shape[1],), torch.float32)
-    else:
-        if not isinstance(g, torch.Tensor) or not g.is_cuda:
-            raise TypeError("g must be a CUDA tensor")
-        if tuple(g.shape) != shape:
-            raise ValueError(f"g has shape {tuple(g.shape)}, expected {shape} or ({shape[1]},)")
-        if g.dtype != torch.float32:
-            raise TypeError(f"g must be torch.float32, got {g.dtype}")
-    return per_head
+    """Checks log-decays [B,H,T] (any strides) or [H]: (per head, contiguous)."""
+    if isinstance(g, torch.Tensor) and g.dim() == 1:
+        _dense(g, "g", (shape[1],), torch.float32)
+        return True, True
+    if not isinstance(g, torch.Tensor) or not g.is_cuda:
+        raise TypeError("g must be a CUDA tensor")
+    if g.shape != shape:
+        raise ValueError(f"g has shape {tuple(g.shape)}, expected {shape} or ({shape[1]},)")
+    if g.dtype is not torch.float32:
+        raise TypeError(f"g must be torch.float32, got {g.dtype}")
+    return False, g.is_contiguous()
 
 
 def _steps(*tensors):
@@ -663,43 +701,42 @@ def _steps(*tensors):
     return (ctypes.c_longlong * 15)(*out)
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(stream):
     """Allocations of a call belong to the stream that it runs on."""
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+    return _HERE if stream is None else torch.cuda.stream(stream)
+
+
+def _overlaps(t):
+    """Whether elements share memory (an expanded tensor)."""
+    return any(s == 0 and n > 1 for n, s in zip(t.shape, t.stride()))
 
 
 def _linattn_sizes(q, k, v, g, cu_seqlens, initial_state):
     if not isinstance(q, torch.Tensor) or not isinstance(v, torch.Tensor) or q.dim() != 4 or v.dim() != 4:
         raise TypeError("q, k and v must be [B,heads,T,D] CUDA tensors")
     B, Hk, T, Dk = q.shape
-    H, Dv = v.shape[1], v.shape[3]
+    _, H, _, Dv = v.shape
     code = _dtype_code(q)
-    _strided(q, "q", (B, Hk, T, Dk), q.dtype)
-    _strided(k, "k", (B, Hk, T, Dk), q.dtype)
-    _strided(v, "v", (B, H, T, Dv), q.dtype)
-    per_head = _gates(g, (B, H, T))
+    dense = _strided(q, "q", (B, Hk, T, Dk), q.dtype)
+    dense = _strided(k, "k", (B, Hk, T, Dk), q.dtype) and dense
+    dense = _strided(v, "v", (B, H, T, Dv), q.dtype) and dense
+    per_head, plain = _gates(g, (B, H, T))
     if Hk == 0 or H % Hk != 0:
         raise ValueError(f"{Hk} query / key heads do not divide {H} value heads")
     n_seq = B
     if cu_seqlens is not None:
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must hold at least two offsets")
-        _check(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32)
+        _dense(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32)
         if B != 1:
             raise ValueError("packed sequences (cu_seqlens) lie in one row: B must be 1")
         n_seq = cu_seqlens.numel() - 1
     if initial_state is not None:
-        _check(initial_state, "initial_state", (n_seq, H, Dk, Dv), torch.float32)
-    return B, H, Hk, T, Dk, Dv, n_seq, code, per_head
-
-
-def _scratch(fn, need, workspace, device):
-    """The caller's workspace or a new one of `need` bytes."""
-    if need == _NO_BYTES:
-        raise ValueError(f"sizes rejected by {fn}")
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _dense(initial_state, "initial_state", (n_seq, H, Dk, Dv), torch.float32)
+    return B, H, Hk, T, Dk, Dv, n_seq, code, per_head, dense and plain
 
 
 def linattn_chunk_fwd(q, k, v, g, initial_state=None, output_final_state=False, cu_seqlens=None, scale=1.0, o=None,
@@ -711,27 +748,27 @@ def linattn_chunk_fwd(q, k, v, g, initial_state=None, output_final_state=False, 
     goes in as x.unsqueeze(0).transpose(1, 2)).  initial_state
     [sequences,H,Dk,Dv] fp32.  Returns (o, final_state or None); o has v's
     strides unless it is given."""
-    B, H, Hk, T, Dk, Dv, n_seq, code, per_head = _linattn_sizes(q, k, v, g, cu_seqlens, initial_state)
-    lib = load()
+    B, H, Hk, T, Dk, Dv, n_seq, code, per_head, dense = _linattn_sizes(q, k, v, g, cu_seqlens, initial_state)
     flags = (GDN_G_PER_HEAD if per_head else 0) | (GDN_PATH_SIMT if simt else 0)
+    need = _bytes("linattn_chunk_fwd_workspace_bytes", B, H, Hk, T, Dk, Dv, n_seq, cu_seqlens is not None, flags, code)
     with _on(stream):
-        q, k, v = (t.contiguous() if _overlaps(t) else t for t in (q, k, v))
+        if not dense:
+            q, k, v = (t.contiguous() if _overlaps(t) else t for t in (q, k, v))
         if o is None:
             o = torch.empty_like(v)
-        _strided(o, "o", (B, H, T, Dv), q.dtype)
+            dense = dense and o.is_contiguous()
+        else:
+            dense = _strided(o, "o", (B, H, T, Dv), q.dtype) and dense
         sf = torch.empty(n_seq, H, Dk, Dv, dtype=torch.float32, device=q.device) if output_final_state else None
-        need = lib.linattn_chunk_fwd_workspace_bytes(B, H, Hk, T, Dk, Dv, n_seq, cu_seqlens is not None, flags, code)
-        workspace, ws_bytes = _scratch("linattn_chunk_fwd", need, workspace, q.device)
-    st = lib.linattn_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(initial_state), _ptr(o), _ptr(sf),
-                               _ptr(cu_seqlens), _steps(q, k, v, o, g), n_seq, B, H, Hk, T, Dk, Dv, float(scale), flags,
-                               code, _ptr(workspace), ws_bytes, _stream(stream))
-    _raise("linattn_chunk_fwd", st)
+        if workspace is None:
+            workspace = _scratch(need, q.device)
+    st = load().linattn_chunk_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _addr(initial_state),
+                                  o.data_ptr(), _addr(sf), _addr(cu_seqlens), None if dense else _steps(q, k, v, o, g),
+                                  n_seq, B, H, Hk, T, Dk, Dv, scale, flags, code, _addr(workspace), _room(workspace),
+                                  _at(stream, q))
+    if st:
+        _raise("linattn_chunk_fwd", st)
     return o, sf
-
-
-def _overlaps(t):
-    """Whether elements share memory (an expanded tensor)."""
-    return any(s == 0 and n > 1 for n, s in zip(t.shape, t.stride()))
 
 
 def linattn_chunk_bwd(q, k, v, g, dout, initial_state=None, dfinal_state=None, cu_seqlens=None, scale=1.0,
@@ -740,63 +777,67 @@ def linattn_chunk_bwd(q, k, v, g, dout, initial_state=None, dfinal_state=None, c
     [sequences,H,Dk,Dv] fp32.  Returns (dq, dk, dv, dg, dinitial_state or
     None): the first three in the tensors' type, dg fp32 in g's shape (its sum
     over batch and tokens for g [H])."""
-    B, H, Hk, T, Dk, Dv, n_seq, code, per_head = _linattn_sizes(q, k, v, g, cu_seqlens, initial_state)
-    _strided(dout, "dout", (B, H, T, Dv), q.dtype)
+    B, H, Hk, T, Dk, Dv, n_seq, code, per_head, dense = _linattn_sizes(q, k, v, g, cu_seqlens, initial_state)
+    dense = _strided(dout, "dout", (B, H, T, Dv), q.dtype) and dense
     if dfinal_state is not None:
-        _check(dfinal_state, "dfinal_state", (n_seq, H, Dk, Dv), torch.float32)
-    lib = load()
+        _dense(dfinal_state, "dfinal_state", (n_seq, H, Dk, Dv), torch.float32)
     flags = (GDN_G_PER_HEAD if per_head else 0) | (GDN_PATH_SIMT if simt else 0)
+    need = _bytes("linattn_chunk_bwd_workspace_bytes", B, H, Hk, T, Dk, Dv, n_seq, cu_seqlens is not None, flags, code)
     with _on(stream):
-        # gradients take their tensors' strides, so those may not overlap
-        q, k, v, g, dout = (t.contiguous() if _overlaps(t) else t for t in (q, k, v, g, dout))
+        if not dense:
+            # gradients take their tensors' strides, so those may not overlap
+            q, k, v, g, dout = (t.contiguous() if _overlaps(t) else t for t in (q, k, v, g, dout))
         dq, dk, dv, dg = (torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device) for t in (q, k, v, g))
         ds0 = torch.empty_like(initial_state) if initial_state is not None else None
-        need = lib.linattn_chunk_bwd_workspace_bytes(B, H, Hk, T, Dk, Dv, n_seq, cu_seqlens is not None, flags, code)
-        workspace, ws_bytes = _scratch("linattn_chunk_bwd", need, workspace, q.device)
-    st = lib.linattn_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(initial_state), _ptr(dout), _ptr(dfinal_state),
-                               _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(ds0), _ptr(cu_seqlens),
-                               _steps(q, k, v, dout, g), n_seq, B, H, Hk, T, Dk, Dv, float(scale), flags, code,
-                               _ptr(workspace), ws_bytes, _stream(stream))
-    _raise("linattn_chunk_bwd", st)
+        if workspace is None:
+            workspace = _scratch(need, q.device)
+    st = load().linattn_chunk_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _addr(initial_state),
+                                  dout.data_ptr(), _addr(dfinal_state), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                  dg.data_ptr(), _addr(ds0), _addr(cu_seqlens),
+                                  None if dense else _steps(q, k, v, dout, g), n_seq, B, H, Hk, T, Dk, Dv, scale, flags,
+                                  code, _addr(workspace), _room(workspace), _at(stream, q))
+    if st:
+        _raise("linattn_chunk_bwd", st)
     return dq, dk, dv, dg, ds0
 
 
 def _step(fn_name, q, k, v, beta, g, state, slots, state_out, scale, l2norm, o, stream):
     B, Hk, Dk = q.shape
-    H, Dv = v.shape[1], v.shape[2]
+    _, H, Dv = v.shape
     n_slots = state.shape[0]
     dt = q.dtype
     code = _dtype_code(q)
-    _check(q, "q", (B, Hk, Dk), dt)
-    _check(k, "k", (B, Hk, Dk), dt)
-    _check(v, "v", (B, H, Dv), dt)
+    _dense(q, "q", (B, Hk, Dk), dt)
+    _dense(k, "k", (B, Hk, Dk), dt)
+    _dense(v, "v", (B, H, Dv), dt)
     if Hk == 0 or H % Hk != 0:
         raise ValueError(f"{Hk} query / key heads do not divide {H} value heads")
     per_head = g.dim() == 1
-    _check(g, "g", (H,) if per_head else (B, H), torch.float32)
-    _check(state, "state", (n_slots, H, Dk, Dv), torch.float32)
+    _dense(g, "g", (H,) if per_head else (B, H), torch.float32)
+    _dense(state, "state", (n_slots, H, Dk, Dv), torch.float32)
     if state_out is None:
         state_out = state
     elif state_out is not state:
-        _check(state_out, "state_out", (n_slots, H, Dk, Dv), torch.float32)
+        _dense(state_out, "state_out", (n_slots, H, Dk, Dv), torch.float32)
     if slots is not None:
-        _check(slots, "slots", (B,), torch.int32)
+        _dense(slots, "slots", (B,), torch.int32)
     elif B > n_slots:
         raise ValueError(f"{B} rows but {n_slots} pages")
     if o is None:
         with _on(stream):
             o = torch.empty_like(v)
     else:
-        _check(o, "o", (B, H, Dv), dt)
+        _dense(o, "o", (B, H, Dv), dt)
     flags = (GDN_G_PER_HEAD if per_head else 0) | (GDN_QK_L2NORM if l2norm else 0)
-    rest = (g.data_ptr(), state.data_ptr(), state_out.data_ptr(), _ptr(slots), o.data_ptr(), B, H, Hk, Dk, Dv, n_slots,
-            float(scale), flags, code, _stream(stream))
+    rest = (g.data_ptr(), state.data_ptr(), state_out.data_ptr(), _addr(slots), o.data_ptr(), B, H, Hk, Dk, Dv, n_slots,
+            scale, flags, code, _at(stream, q))
     if beta is None:
         st = load().linattn_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), *rest)
     else:
-        _check(beta, "beta", (B, H), dt)
+        _dense(beta, "beta", (B, H), dt)
         st = load().gdn_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), beta.data_ptr(), *rest)
-    _raise(fn_name, st)
+    if st:
+        _raise(fn_name, st)
     return o
 
 
@@ -821,11 +862,11 @@ def rms_norm_fwd(x, weight=None, residual=None, eps=1e-6, out_dtype=None, group=
     None, h); h is x itself without a residual."""
     C = x.shape[-1]
     code = _dtype_code(x)
-    _check(x, "x", x.shape)
+    _dense(x, "x", x.shape, x.dtype)
     if residual is not None:
-        _check(residual, "residual", x.shape, x.dtype)
+        _dense(residual, "residual", x.shape, x.dtype)
     if weight is not None:
-        _check(weight, "weight", (C,), torch.float32)
+        _dense(weight, "weight", (C,), torch.float32)
     e4m3 = out_dtype is torch.float8_e4m3fn
     if not e4m3 and out_dtype not in (None, x.dtype):
         raise TypeError(f"out_dtype must be {x.dtype} or torch.float8_e4m3fn, got {out_dtype}")
@@ -838,10 +879,11 @@ def rms_norm_fwd(x, weight=None, residual=None, eps=1e-6, out_dtype=None, group=
             scales = torch.empty((*x.shape[:-1], C // group if group else 1), dtype=torch.float32, device=x.device)
         h = torch.empty_like(x) if residual is not None else x
     rows = x.numel() // C if C else 0
-    st = load().rms_norm_fwd(x.data_ptr(), _ptr(residual), _ptr(weight), y.data_ptr(), _ptr(scales),
-                             h.data_ptr() if residual is not None else None, rows, C, group, float(eps), int(e4m3),
-                             code, _stream(stream))
-    _raise("rms_norm_fwd", st)
+    st = load().rms_norm_fwd(x.data_ptr(), _addr(residual), _addr(weight), y.data_ptr(), _addr(scales),
+                             h.data_ptr() if residual is not None else None, rows, C, group, eps, e4m3, code,
+                             _at(stream, x))
+    if st:
+        _raise("rms_norm_fwd", st)
     return y, scales, h
 
 
@@ -851,21 +893,23 @@ def rms_norm_bwd(dy, h, weight=None, dresidual=None, eps=1e-6, workspace=None, s
     the residual's gradient."""
     C = h.shape[-1]
     code = _dtype_code(h)
-    _check(h, "h", h.shape)
-    _check(dy, "dy", h.shape, h.dtype)
+    _dense(h, "h", h.shape, h.dtype)
+    _dense(dy, "dy", h.shape, h.dtype)
     if dresidual is not None:
-        _check(dresidual, "dresidual", h.shape, h.dtype)
+        _dense(dresidual, "dresidual", h.shape, h.dtype)
     if weight is not None:
-        _check(weight, "weight", (C,), torch.float32)
+        _dense(weight, "weight", (C,), torch.float32)
     rows = h.numel() // C if C else 0
-    lib = load()
+    need = _bytes("rms_norm_bwd_workspace_bytes", rows, C)
     with _on(stream):
         dx = torch.empty_like(h)
         dw = torch.empty(C, dtype=torch.float32, device=h.device)
-        workspace, ws_bytes = _scratch("rms_norm_bwd", lib.rms_norm_bwd_workspace_bytes(rows, C), workspace, h.device)
-    st = lib.rms_norm_bwd(dy.data_ptr(), h.data_ptr(), _ptr(weight), _ptr(dresidual), dx.data_ptr(), dw.data_ptr(), rows,
-                          C, float(eps), code, _ptr(workspace), ws_bytes, _stream(stream))
-    _raise("rms_norm_bwd", st)
+        if workspace is None:
+            workspace = _scratch(need, h.device)
+    st = load().rms_norm_bwd(dy.data_ptr(), h.data_ptr(), _addr(weight), _addr(dresidual), dx.data_ptr(), dw.data_ptr(),
+                             rows, C, eps, code, _addr(workspace), _room(workspace), _at(stream, h))
+    if st:
+        _raise("rms_norm_bwd", st)
     return dx, dw
 
 
@@ -876,7 +920,7 @@ def _pool(pool):
     if pool.dim() < 2 or not pool.is_contiguous():
         raise ValueError("pool must be a contiguous [layers,slots,...] tensor")
     layers, n_slots = pool.shape[:2]
-    page = pool[0, 0].numel() * pool.element_size() if layers and n_slots else 0
+    page = pool.stride(1) * pool.element_size() if layers and n_slots else 0
     if page % 16:
         raise ValueError(f"a page of {page} bytes is not a multiple of 16")
     return layers, n_slots, page
@@ -885,7 +929,7 @@ def _pool(pool):
 def _slots(t, name):
     if not isinstance(t, torch.Tensor) or t.dim() != 1:
         raise TypeError(f"{name} must be a one-dimensional CUDA tensor")
-    _check(t, name, t.shape, torch.int32)
+    _dense(t, name, t.shape, torch.int32)
     return t.numel()
 
 
@@ -896,8 +940,10 @@ def state_pool_copy(pool, src, dst, stream=None):
     n = _slots(src, "src")
     if _slots(dst, "dst") != n:
         raise ValueError(f"{n} sources but {dst.numel()} destinations")
-    _raise("state_pool_copy", load().state_pool_copy(pool.data_ptr(), layers, n_slots, page, src.data_ptr(),
-                                                     dst.data_ptr(), n, _stream(stream)))
+    st = load().state_pool_copy(pool.data_ptr(), layers, n_slots, page, src.data_ptr(), dst.data_ptr(), n,
+                                _at(stream, pool))
+    if st:
+        _raise("state_pool_copy", st)
 
 
 def state_pool_fork(pool, live, parents, stream=None):
@@ -906,24 +952,26 @@ def state_pool_fork(pool, live, parents, stream=None):
     [layers,slots,...].  live uint8 [slots] is updated.  Returns the children,
     int32, -1 where the parent is not live or no slot is left."""
     layers, n_slots, page = _pool(pool)
-    _check(live, "live", (n_slots,), torch.uint8)
+    _dense(live, "live", (n_slots,), torch.uint8)
     n = _slots(parents, "parents")
-    lib = load()
+    need = _bytes("state_pool_fork_workspace_bytes", n_slots, n)
     with _on(stream):
         children = torch.empty_like(parents)
-        ws, ws_bytes = _scratch("state_pool_fork", lib.state_pool_fork_workspace_bytes(n_slots, n), None, pool.device)
-    _raise("state_pool_fork", lib.state_pool_fork(pool.data_ptr(), layers, n_slots, page, live.data_ptr(),
-                                                  parents.data_ptr(), children.data_ptr(), n, _ptr(ws), ws_bytes,
-                                                  _stream(stream)))
+        ws = _scratch(need, pool.device)
+    st = load().state_pool_fork(pool.data_ptr(), layers, n_slots, page, live.data_ptr(), parents.data_ptr(),
+                                children.data_ptr(), n, _addr(ws), need, _at(stream, pool))
+    if st:
+        _raise("state_pool_fork", st)
     return children
 
 
 def state_pool_free(live, slots, stream=None):
     """Marks slots (int32; out-of-range ones are skipped) free in live uint8."""
-    _check(live, "live", live.shape, torch.uint8)
+    _dense(live, "live", live.shape, torch.uint8)
     n = _slots(slots, "slots")
-    _raise("state_pool_free", load().state_pool_free(live.data_ptr(), live.numel(), slots.data_ptr(), n,
-                                                     _stream(stream)))
+    st = load().state_pool_free(live.data_ptr(), live.numel(), slots.data_ptr(), n, _at(stream, live))
+    if st:
+        _raise("state_pool_free", st)
 
 
 def state_pool_compact(pool, live, stream=None):
@@ -931,15 +979,16 @@ def state_pool_compact(pool, live, stream=None):
     updates live.  Returns (remap, n_live): int32 [slots], each slot's new
     place or -1, and the count, int32 [1], on the device."""
     layers, n_slots, page = _pool(pool)
-    _check(live, "live", (n_slots,), torch.uint8)
-    lib = load()
+    _dense(live, "live", (n_slots,), torch.uint8)
+    need = _bytes("state_pool_compact_workspace_bytes", n_slots)
     with _on(stream):
         remap = torch.empty(n_slots, dtype=torch.int32, device=pool.device)
         n_live = torch.empty(1, dtype=torch.int32, device=pool.device)
-        ws, ws_bytes = _scratch("state_pool_compact", lib.state_pool_compact_workspace_bytes(n_slots), None, pool.device)
-    _raise("state_pool_compact", lib.state_pool_compact(pool.data_ptr(), layers, n_slots, page, live.data_ptr(),
-                                                        remap.data_ptr(), n_live.data_ptr(), _ptr(ws), ws_bytes,
-                                                        _stream(stream)))
+        ws = _scratch(need, pool.device)
+    st = load().state_pool_compact(pool.data_ptr(), layers, n_slots, page, live.data_ptr(), remap.data_ptr(),
+                                   n_live.data_ptr(), _addr(ws), need, _at(stream, pool))
+    if st:
+        _raise("state_pool_compact", st)
     return remap, n_live
 
 

@@ -20,6 +20,8 @@
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "gdn_internal.h"
 #include "linattn.cuh"
 #include "tc_util.cuh"
@@ -1568,9 +1570,17 @@ int launched() {
     return GDN_OK;
 }
 
-template <class F>
-bool smem_limit(F f, uint32_t bytes) {
-    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+// Raises a kernel's shared-memory limit, once for each device.
+template <auto F>
+bool smem_limit(uint32_t bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(F, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
 }
 
 template <int DK, int DV>
@@ -1585,7 +1595,7 @@ int run_fwd(const TcArgs &p, cudaStream_t stream) {
     TcArgs w = p;
     w.wide = ((reinterpret_cast<uintptr_t>(a.o) | 2 * a.so.b | 2 * a.so.h | 2 * a.so.t) & 31) == 0;
     auto kern = prompt_kernel<DK, DV>;
-    if (!smem_limit(kern, FwdSmem<DK>::BYTES)) return GDN_ERR_CUDA;
+    if (!smem_limit<prompt_kernel<DK, DV>>(FwdSmem<DK>::BYTES)) return GDN_ERR_CUDA;
     kern<<<dim3(DV / 64, a.H, a.n_seq + (a.cu ? 1 : 0)), kFwdThreads, FwdSmem<DK>::BYTES, stream>>>(mQ, mK, mV, w);
     return launched();
 }
@@ -1627,7 +1637,7 @@ int run_bwd(const TcArgs &p, cudaStream_t stream) {
         !strided_map(&m.dq, a.dq, a.sq, a.B, a.Hk, a.T, DK, kC) || !strided_map(&m.dk, a.dk, a.sk, a.B, a.Hk, a.T, DK, kC) ||
         !strided_map(&m.dv, a.dv, a.sv, a.B, a.H, a.T, DV, kC))
         return GDN_ERR_CUDA;
-    if (!smem_limit(state_kernel<DK, DV>, StateSmem<DK>::BYTES) || !smem_limit(grad_kernel_tc<DK, DV>, GradSmem::BYTES))
+    if (!smem_limit<state_kernel<DK, DV>>(StateSmem<DK>::BYTES) || !smem_limit<grad_kernel_tc<DK, DV>>(GradSmem::BYTES))
         return GDN_ERR_CUDA;
     state_kernel<DK, DV><<<dim3(2 * DV / 64, a.H, a.n_seq), kStateThreads, StateSmem<DK>::BYTES, stream>>>(m.k, m.v, m.q, m.o, p);
     const int st = launched();
