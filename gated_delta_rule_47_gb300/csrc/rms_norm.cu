@@ -63,9 +63,18 @@ __device__ __forceinline__ void stf(float *p, float x) { *p = x; }
 __device__ __forceinline__ void stf(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
 // max that keeps a NaN, so that a bad row shows in its scale
-__device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a != a) ? a : b; }
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
-// Sum / maximum over the CTA; every thread gets it.  `s` has room for 32.
+// A group's scale from its largest |y|, and what y is multiplied by.
+__device__ __forceinline__ float scale_of(float top) { return max_nan(top * (1.f / kTop), 1e-12f); }
+__device__ __forceinline__ float inverse(float x) { return __fdividef(1.f, x); }
+
+// Sum / maximum over the CTA; every thread gets it.  `s` has room for 32, and
+// nobody reads an earlier call's values from it any more.
 template <int NT, bool MAX>
 __device__ __forceinline__ float block_all(float x, float *s) {
 #pragma unroll
@@ -74,7 +83,6 @@ __device__ __forceinline__ float block_all(float x, float *s) {
         x = MAX ? max_nan(x, y) : x + y;
     }
     if (NT == 32) return x;
-    __syncthreads();
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
     __syncthreads();
     x = s[0];
@@ -96,90 +104,111 @@ __device__ __forceinline__ void store_e4m3(void *p, const float (&y)[N], float i
     else *static_cast<uint32_t *>(p) = u[0];
 }
 
-// One row a CTA of NT threads, V vectors a thread (vector j of thread t is
-// number j NT + t, so a group's vectors are consecutive lanes of one warp).
+// Rows blockIdx.x, + gridDim.x, .. by a CTA of NT threads, V vectors a thread
+// (vector j of thread t is number j NT + t, so a group's vectors are
+// consecutive lanes of one warp).  The next row is on its way while this one is
+// summed and written: a CTA that takes one row at a time has nothing to load
+// for half of its life.  The weights stay in registers.  Instructions bound a
+// 8-bit output before the bytes do: a thread takes two or four vectors, so that
+// the sums over the CTA cost less of them, and y is not formed for it:
+// y / scale = (h w) (r / scale).
 // C is a multiple of the vector's width; rows are 16-byte aligned.
 template <typename T, int NT, int V>
 __global__ void __launch_bounds__(NT) norm_kernel(NormArgs a) {
     constexpr int N = Vec<T>::N;
-    __shared__ float red[32];
-    const long long row = blockIdx.x;
+    __shared__ float red[2][32];
     const int nv = a.C / N;
-    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + row * a.C);
-    const uint4 *res = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.res) + row * a.C);
     uint4 px[V], pr[V];
+    auto fetch = [&](long long row) {
+        const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + row * a.C);
+        const uint4 *res = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.res) + row * a.C);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int i = j * NT + threadIdx.x;
-        px[j] = pr[j] = make_uint4(0, 0, 0, 0);
-        if (i < nv) {
-            px[j] = __ldcs(x + i);
-            if (a.res) pr[j] = __ldcs(res + i);
+        for (int j = 0; j < V; ++j) {
+            const int i = j * NT + threadIdx.x;
+            px[j] = pr[j] = make_uint4(0, 0, 0, 0);
+            if (row < a.rows && i < nv) {
+                px[j] = __ldcs(x + i);
+                if (a.res) pr[j] = __ldcs(res + i);
+            }
         }
-    }
-    float h[V][N];
-    float sum = 0.f;
-    uint4 *ho = a.h ? reinterpret_cast<uint4 *>(static_cast<T *>(a.h) + row * a.C) : nullptr;
+    };
+    fetch(blockIdx.x);
+    float w[V][N];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int i = j * NT + threadIdx.x;
-        Vec<T>::unpack(px[j], h[j]);
-        if (a.res) {
-            float r[N];
-            Vec<T>::unpack(pr[j], r);
-#pragma unroll
-            for (int e = 0; e < N; ++e) h[j][e] += r[e];
-        }
-        if (ho && i < nv) ho[i] = Vec<T>::pack(h[j]);
-#pragma unroll
-        for (int e = 0; e < N; ++e) sum = fmaf(h[j][e], h[j][e], sum);
-    }
-    sum = block_all<NT, false>(sum, red);
-    const float r = rsqrtf(sum / a.C + a.eps);
-    float top = 0.f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int i = j * NT + threadIdx.x;
+    for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int e = 0; e < N; e += 4) {
-            float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
-            if (a.w && i < nv) w = __ldg(reinterpret_cast<const float4 *>(a.w) + (i * N + e) / 4);
-            h[j][e] *= r * w.x, h[j][e + 1] *= r * w.y, h[j][e + 2] *= r * w.z, h[j][e + 3] *= r * w.w;
+            const int i = j * NT + threadIdx.x;
+            float4 x = make_float4(1.f, 1.f, 1.f, 1.f);
+            if (a.w && i < nv) x = __ldg(reinterpret_cast<const float4 *>(a.w) + (i * N + e) / 4);
+            w[j][e] = x.x, w[j][e + 1] = x.y, w[j][e + 2] = x.z, w[j][e + 3] = x.w;
         }
-        if (a.out_e4m3 && a.group == 0)
+    int buf = 0;
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
+        float h[V][N];
+        float sum = 0.f;
+        uint4 *ho = a.h ? reinterpret_cast<uint4 *>(static_cast<T *>(a.h) + row * a.C) : nullptr;
 #pragma unroll
-            for (int e = 0; e < N; ++e) top = max_nan(top, fabsf(h[j][e]));
-    }
-    if (!a.out_e4m3) {
-        uint4 *y = reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + row * a.C);
+        for (int j = 0; j < V; ++j) {
+            const int i = j * NT + threadIdx.x;
+            Vec<T>::unpack(px[j], h[j]);
+            if (a.res) {
+                float r[N];
+                Vec<T>::unpack(pr[j], r);
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (j * NT + threadIdx.x < nv) y[j * NT + threadIdx.x] = Vec<T>::pack(h[j]);
-        return;
-    }
-    unsigned char *y = static_cast<unsigned char *>(a.y) + row * a.C;
-    if (a.group == 0) {
-        top = block_all<NT, true>(top, red);
-        const float scale = max_nan(top / kTop, 1e-12f);
-        if (threadIdx.x == 0) a.scales[row] = scale;
-        const float inv = 1.f / scale;
+                for (int e = 0; e < N; ++e) h[j][e] += r[e];
+            }
+            if (ho && i < nv) __stcs(ho + i, Vec<T>::pack(h[j]));
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (j * NT + threadIdx.x < nv) store_e4m3<N>(y + (size_t)(j * NT + threadIdx.x) * N, h[j], inv);
-        return;
-    }
-    const int lanes = a.group / N;  // a power of two, at most 32
+            for (int e = 0; e < N; ++e) sum = fmaf(h[j][e], h[j][e], sum);
+        }
+        fetch(row + gridDim.x);
+        sum = block_all<NT, false>(sum, red[buf]);
+        const float r = rsqrtf(sum / a.C + a.eps);
+        if (!a.out_e4m3) {
+            uint4 *y = reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + row * a.C);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int i = j * NT + threadIdx.x;
-        float t = 0.f;
+            for (int j = 0; j < V; ++j) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) t = max_nan(t, fabsf(h[j][e]));
-        for (int m = lanes >> 1; m; m >>= 1) t = max_nan(t, __shfl_xor_sync(~0u, t, m));
-        const float scale = max_nan(t / kTop, 1e-12f);
-        if (i < nv) {
-            if ((i & (lanes - 1)) == 0) a.scales[row * (a.C / a.group) + i / lanes] = scale;
-            store_e4m3<N>(y + (size_t)i * N, h[j], 1.f / scale);
+                for (int e = 0; e < N; ++e) h[j][e] *= r * w[j][e];
+                if (j * NT + threadIdx.x < nv) __stcs(y + j * NT + threadIdx.x, Vec<T>::pack(h[j]));
+            }
+            continue;
+        }
+        unsigned char *y = static_cast<unsigned char *>(a.y) + row * a.C;
+        float top[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            top[j] = 0.f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                h[j][e] *= w[j][e];
+                top[j] = max_nan(top[j], fabsf(h[j][e]));
+            }
+        }
+        if (a.group == 0) {
+            float all = top[0];
+#pragma unroll
+            for (int j = 1; j < V; ++j) all = max_nan(all, top[j]);
+            __syncthreads();  // the sum has been read by all
+            const float scale = scale_of(r * block_all<NT, true>(all, red[buf]));
+            if (threadIdx.x == 0) a.scales[row] = scale;
+            const float inv = r * inverse(scale);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j * NT + threadIdx.x < nv) store_e4m3<N>(y + (size_t)(j * NT + threadIdx.x) * N, h[j], inv);
+            continue;
+        }
+        const int lanes = a.group / N;  // a power of two, at most 32
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int i = j * NT + threadIdx.x;
+            for (int m = lanes >> 1; m; m >>= 1) top[j] = max_nan(top[j], __shfl_xor_sync(~0u, top[j], m));
+            const float scale = scale_of(r * top[j]);
+            if (i < nv) {
+                if ((i & (lanes - 1)) == 0) a.scales[row * (a.C / a.group) + i / lanes] = scale;
+                store_e4m3<N>(y + (size_t)i * N, h[j], r * inverse(scale));
+            }
         }
     }
 }
@@ -188,7 +217,7 @@ __global__ void __launch_bounds__(NT) norm_kernel(NormArgs a) {
 // maximum), element by element.  Groups are not offered here.
 template <typename T>
 __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
-    __shared__ float red[32];
+    __shared__ float red[2][32];
     const long long row = blockIdx.x;
     const T *x = static_cast<const T *>(a.x) + row * a.C;
     const T *res = a.res ? static_cast<const T *>(a.res) + row * a.C : nullptr;
@@ -198,7 +227,7 @@ __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
         const float h = ldf(x + i) + (res ? ldf(res + i) : 0.f);
         sum = fmaf(h, h, sum);
     }
-    sum = block_all<256, false>(sum, red);
+    sum = block_all<256, false>(sum, red[0]);
     const float r = rsqrtf(sum / a.C + a.eps);
     float inv = 1.f;
     if (a.out_e4m3) {
@@ -206,10 +235,10 @@ __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
             const float h = ldf(x + i) + (res ? ldf(res + i) : 0.f);
             top = max_nan(top, fabsf(h * (r * (a.w ? a.w[i] : 1.f))));
         }
-        top = block_all<256, true>(top, red);
-        const float scale = max_nan(top / kTop, 1e-12f);
+        top = block_all<256, true>(top, red[1]);
+        const float scale = scale_of(top);
         if (threadIdx.x == 0) a.scales[row] = scale;
-        inv = 1.f / scale;
+        inv = inverse(scale);
     }
     for (int i = threadIdx.x; i < a.C; i += 256) {
         const float h = ldf(x + i) + (res ? ldf(res + i) : 0.f);
@@ -225,7 +254,10 @@ __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
 
 template <typename T, int NT, int V>
 void launch_v(const NormArgs &a, cudaStream_t stream) {
-    norm_kernel<T, NT, V><<<(unsigned)a.rows, NT, 0, stream>>>(a);
+    // as many CTAs as the registers let an SM hold, each with its weights
+    const int per_sm = NT * V >= 1024 ? (NT >= 512 ? 1 : 1024 / NT) : 1024 / NT;
+    const long long full = (long long)device_sm_count() * per_sm;
+    norm_kernel<T, NT, V><<<(unsigned)(a.rows < full ? a.rows : full), NT, 0, stream>>>(a);
 }
 
 template <typename T>
@@ -237,19 +269,19 @@ void launch_t(const NormArgs &a, cudaStream_t stream) {
     } else if (nv <= 32) {
         launch_v<T, 32, 1>(a, stream);
     } else if (nv <= 64) {
-        launch_v<T, 64, 1>(a, stream);
+        launch_v<T, 32, 2>(a, stream);
     } else if (nv <= 128) {
-        launch_v<T, 128, 1>(a, stream);
+        launch_v<T, 64, 2>(a, stream);
     } else if (nv <= 256) {
-        launch_v<T, 256, 1>(a, stream);
+        launch_v<T, 128, 2>(a, stream);
     } else if (nv <= 512) {
-        launch_v<T, 256, 2>(a, stream);
+        launch_v<T, 128, 4>(a, stream);
     } else if (nv <= 1024) {
         launch_v<T, 256, 4>(a, stream);
     } else if (nv <= 2048) {
         launch_v<T, 512, 4>(a, stream);
     } else {
-        launch_v<T, 1024, 4>(a, stream);
+        launch_v<T, 512, 8>(a, stream);
     }
 }
 
@@ -264,39 +296,50 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(NormBwdArgs a, fl
     constexpr int N = Vec<T>::N, NT = kBwdThreads;
     __shared__ float red[2][2][NT / 32];
     const int nv = a.C / N, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float dw[V][N];
+    float dw[V][N], w[V][N];
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int e = 0; e < N; ++e) dw[j][e] = 0.f;
+        for (int e = 0; e < N; e += 4) {
+            const int i = j * NT + threadIdx.x;
+            float4 x = make_float4(1.f, 1.f, 1.f, 1.f);
+            if (a.w && i < nv) x = __ldg(reinterpret_cast<const float4 *>(a.w) + (i * N + e) / 4);
+            w[j][e] = x.x, w[j][e + 1] = x.y, w[j][e + 2] = x.z, w[j][e + 3] = x.w;
+            dw[j][e] = dw[j][e + 1] = dw[j][e + 2] = dw[j][e + 3] = 0.f;
+        }
     int buf = 0;
-    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
+    uint4 nh[V], nd[V], nr[V];
+    auto fetch = [&](long long row) {  // the next row is on its way while this one is summed and written
         const uint4 *h4 = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.h) + row * a.C);
         const uint4 *dy4 = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.dy) + row * a.C);
         const uint4 *dr4 = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.dres) + row * a.C);
-        uint4 ph[V], pd[V], pr[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int i = j * NT + threadIdx.x;
-            ph[j] = pd[j] = pr[j] = make_uint4(0, 0, 0, 0);
-            if (i < nv) {
-                ph[j] = __ldcs(h4 + i);
-                pd[j] = __ldcs(dy4 + i);
-                if (a.dres) pr[j] = __ldcs(dr4 + i);
+            nh[j] = nd[j] = nr[j] = make_uint4(0, 0, 0, 0);
+            if (row < a.rows && i < nv) {
+                nh[j] = __ldcs(h4 + i);
+                nd[j] = __ldcs(dy4 + i);
+                if (a.dres) nr[j] = __ldcs(dr4 + i);
             }
         }
+    };
+    fetch(blockIdx.x);
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
+        uint4 ph[V], pd[V], pr[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) ph[j] = nh[j], pd[j] = nd[j], pr[j] = nr[j];
+        fetch(row + gridDim.x);
         float ss = 0.f, sp = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             float h[N], d[N];
             Vec<T>::unpack(ph[j], h);
             Vec<T>::unpack(pd[j], d);
-            const int i = j * NT + threadIdx.x;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const float w = a.w && i < nv ? __ldg(a.w + i * N + e) : 1.f;
                 ss = fmaf(h[e], h[e], ss);
-                sp = fmaf(h[e], d[e] * w, sp);
+                sp = fmaf(h[e], d[e] * w[j][e], sp);
             }
         }
 #pragma unroll
@@ -308,7 +351,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(NormBwdArgs a, fl
         __syncthreads();  // one a row: the buffers alternate
         ss = sp = 0.f;
 #pragma unroll
-        for (int w = 0; w < NT / 32; ++w) ss += red[buf][0][w], sp += red[buf][1][w];
+        for (int i = 0; i < NT / 32; ++i) ss += red[buf][0][i], sp += red[buf][1][i];
         const float r = rsqrtf(ss / a.C + a.eps);
         const float m = r * r * (sp / a.C);
         uint4 *dx = reinterpret_cast<uint4 *>(static_cast<T *>(a.dx) + row * a.C);
@@ -321,11 +364,10 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(NormBwdArgs a, fl
             Vec<T>::unpack(pr[j], g);
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const float w = a.w && i < nv ? __ldg(a.w + i * N + e) : 1.f;
-                g[e] = fmaf(r, fmaf(d[e], w, -h[e] * m), g[e]);
+                g[e] = fmaf(r, fmaf(d[e], w[j][e], -h[e] * m), g[e]);
                 dw[j][e] = fmaf(d[e], h[e] * r, dw[j][e]);
             }
-            if (i < nv) dx[i] = Vec<T>::pack(g);
+            if (i < nv) __stcs(dx + i, Vec<T>::pack(g));
         }
     }
 #pragma unroll
@@ -343,7 +385,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(NormBwdArgs a, fl
 template <typename T>
 __global__ void __launch_bounds__(kBwdThreads) norm_bwd_any_kernel(NormBwdArgs a, float *part) {
     constexpr int NT = kBwdThreads;
-    __shared__ float red[32];
+    __shared__ float red[2][32];
     float *mine = part + (size_t)blockIdx.x * a.C;
     for (int i = threadIdx.x; i < a.C; i += NT) mine[i] = 0.f;
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -355,8 +397,9 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_any_kernel(NormBwdArgs a
             ss = fmaf(x, x, ss);
             sp = fmaf(x, ldf(dy + i) * (a.w ? a.w[i] : 1.f), sp);
         }
-        ss = block_all<NT, false>(ss, red);
-        sp = block_all<NT, false>(sp, red);
+        __syncthreads();  // the last row's sums have been read
+        ss = block_all<NT, false>(ss, red[0]);
+        sp = block_all<NT, false>(sp, red[1]);
         const float r = rsqrtf(ss / a.C + a.eps);
         const float m = r * r * (sp / a.C);
         for (int i = threadIdx.x; i < a.C; i += NT) {
@@ -368,18 +411,21 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_any_kernel(NormBwdArgs a
     }
 }
 
-// dw[c] = the CTAs' shares, in order: 32 columns and 8 strands of shares a CTA.
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float *part, float *dw, int n, int C) {
-    __shared__ float s[8][33];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), strand = threadIdx.x >> 5;
+// dw[c] = the CTAs' shares: 32 columns a CTA, 32 strands of shares, then the
+// strands in order.
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float *part, float *dw, int n, int C) {
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, strand = threadIdx.x >> 5;
     float x = 0.f;
     if (c < C)
-        for (int i = strand; i < n; i += 8) x += part[(size_t)i * C + c];
-    s[strand][threadIdx.x & 31] = x;
+#pragma unroll 4
+        for (int i = strand; i < n; i += 32) x += part[(size_t)i * C + c];
+    s[strand][lane] = x;
     __syncthreads();
     if (strand == 0 && c < C) {
+        x = 0.f;
 #pragma unroll
-        for (int j = 1; j < 8; ++j) x += s[j][threadIdx.x & 31];
+        for (int j = 0; j < 32; ++j) x += s[j][lane];
         dw[c] = x;
     }
 }
@@ -417,7 +463,7 @@ int launch_rms_norm_bwd(const NormBwdArgs &a, cudaStream_t stream) {
     else launch_bwd_t<float>(a, ctas, part, stream);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
     note_launch();
-    norm_dw_kernel<<<(a.C + 31) / 32, 256, 0, stream>>>(part, a.dw, ctas, a.C);
+    norm_dw_kernel<<<(a.C + 31) / 32, 1024, 0, stream>>>(part, a.dw, ctas, a.C);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
     note_launch();
     return GDN_OK;
