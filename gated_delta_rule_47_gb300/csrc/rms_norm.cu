@@ -114,7 +114,7 @@ __device__ __forceinline__ void store_e4m3(void *p, const float (&y)[N], float i
 // y / scale = (h w) (r / scale).
 // C is a multiple of the vector's width; rows are 16-byte aligned.
 template <typename T, int NT, int V>
-__global__ void __launch_bounds__(NT) norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(NT, V <= 2 ? 1024 / NT : 1) norm_kernel(NormArgs a) {
     constexpr int N = Vec<T>::N;
     __shared__ float red[2][32];
     const int nv = a.C / N;
@@ -252,12 +252,21 @@ __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
     }
 }
 
+// A grid of as many CTAs as the SMs hold at once (one more would run alone at
+// the end), or of `rows` where that is less.
+template <auto F, int NT>
+unsigned resident(long long rows) {
+    static const int per_sm = [] {
+        int n = 0;
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, F, NT, 0) == cudaSuccess && n > 0 ? n : 1;
+    }();
+    const long long full = (long long)device_sm_count() * per_sm;
+    return (unsigned)(rows < full ? rows : full);
+}
+
 template <typename T, int NT, int V>
 void launch_v(const NormArgs &a, cudaStream_t stream) {
-    // as many CTAs as the registers let an SM hold, each with its weights
-    const int per_sm = NT * V >= 1024 ? (NT >= 512 ? 1 : 1024 / NT) : 1024 / NT;
-    const long long full = (long long)device_sm_count() * per_sm;
-    norm_kernel<T, NT, V><<<(unsigned)(a.rows < full ? a.rows : full), NT, 0, stream>>>(a);
+    norm_kernel<T, NT, V><<<resident<norm_kernel<T, NT, V>, NT>(a.rows), NT, 0, stream>>>(a);
 }
 
 template <typename T>
@@ -292,7 +301,7 @@ constexpr int kBwdThreads = 256;
 // every row, so its share of dw stays in registers until the CTA's rows are
 // done.  part[blockIdx.x][C].  V vectors a thread, as norm_kernel.
 template <typename T, int V>
-__global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(NormBwdArgs a, float *part) {
+__global__ void __launch_bounds__(kBwdThreads, V == 1 ? 4 : 1) norm_bwd_kernel(NormBwdArgs a, float *part) {
     constexpr int N = Vec<T>::N, NT = kBwdThreads;
     __shared__ float red[2][2][NT / 32];
     const int nv = a.C / N, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -430,18 +439,27 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *part, float 
     }
 }
 
+// The most shares of dw that a call makes (its workspace's size).
 int bwd_ctas(long long rows) {
     const long long full = 4LL * device_sm_count();
     return (int)(rows < full ? rows : full);
 }
 
+// Launches with at most `most` CTAs (what the workspace holds) and says with how many.
+template <auto F>
+int launch_rows(const NormBwdArgs &a, int most, float *part, cudaStream_t stream) {
+    const int fit = (int)resident<F, kBwdThreads>(a.rows), ctas = fit < most ? fit : most;
+    F<<<ctas, kBwdThreads, 0, stream>>>(a, part);
+    return ctas;
+}
+
 template <typename T>
-void launch_bwd_t(const NormBwdArgs &a, int ctas, float *part, cudaStream_t stream) {
+int launch_bwd_t(const NormBwdArgs &a, int most, float *part, cudaStream_t stream) {
     const int nv = a.C / Vec<T>::N;
-    if (a.C % Vec<T>::N != 0 || nv > 4 * kBwdThreads) norm_bwd_any_kernel<T><<<ctas, kBwdThreads, 0, stream>>>(a, part);
-    else if (nv <= kBwdThreads) norm_bwd_kernel<T, 1><<<ctas, kBwdThreads, 0, stream>>>(a, part);
-    else if (nv <= 2 * kBwdThreads) norm_bwd_kernel<T, 2><<<ctas, kBwdThreads, 0, stream>>>(a, part);
-    else norm_bwd_kernel<T, 4><<<ctas, kBwdThreads, 0, stream>>>(a, part);
+    if (a.C % Vec<T>::N != 0 || nv > 4 * kBwdThreads) return launch_rows<norm_bwd_any_kernel<T>>(a, most, part, stream);
+    if (nv <= kBwdThreads) return launch_rows<norm_bwd_kernel<T, 1>>(a, most, part, stream);
+    if (nv <= 2 * kBwdThreads) return launch_rows<norm_bwd_kernel<T, 2>>(a, most, part, stream);
+    return launch_rows<norm_bwd_kernel<T, 4>>(a, most, part, stream);
 }
 
 }  // namespace
@@ -458,9 +476,8 @@ size_t rms_norm_bwd_workspace(long long rows, int C) { return 4 * (size_t)bwd_ct
 
 int launch_rms_norm_bwd(const NormBwdArgs &a, cudaStream_t stream) {
     float *part = static_cast<float *>(a.ws);
-    const int ctas = bwd_ctas(a.rows);
-    if (a.dtype == GDN_BF16) launch_bwd_t<__nv_bfloat16>(a, ctas, part, stream);
-    else launch_bwd_t<float>(a, ctas, part, stream);
+    const int most = bwd_ctas(a.rows);
+    const int ctas = a.dtype == GDN_BF16 ? launch_bwd_t<__nv_bfloat16>(a, most, part, stream) : launch_bwd_t<float>(a, most, part, stream);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
     note_launch();
     norm_dw_kernel<<<(a.C + 31) / 32, 1024, 0, stream>>>(part, a.dw, ctas, a.C);
