@@ -1003,17 +1003,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 }
 
 // ================================================================ grad kernel
-// Warps: 0..7 arithmetic (rows by lane quarter, blocks of 16 columns in turn),
-// 8 loads and products.
-constexpr int kGradThreads = 288;
+// Warps: 0..15 arithmetic (rows by lane quarter, columns in four parts), 16
+// loads and products.
+constexpr int kGradWork = 512, kGradThreads = kGradWork + 32;
 
 struct GradSmem {
-    static constexpr uint32_t Q = 0, K = 32768, V = 65536, O = 98304;  // V: later P; Q, K, V: last dq, dk, dv
-    static constexpr uint32_t X = 131072, Y = 163840, Z = 196608;      // S hi, then R lo; S lo, then R's last term, then N; R hi
+    static constexpr uint32_t Q = 0, K = 32768, V = 65536, O = 98304;  // V: later P
+    // S hi, then R lo, then dv; S lo, then R's last term, then N, then dq; R hi, then dk
+    static constexpr uint32_t X = 131072, Y = 163840, Z = 196608;
     static constexpr uint32_t G = 229376;                              // the chunk's decays, as state_kernel wrote them
     static constexpr uint32_t RED = G + 2048;
-    static constexpr uint32_t BAR = RED + 64;
-    enum { QK = 0, OV, SS, RH, RL, GT, LOADS = 6, CT = 6, CN, CQ, CK, DONE, TAIL, XREAD, READY, XFREE, STORED, DRAIN, NUM };
+    static constexpr uint32_t BAR = RED + 64;  // 16 floats
+    enum { QK = 0, OV, SS, RH, RL, GT, LOADS = 6, CT = 6, CN, CQ, CK, DONE, TAIL, XREAD, READY, XFREE, ROWS, STORED, DRAIN, NUM };
     static constexpr uint32_t TSLOT = BAR + 8 * NUM;
     static constexpr uint32_t BYTES = TSLOT + 16;
 };
@@ -1072,10 +1073,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
     const uint64_t end = deadline_after(p.timeout_ns, items / (int)gridDim.x + 1);
     if (threadIdx.x == 0) {
         for (int b = 0; b < L::NUM; ++b)
-            mbar_init(&bars[b], b == L::XREAD || b == L::READY || b == L::TAIL ? 256 : b == L::XFREE ? 32 : 1);
+            mbar_init(&bars[b], b == L::XREAD || b == L::READY || b == L::TAIL || b == L::ROWS ? kGradWork : b == L::XFREE ? 32 : 1);
         fence_mbar_init();
     }
-    if (warp == 8) {
+    if (warp == 16) {
         tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
@@ -1085,7 +1086,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
     constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
     const uint32_t sbase = smem_u32(sm);
 
-    if (warp == 8) {
+    if (warp == 16) {
         const bool leader = elect_one();
         int loads[L::LOADS] = {0, 0, 0, 0, 0, 0};  // arrivals ordered on each of the loads' barriers
         auto order = [&](int bar, uint32_t bytes) {
@@ -1114,30 +1115,22 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
             const int ci = it / p.a.H, h = it - ci * p.a.H, hk = h / (p.a.H / p.a.Hk);
             const Chunk c = chunk_at<kC>(p.v, p.a.T, ci);
             if (c.len <= 0 || c.seq < 0) continue;
-            // the item before this one: its products are done; its dg has left X
-            // and the decays, its rows Q, K and V
-            order(L::SS, 2 * DK * DV * 2);
-            state(&m.s_lo, L::Y, L::SS, it);
-            order(L::RH, DK * DV * 2);
-            state(&m.r_hi, L::Z, L::RH, it);
-            if (!first) ok = la_wait(&bars[L::XFREE], ph ^ 1, end);
-            if (!ok) break;
-            order(L::GT, 2048);
-            if (leader) bulk_load_global(sm + L::G, p.gates + (size_t)it * 512, 2048, &bars[L::GT]);
-            state(&m.s_hi, L::X, L::SS, it);
-            if (!first) ok = la_wait(&bars[L::STORED], ph ^ 1, end);
-            if (!ok) break;
+            // the item before this one: its products are done, and the tiles and
+            // decays with them; its gradients' rows leave through X, Y and Z
             order(L::QK, 2 * DK * 256);
             tile(&m.q, L::Q, L::QK, DK, hk, c);
             tile(&m.k, L::K, L::QK, DK, hk, c);
             order(L::OV, 2 * DV * 256);
             tile(&m.o, L::O, L::OV, DV, h, c);
             tile(&m.v, L::V, L::OV, DV, h, c);
-            first = false;
+            order(L::GT, 2048);
+            if (leader) bulk_load_global(sm + L::G, p.gates + (size_t)it * 512, 2048, &bars[L::GT]);
+            if (!first) ok = la_wait(&bars[L::ROWS], ph ^ 1, end);
+            if (!ok) break;
+            tc_fence_after_sync();
             ok = la_wait(&bars[L::QK], ph, end);
             if (ok && c.len < kC) ok = la_wait(&bars[L::TAIL], tails++ & 1, end);
             if (!ok) break;
-            tc_fence_after_sync();
             if (leader) {
                 mma_steps<DK / 16>(TM_A, idesc_bf16(128, 128, false, false), km(L::Q, 128), km(L::K, 128));
                 mma_commit(&bars[L::CT]);
@@ -1148,6 +1141,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
                 mma_steps<DV / 16>(TM_B, idesc_bf16(128, 128, false, false), km(L::O, 128), km(L::V, 128));
                 mma_commit(&bars[L::CN]);
             }
+            if (!first) ok = la_wait(&bars[L::STORED], ph ^ 1, end);
+            if (!ok) break;
+            first = false;
+            order(L::SS, 2 * DK * DV * 2);
+            state(&m.s_lo, L::Y, L::SS, it);
+            state(&m.s_hi, L::X, L::SS, it);
+            order(L::RH, DK * DV * 2);
+            state(&m.r_hi, L::Z, L::RH, it);
             constexpr uint32_t idk = idesc_bf16(128, DK, false, false);
             ok = la_wait(&bars[L::SS], ph, end);
             if (!ok) break;
@@ -1192,16 +1193,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
                 if (loads[b]) mbar_wait(&bars[b], (loads[b] - 1) & 1, kDrainNs);
         }
     } else {
-        const int t = 32 * (warp & 3) + lane, half = warp >> 2, tid = threadIdx.x;
+        const int t = 32 * (warp & 3) + lane, four = warp >> 2, tid = threadIdx.x;
         const uint32_t lanes = tmem + lane_base(warp);
         bool ok = true;
         uint32_t ph = 0;
-        // the eight warps' barrier.  A warp whose wait gave up comes to it all the
+        // these warps' barrier.  A warp whose wait gave up comes to it all the
         // same, and none of them goes on.
         auto meet = [&] {
             uint32_t all;
             asm volatile(
-                "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 512, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                 : "=r"(all)
                 : "r"(ok ? 1u : 0u)
                 : "memory");
@@ -1213,8 +1214,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
         auto scale_rows = [&](uint32_t col, float f, uint32_t tile_at) {
             float x = 0.f;
 #pragma unroll 1
-            for (int e = 0; e < DK / 2; e += 16) {
-                const int d0 = half * (DK / 2) + e;
+            for (int e = 0; e < DK / 4; e += 16) {
+                const int d0 = four * (DK / 4) + e;
                 uint32_t u[16];
                 tmem_ld16(lanes + col + d0, u);
                 float q[16];
@@ -1248,18 +1249,18 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
             if (c.seq < 0) {  // tokens of no sequence
                 auto zeros = [&](T *x, long long step, int d) {
 #pragma unroll 1
-                    for (int e = tid; e < c.len * (d / 8); e += 256)
+                    for (int e = tid; e < c.len * (d / 8); e += kGradWork)
                         *reinterpret_cast<uint4 *>(x + (e / (d / 8)) * step + (e % (d / 8)) * 8) = make_uint4(0, 0, 0, 0);
                 };
                 if (shared) {
 #pragma unroll 1
-                    for (int e = tid; e < c.len * DK; e += 256) p.dqh[wide_row + e] = p.dkh[wide_row + e] = 0.f;
+                    for (int e = tid; e < c.len * DK; e += kGradWork) p.dqh[wide_row + e] = p.dkh[wide_row + e] = 0.f;
                 } else {
                     zeros(dq, p.a.sq.t, DK);
                     zeros(dk, p.a.sk.t, DK);
                 }
                 zeros(dv, p.a.sv.t, DV);
-                for (int e = tid; e < c.len; e += 256) dg[e * p.sdg.t] = 0.f;
+                for (int e = tid; e < c.len; e += kGradWork) dg[e * p.sdg.t] = 0.f;
                 continue;
             }
             if (c.len < kC) {
@@ -1268,7 +1269,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
                 wait(L::QK);
                 wait(L::OV);
 #pragma unroll 1
-                for (int e = tid; e < (kC - c.len) * 16; e += 256) {
+                for (int e = tid; e < (kC - c.len) * 16; e += kGradWork) {
                     const int row = c.len + (e >> 4), col = (e & 15) * 8;
                     const uint32_t o = (col >> 6) * 16384 + sw128_offset(row, col & 63);
                     if (col < DK) *reinterpret_cast<uint4 *>(sm + L::Q + o) = make_uint4(0, 0, 0, 0);
@@ -1279,31 +1280,18 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
                 fence_proxy_async_smem();
                 if (ok) mbar_arrive(&bars[L::TAIL]);
             }
-            // <R, S>: (S hi + S lo) . R hi now, S hi . R lo when that is there
-            constexpr int NV = DK * DV / 8 / 256;  // 16-byte words of a state a thread
-            float rowa = 0.f, cola[4] = {0.f, 0.f, 0.f, 0.f}, dot = 0.f, xt = 0.f, yt = 0.f;
-            wait(L::SS);
-            wait(L::RH);
-            uint4 sh[NV];
-#pragma unroll
-            for (int e = 0; e < NV; ++e) {
-                const uint32_t o = (tid + 256 * e) * 16;
-                sh[e] = *reinterpret_cast<const uint4 *>(sm + L::X + o);
-                const uint4 r = *reinterpret_cast<const uint4 *>(sm + L::Z + o);
-                dot = dot8(sh[e], r, dot8(*reinterpret_cast<const uint4 *>(sm + L::Y + o), r, dot));
-            }
-            if (ok) mbar_arrive(&bars[L::XREAD]);
+            float rowa = 0.f, cola[2] = {0.f, 0.f}, dot = 0.f, xt = 0.f, yt = 0.f;
             wait(L::GT);
             wait(L::CT);
             wait(L::CN);
             tc_fence_after_sync();
-            // P, N and A of the thread's row, a block of 16 columns at a time (this
-            // half of the warps' are every other one).  The decays as in
+            // P, N and A of the thread's row, a block of 16 columns at a time (every
+            // fourth is this warp's).  The decays as in
             // prompt_kernel, with c_t - c_s from the pairs.
             const float ht = hi[t], lt = lo[t];
 #pragma unroll 1
-            for (int k = 0; k < 4 && ok; ++k) {
-                const int sb = 16 * (2 * k + half), diag = 32 * (warp & 3);
+            for (int k = 0; k < 2 && ok; ++k) {
+                const int sb = 16 * (4 * k + four), diag = 32 * (warp & 3);
                 uint32_t u[16];
                 if (sb >= diag + 32) {  // past the diagonal for every row of the warp
 #pragma unroll
@@ -1352,8 +1340,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
                 tmem_st16(lanes + TM_A + sb, pn);  // until their tiles' places are free
                 const float sum = column_sums(a);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) cola[j] = j == k ? sum : cola[j];
+                for (int j = 0; j < 2; ++j) cola[j] = j == k ? sum : cola[j];
             }
+            // <R, S>: (S hi + S lo) . R hi now, S hi . R lo when that is there
+            constexpr int NV = DK * DV / 8 / kGradWork;  // 16-byte words of a state a thread
+            wait(L::SS);
+            wait(L::RH);
+            uint4 sh[NV];
+#pragma unroll
+            for (int e = 0; e < NV; ++e) {
+                const uint32_t o = (tid + kGradWork * e) * 16;
+                sh[e] = *reinterpret_cast<const uint4 *>(sm + L::X + o);
+                const uint4 r = *reinterpret_cast<const uint4 *>(sm + L::Z + o);
+                dot = dot8(sh[e], r, dot8(*reinterpret_cast<const uint4 *>(sm + L::Y + o), r, dot));
+            }
+            if (ok) mbar_arrive(&bars[L::XREAD]);
             // dQ's part through S: scaled by its row, and x_t = q_t . it
             const float fe = exp2_fast(te[t] * kLog2e), whole = expf(hi[c.len - 1]);
             wait(L::CQ);
@@ -1361,7 +1362,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
             if (ok) xt = scale_rows(TM_Q, p.a.scale * exp2_fast(ht * kLog2e), L::Q);
             wait(L::RL);
 #pragma unroll
-            for (int e = 0; e < NV; ++e) dot = dot8(sh[e], *reinterpret_cast<const uint4 *>(sm + L::X + (tid + 256 * e) * 16), dot);
+            for (int e = 0; e < NV; ++e) dot = dot8(sh[e], *reinterpret_cast<const uint4 *>(sm + L::X + (tid + kGradWork * e) * 16), dot);
             wait(L::CK);
             tc_fence_after_sync();
             if (ok) {
@@ -1369,8 +1370,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
                 // R's last term and V have been multiplied: N and P take their places
                 tmem_wait_st();
 #pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
-                    const int sb = 16 * (2 * k + half);
+                for (int k = 0; k < 2; ++k) {
+                    const int sb = 16 * (4 * k + four);
                     uint32_t pn[16];
                     tmem_ld16(lanes + TM_A + sb, pn);
                     tmem_wait_ld();
@@ -1384,16 +1385,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
                 tc_fence_before_sync();
                 mbar_arrive(&bars[L::READY]);
             }
-            // dg meanwhile, through R lo's place: partial sums by token, A's rows (2
-            // halves of the warps), x, y, A's columns (4 quarters of rows)
+            // dg meanwhile, through R lo's place: partial sums by token, A's rows, x
+            // and y (4 parts of the columns), A's columns (4 quarters of the rows)
             float *part = reinterpret_cast<float *>(sm + L::X);
             meet();
-            part[half * 128 + t] = rowa;
-            part[256 + half * 128 + t] = xt;
-            part[512 + half * 128 + t] = yt;
+            part[four * 128 + t] = rowa;
+            part[512 + four * 128 + t] = xt;
+            part[1024 + four * 128 + t] = yt;
             if (!(lane & 1))
 #pragma unroll
-                for (int k = 0; k < 4; ++k) part[768 + (warp & 3) * 128 + 16 * (2 * k + half) + lane / 2] = cola[k];
+                for (int k = 0; k < 2; ++k) part[1536 + (warp & 3) * 128 + 16 * (4 * k + four) + lane / 2] = cola[k];
 #pragma unroll
             for (int i = 16; i; i >>= 1) dot += __shfl_xor_sync(~0u, dot, i);
             if (lane == 0) red[warp] = dot;
@@ -1404,12 +1405,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float *q = part + 4 * lane + j;
-                    x[j] = (q[256] + q[384]) + ((q[0] + q[128]) - ((q[768] + q[896]) + (q[1024] + q[1152])));
-                    y[j] = q[512] + q[640];
+                    auto four_of = [&](int i) { return (q[i] + q[i + 128]) + (q[i + 256] + q[i + 384]); };
+                    x[j] = four_of(512) + (four_of(0) - four_of(1536));
+                    y[j] = four_of(1024);
                 }
                 float d = 0.f;
 #pragma unroll
-                for (int w = 0; w < 8; ++w) d += red[w];
+                for (int w = 0; w < kGradWork / 32; ++w) d += red[w];
                 d *= whole;
                 mbar_arrive(&bars[L::XFREE]);
                 x[2] += x[3], x[1] += x[2], x[0] += x[1];
@@ -1431,12 +1433,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
             }
             wait(L::DONE);
             tc_fence_after_sync();
-            // the rows of the gradients: bf16 through the tiles Q, K and V, so that
+            // the rows of the gradients: bf16 through the tiles Y, Z and X, so that
             // the stores are whole rows; fp32 (shared heads) straight
             auto rows = [&](uint32_t col, uint32_t tile_at, int d, float *wide, bool both) {
 #pragma unroll 1
-                for (int e = 0; e < d / 2; e += 16) {
-                    const int d0 = half * (d / 2) + e;
+                for (int e = 0; e < d / 4; e += 16) {
+                    const int d0 = four * (d / 4) + e;
                     uint32_t u[16], w[16];
                     tmem_ld16(lanes + col + d0, u);
                     if (both) tmem_ld16(lanes + TM_B + d0, w);
@@ -1463,14 +1465,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
                     }
                 }
             };
+            wait(L::XFREE);
             if (ok) {
 #pragma unroll 1
                 for (int k = 0; k < 2; ++k)
-                    rows(k ? TM_K : TM_Q, k ? L::K : L::Q, DK, shared ? (k ? p.dkh : p.dqh) + wide_row : nullptr, false);
-                rows(TM_A, L::V, DV, nullptr, true);
+                    rows(k ? TM_K : TM_Q, k ? L::Z : L::Y, DK, shared ? (k ? p.dkh : p.dqh) + wide_row : nullptr, false);
+                rows(TM_A, L::X, DV, nullptr, true);
             }
             fence_proxy_async_smem();
             tc_fence_before_sync();
+            if (ok) mbar_arrive(&bars[L::ROWS]);
             meet();
             if (!ok) break;
             if (c.len == kC) {
@@ -1478,11 +1482,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
 #pragma unroll
                     for (int x = 0; x < DK / 64; ++x) {
                         if (shared) break;
-                        tma_store_4d(&m.dq, sm + L::Q + x * 16384, 64 * x, c.t0, hk, c.row);
-                        tma_store_4d(&m.dk, sm + L::K + x * 16384, 64 * x, c.t0, hk, c.row);
+                        tma_store_4d(&m.dq, sm + L::Y + x * 16384, 64 * x, c.t0, hk, c.row);
+                        tma_store_4d(&m.dk, sm + L::Z + x * 16384, 64 * x, c.t0, hk, c.row);
                     }
 #pragma unroll
-                    for (int x = 0; x < DV / 64; ++x) tma_store_4d(&m.dv, sm + L::V + x * 16384, 64 * x, c.t0, h, c.row);
+                    for (int x = 0; x < DV / 64; ++x) tma_store_4d(&m.dv, sm + L::X + x * 16384, 64 * x, c.t0, h, c.row);
                     tma_store_commit();
                     tma_store_wait_read<0>();
                     mbar_arrive(&bars[L::STORED]);
@@ -1490,17 +1494,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
             } else {
                 auto store = [&](T *x, long long step, int d, uint32_t tile_at) {
 #pragma unroll 1
-                    for (int e = tid; e < c.len * (d / 8); e += 256) {
+                    for (int e = tid; e < c.len * (d / 8); e += kGradWork) {
                         const int row = e / (d / 8), col = (e % (d / 8)) * 8;
                         *reinterpret_cast<uint4 *>(x + row * step + col) =
                             *reinterpret_cast<const uint4 *>(sm + tile_at + (col >> 6) * 16384 + sw128_offset(row, col & 63));
                     }
                 };
                 if (!shared) {
-                    store(dq, p.a.sq.t, DK, L::Q);
-                    store(dk, p.a.sk.t, DK, L::K);
+                    store(dq, p.a.sq.t, DK, L::Y);
+                    store(dk, p.a.sk.t, DK, L::Z);
                 }
-                store(dv, p.a.sv.t, DV, L::V);
+                store(dv, p.a.sv.t, DV, L::X);
                 meet();
                 if (tid == 0) mbar_arrive(&bars[L::STORED]);
             }
@@ -1511,7 +1515,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 16) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, 512);
     }
