@@ -149,16 +149,75 @@ __global__ void __launch_bounds__(1024) head_sum_kernel(const float *src, float 
 }
 
 // ------------------------------------------------------------ chunk kernels
+// Tiles have rows of D + 4 floats: 16-byte aligned, and a column of rows spreads
+// over the banks.
 template <int D>
-constexpr int ld() { return D + 1; }
+constexpr int ld() { return D + 4; }
 
-// Rows t < len of a strided [T][D] slice into a [64][D + 1] fp32 tile, zeros after them.
+// acc[i][4 b + j] += sum_{k < K} A(m, k) B(k, n) with m = ty + (NT / 16) i and n =
+// 4 tx + 64 b + j (tx = thread % 16, ty = thread / 16), A[m lda + k] and
+// B[k ldb + n] in shared memory, all read 16 bytes at a time: for four k a
+// warp's 2 x 8 outputs a thread take 18 shared-memory cycles and 64 multiply-adds.
+template <int NT, int TI, int TB>
+__device__ __forceinline__ void mm_kn(float (&acc)[TI][4 * TB], const float *A, int lda, const float *B, int ldb, int K) {
+    constexpr int RS = NT / 16;
+    const float *a0 = A + (threadIdx.x >> 4) * lda, *b0 = B + 4 * (threadIdx.x & 15);
+#pragma unroll 2
+    for (int k = 0; k < K; k += 4) {
+        float4 a[TI];
+#pragma unroll
+        for (int i = 0; i < TI; ++i) a[i] = *reinterpret_cast<const float4 *>(a0 + RS * i * lda + k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float4 b[TB];
+#pragma unroll
+            for (int c = 0; c < TB; ++c) b[c] = *reinterpret_cast<const float4 *>(b0 + (k + e) * ldb + 64 * c);
+#pragma unroll
+            for (int i = 0; i < TI; ++i) {
+                const float x = e == 0 ? a[i].x : e == 1 ? a[i].y : e == 2 ? a[i].z : a[i].w;
+#pragma unroll
+                for (int c = 0; c < TB; ++c) {
+                    acc[i][4 * c] = fmaf(x, b[c].x, acc[i][4 * c]);
+                    acc[i][4 * c + 1] = fmaf(x, b[c].y, acc[i][4 * c + 1]);
+                    acc[i][4 * c + 2] = fmaf(x, b[c].z, acc[i][4 * c + 2]);
+                    acc[i][4 * c + 3] = fmaf(x, b[c].w, acc[i][4 * c + 3]);
+                }
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ float4 ld4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 ld4(const __nv_bfloat16 *p) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ void st4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
+__device__ __forceinline__ void st4(__nv_bfloat16 *p, float4 x) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+    *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+
+// Rows t < len of a strided [T][D] slice into a [64][D + 4] fp32 tile, zeros
+// after them; f(t) scales row t.
+template <typename T, int D, int NT, class F>
+__device__ __forceinline__ void load_tile(float *dst, const T *src, long long step, int len, F f) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < kC * D / 4; i += NT) {
+        const int t = i / (D / 4), d = i % (D / 4) * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < len) {
+            x = ld4(src + t * step + d);
+            const float w = f(t);
+            x.x *= w, x.y *= w, x.z *= w, x.w *= w;
+        }
+        *reinterpret_cast<float4 *>(dst + t * ld<D>() + d) = x;
+    }
+}
 template <typename T, int D, int NT>
 __device__ __forceinline__ void load_tile(float *dst, const T *src, long long step, int len) {
-    for (int i = threadIdx.x; i < kC * D; i += NT) {
-        const int t = i / D, d = i % D;
-        dst[t * ld<D>() + d] = t < len ? tile::ld_f(src + t * step + d) : 0.f;
-    }
+    load_tile<T, D, NT>(dst, src, step, len, [](int) { return 1.f; });
 }
 
 // Zeros in rows t < len of a strided [T][D] slice (tokens of no sequence).
@@ -172,36 +231,46 @@ __device__ __forceinline__ void zero_rows(T *dst, long long step, int len) {
 // Grid (chunks, H); U [chunk][H][DK][DV], decay [chunk][H] = e^G.
 template <typename T, int DK, int DV, bool REV>
 __global__ void __launch_bounds__(256) share_kernel(LinAttnArgs a, View v, float *U, float *decay) {
-    extern __shared__ float sm[];
+    extern __shared__ __align__(16) float sm[];
     float *X = sm, *Y = X + kC * ld<DK>(), *hi = Y + kC * ld<DV>(), *lo = hi + kC, *te = lo + kC;
     const int ci = blockIdx.x, h = blockIdx.y;
     const Chunk c = chunk_at<kC>(v, a.T, ci);
     if (c.len <= 0 || c.seq < 0) return;
     const int hk = h / (a.H / a.Hk);
-    if (threadIdx.x < 32)
-        gates<kC>(gate_ptr(a, c, h), a.sg.t, c.len, a.flags & GDN_G_PER_HEAD, hi, lo, te);
     const T *xp = REV ? at(static_cast<const T *>(a.q), a.sq, c.row, hk, c.t0) : at(static_cast<const T *>(a.k), a.sk, c.row, hk, c.t0);
     const T *yp = REV ? at(static_cast<const T *>(a.dout), a.sdo, c.row, h, c.t0) : at(static_cast<const T *>(a.v), a.sv, c.row, h, c.t0);
-    load_tile<T, DK, 256>(X, xp, REV ? a.sq.t : a.sk.t, c.len);
+    if (threadIdx.x < 32) gates<kC>(gate_ptr(a, c, h), a.sg.t, c.len, a.flags & GDN_G_PER_HEAD, hi, lo, te);
     load_tile<T, DV, 256>(Y, yp, REV ? a.sdo.t : a.sv.t, c.len);
     __syncthreads();
-    for (int i = threadIdx.x; i < kC * DK; i += 256) {
-        const int t = i / DK;
-        X[t * ld<DK>() + i % DK] *= REV ? a.scale * expf(hi[t]) : expf(te[t]);
-    }
+    load_tile<T, DK, 256>(X, xp, REV ? a.sq.t : a.sk.t, c.len, [&](int t) { return REV ? a.scale * expf(hi[t]) : expf(te[t]); });
     __syncthreads();
-    float acc[DK / 16][DV / 16];
+    // rows 4 ty + 64 i.., columns 4 tx + 64 j..: four and four at a time
+    constexpr int MB = DK / 64, NB = DV / 64;
+    float acc[4 * MB][4 * NB];
 #pragma unroll
-    for (int i = 0; i < DK / 16; ++i)
+    for (int i = 0; i < 4 * MB; ++i)
 #pragma unroll
-        for (int j = 0; j < DV / 16; ++j) acc[i][j] = 0.f;
-    tile::mm<256, DK / 16, DV / 16>(acc, X, 1, ld<DK>(), Y, ld<DV>(), 1, kC);
-    float *u = U + ((long long)ci * a.H + h) * DK * DV;
+        for (int j = 0; j < 4 * NB; ++j) acc[i][j] = 0.f;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll 4
+    for (int t = 0; t < kC; ++t) {
+        float x[4 * MB], y[4 * NB];
 #pragma unroll
-    for (int i = 0; i < DK / 16; ++i)
+        for (int i = 0; i < MB; ++i) *reinterpret_cast<float4 *>(x + 4 * i) = ld4(X + t * ld<DK>() + 4 * ty + 64 * i);
 #pragma unroll
-        for (int j = 0; j < DV / 16; ++j) u[(ty + 16 * i) * DV + tx + 16 * j] = acc[i][j];
+        for (int j = 0; j < NB; ++j) *reinterpret_cast<float4 *>(y + 4 * j) = ld4(Y + t * ld<DV>() + 4 * tx + 64 * j);
+#pragma unroll
+        for (int i = 0; i < 4 * MB; ++i)
+#pragma unroll
+            for (int j = 0; j < 4 * NB; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+    }
+    float *u = U + ((long long)ci * a.H + h) * DK * DV;
+#pragma unroll
+    for (int i = 0; i < 4 * MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            st4(u + (4 * ty + 64 * (i / 4) + i % 4) * DV + 4 * tx + 64 * j,
+                make_float4(acc[i][4 * j], acc[i][4 * j + 1], acc[i][4 * j + 2], acc[i][4 * j + 3]));
     if (threadIdx.x == 0) decay[(long long)ci * a.H + h] = expf(hi[c.len - 1]);
 }
 
@@ -245,18 +314,34 @@ __global__ void __launch_bounds__(256) scan_kernel(View v, float *U, const float
 }
 
 constexpr int kT = tile::kThr;  // 512
+constexpr int kP = kC + 4;      // rows of a [64][64] tile
+constexpr int kSlab = 68;       // rows of 64 columns of a state
+
+// Columns j0 .. j0 + 63 of a [DK][DV] state into [DK][68] (its rows) ..
+template <int DK, int DV>
+__device__ __forceinline__ void load_slab(float *dst, const float *S, int j0) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < DK * 16; i += kT) st4(dst + (i >> 4) * kSlab + (i & 15) * 4, ld4(S + (i >> 4) * DV + j0 + (i & 15) * 4));
+}
+// .. or transposed into [64][DK + 4].
+template <int DK, int DV>
+__device__ __forceinline__ void load_slab_t(float *dst, const float *S, int j0) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < DK * 64; i += kT) dst[(i & 63) * ld<DK>() + (i >> 6)] = S[(i >> 6) * DV + j0 + (i & 63)];
+}
 
 // A chunk's outputs.  Grid (chunks, H); S as scan_kernel left it.
 template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(kT) out_kernel(LinAttnArgs a, View v, const float *S) {
-    extern __shared__ float sm[];
-    float *Q = sm, *K = Q + kC * ld<DK>(), *V = K + kC * ld<DK>(), *P = V + kC * ld<DV>();
-    float *hi = P + kC * (kC + 1), *lo = hi + kC, *te = lo + kC;
+    extern __shared__ __align__(16) float sm[];
+    float *Q = sm, *K = Q + kC * ld<DK>(), *V = K + kC * ld<DK>(), *P = V + kC * ld<DV>(), *slab = P + kC * kP;
+    float *hi = slab + DK * kSlab, *lo = hi + kC, *te = lo + kC;
     const int ci = blockIdx.x, h = blockIdx.y;
     const Chunk c = chunk_at<kC>(v, a.T, ci);
     if (c.len <= 0) return;
+    T *out = at(static_cast<T *>(a.o), a.so, c.row, h, c.t0);
     if (c.seq < 0) {
-        zero_rows<T, DV, kT>(at(static_cast<T *>(a.o), a.so, c.row, h, c.t0), a.so.t, c.len);
+        zero_rows<T, DV, kT>(out, a.so.t, c.len);
         return;
     }
     const int hk = h / (a.H / a.Hk);
@@ -265,35 +350,38 @@ __global__ void __launch_bounds__(kT) out_kernel(LinAttnArgs a, View v, const fl
     load_tile<T, DK, kT>(Q, at(static_cast<const T *>(a.q), a.sq, c.row, hk, c.t0), a.sq.t, c.len);
     load_tile<T, DK, kT>(K, at(static_cast<const T *>(a.k), a.sk, c.row, hk, c.t0), a.sk.t, c.len);
     load_tile<T, DV, kT>(V, at(static_cast<const T *>(a.v), a.sv, c.row, h, c.t0), a.sv.t, c.len);
+    const float *Sc = S + ((long long)ci * a.H + h) * DK * DV;
+    load_slab<DK, DV>(slab, Sc, 0);
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     float p[2][4] = {};
-    tile::mm<kT, 2, 4>(p, Q, ld<DK>(), 1, K, 1, ld<DK>(), DK);
+    tile::mm_nt<kT, 2, 4>(p, Q, ld<DK>(), K, ld<DK>(), DK);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int t = ty + 32 * i, s = tx + 16 * j;
-            P[t * (kC + 1) + s] = s <= t ? p[i][j] * decay_between(hi[t], lo[t], hi[s], lo[s]) : 0.f;
+            P[t * kP + s] = s <= t ? p[i][j] * decay_between(hi[t], lo[t], hi[s], lo[s]) : 0.f;
         }
-    float o[2][DV / 16];
+    for (int j0 = 0; j0 < DV; j0 += 64) {
+        if (j0 > 0) {
+            __syncthreads();
+            load_slab<DK, DV>(slab, Sc, j0);
+        }
+        __syncthreads();
+        float o[2][4] = {};
+        mm_kn<kT, 2, 1>(o, Q, ld<DK>(), slab, kSlab, DK);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < DV / 16; ++j) o[i][j] = 0.f;
-    tile::mm<kT, 2, DV / 16>(o, Q, ld<DK>(), 1, S + ((long long)ci * a.H + h) * DK * DV, DV, 1, DK);
+            for (int j = 0; j < 4; ++j) o[i][j] *= expf(hi[ty + 32 * i]);
+        mm_kn<kT, 2, 1>(o, P, kP, V + j0, ld<DV>(), kC);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < DV / 16; ++j) o[i][j] *= expf(hi[ty + 32 * i]);
-    __syncthreads();
-    tile::mm<kT, 2, DV / 16>(o, P, kC + 1, 1, V, ld<DV>(), 1, kC);
-    T *out = at(static_cast<T *>(a.o), a.so, c.row, h, c.t0);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < DV / 16; ++j)
-            if (ty + 32 * i < c.len) tile::st_f(out + (ty + 32 * i) * a.so.t + tx + 16 * j, a.scale * o[i][j]);
+        for (int i = 0; i < 2; ++i)
+            if (ty + 32 * i < c.len)
+                st4(out + (ty + 32 * i) * a.so.t + j0 + 4 * tx,
+                    make_float4(a.scale * o[i][0], a.scale * o[i][1], a.scale * o[i][2], a.scale * o[i][3]));
+    }
 }
 
 // Sum over the 16 threads of a tile row; every one of them gets it.
@@ -308,25 +396,29 @@ __device__ __forceinline__ float row16(float x) {
 template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(kT) grad_kernel(LinAttnArgs a, View v, const float *S, const float *R, float *dqh,
                                                   float *dkh, float *dgt, Strides sdg) {
-    extern __shared__ float sm[];
+    extern __shared__ __align__(16) float sm[];
     float *Q = sm, *K = Q + kC * ld<DK>(), *V = K + kC * ld<DK>(), *O = V + kC * ld<DV>();
-    float *P = O + kC * ld<DV>(), *N = P + kC * (kC + 1), *slab = N + kC * (kC + 1);  // slab [DK][65]
-    float *hi = slab + DK * 65, *lo = hi + kC, *te = lo + kC, *xq = te + kC, *xk = xq + kC, *xr = xk + kC, *xa = xr + kC, *red = xa + kC;
+    // P by columns (P^T dO), N by rows and columns (N K, N^T Q); a slab of a state
+    float *PT = O + kC * ld<DV>(), *N = PT + kC * kP, *NT = N + kC * kP, *slab = NT + kC * kP;
+    constexpr int kSlabFloats = DK * kSlab > 64 * ld<DK>() ? DK * kSlab : 64 * ld<DK>();
+    float *hi = slab + kSlabFloats, *lo = hi + kC, *te = lo + kC, *xq = te + kC, *xk = xq + kC, *xr = xk + kC, *xa = xr + kC, *red = xa + kC;
     const int ci = blockIdx.x, h = blockIdx.y;
     const Chunk c = chunk_at<kC>(v, a.T, ci);
     if (c.len <= 0) return;
     const int hk = h / (a.H / a.Hk);
     const bool shared = a.H != a.Hk;
     const long long out_row = (((long long)c.row * a.H + h) * a.T + c.t0) * DK;
+    T *dq = at(static_cast<T *>(a.dq), a.sq, c.row, hk, c.t0), *dk = at(static_cast<T *>(a.dk), a.sk, c.row, hk, c.t0);
+    T *dv = at(static_cast<T *>(a.dv), a.sv, c.row, h, c.t0);
     if (c.seq < 0) {
         if (shared) {
             zero_rows<float, DK, kT>(dqh + out_row, DK, c.len);
             zero_rows<float, DK, kT>(dkh + out_row, DK, c.len);
         } else {
-            zero_rows<T, DK, kT>(at(static_cast<T *>(a.dq), a.sq, c.row, hk, c.t0), a.sq.t, c.len);
-            zero_rows<T, DK, kT>(at(static_cast<T *>(a.dk), a.sk, c.row, hk, c.t0), a.sk.t, c.len);
+            zero_rows<T, DK, kT>(dq, a.sq.t, c.len);
+            zero_rows<T, DK, kT>(dk, a.sk.t, c.len);
         }
-        zero_rows<T, DV, kT>(at(static_cast<T *>(a.dv), a.sv, c.row, h, c.t0), a.sv.t, c.len);
+        zero_rows<T, DV, kT>(dv, a.sv.t, c.len);
         zero_rows<float, 1, kT>(at(dgt, sdg, c.row, h, c.t0), sdg.t, c.len);
         return;
     }
@@ -341,17 +433,19 @@ __global__ void __launch_bounds__(kT) grad_kernel(LinAttnArgs a, View v, const f
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     {
         float p[2][4] = {}, n[2][4] = {};
-        tile::mm<kT, 2, 4>(p, Q, ld<DK>(), 1, K, 1, ld<DK>(), DK);
-        tile::mm<kT, 2, 4>(n, O, ld<DV>(), 1, V, 1, ld<DV>(), DV);
+        tile::mm_nt<kT, 2, 4>(p, Q, ld<DK>(), K, ld<DK>(), DK);
+        tile::mm_nt<kT, 2, 4>(n, O, ld<DV>(), V, ld<DV>(), DV);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int t = ty + 32 * i, s = tx + 16 * j;
                 const float f = s <= t ? a.scale * decay_between(hi[t], lo[t], hi[s], lo[s]) : 0.f;
-                P[t * (kC + 1) + s] = s <= t ? p[i][j] * f : 0.f;
-                N[t * (kC + 1) + s] = s <= t ? n[i][j] * f : 0.f;
-                slab[t * 65 + s] = s < t ? p[i][j] * (n[i][j] * f) : 0.f;  // A
+                const float nn = s <= t ? n[i][j] * f : 0.f;
+                PT[s * kP + t] = s <= t ? p[i][j] * f : 0.f;
+                N[t * kP + s] = nn;
+                NT[s * kP + t] = nn;
+                slab[t * 65 + s] = s < t ? p[i][j] * nn : 0.f;  // A
             }
     }
     __syncthreads();
@@ -362,105 +456,87 @@ __global__ void __launch_bounds__(kT) grad_kernel(LinAttnArgs a, View v, const f
         for (int s = 0; s < kC; ++s) x += rows ? slab[t * 65 + s] : slab[s * 65 + t];
         (rows ? xa : xk)[t] = x;
     }
-    // dq: the part through S over its columns in slabs of 64, then the chunk's own
-    {
-        float acc[2][DK / 16];
+    constexpr int NB = DK / 64;
+    // row sums of x against the rows of a tile
+    auto along = [&](const float (&x)[2][4 * NB], const float *tile_, float *to) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float y = 0.f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const float4 q = ld4(tile_ + (ty + 32 * i) * ld<DK>() + 4 * tx + 64 * b);
+                y = fmaf(q.x, x[i][4 * b], fmaf(q.y, x[i][4 * b + 1], fmaf(q.z, x[i][4 * b + 2], fmaf(q.w, x[i][4 * b + 3], y))));
+            }
+            y = row16(y);
+            if (tx == 0) to[ty + 32 * i] = y;
+        }
+    };
+    auto put = [&](const float (&x)[2][4 * NB], T *to, long long step, float *wide) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < DK / 16; ++j) acc[i][j] = 0.f;
-        for (int j0 = 0; j0 < DV; j0 += 64) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < DK * 64; i += kT) slab[(i >> 6) * 65 + (i & 63)] = Sc[(i >> 6) * DV + j0 + (i & 63)];
-            __syncthreads();
-            tile::mm<kT, 2, DK / 16>(acc, O + j0, ld<DV>(), 1, slab, 1, 65, 64);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < DK / 16; ++j) acc[i][j] *= a.scale * expf(hi[ty + 32 * i]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float x = 0.f;
-#pragma unroll
-            for (int j = 0; j < DK / 16; ++j) x = fmaf(Q[(ty + 32 * i) * ld<DK>() + tx + 16 * j], acc[i][j], x);
-            x = row16(x);
-            if (tx == 0) xq[ty + 32 * i] = x;
-        }
-        tile::mm<kT, 2, DK / 16>(acc, N, kC + 1, 1, K, ld<DK>(), 1, kC);
-        T *dq = at(static_cast<T *>(a.dq), a.sq, c.row, hk, c.t0);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = ty + 32 * i;
-#pragma unroll
-            for (int j = 0; j < DK / 16; ++j) {
-                const int d = tx + 16 * j;
+            for (int b = 0; b < NB; ++b) {
+                const int t = ty + 32 * i, d = 4 * tx + 64 * b;
+                const float4 y = make_float4(x[i][4 * b], x[i][4 * b + 1], x[i][4 * b + 2], x[i][4 * b + 3]);
                 if (t < c.len) {
-                    if (shared) dqh[out_row + (long long)t * DK + d] = acc[i][j];
-                    else tile::st_f(dq + t * a.sq.t + d, acc[i][j]);
+                    if (shared) st4(wide + out_row + (long long)t * DK + d, y);
+                    else st4(to + t * step + d, y);
                 }
             }
-        }
-    }
-    // dk and dv, with R in the same slabs; <R, S> on the way
-    float dot = 0.f;
+    };
+    // dq: the part through S over its columns in slabs of 64, then the chunk's own
     {
-        float acc[2][DK / 16];
+        float acc[2][4 * NB] = {};
+        for (int j0 = 0; j0 < DV; j0 += 64) {
+            __syncthreads();
+            load_slab_t<DK, DV>(slab, Sc, j0);
+            __syncthreads();
+            mm_kn<kT, 2, NB>(acc, O + j0, ld<DV>(), slab, ld<DK>(), 64);
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < DK / 16; ++j) acc[i][j] = 0.f;
-        T *dv = at(static_cast<T *>(a.dv), a.sv, c.row, h, c.t0);
+            for (int j = 0; j < 4 * NB; ++j) acc[i][j] *= a.scale * expf(hi[ty + 32 * i]);
+        along(acc, Q, xq);
+        mm_kn<kT, 2, NB>(acc, N, kP, K, ld<DK>(), kC);
+        put(acc, dq, a.sq.t, dqh);
+    }
+    // dk and dv, with R in the same slabs, both ways round; <R, S> on the way
+    float dot = 0.f;
+    {
+        float acc[2][4 * NB] = {};
         for (int j0 = 0; j0 < DV; j0 += 64) {
             __syncthreads();
-            for (int i = threadIdx.x; i < DK * 64; i += kT) {
-                const float r = Rc[(i >> 6) * DV + j0 + (i & 63)];
-                slab[(i >> 6) * 65 + (i & 63)] = r;
-                dot = fmaf(r, Sc[(i >> 6) * DV + j0 + (i & 63)], dot);
+            load_slab_t<DK, DV>(slab, Rc, j0);
+            __syncthreads();
+            mm_kn<kT, 2, NB>(acc, V + j0, ld<DV>(), slab, ld<DK>(), 64);
+            __syncthreads();
+#pragma unroll 4
+            for (int i = threadIdx.x; i < DK * 16; i += kT) {
+                const float4 r = ld4(Rc + (i >> 4) * DV + j0 + (i & 15) * 4), s = ld4(Sc + (i >> 4) * DV + j0 + (i & 15) * 4);
+                st4(slab + (i >> 4) * kSlab + (i & 15) * 4, r);
+                dot = fmaf(r.x, s.x, fmaf(r.y, s.y, fmaf(r.z, s.z, fmaf(r.w, s.w, dot))));
             }
             __syncthreads();
-            tile::mm<kT, 2, DK / 16>(acc, V + j0, ld<DV>(), 1, slab, 1, 65, 64);
             float w[2][4] = {};
-            tile::mm<kT, 2, 4>(w, K, ld<DK>(), 1, slab, 65, 1, DK);
+            mm_kn<kT, 2, 1>(w, K, ld<DK>(), slab, kSlab, DK);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w[i][j] *= expf(te[ty + 32 * i]);
-            tile::mm<kT, 2, 4>(w, P, 1, kC + 1, O + j0, ld<DV>(), 1, kC);
+            mm_kn<kT, 2, 1>(w, PT, kP, O + j0, ld<DV>(), kC);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (ty + 32 * i < c.len) tile::st_f(dv + (ty + 32 * i) * a.sv.t + j0 + tx + 16 * j, w[i][j]);
+                if (ty + 32 * i < c.len)
+                    st4(dv + (ty + 32 * i) * a.sv.t + j0 + 4 * tx, make_float4(w[i][0], w[i][1], w[i][2], w[i][3]));
         }
-        float own[2][DK / 16];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = ty + 32 * i;
-            float x = 0.f;
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < DK / 16; ++j) {
-                own[i][j] = 0.f;
-                acc[i][j] *= expf(te[t]);
-                x = fmaf(K[t * ld<DK>() + tx + 16 * j], acc[i][j], x);
-            }
-            x = row16(x);
-            if (tx == 0) xr[t] = x;
-        }
-        tile::mm<kT, 2, DK / 16>(own, N, 1, kC + 1, Q, ld<DK>(), 1, kC);
-        T *dk = at(static_cast<T *>(a.dk), a.sk, c.row, hk, c.t0);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = ty + 32 * i;
-#pragma unroll
-            for (int j = 0; j < DK / 16; ++j) {
-                const int d = tx + 16 * j;
-                if (t < c.len) {
-                    if (shared) dkh[out_row + (long long)t * DK + d] = acc[i][j] + own[i][j];
-                    else tile::st_f(dk + t * a.sk.t + d, acc[i][j] + own[i][j]);
-                }
-            }
-        }
+            for (int j = 0; j < 4 * NB; ++j) acc[i][j] *= expf(te[ty + 32 * i]);
+        along(acc, K, xr);
+        mm_kn<kT, 2, NB>(acc, NT, kP, Q, ld<DK>(), kC);
+        put(acc, dk, a.sk.t, dkh);
     }
 #pragma unroll
     for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(~0u, dot, m);
@@ -511,7 +587,7 @@ int run_states(const LinAttnArgs &a, const View &v, float *U, float *decay, cuda
 template <typename T, int DK, int DV>
 int run_fwd(const LinAttnArgs &a, const View &v, float *U, float *decay, cudaStream_t stream) {
     LA_TRY((run_states<T, DK, DV, false>(a, v, U, decay, stream)));
-    const int smem = 4 * (kC * (2 * ld<DK>() + ld<DV>() + kC + 1) + 3 * kC);
+    const int smem = 4 * (kC * (2 * ld<DK>() + ld<DV>() + kP) + DK * kSlab + 3 * kC);
     LA_TRY(smem_limit(out_kernel<T, DK, DV>, smem));
     out_kernel<T, DK, DV><<<dim3(v.n_chunks, a.H), kT, smem, stream>>>(a, v, U);
     return launched();
@@ -542,7 +618,8 @@ template <typename T, int DK, int DV>
 int run_bwd(const LinAttnArgs &a, const View &v, const BwdWs &w, cudaStream_t stream) {
     LA_TRY((run_states<T, DK, DV, false>(a, v, w.U, w.decay, stream)));
     LA_TRY((run_states<T, DK, DV, true>(a, v, w.R, w.decay, stream)));
-    const int smem = 4 * (kC * (2 * ld<DK>() + 2 * ld<DV>() + 2 * (kC + 1)) + DK * 65 + 7 * kC + 32);
+    constexpr int slab = DK * kSlab > 64 * ld<DK>() ? DK * kSlab : 64 * ld<DK>();
+    const int smem = 4 * (kC * (2 * ld<DK>() + 2 * ld<DV>() + 3 * kP) + slab + 7 * kC + 32);
     LA_TRY(smem_limit(grad_kernel<T, DK, DV>, smem));
     const bool per_head = a.flags & GDN_G_PER_HEAD;
     const Strides whole{(long long)a.H * a.T, a.T, 1};
