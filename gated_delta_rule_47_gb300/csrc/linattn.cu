@@ -104,17 +104,22 @@ __global__ void __launch_bounds__(kTableThreads) table_kernel(const int *cu, int
     }
 }
 
-// dst[b,hk,t,:] = sum of src[b,h,t,:] over hk's value heads, in their order.
+// dq[b,hk,t,:] = sum of the value heads' shares dqh[b,h,t,:], in their order,
+// and the same for dk: the second half of grid.x.
 template <typename T>
-__global__ void group_sum_kernel(const float4 *src, T *dst, Strides s, int H, int Hk, int T_len, int D) {
-    const int per = D / 4, rep = H / Hk;
-    const long long n = (long long)T_len * per;
+__global__ void group_sum_kernel(LinAttnArgs a, const float4 *dqh, const float4 *dkh) {
+    const int per = a.Dk / 4, rep = a.H / a.Hk, blocks = gridDim.x / 2;
+    const bool key = blockIdx.x >= blocks;
+    const long long n = (long long)a.T * per;
     const int hk = blockIdx.y, b = blockIdx.z;
-    for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
+    const float4 *src = key ? dkh : dqh;
+    const Strides &s = key ? a.sk : a.sq;
+    T *dst = static_cast<T *>(key ? a.dk : a.dq);
+    for (long long i = (key ? blockIdx.x - blocks : blockIdx.x) * (long long)blockDim.x + threadIdx.x; i < n; i += (long long)blocks * blockDim.x) {
         const int t = (int)(i / per), c = (int)(i - (long long)t * per);
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int r = 0; r < rep; ++r) {
-            const float4 y = src[(((long long)b * H + hk * rep + r) * T_len + t) * per + c];
+            const float4 y = src[(((long long)b * a.H + hk * rep + r) * a.T + t) * per + c];
             x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
         }
         T *p = at(dst, s, b, hk, t) + 4 * c;
@@ -226,23 +231,25 @@ __device__ __forceinline__ void zero_rows(T *dst, long long step, int len) {
     for (int i = threadIdx.x; i < len * D; i += NT) tile::st_f(dst + (i / D) * step + i % D, 0.f);
 }
 
-// A chunk's share of the state that leaves it, sum_t e^{G-c_t} k_t v_t^T, or
-// (REV) of the gradient before it, scale sum_t e^{c_t} q_t do_t^T.
-// Grid (chunks, H); U [chunk][H][DK][DV], decay [chunk][H] = e^G.
-template <typename T, int DK, int DV, bool REV>
-__global__ void __launch_bounds__(256) share_kernel(LinAttnArgs a, View v, float *U, float *decay) {
+// A chunk's share of the state that leaves it, sum_t e^{G-c_t} k_t v_t^T (to
+// U), and of the gradient before it, scale sum_t e^{c_t} q_t do_t^T (to R).
+// Grid (chunks, H, 1 or, for the backward, 2); U, R [chunk][H][DK][DV],
+// decay [chunk][H] = e^G.
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(256) share_kernel(LinAttnArgs a, View v, float *U, float *R, float *decay) {
+    const bool rev = blockIdx.z;
     extern __shared__ __align__(16) float sm[];
     float *X = sm, *Y = X + kC * ld<DK>(), *hi = Y + kC * ld<DV>(), *lo = hi + kC, *te = lo + kC;
     const int ci = blockIdx.x, h = blockIdx.y;
     const Chunk c = chunk_at<kC>(v, a.T, ci);
     if (c.len <= 0 || c.seq < 0) return;
     const int hk = h / (a.H / a.Hk);
-    const T *xp = REV ? at(static_cast<const T *>(a.q), a.sq, c.row, hk, c.t0) : at(static_cast<const T *>(a.k), a.sk, c.row, hk, c.t0);
-    const T *yp = REV ? at(static_cast<const T *>(a.dout), a.sdo, c.row, h, c.t0) : at(static_cast<const T *>(a.v), a.sv, c.row, h, c.t0);
+    const T *xp = rev ? at(static_cast<const T *>(a.q), a.sq, c.row, hk, c.t0) : at(static_cast<const T *>(a.k), a.sk, c.row, hk, c.t0);
+    const T *yp = rev ? at(static_cast<const T *>(a.dout), a.sdo, c.row, h, c.t0) : at(static_cast<const T *>(a.v), a.sv, c.row, h, c.t0);
     if (threadIdx.x < 32) gates<kC>(gate_ptr(a, c, h), a.sg.t, c.len, a.flags & GDN_G_PER_HEAD, hi, lo, te);
-    load_tile<T, DV, 256>(Y, yp, REV ? a.sdo.t : a.sv.t, c.len);
+    load_tile<T, DV, 256>(Y, yp, rev ? a.sdo.t : a.sv.t, c.len);
     __syncthreads();
-    load_tile<T, DK, 256>(X, xp, REV ? a.sq.t : a.sk.t, c.len, [&](int t) { return REV ? a.scale * expf(hi[t]) : expf(te[t]); });
+    load_tile<T, DK, 256>(X, xp, rev ? a.sq.t : a.sk.t, c.len, [&](int t) { return rev ? a.scale * expf(hi[t]) : expf(te[t]); });
     __syncthreads();
     // rows 4 ty + 64 i.., columns 4 tx + 64 j..: four and four at a time
     constexpr int MB = DK / 64, NB = DV / 64;
@@ -264,32 +271,36 @@ __global__ void __launch_bounds__(256) share_kernel(LinAttnArgs a, View v, float
 #pragma unroll
             for (int j = 0; j < 4 * NB; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
     }
-    float *u = U + ((long long)ci * a.H + h) * DK * DV;
+    float *u = (rev ? R : U) + ((long long)ci * a.H + h) * DK * DV;
 #pragma unroll
     for (int i = 0; i < 4 * MB; ++i)
 #pragma unroll
         for (int j = 0; j < NB; ++j)
             st4(u + (4 * ty + 64 * (i / 4) + i % 4) * DV + 4 * tx + 64 * j,
                 make_float4(acc[i][4 * j], acc[i][4 * j + 1], acc[i][4 * j + 2], acc[i][4 * j + 3]));
-    if (threadIdx.x == 0) decay[(long long)ci * a.H + h] = expf(hi[c.len - 1]);
+    if (!rev && threadIdx.x == 0) decay[(long long)ci * a.H + h] = expf(hi[c.len - 1]);
 }
 
 // Turns the shares of a sequence's chunks into the states that enter them
-// (forwards, from s0; the last one to sf), or (REV) into the gradients of the
-// states that leave them (backwards, from dsf; the last one to ds0).
-// Grid (page / 1024, H, n_seq), a thread for four elements.
-template <bool REV>
-__global__ void __launch_bounds__(256) scan_kernel(View v, float *U, const float *decay, const float *start,
-                                                   float *end, int H, int page) {
-    const int e = (blockIdx.x * 256 + threadIdx.x) * 4, h = blockIdx.y, s = blockIdx.z;
+// (forwards, from s0; the last one to sf), and into the gradients of the states
+// that leave them (backwards, from dsf; the last one to ds0).
+// Grid (blocks of a page, H, n_seq), twice as many blocks for both; a thread
+// takes four elements.
+__global__ void __launch_bounds__(256) scan_kernel(LinAttnArgs a, View v, float *U, float *R, const float *decay, int page,
+                                                   int blocks) {
+    const bool rev = blockIdx.x >= blocks;
+    const int e = ((rev ? blockIdx.x - blocks : blockIdx.x) * 256 + threadIdx.x) * 4, H = a.H, h = blockIdx.y, s = blockIdx.z;
     if (e >= page) return;
+    if (rev) U = R;
+    const float *start = rev ? a.dsf : a.s0;
+    float *end = rev ? a.ds0 : a.sf;
     const int2 q = seq_at(v, s);
     const long long mine = ((long long)s * H + h) * page + e;
     float4 x = start ? *reinterpret_cast<const float4 *>(start + mine) : make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int A = 4;  // chunks read ahead
     float4 u[A];
     float d[A];
-    auto slot = [&](int i) { return ((long long)(q.x + (REV ? q.y - 1 - i : i)) * H + h); };
+    auto slot = [&](int i) { return ((long long)(q.x + (rev ? q.y - 1 - i : i)) * H + h); };
 #pragma unroll
     for (int j = 0; j < A; ++j)
         if (j < q.y) {
@@ -573,20 +584,20 @@ int launched() {
         if (st_ != GDN_OK) return st_;  \
     } while (0)
 
-template <typename T, int DK, int DV, bool REV>
-int run_states(const LinAttnArgs &a, const View &v, float *U, float *decay, cudaStream_t stream) {
-    const int smem = 4 * (kC * (ld<DK>() + ld<DV>()) + 3 * kC);
-    LA_TRY(smem_limit(share_kernel<T, DK, DV, REV>, smem));
-    share_kernel<T, DK, DV, REV><<<dim3(v.n_chunks, a.H), 256, smem, stream>>>(a, v, U, decay);
+// The states that enter the chunks, to U; with R also their gradients.
+template <typename T, int DK, int DV>
+int run_states(const LinAttnArgs &a, const View &v, float *U, float *R, float *decay, cudaStream_t stream) {
+    const int smem = 4 * (kC * (ld<DK>() + ld<DV>()) + 3 * kC), both = R ? 2 : 1, blocks = (DK * DV + 1023) / 1024;
+    LA_TRY(smem_limit(share_kernel<T, DK, DV>, smem));
+    share_kernel<T, DK, DV><<<dim3(v.n_chunks, a.H, both), 256, smem, stream>>>(a, v, U, R, decay);
     LA_TRY(launched());
-    scan_kernel<REV><<<dim3((DK * DV + 1023) / 1024, a.H, a.n_seq), 256, 0, stream>>>(
-        v, U, decay, REV ? a.dsf : a.s0, REV ? a.ds0 : a.sf, a.H, DK * DV);
+    scan_kernel<<<dim3(both * blocks, a.H, a.n_seq), 256, 0, stream>>>(a, v, U, R, decay, DK * DV, blocks);
     return launched();
 }
 
 template <typename T, int DK, int DV>
 int run_fwd(const LinAttnArgs &a, const View &v, float *U, float *decay, cudaStream_t stream) {
-    LA_TRY((run_states<T, DK, DV, false>(a, v, U, decay, stream)));
+    LA_TRY((run_states<T, DK, DV>(a, v, U, nullptr, decay, stream)));
     const int smem = 4 * (kC * (2 * ld<DK>() + ld<DV>() + kP) + DK * kSlab + 3 * kC);
     LA_TRY(smem_limit(out_kernel<T, DK, DV>, smem));
     out_kernel<T, DK, DV><<<dim3(v.n_chunks, a.H), kT, smem, stream>>>(a, v, U);
@@ -616,8 +627,7 @@ BwdWs bwd_ws(const LinAttnArgs &a, void *ws) {
 
 template <typename T, int DK, int DV>
 int run_bwd(const LinAttnArgs &a, const View &v, const BwdWs &w, cudaStream_t stream) {
-    LA_TRY((run_states<T, DK, DV, false>(a, v, w.U, w.decay, stream)));
-    LA_TRY((run_states<T, DK, DV, true>(a, v, w.R, w.decay, stream)));
+    LA_TRY((run_states<T, DK, DV>(a, v, w.U, w.R, w.decay, stream)));
     constexpr int slab = DK * kSlab > 64 * ld<DK>() ? DK * kSlab : 64 * ld<DK>();
     const int smem = 4 * (kC * (2 * ld<DK>() + 2 * ld<DV>() + 3 * kP) + slab + 7 * kC + 32);
     LA_TRY(smem_limit(grad_kernel<T, DK, DV>, smem));
@@ -653,12 +663,12 @@ int make_view(const LinAttnArgs &a, int C, void *ws, View *v, cudaStream_t strea
     return launched();
 }
 
-int launch_group_sum(const float *src, void *dst, const Strides &s, int B, int H, int Hk, int T, int D, int dtype,
-                     cudaStream_t stream) {
-    const long long n = (long long)T * D / 4;
-    const dim3 grid((unsigned)(n < 256 * 1024 ? (n + 255) / 256 : 1024), Hk, B);
-    if (dtype == GDN_BF16) group_sum_kernel<<<grid, 256, 0, stream>>>(reinterpret_cast<const float4 *>(src), static_cast<__nv_bfloat16 *>(dst), s, H, Hk, T, D);
-    else group_sum_kernel<<<grid, 256, 0, stream>>>(reinterpret_cast<const float4 *>(src), static_cast<float *>(dst), s, H, Hk, T, D);
+int launch_group_sum(const LinAttnArgs &a, const float *dqh, const float *dkh, cudaStream_t stream) {
+    const long long n = (long long)a.T * a.Dk / 4;
+    const dim3 grid(2 * (unsigned)(n < 256 * 1024 ? (n + 255) / 256 : 1024), a.Hk, a.B);
+    const float4 *q = reinterpret_cast<const float4 *>(dqh), *k = reinterpret_cast<const float4 *>(dkh);
+    if (a.dtype == GDN_BF16) group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, q, k);
+    else group_sum_kernel<float><<<grid, 256, 0, stream>>>(a, q, k);
     return launched();
 }
 
@@ -691,10 +701,7 @@ int launch_linattn_bwd(const LinAttnArgs &a, cudaStream_t stream) {
     const bool shared = a.H != a.Hk, per_head = a.flags & GDN_G_PER_HEAD;
     const BwdWs w = bwd_ws(a, a.ws);
     LA_TRY(a.dtype == GDN_BF16 ? bwd_t<__nv_bfloat16>(a, v, w, stream) : bwd_t<float>(a, v, w, stream));
-    if (shared) {
-        LA_TRY(launch_group_sum(w.dqh, a.dq, a.sq, a.B, a.H, a.Hk, a.T, a.Dk, a.dtype, stream));
-        LA_TRY(launch_group_sum(w.dkh, a.dk, a.sk, a.B, a.H, a.Hk, a.T, a.Dk, a.dtype, stream));
-    }
+    if (shared) LA_TRY(launch_group_sum(a, w.dqh, w.dkh, stream));
     if (per_head) LA_TRY(launch_head_sum(w.dgt, a.dg, a.B, a.H, a.T, stream));
     return GDN_OK;
 }

@@ -165,10 +165,9 @@ __device__ __forceinline__ T *at(T *p, const Strides &s, int row, int h, int t) 
     return p + row * s.b + h * s.h + t * s.t;
 }
 
-// Sums the value heads' shares of the shared heads' gradients: dst (strided,
-// the tensors' type) [B,Hk,T,D] from src [B,H,T,D] fp32.
-int launch_group_sum(const float *src, void *dst, const Strides &s, int B, int H, int Hk, int T, int D, int dtype,
-                     cudaStream_t stream);
+// Sums the value heads' shares [B,H,T,Dk] fp32 of the shared heads' gradients
+// into dq and dk (strided, the tensors' type).
+int launch_group_sum(const LinAttnArgs &a, const float *dqh, const float *dkh, cudaStream_t stream);
 // dg[h] = sum over b, t of src [B,H,T].
 int launch_head_sum(const float *src, float *dg, int B, int H, int T, cudaStream_t stream);
 

@@ -1689,10 +1689,7 @@ int launch_linattn_tc_bwd(const LinAttnArgs &a, cudaStream_t stream) {
     p.sdg = per_head ? Strides{(long long)a.H * a.T, a.T, 1} : a.sg;
     if (a.Dk == 128) st = a.Dv == 128 ? run_bwd<128, 128>(p, stream) : run_bwd<128, 64>(p, stream);
     else st = a.Dv == 128 ? run_bwd<64, 128>(p, stream) : run_bwd<64, 64>(p, stream);
-    if (st == GDN_OK && a.H != a.Hk) {
-        st = launch_group_sum(w.dqh, a.dq, a.sq, a.B, a.H, a.Hk, a.T, a.Dk, a.dtype, stream);
-        if (st == GDN_OK) st = launch_group_sum(w.dkh, a.dk, a.sk, a.B, a.H, a.Hk, a.T, a.Dk, a.dtype, stream);
-    }
+    if (st == GDN_OK && a.H != a.Hk) st = launch_group_sum(a, w.dqh, w.dkh, stream);
     if (st == GDN_OK && per_head) st = launch_head_sum(w.dgt, a.dg, a.B, a.H, a.T, stream);
     return st;
 }
