@@ -39,8 +39,9 @@ __device__ unsigned int g_la_error = 0;  // set when a bounded wait gives up
 constexpr unsigned long long kDrainNs = 200000000ull;
 
 // Waits for the phase of the given parity, until the CTA's deadline at most.
-// Small on purpose: the roles' loops share the instruction cache.
-__device__ __forceinline__ bool la_wait(uint64_t *bar, uint32_t parity, uint64_t deadline) {
+// Small on purpose: the roles' loops share the instruction cache.  The deadline
+// is a reference so that one in shared memory is read when it is looked at.
+__device__ __forceinline__ bool la_wait(uint64_t *bar, uint32_t parity, const uint64_t &deadline) {
 #pragma unroll 1
     while (!mbar_try_wait_sleep(bar, parity, 20000u))
         if (global_timer_ns() > deadline) {
@@ -126,10 +127,25 @@ __device__ __forceinline__ void weigh3(uint32_t v, const Weight &w, uint32_t &hi
     lo = fma2(v, w.l, add2(mr, e));
 }
 
+// A forward whose long sequences are cut into pieces of whole chunks: a piece
+// but the last of its sequence has its own share of the state made first (a
+// row of the tables here, one item a head and 64 columns), and a piece starts
+// from the shares before it.
+struct Plan {
+    int *head;        // {next item, rows of shares, pieces, chunks of a piece at most}; null: no plan
+    int4 *shares;     // [rows] {sequence, first token, tokens, piece of its sequence}
+    int4 *pieces;     // {sequence, first token, tokens, 32 first row of its sequence's shares + 2 piece + last}
+    unsigned *flags;  // [rows][items of a row] made
+    float *decay;     // [rows][items of a row] e^(sum of the piece's log-decays)
+    float *share;     // [rows][items of a row][DK][64]
+    int rows;         // places
+};
+
 // What the tensor-core kernels take besides their maps.
 struct TcArgs {
     LinAttnArgs a;
     View v;
+    Plan plan;
     uint16_t *Shi, *Slo;  // [chunk][H][DK][DV] bf16 hi + lo: the states that enter the chunks
     uint16_t *Rhi, *Rlo, *Rend;  // and, in three terms, the gradients of the states that leave them
     float *gates;         // [chunk][H][4][128] decays for the gradients, see state_kernel
@@ -542,7 +558,8 @@ struct FwdSmem {
     static constexpr uint32_t W = S + DK * 128;              // [ring][3][128] weights
     static constexpr uint32_t G = W + kGRing * 1536;         // [ring] log2 decays | block factors, 128 each
     static constexpr uint32_t D = G + kGRing * 1024;         // [ring] chunk decays
-    static constexpr uint32_t BAR = D + 64;
+    static constexpr uint32_t ITEM = D + 16;                 // the item, and the next one
+    static constexpr uint32_t BAR = D + 112;
     enum { KFULL = 0, KEMPTY = 2, QFULL = 4, QEMPTY = 6, VFULL = 8, VREADY = 11, VEMPTY = 14, XREADY = 17,
            XEMPTY = XREADY + kXMax, UFULL = XEMPTY + kXMax,
            UEMPTY, SREADY, SEMPTY, TFULL, PREADY = TFULL + 2, OFULL = PREADY + 2, OEMPTY, GFULL, GEMPTY = GFULL + kGRing,
@@ -555,9 +572,153 @@ static_assert(FwdSmem<128>::BYTES <= 232448, "prompt kernel fits the shared memo
 // twice, P V, the chunk's share of the state
 constexpr uint32_t TM_T = 0, TM_OS = 256, TM_OP = 384, TM_U = 448;
 
-// Grid (DV / 64, H, n_seq, and one more for the tokens of no sequence).  A CTA walks the chunks of
-// one sequence for 64 value columns of one head.
-template <int DK, int DV>
+// ---- the plan: how a call's sequences are cut.  Costs are in chunks that a
+// CTA walks (2 us); one of a share alone is kShareCost of it (0.9 us), an item's
+// start and end kItemCost, a share that a piece adds up kJoinCost, making the
+// plan kPlanCost.
+constexpr int kSms = 152, kShareItems = 4 * kSms, kMostPieces = 16;
+constexpr float kShareCost = 0.45f, kItemCost = 2.5f, kJoinCost = 0.4f, kPlanCost = 1.5f;
+// With the longest sequence in p pieces of up to len chunks: chunks and shared
+// chunks of the call (over heads and columns), its items and shares.  What runs
+// at once takes as long as the longest walk, what does not is spread over the
+// SMs to half a walk or so.
+__host__ __device__ inline float plan_cost(long long chunks, long long shared, int len, long long items, long long shares, int p) {
+    const float chain = p > 1 ? (1.f + kShareCost) * len + 2 * kItemCost + kJoinCost * p + kPlanCost : len + kItemCost;
+    const float work = chunks + kShareCost * shared + kItemCost * items + kJoinCost * 0.5f * p * shares;
+    const float even = work / kSms + 0.5f * len;
+    return items > kSms && even > chain ? even : chain;
+}
+__host__ __device__ inline int pieces_of(int n, int len) { return n > len ? (n + len - 1) / len : 1; }
+
+// One CTA.  Cuts packed sequences by the lengths that are there, which the host
+// does not know (known: rows, in pieces of that many chunks).
+// Items are taken in order: shares, then pieces, long ones first.
+constexpr int kPlanThreads = 256;
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(LinAttnArgs a, Plan pl, int slots, int known) {
+    __shared__ float costs[kMostPieces + 1];  // by pieces of the longest
+    __shared__ unsigned long long all;
+    __shared__ int longest, some, len, rows, place[4];
+    if (threadIdx.x == 0) all = 0, longest = some = rows = 0;
+    if (threadIdx.x < 4) place[threadIdx.x] = 0;
+    __syncthreads();
+    if (known) {
+        if (threadIdx.x == 0) len = known;
+    } else {
+#pragma unroll 1
+        for (int s = threadIdx.x; s < a.n_seq; s += kPlanThreads) {
+            const int n = (span_of(a, s).len + kC - 1) / kC;
+            if (!n) continue;
+            atomicAdd(&all, (unsigned long long)n);
+            atomicMax(&longest, n);
+            atomicAdd(&some, 1);
+        }
+        __syncthreads();
+        const int lane = threadIdx.x & 31;
+#pragma unroll 1
+        for (int p = 2 + (threadIdx.x >> 5); p <= kMostPieces && longest; p += kPlanThreads / 32) {
+            const int most = (longest + p - 1) / p;
+            unsigned r = 0, c = 0;  // rows and chunks of shares
+#pragma unroll 1
+            for (int s = lane; s < a.n_seq; s += 32) {
+                const int n = (span_of(a, s).len + kC - 1) / kC, k = pieces_of(n, most);
+                if (k > 1) r += k - 1, c += (k - 1) * ((n + k - 1) / k);
+            }
+            r = __reduce_add_sync(~0u, r), c = __reduce_add_sync(~0u, c);
+            if (lane == 0)
+                costs[p] = r > pl.rows ? 1e30f
+                                       : plan_cost((long long)all * slots, (long long)c * slots, most, (some + 2ll * r) * slots, (long long)r * slots, p);
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            len = max(longest, 1);
+            float best = plan_cost((long long)all * slots, 0, longest, (long long)some * slots, 0, 1);
+#pragma unroll 1
+            for (int p = 2; p <= kMostPieces && longest; ++p)
+                if (costs[p] < best) best = costs[p], len = (longest + p - 1) / p;
+        }
+    }
+    __syncthreads();
+    auto size = [&](int n, int &q) {  // pieces of a sequence of n chunks, and their chunks
+        int k = pieces_of(n, len);
+        q = (n + k - 1) / k;
+        return max((n + q - 1) / max(q, 1), 1);
+    };
+    auto bucket = [&](int chunks) { return 2 * chunks > len ? 0 : 4 * chunks > len ? 1 : 8 * chunks > len ? 2 : 3; };
+#pragma unroll 1
+    for (int s = threadIdx.x; s < a.n_seq; s += kPlanThreads) {
+        int q;
+        const int n = (span_of(a, s).len + kC - 1) / kC, k = size(n, q);
+        if (k > 1) atomicAdd(&place[bucket(q)], k - 1);
+        atomicAdd(&place[bucket(n - (k - 1) * q)], 1);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int at = 0;
+        for (int &x : place) {
+            const int y = x;
+            x = at, at += y;
+        }
+        pl.head[0] = 0, pl.head[2] = at, pl.head[3] = len;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int s = threadIdx.x; s < a.n_seq; s += kPlanThreads) {
+        const Span sp = span_of(a, s);
+        int q;
+        const int n = (sp.len + kC - 1) / kC, k = size(n, q);
+        const int row = k > 1 ? atomicAdd(&rows, k - 1) : 0;
+        int at = k > 1 ? atomicAdd(&place[bucket(q)], k - 1) : 0;
+#pragma unroll 1
+        for (int j = 0; j < k - 1; ++j) {
+            const int t0 = sp.start + j * q * kC;
+            pl.shares[row + j] = make_int4(s, t0, q * kC, j);
+            pl.pieces[at + j] = make_int4(s, t0, q * kC, 32 * row + 2 * j);
+        }
+        const int done = (k - 1) * q;
+        at = atomicAdd(&place[bucket(n - done)], 1);
+        pl.pieces[at] = make_int4(s, sp.start + done * kC, sp.len - done * kC, 32 * row + 2 * (k - 1) + 1);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) pl.head[1] = rows;
+#pragma unroll 1
+    for (int e = threadIdx.x; e < rows * slots; e += kPlanThreads) pl.flags[e] = 0u;
+}
+
+// An item: some chunks of one sequence for 64 value columns of one head.
+enum { kNone = 0, kShare = 1, kPiece = 2, kFill = 3 };
+struct Item {
+    int seq, t0, tokens, kind;
+    int slot, row, piece;  // head and columns; the sequence's first row of shares; 2 piece + last
+    int base, full;        // the CTA's chunks before it, and those of pieces
+    uint64_t end;          // when its waits give up
+};
+static_assert(sizeof(Item) == 48, "two items take 96 bytes");
+
+// Waits for a share that another CTA makes.
+__device__ __forceinline__ bool share_wait(const unsigned *flag, const uint64_t &deadline) {
+    for (;;) {
+        unsigned v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+        if (v) return true;
+        if (global_timer_ns() > deadline) {
+            *reinterpret_cast<volatile unsigned *>(&g_la_error) = 1u;
+            return false;
+        }
+        __nanosleep(200);
+    }
+}
+
+// Bound by a chunk's chain of products, decays and shared-memory traffic: about
+// 4,000 cycles.  Measured, bf16, D 128: 4 x 4096 of 16 heads 67 us (40 at the
+// memory's rate); cut, 1 x 32768 of 16 heads 257 us (uncut 532), of 2 heads 91.
+// Grid (DV / 64, H, n_seq, and one more for the tokens of no sequence): a CTA
+// walks the chunks of one sequence for 64 value columns of one head.  TERMS of
+// a weighted value: three where the final state, an fp32 output, is asked for;
+// for bf16 outputs alone two (2^-16) are far below their rounding.  With a
+// plan, as many CTAs as there are SMs that take the plan's items in order, so
+// that the shares a piece waits for have all been started.  Rings and phases go
+// on from item to item.
+template <int DK, int DV, bool PLANNED, int TERMS>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                   const __grid_constant__ CUtensorMap mV, TcArgs p) {
@@ -568,25 +729,34 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     float *gring = reinterpret_cast<float *>(sm + L::G), *dring = reinterpret_cast<float *>(sm + L::D);
     uint32_t *wring = reinterpret_cast<uint32_t *>(sm + L::W);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int slice = blockIdx.x, h = blockIdx.y, seq = blockIdx.z;
-    if (seq >= p.a.n_seq) {  // packed: zeros for the tokens of no sequence
-        const int T = p.a.T, head = min(max(p.a.cu[0], 0), T), tail = min(max(p.a.cu[p.a.n_seq], 0), T);
-#pragma unroll 1
-        for (int e = threadIdx.x; e < (head + T - tail) * 8; e += kFwdThreads) {
-            const int i = e >> 3, t = i < head ? i : tail + i - head;
-            *reinterpret_cast<uint4 *>(at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, 0, h, t) + 64 * slice + (e & 7) * 8) =
-                make_uint4(0, 0, 0, 0);
+    Item *item = reinterpret_cast<Item *>(sm + L::ITEM);
+    const int slots = p.a.H * (DV / 64);
+    auto take = [&](Item *to, int base, int full) {  // thread 0's
+        const int t = atomicAdd(p.plan.head, 1), rows = p.plan.head[1], u = t / slots - rows;
+        Item x = {0, 0, 0, kNone, t % slots, 0, 1, base, full, 0};
+        if (u < 0) {
+            const int4 e = p.plan.shares[t / slots];
+            x.seq = e.x, x.t0 = e.y, x.tokens = e.z, x.kind = kShare, x.row = t / slots, x.piece = 2 * e.w;
+        } else if (u < p.plan.head[2]) {
+            const int4 e = p.plan.pieces[u];
+            x.seq = e.x, x.t0 = e.y, x.tokens = e.z, x.kind = kPiece, x.row = e.w >> 5, x.piece = e.w & 31;
+        } else if (u == p.plan.head[2] && p.a.cu) {
+            x.kind = kFill;
         }
-        return;
+        x.end = deadline_after(p.timeout_ns, x.tokens / kC + 1 + p.plan.head[3]);  // a share's time included
+        *to = x;
+    };
+    if (threadIdx.x == 0) {
+        if (PLANNED) {
+            take(item, 0, 0);
+        } else {
+            const int seq = blockIdx.z;
+            const Span sp = seq < p.a.n_seq ? span_of(p.a, seq) : Span{0, 0};
+            *item = {seq, sp.start, sp.len, seq < p.a.n_seq ? kPiece : kFill, (int)(blockIdx.y * gridDim.x + blockIdx.x), 0, 1, 0, 0,
+                     deadline_after(p.timeout_ns, sp.len / kC + 1)};
+        }
     }
-    const int row = p.a.cu ? 0 : seq;
-    const Span sp = span_of(p.a, seq);
-    const int n = (sp.len + kC - 1) / kC;
-    auto chunk = [&](int i) { return Chunk{row, sp.start + i * kC, min(kC, sp.len - i * kC), seq}; };
-    // the final state is an fp32 output: three bf16 terms a weighted value; for
-    // bf16 outputs alone two (2^-16) are far below their rounding
-    const int terms = p.a.sf ? 3 : 2, xring = p.a.sf ? 2 : 3;  // slots of X: 24 KB in all
-    const uint64_t end = deadline_after(p.timeout_ns, n);
+    constexpr int kXRing = TERMS == 3 ? 2 : 3;  // slots of X: 24 KB in all
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kQKStages; ++s) {
@@ -629,113 +799,147 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
     const uint32_t sbase = smem_u32(sm);
 
-    if (warp == 0) {
+#pragma unroll 1
+    for (;;) {
+    const Item &it = *item;
+    // the same in all lanes, which the compiler is to see (uniform registers)
+    auto same = [](int x) { return __shfl_sync(~0u, x, 0); };
+    const int kind = same(it.kind);
+    if (kind == kNone) break;
+    const bool share = PLANNED && kind == kShare;
+    const int slice = it.slot % (DV / 64), h = it.slot / (DV / 64), seq = it.seq, row = p.a.cu ? 0 : seq;
+    const int tokens = same(it.tokens), t0 = same(it.t0), n = (tokens + kC - 1) / kC;
+    const int base = PLANNED ? same(it.base) : 0, full = PLANNED ? same(it.full) : 0;
+    auto chunk = [&](int i) { return Chunk{row, t0 + i * kC, min(kC, tokens - i * kC), seq}; };
+    const uint64_t &end = it.end;
+    bool ok = true;
+    if (kind == kFill) {  // packed: zeros for the tokens of no sequence
+        const int T = p.a.T, head = min(max(p.a.cu[0], 0), T), tail = min(max(p.a.cu[p.a.n_seq], 0), T);
+#pragma unroll 1
+        for (int e = threadIdx.x; e < (head + T - tail) * 8; e += kFwdThreads) {
+            const int i = e >> 3, t = i < head ? i : tail + i - head;
+            *reinterpret_cast<uint4 *>(at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, 0, h, t) + 64 * slice + (e & 7) * 8) =
+                make_uint4(0, 0, 0, 0);
+        }
+        if (PLANNED && threadIdx.x == 0) take(item + 1, base, full);
+    } else if (warp == 0) {
         if (lane == 0) {
             const int hk = h / (p.a.H / p.a.Hk);
             int ik = 0, iq = 0, iv = 0;
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 const Chunk c = chunk(i);
-                const int s = i % kQKStages, v = i % kVStages;
-                uint8_t *st = sm + L::QK + s * 2 * L::TB;
-                if (i >= kVStages && !la_wait(&bars[L::VEMPTY + v], (i / kVStages - 1) & 1, end)) break;
+                const int gi = base + i, fi = full + i, s = gi % kQKStages, v = gi % kVStages, f = fi % kQKStages;
+                uint8_t *st = sm + L::QK + s * 2 * L::TB, *sq = sm + L::QK + f * 2 * L::TB + L::TB;
+                if (gi >= kVStages && !(ok = la_wait(&bars[L::VEMPTY + v], (gi / kVStages - 1) & 1, end))) break;
                 mbar_arrive_expect_tx(&bars[L::VFULL + v], 16384);
                 tma_load_4d(sm + L::V + v * 16384, &mV, &bars[L::VFULL + v], 64 * slice, c.t0, h, c.row);
                 ++iv;
-                if (i >= kQKStages && !la_wait(&bars[L::KEMPTY + s], (i / kQKStages - 1) & 1, end)) break;
+                if (gi >= kQKStages && !(ok = la_wait(&bars[L::KEMPTY + s], (gi / kQKStages - 1) & 1, end))) break;
                 mbar_arrive_expect_tx(&bars[L::KFULL + s], L::TB);
 #pragma unroll
                 for (int x = 0; x < DK / 64; ++x) tma_load_4d(st + x * 16384, &mK, &bars[L::KFULL + s], 64 * x, c.t0, hk, c.row);
                 ++ik;
-                if (i >= kQKStages && !la_wait(&bars[L::QEMPTY + s], (i / kQKStages - 1) & 1, end)) break;
-                mbar_arrive_expect_tx(&bars[L::QFULL + s], L::TB);
+                if (share) continue;
+                if (fi >= kQKStages && !(ok = la_wait(&bars[L::QEMPTY + f], (fi / kQKStages - 1) & 1, end))) break;
+                mbar_arrive_expect_tx(&bars[L::QFULL + f], L::TB);
 #pragma unroll
                 for (int x = 0; x < DK / 64; ++x)
-                    tma_load_4d(st + L::TB + x * 16384, &mQ, &bars[L::QFULL + s], 64 * x, c.t0, hk, c.row);
+                    tma_load_4d(sq + x * 16384, &mQ, &bars[L::QFULL + f], 64 * x, c.t0, hk, c.row);
                 ++iq;
             }
-            // no copy is in flight when the CTA ends
-            auto drain = [&](int full, int stages, int count) {
+            if (PLANNED) take(item + 1, base + n, share ? full : full + n);
+            // no copy is in flight when the item ends
+            auto drain = [&](int bar, int stages, int first, int count) {
 #pragma unroll 1
-                for (int j = count > stages ? count - stages : 0; j < count; ++j)
-                    mbar_wait(&bars[full + j % stages], (j / stages) & 1, kDrainNs);
+                for (int j = count > stages ? first + count - stages : first; j < first + count; ++j)
+                    mbar_wait(&bars[bar + j % stages], (j / stages) & 1, kDrainNs);
             };
-            drain(L::KFULL, kQKStages, ik);
-            drain(L::QFULL, kQKStages, iq);
-            drain(L::VFULL, kVStages, iv);
+            drain(L::KFULL, kQKStages, base, ik);
+            drain(L::QFULL, kQKStages, full, iq);
+            drain(L::VFULL, kVStages, base, iv);
         }
     } else if (warp == 1) {
         // the products of the outputs: Q K^T a chunk ahead, Q S and P V.  All
         // lanes wait, one issues.
         constexpr uint32_t idT = idesc_bf16(128, 128, false, false), idO = idesc_bf16(128, 64, false, true);
         const bool leader = elect_one();
+        if (share) {  // K and V pass by
 #pragma unroll 1
-        for (int i = -1; i < n; ++i) {
+            for (int gi = base; gi < base + n && ok; ++gi) {
+                const int s = gi % kQKStages, v = gi % kVStages;
+                ok = la_wait(&bars[L::KFULL + s], (gi / kQKStages) & 1, end) && la_wait(&bars[L::VFULL + v], (gi / kVStages) & 1, end);
+                if (leader && ok) {
+                    mbar_arrive(&bars[L::KEMPTY + s]);
+                    mbar_arrive(&bars[L::VEMPTY + v]);
+                }
+            }
+        }
+#pragma unroll 1
+        for (int i = share ? n : -1; i < n; ++i) {
             if (i + 1 < n) {
                 // T's place is free: P V of two chunks before, the last to read
                 // it, was issued before (products run in the order of their issue)
-                const int j = i + 1, st = j % kQKStages;
-                if (!la_wait(&bars[L::KFULL + st], (j / kQKStages) & 1, end)) break;
-                if (!la_wait(&bars[L::QFULL + st], (j / kQKStages) & 1, end)) break;
-                const uint32_t k = desc_lo(sbase + L::QK + st * 2 * L::TB, 16), q = k + (L::TB >> 4), d = TM_T + 128u * (j & 1);
+                const int gj = base + i + 1, fj = full + i + 1, st = gj % kQKStages, sq = fj % kQKStages;
+                if (!(ok = la_wait(&bars[L::KFULL + st], (gj / kQKStages) & 1, end))) break;
+                if (!(ok = la_wait(&bars[L::QFULL + sq], (fj / kQKStages) & 1, end))) break;
+                const uint32_t k = desc_lo(sbase + L::QK + st * 2 * L::TB, 16);
+                const uint32_t q = desc_lo(sbase + L::QK + sq * 2 * L::TB + L::TB, 16), d = TM_T + 128u * (fj & 1);
                 if (leader) {
                     mma_steps<DK / 16>(d, idT, [&](int ks) { return q + (ks >> 2) * 1024 + (ks & 3) * 2; },
                                        [&](int ks) { return k + (ks >> 2) * 1024 + (ks & 3) * 2; });
-                    mma_commit(&bars[L::TFULL + (j & 1)]);
+                    mma_commit(&bars[L::TFULL + (fj & 1)]);
                     mma_commit(&bars[L::KEMPTY + st]);
                 }
             }
             if (i < 0) continue;
-            if (!la_wait(&bars[L::SREADY], i & 1, end)) break;
+            const int gi = base + i, fi = full + i;
+            if (!(ok = la_wait(&bars[L::SREADY], fi & 1, end))) break;
             if (leader) {  // into the place that P V of one chunk before has waited for
-                const uint32_t q = desc_lo(sbase + L::QK + (i % kQKStages) * 2 * L::TB + L::TB, 16), x = desc_lo(sbase + L::S, 8192);
-                mma_steps<DK / 16>(TM_OS + 64u * (i & 1), idO, [&](int ks) { return q + (ks >> 2) * 1024 + (ks & 3) * 2; },
+                const uint32_t q = desc_lo(sbase + L::QK + (fi % kQKStages) * 2 * L::TB + L::TB, 16), x = desc_lo(sbase + L::S, 8192);
+                mma_steps<DK / 16>(TM_OS + 64u * (fi & 1), idO, [&](int ks) { return q + (ks >> 2) * 1024 + (ks & 3) * 2; },
                                    [&](int ks) { return x + ks * 128; });
                 mma_commit(&bars[L::SEMPTY]);
-                mma_commit(&bars[L::QEMPTY + i % kQKStages]);
+                mma_commit(&bars[L::QEMPTY + fi % kQKStages]);
             }
-            if (!la_wait(&bars[L::PREADY + (i & 1)], (i / 2) & 1, end)) break;
-            if (!la_wait(&bars[L::VREADY + i % kVStages], (i / kVStages) & 1, end)) break;
-            if (i >= 1 && !la_wait(&bars[L::OEMPTY], (i - 1) & 1, end)) break;
+            if (!(ok = la_wait(&bars[L::PREADY + (fi & 1)], (fi / 2) & 1, end))) break;
+            if (!(ok = la_wait(&bars[L::VREADY + gi % kVStages], (gi / kVStages) & 1, end))) break;
+            if (fi >= 1 && !(ok = la_wait(&bars[L::OEMPTY], (fi - 1) & 1, end))) break;
             tc_fence_after_sync();
-            const uint32_t v = desc_lo(sbase + L::V + (i % kVStages) * 16384, 8192), t = TM_T + 128u * (i & 1);
+            const uint32_t v = desc_lo(sbase + L::V + (gi % kVStages) * 16384, 8192), t = TM_T + 128u * (fi & 1);
             if (leader) {
                 mma_ts<0>(TM_OP, t, desc_of(v), idO);
 #pragma unroll
                 for (int ks = 1; ks < kC / 16; ++ks) mma_ts<1>(TM_OP, t + 8 * ks, desc_of(v + ks * 128), idO);
                 mma_commit(&bars[L::OFULL]);
-                mma_commit(&bars[L::VEMPTY + i % kVStages]);
+                mma_commit(&bars[L::VEMPTY + gi % kVStages]);
             }
         }
-        // every MMA issued here is complete before TMEM is released
-        if (leader) mma_commit(&bars[L::DRAIN]);
-        mbar_wait(&bars[L::DRAIN], 0, kDrainNs);
     } else if (warp == 2) {
         // the chunk's share of the state, as far as the weighted values are there
         constexpr uint32_t idU = idesc_bf16(128, 64, true, true);
         const bool leader = elect_one();
-        int xs = 0;  // slot of X, and its phase
-        uint32_t xp = 0;
-        bool ok = true;
+        int xs = 4 * base % kXRing;  // slot of X, and its phase
+        uint32_t xp = (4 * base / kXRing) & 1;
 #pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-            const int st = i % kQKStages;
+        for (int gi = base; gi < base + n; ++gi) {
+            const int st = gi % kQKStages;
             uint32_t k = desc_lo(sbase + L::QK + st * 2 * L::TB, 16384);
-            ok = la_wait(&bars[L::KFULL + st], (i / kQKStages) & 1, end);
-            if (i >= 1) ok = ok && la_wait(&bars[L::UEMPTY], (i - 1) & 1, end);
+            ok = la_wait(&bars[L::KFULL + st], (gi / kQKStages) & 1, end);
+            if (gi >= 1) ok = ok && la_wait(&bars[L::UEMPTY], (gi - 1) & 1, end);
             tc_fence_after_sync();
 #pragma unroll 1
             for (int qd = 0; qd < 4; ++qd, k += 256) {
                 ok = ok && la_wait(&bars[L::XREADY + xs], xp, end);
                 if (!ok) break;
-                const uint32_t x = desc_lo(sbase + L::X + xs * terms * 4096, 8192);
+                const uint32_t x = desc_lo(sbase + L::X + xs * TERMS * 4096, 8192);
                 if (leader) {
                     if (qd == 0) mma_ss<0>(TM_U, desc_of(k), desc_of(x), idU);
                     else mma_ss<1>(TM_U, desc_of(k), desc_of(x), idU);
                     mma_ss<1>(TM_U, desc_of(k + 128), desc_of(x + 128), idU);
                     mma_ss<1>(TM_U, desc_of(k), desc_of(x + 256), idU);
                     mma_ss<1>(TM_U, desc_of(k + 128), desc_of(x + 384), idU);
-                    if (terms == 3) {
+                    if constexpr (TERMS == 3) {
                         mma_ss<1>(TM_U, desc_of(k), desc_of(x + 512), idU);
                         mma_ss<1>(TM_U, desc_of(k + 128), desc_of(x + 640), idU);
                     }
@@ -743,18 +947,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     mma_commit(&bars[L::XEMPTY + xs]);
                     if (qd == 3) mma_commit(&bars[L::KEMPTY + st]);
                 }
-                if (++xs == xring) xs = 0, xp ^= 1;
+                if (++xs == kXRing) xs = 0, xp ^= 1;
             }
             if (!ok) break;
         }
-        if (leader) mma_commit(&bars[L::DRAIN + 1]);
-        mbar_wait(&bars[L::DRAIN + 1], 0, kDrainNs);
     } else if (warp == 3) {
         // a chunk's decays: e^{G - c_t}, log2(e) c_t, e^{c_r - c_t} with r the last
         // token of t's block of 32, and e^G; the next chunk's gates are on their
         // way meanwhile
         const bool per_head = p.a.flags & GDN_G_PER_HEAD;
-        float next[4];
+        float next[4], whole = 0.f;
         auto fetch = [&](int i) {
             if (i >= n) return;
             load_gates<kC>(gate_ptr(p.a, chunk(i), h), p.a.sg.t, chunk(i).len, per_head, next);
@@ -762,10 +964,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         fetch(0);
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
-            const int w = i % kGRing;
+            const int gi = base + i, w = gi % kGRing;
             const Sums g = scan_sums(next);
             fetch(i + 1);
-            if (i >= kGRing && !la_wait(&bars[L::GEMPTY + w], (i / kGRing - 1) & 1, end)) break;
+            if (gi >= kGRing && !(ok = la_wait(&bars[L::GEMPTY + w], (gi / kGRing - 1) & 1, end))) break;
             Weight wt[4];
             float c2[4];
 #pragma unroll
@@ -782,6 +984,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const float r = __shfl_sync(~0u, c2[3], lane | 7);
             slot[lane + 32] = make_float4(exp2_fast(r - c2[0]), exp2_fast(r - c2[1]), exp2_fast(r - c2[2]), exp2_fast(r - c2[3]));
             if (lane == 0) dring[w] = expf(g.all);
+            whole += g.all;
+            if (share && i == n - 1 && lane == 0) p.plan.decay[(size_t)it.row * slots + it.slot] = expf(whole);
             mbar_arrive(&bars[L::GFULL + w]);
         }
     } else if (warp < 8) {
@@ -790,27 +994,32 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const bool mine = row < DK;
         float S[64];
         const size_t page = (((size_t)seq * p.a.H + h) * DK + row) * DV + 64 * slice;
+        const int piece = PLANNED ? it.piece >> 1 : 0;
 #pragma unroll
         for (int e = 0; e < 64; e += 4) {
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (mine && p.a.s0) x = *reinterpret_cast<const float4 *>(p.a.s0 + page + e);
+            if (mine && p.a.s0 && piece == 0) x = *reinterpret_cast<const float4 *>(p.a.s0 + page + e);
             S[e] = x.x, S[e + 1] = x.y, S[e + 2] = x.z, S[e + 3] = x.w;
         }
-        bool ok = true;
+        if (PLANNED && !share)
 #pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-            const int w = i % kGRing;
-            if (i >= 1) ok = la_wait(&bars[L::SEMPTY], (i - 1) & 1, end);
-            if (mine)
+            for (int j = 0; j < piece; ++j) {  // the shares before the piece, the first with s0 in it
+                const size_t at = (size_t)(it.row + j) * slots + it.slot;
+                ok = warp_ok(ok && share_wait(p.plan.flags + at, end));
+                if (!ok) break;
+                const float d = j ? __ldcg(p.plan.decay + at) : 0.f;
+                const float4 *from = reinterpret_cast<const float4 *>(p.plan.share + (at * DK + (mine ? row : 0)) * 64);
 #pragma unroll
-                for (int e = 0; e < 64; e += 8)
-                    *reinterpret_cast<uint4 *>(sm + L::S + sw128_offset(row, e)) =
-                        make_uint4(pack_bf16(S[e], S[e + 1]), pack_bf16(S[e + 2], S[e + 3]), pack_bf16(S[e + 4], S[e + 5]),
-                                   pack_bf16(S[e + 6], S[e + 7]));
-            fence_proxy_async_smem();
-            mbar_arrive(&bars[L::SREADY]);
-            ok = ok && la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, end) && la_wait(&bars[L::UFULL], i & 1, end);
-            if (!warp_ok(ok)) break;
+                for (int e = 0; e < 64; e += 4) {
+                    const float4 x = __ldcg(from + e / 4);
+                    S[e] = fmaf(d, S[e], x.x), S[e + 1] = fmaf(d, S[e + 1], x.y);
+                    S[e + 2] = fmaf(d, S[e + 2], x.z), S[e + 3] = fmaf(d, S[e + 3], x.w);
+                }
+            }
+        auto step = [&](int gi) {  // S = e^G S + the chunk's share
+            const int w = gi % kGRing;
+            ok = warp_ok(ok && la_wait(&bars[L::GFULL + w], (gi / kGRing) & 1, end) && la_wait(&bars[L::UFULL], gi & 1, end));
+            if (!ok) return;
             const float d = dring[w];
             tc_fence_after_sync();
 #pragma unroll
@@ -824,11 +1033,45 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             tc_fence_before_sync();
             mbar_arrive(&bars[L::UEMPTY]);
             mbar_arrive(&bars[L::GEMPTY + w]);
+        };
+        if (share) {
+#pragma unroll 1
+            for (int gi = base; gi < base + n && ok; ++gi) step(gi);
+        } else {
+#pragma unroll 1
+            for (int gi = base; gi < base + n && ok; ++gi) {
+                ok = la_wait(&bars[L::SEMPTY], (gi + full - base + 1) & 1, end);  // the first passes
+                if (mine)
+#pragma unroll
+                    for (int e = 0; e < 64; e += 8)
+                        *reinterpret_cast<uint4 *>(sm + L::S + sw128_offset(row, e)) =
+                            make_uint4(pack_bf16(S[e], S[e + 1]), pack_bf16(S[e + 2], S[e + 3]), pack_bf16(S[e + 4], S[e + 5]),
+                                       pack_bf16(S[e + 6], S[e + 7]));
+                fence_proxy_async_smem();
+                mbar_arrive(&bars[L::SREADY]);
+                step(gi);
+            }
         }
-        if (p.a.sf && mine && ok)
+        if (share) {
+            const size_t at = (size_t)it.row * slots + it.slot;
+            if (mine && ok)
+#pragma unroll
+                for (int e = 0; e < 64; e += 4)
+                    *reinterpret_cast<float4 *>(p.plan.share + (at * DK + row) * 64 + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+            __threadfence();
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (ok && threadIdx.x == 128) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p.plan.flags + at), "r"(1u) : "memory");
+        } else if (p.a.sf && (it.piece & 1) && mine && ok) {
 #pragma unroll
             for (int e = 0; e < 64; e += 4)
                 *reinterpret_cast<float4 *>(p.a.sf + page + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+        }
+    } else if (share && (warp < 12 || warp >= 16)) {  // the decays pass by
+#pragma unroll 1
+        for (int gi = base; gi < base + n && ok; ++gi) {
+            ok = la_wait(&bars[L::GFULL + gi % kGRing], (gi / kGRing) & 1, end);
+            if (ok) mbar_arrive(&bars[L::GEMPTY + gi % kGRing]);
+        }
     } else if (warp < 12) {
         // P in blocks of 16 columns, thread's row t.  On the warp's diagonal (32
         // columns) the decay is e^{c_t - c_s}; before it e^{c_t - c_r} e^{c_r - c_s}
@@ -837,13 +1080,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int t = 32 * (warp & 3) + lane, diag = 32 * (warp & 3);
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
-            const int w = i % kGRing;
-            const bool ok = la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, end) && la_wait(&bars[L::TFULL + (i & 1)], (i / 2) & 1, end);
-            if (!warp_ok(ok)) break;
+            const int gi = base + i, fi = full + i, w = gi % kGRing;
+            ok = warp_ok(la_wait(&bars[L::GFULL + w], (gi / kGRing) & 1, end) && la_wait(&bars[L::TFULL + (fi & 1)], (fi / 2) & 1, end));
+            if (!ok) break;
             tc_fence_after_sync();
             const float *c2 = gring + w * 256, *cf = c2 + 128;
             const float ct = c2[t];
-            const uint32_t tt = tmem + lane_base(warp) + TM_T + 128u * (i & 1);
+            const uint32_t tt = tmem + lane_base(warp) + TM_T + 128u * (fi & 1);
             uint32_t u[16], y[8];
 #pragma unroll 1
             for (int s = 0; s < diag; s += 16) {
@@ -882,25 +1125,25 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             for (int s = diag + 32; s < kC; s += 16) tmem_st8(tt + s / 2, y);
             tmem_wait_st();
             tc_fence_before_sync();
-            mbar_arrive(&bars[L::PREADY + (i & 1)]);
+            mbar_arrive(&bars[L::PREADY + (fi & 1)]);
             mbar_arrive(&bars[L::GEMPTY + w]);
         }
     } else if (warp < 16) {
         // the weighted values, in quarters of 32 tokens: row r of each, 16 columns
         const int ct = threadIdx.x - 384, r = ct >> 2, c0 = (ct & 3) * 16;
         const uint32_t off[2] = {sw128_offset(r, c0), sw128_offset(r, c0 + 8)};
-        int xs = 0, xp = 1;  // slot of X, and the phase of its last release
-        bool ok = true;
+        int xs = 4 * base % kXRing;  // slot of X, and the phase of its last release
+        uint32_t xp = (4 * base / kXRing + 1) & 1;
 #pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
-            const int v = i % kVStages, w = i % kGRing, len = chunk(i).len;
-            ok = la_wait(&bars[L::VFULL + v], (i / kVStages) & 1, end) && la_wait(&bars[L::GFULL + w], (i / kGRing) & 1, end);
+            const int gi = base + i, v = gi % kVStages, w = gi % kGRing, len = chunk(i).len;
+            ok = la_wait(&bars[L::VFULL + v], (gi / kVStages) & 1, end) && la_wait(&bars[L::GFULL + w], (gi / kGRing) & 1, end);
             uint8_t *vt = sm + L::V + v * 16384;
             if (len < kC) {
                 // rows past the chunk's tokens are another sequence's: zeros, so
                 // that nothing of theirs (an infinity, say) meets a zero weight
-                ok = ok && la_wait(&bars[L::KFULL + i % kQKStages], (i / kQKStages) & 1, end);
-                uint8_t *k = sm + L::QK + (i % kQKStages) * 2 * L::TB;
+                ok = ok && la_wait(&bars[L::KFULL + gi % kQKStages], (gi / kQKStages) & 1, end);
+                uint8_t *k = sm + L::QK + (gi % kQKStages) * 2 * L::TB;
                 if (ok) {
 #pragma unroll 1
                     for (int row = r; row < kC; row += 32)
@@ -924,8 +1167,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 const Weight wt = {wr[0], wr[128], wr[256]};
                 ok = ok && la_wait(&bars[L::XEMPTY + xs], xp, end);
                 if (!ok) break;
-                uint8_t *xb = sm + L::X + xs * terms * 4096;
-                if (terms == 3) {
+                uint8_t *xb = sm + L::X + xs * TERMS * 4096;
+                if constexpr (TERMS == 3) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         uint4 a, b, d;
@@ -947,7 +1190,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&bars[L::XREADY + xs]);
-                if (++xs == xring) xs = 0, xp ^= 1;
+                if (++xs == kXRing) xs = 0, xp ^= 1;
             }
             if (!ok) break;
             mbar_arrive(&bars[L::VEMPTY + v]);
@@ -958,12 +1201,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int t = 32 * (warp & 3) + lane;
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
-            const int w = i % kGRing;
-            if (!warp_ok(la_wait(&bars[L::OFULL], i & 1, end))) break;
+            const int gi = base + i, fi = full + i, w = gi % kGRing;
+            ok = warp_ok(la_wait(&bars[L::OFULL], fi & 1, end));
+            if (!ok) break;
             tc_fence_after_sync();
             const Chunk c = chunk(i);
             const float f = exp2_fast(gring[w * 256 + t]) * p.a.scale;
-            const uint32_t ts = tmem + lane_base(warp) + TM_OS + 64u * (i & 1), tp = tmem + lane_base(warp) + TM_OP;
+            const uint32_t ts = tmem + lane_base(warp) + TM_OS + 64u * (fi & 1), tp = tmem + lane_base(warp) + TM_OP;
             uint32_t z[4][8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -992,6 +1236,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 }
             }
         }
+    }
+    if (!PLANNED) break;
+    __syncwarp();
+    tc_fence_before_sync();
+    const bool bad = __syncthreads_or(!ok);
+    if (threadIdx.x == 0) *item = item[1];
+    if (bad) break;
+    __syncthreads();
+    tc_fence_after_sync();
+    }
+    if (warp == 1 || warp == 2) {  // every MMA issued here is complete before TMEM is released
+        if (elect_one()) mma_commit(&bars[L::DRAIN + warp - 1]);
+        mbar_wait(&bars[L::DRAIN + warp - 1], 0, kDrainNs);
     }
     __syncwarp();
     tc_fence_before_sync();
@@ -1587,6 +1844,68 @@ bool smem_limit(uint32_t bytes) {
     return true;
 }
 
+// Chunks of a piece where cutting may pay (0: it does not): of the rows, whose
+// length is known, or, packed, if one sequence had all of the tokens.  What it
+// must save is more there, as lengths that need no cut lose by the plan (32760
+// tokens of 32 heads, states out: one sequence 562 -> 466 us, but eight equal
+// ones 291 -> 313; of 16 heads: 560 -> 295, so those are cut and these are not).
+int plan_len(const LinAttnArgs &a) {
+    const int slots = a.H * (a.Dv / 64), seqs = a.cu ? 1 : a.B;
+    const int n = (int)(((long long)a.T + kC - 1) / kC);
+    const long long chunks = (long long)seqs * n * slots;
+    float best = (a.cu ? 0.6f : 0.8f) * plan_cost(chunks, 0, n, (long long)seqs * slots, 0, 1);
+    int found = 0;
+    for (int p = 2; p <= kMostPieces; ++p) {
+        const int len = (n + p - 1) / p;
+        const long long rows = (long long)seqs * (pieces_of(n, len) - 1);
+        if (rows * slots > kShareItems) break;
+        const float cost = plan_cost(chunks, rows * len * slots, len, (seqs + 2 * rows) * slots, rows * slots, p);
+        if (cost < best) best = cost, found = len;
+    }
+    return found;
+}
+
+Plan plan_at(const LinAttnArgs &a, void *ws, size_t *bytes) {
+    Plan l{};
+    *bytes = 0;
+    if (!plan_len(a)) return l;
+    const size_t slots = (size_t)a.H * (a.Dv / 64);
+    l.rows = (int)(kShareItems / slots);
+    const uintptr_t p0 = up(reinterpret_cast<uintptr_t>(ws));
+    uintptr_t p = p0;
+    auto room = [&](size_t n) {
+        const uintptr_t at = p;
+        p += up(n);
+        return at;
+    };
+    l.head = reinterpret_cast<int *>(room(16));
+    l.shares = reinterpret_cast<int4 *>(room(16 * (size_t)l.rows));
+    l.pieces = reinterpret_cast<int4 *>(room(16 * ((size_t)a.n_seq + l.rows)));
+    l.flags = reinterpret_cast<unsigned *>(room(4 * l.rows * slots));
+    l.decay = reinterpret_cast<float *>(room(4 * l.rows * slots));
+    l.share = reinterpret_cast<float *>(room(256 * l.rows * slots * a.Dk));
+    *bytes = p - p0 + 1024;
+    return l;
+}
+
+template <int DK, int DV, int TERMS>
+int launch_prompt(const CUtensorMap &mQ, const CUtensorMap &mK, const CUtensorMap &mV, const TcArgs &p, cudaStream_t stream) {
+    const LinAttnArgs &a = p.a;
+    constexpr uint32_t bytes = FwdSmem<DK>::BYTES;
+    if (!p.plan.head) {
+        if (!smem_limit<prompt_kernel<DK, DV, false, TERMS>>(bytes)) return GDN_ERR_CUDA;
+        const dim3 grid(DV / 64, a.H, a.n_seq + (a.cu ? 1 : 0));
+        prompt_kernel<DK, DV, false, TERMS><<<grid, kFwdThreads, bytes, stream>>>(mQ, mK, mV, p);
+        return launched();
+    }
+    if (!smem_limit<prompt_kernel<DK, DV, true, TERMS>>(bytes)) return GDN_ERR_CUDA;
+    plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, p.plan, a.H * (DV / 64), a.cu ? 0 : plan_len(a));
+    const int st = launched();
+    if (st != GDN_OK) return st;
+    prompt_kernel<DK, DV, true, TERMS><<<device_sm_count(), kFwdThreads, bytes, stream>>>(mQ, mK, mV, p);
+    return launched();
+}
+
 template <int DK, int DV>
 int run_fwd(const TcArgs &p, cudaStream_t stream) {
     const LinAttnArgs &a = p.a;
@@ -1598,10 +1917,7 @@ int run_fwd(const TcArgs &p, cudaStream_t stream) {
         return GDN_ERR_CUDA;
     TcArgs w = p;
     w.wide = ((reinterpret_cast<uintptr_t>(a.o) | 2 * a.so.b | 2 * a.so.h | 2 * a.so.t) & 31) == 0;
-    auto kern = prompt_kernel<DK, DV>;
-    if (!smem_limit<prompt_kernel<DK, DV>>(FwdSmem<DK>::BYTES)) return GDN_ERR_CUDA;
-    kern<<<dim3(DV / 64, a.H, a.n_seq + (a.cu ? 1 : 0)), kFwdThreads, FwdSmem<DK>::BYTES, stream>>>(mQ, mK, mV, w);
-    return launched();
+    return a.sf ? launch_prompt<DK, DV, 3>(mQ, mK, mV, w, stream) : launch_prompt<DK, DV, 2>(mQ, mK, mV, w, stream);
 }
 
 struct BwdWs {
@@ -1661,12 +1977,18 @@ bool linattn_tc_supported(const LinAttnArgs &a) {
     return a.dtype == GDN_BF16 && !(a.flags & GDN_PATH_SIMT) && sm100_family();
 }
 
-size_t linattn_tc_fwd_workspace(const LinAttnArgs &) { return 0; }
+size_t linattn_tc_fwd_workspace(const LinAttnArgs &a) {
+    size_t bytes;
+    plan_at(a, nullptr, &bytes);
+    return bytes;
+}
 
 int launch_linattn_tc_fwd(const LinAttnArgs &a, cudaStream_t stream) {
     TcArgs p{};
     p.a = a;
     p.timeout_ns = wait_limit_ns();
+    size_t bytes;
+    p.plan = plan_at(a, a.ws, &bytes);
     if (a.Dk == 128) return a.Dv == 128 ? run_fwd<128, 128>(p, stream) : run_fwd<128, 64>(p, stream);
     return a.Dv == 128 ? run_fwd<64, 128>(p, stream) : run_fwd<64, 64>(p, stream);
 }
