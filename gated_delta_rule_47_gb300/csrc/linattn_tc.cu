@@ -146,8 +146,8 @@ struct TcArgs {
     LinAttnArgs a;
     View v;
     Plan plan;
-    uint16_t *Shi, *Slo;  // [chunk][H][DK][DV] bf16 hi + lo: the states that enter the chunks
-    uint16_t *Rhi, *Rlo, *Rend;  // and, in three terms, the gradients of the states that leave them
+    uint16_t *S[3], *R[3];  // [chunk][H][DK][DV], in three bf16 terms: the states that enter the chunks, and the
+                            // gradients of those that leave them
     float *gates;         // [chunk][H][4][128] decays for the gradients, see state_kernel
     float *dqh, *dkh;     // [B,H,T,DK] fp32, where value heads share dq and dk
     float *dgt;           // dg by token, with its strides
@@ -274,9 +274,9 @@ static_assert(StateSmem<128>::BYTES <= 232448, "state kernel fits the shared mem
 
 // Grid (2 DV / 64, H, n_seq): the states that enter a sequence's chunks, and
 // (the second half of x) backwards over them the gradients of the states that
-// leave them, with Q and dO in the places of K and V.  They go out as bf16
-// terms, which the gradients' products take as operands: S in two (2^-17), R,
-// on which more of dg's error hangs, in three.
+// leave them, with Q and dO in the places of K and V.  They go out as three
+// bf16 terms, which the gradients' products take as operands: dg is fp32, and
+// with two terms of S (2^-17) it was 4e-6 off where a state comes in.
 template <int DK, int DV>
 __global__ void __launch_bounds__(kStateThreads, 1)
     state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             Weight wt[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                wt[j] = split_weight(rev ? p.a.scale * exp2_fast(g.cum[j].hi * kLog2e) : exp2_fast(g.to_end(j) * kLog2e));
+                wt[j] = split_weight(rev ? p.a.scale * expf(g.cum[j].hi) : expf(g.to_end(j)));
             if (blockIdx.x == 0) {
                 // the gradient kernel's decays: c_t as a pair, G - c_t, and
                 // e^{c_r - c_t} with r the last token of t's block of 32
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 float4 *out = reinterpret_cast<float4 *>(p.gates + ((size_t)(sq.x + i) * p.a.H + h) * 512) + lane;
                 float cf[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) cf[j] = exp2_fast(((rh - g.cum[j].hi) + (rl - g.cum[j].lo)) * kLog2e);
+                for (int j = 0; j < 4; ++j) cf[j] = expf(((rh - g.cum[j].hi) + (rl - g.cum[j].lo)));
                 out[0] = make_float4(g.cum[0].hi, g.cum[1].hi, g.cum[2].hi, g.cum[3].hi);
                 out[32] = make_float4(g.cum[0].lo, g.cum[1].lo, g.cum[2].lo, g.cum[3].lo);
                 out[64] = make_float4(g.to_end(0), g.to_end(1), g.to_end(2), g.to_end(3));
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         for (int i = 0; i < n; ++i) {
             const int acc = i & 1, w = i % kWRing;
             const size_t at = (((size_t)(sq.x + number(i)) * p.a.H + h) * DK + row) * DV + 64 * slice;
-            uint16_t *hi = (rev ? p.Rhi : p.Shi) + at, *lo = (rev ? p.Rlo : p.Slo) + at, *last = rev ? p.Rend + at : nullptr;
+            uint16_t *hi = (rev ? p.R[0] : p.S[0]) + at, *lo = (rev ? p.R[1] : p.S[1]) + at, *last = (rev ? p.R[2] : p.S[2]) + at;
             if (mine)
 #pragma unroll
                 for (int e = 0; e < 64; e += 16) {
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                     }
                     st_global_32(hi + e, a);
                     st_global_32(lo + e, b);
-                    if (last) st_global_32(last + e, c);
+                    st_global_32(last + e, c);
                 }
             ok = warp_ok(la_wait(&bars[L::WFULL + w], (i / kWRing) & 1, end) && la_wait(&bars[L::UFULL + acc], (i >> 1) & 1, end));
             if (!ok) break;
@@ -1266,12 +1266,12 @@ constexpr int kGradWork = 512, kGradThreads = kGradWork + 32;
 
 struct GradSmem {
     static constexpr uint32_t Q = 0, K = 32768, V = 65536, O = 98304;  // V: later P
-    // S hi, then R lo, then dv; S lo, then R's last term, then N, then dq; R hi, then dk
+    // S hi, then R lo, then dv; S lo, then R's last term, then N, then dq; S's last term, then R hi, then dk
     static constexpr uint32_t X = 131072, Y = 163840, Z = 196608;
     static constexpr uint32_t G = 229376;                              // the chunk's decays, as state_kernel wrote them
     static constexpr uint32_t RED = G + 2048;
     static constexpr uint32_t BAR = RED + 64;  // 16 floats
-    enum { QK = 0, OV, SS, RH, RL, GT, LOADS = 6, CT = 6, CN, CQ, CK, DONE, TAIL, XREAD, READY, XFREE, ROWS, STORED, DRAIN, NUM };
+    enum { QK = 0, OV, SS, RR, GT, LOADS = 5, CT = 5, CN, CQ, CK, DONE, TAIL, XREAD, READY, XFREE, ROWS, STORED, DRAIN, NUM };
     static constexpr uint32_t TSLOT = BAR + 8 * NUM;
     static constexpr uint32_t BYTES = TSLOT + 16;
 };
@@ -1294,17 +1294,8 @@ __device__ __forceinline__ float column_sums(float (&x)[16]) {
     return x[0] + __shfl_xor_sync(~0u, x[0], 1);
 }
 
-__device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float x) {
-    float u[8], v[8];
-    unpack8(a, u);
-    unpack8(b, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x = fmaf(u[e], v[e], x);
-    return x;
-}
-
 struct GradMaps {
-    CUtensorMap q, k, v, o, s_hi, s_lo, r_hi, r_lo, r_last, dq, dk, dv;
+    CUtensorMap q, k, v, o, s[3], r[3], dq, dk, dv;
 };
 
 // The chunks' gradients (the formulas are linattn.cu's): one CTA an SM takes
@@ -1314,7 +1305,7 @@ struct GradMaps {
 // with P and N = dO V^T under the decay mask rounded to bf16, N K, N^T Q, P^T dO
 // and K R.  What dg is made of never passes through a rounded operand: the
 // pairs' terms A come from the fp32 products, the terms through S and R from
-// the split ones.  Bound by the bytes: 288 KB in, 96 KB out a chunk.
+// the split ones.  Bound by the bytes: 320 KB in, 96 KB out a chunk.
 template <int DK, int DV>
 __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_constant__ GradMaps m, TcArgs p) {
     using L = GradSmem;
@@ -1345,7 +1336,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
 
     if (warp == 16) {
         const bool leader = elect_one();
-        int loads[L::LOADS] = {0, 0, 0, 0, 0, 0};  // arrivals ordered on each of the loads' barriers
+        int loads[L::LOADS] = {0, 0, 0, 0, 0};  // arrivals ordered on each of the loads' barriers
         auto order = [&](int bar, uint32_t bytes) {
             ++loads[bar];
             if (leader) mbar_arrive_expect_tx(&bars[bar], bytes);
@@ -1401,26 +1392,27 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
             if (!first) ok = la_wait(&bars[L::STORED], ph ^ 1, end);
             if (!ok) break;
             first = false;
-            order(L::SS, 2 * DK * DV * 2);
-            state(&m.s_lo, L::Y, L::SS, it);
-            state(&m.s_hi, L::X, L::SS, it);
-            order(L::RH, DK * DV * 2);
-            state(&m.r_hi, L::Z, L::RH, it);
+            order(L::SS, 3 * DK * DV * 2);
+            state(&m.s[2], L::Z, L::SS, it);
+            state(&m.s[1], L::Y, L::SS, it);
+            state(&m.s[0], L::X, L::SS, it);
             constexpr uint32_t idk = idesc_bf16(128, DK, false, false);
             ok = la_wait(&bars[L::SS], ph, end);
             if (!ok) break;
             if (leader) {
-                mma_steps<DV / 16>(TM_Q, idk, km(L::O, 128), km(L::Y, DK));  // the smaller term first, as in state_kernel
+                mma_steps<DV / 16>(TM_Q, idk, km(L::O, 128), km(L::Z, DK));  // the smaller terms first, as in state_kernel
+                mma_more<DV / 16>(TM_Q, idk, km(L::O, 128), km(L::Y, DK));
                 mma_more<DV / 16>(TM_Q, idk, km(L::O, 128), km(L::X, DK));
                 mma_commit(&bars[L::CQ]);
             }
-            // R's lower terms in S's places, which have been multiplied and read
+            // R's terms in S's places, which have been multiplied and read
             ok = la_wait(&bars[L::CQ], ph, end) && la_wait(&bars[L::XREAD], ph, end);
             if (!ok) break;
-            order(L::RL, 2 * DK * DV * 2);
-            state(&m.r_lo, L::X, L::RL, it);
-            state(&m.r_last, L::Y, L::RL, it);
-            ok = la_wait(&bars[L::RL], ph, end) && la_wait(&bars[L::RH], ph, end);
+            order(L::RR, 3 * DK * DV * 2);
+            state(&m.r[2], L::Y, L::RR, it);
+            state(&m.r[1], L::X, L::RR, it);
+            state(&m.r[0], L::Z, L::RR, it);
+            ok = la_wait(&bars[L::RR], ph, end);
             if (!ok) break;
             if (leader) {
                 mma_steps<DV / 16>(TM_K, idk, km(L::V, 128), km(L::Y, DK));
@@ -1561,7 +1553,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
                 tmem_ld16(lanes + TM_A + sb, u);
                 tmem_ld16(lanes + TM_B + sb, w);
                 const int r = sb | 31;
-                const float rf = p.a.scale * exp2_fast(((ht - hi[r]) + (lt - lo[r])) * kLog2e);
+                const float rf = p.a.scale * expf(((ht - hi[r]) + (lt - lo[r])));
                 tmem_wait_ld();
                 if (sb < diag) {
 #pragma unroll
@@ -1580,7 +1572,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const int s = sb + j;
-                        const float f = s <= t ? p.a.scale * exp2_fast(((ht - hi[s]) + (lt - lo[s])) * kLog2e) : 0.f;
+                        const float f = s <= t ? p.a.scale * expf(((ht - hi[s]) + (lt - lo[s]))) : 0.f;
                         const float qk = __uint_as_float(u[j]), nn = __uint_as_float(w[j]) * f;
                         a[j] = s < t ? qk * nn : 0.f;
                         u[j] = __float_as_uint(qk * f);
@@ -1599,32 +1591,42 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
 #pragma unroll
                 for (int j = 0; j < 2; ++j) cola[j] = j == k ? sum : cola[j];
             }
-            // <R, S>: (S hi + S lo) . R hi now, S hi . R lo when that is there
-            constexpr int NV = DK * DV / 8 / kGradWork;  // 16-byte words of a state a thread
-            wait(L::SS);
-            wait(L::RH);
-            uint4 sh[NV];
-#pragma unroll
-            for (int e = 0; e < NV; ++e) {
+            // the thread's part of S for <R, S>, until R is there
+            constexpr int NV = DK * DV / 8 / kGradWork;  // 16-byte words of a term a thread
+            auto words = [&](int e, float (&x)[8], uint32_t t0, uint32_t t1, uint32_t t2) {  // t0's are the largest
                 const uint32_t o = (tid + kGradWork * e) * 16;
-                sh[e] = *reinterpret_cast<const uint4 *>(sm + L::X + o);
-                const uint4 r = *reinterpret_cast<const uint4 *>(sm + L::Z + o);
-                dot = dot8(sh[e], r, dot8(*reinterpret_cast<const uint4 *>(sm + L::Y + o), r, dot));
-            }
+                float y[8], z[8];
+                unpack8(*reinterpret_cast<const uint4 *>(sm + t0 + o), x);
+                unpack8(*reinterpret_cast<const uint4 *>(sm + t1 + o), y);
+                unpack8(*reinterpret_cast<const uint4 *>(sm + t2 + o), z);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] += y[j] + z[j];
+            };
+            wait(L::SS);
+            float sw[NV][8];
+#pragma unroll
+            for (int e = 0; e < NV; ++e) words(e, sw[e], L::X, L::Y, L::Z);
             if (ok) mbar_arrive(&bars[L::XREAD]);
             // dQ's part through S: scaled by its row, and x_t = q_t . it
-            const float fe = exp2_fast(te[t] * kLog2e), whole = expf(hi[c.len - 1]);
+            const float fe = expf(te[t]), whole = expf(hi[c.len - 1]);
             wait(L::CQ);
             tc_fence_after_sync();
-            if (ok) xt = scale_rows(TM_Q, p.a.scale * exp2_fast(ht * kLog2e), L::Q);
-            wait(L::RL);
+            if (ok) xt = scale_rows(TM_Q, p.a.scale * expf(ht), L::Q);
+            wait(L::RR);
 #pragma unroll
-            for (int e = 0; e < NV; ++e) dot = dot8(sh[e], *reinterpret_cast<const uint4 *>(sm + L::X + (tid + kGradWork * e) * 16), dot);
+            for (int e = 0; e < NV; ++e) {
+                float r[8];
+                words(e, r, L::Z, L::X, L::Y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dot = fmaf(sw[e][j], r[j], dot);
+            }
             wait(L::CK);
             tc_fence_after_sync();
+            if (ok) yt = scale_rows(TM_K, fe, L::K);
+            meet();
             if (ok) {
-                yt = scale_rows(TM_K, fe, L::K);
-                // R's last term and V have been multiplied: N and P take their places
+                // R's last term and V have been multiplied, and read by all: N and P
+                // take their places
                 tmem_wait_st();
 #pragma unroll 1
                 for (int k = 0; k < 2; ++k) {
@@ -1921,7 +1923,7 @@ int run_fwd(const TcArgs &p, cudaStream_t stream) {
 }
 
 struct BwdWs {
-    char *S[5];  // S hi, lo, R hi, lo, last
+    char *S[6];  // the terms of S, then R's
     float *gates, *dqh, *dkh, *dgt;
     size_t bytes;
 };
@@ -1948,10 +1950,10 @@ int run_bwd(const TcArgs &p, cudaStream_t stream) {
         !mappable(a.sdo, a.B, a.H, a.T))
         return GDN_ERR_UNSUPPORTED;
     GradMaps m;
-    const uint16_t *states[5] = {p.Shi, p.Slo, p.Rhi, p.Rlo, p.Rend};
-    CUtensorMap *maps[5] = {&m.s_hi, &m.s_lo, &m.r_hi, &m.r_lo, &m.r_last};
-    for (int i = 0; i < 5; ++i)
-        if (!state_map(maps[i], states[i], (long long)p.v.n_chunks * a.H, DK, DV)) return GDN_ERR_CUDA;
+    for (int i = 0; i < 3; ++i)
+        if (!state_map(&m.s[i], p.S[i], (long long)p.v.n_chunks * a.H, DK, DV) ||
+            !state_map(&m.r[i], p.R[i], (long long)p.v.n_chunks * a.H, DK, DV))
+            return GDN_ERR_CUDA;
     if (!strided_map(&m.q, a.q, a.sq, a.B, a.Hk, a.T, DK, kC) || !strided_map(&m.k, a.k, a.sk, a.B, a.Hk, a.T, DK, kC) ||
         !strided_map(&m.v, a.v, a.sv, a.B, a.H, a.T, DV, kC) || !strided_map(&m.o, a.dout, a.sdo, a.B, a.H, a.T, DV, kC) ||
         !strided_map(&m.dq, a.dq, a.sq, a.B, a.Hk, a.T, DK, kC) || !strided_map(&m.dk, a.dk, a.sk, a.B, a.Hk, a.T, DK, kC) ||
@@ -2002,9 +2004,10 @@ int launch_linattn_tc_bwd(const LinAttnArgs &a, cudaStream_t stream) {
     const BwdWs w = bwd_ws(a, a.ws);
     int st = make_view(a, kC, a.ws, &p.v, stream);
     if (st != GDN_OK) return st;
-    p.Shi = reinterpret_cast<uint16_t *>(w.S[0]), p.Slo = reinterpret_cast<uint16_t *>(w.S[1]);
-    p.Rhi = reinterpret_cast<uint16_t *>(w.S[2]), p.Rlo = reinterpret_cast<uint16_t *>(w.S[3]);
-    p.Rend = reinterpret_cast<uint16_t *>(w.S[4]);
+    for (int i = 0; i < 3; ++i) {
+        p.S[i] = reinterpret_cast<uint16_t *>(w.S[i]);
+        p.R[i] = reinterpret_cast<uint16_t *>(w.S[3 + i]);
+    }
     p.gates = w.gates, p.dqh = w.dqh, p.dkh = w.dkh;
     const bool per_head = a.flags & GDN_G_PER_HEAD;
     p.dgt = per_head ? w.dgt : a.dg;
