@@ -5,12 +5,18 @@ expected dtype and shape, allocates the outputs with torch, and calls the C
 entry point of the same name with raw device pointers and the current CUDA
 stream.  All computation happens in the library's kernels; there is no
 fallback: if ``libgdn.so`` is missing or fails to load, ``load()`` raises.
+
+The layer operators, whose smallest calls are bound by the host, go through
+``_front.so`` first, which does the same for calls in which all is well and
+declines the others.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -18,6 +24,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libgdn.so")
+FRONT_PATH = os.path.join(_PKG, "_build", "_front.so")
 
 GDN_F32, GDN_BF16 = 0, 1
 GDN_QK_L2NORM = 1
@@ -42,6 +49,7 @@ EXPORTS = ("gdn_status_string", "gdn_version", "gdn_chunk_fwd_workspace_bytes", 
 
 _lock = threading.Lock()
 _lib = None
+_front = None
 
 
 class GdnError(RuntimeError):
@@ -137,8 +145,32 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.gdn_set_cluster_shape.restype = i
         lib.gdn_launch_count.restype = ctypes.c_ulonglong
         if path is None:
+            _load_front(lib)
             _lib = lib
         return lib
+
+
+def _load_front(lib):
+    global _front
+    if not os.path.exists(FRONT_PATH):
+        raise RuntimeError(f"_front.so not found at {FRONT_PATH}; build it with "
+                           "`python -m gated_delta_rule_47_gb300.build`")
+    loader = importlib.machinery.ExtensionFileLoader("_front", FRONT_PATH)
+    front = importlib.util.module_from_spec(importlib.util.spec_from_loader("_front", loader))
+    loader.exec_module(front)
+    names = ("linattn_chunk_fwd_workspace_bytes", "linattn_chunk_fwd", "linattn_chunk_bwd_workspace_bytes",
+             "linattn_chunk_bwd", "linattn_step", "gdn_step", "rms_norm_fwd", "rms_norm_bwd_workspace_bytes",
+             "rms_norm_bwd", "state_pool_fork_workspace_bytes", "state_pool_fork",
+             "state_pool_compact_workspace_bytes", "state_pool_compact")
+    stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent without CUDA, where nothing asks for it
+    front.init(tuple(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in names), stream, _raise)
+    _front = front
+
+
+def _quick():
+    """The front, loaded."""
+    load()
+    return _front
 
 
 def _ptr(t):
@@ -748,6 +780,10 @@ def linattn_chunk_fwd(q, k, v, g, initial_state=None, output_final_state=False, 
     goes in as x.unsqueeze(0).transpose(1, 2)).  initial_state
     [sequences,H,Dk,Dv] fp32.  Returns (o, final_state or None); o has v's
     strides unless it is given."""
+    if o is None and workspace is None and stream is None:
+        r = (_front or _quick()).fwd(q, k, v, g, initial_state, output_final_state, cu_seqlens, scale, simt)
+        if r is not NotImplemented:
+            return r
     B, H, Hk, T, Dk, Dv, n_seq, code, per_head, dense = _linattn_sizes(q, k, v, g, cu_seqlens, initial_state)
     flags = (GDN_G_PER_HEAD if per_head else 0) | (GDN_PATH_SIMT if simt else 0)
     need = _bytes("linattn_chunk_fwd_workspace_bytes", B, H, Hk, T, Dk, Dv, n_seq, cu_seqlens is not None, flags, code)
@@ -777,6 +813,10 @@ def linattn_chunk_bwd(q, k, v, g, dout, initial_state=None, dfinal_state=None, c
     [sequences,H,Dk,Dv] fp32.  Returns (dq, dk, dv, dg, dinitial_state or
     None): the first three in the tensors' type, dg fp32 in g's shape (its sum
     over batch and tokens for g [H])."""
+    if workspace is None and stream is None:
+        r = (_front or _quick()).bwd(q, k, v, g, dout, initial_state, dfinal_state, cu_seqlens, scale, simt)
+        if r is not NotImplemented:
+            return r
     B, H, Hk, T, Dk, Dv, n_seq, code, per_head, dense = _linattn_sizes(q, k, v, g, cu_seqlens, initial_state)
     dense = _strided(dout, "dout", (B, H, T, Dv), q.dtype) and dense
     if dfinal_state is not None:
@@ -802,6 +842,10 @@ def linattn_chunk_bwd(q, k, v, g, dout, initial_state=None, dfinal_state=None, c
 
 
 def _step(fn_name, q, k, v, beta, g, state, slots, state_out, scale, l2norm, o, stream):
+    if o is None and stream is None:
+        r = (_front or _quick()).step(q, k, v, beta, g, state, slots, state_out, scale, l2norm)
+        if r is not NotImplemented:
+            return r
     B, Hk, Dk = q.shape
     _, H, Dv = v.shape
     n_slots = state.shape[0]
@@ -860,6 +904,11 @@ def rms_norm_fwd(x, weight=None, residual=None, eps=1e-6, out_dtype=None, group=
     out_dtype: None (x's) or torch.float8_e4m3fn, then with scales [...,C/group]
     (group 32, 64 or 128) or [...,1] (group 0: one a row).  Returns (y, scales or
     None, h); h is x itself without a residual."""
+    e4m3 = out_dtype is torch.float8_e4m3fn
+    if stream is None and (e4m3 or out_dtype is None):
+        r = (_front or _quick()).norm(x, weight, residual, eps, e4m3, group)
+        if r is not NotImplemented:
+            return r
     C = x.shape[-1]
     code = _dtype_code(x)
     _dense(x, "x", x.shape, x.dtype)
@@ -867,7 +916,6 @@ def rms_norm_fwd(x, weight=None, residual=None, eps=1e-6, out_dtype=None, group=
         _dense(residual, "residual", x.shape, x.dtype)
     if weight is not None:
         _dense(weight, "weight", (C,), torch.float32)
-    e4m3 = out_dtype is torch.float8_e4m3fn
     if not e4m3 and out_dtype not in (None, x.dtype):
         raise TypeError(f"out_dtype must be {x.dtype} or torch.float8_e4m3fn, got {out_dtype}")
     if group and (not e4m3 or group not in (32, 64, 128) or C % group):
@@ -891,6 +939,10 @@ def rms_norm_bwd(dy, h, weight=None, dresidual=None, eps=1e-6, workspace=None, s
     """Backward of rms_norm_fwd at the h that it returned: (dx, dweight [C]
     fp32).  dresidual: the gradient that reaches h past the norm; dx is also
     the residual's gradient."""
+    if workspace is None and stream is None:
+        r = (_front or _quick()).norm_back(dy, h, weight, dresidual, eps)
+        if r is not NotImplemented:
+            return r
     C = h.shape[-1]
     code = _dtype_code(h)
     _dense(h, "h", h.shape, h.dtype)
@@ -951,6 +1003,10 @@ def state_pool_fork(pool, live, parents, stream=None):
     the lowest free slot, with a copy of its page in every layer of pool
     [layers,slots,...].  live uint8 [slots] is updated.  Returns the children,
     int32, -1 where the parent is not live or no slot is left."""
+    if stream is None:
+        r = (_front or _quick()).fork(pool, live, parents)
+        if r is not NotImplemented:
+            return r
     layers, n_slots, page = _pool(pool)
     _dense(live, "live", (n_slots,), torch.uint8)
     n = _slots(parents, "parents")
@@ -978,6 +1034,10 @@ def state_pool_compact(pool, live, stream=None):
     """Moves the live pages of pool [layers,slots,...] into its first slots and
     updates live.  Returns (remap, n_live): int32 [slots], each slot's new
     place or -1, and the count, int32 [1], on the device."""
+    if stream is None:
+        r = (_front or _quick()).compact(pool, live)
+        if r is not NotImplemented:
+            return r
     layers, n_slots, page = _pool(pool)
     _dense(live, "live", (n_slots,), torch.uint8)
     need = _bytes("state_pool_compact_workspace_bytes", n_slots)

@@ -1,17 +1,21 @@
 """Builds libgdn.so in-tree from csrc/*.cu for sm_103a with nvcc.
 
 Each translation unit compiles in parallel to an object file, then nvcc links
-the shared library into ``_build/libgdn.so``.  Rebuilds only what is stale.
+the shared library into ``_build/libgdn.so``.  ``_build/_front.so`` is the
+binding's way into the layer operators, host code over torch's C++ headers.
+Rebuilds only what is stale.
 Usage: ``python -m gated_delta_rule_47_gb300.build [--force]``.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libgdn.so")
+FRONT = os.path.join(OUT_DIR, "_front.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -54,15 +59,32 @@ def _compile(src, extra):
     return obj
 
 
+def _front():
+    src = os.path.join(CSRC, "front.cpp")
+    if _stale(FRONT, [src, os.path.join(INCLUDE, "gdn.h")]):
+        torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+        tmp = FRONT + f".{os.getpid()}.tmp"
+        includes = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(torch, "include"),
+                    os.path.join(torch, "include", "torch", "csrc", "api", "include")]
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", *(f"-I{d}" for d in includes), src,
+               "-o", tmp, "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"{cmd[0]} failed for {src}:\n{res.stdout}\n{res.stderr}")
+        os.replace(tmp, FRONT)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     if force:
-        for f in glob.glob(os.path.join(OUT_DIR, "*.o")):
+        for f in glob.glob(os.path.join(OUT_DIR, "*.o")) + glob.glob(FRONT):
             os.remove(f)
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        front = ex.submit(_front)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
+        front.result()
     if force or _stale(LIB, objs):
         tmp = LIB + f".{os.getpid()}.tmp"
         cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart"]
