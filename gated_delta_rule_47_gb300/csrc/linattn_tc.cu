@@ -60,6 +60,16 @@ __device__ __forceinline__ uint64_t deadline_after(unsigned long long limit, int
 // A wait's outcome made uniform across the warp, so that the warp's
 // .sync.aligned TMEM accesses that follow are reached by all of its lanes.
 __device__ __forceinline__ bool warp_ok(bool ok) { return __all_sync(0xffffffffu, ok) != 0; }
+// A barrier (1) of THREADS of the CTA's threads, and whether all of them say so.
+template <int THREADS>
+__device__ __forceinline__ bool all_of(bool ok) {
+    uint32_t all;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(all)
+                 : "r"(ok ? 1u : 0u), "n"(THREADS)
+                 : "memory");
+    return all != 0;
+}
 __device__ __forceinline__ uint32_t lane_base(int warp) { return (uint32_t)(32 * (warp & 3)) << 16; }
 
 __device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
@@ -252,10 +262,15 @@ __device__ __forceinline__ void mma_more(uint32_t d, uint32_t idesc, const A &a,
     for (int ks = 0; ks < KS; ++ks) mma_ss<1>(d, desc_of(a(ks)), desc_of(b(ks)), idesc);
 }
 
+// The backward's tensors; boxes of 64 columns, the states' of DK rows.
+struct GradMaps {
+    CUtensorMap q, k, v, o, s[3], r[3], dq, dk, dv;
+};
+
 // ================================================================ state kernel
 // Warps: 0 TMA, 1 products, 2 decays, 4..7 state, 8..15 weighting.
 constexpr int kStateThreads = 512;
-constexpr int kStages = 3, kWRing = 4;
+constexpr int kStages = 2, kWRing = 4;
 
 template <int DK>
 struct StateSmem {
@@ -264,9 +279,10 @@ struct StateSmem {
     // with DK = 64 the product's rows 64..127 read the bytes after K, in the
     // stage's own V tile: rows that nobody looks at
     static constexpr uint32_t X = kStages * STAGE;        // [half][3][64 tokens][128 B] weighted values
-    static constexpr uint32_t W = X + 2 * 3 * 8192;       // [ring][3][128] weights, then [ring] chunk decays
+    static constexpr uint32_t OUT = X + 2 * 3 * 8192;     // [3][DK][128 B] the state's terms on their way out
+    static constexpr uint32_t W = OUT + 3 * DK * 128;       // [ring][3][128] weights, then [ring] chunk decays
     static constexpr uint32_t BAR = W + kWRing * 1536 + 64;
-    enum { FULL = 0, EMPTY = 3, XREADY = 6, XEMPTY = 8, UFULL = 10, UEMPTY = 12, WFULL = 14, WEMPTY = 18, DRAIN = 22, NUM = 23 };
+    enum { FULL = 0, EMPTY = 2, XREADY = 4, XEMPTY = 6, UFULL = 8, UEMPTY = 10, WFULL = 12, WEMPTY = 16, DRAIN = 20, NUM = 21 };
     static constexpr uint32_t TSLOT = BAR + 8 * NUM;
     static constexpr uint32_t BYTES = TSLOT + 16;
 };
@@ -277,10 +293,12 @@ static_assert(StateSmem<128>::BYTES <= 232448, "state kernel fits the shared mem
 // leave them, with Q and dO in the places of K and V.  They go out as three
 // bf16 terms, which the gradients' products take as operands: dg is fp32, and
 // with two terms of S (2^-17) it was 4e-6 off where a state comes in.
+// Bound by what it writes, 48 KB a CTA and chunk, and by the waves of CTAs: 125
+// us at B4 H16 T4096 (670 MB, 256 CTAs on 152 SMs), 1.7 us a chunk alone.  Two
+// smaller CTAs an SM wait for each other's stores and were no faster.
 template <int DK, int DV>
 __global__ void __launch_bounds__(kStateThreads, 1)
-    state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
-                 const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mO, TcArgs p) {
+    state_kernel(const __grid_constant__ GradMaps m, TcArgs p) {
     using L = StateSmem<DK>;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
@@ -328,7 +346,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     if (warp == 0) {
         if (lane == 0) {
             const int hk = h / (p.a.H / p.a.Hk);
-            const CUtensorMap *m1 = rev ? &mQ : &mK, *m2 = rev ? &mO : &mV;
+            const CUtensorMap *m1 = rev ? &m.q : &m.k, *m2 = rev ? &m.o : &m.v;
             int i = 0;
 #pragma unroll 1
             for (; i < n; ++i) {
@@ -489,14 +507,20 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
             const int acc = i & 1, w = i % kWRing;
-            const size_t at = (((size_t)(sq.x + number(i)) * p.a.H + h) * DK + row) * DV + 64 * slice;
-            uint16_t *hi = (rev ? p.R[0] : p.S[0]) + at, *lo = (rev ? p.R[1] : p.S[1]) + at, *last = (rev ? p.R[2] : p.S[2]) + at;
+            // the terms leave through a tile each, whole lines at a time: by the
+            // threads' own stores, 32 bytes of 32 lines an instruction, the walks
+            // took 167 us (B4 H16 T4096)
+            if (i >= 1 && threadIdx.x == 128) tma_store_wait_read<0>();
+            // a warp whose wait gave up comes to this barrier all the same, and none
+            // of the four goes on
+            ok = all_of<128>(ok);
+            if (!ok) break;
             if (mine)
 #pragma unroll
-                for (int e = 0; e < 64; e += 16) {
-                    uint32_t a[8], b[8], c[8];
+                for (int e = 0; e < 64; e += 8) {
+                    uint32_t a[4], b[4], c[4];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < 4; ++j) {
                         float x = S[e + 2 * j], y = S[e + 2 * j + 1];
                         a[j] = pack_bf16(x, y);
                         x -= __uint_as_float(a[j] << 16), y -= __uint_as_float(a[j] & 0xffff0000u);
@@ -504,12 +528,21 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                         x -= __uint_as_float(b[j] << 16), y -= __uint_as_float(b[j] & 0xffff0000u);
                         c[j] = pack_bf16(x, y);
                     }
-                    st_global_32(hi + e, a);
-                    st_global_32(lo + e, b);
-                    st_global_32(last + e, c);
+                    uint8_t *to = sm + L::OUT + sw128_offset(row, e);
+                    *reinterpret_cast<uint4 *>(to) = make_uint4(a[0], a[1], a[2], a[3]);
+                    *reinterpret_cast<uint4 *>(to + DK * 128) = make_uint4(b[0], b[1], b[2], b[3]);
+                    *reinterpret_cast<uint4 *>(to + 2 * DK * 128) = make_uint4(c[0], c[1], c[2], c[3]);
                 }
+            fence_proxy_async_smem();
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (threadIdx.x == 128) {
+                const int item = (sq.x + number(i)) * p.a.H + h;
+#pragma unroll
+                for (int e = 0; e < 3; ++e) tma_store_3d(rev ? &m.r[e] : &m.s[e], sm + L::OUT + e * DK * 128, 64 * slice, 0, item);
+                tma_store_commit();
+            }
             ok = warp_ok(la_wait(&bars[L::WFULL + w], (i / kWRing) & 1, end) && la_wait(&bars[L::UFULL + acc], (i >> 1) & 1, end));
-            if (!ok) break;
+            if (!ok) continue;
             const float d = dring[w];
             tc_fence_after_sync();
 #pragma unroll
@@ -524,6 +557,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             mbar_arrive(&bars[L::UEMPTY + acc]);
             mbar_arrive(&bars[L::WEMPTY + w]);
         }
+        if (threadIdx.x == 128) tma_store_wait_all<0>();
         float *to = rev ? p.a.ds0 : p.a.sf;
         if (to && mine && ok)
 #pragma unroll
@@ -1294,10 +1328,6 @@ __device__ __forceinline__ float column_sums(float (&x)[16]) {
     return x[0] + __shfl_xor_sync(~0u, x[0], 1);
 }
 
-struct GradMaps {
-    CUtensorMap q, k, v, o, s[3], r[3], dq, dk, dv;
-};
-
 // The chunks' gradients (the formulas are linattn.cu's): one CTA an SM takes
 // (chunk, head) items in turn, the next item's tiles coming in as this one's
 // places get free.
@@ -1448,15 +1478,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
         uint32_t ph = 0;
         // these warps' barrier.  A warp whose wait gave up comes to it all the
         // same, and none of them goes on.
-        auto meet = [&] {
-            uint32_t all;
-            asm volatile(
-                "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 512, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                : "=r"(all)
-                : "r"(ok ? 1u : 0u)
-                : "memory");
-            ok = all != 0;
-        };
+        auto meet = [&] { ok = all_of<kGradWork>(ok); };
         auto wait = [&](int bar) { ok = warp_ok(ok && la_wait(&bars[bar], ph, end)); };
         // Scales the thread's part of its row of dQ or dK and gives its product
         // with the row of Q or K.
@@ -1961,7 +1983,7 @@ int run_bwd(const TcArgs &p, cudaStream_t stream) {
         return GDN_ERR_CUDA;
     if (!smem_limit<state_kernel<DK, DV>>(StateSmem<DK>::BYTES) || !smem_limit<grad_kernel_tc<DK, DV>>(GradSmem::BYTES))
         return GDN_ERR_CUDA;
-    state_kernel<DK, DV><<<dim3(2 * DV / 64, a.H, a.n_seq), kStateThreads, StateSmem<DK>::BYTES, stream>>>(m.k, m.v, m.q, m.o, p);
+    state_kernel<DK, DV><<<dim3(2 * DV / 64, a.H, a.n_seq), kStateThreads, StateSmem<DK>::BYTES, stream>>>(m, p);
     const int st = launched();
     if (st != GDN_OK) return st;
     const long long items = (long long)p.v.n_chunks * a.H;
