@@ -1257,16 +1257,31 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             tc_fence_before_sync();
             mbar_arrive(&bars[L::OEMPTY]);
             mbar_arrive(&bars[L::GEMPTY + w]);
-            __nv_bfloat16 *out = at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, c.row, h, c.t0 + t) + 64 * slice;
-            if (t < c.len) {
+            // four lanes exchange their rows' quarters, so that a store is of 8 whole
+            // lines and not of a piece of 32
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (p.wide) {
-                        st_global_32(out + 16 * e, z[e]);
-                    } else {
-                        reinterpret_cast<uint4 *>(out)[2 * e] = make_uint4(z[e][0], z[e][1], z[e][2], z[e][3]);
-                        reinterpret_cast<uint4 *>(out)[2 * e + 1] = make_uint4(z[e][4], z[e][5], z[e][6], z[e][7]);
-                    }
+            for (int m = 2; m; m >>= 1) {
+                const bool up = lane & m;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!(e & m))
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t got = __shfl_xor_sync(~0u, up ? z[e][j] : z[e | m][j], m);
+                            if (up) z[e][j] = got;
+                            else z[e | m][j] = got;
+                        }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int u = (t & ~3) + e;
+                if (u >= c.len) break;
+                __nv_bfloat16 *out = at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, c.row, h, c.t0 + u) + 64 * slice + 16 * (lane & 3);
+                if (p.wide) {
+                    st_global_32(out, z[e]);
+                } else {
+                    reinterpret_cast<uint4 *>(out)[0] = make_uint4(z[e][0], z[e][1], z[e][2], z[e][3]);
+                    reinterpret_cast<uint4 *>(out)[1] = make_uint4(z[e][4], z[e][5], z[e][6], z[e][7]);
                 }
             }
         }
