@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kTableThreads) table_kernel(const int *cu, int
 }
 
 // dq[b,hk,t,:] = sum of the value heads' shares dqh[b,h,t,:], in their order,
-// and the same for dk: the second half of grid.x.
+// and the same for dk: the second half of grid.x.  Bound by the bytes.
 template <typename T>
 __global__ void group_sum_kernel(LinAttnArgs a, const float4 *dqh, const float4 *dkh) {
     const int per = a.Dk / 4, rep = a.H / a.Hk, blocks = gridDim.x / 2;
@@ -123,7 +123,12 @@ __global__ void group_sum_kernel(LinAttnArgs a, const float4 *dqh, const float4 
             x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
         }
         T *p = at(dst, s, b, hk, t) + 4 * c;
-        tile::st_f(p, x.x), tile::st_f(p + 1, x.y), tile::st_f(p + 2, x.z), tile::st_f(p + 3, x.w);
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4 *>(p) = x;
+        } else {
+            __nv_bfloat162 y[2] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w)};
+            *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(y);
+        }
     }
 }
 

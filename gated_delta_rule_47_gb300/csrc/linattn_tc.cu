@@ -226,6 +226,25 @@ __device__ __forceinline__ void st_global_32(void *p, const uint32_t (&x)[8]) {
                  : "memory");
 }
 
+// Four lanes (rows) of four words of 32 bytes each exchange them: before, z[e] is
+// word e of the lane's row; after, z[e] is word lane % 4 of the e-th row.  A store
+// is then of 8 whole lines and not of a piece of 32.
+__device__ __forceinline__ void exchange(uint32_t (&z)[4][8]) {
+#pragma unroll
+    for (int m = 2; m; m >>= 1) {
+        const bool up = threadIdx.x & m;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (!(e & m))
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t got = __shfl_xor_sync(~0u, up ? z[e][j] : z[e | m][j], m);
+                    if (up) z[e][j] = got;
+                    else z[e | m][j] = got;
+                }
+    }
+}
+
 // D[tmem] (+)= A * B[smem]^T with A in shared memory, or (ts) in tensor memory:
 // rows are lanes, two bf16 of a row a column.  ADD is a constant: as a run-time
 // operand it costs more instructions than all the rest of a product.
@@ -1257,21 +1276,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             tc_fence_before_sync();
             mbar_arrive(&bars[L::OEMPTY]);
             mbar_arrive(&bars[L::GEMPTY + w]);
-            // four lanes exchange their rows' quarters, so that a store is of 8 whole
-            // lines and not of a piece of 32
-#pragma unroll
-            for (int m = 2; m; m >>= 1) {
-                const bool up = lane & m;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (!(e & m))
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint32_t got = __shfl_xor_sync(~0u, up ? z[e][j] : z[e | m][j], m);
-                            if (up) z[e][j] = got;
-                            else z[e | m][j] = got;
-                        }
-            }
+            exchange(z);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int u = (t & ~3) + e;
@@ -1732,6 +1737,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
             // the rows of the gradients: bf16 through the tiles Y, Z and X, so that
             // the stores are whole rows; fp32 (shared heads) straight
             auto rows = [&](uint32_t col, uint32_t tile_at, int d, float *wide, bool both) {
+                if (wide && d == 128) {
+                    uint32_t z[4][8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) tmem_ld8(lanes + col + four * 32 + 8 * e, z[e]);
+                    tmem_wait_ld();
+                    exchange(z);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int u = (t & ~3) + e;
+                        if (u < c.len) st_global_32(wide + (size_t)u * d + four * 32 + 8 * (lane & 3), z[e]);
+                    }
+                    return;
+                }
 #pragma unroll 1
                 for (int e = 0; e < d / 4; e += 16) {
                     const int d0 = four * (d / 4) + e;
