@@ -108,10 +108,12 @@ __device__ __forceinline__ void store_e4m3(void *p, const float (&y)[N], float i
 // (vector j of thread t is number j NT + t, so a group's vectors are
 // consecutive lanes of one warp).  The next row is on its way while this one is
 // summed and written: a CTA that takes one row at a time has nothing to load
-// for half of its life.  The weights stay in registers.  Instructions bound a
+// for half of its life.  The weights stay in registers.  Instructions bound an
 // 8-bit output before the bytes do: a thread takes two or four vectors, so that
 // the sums over the CTA cost less of them, and y is not formed for it:
-// y / scale = (h w) (r / scale).
+// y / scale = (h w) (r / scale).  Measured, bf16, 32768 x 2048 with a residual:
+// to e4m3 in groups of 128 69 us (472 MB at 6.8 TB/s, as a plain copy), to bf16
+// 64; 8 rows 2.5 us.
 // C is a multiple of the vector's width; rows are 16-byte aligned.
 template <typename T, int NT, int V>
 __global__ void __launch_bounds__(NT, V <= 2 ? 1024 / NT : 1) norm_kernel(NormArgs a) {
@@ -214,7 +216,8 @@ __global__ void __launch_bounds__(NT, V <= 2 ? 1024 / NT : 1) norm_kernel(NormAr
 }
 
 // Any C: the row is read again after its sum of squares (and again for its
-// maximum), element by element.  Groups are not offered here.
+// maximum), element by element, from L2: 16384 x 2047 bf16 49 us, 2.7 TB/s.
+// Groups are not offered here.
 template <typename T>
 __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
     __shared__ float red[2][32];
@@ -269,10 +272,18 @@ void launch_v(const NormArgs &a, cudaStream_t stream) {
     norm_kernel<T, NT, V><<<resident<norm_kernel<T, NT, V>, NT>(a.rows), NT, 0, stream>>>(a);
 }
 
+// Four vectors a thread as far as there are rows' worth of them: the sums over
+// the CTA cost less (2048 bf16 columns, 32768 rows, residual, to e4m3 in groups
+// of 128: 256 threads of one vector 80 us, 128 of two 75, 64 of four 69; to bf16
+// 69, 65 and 64).  With eight the registers leave too few warps (4096 columns:
+// 97 us against 70).  A few rows are bound by a row's time, which more threads
+// make shorter (8 rows of 2048: 2.5 us with 128 threads, 3.1 with 64; 500 rows
+// 3.4 and 3.7).
 template <typename T>
 void launch_t(const NormArgs &a, cudaStream_t stream) {
     constexpr int N = Vec<T>::N;
     const int nv = a.C / N;
+    const bool few = a.rows <= 4 * device_sm_count();
     if (a.C % N != 0 || nv > 4096) {
         norm_any_kernel<T><<<(unsigned)a.rows, 256, 0, stream>>>(a);
     } else if (nv <= 32) {
@@ -280,9 +291,9 @@ void launch_t(const NormArgs &a, cudaStream_t stream) {
     } else if (nv <= 64) {
         launch_v<T, 32, 2>(a, stream);
     } else if (nv <= 128) {
-        launch_v<T, 64, 2>(a, stream);
+        few ? launch_v<T, 64, 2>(a, stream) : launch_v<T, 32, 4>(a, stream);
     } else if (nv <= 256) {
-        launch_v<T, 128, 2>(a, stream);
+        few ? launch_v<T, 128, 2>(a, stream) : launch_v<T, 64, 4>(a, stream);
     } else if (nv <= 512) {
         launch_v<T, 128, 4>(a, stream);
     } else if (nv <= 1024) {
@@ -299,7 +310,8 @@ constexpr int kBwdThreads = 256;
 
 // Rows blockIdx.x, + gridDim.x, ... ; each thread's columns are the same in
 // every row, so its share of dw stays in registers until the CTA's rows are
-// done.  part[blockIdx.x][C].  V vectors a thread, as norm_kernel.
+// done.  part[blockIdx.x][C].  V vectors a thread, as norm_kernel.  Bound by the
+// bytes: bf16, 16384 x 2048 with a residual's gradient 39 us, 268 MB at 6.8 TB/s.
 template <typename T, int V>
 __global__ void __launch_bounds__(kBwdThreads, V == 1 ? 4 : 1) norm_bwd_kernel(NormBwdArgs a, float *part) {
     constexpr int N = Vec<T>::N, NT = kBwdThreads;
@@ -391,6 +403,7 @@ __global__ void __launch_bounds__(kBwdThreads, V == 1 ? 4 : 1) norm_bwd_kernel(N
 }
 
 // Any C: rows are read twice; dw's share of a column is summed in `part`.
+// 16384 x 2047 bf16: 108 us.
 template <typename T>
 __global__ void __launch_bounds__(kBwdThreads) norm_bwd_any_kernel(NormBwdArgs a, float *part) {
     constexpr int NT = kBwdThreads;
@@ -421,7 +434,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_any_kernel(NormBwdArgs a
 }
 
 // dw[c] = the CTAs' shares: 32 columns a CTA, 32 strands of shares, then the
-// strands in order.
+// strands in order.  4 us for 2048 columns of 608 shares: latency.
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *part, float *dw, int n, int C) {
     __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, strand = threadIdx.x >> 5;

@@ -19,7 +19,9 @@ constexpr int kPlanThreads = 1024;
 
 // Copies page src[i] to page dst[i] of every layer, i < *count (or n where
 // count is null); src -1 writes zeros.  Entries out of range are skipped.
-// A CTA takes pieces of 16 KB in turn.
+// A CTA takes pieces of 16 KB in turn, four 16-byte words a thread in flight.
+// Bound by the bytes: 190 of 400 slots closed up in 6 layers of 1 MB pages, 1.25
+// GB, 190 to 206 us, 6.1 to 6.6 TB/s; one page copied 2.1 us.
 __global__ void __launch_bounds__(kThreads) move_kernel(PoolArgs p, const int *src, const int *dst, int n,
                                                         const int *count) {
     if (count) n = min(n, *count);
@@ -76,7 +78,8 @@ __device__ int block_scan(int x, int *total) {
 }
 
 // The i-th valid parent gets the i-th free page, lowest first; where none is
-// left, and for an invalid parent, the child is -1.
+// left, and for an invalid parent, the child is -1.  2.8 us for 64 slots: one
+// CTA's barriers and scans, as in compact_plan_kernel (3.1 us for 400).
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(unsigned char *live, int n_slots, const int *parents,
                                                                  int *children, int n, int *src, int *dst,
                                                                  int *free_slots) {

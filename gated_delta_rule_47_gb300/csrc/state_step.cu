@@ -29,6 +29,8 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
+// Measured, D 128, in place: 8192 heads 158 us for the delta rule and 156
+// without it, 1.07 GB at 6.8 TB/s, as a plain copy; 16 heads 2.4 us.
 // Grid: (Dv / W, H, B).  Thread (r, c): columns 4c..4c+3 of rows r, r + RP, ...
 template <typename T, int DK, int DV, int W, bool DELTA>
 __global__ void __launch_bounds__(kThreads) step_kernel(StepArgs a) {
@@ -142,9 +144,10 @@ __global__ void __launch_bounds__(kThreads) step_kernel(StepArgs a) {
 
 template <typename T, int DK, int DV, bool DELTA>
 void launch_w(const StepArgs &a, cudaStream_t stream) {
-    // A page's columns in one CTA where there are heads enough to fill the
-    // SMs twice over, else in slices of 32 columns.
-    if ((long long)a.B * a.H >= 2 * device_sm_count()) {
+    // Slices of 32 columns while their CTAs are few (32 heads, D 128: 2.6 us
+    // against 3.7), else a page's columns in one CTA, whose rows are whole
+    // lines (128 heads 4.0 us against 5.0, 8192 heads 158 against 196).
+    if ((long long)a.B * a.H * (DV / 32) > 2 * device_sm_count()) {
         step_kernel<T, DK, DV, DV, DELTA><<<dim3(1, a.H, a.B), kThreads, 0, stream>>>(a);
     } else {
         step_kernel<T, DK, DV, 32, DELTA><<<dim3(DV / 32, a.H, a.B), kThreads, 0, stream>>>(a);
