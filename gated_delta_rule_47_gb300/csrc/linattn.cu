@@ -414,12 +414,13 @@ __device__ __forceinline__ float row16(float x) {
 // dq and dk go to dqh, dkh [B,H,T,DK] fp32 where value heads share them.
 // Nine products on the CUDA cores: 1.05 ms for the same.
 template <typename T, int DK, int DV>
-__global__ void __launch_bounds__(kT) grad_kernel(LinAttnArgs a, View v, const float *S, const float *R, float *dqh,
+__global__ void __launch_bounds__(kT, DK + DV == 128 ? 2 : 1) grad_kernel(LinAttnArgs a, View v, const float *S, const float *R, float *dqh,
                                                   float *dkh, float *dgt, Strides sdg) {
     extern __shared__ __align__(16) float sm[];
     float *Q = sm, *K = Q + kC * ld<DK>(), *V = K + kC * ld<DK>(), *O = V + kC * ld<DV>();
-    // P by columns (P^T dO), N by rows and columns (N K, N^T Q); a slab of a state
-    float *PT = O + kC * ld<DV>(), *N = PT + kC * kP, *NT = N + kC * kP, *slab = NT + kC * kP;
+    // N by rows (N K), P by columns (P^T dO) and N by columns (N^T Q) in turn, from
+    // the threads' registers; a slab of a state
+    float *W = O + kC * ld<DV>(), *slab = W + kC * kP;
     constexpr int kSlabFloats = DK * kSlab > 64 * ld<DK>() ? DK * kSlab : 64 * ld<DK>();
     float *hi = slab + kSlabFloats, *lo = hi + kC, *te = lo + kC, *xq = te + kC, *xk = xq + kC, *xr = xk + kC, *xa = xr + kC, *red = xa + kC;
     const int ci = blockIdx.x, h = blockIdx.y;
@@ -451,8 +452,8 @@ __global__ void __launch_bounds__(kT) grad_kernel(LinAttnArgs a, View v, const f
     const float *Sc = S + ((long long)ci * a.H + h) * DK * DV, *Rc = R + ((long long)ci * a.H + h) * DK * DV;
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    float p[2][4] = {}, n[2][4] = {};
     {
-        float p[2][4] = {}, n[2][4] = {};
         tile::mm_nt<kT, 2, 4>(p, Q, ld<DK>(), K, ld<DK>(), DK);
         tile::mm_nt<kT, 2, 4>(n, O, ld<DV>(), V, ld<DV>(), DV);
 #pragma unroll
@@ -462,10 +463,10 @@ __global__ void __launch_bounds__(kT) grad_kernel(LinAttnArgs a, View v, const f
                 const int t = ty + 32 * i, s = tx + 16 * j;
                 const float f = s <= t ? a.scale * decay_between(hi[t], lo[t], hi[s], lo[s]) : 0.f;
                 const float nn = s <= t ? n[i][j] * f : 0.f;
-                PT[s * kP + t] = s <= t ? p[i][j] * f : 0.f;
-                N[t * kP + s] = nn;
-                NT[s * kP + t] = nn;
+                W[t * kP + s] = nn;
                 slab[t * 65 + s] = s < t ? p[i][j] * nn : 0.f;  // A
+                p[i][j] = s <= t ? p[i][j] * f : 0.f;
+                n[i][j] = nn;
             }
     }
     __syncthreads();
@@ -476,6 +477,12 @@ __global__ void __launch_bounds__(kT) grad_kernel(LinAttnArgs a, View v, const f
         for (int s = 0; s < kC; ++s) x += rows ? slab[t * 65 + s] : slab[s * 65 + t];
         (rows ? xa : xk)[t] = x;
     }
+    auto columns = [&](const float (&x)[2][4]) {  // into W, which has been read
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) W[(tx + 16 * j) * kP + ty + 32 * i] = x[i][j];
+    };
     constexpr int NB = DK / 64;
     // row sums of x against the rows of a tile
     auto along = [&](const float (&x)[2][4 * NB], const float *tile_, float *to) {
@@ -518,7 +525,7 @@ __global__ void __launch_bounds__(kT) grad_kernel(LinAttnArgs a, View v, const f
 #pragma unroll
             for (int j = 0; j < 4 * NB; ++j) acc[i][j] *= a.scale * expf(hi[ty + 32 * i]);
         along(acc, Q, xq);
-        mm_kn<kT, 2, NB>(acc, N, kP, K, ld<DK>(), kC);
+        mm_kn<kT, 2, NB>(acc, W, kP, K, ld<DK>(), kC);
         put(acc, dq, a.sq.t, dqh);
     }
     // dk and dv, with R in the same slabs, both ways round; <R, S> on the way
@@ -528,6 +535,7 @@ __global__ void __launch_bounds__(kT) grad_kernel(LinAttnArgs a, View v, const f
         for (int j0 = 0; j0 < DV; j0 += 64) {
             __syncthreads();
             load_slab_t<DK, DV>(slab, Rc, j0);
+            if (j0 == 0) columns(p);
             __syncthreads();
             mm_kn<kT, 2, NB>(acc, V + j0, ld<DV>(), slab, ld<DK>(), 64);
             __syncthreads();
@@ -544,7 +552,7 @@ __global__ void __launch_bounds__(kT) grad_kernel(LinAttnArgs a, View v, const f
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w[i][j] *= expf(te[ty + 32 * i]);
-            mm_kn<kT, 2, 1>(w, PT, kP, O + j0, ld<DV>(), kC);
+            mm_kn<kT, 2, 1>(w, W, kP, O + j0, ld<DV>(), kC);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (ty + 32 * i < c.len)
@@ -555,7 +563,10 @@ __global__ void __launch_bounds__(kT) grad_kernel(LinAttnArgs a, View v, const f
 #pragma unroll
             for (int j = 0; j < 4 * NB; ++j) acc[i][j] *= expf(te[ty + 32 * i]);
         along(acc, K, xr);
-        mm_kn<kT, 2, NB>(acc, NT, kP, Q, ld<DK>(), kC);
+        __syncthreads();
+        columns(n);
+        __syncthreads();
+        mm_kn<kT, 2, NB>(acc, W, kP, Q, ld<DK>(), kC);
         put(acc, dk, a.sk.t, dkh);
     }
 #pragma unroll
@@ -638,7 +649,7 @@ template <typename T, int DK, int DV>
 int run_bwd(const LinAttnArgs &a, const View &v, const BwdWs &w, cudaStream_t stream) {
     LA_TRY((run_states<T, DK, DV>(a, v, w.U, w.R, w.decay, stream)));
     constexpr int slab = DK * kSlab > 64 * ld<DK>() ? DK * kSlab : 64 * ld<DK>();
-    const int smem = 4 * (kC * (2 * ld<DK>() + 2 * ld<DV>() + 3 * kP) + slab + 7 * kC + 32);
+    const int smem = 4 * (kC * (2 * ld<DK>() + 2 * ld<DV>() + kP) + slab + 7 * kC + 32);
     LA_TRY(smem_limit(grad_kernel<T, DK, DV>, smem));
     const bool per_head = a.flags & GDN_G_PER_HEAD;
     const Strides whole{(long long)a.H * a.T, a.T, 1};

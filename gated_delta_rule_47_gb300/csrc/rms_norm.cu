@@ -111,9 +111,9 @@ __device__ __forceinline__ void store_e4m3(void *p, const float (&y)[N], float i
 // for half of its life.  The weights stay in registers.  Instructions bound an
 // 8-bit output before the bytes do: a thread takes two or four vectors, so that
 // the sums over the CTA cost less of them, and y is not formed for it:
-// y / scale = (h w) (r / scale).  Measured, bf16, 32768 x 2048 with a residual:
-// to e4m3 in groups of 128 69 us (472 MB at 6.8 TB/s, as a plain copy), to bf16
-// 64; 8 rows 2.5 us.
+// y / scale = (h w) (r / scale).  Measured, bf16, 32760 x 2048 with a residual:
+// to e4m3 in groups of 128 76 us (472 MB at 6.2 TB/s), to bf16 86 (6.2 TB/s);
+// 8 rows 2.5 us.
 // C is a multiple of the vector's width; rows are 16-byte aligned.
 template <typename T, int NT, int V>
 __global__ void __launch_bounds__(NT, V <= 2 ? 1024 / NT : 1) norm_kernel(NormArgs a) {
@@ -272,18 +272,13 @@ void launch_v(const NormArgs &a, cudaStream_t stream) {
     norm_kernel<T, NT, V><<<resident<norm_kernel<T, NT, V>, NT>(a.rows), NT, 0, stream>>>(a);
 }
 
-// Four vectors a thread as far as there are rows' worth of them: the sums over
-// the CTA cost less (2048 bf16 columns, 32768 rows, residual, to e4m3 in groups
-// of 128: 256 threads of one vector 80 us, 128 of two 75, 64 of four 69; to bf16
-// 69, 65 and 64).  With eight the registers leave too few warps (4096 columns:
-// 97 us against 70).  A few rows are bound by a row's time, which more threads
-// make shorter (8 rows of 2048: 2.5 us with 128 threads, 3.1 with 64; 500 rows
-// 3.4 and 3.7).
+// Two vectors a thread, four from 4096 bf16 columns on: one leaves the sums over
+// the CTA too large a share (32768 x 2048, a residual, to e4m3: 80 us against
+// 75), eight too few warps (4096 columns: 97 against 75).
 template <typename T>
 void launch_t(const NormArgs &a, cudaStream_t stream) {
     constexpr int N = Vec<T>::N;
     const int nv = a.C / N;
-    const bool few = a.rows <= 4 * device_sm_count();
     if (a.C % N != 0 || nv > 4096) {
         norm_any_kernel<T><<<(unsigned)a.rows, 256, 0, stream>>>(a);
     } else if (nv <= 32) {
@@ -291,9 +286,9 @@ void launch_t(const NormArgs &a, cudaStream_t stream) {
     } else if (nv <= 64) {
         launch_v<T, 32, 2>(a, stream);
     } else if (nv <= 128) {
-        few ? launch_v<T, 64, 2>(a, stream) : launch_v<T, 32, 4>(a, stream);
+        launch_v<T, 64, 2>(a, stream);
     } else if (nv <= 256) {
-        few ? launch_v<T, 128, 2>(a, stream) : launch_v<T, 64, 4>(a, stream);
+        launch_v<T, 128, 2>(a, stream);
     } else if (nv <= 512) {
         launch_v<T, 128, 4>(a, stream);
     } else if (nv <= 1024) {
@@ -308,21 +303,27 @@ void launch_t(const NormArgs &a, cudaStream_t stream) {
 // ------------------------------------------------------------------ backward
 constexpr int kBwdThreads = 256;
 
-// Rows blockIdx.x, + gridDim.x, ... ; each thread's columns are the same in
-// every row, so its share of dw stays in registers until the CTA's rows are
-// done.  part[blockIdx.x][C].  V vectors a thread, as norm_kernel.  Bound by the
-// bytes: bf16, 16384 x 2048 with a residual's gradient 39 us, 268 MB at 6.8 TB/s.
-template <typename T, int V>
-__global__ void __launch_bounds__(kBwdThreads, V == 1 ? 4 : 1) norm_bwd_kernel(NormBwdArgs a, float *part) {
-    constexpr int N = Vec<T>::N, NT = kBwdThreads;
-    __shared__ float red[2][2][NT / 32];
+// Rows by groups of NT of the CTA's threads, a row each in turn, V vectors a
+// thread as in norm_kernel: narrow rows would leave most of a CTA idle (512
+// columns, 131072 rows: 259 us with 256 threads a row).  A thread's columns are
+// the same in every row, so its share of dw stays in registers until the rows
+// are done; then the groups' shares are added in order to part[blockIdx.x][C].
+// Bound by the bytes: bf16, 16384 x 2048 with a residual's gradient 42 us, 268 MB
+// at 6.4 TB/s.
+template <typename T, int NT, int V>
+__global__ void __launch_bounds__(kBwdThreads, V == 1 ? 4 : V == 2 ? 2 : 1) norm_bwd_kernel(NormBwdArgs a, float *part) {
+    constexpr int N = Vec<T>::N, GROUPS = kBwdThreads / NT;
+    __shared__ float red[2][2][kBwdThreads / 32];
+    __shared__ float4 share[GROUPS > 1 ? kBwdThreads * N * V / 4 : 1];
     const int nv = a.C / N, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int group = threadIdx.x / NT, tid = threadIdx.x % NT, first = group * (NT / 32);
+    const long long step = (long long)gridDim.x * GROUPS;
     float dw[V][N], w[V][N];
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int e = 0; e < N; e += 4) {
-            const int i = j * NT + threadIdx.x;
+            const int i = j * NT + tid;
             float4 x = make_float4(1.f, 1.f, 1.f, 1.f);
             if (a.w && i < nv) x = __ldg(reinterpret_cast<const float4 *>(a.w) + (i * N + e) / 4);
             w[j][e] = x.x, w[j][e + 1] = x.y, w[j][e + 2] = x.z, w[j][e + 3] = x.w;
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(kBwdThreads, V == 1 ? 4 : 1) norm_bwd_kernel(N
         const uint4 *dr4 = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.dres) + row * a.C);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int i = j * NT + threadIdx.x;
+            const int i = j * NT + tid;
             nh[j] = nd[j] = nr[j] = make_uint4(0, 0, 0, 0);
             if (row < a.rows && i < nv) {
                 nh[j] = __ldcs(h4 + i);
@@ -345,12 +346,13 @@ __global__ void __launch_bounds__(kBwdThreads, V == 1 ? 4 : 1) norm_bwd_kernel(N
             }
         }
     };
-    fetch(blockIdx.x);
-    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
+    long long row = (long long)blockIdx.x * GROUPS + group;
+    fetch(row);
+    for (; row < a.rows; row += step, buf ^= 1) {
         uint4 ph[V], pd[V], pr[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) ph[j] = nh[j], pd[j] = nd[j], pr[j] = nr[j];
-        fetch(row + gridDim.x);
+        fetch(row + step);
         float ss = 0.f, sp = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -368,17 +370,21 @@ __global__ void __launch_bounds__(kBwdThreads, V == 1 ? 4 : 1) norm_bwd_kernel(N
             ss += __shfl_xor_sync(~0u, ss, m);
             sp += __shfl_xor_sync(~0u, sp, m);
         }
-        if (lane == 0) red[buf][0][warp] = ss, red[buf][1][warp] = sp;
-        __syncthreads();  // one a row: the buffers alternate
-        ss = sp = 0.f;
+        if constexpr (NT > 32) {
+            if (lane == 0) red[buf][0][warp] = ss, red[buf][1][warp] = sp;
+            // one a row, of the group's threads: the buffers alternate
+            if constexpr (GROUPS == 1) __syncthreads();
+            else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(NT) : "memory");
+            ss = sp = 0.f;
 #pragma unroll
-        for (int i = 0; i < NT / 32; ++i) ss += red[buf][0][i], sp += red[buf][1][i];
+            for (int i = 0; i < NT / 32; ++i) ss += red[buf][0][first + i], sp += red[buf][1][first + i];
+        }
         const float r = rsqrtf(ss / a.C + a.eps);
         const float m = r * r * (sp / a.C);
         uint4 *dx = reinterpret_cast<uint4 *>(static_cast<T *>(a.dx) + row * a.C);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int i = j * NT + threadIdx.x;
+            const int i = j * NT + tid;
             float h[N], d[N], g[N];
             Vec<T>::unpack(ph[j], h);
             Vec<T>::unpack(pd[j], d);
@@ -391,14 +397,28 @@ __global__ void __launch_bounds__(kBwdThreads, V == 1 ? 4 : 1) norm_bwd_kernel(N
             if (i < nv) __stcs(dx + i, Vec<T>::pack(g));
         }
     }
+    float4 *to = reinterpret_cast<float4 *>(part + (size_t)blockIdx.x * a.C);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int i = j * NT + threadIdx.x;
-        if (i < nv)
+        const int i = j * NT + tid;
 #pragma unroll
-            for (int e = 0; e < N; e += 4)
-                reinterpret_cast<float4 *>(part + (size_t)blockIdx.x * a.C)[(i * N + e) / 4] =
-                    make_float4(dw[j][e], dw[j][e + 1], dw[j][e + 2], dw[j][e + 3]);
+        for (int e = 0; e < N; e += 4) {
+            const float4 x = make_float4(dw[j][e], dw[j][e + 1], dw[j][e + 2], dw[j][e + 3]);
+            if constexpr (GROUPS > 1) share[(group * V * NT + i) * (N / 4) + e / 4] = x;
+            else if (i < nv) to[(i * N + e) / 4] = x;
+        }
+    }
+    if constexpr (GROUPS > 1) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < a.C / 4; i += kBwdThreads) {
+            float4 x = share[i];
+#pragma unroll
+            for (int g = 1; g < GROUPS; ++g) {
+                const float4 y = share[g * V * NT * (N / 4) + i];
+                x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+            }
+            to[i] = x;
+        }
     }
 }
 
@@ -470,9 +490,12 @@ template <typename T>
 int launch_bwd_t(const NormBwdArgs &a, int most, float *part, cudaStream_t stream) {
     const int nv = a.C / Vec<T>::N;
     if (a.C % Vec<T>::N != 0 || nv > 4 * kBwdThreads) return launch_rows<norm_bwd_any_kernel<T>>(a, most, part, stream);
-    if (nv <= kBwdThreads) return launch_rows<norm_bwd_kernel<T, 1>>(a, most, part, stream);
-    if (nv <= 2 * kBwdThreads) return launch_rows<norm_bwd_kernel<T, 2>>(a, most, part, stream);
-    return launch_rows<norm_bwd_kernel<T, 4>>(a, most, part, stream);
+    if (nv <= 32) return launch_rows<norm_bwd_kernel<T, 32, 1>>(a, most, part, stream);
+    if (nv <= 64) return launch_rows<norm_bwd_kernel<T, 64, 1>>(a, most, part, stream);
+    if (nv <= 128) return launch_rows<norm_bwd_kernel<T, 128, 1>>(a, most, part, stream);
+    if (nv <= kBwdThreads) return launch_rows<norm_bwd_kernel<T, kBwdThreads, 1>>(a, most, part, stream);
+    if (nv <= 2 * kBwdThreads) return launch_rows<norm_bwd_kernel<T, kBwdThreads, 2>>(a, most, part, stream);
+    return launch_rows<norm_bwd_kernel<T, kBwdThreads, 4>>(a, most, part, stream);
 }
 
 }  // namespace
