@@ -308,8 +308,8 @@ constexpr int kBwdThreads = 256;
 // columns, 131072 rows: 259 us with 256 threads a row).  A thread's columns are
 // the same in every row, so its share of dw stays in registers until the rows
 // are done; then the groups' shares are added in order to part[blockIdx.x][C].
-// Bound by the bytes: bf16, 16384 x 2048 with a residual's gradient 42 us, 268 MB
-// at 6.4 TB/s.
+// Bound by the bytes: bf16, 16384 x 2048 with a residual's gradient 41 us, 268 MB
+// at 6.6 TB/s.
 template <typename T, int NT, int V>
 __global__ void __launch_bounds__(kBwdThreads, V == 1 ? 4 : V == 2 ? 2 : 1) norm_bwd_kernel(NormBwdArgs a, float *part) {
     constexpr int N = Vec<T>::N, GROUPS = kBwdThreads / NT;
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_any_kernel(NormBwdArgs a
 }
 
 // dw[c] = the CTAs' shares: 32 columns a CTA, 32 strands of shares, then the
-// strands in order.  4 us for 2048 columns of 608 shares: latency.
+// strands in order.  3 us for 2048 columns of 304 shares: latency.
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *part, float *dw, int n, int C) {
     __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, strand = threadIdx.x >> 5;
@@ -490,10 +490,12 @@ template <typename T>
 int launch_bwd_t(const NormBwdArgs &a, int most, float *part, cudaStream_t stream) {
     const int nv = a.C / Vec<T>::N;
     if (a.C % Vec<T>::N != 0 || nv > 4 * kBwdThreads) return launch_rows<norm_bwd_any_kernel<T>>(a, most, part, stream);
+    // two vectors a thread, whose loads cover more of a row's sums than one's
+    // (bf16, 131072 x 512: 82 us against 102)
     if (nv <= 32) return launch_rows<norm_bwd_kernel<T, 32, 1>>(a, most, part, stream);
-    if (nv <= 64) return launch_rows<norm_bwd_kernel<T, 64, 1>>(a, most, part, stream);
-    if (nv <= 128) return launch_rows<norm_bwd_kernel<T, 128, 1>>(a, most, part, stream);
-    if (nv <= kBwdThreads) return launch_rows<norm_bwd_kernel<T, kBwdThreads, 1>>(a, most, part, stream);
+    if (nv <= 64) return launch_rows<norm_bwd_kernel<T, 32, 2>>(a, most, part, stream);
+    if (nv <= 128) return launch_rows<norm_bwd_kernel<T, 64, 2>>(a, most, part, stream);
+    if (nv <= 256) return launch_rows<norm_bwd_kernel<T, 128, 2>>(a, most, part, stream);
     if (nv <= 2 * kBwdThreads) return launch_rows<norm_bwd_kernel<T, kBwdThreads, 2>>(a, most, part, stream);
     return launch_rows<norm_bwd_kernel<T, kBwdThreads, 4>>(a, most, part, stream);
 }
