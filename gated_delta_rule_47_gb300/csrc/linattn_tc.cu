@@ -152,11 +152,21 @@ struct Plan {
     int rows;         // places
 };
 
+// A backward whose walks are cut into pieces of `len` chunks (0: they are not):
+// the shares of the pieces first, in a launch of their own.
+struct Cut {
+    View pieces;   // chunks of len * kC tokens
+    int len;
+    float *share;  // [piece][direction][H][DV / 64][DK][64]
+    float *decay;  // [piece][direction][H]
+};
+
 // What the tensor-core kernels take besides their maps.
 struct TcArgs {
     LinAttnArgs a;
     View v;
     Plan plan;
+    Cut cut;
     uint16_t *S[3], *R[3];  // [chunk][H][DK][DV], in three bf16 terms: the states that enter the chunks, and the
                             // gradients of those that leave them
     float *gates;         // [chunk][H][4][128] decays for the gradients, see state_kernel
@@ -308,7 +318,7 @@ struct StateSmem {
 };
 static_assert(StateSmem<128>::BYTES <= 232448, "state kernel fits the shared memory of one CTA");
 
-// Grid (2 DV / 64, H, n_seq): the states that enter a sequence's chunks, and
+// Grid (2 DV / 64, H, n_seq or pieces): the states that enter a sequence's chunks, and
 // (the second half of x) backwards over them the gradients of the states that
 // leave them, with Q and dO in the places of K and V.  They go out as three
 // bf16 terms, which the gradients' products take as operands: dg is fp32, and
@@ -316,7 +326,9 @@ static_assert(StateSmem<128>::BYTES <= 232448, "state kernel fits the shared mem
 // Bound by what it writes, 48 KB a CTA and chunk, and by the waves of CTAs: 125
 // us at B4 H16 T4096 (670 MB, 256 CTAs on 152 SMs), 1.7 us a chunk alone.  Two
 // smaller CTAs an SM wait for each other's stores and were no faster.
-template <int DK, int DV>
+// SHARE: a piece's share of the state after it (before it, backwards) and
+// nothing else; the walk of a piece then starts from the shares on its way.
+template <int DK, int DV, bool SHARE>
 __global__ void __launch_bounds__(kStateThreads, 1)
     state_kernel(const __grid_constant__ GradMaps m, TcArgs p) {
     using L = StateSmem<DK>;
@@ -327,13 +339,25 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     float *dring = reinterpret_cast<float *>(wring + kWRing * 384);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool rev = blockIdx.x >= DV / 64;
-    const int slice = blockIdx.x % (DV / 64), h = blockIdx.y, seq = blockIdx.z;
+    const int slice = blockIdx.x % (DV / 64), h = blockIdx.y;
+    int seq = blockIdx.z, first = 0, pieces = 1, piece = 0;  // its sequence's pieces, and which it is
+    if (p.cut.len) {
+        const int z = blockIdx.z, over = z - p.cut.pieces.n_chunks;
+        seq = over >= 0 ? over : p.a.cu ? p.cut.pieces.chunks[z].w : z / p.cut.pieces.per_row;
+        if (seq < 0) return;  // tokens of no sequence
+        const int2 all = seq_at(p.cut.pieces, seq);
+        if (over >= 0 && all.y) return;  // those of sequences without tokens
+        first = all.x, pieces = max(all.y, 1), piece = over >= 0 ? 0 : z - first;
+        if (piece >= pieces) return;
+        if (SHARE && (over >= 0 || piece == (rev ? 0 : pieces - 1))) return;
+    }
     const Span sp = span_of(p.a, seq);
     const int2 sq = seq_at(p.v, seq);
-    const int n = sq.y, row0 = p.a.cu ? 0 : seq;
+    const int c0 = piece * p.cut.len, n = p.cut.len ? min(p.cut.len, sq.y - c0) : sq.y, row0 = p.a.cu ? 0 : seq;
     const uint64_t end = deadline_after(p.timeout_ns, n);
-    auto number = [&](int i) { return rev ? n - 1 - i : i; };
+    auto number = [&](int i) { return c0 + (rev ? n - 1 - i : i); };
     auto chunk = [&](int i) { return Chunk{row0, sp.start + number(i) * kC, min(kC, sp.len - number(i) * kC), seq}; };
+    auto share_of = [&](int i) { return ((size_t)(first + i) * 2 + rev) * p.a.H + h; };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -423,7 +447,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         // the weights: e^{G - c_t}, or backwards scale e^{c_t}; the next chunk's
         // gates are on their way meanwhile
         const bool per_head = p.a.flags & GDN_G_PER_HEAD;
-        float next[4];
+        float next[4], whole = 0.f;
         auto fetch = [&](int i) {
             if (i >= n) return;
             load_gates<kC>(gate_ptr(p.a, chunk(i), h), p.a.sg.t, chunk(i).len, per_head, next);
@@ -439,11 +463,11 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 wt[j] = split_weight(rev ? p.a.scale * expf(g.cum[j].hi) : expf(g.to_end(j)));
-            if (blockIdx.x == 0) {
+            if (!SHARE && blockIdx.x == 0) {
                 // the gradient kernel's decays: c_t as a pair, G - c_t, and
                 // e^{c_r - c_t} with r the last token of t's block of 32
                 const float rh = __shfl_sync(~0u, g.cum[3].hi, lane | 7), rl = __shfl_sync(~0u, g.cum[3].lo, lane | 7);
-                float4 *out = reinterpret_cast<float4 *>(p.gates + ((size_t)(sq.x + i) * p.a.H + h) * 512) + lane;
+                float4 *out = reinterpret_cast<float4 *>(p.gates + ((size_t)(sq.x + number(i)) * p.a.H + h) * 512) + lane;
                 float cf[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) cf[j] = expf(((rh - g.cum[j].hi) + (rl - g.cum[j].lo)));
@@ -457,6 +481,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             ws[lane + 32] = make_uint4(wt[0].m, wt[1].m, wt[2].m, wt[3].m);
             ws[lane + 64] = make_uint4(wt[0].l, wt[1].l, wt[2].l, wt[3].l);
             if (lane == 0) dring[w] = expf(g.all.hi);
+            whole += g.all.hi;
+            if (SHARE && slice == 0 && i == n - 1 && lane == 0) p.cut.decay[share_of(piece)] = expf(whole);
             mbar_arrive(&bars[L::WFULL + w]);
         }
     } else if (warp >= 8) {
@@ -515,7 +541,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         const int row = 32 * (warp & 3) + lane;
         const bool mine = row < DK;
         float S[64];
-        const float *from = rev ? p.a.dsf : p.a.s0;
+        const int start = rev ? pieces - 1 : 0;  // the piece where the sequence's walk starts
+        const float *from = piece != start ? nullptr : rev ? p.a.dsf : p.a.s0;
         const size_t page = (((size_t)seq * p.a.H + h) * DK + row) * DV + 64 * slice;
 #pragma unroll
         for (int e = 0; e < 64; e += 4) {
@@ -523,10 +550,23 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             if (mine && from) x = *reinterpret_cast<const float4 *>(from + page + e);
             S[e] = x.x, S[e + 1] = x.y, S[e + 2] = x.z, S[e + 3] = x.w;
         }
+        if (!SHARE && mine)
+#pragma unroll 1
+            for (int j = start; j != piece; j += rev ? -1 : 1) {  // the shares on the way, the first with s0 in it
+                const float d = j == start ? 0.f : p.cut.decay[share_of(j)];
+                const float4 *x4 = reinterpret_cast<const float4 *>(p.cut.share + ((share_of(j) * (DV / 64) + slice) * DK + row) * 64);
+#pragma unroll
+                for (int e = 0; e < 64; e += 4) {
+                    const float4 x = x4[e / 4];
+                    S[e] = fmaf(d, S[e], x.x), S[e + 1] = fmaf(d, S[e + 1], x.y);
+                    S[e + 2] = fmaf(d, S[e + 2], x.z), S[e + 3] = fmaf(d, S[e + 3], x.w);
+                }
+            }
         bool ok = true;
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
             const int acc = i & 1, w = i % kWRing;
+            if constexpr (!SHARE) {
             // the terms leave through a tile each, whole lines at a time: by the
             // threads' own stores, 32 bytes of 32 lines an instruction, the walks
             // took 167 us (B4 H16 T4096)
@@ -561,8 +601,12 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 for (int e = 0; e < 3; ++e) tma_store_3d(rev ? &m.r[e] : &m.s[e], sm + L::OUT + e * DK * 128, 64 * slice, 0, item);
                 tma_store_commit();
             }
+            }
             ok = warp_ok(la_wait(&bars[L::WFULL + w], (i / kWRing) & 1, end) && la_wait(&bars[L::UFULL + acc], (i >> 1) & 1, end));
-            if (!ok) continue;
+            if (!ok) {
+                if (SHARE) break;
+                continue;
+            }
             const float d = dring[w];
             tc_fence_after_sync();
 #pragma unroll
@@ -577,12 +621,14 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             mbar_arrive(&bars[L::UEMPTY + acc]);
             mbar_arrive(&bars[L::WEMPTY + w]);
         }
-        if (threadIdx.x == 128) tma_store_wait_all<0>();
-        float *to = rev ? p.a.ds0 : p.a.sf;
+        if (!SHARE && threadIdx.x == 128) tma_store_wait_all<0>();
+        float *to = SHARE                               ? p.cut.share + ((share_of(piece) * (DV / 64) + slice) * DK + row) * 64
+                    : piece != (rev ? 0 : pieces - 1)   ? nullptr
+                    : rev                               ? (p.a.ds0 ? p.a.ds0 + page : nullptr)
+                                                        : nullptr;
         if (to && mine && ok)
 #pragma unroll
-            for (int e = 0; e < 64; e += 4)
-                *reinterpret_cast<float4 *>(to + page + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+            for (int e = 0; e < 64; e += 4) *reinterpret_cast<float4 *>(to + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
     }
     __syncwarp();
     tc_fence_before_sync();
@@ -631,6 +677,7 @@ constexpr uint32_t TM_T = 0, TM_OS = 256, TM_OP = 384, TM_U = 448;
 // start and end kItemCost, a share that a piece adds up kJoinCost, making the
 // plan kPlanCost.
 constexpr int kSms = 152, kShareItems = 4 * kSms, kMostPieces = 16;
+constexpr float kCutShare = 0.6f;  // a share's chunk in the backward's walks
 constexpr float kShareCost = 0.45f, kItemCost = 2.5f, kJoinCost = 0.4f, kPlanCost = 1.5f;
 // With the longest sequence in p pieces of up to len chunks: chunks and shared
 // chunks of the call (over heads and columns), its items and shares.  What runs
@@ -1980,9 +2027,34 @@ int run_fwd(const TcArgs &p, cudaStream_t stream) {
     return a.sf ? launch_prompt<DK, DV, 3>(mQ, mK, mV, w, stream) : launch_prompt<DK, DV, 2>(mQ, mK, mV, w, stream);
 }
 
+// Chunks of a piece of the backward's walks (0: they are not cut), as plan_len:
+// two launches of the walks' CTAs, of which the shares write no states.  Where
+// the CTAs fill the SMs a chunk takes 1.4 of its time alone (the bytes bound it).
+// D 128: 1 x 32768 tokens of 4 heads 115 us, uncut 404; 1 x 4096 of one head 29
+// and 55; but of 16 heads 490 and 451, which are left uncut.
+int cut_len(const LinAttnArgs &a) {
+    const int slots = 2 * a.H * (a.Dv / 64), seqs = a.cu ? 1 : a.B;
+    const int n = (int)(((long long)a.T + kC - 1) / kC);
+    auto pass = [](long long items, int len) {
+        return items <= kSms ? (float)len : fmaxf((float)len, 1.4f * items * len / kSms + 0.5f * len);
+    };
+    float best = (a.cu ? 0.6f : 0.8f) * pass((long long)seqs * slots, n);
+    int found = 0;
+    for (int p = 2; p <= kMostPieces; ++p) {
+        const int len = (n + p - 1) / p, k = pieces_of(n, len);
+        if (((long long)chunk_bound(a, len * kC)) * slots > 2 * kShareItems) break;
+        const float cost = kCutShare * pass((long long)seqs * slots * (k - 1), len) + pass((long long)seqs * slots * k, len) +
+                           2 * kItemCost + kJoinCost * k;
+        if (cost < best) best = cost, found = len;
+    }
+    return found;
+}
+
 struct BwdWs {
     char *S[6];  // the terms of S, then R's
-    float *gates, *dqh, *dkh, *dgt;
+    float *gates, *dqh, *dkh, *dgt, *share, *decay;
+    void *tables;  // the pieces'
+    int len;
     size_t bytes;
 };
 
@@ -1991,12 +2063,18 @@ BwdWs bwd_ws(const LinAttnArgs &a, void *ws) {
     const size_t heads = a.H != a.Hk ? up(4 * (size_t)a.B * a.H * a.T * a.Dk) : 0;
     // 1024-byte alignment for the kernels' wide stores, whatever the caller's
     char *p = reinterpret_cast<char *>(up(reinterpret_cast<uintptr_t>(ws) + table_bytes(a, kC)));
-    BwdWs w;
+    BwdWs w{};
     for (char *&s : w.S) s = p, p += states;
     w.gates = reinterpret_cast<float *>(p), p += up(2048 * (size_t)chunk_bound(a, kC) * a.H);
     w.dqh = reinterpret_cast<float *>(p), p += heads;
     w.dkh = reinterpret_cast<float *>(p), p += heads;
     w.dgt = reinterpret_cast<float *>(p), p += (a.flags & GDN_G_PER_HEAD) ? up(4 * (size_t)a.B * a.H * a.T) : 0;
+    if ((w.len = cut_len(a))) {
+        const size_t pieces = chunk_bound(a, w.len * kC);
+        w.tables = p, p += up(table_bytes(a, w.len * kC));
+        w.share = reinterpret_cast<float *>(p), p += up(8 * pieces * a.H * a.Dk * a.Dv);
+        w.decay = reinterpret_cast<float *>(p), p += up(8 * pieces * a.H);
+    }
     w.bytes = p - static_cast<char *>(ws) + 1024;
     return w;
 }
@@ -2017,11 +2095,19 @@ int run_bwd(const TcArgs &p, cudaStream_t stream) {
         !strided_map(&m.dq, a.dq, a.sq, a.B, a.Hk, a.T, DK, kC) || !strided_map(&m.dk, a.dk, a.sk, a.B, a.Hk, a.T, DK, kC) ||
         !strided_map(&m.dv, a.dv, a.sv, a.B, a.H, a.T, DV, kC))
         return GDN_ERR_CUDA;
-    if (!smem_limit<state_kernel<DK, DV>>(StateSmem<DK>::BYTES) || !smem_limit<grad_kernel_tc<DK, DV>>(GradSmem::BYTES))
+    constexpr uint32_t bytes = StateSmem<DK>::BYTES;
+    if (!smem_limit<state_kernel<DK, DV, false>>(bytes) || !smem_limit<state_kernel<DK, DV, true>>(bytes) ||
+        !smem_limit<grad_kernel_tc<DK, DV>>(GradSmem::BYTES))
         return GDN_ERR_CUDA;
-    state_kernel<DK, DV><<<dim3(2 * DV / 64, a.H, a.n_seq), kStateThreads, StateSmem<DK>::BYTES, stream>>>(m, p);
-    const int st = launched();
-    if (st != GDN_OK) return st;
+    int st = GDN_OK;
+    dim3 grid(2 * DV / 64, a.H, a.n_seq);
+    if (p.cut.len) {
+        grid.z = p.cut.pieces.n_chunks + (a.cu ? a.n_seq : 0);
+        state_kernel<DK, DV, true><<<grid, kStateThreads, bytes, stream>>>(m, p);
+        if ((st = launched()) != GDN_OK) return st;
+    }
+    state_kernel<DK, DV, false><<<grid, kStateThreads, bytes, stream>>>(m, p);
+    if ((st = launched()) != GDN_OK) return st;
     const long long items = (long long)p.v.n_chunks * a.H;
     const int sms = device_sm_count();
     grad_kernel_tc<DK, DV><<<(unsigned)(items < sms ? items : sms), kGradThreads, GradSmem::BYTES, stream>>>(m, p);
@@ -2065,6 +2151,11 @@ int launch_linattn_tc_bwd(const LinAttnArgs &a, cudaStream_t stream) {
     for (int i = 0; i < 3; ++i) {
         p.S[i] = reinterpret_cast<uint16_t *>(w.S[i]);
         p.R[i] = reinterpret_cast<uint16_t *>(w.S[3 + i]);
+    }
+    if (w.len) {
+        st = make_view(a, w.len * kC, w.tables, &p.cut.pieces, stream);
+        if (st != GDN_OK) return st;
+        p.cut.len = w.len, p.cut.share = w.share, p.cut.decay = w.decay;
     }
     p.gates = w.gates, p.dqh = w.dqh, p.dkh = w.dkh;
     const bool per_head = a.flags & GDN_G_PER_HEAD;
