@@ -1406,7 +1406,11 @@ __device__ __forceinline__ float column_sums(float (&x)[16]) {
 // the split ones.  Bound by the bytes and the chain of products and arithmetic
 // behind them: 320 KB in, 96 KB out a chunk; at B4 H16 T4096, D 128, 171 us,
 // 852 MB at 5.0 TB/s (74% of a plain copy's rate).
-template <int DK, int DV>
+// FEW: P and N of chunks of up to 64 tokens go into their products in two bf16
+// terms, in the tiles' other half: few pairs do not average the rounding out, and
+// heads that share keys may cancel (1 token: dq 1e-2 off with one term).  A kernel
+// of its own, as it costs the long ones 186 us in place of 171 (code and registers).
+template <int DK, int DV, bool FEW>
 __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_constant__ GradMaps m, TcArgs p) {
     using L = GradSmem;
     using T = __nv_bfloat16;
@@ -1621,6 +1625,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
                 fence_proxy_async_smem();
                 if (ok) mbar_arrive(&bars[L::TAIL]);
             }
+            const bool half = FEW && c.len <= 64;
             float rowa = 0.f, cola[2] = {0.f, 0.f}, dot = 0.f, xt = 0.f, yt = 0.f;
             wait(L::GT);
             wait(L::CT);
@@ -1634,10 +1639,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
             for (int k = 0; k < 2 && ok; ++k) {
                 const int sb = 16 * (4 * k + four), diag = 32 * (warp & 3);
                 uint32_t u[16];
+                if (half && k) break;  // the second terms are there
                 if (sb >= diag + 32) {  // past the diagonal for every row of the warp
 #pragma unroll
                     for (int j = 0; j < 16; ++j) u[j] = 0u;
                     tmem_st16(lanes + TM_A + sb, u);
+                    if (half) tmem_st16(lanes + TM_A + 64 + sb, u);
                     continue;
                 }
                 uint32_t w[16];
@@ -1679,6 +1686,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
                     rowa += a[2 * j] + a[2 * j + 1];
                 }
                 tmem_st16(lanes + TM_A + sb, pn);  // until their tiles' places are free
+                if (half) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        pn[j] = pack_bf16(__uint_as_float(u[2 * j]) - __uint_as_float(pn[j] << 16),
+                                          __uint_as_float(u[2 * j + 1]) - __uint_as_float(pn[j] & 0xffff0000u));
+                        pn[j + 8] = pack_bf16(__uint_as_float(w[2 * j]) - __uint_as_float(pn[j + 8] << 16),
+                                              __uint_as_float(w[2 * j + 1]) - __uint_as_float(pn[j + 8] & 0xffff0000u));
+                    }
+                    tmem_st16(lanes + TM_A + 64 + sb, pn);
+                }
                 const float sum = column_sums(a);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) cola[j] = j == k ? sum : cola[j];
@@ -1720,6 +1737,40 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
                 // R's last term and V have been multiplied, and read by all: N and P
                 // take their places
                 tmem_wait_st();
+                if (half) {
+                    // rows 64.. repeat the rows 64 before them, for the second terms
+                    auto repeat = [&](uint32_t tile_at, int d) {
+                        for (int e = four * (d / 4); e < (four + 1) * (d / 4); e += 8) {
+                            uint8_t *x = sm + tile_at + (e >> 6) * 16384 + sw128_offset(t, e & 63);
+                            *reinterpret_cast<uint4 *>(x) = *reinterpret_cast<const uint4 *>(x - 8192);
+                        }
+                    };
+                    if (warp & 2) {
+                        repeat(L::Q, DK);
+                        repeat(L::K, DK);
+                        repeat(L::O, DV);
+                    } else {
+                        const uint32_t at_[2] = {sw128_offset(t, 16 * four), sw128_offset(t, 16 * four + 8)};
+#pragma unroll 1
+                        for (int k = 0; k < 2; ++k) {  // first and second terms: P | N of 16 columns
+                            uint32_t pn[16];
+                            tmem_ld16(lanes + TM_A + 64 * k + 16 * four, pn);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const uint4 zero = make_uint4(0, 0, 0, 0);
+                                const uint4 pp = make_uint4(pn[4 * x], pn[4 * x + 1], pn[4 * x + 2], pn[4 * x + 3]);
+                                const uint4 nn = make_uint4(pn[4 * x + 8], pn[4 * x + 9], pn[4 * x + 10], pn[4 * x + 11]);
+                                uint8_t *v = sm + L::V + at_[x], *y = sm + L::Y + at_[x];
+                                *reinterpret_cast<uint4 *>(v + 8192 * k) = pp;
+                                *reinterpret_cast<uint4 *>(v + 16384 + 8192 * k) = zero;
+                                *reinterpret_cast<uint4 *>(y + 8192 * k) = nn;
+                                *reinterpret_cast<uint4 *>(y + 16384 + 8192 * k) = zero;
+                                if (k) *reinterpret_cast<uint4 *>(y + 16384) = nn;
+                            }
+                        }
+                    }
+                } else
 #pragma unroll 1
                 for (int k = 0; k < 2; ++k) {
                     const int sb = 16 * (4 * k + four);
@@ -2097,7 +2148,7 @@ int run_bwd(const TcArgs &p, cudaStream_t stream) {
         return GDN_ERR_CUDA;
     constexpr uint32_t bytes = StateSmem<DK>::BYTES;
     if (!smem_limit<state_kernel<DK, DV, false>>(bytes) || !smem_limit<state_kernel<DK, DV, true>>(bytes) ||
-        !smem_limit<grad_kernel_tc<DK, DV>>(GradSmem::BYTES))
+        !smem_limit<grad_kernel_tc<DK, DV, false>>(GradSmem::BYTES) || !smem_limit<grad_kernel_tc<DK, DV, true>>(GradSmem::BYTES))
         return GDN_ERR_CUDA;
     int st = GDN_OK;
     dim3 grid(2 * DV / 64, a.H, a.n_seq);
@@ -2110,7 +2161,10 @@ int run_bwd(const TcArgs &p, cudaStream_t stream) {
     if ((st = launched()) != GDN_OK) return st;
     const long long items = (long long)p.v.n_chunks * a.H;
     const int sms = device_sm_count();
-    grad_kernel_tc<DK, DV><<<(unsigned)(items < sms ? items : sms), kGradThreads, GradSmem::BYTES, stream>>>(m, p);
+    const unsigned ctas = (unsigned)(items < sms ? items : sms);
+    // sequences of up to 64 tokens, or packed ones of no more on average
+    if (a.T <= 64LL * (a.cu ? a.n_seq : 1)) grad_kernel_tc<DK, DV, true><<<ctas, kGradThreads, GradSmem::BYTES, stream>>>(m, p);
+    else grad_kernel_tc<DK, DV, false><<<ctas, kGradThreads, GradSmem::BYTES, stream>>>(m, p);
     return launched();
 }
 

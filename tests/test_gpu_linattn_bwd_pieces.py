@@ -57,3 +57,18 @@ def test_cleared_states():
     want = ref.linattn_bwd(d["q"], d["k"], d["v"], d["g"], d["do"], d["s0"], d["dsf"])
     for name, x, r, tol in zip(("dq", "dk", "dv", "dg", "ds0"), got, want, (TOL_BF16,) * 3 + (1e-4, 1e-5)):
         assert rel_err(x, r) <= tol, name
+
+
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (128, 128), (64, 128)])
+@pytest.mark.parametrize("T,lens", [(1, None), (3, None), (64, None), (90, [1, 1, 64, 0, 24])])
+def test_few_tokens_of_heads_that_cancel(T, lens, Dk, Dv):
+    """Two value heads of one key whose gradients nearly cancel in dq and dk: what
+    remains is 2^-4 of them, so that a term rounded to bf16 (2^-9) would be 2^-5 off."""
+    d = inputs(2 if lens is None else 1, 2, 1, T, Dk, Dv, "bf16", 17, lens)
+    d["g"][:, 1] = d["g"][:, 0]
+    d["do"][:, 1] = -(d["do"][:, 0].float() * 1.0625).bfloat16()
+    d["v"][:, 1] = d["v"][:, 0]
+    got = binding.linattn_chunk_bwd(d["q"], d["k"], d["v"], d["g"], d["do"], cu_seqlens=None if lens is None else offsets(lens))
+    want = ref.linattn_bwd(d["q"], d["k"], d["v"], d["g"], d["do"], None, None, lens)
+    for name, x, r in zip(("dq", "dk", "dv"), got, want):
+        assert rel_err(x, r) <= TOL_BF16, name
