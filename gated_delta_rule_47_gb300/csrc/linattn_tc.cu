@@ -727,7 +727,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(LinAttnArgs a, Plan 
             r = __reduce_add_sync(~0u, r), c = __reduce_add_sync(~0u, c);
             if (lane == 0)
                 costs[p] = r > pl.rows ? 1e30f
-                                       : plan_cost((long long)all * slots, (long long)c * slots, most, (some + 2ll * r) * slots, (long long)r * slots, p);
+                                       : plan_cost((long long)all * slots, (long long)c * slots, most,
+                                                   (some + 2ll * r) * slots, (long long)r * slots, p);
         }
         __syncthreads();
         if (threadIdx.x == 0) {
@@ -902,451 +903,451 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
 #pragma unroll 1
     for (;;) {
-    const Item &it = *item;
-    // the same in all lanes, which the compiler is to see (uniform registers)
-    auto same = [](int x) { return __shfl_sync(~0u, x, 0); };
-    const int kind = same(it.kind);
-    if (kind == kNone) break;
-    const bool share = PLANNED && kind == kShare;
-    const int slice = it.slot % (DV / 64), h = it.slot / (DV / 64), seq = it.seq, row = p.a.cu ? 0 : seq;
-    const int tokens = same(it.tokens), t0 = same(it.t0), n = (tokens + kC - 1) / kC;
-    const int base = PLANNED ? same(it.base) : 0, full = PLANNED ? same(it.full) : 0;
-    auto chunk = [&](int i) { return Chunk{row, t0 + i * kC, min(kC, tokens - i * kC), seq}; };
-    const uint64_t &end = it.end;
-    bool ok = true;
-    if (kind == kFill) {  // packed: zeros for the tokens of no sequence
-        const int T = p.a.T, head = min(max(p.a.cu[0], 0), T), tail = min(max(p.a.cu[p.a.n_seq], 0), T);
+        const Item &it = *item;
+        // the same in all lanes, which the compiler is to see (uniform registers)
+        auto same = [](int x) { return __shfl_sync(~0u, x, 0); };
+        const int kind = same(it.kind);
+        if (kind == kNone) break;
+        const bool share = PLANNED && kind == kShare;
+        const int slice = it.slot % (DV / 64), h = it.slot / (DV / 64), seq = it.seq, row = p.a.cu ? 0 : seq;
+        const int tokens = same(it.tokens), t0 = same(it.t0), n = (tokens + kC - 1) / kC;
+        const int base = PLANNED ? same(it.base) : 0, full = PLANNED ? same(it.full) : 0;
+        auto chunk = [&](int i) { return Chunk{row, t0 + i * kC, min(kC, tokens - i * kC), seq}; };
+        const uint64_t &end = it.end;
+        bool ok = true;
+        if (kind == kFill) {  // packed: zeros for the tokens of no sequence
+            const int T = p.a.T, head = min(max(p.a.cu[0], 0), T), tail = min(max(p.a.cu[p.a.n_seq], 0), T);
 #pragma unroll 1
-        for (int e = threadIdx.x; e < (head + T - tail) * 8; e += kFwdThreads) {
-            const int i = e >> 3, t = i < head ? i : tail + i - head;
-            *reinterpret_cast<uint4 *>(at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, 0, h, t) + 64 * slice + (e & 7) * 8) =
-                make_uint4(0, 0, 0, 0);
-        }
-        if (PLANNED && threadIdx.x == 0) take(item + 1, base, full);
-    } else if (warp == 0) {
-        if (lane == 0) {
-            const int hk = h / (p.a.H / p.a.Hk);
-            int ik = 0, iq = 0, iv = 0;
+            for (int e = threadIdx.x; e < (head + T - tail) * 8; e += kFwdThreads) {
+                const int i = e >> 3, t = i < head ? i : tail + i - head;
+                *reinterpret_cast<uint4 *>(at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, 0, h, t) + 64 * slice + (e & 7) * 8) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            if (PLANNED && threadIdx.x == 0) take(item + 1, base, full);
+        } else if (warp == 0) {
+            if (lane == 0) {
+                const int hk = h / (p.a.H / p.a.Hk);
+                int ik = 0, iq = 0, iv = 0;
+#pragma unroll 1
+                for (int i = 0; i < n; ++i) {
+                    const Chunk c = chunk(i);
+                    const int gi = base + i, fi = full + i, s = gi % kQKStages, v = gi % kVStages, f = fi % kQKStages;
+                    uint8_t *st = sm + L::QK + s * 2 * L::TB, *sq = sm + L::QK + f * 2 * L::TB + L::TB;
+                    if (gi >= kVStages && !(ok = la_wait(&bars[L::VEMPTY + v], (gi / kVStages - 1) & 1, end))) break;
+                    mbar_arrive_expect_tx(&bars[L::VFULL + v], 16384);
+                    tma_load_4d(sm + L::V + v * 16384, &mV, &bars[L::VFULL + v], 64 * slice, c.t0, h, c.row);
+                    ++iv;
+                    if (gi >= kQKStages && !(ok = la_wait(&bars[L::KEMPTY + s], (gi / kQKStages - 1) & 1, end))) break;
+                    mbar_arrive_expect_tx(&bars[L::KFULL + s], L::TB);
+#pragma unroll
+                    for (int x = 0; x < DK / 64; ++x) tma_load_4d(st + x * 16384, &mK, &bars[L::KFULL + s], 64 * x, c.t0, hk, c.row);
+                    ++ik;
+                    if (share) continue;
+                    if (fi >= kQKStages && !(ok = la_wait(&bars[L::QEMPTY + f], (fi / kQKStages - 1) & 1, end))) break;
+                    mbar_arrive_expect_tx(&bars[L::QFULL + f], L::TB);
+#pragma unroll
+                    for (int x = 0; x < DK / 64; ++x)
+                        tma_load_4d(sq + x * 16384, &mQ, &bars[L::QFULL + f], 64 * x, c.t0, hk, c.row);
+                    ++iq;
+                }
+                if (PLANNED) take(item + 1, base + n, share ? full : full + n);
+                // no copy is in flight when the item ends
+                auto drain = [&](int bar, int stages, int first, int count) {
+#pragma unroll 1
+                    for (int j = count > stages ? first + count - stages : first; j < first + count; ++j)
+                        mbar_wait(&bars[bar + j % stages], (j / stages) & 1, kDrainNs);
+                };
+                drain(L::KFULL, kQKStages, base, ik);
+                drain(L::QFULL, kQKStages, full, iq);
+                drain(L::VFULL, kVStages, base, iv);
+            }
+        } else if (warp == 1) {
+            // the products of the outputs: Q K^T a chunk ahead, Q S and P V.  All
+            // lanes wait, one issues.
+            constexpr uint32_t idT = idesc_bf16(128, 128, false, false), idO = idesc_bf16(128, 64, false, true);
+            const bool leader = elect_one();
+            if (share) {  // K and V pass by
+#pragma unroll 1
+                for (int gi = base; gi < base + n && ok; ++gi) {
+                    const int s = gi % kQKStages, v = gi % kVStages;
+                    ok = la_wait(&bars[L::KFULL + s], (gi / kQKStages) & 1, end) && la_wait(&bars[L::VFULL + v], (gi / kVStages) & 1, end);
+                    if (leader && ok) {
+                        mbar_arrive(&bars[L::KEMPTY + s]);
+                        mbar_arrive(&bars[L::VEMPTY + v]);
+                    }
+                }
+            }
+#pragma unroll 1
+            for (int i = share ? n : -1; i < n; ++i) {
+                if (i + 1 < n) {
+                    // T's place is free: P V of two chunks before, the last to read
+                    // it, was issued before (products run in the order of their issue)
+                    const int gj = base + i + 1, fj = full + i + 1, st = gj % kQKStages, sq = fj % kQKStages;
+                    if (!(ok = la_wait(&bars[L::KFULL + st], (gj / kQKStages) & 1, end))) break;
+                    if (!(ok = la_wait(&bars[L::QFULL + sq], (fj / kQKStages) & 1, end))) break;
+                    const uint32_t k = desc_lo(sbase + L::QK + st * 2 * L::TB, 16);
+                    const uint32_t q = desc_lo(sbase + L::QK + sq * 2 * L::TB + L::TB, 16), d = TM_T + 128u * (fj & 1);
+                    if (leader) {
+                        mma_steps<DK / 16>(d, idT, [&](int ks) { return q + (ks >> 2) * 1024 + (ks & 3) * 2; },
+                                           [&](int ks) { return k + (ks >> 2) * 1024 + (ks & 3) * 2; });
+                        mma_commit(&bars[L::TFULL + (fj & 1)]);
+                        mma_commit(&bars[L::KEMPTY + st]);
+                    }
+                }
+                if (i < 0) continue;
+                const int gi = base + i, fi = full + i;
+                if (!(ok = la_wait(&bars[L::SREADY], fi & 1, end))) break;
+                if (leader) {  // into the place that P V of one chunk before has waited for
+                    const uint32_t q = desc_lo(sbase + L::QK + (fi % kQKStages) * 2 * L::TB + L::TB, 16), x = desc_lo(sbase + L::S, 8192);
+                    mma_steps<DK / 16>(TM_OS + 64u * (fi & 1), idO, [&](int ks) { return q + (ks >> 2) * 1024 + (ks & 3) * 2; },
+                                       [&](int ks) { return x + ks * 128; });
+                    mma_commit(&bars[L::SEMPTY]);
+                    mma_commit(&bars[L::QEMPTY + fi % kQKStages]);
+                }
+                if (!(ok = la_wait(&bars[L::PREADY + (fi & 1)], (fi / 2) & 1, end))) break;
+                if (!(ok = la_wait(&bars[L::VREADY + gi % kVStages], (gi / kVStages) & 1, end))) break;
+                if (fi >= 1 && !(ok = la_wait(&bars[L::OEMPTY], (fi - 1) & 1, end))) break;
+                tc_fence_after_sync();
+                const uint32_t v = desc_lo(sbase + L::V + (gi % kVStages) * 16384, 8192), t = TM_T + 128u * (fi & 1);
+                if (leader) {
+                    mma_ts<0>(TM_OP, t, desc_of(v), idO);
+#pragma unroll
+                    for (int ks = 1; ks < kC / 16; ++ks) mma_ts<1>(TM_OP, t + 8 * ks, desc_of(v + ks * 128), idO);
+                    mma_commit(&bars[L::OFULL]);
+                    mma_commit(&bars[L::VEMPTY + gi % kVStages]);
+                }
+            }
+        } else if (warp == 2) {
+            // the chunk's share of the state, as far as the weighted values are there
+            constexpr uint32_t idU = idesc_bf16(128, 64, true, true);
+            const bool leader = elect_one();
+            int xs = 4 * base % kXRing;  // slot of X, and its phase
+            uint32_t xp = (4 * base / kXRing) & 1;
+#pragma unroll 1
+            for (int gi = base; gi < base + n; ++gi) {
+                const int st = gi % kQKStages;
+                uint32_t k = desc_lo(sbase + L::QK + st * 2 * L::TB, 16384);
+                ok = la_wait(&bars[L::KFULL + st], (gi / kQKStages) & 1, end);
+                if (gi >= 1) ok = ok && la_wait(&bars[L::UEMPTY], (gi - 1) & 1, end);
+                tc_fence_after_sync();
+#pragma unroll 1
+                for (int qd = 0; qd < 4; ++qd, k += 256) {
+                    ok = ok && la_wait(&bars[L::XREADY + xs], xp, end);
+                    if (!ok) break;
+                    const uint32_t x = desc_lo(sbase + L::X + xs * TERMS * 4096, 8192);
+                    if (leader) {
+                        if (qd == 0) mma_ss<0>(TM_U, desc_of(k), desc_of(x), idU);
+                        else mma_ss<1>(TM_U, desc_of(k), desc_of(x), idU);
+                        mma_ss<1>(TM_U, desc_of(k + 128), desc_of(x + 128), idU);
+                        mma_ss<1>(TM_U, desc_of(k), desc_of(x + 256), idU);
+                        mma_ss<1>(TM_U, desc_of(k + 128), desc_of(x + 384), idU);
+                        if constexpr (TERMS == 3) {
+                            mma_ss<1>(TM_U, desc_of(k), desc_of(x + 512), idU);
+                            mma_ss<1>(TM_U, desc_of(k + 128), desc_of(x + 640), idU);
+                        }
+                        if (qd == 3) mma_commit(&bars[L::UFULL]);
+                        mma_commit(&bars[L::XEMPTY + xs]);
+                        if (qd == 3) mma_commit(&bars[L::KEMPTY + st]);
+                    }
+                    if (++xs == kXRing) xs = 0, xp ^= 1;
+                }
+                if (!ok) break;
+            }
+        } else if (warp == 3) {
+            // a chunk's decays: e^{G - c_t}, log2(e) c_t, e^{c_r - c_t} with r the last
+            // token of t's block of 32, and e^G; the next chunk's gates are on their
+            // way meanwhile
+            const bool per_head = p.a.flags & GDN_G_PER_HEAD;
+            float next[4], whole = 0.f;
+            auto fetch = [&](int i) {
+                if (i >= n) return;
+                load_gates<kC>(gate_ptr(p.a, chunk(i), h), p.a.sg.t, chunk(i).len, per_head, next);
+            };
+            fetch(0);
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
-                const Chunk c = chunk(i);
-                const int gi = base + i, fi = full + i, s = gi % kQKStages, v = gi % kVStages, f = fi % kQKStages;
-                uint8_t *st = sm + L::QK + s * 2 * L::TB, *sq = sm + L::QK + f * 2 * L::TB + L::TB;
-                if (gi >= kVStages && !(ok = la_wait(&bars[L::VEMPTY + v], (gi / kVStages - 1) & 1, end))) break;
-                mbar_arrive_expect_tx(&bars[L::VFULL + v], 16384);
-                tma_load_4d(sm + L::V + v * 16384, &mV, &bars[L::VFULL + v], 64 * slice, c.t0, h, c.row);
-                ++iv;
-                if (gi >= kQKStages && !(ok = la_wait(&bars[L::KEMPTY + s], (gi / kQKStages - 1) & 1, end))) break;
-                mbar_arrive_expect_tx(&bars[L::KFULL + s], L::TB);
+                const int gi = base + i, w = gi % kGRing;
+                const Sums g = scan_sums(next);
+                fetch(i + 1);
+                if (gi >= kGRing && !(ok = la_wait(&bars[L::GEMPTY + w], (gi / kGRing - 1) & 1, end))) break;
+                Weight wt[4];
+                float c2[4];
 #pragma unroll
-                for (int x = 0; x < DK / 64; ++x) tma_load_4d(st + x * 16384, &mK, &bars[L::KFULL + s], 64 * x, c.t0, hk, c.row);
-                ++ik;
-                if (share) continue;
-                if (fi >= kQKStages && !(ok = la_wait(&bars[L::QEMPTY + f], (fi / kQKStages - 1) & 1, end))) break;
-                mbar_arrive_expect_tx(&bars[L::QFULL + f], L::TB);
-#pragma unroll
-                for (int x = 0; x < DK / 64; ++x)
-                    tma_load_4d(sq + x * 16384, &mQ, &bars[L::QFULL + f], 64 * x, c.t0, hk, c.row);
-                ++iq;
-            }
-            if (PLANNED) take(item + 1, base + n, share ? full : full + n);
-            // no copy is in flight when the item ends
-            auto drain = [&](int bar, int stages, int first, int count) {
-#pragma unroll 1
-                for (int j = count > stages ? first + count - stages : first; j < first + count; ++j)
-                    mbar_wait(&bars[bar + j % stages], (j / stages) & 1, kDrainNs);
-            };
-            drain(L::KFULL, kQKStages, base, ik);
-            drain(L::QFULL, kQKStages, full, iq);
-            drain(L::VFULL, kVStages, base, iv);
-        }
-    } else if (warp == 1) {
-        // the products of the outputs: Q K^T a chunk ahead, Q S and P V.  All
-        // lanes wait, one issues.
-        constexpr uint32_t idT = idesc_bf16(128, 128, false, false), idO = idesc_bf16(128, 64, false, true);
-        const bool leader = elect_one();
-        if (share) {  // K and V pass by
-#pragma unroll 1
-            for (int gi = base; gi < base + n && ok; ++gi) {
-                const int s = gi % kQKStages, v = gi % kVStages;
-                ok = la_wait(&bars[L::KFULL + s], (gi / kQKStages) & 1, end) && la_wait(&bars[L::VFULL + v], (gi / kVStages) & 1, end);
-                if (leader && ok) {
-                    mbar_arrive(&bars[L::KEMPTY + s]);
-                    mbar_arrive(&bars[L::VEMPTY + v]);
+                for (int j = 0; j < 4; ++j) {
+                    wt[j] = split_weight(exp2_fast(g.to_end[j] * kLog2e));
+                    c2[j] = g.cum[j] * kLog2e;
                 }
+                uint4 *ws = reinterpret_cast<uint4 *>(wring + w * 384);
+                ws[lane] = make_uint4(wt[0].h, wt[1].h, wt[2].h, wt[3].h);
+                ws[lane + 32] = make_uint4(wt[0].m, wt[1].m, wt[2].m, wt[3].m);
+                ws[lane + 64] = make_uint4(wt[0].l, wt[1].l, wt[2].l, wt[3].l);
+                float4 *slot = reinterpret_cast<float4 *>(gring + w * 256);
+                slot[lane] = make_float4(c2[0], c2[1], c2[2], c2[3]);
+                const float r = __shfl_sync(~0u, c2[3], lane | 7);
+                slot[lane + 32] = make_float4(exp2_fast(r - c2[0]), exp2_fast(r - c2[1]), exp2_fast(r - c2[2]), exp2_fast(r - c2[3]));
+                if (lane == 0) dring[w] = expf(g.all);
+                whole += g.all;
+                if (share && i == n - 1 && lane == 0) p.plan.decay[(size_t)it.row * slots + it.slot] = expf(whole);
+                mbar_arrive(&bars[L::GFULL + w]);
             }
-        }
-#pragma unroll 1
-        for (int i = share ? n : -1; i < n; ++i) {
-            if (i + 1 < n) {
-                // T's place is free: P V of two chunks before, the last to read
-                // it, was issued before (products run in the order of their issue)
-                const int gj = base + i + 1, fj = full + i + 1, st = gj % kQKStages, sq = fj % kQKStages;
-                if (!(ok = la_wait(&bars[L::KFULL + st], (gj / kQKStages) & 1, end))) break;
-                if (!(ok = la_wait(&bars[L::QFULL + sq], (fj / kQKStages) & 1, end))) break;
-                const uint32_t k = desc_lo(sbase + L::QK + st * 2 * L::TB, 16);
-                const uint32_t q = desc_lo(sbase + L::QK + sq * 2 * L::TB + L::TB, 16), d = TM_T + 128u * (fj & 1);
-                if (leader) {
-                    mma_steps<DK / 16>(d, idT, [&](int ks) { return q + (ks >> 2) * 1024 + (ks & 3) * 2; },
-                                       [&](int ks) { return k + (ks >> 2) * 1024 + (ks & 3) * 2; });
-                    mma_commit(&bars[L::TFULL + (fj & 1)]);
-                    mma_commit(&bars[L::KEMPTY + st]);
-                }
-            }
-            if (i < 0) continue;
-            const int gi = base + i, fi = full + i;
-            if (!(ok = la_wait(&bars[L::SREADY], fi & 1, end))) break;
-            if (leader) {  // into the place that P V of one chunk before has waited for
-                const uint32_t q = desc_lo(sbase + L::QK + (fi % kQKStages) * 2 * L::TB + L::TB, 16), x = desc_lo(sbase + L::S, 8192);
-                mma_steps<DK / 16>(TM_OS + 64u * (fi & 1), idO, [&](int ks) { return q + (ks >> 2) * 1024 + (ks & 3) * 2; },
-                                   [&](int ks) { return x + ks * 128; });
-                mma_commit(&bars[L::SEMPTY]);
-                mma_commit(&bars[L::QEMPTY + fi % kQKStages]);
-            }
-            if (!(ok = la_wait(&bars[L::PREADY + (fi & 1)], (fi / 2) & 1, end))) break;
-            if (!(ok = la_wait(&bars[L::VREADY + gi % kVStages], (gi / kVStages) & 1, end))) break;
-            if (fi >= 1 && !(ok = la_wait(&bars[L::OEMPTY], (fi - 1) & 1, end))) break;
-            tc_fence_after_sync();
-            const uint32_t v = desc_lo(sbase + L::V + (gi % kVStages) * 16384, 8192), t = TM_T + 128u * (fi & 1);
-            if (leader) {
-                mma_ts<0>(TM_OP, t, desc_of(v), idO);
+        } else if (warp < 8) {
+            // the state: a row of 64 columns a thread, in registers
+            const int row = 32 * (warp & 3) + lane;
+            const bool mine = row < DK;
+            float S[64];
+            const size_t page = (((size_t)seq * p.a.H + h) * DK + row) * DV + 64 * slice;
+            const int piece = PLANNED ? it.piece >> 1 : 0;
 #pragma unroll
-                for (int ks = 1; ks < kC / 16; ++ks) mma_ts<1>(TM_OP, t + 8 * ks, desc_of(v + ks * 128), idO);
-                mma_commit(&bars[L::OFULL]);
-                mma_commit(&bars[L::VEMPTY + gi % kVStages]);
+            for (int e = 0; e < 64; e += 4) {
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (mine && p.a.s0 && piece == 0) x = *reinterpret_cast<const float4 *>(p.a.s0 + page + e);
+                S[e] = x.x, S[e + 1] = x.y, S[e + 2] = x.z, S[e + 3] = x.w;
             }
-        }
-    } else if (warp == 2) {
-        // the chunk's share of the state, as far as the weighted values are there
-        constexpr uint32_t idU = idesc_bf16(128, 64, true, true);
-        const bool leader = elect_one();
-        int xs = 4 * base % kXRing;  // slot of X, and its phase
-        uint32_t xp = (4 * base / kXRing) & 1;
+            if (PLANNED && !share)
 #pragma unroll 1
-        for (int gi = base; gi < base + n; ++gi) {
-            const int st = gi % kQKStages;
-            uint32_t k = desc_lo(sbase + L::QK + st * 2 * L::TB, 16384);
-            ok = la_wait(&bars[L::KFULL + st], (gi / kQKStages) & 1, end);
-            if (gi >= 1) ok = ok && la_wait(&bars[L::UEMPTY], (gi - 1) & 1, end);
-            tc_fence_after_sync();
-#pragma unroll 1
-            for (int qd = 0; qd < 4; ++qd, k += 256) {
-                ok = ok && la_wait(&bars[L::XREADY + xs], xp, end);
-                if (!ok) break;
-                const uint32_t x = desc_lo(sbase + L::X + xs * TERMS * 4096, 8192);
-                if (leader) {
-                    if (qd == 0) mma_ss<0>(TM_U, desc_of(k), desc_of(x), idU);
-                    else mma_ss<1>(TM_U, desc_of(k), desc_of(x), idU);
-                    mma_ss<1>(TM_U, desc_of(k + 128), desc_of(x + 128), idU);
-                    mma_ss<1>(TM_U, desc_of(k), desc_of(x + 256), idU);
-                    mma_ss<1>(TM_U, desc_of(k + 128), desc_of(x + 384), idU);
-                    if constexpr (TERMS == 3) {
-                        mma_ss<1>(TM_U, desc_of(k), desc_of(x + 512), idU);
-                        mma_ss<1>(TM_U, desc_of(k + 128), desc_of(x + 640), idU);
+                for (int j = 0; j < piece; ++j) {  // the shares before the piece, the first with s0 in it
+                    const size_t at = (size_t)(it.row + j) * slots + it.slot;
+                    ok = warp_ok(ok && share_wait(p.plan.flags + at, end));
+                    if (!ok) break;
+                    const float d = j ? __ldcg(p.plan.decay + at) : 0.f;
+                    const float4 *from = reinterpret_cast<const float4 *>(p.plan.share + (at * DK + (mine ? row : 0)) * 64);
+#pragma unroll
+                    for (int e = 0; e < 64; e += 4) {
+                        const float4 x = __ldcg(from + e / 4);
+                        S[e] = fmaf(d, S[e], x.x), S[e + 1] = fmaf(d, S[e + 1], x.y);
+                        S[e + 2] = fmaf(d, S[e + 2], x.z), S[e + 3] = fmaf(d, S[e + 3], x.w);
                     }
-                    if (qd == 3) mma_commit(&bars[L::UFULL]);
-                    mma_commit(&bars[L::XEMPTY + xs]);
-                    if (qd == 3) mma_commit(&bars[L::KEMPTY + st]);
                 }
-                if (++xs == kXRing) xs = 0, xp ^= 1;
-            }
-            if (!ok) break;
-        }
-    } else if (warp == 3) {
-        // a chunk's decays: e^{G - c_t}, log2(e) c_t, e^{c_r - c_t} with r the last
-        // token of t's block of 32, and e^G; the next chunk's gates are on their
-        // way meanwhile
-        const bool per_head = p.a.flags & GDN_G_PER_HEAD;
-        float next[4], whole = 0.f;
-        auto fetch = [&](int i) {
-            if (i >= n) return;
-            load_gates<kC>(gate_ptr(p.a, chunk(i), h), p.a.sg.t, chunk(i).len, per_head, next);
-        };
-        fetch(0);
+            auto step = [&](int gi) {  // S = e^G S + the chunk's share
+                const int w = gi % kGRing;
+                ok = warp_ok(ok && la_wait(&bars[L::GFULL + w], (gi / kGRing) & 1, end) && la_wait(&bars[L::UFULL], gi & 1, end));
+                if (!ok) return;
+                const float d = dring[w];
+                tc_fence_after_sync();
+#pragma unroll
+                for (int e = 0; e < 64; e += 16) {
+                    uint32_t u[16];
+                    tmem_ld16(tmem + lane_base(warp) + TM_U + e, u);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) S[e + j] = fmaf(d, S[e + j], __uint_as_float(u[j]));
+                }
+                tc_fence_before_sync();
+                mbar_arrive(&bars[L::UEMPTY]);
+                mbar_arrive(&bars[L::GEMPTY + w]);
+            };
+            if (share) {
 #pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-            const int gi = base + i, w = gi % kGRing;
-            const Sums g = scan_sums(next);
-            fetch(i + 1);
-            if (gi >= kGRing && !(ok = la_wait(&bars[L::GEMPTY + w], (gi / kGRing - 1) & 1, end))) break;
-            Weight wt[4];
-            float c2[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                wt[j] = split_weight(exp2_fast(g.to_end[j] * kLog2e));
-                c2[j] = g.cum[j] * kLog2e;
-            }
-            uint4 *ws = reinterpret_cast<uint4 *>(wring + w * 384);
-            ws[lane] = make_uint4(wt[0].h, wt[1].h, wt[2].h, wt[3].h);
-            ws[lane + 32] = make_uint4(wt[0].m, wt[1].m, wt[2].m, wt[3].m);
-            ws[lane + 64] = make_uint4(wt[0].l, wt[1].l, wt[2].l, wt[3].l);
-            float4 *slot = reinterpret_cast<float4 *>(gring + w * 256);
-            slot[lane] = make_float4(c2[0], c2[1], c2[2], c2[3]);
-            const float r = __shfl_sync(~0u, c2[3], lane | 7);
-            slot[lane + 32] = make_float4(exp2_fast(r - c2[0]), exp2_fast(r - c2[1]), exp2_fast(r - c2[2]), exp2_fast(r - c2[3]));
-            if (lane == 0) dring[w] = expf(g.all);
-            whole += g.all;
-            if (share && i == n - 1 && lane == 0) p.plan.decay[(size_t)it.row * slots + it.slot] = expf(whole);
-            mbar_arrive(&bars[L::GFULL + w]);
-        }
-    } else if (warp < 8) {
-        // the state: a row of 64 columns a thread, in registers
-        const int row = 32 * (warp & 3) + lane;
-        const bool mine = row < DK;
-        float S[64];
-        const size_t page = (((size_t)seq * p.a.H + h) * DK + row) * DV + 64 * slice;
-        const int piece = PLANNED ? it.piece >> 1 : 0;
-#pragma unroll
-        for (int e = 0; e < 64; e += 4) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (mine && p.a.s0 && piece == 0) x = *reinterpret_cast<const float4 *>(p.a.s0 + page + e);
-            S[e] = x.x, S[e + 1] = x.y, S[e + 2] = x.z, S[e + 3] = x.w;
-        }
-        if (PLANNED && !share)
+                for (int gi = base; gi < base + n && ok; ++gi) step(gi);
+            } else {
 #pragma unroll 1
-            for (int j = 0; j < piece; ++j) {  // the shares before the piece, the first with s0 in it
-                const size_t at = (size_t)(it.row + j) * slots + it.slot;
-                ok = warp_ok(ok && share_wait(p.plan.flags + at, end));
-                if (!ok) break;
-                const float d = j ? __ldcg(p.plan.decay + at) : 0.f;
-                const float4 *from = reinterpret_cast<const float4 *>(p.plan.share + (at * DK + (mine ? row : 0)) * 64);
+                for (int gi = base; gi < base + n && ok; ++gi) {
+                    ok = la_wait(&bars[L::SEMPTY], (gi + full - base + 1) & 1, end);  // the first passes
+                    if (mine)
 #pragma unroll
-                for (int e = 0; e < 64; e += 4) {
-                    const float4 x = __ldcg(from + e / 4);
-                    S[e] = fmaf(d, S[e], x.x), S[e + 1] = fmaf(d, S[e + 1], x.y);
-                    S[e + 2] = fmaf(d, S[e + 2], x.z), S[e + 3] = fmaf(d, S[e + 3], x.w);
+                        for (int e = 0; e < 64; e += 8)
+                            *reinterpret_cast<uint4 *>(sm + L::S + sw128_offset(row, e)) =
+                                make_uint4(pack_bf16(S[e], S[e + 1]), pack_bf16(S[e + 2], S[e + 3]), pack_bf16(S[e + 4], S[e + 5]),
+                                           pack_bf16(S[e + 6], S[e + 7]));
+                    fence_proxy_async_smem();
+                    mbar_arrive(&bars[L::SREADY]);
+                    step(gi);
                 }
             }
-        auto step = [&](int gi) {  // S = e^G S + the chunk's share
-            const int w = gi % kGRing;
-            ok = warp_ok(ok && la_wait(&bars[L::GFULL + w], (gi / kGRing) & 1, end) && la_wait(&bars[L::UFULL], gi & 1, end));
-            if (!ok) return;
-            const float d = dring[w];
-            tc_fence_after_sync();
+            if (share) {
+                const size_t at = (size_t)it.row * slots + it.slot;
+                if (mine && ok)
 #pragma unroll
-            for (int e = 0; e < 64; e += 16) {
-                uint32_t u[16];
-                tmem_ld16(tmem + lane_base(warp) + TM_U + e, u);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) S[e + j] = fmaf(d, S[e + j], __uint_as_float(u[j]));
-            }
-            tc_fence_before_sync();
-            mbar_arrive(&bars[L::UEMPTY]);
-            mbar_arrive(&bars[L::GEMPTY + w]);
-        };
-        if (share) {
-#pragma unroll 1
-            for (int gi = base; gi < base + n && ok; ++gi) step(gi);
-        } else {
-#pragma unroll 1
-            for (int gi = base; gi < base + n && ok; ++gi) {
-                ok = la_wait(&bars[L::SEMPTY], (gi + full - base + 1) & 1, end);  // the first passes
-                if (mine)
-#pragma unroll
-                    for (int e = 0; e < 64; e += 8)
-                        *reinterpret_cast<uint4 *>(sm + L::S + sw128_offset(row, e)) =
-                            make_uint4(pack_bf16(S[e], S[e + 1]), pack_bf16(S[e + 2], S[e + 3]), pack_bf16(S[e + 4], S[e + 5]),
-                                       pack_bf16(S[e + 6], S[e + 7]));
-                fence_proxy_async_smem();
-                mbar_arrive(&bars[L::SREADY]);
-                step(gi);
-            }
-        }
-        if (share) {
-            const size_t at = (size_t)it.row * slots + it.slot;
-            if (mine && ok)
+                    for (int e = 0; e < 64; e += 4)
+                        *reinterpret_cast<float4 *>(p.plan.share + (at * DK + row) * 64 + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+                __threadfence();
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (ok && threadIdx.x == 128) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p.plan.flags + at), "r"(1u) : "memory");
+            } else if (p.a.sf && (it.piece & 1) && mine && ok) {
 #pragma unroll
                 for (int e = 0; e < 64; e += 4)
-                    *reinterpret_cast<float4 *>(p.plan.share + (at * DK + row) * 64 + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
-            __threadfence();
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (ok && threadIdx.x == 128) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p.plan.flags + at), "r"(1u) : "memory");
-        } else if (p.a.sf && (it.piece & 1) && mine && ok) {
-#pragma unroll
-            for (int e = 0; e < 64; e += 4)
-                *reinterpret_cast<float4 *>(p.a.sf + page + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
-        }
-    } else if (share && (warp < 12 || warp >= 16)) {  // the decays pass by
-#pragma unroll 1
-        for (int gi = base; gi < base + n && ok; ++gi) {
-            ok = la_wait(&bars[L::GFULL + gi % kGRing], (gi / kGRing) & 1, end);
-            if (ok) mbar_arrive(&bars[L::GEMPTY + gi % kGRing]);
-        }
-    } else if (warp < 12) {
-        // P in blocks of 16 columns, thread's row t.  On the warp's diagonal (32
-        // columns) the decay is e^{c_t - c_s}; before it e^{c_t - c_r} e^{c_r - c_s}
-        // with r the last token of s's block of 32, whose factors are both at most
-        // 1 for decays, so that a row costs one exponential a block.
-        const int t = 32 * (warp & 3) + lane, diag = 32 * (warp & 3);
-#pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-            const int gi = base + i, fi = full + i, w = gi % kGRing;
-            ok = warp_ok(la_wait(&bars[L::GFULL + w], (gi / kGRing) & 1, end) && la_wait(&bars[L::TFULL + (fi & 1)], (fi / 2) & 1, end));
-            if (!ok) break;
-            tc_fence_after_sync();
-            const float *c2 = gring + w * 256, *cf = c2 + 128;
-            const float ct = c2[t];
-            const uint32_t tt = tmem + lane_base(warp) + TM_T + 128u * (fi & 1);
-            uint32_t u[16], y[8];
-#pragma unroll 1
-            for (int s = 0; s < diag; s += 16) {
-                tmem_ld16(tt + s, u);
-                const float rf = exp2_fast(ct - c2[s | 31]);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(cf + s + j);
-                    y[j / 2] = pack_bf16(__uint_as_float(u[j]) * (rf * f.x), __uint_as_float(u[j + 1]) * (rf * f.y));
-                    y[j / 2 + 1] = pack_bf16(__uint_as_float(u[j + 2]) * (rf * f.z), __uint_as_float(u[j + 3]) * (rf * f.w));
-                }
-                tmem_st8(tt + s / 2, y);
+                    *reinterpret_cast<float4 *>(p.a.sf + page + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
             }
+        } else if (share && (warp < 12 || warp >= 16)) {  // the decays pass by
 #pragma unroll 1
-            for (int s = diag; s < diag + 32; s += 16) {
-                tmem_ld16(tt + s, u);
-                tmem_wait_ld();
-                const int last = t - s;  // the row's last column of the block
-#pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 cs = *reinterpret_cast<const float4 *>(c2 + s + j);
-                    const float x0 = j + 0 <= last ? __uint_as_float(u[j]) * exp2_fast(ct - cs.x) : 0.f;
-                    const float x1 = j + 1 <= last ? __uint_as_float(u[j + 1]) * exp2_fast(ct - cs.y) : 0.f;
-                    const float x2 = j + 2 <= last ? __uint_as_float(u[j + 2]) * exp2_fast(ct - cs.z) : 0.f;
-                    const float x3 = j + 3 <= last ? __uint_as_float(u[j + 3]) * exp2_fast(ct - cs.w) : 0.f;
-                    y[j / 2] = pack_bf16(x0, x1);
-                    y[j / 2 + 1] = pack_bf16(x2, x3);
-                }
-                tmem_st8(tt + s / 2, y);
+            for (int gi = base; gi < base + n && ok; ++gi) {
+                ok = la_wait(&bars[L::GFULL + gi % kGRing], (gi / kGRing) & 1, end);
+                if (ok) mbar_arrive(&bars[L::GEMPTY + gi % kGRing]);
             }
-            // P's columns past the diagonal take the place of T's that have been read
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = 0u;
+        } else if (warp < 12) {
+            // P in blocks of 16 columns, thread's row t.  On the warp's diagonal (32
+            // columns) the decay is e^{c_t - c_s}; before it e^{c_t - c_r} e^{c_r - c_s}
+            // with r the last token of s's block of 32, whose factors are both at most
+            // 1 for decays, so that a row costs one exponential a block.
+            const int t = 32 * (warp & 3) + lane, diag = 32 * (warp & 3);
 #pragma unroll 1
-            for (int s = diag + 32; s < kC; s += 16) tmem_st8(tt + s / 2, y);
-            tmem_wait_st();
-            tc_fence_before_sync();
-            mbar_arrive(&bars[L::PREADY + (fi & 1)]);
-            mbar_arrive(&bars[L::GEMPTY + w]);
-        }
-    } else if (warp < 16) {
-        // the weighted values, in quarters of 32 tokens: row r of each, 16 columns
-        const int ct = threadIdx.x - 384, r = ct >> 2, c0 = (ct & 3) * 16;
-        const uint32_t off[2] = {sw128_offset(r, c0), sw128_offset(r, c0 + 8)};
-        int xs = 4 * base % kXRing;  // slot of X, and the phase of its last release
-        uint32_t xp = (4 * base / kXRing + 1) & 1;
-#pragma unroll 1
-        for (int i = 0; i < n && ok; ++i) {
-            const int gi = base + i, v = gi % kVStages, w = gi % kGRing, len = chunk(i).len;
-            ok = la_wait(&bars[L::VFULL + v], (gi / kVStages) & 1, end) && la_wait(&bars[L::GFULL + w], (gi / kGRing) & 1, end);
-            uint8_t *vt = sm + L::V + v * 16384;
-            if (len < kC) {
-                // rows past the chunk's tokens are another sequence's: zeros, so
-                // that nothing of theirs (an infinity, say) meets a zero weight
-                ok = ok && la_wait(&bars[L::KFULL + gi % kQKStages], (gi / kQKStages) & 1, end);
-                uint8_t *k = sm + L::QK + (gi % kQKStages) * 2 * L::TB;
-                if (ok) {
-#pragma unroll 1
-                    for (int row = r; row < kC; row += 32)
-                        if (row >= len) {
-                            *reinterpret_cast<uint4 *>(vt + (row - r) * 128 + off[0]) = make_uint4(0, 0, 0, 0);
-                            *reinterpret_cast<uint4 *>(vt + (row - r) * 128 + off[1]) = make_uint4(0, 0, 0, 0);
-                        }
-#pragma unroll 1
-                    for (int e = ct; e < (kC - len) * (DK / 8); e += 128) {
-                        const int row = len + e / (DK / 8), col = (e % (DK / 8)) * 8;
-                        *reinterpret_cast<uint4 *>(k + (col >> 6) * 16384 + sw128_offset(row, col & 63)) = make_uint4(0, 0, 0, 0);
-                    }
-                }
-                fence_proxy_async_smem();
-            }
-            if (ok) mbar_arrive(&bars[L::VREADY + v]);
-            const uint32_t *wr = wring + w * 384 + r;
-#pragma unroll 1
-            for (int qd = 0; qd < 4; ++qd, wr += 32, vt += 4096) {
-                const uint4 x[2] = {*reinterpret_cast<const uint4 *>(vt + off[0]), *reinterpret_cast<const uint4 *>(vt + off[1])};
-                const Weight wt = {wr[0], wr[128], wr[256]};
-                ok = ok && la_wait(&bars[L::XEMPTY + xs], xp, end);
+            for (int i = 0; i < n; ++i) {
+                const int gi = base + i, fi = full + i, w = gi % kGRing;
+                ok = warp_ok(la_wait(&bars[L::GFULL + w], (gi / kGRing) & 1, end) && la_wait(&bars[L::TFULL + (fi & 1)], (fi / 2) & 1, end));
                 if (!ok) break;
-                uint8_t *xb = sm + L::X + xs * TERMS * 4096;
-                if constexpr (TERMS == 3) {
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        uint4 a, b, d;
-                        weigh3(x[u].x, wt, a.x, b.x, d.x), weigh3(x[u].y, wt, a.y, b.y, d.y);
-                        weigh3(x[u].z, wt, a.z, b.z, d.z), weigh3(x[u].w, wt, a.w, b.w, d.w);
-                        *reinterpret_cast<uint4 *>(xb + off[u]) = a;
-                        *reinterpret_cast<uint4 *>(xb + 4096 + off[u]) = b;
-                        *reinterpret_cast<uint4 *>(xb + 8192 + off[u]) = d;
-                    }
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        uint4 a, b;
-                        weigh2(x[u].x, wt, a.x, b.x), weigh2(x[u].y, wt, a.y, b.y);
-                        weigh2(x[u].z, wt, a.z, b.z), weigh2(x[u].w, wt, a.w, b.w);
-                        *reinterpret_cast<uint4 *>(xb + off[u]) = a;
-                        *reinterpret_cast<uint4 *>(xb + 4096 + off[u]) = b;
-                    }
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(&bars[L::XREADY + xs]);
-                if (++xs == kXRing) xs = 0, xp ^= 1;
-            }
-            if (!ok) break;
-            mbar_arrive(&bars[L::VEMPTY + v]);
-            mbar_arrive(&bars[L::GEMPTY + w]);
-        }
-    } else {
-        // the rows of O: scale (e^c (Q S) + P V)
-        const int t = 32 * (warp & 3) + lane;
+                tc_fence_after_sync();
+                const float *c2 = gring + w * 256, *cf = c2 + 128;
+                const float ct = c2[t];
+                const uint32_t tt = tmem + lane_base(warp) + TM_T + 128u * (fi & 1);
+                uint32_t u[16], y[8];
 #pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-            const int gi = base + i, fi = full + i, w = gi % kGRing;
-            ok = warp_ok(la_wait(&bars[L::OFULL], fi & 1, end));
-            if (!ok) break;
-            tc_fence_after_sync();
-            const Chunk c = chunk(i);
-            const float f = exp2_fast(gring[w * 256 + t]) * p.a.scale;
-            const uint32_t ts = tmem + lane_base(warp) + TM_OS + 64u * (fi & 1), tp = tmem + lane_base(warp) + TM_OP;
-            uint32_t z[4][8];
+                for (int s = 0; s < diag; s += 16) {
+                    tmem_ld16(tt + s, u);
+                    const float rf = exp2_fast(ct - c2[s | 31]);
+                    tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                uint32_t x[16], y[16];
-                tmem_ld16(ts + 16 * e, x);
-                tmem_ld16(tp + 16 * e, y);
-                tmem_wait_ld();
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(cf + s + j);
+                        y[j / 2] = pack_bf16(__uint_as_float(u[j]) * (rf * f.x), __uint_as_float(u[j + 1]) * (rf * f.y));
+                        y[j / 2 + 1] = pack_bf16(__uint_as_float(u[j + 2]) * (rf * f.z), __uint_as_float(u[j + 3]) * (rf * f.w));
+                    }
+                    tmem_st8(tt + s / 2, y);
+                }
+#pragma unroll 1
+                for (int s = diag; s < diag + 32; s += 16) {
+                    tmem_ld16(tt + s, u);
+                    tmem_wait_ld();
+                    const int last = t - s;  // the row's last column of the block
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    z[e][j] = pack_bf16(fmaf(f, __uint_as_float(x[2 * j]), p.a.scale * __uint_as_float(y[2 * j])),
-                                        fmaf(f, __uint_as_float(x[2 * j + 1]), p.a.scale * __uint_as_float(y[2 * j + 1])));
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 cs = *reinterpret_cast<const float4 *>(c2 + s + j);
+                        const float x0 = j + 0 <= last ? __uint_as_float(u[j]) * exp2_fast(ct - cs.x) : 0.f;
+                        const float x1 = j + 1 <= last ? __uint_as_float(u[j + 1]) * exp2_fast(ct - cs.y) : 0.f;
+                        const float x2 = j + 2 <= last ? __uint_as_float(u[j + 2]) * exp2_fast(ct - cs.z) : 0.f;
+                        const float x3 = j + 3 <= last ? __uint_as_float(u[j + 3]) * exp2_fast(ct - cs.w) : 0.f;
+                        y[j / 2] = pack_bf16(x0, x1);
+                        y[j / 2 + 1] = pack_bf16(x2, x3);
+                    }
+                    tmem_st8(tt + s / 2, y);
+                }
+                // P's columns past the diagonal take the place of T's that have been read
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = 0u;
+#pragma unroll 1
+                for (int s = diag + 32; s < kC; s += 16) tmem_st8(tt + s / 2, y);
+                tmem_wait_st();
+                tc_fence_before_sync();
+                mbar_arrive(&bars[L::PREADY + (fi & 1)]);
+                mbar_arrive(&bars[L::GEMPTY + w]);
             }
-            tc_fence_before_sync();
-            mbar_arrive(&bars[L::OEMPTY]);
-            mbar_arrive(&bars[L::GEMPTY + w]);
-            exchange(z);
+        } else if (warp < 16) {
+            // the weighted values, in quarters of 32 tokens: row r of each, 16 columns
+            const int ct = threadIdx.x - 384, r = ct >> 2, c0 = (ct & 3) * 16;
+            const uint32_t off[2] = {sw128_offset(r, c0), sw128_offset(r, c0 + 8)};
+            int xs = 4 * base % kXRing;  // slot of X, and the phase of its last release
+            uint32_t xp = (4 * base / kXRing + 1) & 1;
+#pragma unroll 1
+            for (int i = 0; i < n && ok; ++i) {
+                const int gi = base + i, v = gi % kVStages, w = gi % kGRing, len = chunk(i).len;
+                ok = la_wait(&bars[L::VFULL + v], (gi / kVStages) & 1, end) && la_wait(&bars[L::GFULL + w], (gi / kGRing) & 1, end);
+                uint8_t *vt = sm + L::V + v * 16384;
+                if (len < kC) {
+                    // rows past the chunk's tokens are another sequence's: zeros, so
+                    // that nothing of theirs (an infinity, say) meets a zero weight
+                    ok = ok && la_wait(&bars[L::KFULL + gi % kQKStages], (gi / kQKStages) & 1, end);
+                    uint8_t *k = sm + L::QK + (gi % kQKStages) * 2 * L::TB;
+                    if (ok) {
+#pragma unroll 1
+                        for (int row = r; row < kC; row += 32)
+                            if (row >= len) {
+                                *reinterpret_cast<uint4 *>(vt + (row - r) * 128 + off[0]) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4 *>(vt + (row - r) * 128 + off[1]) = make_uint4(0, 0, 0, 0);
+                            }
+#pragma unroll 1
+                        for (int e = ct; e < (kC - len) * (DK / 8); e += 128) {
+                            const int row = len + e / (DK / 8), col = (e % (DK / 8)) * 8;
+                            *reinterpret_cast<uint4 *>(k + (col >> 6) * 16384 + sw128_offset(row, col & 63)) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                if (ok) mbar_arrive(&bars[L::VREADY + v]);
+                const uint32_t *wr = wring + w * 384 + r;
+#pragma unroll 1
+                for (int qd = 0; qd < 4; ++qd, wr += 32, vt += 4096) {
+                    const uint4 x[2] = {*reinterpret_cast<const uint4 *>(vt + off[0]), *reinterpret_cast<const uint4 *>(vt + off[1])};
+                    const Weight wt = {wr[0], wr[128], wr[256]};
+                    ok = ok && la_wait(&bars[L::XEMPTY + xs], xp, end);
+                    if (!ok) break;
+                    uint8_t *xb = sm + L::X + xs * TERMS * 4096;
+                    if constexpr (TERMS == 3) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int u = (t & ~3) + e;
-                if (u >= c.len) break;
-                __nv_bfloat16 *out = at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, c.row, h, c.t0 + u) + 64 * slice + 16 * (lane & 3);
-                if (p.wide) {
-                    st_global_32(out, z[e]);
-                } else {
-                    reinterpret_cast<uint4 *>(out)[0] = make_uint4(z[e][0], z[e][1], z[e][2], z[e][3]);
-                    reinterpret_cast<uint4 *>(out)[1] = make_uint4(z[e][4], z[e][5], z[e][6], z[e][7]);
+                        for (int u = 0; u < 2; ++u) {
+                            uint4 a, b, d;
+                            weigh3(x[u].x, wt, a.x, b.x, d.x), weigh3(x[u].y, wt, a.y, b.y, d.y);
+                            weigh3(x[u].z, wt, a.z, b.z, d.z), weigh3(x[u].w, wt, a.w, b.w, d.w);
+                            *reinterpret_cast<uint4 *>(xb + off[u]) = a;
+                            *reinterpret_cast<uint4 *>(xb + 4096 + off[u]) = b;
+                            *reinterpret_cast<uint4 *>(xb + 8192 + off[u]) = d;
+                        }
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            uint4 a, b;
+                            weigh2(x[u].x, wt, a.x, b.x), weigh2(x[u].y, wt, a.y, b.y);
+                            weigh2(x[u].z, wt, a.z, b.z), weigh2(x[u].w, wt, a.w, b.w);
+                            *reinterpret_cast<uint4 *>(xb + off[u]) = a;
+                            *reinterpret_cast<uint4 *>(xb + 4096 + off[u]) = b;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(&bars[L::XREADY + xs]);
+                    if (++xs == kXRing) xs = 0, xp ^= 1;
+                }
+                if (!ok) break;
+                mbar_arrive(&bars[L::VEMPTY + v]);
+                mbar_arrive(&bars[L::GEMPTY + w]);
+            }
+        } else {
+            // the rows of O: scale (e^c (Q S) + P V)
+            const int t = 32 * (warp & 3) + lane;
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+                const int gi = base + i, fi = full + i, w = gi % kGRing;
+                ok = warp_ok(la_wait(&bars[L::OFULL], fi & 1, end));
+                if (!ok) break;
+                tc_fence_after_sync();
+                const Chunk c = chunk(i);
+                const float f = exp2_fast(gring[w * 256 + t]) * p.a.scale;
+                const uint32_t ts = tmem + lane_base(warp) + TM_OS + 64u * (fi & 1), tp = tmem + lane_base(warp) + TM_OP;
+                uint32_t z[4][8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t x[16], y[16];
+                    tmem_ld16(ts + 16 * e, x);
+                    tmem_ld16(tp + 16 * e, y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        z[e][j] = pack_bf16(fmaf(f, __uint_as_float(x[2 * j]), p.a.scale * __uint_as_float(y[2 * j])),
+                                            fmaf(f, __uint_as_float(x[2 * j + 1]), p.a.scale * __uint_as_float(y[2 * j + 1])));
+                }
+                tc_fence_before_sync();
+                mbar_arrive(&bars[L::OEMPTY]);
+                mbar_arrive(&bars[L::GEMPTY + w]);
+                exchange(z);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int u = (t & ~3) + e;
+                    if (u >= c.len) break;
+                    __nv_bfloat16 *out = at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, c.row, h, c.t0 + u) + 64 * slice + 16 * (lane & 3);
+                    if (p.wide) {
+                        st_global_32(out, z[e]);
+                    } else {
+                        reinterpret_cast<uint4 *>(out)[0] = make_uint4(z[e][0], z[e][1], z[e][2], z[e][3]);
+                        reinterpret_cast<uint4 *>(out)[1] = make_uint4(z[e][4], z[e][5], z[e][6], z[e][7]);
+                    }
                 }
             }
         }
-    }
-    if (!PLANNED) break;
-    __syncwarp();
-    tc_fence_before_sync();
-    const bool bad = __syncthreads_or(!ok);
-    if (threadIdx.x == 0) *item = item[1];
-    if (bad) break;
-    __syncthreads();
-    tc_fence_after_sync();
+        if (!PLANNED) break;
+        __syncwarp();
+        tc_fence_before_sync();
+        const bool bad = __syncthreads_or(!ok);
+        if (threadIdx.x == 0) *item = item[1];
+        if (bad) break;
+        __syncthreads();
+        tc_fence_after_sync();
     }
     if (warp == 1 || warp == 2) {  // every MMA issued here is complete before TMEM is released
         if (elect_one()) mma_commit(&bars[L::DRAIN + warp - 1]);
