@@ -21,12 +21,15 @@ namespace {
 
 constexpr float kTop = 448.f;  // the largest e4m3 value
 
-// Vectors of 16 bytes: 8 bf16 or 4 fp32.
+// Vectors of N elements: 16 bytes (8 bf16 or 4 fp32), and what rows of other
+// lengths divide into.
 template <typename T>
+constexpr int kWide = 16 / sizeof(T);
+template <typename T, int N>
 struct Vec;
 template <>
-struct Vec<__nv_bfloat16> {
-    static constexpr int N = 8;
+struct Vec<__nv_bfloat16, 8> {
+    using Raw = uint4;
     static __device__ __forceinline__ void unpack(uint4 p, float (&x)[8]) {
         const uint32_t u[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
@@ -46,8 +49,33 @@ struct Vec<__nv_bfloat16> {
     }
 };
 template <>
-struct Vec<float> {
-    static constexpr int N = 4;
+struct Vec<__nv_bfloat16, 2> {
+    using Raw = uint32_t;
+    static __device__ __forceinline__ void unpack(uint32_t p, float (&x)[2]) {
+        x[0] = __uint_as_float(p << 16), x[1] = __uint_as_float(p & 0xffff0000u);
+    }
+    static __device__ __forceinline__ uint32_t pack(const float (&x)[2]) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(x[0], x[1]);
+        return *reinterpret_cast<const uint32_t *>(&t);
+    }
+};
+template <>
+struct Vec<__nv_bfloat16, 1> {
+    using Raw = unsigned short;
+    static __device__ __forceinline__ void unpack(unsigned short p, float (&x)[1]) { x[0] = __uint_as_float((uint32_t)p << 16); }
+    static __device__ __forceinline__ unsigned short pack(const float (&x)[1]) {
+        return __bfloat16_as_ushort(__float2bfloat16_rn(x[0]));
+    }
+};
+template <>
+struct Vec<float, 1> {
+    using Raw = uint32_t;
+    static __device__ __forceinline__ void unpack(uint32_t p, float (&x)[1]) { x[0] = __uint_as_float(p); }
+    static __device__ __forceinline__ uint32_t pack(const float (&x)[1]) { return __float_as_uint(x[0]); }
+};
+template <>
+struct Vec<float, 4> {
+    using Raw = uint4;
     static __device__ __forceinline__ void unpack(uint4 p, float (&x)[4]) {
         x[0] = __uint_as_float(p.x), x[1] = __uint_as_float(p.y);
         x[2] = __uint_as_float(p.z), x[3] = __uint_as_float(p.w);
@@ -91,17 +119,41 @@ __device__ __forceinline__ float block_all(float x, float *s) {
     return x;
 }
 
+// A vector's weights (1 where there are none).
+template <int N>
+__device__ __forceinline__ void load_weights(const float *w, int i, bool there, float (&x)[N]) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+            float4 y = make_float4(1.f, 1.f, 1.f, 1.f);
+            if (w && there) y = __ldg(reinterpret_cast<const float4 *>(w) + (i * N + e) / 4);
+            x[e] = y.x, x[e + 1] = y.y, x[e + 2] = y.z, x[e + 3] = y.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[e] = w && there ? __ldg(w + i * N + e) : 1.f;
+    }
+}
+
 template <int N>
 __device__ __forceinline__ void store_e4m3(void *p, const float (&y)[N], float inv) {
-    uint32_t u[N / 4];
+    if constexpr (N == 1) {
+        *static_cast<unsigned char *>(p) = __nv_cvt_float_to_fp8(y[0] * inv, __NV_SATFINITE, __NV_E4M3);
+        return;
+    } else if constexpr (N == 2) {
+        *static_cast<unsigned short *>(p) = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * inv, y[1] * inv), __NV_SATFINITE, __NV_E4M3);
+        return;
+    } else {
+        uint32_t u[N / 4];
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * i] * inv, y[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * i + 2] * inv, y[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-        u[i] = lo | hi << 16;
+        for (int i = 0; i < N / 4; ++i) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * i] * inv, y[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * i + 2] * inv, y[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+            u[i] = lo | hi << 16;
+        }
+        if (N == 8) *static_cast<uint2 *>(p) = make_uint2(u[0], u[N / 4 - 1]);
+        else *static_cast<uint32_t *>(p) = u[0];
     }
-    if (N == 8) *static_cast<uint2 *>(p) = make_uint2(u[0], u[N / 4 - 1]);
-    else *static_cast<uint32_t *>(p) = u[0];
 }
 
 // Rows blockIdx.x, + gridDim.x, .. by a CTA of NT threads, V vectors a thread
@@ -114,20 +166,21 @@ __device__ __forceinline__ void store_e4m3(void *p, const float (&y)[N], float i
 // y / scale = (h w) (r / scale).  Measured, bf16, 32760 x 2048 with a residual:
 // to e4m3 in groups of 128 76 us (472 MB at 6.2 TB/s), to bf16 86 (6.2 TB/s);
 // 8 rows 2.5 us.
-// C is a multiple of the vector's width; rows are 16-byte aligned.
-template <typename T, int NT, int V>
+// C is a multiple of the vector's width N: 16384 x 2046 bf16 with a residual 45 us
+// in vectors of two, x 2047 56 in single elements (x 2048: 43).
+template <typename T, int N, int NT, int V>
 __global__ void __launch_bounds__(NT, V <= 2 ? 1024 / NT : 1) norm_kernel(NormArgs a) {
-    constexpr int N = Vec<T>::N;
+    using Raw = typename Vec<T, N>::Raw;
     __shared__ float red[2][32];
     const int nv = a.C / N;
-    uint4 px[V], pr[V];
+    Raw px[V], pr[V];
     auto fetch = [&](long long row) {
-        const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + row * a.C);
-        const uint4 *res = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.res) + row * a.C);
+        const Raw *x = reinterpret_cast<const Raw *>(static_cast<const T *>(a.x) + row * a.C);
+        const Raw *res = reinterpret_cast<const Raw *>(static_cast<const T *>(a.res) + row * a.C);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int i = j * NT + threadIdx.x;
-            px[j] = pr[j] = make_uint4(0, 0, 0, 0);
+            px[j] = pr[j] = Raw{};
             if (row < a.rows && i < nv) {
                 px[j] = __ldcs(x + i);
                 if (a.res) pr[j] = __ldcs(res + i);
@@ -137,30 +190,23 @@ __global__ void __launch_bounds__(NT, V <= 2 ? 1024 / NT : 1) norm_kernel(NormAr
     fetch(blockIdx.x);
     float w[V][N];
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-#pragma unroll
-        for (int e = 0; e < N; e += 4) {
-            const int i = j * NT + threadIdx.x;
-            float4 x = make_float4(1.f, 1.f, 1.f, 1.f);
-            if (a.w && i < nv) x = __ldg(reinterpret_cast<const float4 *>(a.w) + (i * N + e) / 4);
-            w[j][e] = x.x, w[j][e + 1] = x.y, w[j][e + 2] = x.z, w[j][e + 3] = x.w;
-        }
+    for (int j = 0; j < V; ++j) load_weights(a.w, j * NT + threadIdx.x, j * NT + threadIdx.x < nv, w[j]);
     int buf = 0;
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
         float h[V][N];
         float sum = 0.f;
-        uint4 *ho = a.h ? reinterpret_cast<uint4 *>(static_cast<T *>(a.h) + row * a.C) : nullptr;
+        Raw *ho = a.h ? reinterpret_cast<Raw *>(static_cast<T *>(a.h) + row * a.C) : nullptr;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int i = j * NT + threadIdx.x;
-            Vec<T>::unpack(px[j], h[j]);
+            Vec<T, N>::unpack(px[j], h[j]);
             if (a.res) {
                 float r[N];
-                Vec<T>::unpack(pr[j], r);
+                Vec<T, N>::unpack(pr[j], r);
 #pragma unroll
                 for (int e = 0; e < N; ++e) h[j][e] += r[e];
             }
-            if (ho && i < nv) __stcs(ho + i, Vec<T>::pack(h[j]));
+            if (ho && i < nv) __stcs(ho + i, Vec<T, N>::pack(h[j]));
 #pragma unroll
             for (int e = 0; e < N; ++e) sum = fmaf(h[j][e], h[j][e], sum);
         }
@@ -168,12 +214,12 @@ __global__ void __launch_bounds__(NT, V <= 2 ? 1024 / NT : 1) norm_kernel(NormAr
         sum = block_all<NT, false>(sum, red[buf]);
         const float r = rsqrtf(sum / a.C + a.eps);
         if (!a.out_e4m3) {
-            uint4 *y = reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + row * a.C);
+            Raw *y = reinterpret_cast<Raw *>(static_cast<T *>(a.y) + row * a.C);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
 #pragma unroll
                 for (int e = 0; e < N; ++e) h[j][e] *= r * w[j][e];
-                if (j * NT + threadIdx.x < nv) __stcs(y + j * NT + threadIdx.x, Vec<T>::pack(h[j]));
+                if (j * NT + threadIdx.x < nv) __stcs(y + j * NT + threadIdx.x, Vec<T, N>::pack(h[j]));
             }
             continue;
         }
@@ -215,8 +261,8 @@ __global__ void __launch_bounds__(NT, V <= 2 ? 1024 / NT : 1) norm_kernel(NormAr
     }
 }
 
-// Any C: the row is read again after its sum of squares (and again for its
-// maximum), element by element, from L2: 16384 x 2047 bf16 49 us, 2.7 TB/s.
+// Any C, for rows that the registers do not hold: the row is read again after its
+// sum of squares (and again for its maximum), element by element, from L2.
 // Groups are not offered here.
 template <typename T>
 __global__ void __launch_bounds__(256) norm_any_kernel(NormArgs a) {
@@ -267,9 +313,24 @@ unsigned resident(long long rows) {
     return (unsigned)(rows < full ? rows : full);
 }
 
-template <typename T, int NT, int V>
+template <typename T, int N, int NT, int V>
 void launch_v(const NormArgs &a, cudaStream_t stream) {
-    norm_kernel<T, NT, V><<<resident<norm_kernel<T, NT, V>, NT>(a.rows), NT, 0, stream>>>(a);
+    norm_kernel<T, N, NT, V><<<resident<norm_kernel<T, N, NT, V>, NT>(a.rows), NT, 0, stream>>>(a);
+}
+
+// Rows of narrow vectors: eight a thread.  Element by element in two passes they
+// took 49 us where this takes 45 (16384 x 2047 bf16 without a residual), and the
+// backward 108 where it takes 56.
+template <typename T, int N>
+void launch_narrow(const NormArgs &a, cudaStream_t stream) {
+    const int nv = a.C / N;
+    if (nv <= 64) launch_v<T, N, 32, 2>(a, stream);
+    else if (nv <= 256) launch_v<T, N, 32, 8>(a, stream);
+    else if (nv <= 512) launch_v<T, N, 64, 8>(a, stream);
+    else if (nv <= 1024) launch_v<T, N, 128, 8>(a, stream);
+    else if (nv <= 2048) launch_v<T, N, 256, 8>(a, stream);
+    else if (nv <= 4096) launch_v<T, N, 512, 8>(a, stream);
+    else norm_any_kernel<T><<<(unsigned)a.rows, 256, 0, stream>>>(a);
 }
 
 // Two vectors a thread, four from 4096 bf16 columns on: one leaves the sums over
@@ -277,26 +338,28 @@ void launch_v(const NormArgs &a, cudaStream_t stream) {
 // 75), eight too few warps (4096 columns: 97 against 75).
 template <typename T>
 void launch_t(const NormArgs &a, cudaStream_t stream) {
-    constexpr int N = Vec<T>::N;
+    constexpr int N = kWide<T>;
     const int nv = a.C / N;
-    if (a.C % N != 0 || nv > 4096) {
+    if (a.C % N != 0) {
+        sizeof(T) == 2 && a.C % 2 == 0 ? launch_narrow<T, sizeof(T) == 2 ? 2 : 1>(a, stream) : launch_narrow<T, 1>(a, stream);
+    } else if (nv > 4096) {
         norm_any_kernel<T><<<(unsigned)a.rows, 256, 0, stream>>>(a);
     } else if (nv <= 32) {
-        launch_v<T, 32, 1>(a, stream);
+        launch_v<T, N, 32, 1>(a, stream);
     } else if (nv <= 64) {
-        launch_v<T, 32, 2>(a, stream);
+        launch_v<T, N, 32, 2>(a, stream);
     } else if (nv <= 128) {
-        launch_v<T, 64, 2>(a, stream);
+        launch_v<T, N, 64, 2>(a, stream);
     } else if (nv <= 256) {
-        launch_v<T, 128, 2>(a, stream);
+        launch_v<T, N, 128, 2>(a, stream);
     } else if (nv <= 512) {
-        launch_v<T, 128, 4>(a, stream);
+        launch_v<T, N, 128, 4>(a, stream);
     } else if (nv <= 1024) {
-        launch_v<T, 256, 4>(a, stream);
+        launch_v<T, N, 256, 4>(a, stream);
     } else if (nv <= 2048) {
-        launch_v<T, 512, 4>(a, stream);
+        launch_v<T, N, 512, 4>(a, stream);
     } else {
-        launch_v<T, 512, 8>(a, stream);
+        launch_v<T, N, 512, 8>(a, stream);
     }
 }
 
@@ -309,36 +372,33 @@ constexpr int kBwdThreads = 256;
 // the same in every row, so its share of dw stays in registers until the rows
 // are done; then the groups' shares are added in order to part[blockIdx.x][C].
 // Bound by the bytes: bf16, 16384 x 2048 with a residual's gradient 41 us, 268 MB
-// at 6.6 TB/s.
-template <typename T, int NT, int V>
-__global__ void __launch_bounds__(kBwdThreads, V == 1 ? 4 : V == 2 ? 2 : 1) norm_bwd_kernel(NormBwdArgs a, float *part) {
-    constexpr int N = Vec<T>::N, GROUPS = kBwdThreads / NT;
+// at 6.6 TB/s (x 2046 45, x 2047 62).
+template <typename T, int N, int NT, int V>
+__global__ void __launch_bounds__(kBwdThreads, V == 1 ? 4 : V == 4 || V == 16 ? 1 : 2) norm_bwd_kernel(NormBwdArgs a, float *part) {
+    using Raw = typename Vec<T, N>::Raw;
+    constexpr int GROUPS = kBwdThreads / NT;
     __shared__ float red[2][2][kBwdThreads / 32];
-    __shared__ float4 share[GROUPS > 1 ? kBwdThreads * N * V / 4 : 1];
+    __shared__ __align__(16) float share[GROUPS > 1 ? kBwdThreads * N * V : 1];
     const int nv = a.C / N, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = threadIdx.x / NT, tid = threadIdx.x % NT, first = group * (NT / 32);
     const long long step = (long long)gridDim.x * GROUPS;
     float dw[V][N], w[V][N];
 #pragma unroll
-    for (int j = 0; j < V; ++j)
+    for (int j = 0; j < V; ++j) {
+        load_weights(a.w, j * NT + tid, j * NT + tid < nv, w[j]);
 #pragma unroll
-        for (int e = 0; e < N; e += 4) {
-            const int i = j * NT + tid;
-            float4 x = make_float4(1.f, 1.f, 1.f, 1.f);
-            if (a.w && i < nv) x = __ldg(reinterpret_cast<const float4 *>(a.w) + (i * N + e) / 4);
-            w[j][e] = x.x, w[j][e + 1] = x.y, w[j][e + 2] = x.z, w[j][e + 3] = x.w;
-            dw[j][e] = dw[j][e + 1] = dw[j][e + 2] = dw[j][e + 3] = 0.f;
-        }
+        for (int e = 0; e < N; ++e) dw[j][e] = 0.f;
+    }
     int buf = 0;
-    uint4 nh[V], nd[V], nr[V];
+    Raw nh[V], nd[V], nr[V];
     auto fetch = [&](long long row) {  // the next row is on its way while this one is summed and written
-        const uint4 *h4 = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.h) + row * a.C);
-        const uint4 *dy4 = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.dy) + row * a.C);
-        const uint4 *dr4 = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.dres) + row * a.C);
+        const Raw *h4 = reinterpret_cast<const Raw *>(static_cast<const T *>(a.h) + row * a.C);
+        const Raw *dy4 = reinterpret_cast<const Raw *>(static_cast<const T *>(a.dy) + row * a.C);
+        const Raw *dr4 = reinterpret_cast<const Raw *>(static_cast<const T *>(a.dres) + row * a.C);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int i = j * NT + tid;
-            nh[j] = nd[j] = nr[j] = make_uint4(0, 0, 0, 0);
+            nh[j] = nd[j] = nr[j] = Raw{};
             if (row < a.rows && i < nv) {
                 nh[j] = __ldcs(h4 + i);
                 nd[j] = __ldcs(dy4 + i);
@@ -349,7 +409,7 @@ __global__ void __launch_bounds__(kBwdThreads, V == 1 ? 4 : V == 2 ? 2 : 1) norm
     long long row = (long long)blockIdx.x * GROUPS + group;
     fetch(row);
     for (; row < a.rows; row += step, buf ^= 1) {
-        uint4 ph[V], pd[V], pr[V];
+        Raw ph[V], pd[V], pr[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) ph[j] = nh[j], pd[j] = nd[j], pr[j] = nr[j];
         fetch(row + step);
@@ -357,8 +417,8 @@ __global__ void __launch_bounds__(kBwdThreads, V == 1 ? 4 : V == 2 ? 2 : 1) norm
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             float h[N], d[N];
-            Vec<T>::unpack(ph[j], h);
-            Vec<T>::unpack(pd[j], d);
+            Vec<T, N>::unpack(ph[j], h);
+            Vec<T, N>::unpack(pd[j], d);
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 ss = fmaf(h[e], h[e], ss);
@@ -381,49 +441,51 @@ __global__ void __launch_bounds__(kBwdThreads, V == 1 ? 4 : V == 2 ? 2 : 1) norm
         }
         const float r = rsqrtf(ss / a.C + a.eps);
         const float m = r * r * (sp / a.C);
-        uint4 *dx = reinterpret_cast<uint4 *>(static_cast<T *>(a.dx) + row * a.C);
+        Raw *dx = reinterpret_cast<Raw *>(static_cast<T *>(a.dx) + row * a.C);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int i = j * NT + tid;
             float h[N], d[N], g[N];
-            Vec<T>::unpack(ph[j], h);
-            Vec<T>::unpack(pd[j], d);
-            Vec<T>::unpack(pr[j], g);
+            Vec<T, N>::unpack(ph[j], h);
+            Vec<T, N>::unpack(pd[j], d);
+            Vec<T, N>::unpack(pr[j], g);
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 g[e] = fmaf(r, fmaf(d[e], w[j][e], -h[e] * m), g[e]);
                 dw[j][e] = fmaf(d[e], h[e] * r, dw[j][e]);
             }
-            if (i < nv) __stcs(dx + i, Vec<T>::pack(g));
+            if (i < nv) __stcs(dx + i, Vec<T, N>::pack(g));
         }
     }
-    float4 *to = reinterpret_cast<float4 *>(part + (size_t)blockIdx.x * a.C);
+    float *to = part + (size_t)blockIdx.x * a.C;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int i = j * NT + tid;
+        float *mine = GROUPS > 1 ? share + (group * V * NT + i) * N : to + (size_t)i * N;
+        if (GROUPS > 1 || i < nv) {
+            if constexpr (N % 4 == 0) {
 #pragma unroll
-        for (int e = 0; e < N; e += 4) {
-            const float4 x = make_float4(dw[j][e], dw[j][e + 1], dw[j][e + 2], dw[j][e + 3]);
-            if constexpr (GROUPS > 1) share[(group * V * NT + i) * (N / 4) + e / 4] = x;
-            else if (i < nv) to[(i * N + e) / 4] = x;
+                for (int e = 0; e < N; e += 4)
+                    *reinterpret_cast<float4 *>(mine + e) = make_float4(dw[j][e], dw[j][e + 1], dw[j][e + 2], dw[j][e + 3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e) mine[e] = dw[j][e];
+            }
         }
     }
     if constexpr (GROUPS > 1) {
         __syncthreads();
-        for (int i = threadIdx.x; i < a.C / 4; i += kBwdThreads) {
-            float4 x = share[i];
+        for (int i = threadIdx.x; i < a.C; i += kBwdThreads) {
+            float x = share[i];
 #pragma unroll
-            for (int g = 1; g < GROUPS; ++g) {
-                const float4 y = share[g * V * NT * (N / 4) + i];
-                x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-            }
+            for (int g = 1; g < GROUPS; ++g) x += share[g * V * NT * N + i];
             to[i] = x;
         }
     }
 }
 
-// Any C: rows are read twice; dw's share of a column is summed in `part`.
-// 16384 x 2047 bf16: 108 us.
+// Any C, for rows that the registers do not hold: rows are read twice, and dw's
+// share of a column is summed in `part` (8192 x 4095 bf16 took 223 us here).
 template <typename T>
 __global__ void __launch_bounds__(kBwdThreads) norm_bwd_any_kernel(NormBwdArgs a, float *part) {
     constexpr int NT = kBwdThreads;
@@ -486,18 +548,34 @@ int launch_rows(const NormBwdArgs &a, int most, float *part, cudaStream_t stream
     return ctas;
 }
 
+template <typename T, int N>
+int launch_bwd_narrow(const NormBwdArgs &a, int most, float *part, cudaStream_t stream) {
+    const int nv = a.C / N;
+    if (nv <= 64) return launch_rows<norm_bwd_kernel<T, N, 32, 2>>(a, most, part, stream);
+    if (nv <= 256) return launch_rows<norm_bwd_kernel<T, N, 32, 8>>(a, most, part, stream);
+    if (nv <= 512) return launch_rows<norm_bwd_kernel<T, N, 64, 8>>(a, most, part, stream);
+    if (nv <= 1024) return launch_rows<norm_bwd_kernel<T, N, 128, 8>>(a, most, part, stream);
+    if (nv <= 2048) return launch_rows<norm_bwd_kernel<T, N, kBwdThreads, 8>>(a, most, part, stream);
+    if (nv <= 4096) return launch_rows<norm_bwd_kernel<T, N, kBwdThreads, 16>>(a, most, part, stream);
+    return launch_rows<norm_bwd_any_kernel<T>>(a, most, part, stream);
+}
+
 template <typename T>
 int launch_bwd_t(const NormBwdArgs &a, int most, float *part, cudaStream_t stream) {
-    const int nv = a.C / Vec<T>::N;
-    if (a.C % Vec<T>::N != 0 || nv > 4 * kBwdThreads) return launch_rows<norm_bwd_any_kernel<T>>(a, most, part, stream);
+    constexpr int N = kWide<T>;
+    const int nv = a.C / N;
+    if (a.C % N != 0)
+        return sizeof(T) == 2 && a.C % 2 == 0 ? launch_bwd_narrow<T, sizeof(T) == 2 ? 2 : 1>(a, most, part, stream)
+                                              : launch_bwd_narrow<T, 1>(a, most, part, stream);
+    if (nv > 4 * kBwdThreads) return launch_rows<norm_bwd_any_kernel<T>>(a, most, part, stream);
     // two vectors a thread, whose loads cover more of a row's sums than one's
     // (bf16, 131072 x 512: 82 us against 102)
-    if (nv <= 32) return launch_rows<norm_bwd_kernel<T, 32, 1>>(a, most, part, stream);
-    if (nv <= 64) return launch_rows<norm_bwd_kernel<T, 32, 2>>(a, most, part, stream);
-    if (nv <= 128) return launch_rows<norm_bwd_kernel<T, 64, 2>>(a, most, part, stream);
-    if (nv <= 256) return launch_rows<norm_bwd_kernel<T, 128, 2>>(a, most, part, stream);
-    if (nv <= 2 * kBwdThreads) return launch_rows<norm_bwd_kernel<T, kBwdThreads, 2>>(a, most, part, stream);
-    return launch_rows<norm_bwd_kernel<T, kBwdThreads, 4>>(a, most, part, stream);
+    if (nv <= 32) return launch_rows<norm_bwd_kernel<T, N, 32, 1>>(a, most, part, stream);
+    if (nv <= 64) return launch_rows<norm_bwd_kernel<T, N, 32, 2>>(a, most, part, stream);
+    if (nv <= 128) return launch_rows<norm_bwd_kernel<T, N, 64, 2>>(a, most, part, stream);
+    if (nv <= 256) return launch_rows<norm_bwd_kernel<T, N, 128, 2>>(a, most, part, stream);
+    if (nv <= 2 * kBwdThreads) return launch_rows<norm_bwd_kernel<T, N, kBwdThreads, 2>>(a, most, part, stream);
+    return launch_rows<norm_bwd_kernel<T, N, kBwdThreads, 4>>(a, most, part, stream);
 }
 
 }  // namespace
