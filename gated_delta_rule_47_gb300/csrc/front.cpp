@@ -104,6 +104,16 @@ double number(PyObject *o) {
     return x;
 }
 
+// A flag, by its truth as Python has it.
+bool truth(PyObject *o) {
+    const int yes = PyObject_IsTrue(o);
+    if (yes < 0) {
+        PyErr_Clear();
+        throw Odd{};
+    }
+    return yes;
+}
+
 Tensor scratch(size_t bytes, const Tensor &like) {
     need(bytes != (size_t)-1);
     return bytes ? at::empty({(int64_t)bytes}, like.options().dtype(at::kByte)) : Tensor();
@@ -171,7 +181,7 @@ PyObject *step(PyObject *, PyObject *const *x, Py_ssize_t n) {
         dense(beta, {B, H}, type);
         need(slots || B <= pages);
         const float scale = (float)number(x[8]);
-        const unsigned flags = (per_head ? GDN_G_PER_HEAD : 0) | (x[9] == Py_True ? GDN_QK_L2NORM : 0);
+        const unsigned flags = (per_head ? GDN_G_PER_HEAD : 0) | (truth(x[9]) ? GDN_QK_L2NORM : 0);
         Tensor o = at::empty_like(v);
         float *out = to ? to.ptr<float>() : s.data_ptr<float>();
         void *stream = stream_of(q);
@@ -192,7 +202,7 @@ PyObject *norm(PyObject *, PyObject *const *x, Py_ssize_t n) {
         need(in.dim() > 0);
         const int64_t C = in.size(-1), group = (int64_t)number(x[5]), rows = C ? in.numel() / C : 0;
         const int dt = code(in);
-        const bool e4m3 = x[4] == Py_True;
+        const bool e4m3 = truth(x[4]);
         ints({C});
         dense(in, in.sizes(), in.scalar_type());
         dense(res, in.sizes(), in.scalar_type());
@@ -302,7 +312,7 @@ struct Prompt {
             seqs = cu.t->numel() - 1;
         }
         dense(s0, {seqs, H, Dk, Dv}, at::kFloat);
-        flags = (per_head ? GDN_G_PER_HEAD : 0) | (simt == Py_True ? GDN_PATH_SIMT : 0);
+        flags = (per_head ? GDN_G_PER_HEAD : 0) | (truth(simt) ? GDN_PATH_SIMT : 0);
     }
     // [..,D] with D contiguous, other strides multiples of 16 bytes and none of 0 over several elements
     void strided(const Tensor &t, IntArrayRef shape, at::ScalarType type) {
@@ -324,11 +334,10 @@ PyObject *fwd(PyObject *, PyObject *const *x, Py_ssize_t n) {
         const Tensor &q = tensor(x[0]), &k = tensor(x[1]), &v = tensor(x[2]), &g = tensor(x[3]);
         const Maybe s0(x[4]), cu(x[6]);
         const Prompt p(q, k, v, g, s0, cu, x[8]);
-        const int sure = PyObject_IsTrue(x[5]);
-        need(sure >= 0);
+        const bool final_state = truth(x[5]);
         const size_t bytes = api.fwd_bytes(p.B, p.H, p.Hk, p.T, p.Dk, p.Dv, p.seqs, cu ? 1 : 0, p.flags, p.dt);
         Tensor o = at::empty_like(v), sf, ws = scratch(bytes, q);
-        if (sure) sf = at::empty({p.seqs, p.H, p.Dk, p.Dv}, g.options());
+        if (final_state) sf = at::empty({p.seqs, p.H, p.Dk, p.Dv}, g.options());
         long long st[15];
         const bool plain = p.plain && o.is_contiguous();
         if (!plain) steps(q, st), steps(k, st + 3), steps(v, st + 6), steps(o, st + 9), steps(g, st + 12);
