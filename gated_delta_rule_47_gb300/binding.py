@@ -896,6 +896,8 @@ def linattn_step(q, k, v, g, state, slots=None, state_out=None, scale=1.0, o=Non
 def gdn_step(q, k, v, beta, g, state, slots=None, state_out=None, scale=1.0, l2norm=False, o=None, stream=None):
     """One token of the gated delta rule (gdn_chunk_fwd's recurrence) against a
     pool of states; beta [B,H], the rest as linattn_step."""
+    if beta is None:
+        raise TypeError("beta must be a CUDA tensor (the step without the delta rule is linattn_step)")
     return _step("gdn_step", q, k, v, beta, g, state, slots, state_out, scale, l2norm, o, stream)
 
 
