@@ -974,7 +974,7 @@ def _pool(pool):
     if pool.dim() < 2 or not pool.is_contiguous():
         raise ValueError("pool must be a contiguous [layers,slots,...] tensor")
     layers, n_slots = pool.shape[:2]
-    page = pool.stride(1) * pool.element_size() if layers and n_slots else 0
+    page = pool.stride(1) * pool.element_size() if pool.numel() else 0
     if page % 16:
         raise ValueError(f"a page of {page} bytes is not a multiple of 16")
     return layers, n_slots, page

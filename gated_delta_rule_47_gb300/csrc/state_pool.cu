@@ -150,6 +150,7 @@ __global__ void free_kernel(unsigned char *live, int n_slots, const int *slots, 
 
 int launch_moves(const PoolArgs &p, const int *src, const int *dst, int most, const int *count, cudaStream_t stream) {
     const long long pieces = (p.page_bytes / 16 + kPiece - 1) / kPiece * p.layers * most;
+    if (pieces == 0) return GDN_OK;  // a pool without bytes: its marks alone
     const long long full = 8LL * device_sm_count();  // 2,048 threads an SM
     move_kernel<<<(unsigned)(pieces < full ? pieces : full), kThreads, 0, stream>>>(p, src, dst, most, count);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
