@@ -7,8 +7,9 @@ stream.  All computation happens in the library's kernels; there is no
 fallback: if ``libgdn.so`` is missing or fails to load, ``load()`` raises.
 
 The layer operators, whose smallest calls are bound by the host, go through
-``_front.so`` first, which does the same for calls in which all is well and
-declines the others.
+a native module (``build.front_path``) first, which does the same for calls in
+which all is well and declines the others.  It is loaded by the first call of
+one of them; the other operators need ``libgdn.so`` alone.
 """
 from __future__ import annotations
 
@@ -22,9 +23,11 @@ import threading
 
 import torch
 
+from .build import front_path
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libgdn.so")
-FRONT_PATH = os.path.join(_PKG, "_build", "_front.so")
+FRONT_PATH = front_path(torch.__version__)
 
 GDN_F32, GDN_BF16 = 0, 1
 GDN_QK_L2NORM = 1
@@ -145,15 +148,13 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.gdn_set_cluster_shape.restype = i
         lib.gdn_launch_count.restype = ctypes.c_ulonglong
         if path is None:
-            _load_front(lib)
             _lib = lib
         return lib
 
 
 def _load_front(lib):
-    global _front
     if not os.path.exists(FRONT_PATH):
-        raise RuntimeError(f"_front.so not found at {FRONT_PATH}; build it with "
+        raise RuntimeError(f"the layer operators' module for this torch and Python is not at {FRONT_PATH}; build it with "
                            "`python -m gated_delta_rule_47_gb300.build`")
     loader = importlib.machinery.ExtensionFileLoader("_front", FRONT_PATH)
     front = importlib.util.module_from_spec(importlib.util.spec_from_loader("_front", loader))
@@ -164,12 +165,16 @@ def _load_front(lib):
              "state_pool_compact_workspace_bytes", "state_pool_compact")
     stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent without CUDA, where nothing asks for it
     front.init(tuple(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in names), stream, _raise)
-    _front = front
+    return front
 
 
 def _quick():
     """The front, loaded."""
-    load()
+    global _front
+    lib = load()
+    with _lock:
+        if _front is None:
+            _front = _load_front(lib)
     return _front
 
 
