@@ -14,6 +14,7 @@
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
 #include <ATen/ops/empty_strided.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "gdn.h"
@@ -140,17 +141,17 @@ PyObject *pack(std::initializer_list<Tensor> ts) {
 }
 
 // Runs f, which gives the answer; what binding.py reports or takes is left to it.
+// An allocation that failed is torch's own error, as on the long way.
 template <typename F>
 PyObject *guarded(Py_ssize_t given, Py_ssize_t wanted, F f) {
+    HANDLE_TH_ERRORS
     try {
         need(given == wanted);
         return f();
     } catch (const Odd &) {
         Py_RETURN_NOTIMPLEMENTED;
-    } catch (const std::exception &e) {  // an allocation that failed, say
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
     }
+    END_HANDLE_TH_ERRORS
 }
 bool good(const char *name, int status) {
     if (status == GDN_OK) return true;
