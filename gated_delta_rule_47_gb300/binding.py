@@ -746,9 +746,19 @@ def _on(stream):
     return _HERE if stream is None else torch.cuda.stream(stream)
 
 
-def _overlaps(t):
-    """Whether elements share memory (an expanded tensor)."""
+def _expanded(t):
     return any(s == 0 and n > 1 for n, s in zip(t.shape, t.stride()))
+
+
+def _overlaps(t):
+    """Whether elements may share memory (an expanded tensor, sliding windows):
+    a dimension steps by less than those of smaller steps span."""
+    span = 1
+    for s, n in sorted((s, n) for n, s in zip(t.shape, t.stride()) if n > 1):
+        if s < span:
+            return True
+        span += s * (n - 1)
+    return False
 
 
 def _linattn_sizes(q, k, v, g, cu_seqlens, initial_state):
@@ -794,7 +804,7 @@ def linattn_chunk_fwd(q, k, v, g, initial_state=None, output_final_state=False, 
     need = _bytes("linattn_chunk_fwd_workspace_bytes", B, H, Hk, T, Dk, Dv, n_seq, cu_seqlens is not None, flags, code)
     with _on(stream):
         if not dense:
-            q, k, v = (t.contiguous() if _overlaps(t) else t for t in (q, k, v))
+            q, k, v = (t.contiguous() if _expanded(t) else t for t in (q, k, v))
         if o is None:
             o = torch.empty_like(v)
             dense = dense and o.is_contiguous()
@@ -831,7 +841,8 @@ def linattn_chunk_bwd(q, k, v, g, dout, initial_state=None, dfinal_state=None, c
     with _on(stream):
         if not dense:
             # gradients take their tensors' strides, so those may not overlap
-            q, k, v, g, dout = (t.contiguous() if _overlaps(t) else t for t in (q, k, v, g, dout))
+            q, k, v, g = (t.contiguous() if _overlaps(t) else t for t in (q, k, v, g))
+            dout = dout.contiguous() if _expanded(dout) else dout
         dq, dk, dv, dg = (torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device) for t in (q, k, v, g))
         ds0 = torch.empty_like(initial_state) if initial_state is not None else None
         if workspace is None:

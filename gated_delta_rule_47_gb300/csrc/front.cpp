@@ -10,6 +10,9 @@
 
 #include <limits.h>
 
+#include <algorithm>
+#include <utility>
+
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
@@ -325,6 +328,20 @@ struct Prompt {
             need(t.size(i) <= 1 || (t.stride(i) > 0 && t.stride(i) * t.element_size() % 16 == 0));
     }
 };
+// No two elements in one place, as far as strides tell: each dimension steps by
+// at least what those of smaller steps span.
+void apart(const Tensor &t) {
+    std::pair<int64_t, int64_t> by[4];  // step, elements
+    int n = 0;
+    for (int i = 0; i < t.dim(); ++i)
+        if (t.size(i) > 1) by[n++] = {t.stride(i), t.size(i)};
+    std::sort(by, by + n);
+    int64_t span = 1;
+    for (int i = 0; i < n; ++i) {
+        need(by[i].first >= span);
+        span += by[i].first * (by[i].second - 1);
+    }
+}
 void steps(const Tensor &t, long long *out) {
     for (int i = 0; i < 3; ++i) out[i] = t.dim() > 1 && t.size(i) > 1 ? t.stride(i) : 0;
 }
@@ -357,9 +374,8 @@ PyObject *bwd(PyObject *, PyObject *const *x, Py_ssize_t n) {
         Prompt p(q, k, v, g, s0, cu, x[9]);
         p.strided(go, {p.B, p.H, p.T, p.Dv}, q.scalar_type());
         dense(dsf, {p.seqs, p.H, p.Dk, p.Dv}, at::kFloat);
-        // g's gradient takes its strides
-        if (g.dim() > 1)
-            for (int i = 0; i < 3; ++i) need(g.size(i) <= 1 || g.stride(i) > 0);
+        // gradients take their tensors' strides
+        if (!p.plain) apart(q), apart(k), apart(v), apart(g);
         const size_t bytes = api.bwd_bytes(p.B, p.H, p.Hk, p.T, p.Dk, p.Dv, p.seqs, cu ? 1 : 0, p.flags, p.dt);
         auto like = [](const Tensor &t) { return at::empty_strided(t.sizes(), t.strides(), t.options()); };
         Tensor dq = like(q), dk = like(k), dv = like(v), dg = like(g), ds0, ws = scratch(bytes, q);

@@ -4,6 +4,9 @@
 // gdn_api.cu nothing is allocated, nothing waits and no exception crosses.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <utility>
+
 #include "api_util.h"
 #include "gdn_internal.h"
 #include "layer_ops.h"
@@ -24,6 +27,20 @@ bool bad_strides(const Strides &s, int dtype) {
     return ((s.b | s.h | s.t) & m) != 0;
 }
 bool negative(const Strides &s) { return s.b < 0 || s.h < 0 || s.t < 0; }
+
+// Whether elements of a [B,H,T,D] tensor that is written may share memory: a
+// dimension steps by less than those of smaller steps span.
+bool overlaps(const Strides &s, int B, int H, int T, int D) {
+    std::pair<long long, int> by[3] = {{s.b, B}, {s.h, H}, {s.t, T}};
+    std::sort(by, by + 3);
+    long long span = D;
+    for (const auto &d : by) {
+        if (d.second <= 1) continue;
+        if (d.first < span) return true;
+        span += d.first * (d.second - 1);
+    }
+    return false;
+}
 
 Strides dense(int H, int T, int D) { return {(long long)H * T * D, (long long)T * D, D}; }
 
@@ -143,6 +160,7 @@ int linattn_chunk_fwd(const void *q, const void *k, const void *v, const float *
     if (!empty(a) && (!q || !k || !v || !g || !o)) return GDN_ERR_INVALID_ARG;
     st = check_tensors(a);
     if (st != GDN_OK) return st;
+    if (!empty(a) && overlaps(a.so, B, H, T, Dv)) return GDN_ERR_INVALID_ARG;
     const cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
     if (empty(a) || n_seq == 0) {
         if (!empty(a)) return GDN_ERR_INVALID_ARG;  // tokens, but no sequence that holds them
@@ -175,6 +193,10 @@ int linattn_chunk_bwd(const void *q, const void *k, const void *v, const float *
     if (!empty(a) && (!q || !k || !v || !g || !dout || !dq || !dk || !dv || !dg)) return GDN_ERR_INVALID_ARG;
     st = check_tensors(a);
     if (st != GDN_OK) return st;
+    // gradients have these strides
+    if (!empty(a) && (overlaps(a.sq, B, Hk, T, Dk) || overlaps(a.sk, B, Hk, T, Dk) || overlaps(a.sv, B, H, T, Dv) ||
+                      (!(flags & GDN_G_PER_HEAD) && overlaps(a.sg, B, H, T, 1))))
+        return GDN_ERR_INVALID_ARG;
     const cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
     if (empty(a) || n_seq == 0) {
         if (!empty(a)) return GDN_ERR_INVALID_ARG;

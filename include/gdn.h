@@ -507,7 +507,9 @@ int cam_prep_bwd(const void *q_raw, const void *k_raw, const float *q_norm_w, co
  *           contiguous.  Those of q, k, v, o are multiples of 16 bytes
  *           (GDN_ERR_MISALIGNED), not negative and, for bf16 q, k, v without
  *           GDN_PATH_SIMT, not 0 over more than one element
- *           (GDN_ERR_UNSUPPORTED).  A token-major [T,H,D] tensor is a
+ *           (GDN_ERR_UNSUPPORTED).  o's elements lie apart: a dimension steps
+ *           by at least what those of smaller steps span
+ *           (GDN_ERR_INVALID_ARG).  A token-major [T,H,D] tensor is a
  *           [1,H,T,D] one with strides (0, D, H*D).
  *   flags   0 or GDN_G_PER_HEAD, GDN_PATH_SIMT
  *   Dk, Dv  64 or 128 each; n_seq and B up to 65534, H up to 65535
@@ -535,7 +537,9 @@ int linattn_chunk_fwd(const void *q, const void *k, const void *v, const float *
  *           heads get the sum over their value heads); dg those of g, fp32
  *           (with GDN_G_PER_HEAD the sum over batch and tokens)
  *   dinitial_state [n_seq,H,Dk,Dv] fp32 or NULL (not wanted)
- *   strides those of q, k, v, dout, g, or NULL
+ *   strides those of q, k, v, dout, g, or NULL; as dq, dk, dv and dg are
+ *           written with them, those of q, k, v and g are of elements that lie
+ *           apart, as o's in linattn_chunk_fwd
  * Tokens of no sequence get zeros.  Every sum has a fixed order: equal calls
  * give equal bits.
  */
