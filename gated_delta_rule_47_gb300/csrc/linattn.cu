@@ -44,9 +44,9 @@ constexpr int kTableThreads = 1024;
 // the tables' room, so that no entry leads outside the tensors.
 __global__ void __launch_bounds__(kTableThreads) table_kernel(const int *cu, int n_seq, int T, int C, int4 *chunks,
                                                               int4 *seqs, int bound) {
-    __shared__ int sums[32];
+    __shared__ long long sums[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int first = 0;
+    long long first = 0;
     for (int s0 = 0; s0 < n_seq; s0 += kTableThreads) {
         const int s = s0 + threadIdx.x;
         int start = 0, len = 0;
@@ -55,31 +55,31 @@ __global__ void __launch_bounds__(kTableThreads) table_kernel(const int *cu, int
             len = max(min(cu[s + 1], T) - start, 0);
         }
         const int n = (int)(((long long)len + C - 1) / C);
-        int y = n;
+        long long y = n;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
-            const int t = __shfl_up_sync(~0u, y, m);
+            const long long t = __shfl_up_sync(~0u, y, m);
             if (lane >= m) y += t;
         }
         __syncthreads();
         if (lane == 31) sums[warp] = y;
         __syncthreads();
         if (warp == 0) {
-            int z = sums[lane];
+            long long z = sums[lane];
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
-                const int t = __shfl_up_sync(~0u, z, m);
+                const long long t = __shfl_up_sync(~0u, z, m);
                 if (lane >= m) z += t;
             }
             sums[lane] = z;
         }
         __syncthreads();
-        const int at = first + y - n + (warp ? sums[warp - 1] : 0);
+        const int2 in = in_table(first + y - n + (warp ? sums[warp - 1] : 0), n, bound);
         first += sums[31];
-        if (s < n_seq) seqs[s] = make_int4(min(at, bound), max(min(n, bound - at), 0), start, len);
+        if (s < n_seq) seqs[s] = make_int4(in.x, in.y, start, len);
     }
     __syncthreads();
-    const int count = min(first, bound);
+    const int count = in_table(first, 0, bound).x;
     const int head = min(max(cu[0], 0), T), tail = min(max(cu[n_seq], 0), T);
     const int fill0 = (head + C - 1) / C;
     for (int ci = threadIdx.x; ci < bound; ci += kTableThreads) {

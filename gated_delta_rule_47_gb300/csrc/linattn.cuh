@@ -61,6 +61,14 @@ inline int chunk_bound(const LinAttnArgs &a, int C) {
     return (int)((long long)a.B * ((a.T + C - 1) / C));
 }
 
+// {first chunk, chunks} of n chunks from `at` on in a table with room for
+// `bound`.  In 64 bits: sequences of offsets out of order overlap, and up to
+// 65534 of them may count every token.
+__host__ __device__ inline int2 in_table(long long at, int n, int bound) {
+    const long long room = at < bound ? bound - at : 0;
+    return make_int2((int)(bound - room), (int)(n < room ? n : room));
+}
+
 // Bytes of the tables (a multiple of 256).
 inline size_t table_bytes(const LinAttnArgs &a, int C) {
     if (!a.cu) return 0;
