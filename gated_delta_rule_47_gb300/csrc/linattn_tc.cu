@@ -918,9 +918,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (kind == kFill) {  // packed: zeros for the tokens of no sequence
             const int T = p.a.T, head = min(max(p.a.cu[0], 0), T), tail = min(max(p.a.cu[p.a.n_seq], 0), T);
 #pragma unroll 1
-            for (int e = threadIdx.x; e < (head + T - tail) * 8; e += kFwdThreads) {
-                const int i = e >> 3, t = i < head ? i : tail + i - head;
-                *reinterpret_cast<uint4 *>(at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, 0, h, t) + 64 * slice + (e & 7) * 8) =
+            for (long long e = threadIdx.x; e < ((long long)head + T - tail) * 8; e += kFwdThreads) {
+                const long long i = e >> 3, t = i < head ? i : tail + i - head;
+                *reinterpret_cast<uint4 *>(at(static_cast<__nv_bfloat16 *>(p.a.o), p.a.so, 0, h, (int)t) + 64 * slice + (e & 7) * 8) =
                     make_uint4(0, 0, 0, 0);
             }
             if (PLANNED && threadIdx.x == 0) take(item + 1, base, full);
