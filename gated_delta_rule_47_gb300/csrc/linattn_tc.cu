@@ -22,6 +22,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "gdn_internal.h"
 #include "linattn.cuh"
@@ -1407,11 +1408,13 @@ __device__ __forceinline__ float column_sums(float (&x)[16]) {
 // the split ones.  Bound by the bytes and the chain of products and arithmetic
 // behind them: 320 KB in, 96 KB out a chunk; at B4 H16 T4096, D 128, 171 us,
 // 852 MB at 5.0 TB/s (74% of a plain copy's rate).
-// FEW: P and N of chunks of up to 64 tokens go into their products in two bf16
-// terms, in the tiles' other half: few pairs do not average the rounding out, and
-// heads that share keys may cancel (1 token: dq 1e-2 off with one term).  A kernel
-// of its own, as it costs the long ones 186 us in place of 171 (code and registers).
-template <int DK, int DV, bool FEW>
+// P and N of a chunk of up to 64 tokens go into their products in two bf16 terms,
+// in the tiles' other half: few pairs do not average the rounding out, and heads
+// that share keys may cancel (1 token: dq 6e-2 off with one term).  The chunk
+// alone decides, so that a sequence's precision does not depend on the call that it
+// is in.  Both ways of the pairs' loop are compiled apart: as conditions in one
+// loop they cost the long chunks 186 us in place of 171 (registers).
+template <int DK, int DV>
 __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_constant__ GradMaps m, TcArgs p) {
     using L = GradSmem;
     using T = __nv_bfloat16;
@@ -1626,7 +1629,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
                 fence_proxy_async_smem();
                 if (ok) mbar_arrive(&bars[L::TAIL]);
             }
-            const bool half = FEW && c.len <= 64;
+            const bool half = c.len <= 64;
             float rowa = 0.f, cola[2] = {0.f, 0.f}, dot = 0.f, xt = 0.f, yt = 0.f;
             wait(L::GT);
             wait(L::CT);
@@ -1636,71 +1639,75 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel_tc(const __grid_c
             // fourth is this warp's).  The decays as in
             // prompt_kernel, with c_t - c_s from the pairs.
             const float ht = hi[t], lt = lo[t];
+            auto pairs = [&](auto two) __attribute__((always_inline)) {
+                constexpr bool TWO = decltype(two)::value;
 #pragma unroll 1
-            for (int k = 0; k < 2 && ok; ++k) {
-                const int sb = 16 * (4 * k + four), diag = 32 * (warp & 3);
-                uint32_t u[16];
-                if (half && k) break;  // the second terms are there
-                if (sb >= diag + 32) {  // past the diagonal for every row of the warp
+                for (int k = 0; k < (TWO ? 1 : 2) && ok; ++k) {
+                    const int sb = 16 * (4 * k + four), diag = 32 * (warp & 3);
+                    uint32_t u[16];
+                    if (sb >= diag + 32) {  // past the diagonal for every row of the warp
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) u[j] = 0u;
-                    tmem_st16(lanes + TM_A + sb, u);
-                    if (half) tmem_st16(lanes + TM_A + 64 + sb, u);
-                    continue;
-                }
-                uint32_t w[16];
-                float a[16];
-                tmem_ld16(lanes + TM_A + sb, u);
-                tmem_ld16(lanes + TM_B + sb, w);
-                const int r = sb | 31;
-                const float rf = p.a.scale * expf(((ht - hi[r]) + (lt - lo[r])));
-                tmem_wait_ld();
-                if (sb < diag) {
+                        for (int j = 0; j < 16; ++j) u[j] = 0u;
+                        tmem_st16(lanes + TM_A + sb, u);
+                        if constexpr (TWO) tmem_st16(lanes + TM_A + 64 + sb, u);
+                        continue;
+                    }
+                    uint32_t w[16];
+                    float a[16];
+                    tmem_ld16(lanes + TM_A + sb, u);
+                    tmem_ld16(lanes + TM_B + sb, w);
+                    const int r = sb | 31;
+                    const float rf = p.a.scale * expf(((ht - hi[r]) + (lt - lo[r])));
+                    tmem_wait_ld();
+                    if (sb < diag) {
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        const float4 f4 = *reinterpret_cast<const float4 *>(cf + sb + j);
-                        const float f[4] = {rf * f4.x, rf * f4.y, rf * f4.z, rf * f4.w};
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 f4 = *reinterpret_cast<const float4 *>(cf + sb + j);
+                            const float f[4] = {rf * f4.x, rf * f4.y, rf * f4.z, rf * f4.w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float qk = __uint_as_float(u[j + e]), nn = __uint_as_float(w[j + e]) * f[e];
-                            a[j + e] = qk * nn;
-                            u[j + e] = __float_as_uint(qk * f[e]);
-                            w[j + e] = __float_as_uint(nn);
+                            for (int e = 0; e < 4; ++e) {
+                                const float qk = __uint_as_float(u[j + e]), nn = __uint_as_float(w[j + e]) * f[e];
+                                a[j + e] = qk * nn;
+                                u[j + e] = __float_as_uint(qk * f[e]);
+                                w[j + e] = __float_as_uint(nn);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const int s = sb + j;
+                            const float f = s <= t ? p.a.scale * expf(((ht - hi[s]) + (lt - lo[s]))) : 0.f;
+                            const float qk = __uint_as_float(u[j]), nn = __uint_as_float(w[j]) * f;
+                            a[j] = s < t ? qk * nn : 0.f;
+                            u[j] = __float_as_uint(qk * f);
+                            w[j] = __float_as_uint(nn);
                         }
                     }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int s = sb + j;
-                        const float f = s <= t ? p.a.scale * expf(((ht - hi[s]) + (lt - lo[s]))) : 0.f;
-                        const float qk = __uint_as_float(u[j]), nn = __uint_as_float(w[j]) * f;
-                        a[j] = s < t ? qk * nn : 0.f;
-                        u[j] = __float_as_uint(qk * f);
-                        w[j] = __float_as_uint(nn);
-                    }
-                }
-                uint32_t pn[16];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    pn[j] = pack_bf16(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
-                    pn[j + 8] = pack_bf16(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
-                    rowa += a[2 * j] + a[2 * j + 1];
-                }
-                tmem_st16(lanes + TM_A + sb, pn);  // until their tiles' places are free
-                if (half) {
+                    uint32_t pn[16];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        pn[j] = pack_bf16(__uint_as_float(u[2 * j]) - __uint_as_float(pn[j] << 16),
-                                          __uint_as_float(u[2 * j + 1]) - __uint_as_float(pn[j] & 0xffff0000u));
-                        pn[j + 8] = pack_bf16(__uint_as_float(w[2 * j]) - __uint_as_float(pn[j + 8] << 16),
-                                              __uint_as_float(w[2 * j + 1]) - __uint_as_float(pn[j + 8] & 0xffff0000u));
+                        pn[j] = pack_bf16(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+                        pn[j + 8] = pack_bf16(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+                        rowa += a[2 * j] + a[2 * j + 1];
                     }
-                    tmem_st16(lanes + TM_A + 64 + sb, pn);
-                }
-                const float sum = column_sums(a);
+                    tmem_st16(lanes + TM_A + sb, pn);  // until their tiles' places are free
+                    if constexpr (TWO) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) cola[j] = j == k ? sum : cola[j];
-            }
+                        for (int j = 0; j < 8; ++j) {
+                            pn[j] = pack_bf16(__uint_as_float(u[2 * j]) - __uint_as_float(pn[j] << 16),
+                                              __uint_as_float(u[2 * j + 1]) - __uint_as_float(pn[j] & 0xffff0000u));
+                            pn[j + 8] = pack_bf16(__uint_as_float(w[2 * j]) - __uint_as_float(pn[j + 8] << 16),
+                                                  __uint_as_float(w[2 * j + 1]) - __uint_as_float(pn[j + 8] & 0xffff0000u));
+                        }
+                        tmem_st16(lanes + TM_A + 64 + sb, pn);
+                    }
+                    const float sum = column_sums(a);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) cola[j] = j == k ? sum : cola[j];
+                }
+            };
+            if (half) pairs(std::true_type{});
+            else pairs(std::false_type{});
             // the thread's part of S for <R, S>, until R is there
             constexpr int NV = DK * DV / 8 / kGradWork;  // 16-byte words of a term a thread
             auto words = [&](int e, float (&x)[8], uint32_t t0, uint32_t t1, uint32_t t2) {  // t0's are the largest
@@ -2149,7 +2156,7 @@ int run_bwd(const TcArgs &p, cudaStream_t stream) {
         return GDN_ERR_CUDA;
     constexpr uint32_t bytes = StateSmem<DK>::BYTES;
     if (!smem_limit<state_kernel<DK, DV, false>>(bytes) || !smem_limit<state_kernel<DK, DV, true>>(bytes) ||
-        !smem_limit<grad_kernel_tc<DK, DV, false>>(GradSmem::BYTES) || !smem_limit<grad_kernel_tc<DK, DV, true>>(GradSmem::BYTES))
+        !smem_limit<grad_kernel_tc<DK, DV>>(GradSmem::BYTES))
         return GDN_ERR_CUDA;
     int st = GDN_OK;
     dim3 grid(2 * DV / 64, a.H, a.n_seq);
@@ -2163,9 +2170,7 @@ int run_bwd(const TcArgs &p, cudaStream_t stream) {
     const long long items = (long long)p.v.n_chunks * a.H;
     const int sms = device_sm_count();
     const unsigned ctas = (unsigned)(items < sms ? items : sms);
-    // sequences of up to 64 tokens, or packed ones of no more on average
-    if (a.T <= 64LL * (a.cu ? a.n_seq : 1)) grad_kernel_tc<DK, DV, true><<<ctas, kGradThreads, GradSmem::BYTES, stream>>>(m, p);
-    else grad_kernel_tc<DK, DV, false><<<ctas, kGradThreads, GradSmem::BYTES, stream>>>(m, p);
+    grad_kernel_tc<DK, DV><<<ctas, kGradThreads, GradSmem::BYTES, stream>>>(m, p);
     return launched();
 }
 
