@@ -794,7 +794,8 @@ def linattn_chunk_fwd(q, k, v, g, initial_state=None, output_final_state=False, 
     offsets of sequences packed into one row (a token-major [T,H,D] tensor x
     goes in as x.unsqueeze(0).transpose(1, 2)).  initial_state
     [sequences,H,Dk,Dv] fp32.  Returns (o, final_state or None); o has v's
-    strides unless it is given."""
+    strides unless it is given.  In bf16, o's last bit may depend on whether a
+    final state is asked for."""
     if o is None and workspace is None and stream is None:
         r = (_front or _quick()).fwd(q, k, v, g, initial_state, output_final_state, cu_seqlens, scale, simt)
         if r is not NotImplemented:
@@ -827,7 +828,11 @@ def linattn_chunk_bwd(q, k, v, g, dout, initial_state=None, dfinal_state=None, c
     """Backward of linattn_chunk_fwd.  dout [B,H,T,Dv], dfinal_state
     [sequences,H,Dk,Dv] fp32.  Returns (dq, dk, dv, dg, dinitial_state or
     None): the first three in the tensors' type, dg fp32 in g's shape (its sum
-    over batch and tokens for g [H])."""
+    over batch and tokens for g [H]).  Gradients are allocated with their
+    tensors' strides: those of slices of one projection take its memory each.
+    The workspace, if not given, is 12 bytes (fp32: 16) for each Dk*Dv of every
+    128 tokens and value head, and 8*Dk for each token and value head of shared
+    heads."""
     if workspace is None and stream is None:
         r = (_front or _quick()).bwd(q, k, v, g, dout, initial_state, dfinal_state, cu_seqlens, scale, simt)
         if r is not NotImplemented:

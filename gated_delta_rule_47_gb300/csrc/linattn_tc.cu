@@ -1408,6 +1408,10 @@ __device__ __forceinline__ float column_sums(float (&x)[16]) {
 // the split ones.  Bound by the bytes and the chain of products and arithmetic
 // behind them: 320 KB in, 96 KB out a chunk; at B4 H16 T4096, D 128, 171 us,
 // 852 MB at 5.0 TB/s (74% of a plain copy's rate).
+// dv's part through R takes R's first term alone (2^-9, as dv's own rounding); so
+// do P and N, which costs dq and dk 2^-9 of each value head's part: where heads of
+// one key cancel to 2^-4, up to 6e-2 of what is left of a chunk of more than 64
+// tokens.
 // P and N of a chunk of up to 64 tokens go into their products in two bf16 terms,
 // in the tiles' other half: few pairs do not average the rounding out, and heads
 // that share keys may cancel (1 token: dq 6e-2 off with one term).  The chunk
@@ -2012,9 +2016,11 @@ bool smem_limit(uint32_t bytes) {
 
 // Chunks of a piece where cutting may pay (0: it does not): of the rows, whose
 // length is known, or, packed, if one sequence had all of the tokens.  What it
-// must save is more there, as lengths that need no cut lose by the plan (32760
-// tokens of 32 heads, states out: one sequence 562 -> 466 us, but eight equal
-// ones 291 -> 313; of 16 heads: 560 -> 295, so those are cut and these are not).
+// must save is more there, as lengths that need no cut lose by the plan and the
+// costs are up to a fifth off for ragged ones (32760 tokens of 32 heads, states
+// out: one sequence 517 -> 472 us, but eight equal ones 283 -> 318 and eight of
+// 21001 tokens and fewer 357 -> 413; of 16 heads: one 560 -> 290, so those are cut
+// and these are not).
 int plan_len(const LinAttnArgs &a) {
     const int slots = a.H * (a.Dv / 64), seqs = a.cu ? 1 : a.B;
     const int n = (int)(((long long)a.T + kC - 1) / kC);

@@ -517,6 +517,14 @@ int cam_prep_bwd(const void *q_raw, const void *k_raw, const float *q_norm_w, co
  *           (packed: 1 where cu_seqlens is given), 16-byte aligned; no
  *           initialisation needed, contents not meaningful afterwards.
  * T = 0 or B*H = 0 is valid and passes the state on.
+ * Sums and states are fp32.  The tensor-core path (bf16 without
+ * GDN_PATH_SIMT) rounds the weighted q.k and the state to bf16 where they enter
+ * o, each about as much as o's own rounding (bf16 outputs 2.6e-3 off, their
+ * rounding alone 1.7e-3), and takes k's weighted values to 2^-24 where a final
+ * state is asked for, to 2^-16 otherwise: o may differ in its last bit between
+ * the two.  An infinity or NaN of a token reaches its sequence's outputs from
+ * the start of its chunk (128 tokens; 64 on the CUDA cores) on, and no other
+ * sequence's.
  */
 size_t linattn_chunk_fwd_workspace_bytes(int B, int H, int Hk, int T, int Dk, int Dv, int n_seq, int packed,
                                          unsigned flags, int dtype);
@@ -542,6 +550,15 @@ int linattn_chunk_fwd(const void *q, const void *k, const void *v, const float *
  *           apart, as o's in linattn_chunk_fwd
  * Tokens of no sequence get zeros.  Every sum has a fixed order: equal calls
  * give equal bits.
+ * On the tensor cores dg and dinitial_state are fp32 throughout (terms to
+ * 2^-24); dq, dk and dv are sums with the pairs' terms rounded to bf16 by value
+ * head, in chunks of up to 64 tokens kept to 2^-16.  Where value heads of one
+ * key cancel in dq or dk, what is left of a longer chunk's carries 2^-9 of what
+ * they were.
+ * The workspace holds the states of all chunks: Dk*Dv elements for each chunk
+ * and value head, 12 bytes each in chunks of 128 tokens on the tensor cores, 8
+ * in chunks of 64 on the CUDA cores, and 8 bytes for each of B*H*T*Dk where
+ * heads are shared.
  */
 size_t linattn_chunk_bwd_workspace_bytes(int B, int H, int Hk, int T, int Dk, int Dv, int n_seq, int packed,
                                          unsigned flags, int dtype);
