@@ -34,6 +34,11 @@ GDN_QK_L2NORM = 1
 GDN_PATH_SIMT = 2
 GDN_CAM_REVERSE = 4
 GDN_G_PER_HEAD = 8
+GDN_DT_SOFTPLUS = 16
+GDN_SILU = 32
+GDN_GATE_FIRST = 64
+GDN_GATE_SIGMOID = 128
+GDN_W_SHARED = 256
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARG", 2: "GDN_ERR_UNSUPPORTED", 3: "GDN_ERR_MISALIGNED",
           4: "GDN_ERR_WORKSPACE", 5: "GDN_ERR_CUDA", 6: "GDN_ERR_TIMEOUT"}
 
@@ -48,7 +53,11 @@ EXPORTS = ("gdn_status_string", "gdn_version", "gdn_chunk_fwd_workspace_bytes", 
            "linattn_chunk_fwd_workspace_bytes", "linattn_chunk_fwd", "linattn_chunk_bwd_workspace_bytes",
            "linattn_chunk_bwd", "linattn_step", "gdn_step", "rms_norm_fwd", "rms_norm_bwd_workspace_bytes",
            "rms_norm_bwd", "state_pool_copy", "state_pool_fork_workspace_bytes", "state_pool_fork", "state_pool_free",
-           "state_pool_compact_workspace_bytes", "state_pool_compact")
+           "state_pool_compact_workspace_bytes", "state_pool_compact",
+           "causal_conv_fwd", "causal_conv_bwd_workspace_bytes", "causal_conv_bwd", "causal_conv_step",
+           "ssm_scan_fwd_workspace_bytes", "ssm_scan_fwd", "ssm_scan_bwd_workspace_bytes", "ssm_scan_bwd", "ssm_step",
+           "gated_norm_fwd", "gated_norm_bwd_workspace_bytes", "gated_norm_bwd", "block_norm_fwd",
+           "block_norm_bwd_workspace_bytes", "block_norm_bwd")
 
 _lock = threading.Lock()
 _lib = None
@@ -134,8 +143,28 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.state_pool_free.argtypes = [vp, i, vp, i, vp]
         lib.state_pool_compact_workspace_bytes.argtypes = [i]
         lib.state_pool_compact.argtypes = [vp, i, i, ll, vp, vp, vp, vp, sz, vp]
+        lib.causal_conv_fwd.argtypes = [vp] * 8 + [i] * 5 + [u, i, vp]
+        lib.causal_conv_bwd_workspace_bytes.argtypes = [i] * 4
+        lib.causal_conv_bwd.argtypes = [vp] * 12 + [i] * 5 + [u, i, vp, sz, vp]
+        lib.causal_conv_step.argtypes = [vp] * 7 + [ll] + [i] * 4 + [u, i, vp]
+        lib.ssm_scan_fwd_workspace_bytes.argtypes = [i] * 5
+        lib.ssm_scan_fwd.argtypes = [vp] * 13 + [i] * 5 + [u, i, vp, sz, vp]
+        lib.ssm_scan_bwd_workspace_bytes.argtypes = [i] * 5
+        lib.ssm_scan_bwd.argtypes = [vp] * 22 + [i] * 5 + [u, i, vp, sz, vp]
+        lib.ssm_step.argtypes = [vp] * 13 + [i] * 4 + [u, i, vp]
+        lib.gated_norm_fwd.argtypes = [vp] * 5 + [i] * 4 + [f, u, i, vp]
+        lib.gated_norm_bwd_workspace_bytes.argtypes = [i] * 4 + [u]
+        lib.gated_norm_bwd.argtypes = [vp] * 8 + [i] * 4 + [f, u, i, vp, sz, vp]
+        lib.block_norm_fwd.argtypes = [vp] * 7 + [ll, i, i, f, i, vp]
+        lib.block_norm_bwd_workspace_bytes.argtypes = [ll, i, i]
+        lib.block_norm_bwd.argtypes = [vp] * 12 + [ll, i, i, f, i, vp, sz, vp]
+        for name in ("causal_conv_fwd", "causal_conv_bwd", "causal_conv_step", "ssm_scan_fwd", "ssm_scan_bwd", "ssm_step",
+                     "gated_norm_fwd", "gated_norm_bwd", "block_norm_fwd", "block_norm_bwd"):
+            getattr(lib, name).restype = i
         for name in ("rms_norm_bwd_workspace_bytes", "state_pool_fork_workspace_bytes",
-                     "state_pool_compact_workspace_bytes"):
+                     "state_pool_compact_workspace_bytes", "causal_conv_bwd_workspace_bytes",
+                     "ssm_scan_fwd_workspace_bytes", "ssm_scan_bwd_workspace_bytes", "gated_norm_bwd_workspace_bytes",
+                     "block_norm_bwd_workspace_bytes"):
             getattr(lib, name).restype = sz
         for name in ("linattn_chunk_fwd", "linattn_chunk_bwd", "linattn_step", "gdn_step", "rms_norm_fwd",
                      "rms_norm_bwd", "state_pool_copy", "state_pool_fork", "state_pool_free", "state_pool_compact"):
@@ -162,7 +191,11 @@ def _load_front(lib):
     names = ("linattn_chunk_fwd_workspace_bytes", "linattn_chunk_fwd", "linattn_chunk_bwd_workspace_bytes",
              "linattn_chunk_bwd", "linattn_step", "gdn_step", "rms_norm_fwd", "rms_norm_bwd_workspace_bytes",
              "rms_norm_bwd", "state_pool_fork_workspace_bytes", "state_pool_fork",
-             "state_pool_compact_workspace_bytes", "state_pool_compact")
+             "state_pool_compact_workspace_bytes", "state_pool_compact", "causal_conv_fwd",
+             "causal_conv_bwd_workspace_bytes", "causal_conv_bwd", "causal_conv_step", "ssm_scan_fwd_workspace_bytes",
+             "ssm_scan_fwd", "ssm_scan_bwd_workspace_bytes", "ssm_scan_bwd", "ssm_step", "gated_norm_fwd",
+             "gated_norm_bwd_workspace_bytes", "gated_norm_bwd", "block_norm_fwd", "block_norm_bwd_workspace_bytes",
+             "block_norm_bwd")
     stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent without CUDA, where nothing asks for it
     front.init(tuple(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in names), stream, _raise)
     return front
@@ -1073,6 +1106,460 @@ def state_pool_compact(pool, live, stream=None):
     if st:
         _raise("state_pool_compact", st)
     return remap, n_live
+
+
+# ------------------------------------------------- next to a mixer
+def _same_device(like, *tensors):
+    """All tensors of a call lie on one device."""
+    for t in tensors:
+        if t is not None and t.device != like.device:
+            raise ValueError(f"tensors on {like.device} and {t.device}: a call's tensors lie on one device")
+
+
+@contextlib.contextmanager
+def _device(t, stream):
+    """The device of a call's tensors is the current one while it launches, and its
+    allocations belong to the stream that it runs on."""
+    with torch.cuda.device(t.device), _on(stream):
+        yield
+
+
+def _pitches(*tensors):
+    """A strides array: those of every dimension but the last; a dimension of one
+    element has none that matters."""
+    out = []
+    for t in tensors:
+        out += [s if n > 1 else 0 for n, s in zip(t.shape[:-1], t.stride())]
+    return (ctypes.c_longlong * len(out))(*out)
+
+
+def _rows_of(x, name, cu_seqlens, C=None):
+    """(B, T, C, sequences) of [B,T,C] rows."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise TypeError(f"{name} must be a [B,T,channels] CUDA tensor")
+    B, T, C = x.shape
+    n_seq = B
+    if cu_seqlens is not None:
+        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must hold at least two offsets")
+        _dense(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32)
+        if B != 1:
+            raise ValueError("packed sequences (cu_seqlens) lie in one row: B must be 1")
+        n_seq = cu_seqlens.numel() - 1
+    return B, T, C, n_seq
+
+
+def _maybe(t, name, shape, dtype):
+    if t is not None:
+        _dense(t, name, shape, dtype)
+
+
+def _written(t, name, shape, dtype):
+    """As _strided, for an output of the caller's: no two elements in one place."""
+    _strided(t, name, shape, dtype)
+    if _overlaps(t):
+        raise ValueError(f"{name}'s elements share memory")
+
+
+def _apart(a, b, names):
+    """An output that a call reads the input of after it has begun to write."""
+    if a is not None and b is not None and a.numel() and b.numel():
+        span = lambda t: t.data_ptr() + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()  # noqa: E731
+        if a.data_ptr() < span(b) and b.data_ptr() < span(a):
+            raise ValueError(f"{names} share memory")
+
+
+def _taps(weight, bias, C):
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise TypeError("weight must be a [channels,W] CUDA tensor")
+    W = weight.shape[1]
+    _dense(weight, "weight", (C, W), torch.float32)
+    _maybe(bias, "bias", (C,), torch.float32)
+    return W
+
+
+def causal_conv_fwd(x, weight, bias=None, initial_window=None, output_final_window=False, cu_seqlens=None, silu=True,
+                    y=None, stream=None):
+    """The short causal convolution of each channel, then SiLU (or not).  x [B,T,C]
+    (bf16 or fp32, channels contiguous, C a multiple of 8 or 4); weight [C,W] fp32,
+    W 2 to 4, the last tap the token's own; bias [C] fp32.  initial_window
+    [sequences,W-1,C], the inputs before each sequence; cu_seqlens as in
+    linattn_chunk_fwd.  Returns (y, final_window or None): the last W-1 inputs of
+    each sequence, counted over its window and its tokens."""
+    if y is None and stream is None:
+        r = (_front or _quick()).conv(x, weight, bias, initial_window, output_final_window, cu_seqlens, silu)
+        if r is not NotImplemented:
+            return r
+    B, T, C, n_seq = _rows_of(x, "x", cu_seqlens)
+    code, W = _dtype_code(x), _taps(weight, bias, C)
+    _strided(x, "x", (B, T, C), x.dtype)
+    _maybe(initial_window, "initial_window", (n_seq, W - 1, C), x.dtype)
+    _same_device(x, weight, bias, initial_window, cu_seqlens, y)
+    with _device(x, stream):
+        if y is None:
+            y = torch.empty(B, T, C, dtype=x.dtype, device=x.device)
+        else:
+            _written(y, "y", (B, T, C), x.dtype)
+            _apart(y, x, "x and y")
+        win = torch.empty(n_seq, W - 1, C, dtype=x.dtype, device=x.device) if output_final_window else None
+        st = load().causal_conv_fwd(x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(initial_window), y.data_ptr(),
+                                    _addr(win), _addr(cu_seqlens), _pitches(x, y), n_seq, B, T, C, W,
+                                    GDN_SILU if silu else 0, code, _at(stream, x))
+    if st:
+        _raise("causal_conv_fwd", st)
+    return y, win
+
+
+def causal_conv_bwd(x, weight, dy, bias=None, initial_window=None, dfinal_window=None, cu_seqlens=None, silu=True,
+                    workspace=None, stream=None):
+    """Backward of causal_conv_fwd.  dy [B,T,C], dfinal_window [sequences,W-1,C] in
+    x's type.  Returns (dx, dweight [C,W] fp32, dbias [C] fp32 or None without a
+    bias, dinitial_window or None without an initial window)."""
+    if workspace is None and stream is None:
+        r = (_front or _quick()).conv_back(x, weight, dy, bias, initial_window, dfinal_window, cu_seqlens, silu)
+        if r is not NotImplemented:
+            return r
+    B, T, C, n_seq = _rows_of(x, "x", cu_seqlens)
+    code, W = _dtype_code(x), _taps(weight, bias, C)
+    _strided(x, "x", (B, T, C), x.dtype)
+    _strided(dy, "dy", (B, T, C), x.dtype)
+    _maybe(initial_window, "initial_window", (n_seq, W - 1, C), x.dtype)
+    _maybe(dfinal_window, "dfinal_window", (n_seq, W - 1, C), x.dtype)
+    _same_device(x, weight, dy, bias, initial_window, dfinal_window, cu_seqlens, workspace)
+    need = _bytes("causal_conv_bwd_workspace_bytes", B, T, C, W)
+    with _device(x, stream):
+        dx = torch.empty(B, T, C, dtype=x.dtype, device=x.device)
+        dw = torch.empty(C, W, dtype=torch.float32, device=x.device)
+        db = torch.empty(C, dtype=torch.float32, device=x.device) if bias is not None else None
+        dwin = torch.empty_like(initial_window) if initial_window is not None else None
+        if workspace is None:
+            workspace = _scratch(need, x.device)
+        st = load().causal_conv_bwd(x.data_ptr(), weight.data_ptr(), _addr(bias), dy.data_ptr(), _addr(initial_window),
+                                    _addr(dfinal_window), dx.data_ptr(), dw.data_ptr(), _addr(db), _addr(dwin),
+                                    _addr(cu_seqlens), _pitches(x, dy), n_seq, B, T, C, W, GDN_SILU if silu else 0, code,
+                                    _addr(workspace), _room(workspace), _at(stream, x))
+    if st:
+        _raise("causal_conv_bwd", st)
+    return dx, dw, db, dwin
+
+
+def _row(t, name, shape, dtype):
+    """A [B,n] tensor whose rows may lie apart."""
+    _strided(t, name, shape, dtype)
+    return t.stride(0) if shape[0] > 1 else 0
+
+
+def _pages(pool, name, shape, dtype, slots, B):
+    """Checks a pool [slots,...] and the rows' slots; how many pages it has."""
+    if not isinstance(pool, torch.Tensor) or pool.dim() != 1 + len(shape):
+        raise TypeError(f"{name} must be a [slots,{','.join(map(str, shape))}] CUDA tensor")
+    n = pool.shape[0]
+    _dense(pool, name, (n, *shape), dtype)
+    if slots is not None:
+        _dense(slots, "slots", (B,), torch.int32)
+    elif B > n:
+        raise ValueError(f"{B} rows but {n} pages")
+    return n
+
+
+def causal_conv_step(x, weight, window, bias=None, slots=None, window_out=None, silu=True, y=None, stream=None):
+    """One token of causal_conv_fwd for each row of x [B,C] (rows may lie apart)
+    against a pool of windows [slots,W-1,C] in x's type, updated in place unless
+    window_out is given; slots int32 [B]: each row's page, -1 for an idle row (y =
+    0).  Returns y [B,C]."""
+    if y is None and stream is None:
+        r = (_front or _quick()).conv_step(x, weight, window, bias, slots, window_out, silu)
+        if r is not NotImplemented:
+            return r
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise TypeError("x must be a [B,channels] CUDA tensor")
+    B, C = x.shape
+    code, W = _dtype_code(x), _taps(weight, bias, C)
+    step = _row(x, "x", (B, C), x.dtype)
+    n = _pages(window, "window", (W - 1, C), x.dtype, slots, B)
+    if window_out is None:
+        window_out = window
+    elif window_out is not window:
+        _dense(window_out, "window_out", window.shape, x.dtype)
+    _same_device(x, weight, window, bias, slots, window_out, y)
+    with _device(x, stream):
+        if y is None:
+            y = torch.empty(B, C, dtype=x.dtype, device=x.device)
+        else:
+            _dense(y, "y", (B, C), x.dtype)
+            _apart(y, x, "x and y")
+        st = load().causal_conv_step(x.data_ptr(), weight.data_ptr(), _addr(bias), window.data_ptr(), window_out.data_ptr(),
+                                     _addr(slots), y.data_ptr(), step, B, C, W, n, GDN_SILU if silu else 0, code,
+                                     _at(stream, x))
+    if st:
+        _raise("causal_conv_step", st)
+    return y
+
+
+def _scan_sizes(x, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens):
+    rows, T, Di, n_seq = _rows_of(x, "x", cu_seqlens)
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise TypeError("A must be a [channels,N] CUDA tensor")
+    code, N = _dtype_code(x), A.shape[1]
+    _dense(A, "A", (Di, N), torch.float32)
+    for t, name, n in ((x, "x", Di), (dt, "dt", Di), (B, "B", N), (C, "C", N), (z, "z", Di)):
+        if t is not None or name != "z":
+            _strided(t, name, (rows, T, n), x.dtype)
+    _maybe(D, "D", (Di,), torch.float32)
+    _maybe(dt_bias, "dt_bias", (Di,), torch.float32)
+    _maybe(initial_state, "initial_state", (n_seq, Di, N), torch.float32)
+    _same_device(x, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens)
+    return rows, T, Di, N, n_seq, code
+
+
+def ssm_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, initial_state=None, output_final_state=False,
+                 cu_seqlens=None, softplus=True, y=None, workspace=None, stream=None):
+    """The selective state space scan over prompts: with steps s = softplus(dt +
+    dt_bias) (or their sum alone), h = exp(s A) h + s x B, y = (C.h + D x) silu(z).
+    x, dt, z [B,T,Di], B, C [B,T,N] (all bf16 or all fp32, the last dimension
+    contiguous, Di a multiple of 8 or 4, N 8, 16 or 32); A [Di,N], D, dt_bias [Di]
+    fp32; initial_state [sequences,Di,N] fp32; cu_seqlens as in linattn_chunk_fwd.
+    Returns (y, final_state or None)."""
+    if y is None and workspace is None and stream is None:
+        r = (_front or _quick()).scan(x, dt, A, B, C, D, z, dt_bias, initial_state, output_final_state, cu_seqlens, softplus)
+        if r is not NotImplemented:
+            return r
+    rows, T, Di, N, n_seq, code = _scan_sizes(x, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens)
+    _same_device(x, y, workspace)
+    need = _bytes("ssm_scan_fwd_workspace_bytes", rows, T, Di, N, code)
+    with _device(x, stream):
+        if y is None:
+            y = torch.empty(rows, T, Di, dtype=x.dtype, device=x.device)
+        else:
+            _written(y, "y", (rows, T, Di), x.dtype)
+            for t, name in ((x, "x"), (dt, "dt"), (B, "B"), (C, "C"), (z, "z")):
+                _apart(y, t, f"{name} and y")
+        sf = torch.empty(n_seq, Di, N, dtype=torch.float32, device=x.device) if output_final_state else None
+        if workspace is None:
+            workspace = _scratch(need, x.device)
+        st = load().ssm_scan_fwd(x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _addr(D), _addr(z),
+                                 _addr(dt_bias), _addr(initial_state), y.data_ptr(), _addr(sf), _addr(cu_seqlens),
+                                 _pitches(x, dt, B, C, x if z is None else z, y), n_seq, rows, T, Di, N,
+                                 GDN_DT_SOFTPLUS if softplus else 0, code, _addr(workspace), _room(workspace),
+                                 _at(stream, x))
+    if st:
+        _raise("ssm_scan_fwd", st)
+    return y, sf
+
+
+def ssm_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, initial_state=None, dfinal_state=None,
+                 cu_seqlens=None, softplus=True, workspace=None, stream=None):
+    """Backward of ssm_scan_fwd.  dy [B,T,Di] in x's type, dfinal_state
+    [sequences,Di,N] fp32.  Returns (dx, ddt, dA, dB, dC, dD, dz, ddt_bias,
+    dinitial_state), contiguous: those of tensors in their type, dA, dD, ddt_bias and
+    dinitial_state in fp32; None for inputs that are not given.  The workspace, if
+    not given, takes Di N / 2 bytes a token and more."""
+    if workspace is None and stream is None:
+        r = (_front or _quick()).scan_back(x, dt, A, B, C, dy, D, z, dt_bias, initial_state, dfinal_state, cu_seqlens, softplus)
+        if r is not NotImplemented:
+            return r
+    rows, T, Di, N, n_seq, code = _scan_sizes(x, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens)
+    _strided(dy, "dy", (rows, T, Di), x.dtype)
+    _maybe(dfinal_state, "dfinal_state", (n_seq, Di, N), torch.float32)
+    _same_device(x, dy, dfinal_state, workspace)
+    need = _bytes("ssm_scan_bwd_workspace_bytes", rows, T, Di, N, code)
+    with _device(x, stream):
+        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=x.device)  # noqa: E731
+        dx, ddt = new((rows, T, Di), x.dtype), new((rows, T, Di), x.dtype)
+        dB, dC = new((rows, T, N), x.dtype), new((rows, T, N), x.dtype)
+        dA = new((Di, N), torch.float32)
+        dD = new((Di,), torch.float32) if D is not None else None
+        dz = new((rows, T, Di), x.dtype) if z is not None else None
+        dbias = new((Di,), torch.float32) if dt_bias is not None else None
+        ds0 = torch.empty_like(initial_state) if initial_state is not None else None
+        if workspace is None:
+            workspace = _scratch(need, x.device)
+        st = load().ssm_scan_bwd(x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _addr(D), _addr(z),
+                                 _addr(dt_bias), _addr(initial_state), dy.data_ptr(), _addr(dfinal_state), dx.data_ptr(),
+                                 ddt.data_ptr(), dA.data_ptr(), dB.data_ptr(), dC.data_ptr(), _addr(dD), _addr(dz),
+                                 _addr(dbias), _addr(ds0), _addr(cu_seqlens),
+                                 _pitches(x, dt, B, C, x if z is None else z, dy), n_seq, rows, T, Di, N,
+                                 GDN_DT_SOFTPLUS if softplus else 0, code, _addr(workspace), _room(workspace),
+                                 _at(stream, x))
+    if st:
+        _raise("ssm_scan_bwd", st)
+    return dx, ddt, dA, dB, dC, dD, dz, dbias, ds0
+
+
+def ssm_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, slots=None, state_out=None, softplus=True, y=None,
+             stream=None):
+    """One token of ssm_scan_fwd for each row: x, dt, z [B,Di], B, C [B,N] (rows may
+    lie apart) against a pool of states [slots,Di,N] fp32, updated in place unless
+    state_out is given; slots int32 [B]: each row's page, -1 for an idle row (y =
+    0).  Returns y [B,Di]."""
+    if y is None and stream is None:
+        r = (_front or _quick()).scan_step(x, dt, A, B, C, state, D, z, dt_bias, slots, state_out, softplus)
+        if r is not NotImplemented:
+            return r
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise TypeError("x must be a [B,channels] CUDA tensor")
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise TypeError("A must be a [channels,N] CUDA tensor")
+    rows, Di = x.shape
+    code, N, dtype = _dtype_code(x), A.shape[1], x.dtype
+    _dense(A, "A", (Di, N), torch.float32)
+    steps = [_row(t, name, (rows, n), dtype) for t, name, n in
+             ((x, "x", Di), (dt, "dt", Di), (B, "B", N), (C, "C", N), (x if z is None else z, "z", Di))]
+    _maybe(D, "D", (Di,), torch.float32)
+    _maybe(dt_bias, "dt_bias", (Di,), torch.float32)
+    n = _pages(state, "state", (Di, N), torch.float32, slots, rows)
+    if state_out is None:
+        state_out = state
+    elif state_out is not state:
+        _dense(state_out, "state_out", state.shape, torch.float32)
+    _same_device(x, dt, A, B, C, state, D, z, dt_bias, slots, state_out, y)
+    with _device(x, stream):
+        if y is None:
+            y = torch.empty(rows, Di, dtype=dtype, device=x.device)
+        else:
+            _dense(y, "y", (rows, Di), dtype)
+            for t, name in ((x, "x"), (dt, "dt"), (B, "B"), (C, "C"), (z, "z")):
+                _apart(y, t, f"{name} and y")
+        st = load().ssm_step(x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _addr(D), _addr(z),
+                             _addr(dt_bias), state.data_ptr(), state_out.data_ptr(), _addr(slots), y.data_ptr(),
+                             (ctypes.c_longlong * 5)(*steps), rows, Di, N, n, GDN_DT_SOFTPLUS if softplus else 0, code,
+                             _at(stream, x))
+    if st:
+        _raise("ssm_step", st)
+    return y
+
+
+def _gated(x, gate, weight, gate_first, sigmoid):
+    if not isinstance(x, torch.Tensor) or x.dim() != 4:
+        raise TypeError("x must be a [B,T,heads,D] CUDA tensor")
+    code, D = _dtype_code(x), x.shape[3]
+    _strided(x, "x", x.shape, x.dtype)
+    _strided(gate, "gate", x.shape, x.dtype)
+    shared = weight is None or weight.dim() == 1
+    _maybe(weight, "weight", (D,) if shared else (x.shape[2], D), torch.float32)
+    flags = (GDN_GATE_FIRST if gate_first else 0) | (GDN_GATE_SIGMOID if sigmoid else 0) | (GDN_W_SHARED if shared else 0)
+    return code, flags
+
+
+def gated_norm_fwd(x, gate, weight=None, eps=1e-6, gate_first=False, sigmoid=False, y=None, stream=None):
+    """The root-mean-square norm of each head with its gate: weight n(x) act(gate),
+    or weight n(x act(gate)) with gate_first; act is SiLU or the sigmoid.  x, gate
+    [B,T,H,D] (last dimension contiguous; heads first, as the attention gives them,
+    are x.transpose(1, 2)); weight [D] or [H,D] fp32.  Returns y [B,T,H,D],
+    contiguous."""
+    if y is None and stream is None:
+        r = (_front or _quick()).gated(x, gate, weight, eps, gate_first, sigmoid)
+        if r is not NotImplemented:
+            return r
+    code, flags = _gated(x, gate, weight, gate_first, sigmoid)
+    _same_device(x, gate, weight, y)
+    with _device(x, stream):
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        else:
+            _dense(y, "y", x.shape, x.dtype)
+            _apart(y, x, "x and y")
+            _apart(y, gate, "gate and y")
+        st = load().gated_norm_fwd(x.data_ptr(), gate.data_ptr(), _addr(weight), y.data_ptr(), _pitches(x, gate), *x.shape,
+                                   eps, flags, code, _at(stream, x))
+    if st:
+        _raise("gated_norm_fwd", st)
+    return y
+
+
+def gated_norm_bwd(dy, x, gate, weight=None, eps=1e-6, gate_first=False, sigmoid=False, workspace=None, stream=None):
+    """Backward of gated_norm_fwd: (dx, dgate, dweight).  dx has x's strides where
+    those leave every element a place of its own; dweight is fp32 in weight's shape
+    ([D], the sum over the heads, without one)."""
+    if workspace is None and stream is None:
+        r = (_front or _quick()).gated_back(dy, x, gate, weight, eps, gate_first, sigmoid)
+        if r is not NotImplemented:
+            return r
+    code, flags = _gated(x, gate, weight, gate_first, sigmoid)
+    _strided(dy, "dy", x.shape, x.dtype)
+    _same_device(x, dy, gate, weight, workspace)
+    B, T, H, D = x.shape
+    need = _bytes("gated_norm_bwd_workspace_bytes", B, T, H, D, flags)
+    with _device(x, stream):
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if _overlaps(x) else torch.empty_like(x)
+        dgate = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dw = torch.empty((D,) if flags & GDN_W_SHARED else (H, D), dtype=torch.float32, device=x.device)
+        if workspace is None:
+            workspace = _scratch(need, x.device)
+        st = load().gated_norm_bwd(dy.data_ptr(), x.data_ptr(), gate.data_ptr(), _addr(weight), dx.data_ptr(),
+                                   dgate.data_ptr(), dw.data_ptr(), _pitches(x, gate, dy, dx), B, T, H, D, eps, flags,
+                                   code, _addr(workspace), _room(workspace), _at(stream, x))
+    if st:
+        _raise("gated_norm_bwd", st)
+    return dx, dgate, dw
+
+
+def _block(x, post_weight, scale, weight):
+    """(rows, C, groups, code) of [...,C] rows; a scale [C] is one group's."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise TypeError("x must be a [...,C] CUDA tensor")
+    C, code = x.shape[-1], _dtype_code(x)
+    _dense(x, "x", x.shape, x.dtype)
+    _maybe(post_weight, "post_weight", (C,), torch.float32)
+    _maybe(weight, "weight", (C,), torch.float32)
+    rows = x.numel() // C if C else 0
+    groups = 0
+    if scale is not None:
+        if not isinstance(scale, torch.Tensor) or scale.dim() not in (1, 2):
+            raise TypeError("scale must be a [C] or [groups,C] CUDA tensor")
+        groups = 1 if scale.dim() == 1 else scale.shape[0]
+        _dense(scale, "scale", (C,) if scale.dim() == 1 else (groups, C), torch.float32)
+        if groups == 0 or rows % groups:
+            raise ValueError(f"{groups} groups do not divide {rows} rows")
+    return rows, C, groups, code
+
+
+def block_norm_fwd(x, residual, post_weight=None, scale=None, weight=None, eps=1e-6, stream=None):
+    """The norm after a block, its scale, the residual's sum and the norm before the
+    next block: h = residual + scale n(x) post_weight, y = n(h) weight.  x, residual
+    [...,C]; post_weight, weight [C] fp32; scale [C] or [groups,C] fp32, each group's
+    for an equal run of rows.  Returns (y, h)."""
+    if stream is None:
+        r = (_front or _quick()).block(x, residual, post_weight, scale, weight, eps)
+        if r is not NotImplemented:
+            return r
+    rows, C, groups, code = _block(x, post_weight, scale, weight)
+    _dense(residual, "residual", x.shape, x.dtype)
+    _same_device(x, residual, post_weight, scale, weight)
+    with _device(x, stream):
+        y, h = torch.empty_like(x), torch.empty_like(x)
+        st = load().block_norm_fwd(x.data_ptr(), residual.data_ptr(), _addr(post_weight), _addr(scale), _addr(weight),
+                                   y.data_ptr(), h.data_ptr(), rows, C, groups, eps, code, _at(stream, x))
+    if st:
+        _raise("block_norm_fwd", st)
+    return y, h
+
+
+def block_norm_bwd(dy, dh, x, h, post_weight=None, scale=None, weight=None, eps=1e-6, workspace=None, stream=None):
+    """Backward of block_norm_fwd at the h that it returned.  dh (or None): the
+    gradient that reaches h past the norm.  Returns (dx, dresidual, dpost_weight,
+    dscale, dweight): the weights' in fp32, None for those that are not given."""
+    if workspace is None and stream is None:
+        r = (_front or _quick()).block_back(dy, dh, x, h, post_weight, scale, weight, eps)
+        if r is not NotImplemented:
+            return r
+    rows, C, groups, code = _block(x, post_weight, scale, weight)
+    _dense(dy, "dy", x.shape, x.dtype)
+    _dense(h, "h", x.shape, x.dtype)
+    _maybe(dh, "dh", x.shape, x.dtype)
+    _same_device(x, dy, dh, h, post_weight, scale, weight, workspace)
+    need = _bytes("block_norm_bwd_workspace_bytes", rows, C, groups)
+    with _device(x, stream):
+        dx, dres = torch.empty_like(x), torch.empty_like(x)
+        dw1, ds, dw2 = (torch.empty_like(t) if t is not None else None for t in (post_weight, scale, weight))
+        if workspace is None:
+            workspace = _scratch(need, x.device)
+        st = load().block_norm_bwd(dy.data_ptr(), _addr(dh), x.data_ptr(), h.data_ptr(), _addr(post_weight), _addr(scale),
+                                   _addr(weight), dx.data_ptr(), dres.data_ptr(), _addr(dw1), _addr(ds), _addr(dw2), rows, C,
+                                   groups, eps, code, _addr(workspace), _room(workspace), _at(stream, x))
+    if st:
+        _raise("block_norm_bwd", st)
+    return dx, dres, dw1, ds, dw2
 
 
 def device_error(stream=None) -> int:

@@ -1,0 +1,409 @@
+// causal_conv.cu -- the short causal convolution in front of a mixer: each
+// channel of a token sees its own last W inputs, with a bias and SiLU.
+//
+//   z_t = b + sum_j w[j] x_{t-W+1+j};   y = silu(z) or z
+//
+// Inputs before a sequence's start are its window's W-1 rows, or 0; the window
+// it leaves is the last W-1 inputs, counted over window and tokens.  Backward:
+//   dz = dy silu'(z),  dx_t = sum_j w[j] dz_{t+W-1-j},
+//   dw[j] = sum_t dz_t x_{t-W+1+j},  db = sum_t dz_t
+//
+// The bytes bound it: 2 rows a token forwards, 3 backwards.  A thread walks a
+// strip of tokens of its channels with the last inputs (and the unfinished
+// gradients) in registers, so that a row is read once but for the W-1 rows
+// around a strip's ends; strips are as long as one wave of threads allows.
+#include "mixer.cuh"
+
+namespace gdn {
+namespace {
+
+using mx::Run;
+
+// Weights [C,W] of channels c .. c+N-1.
+template <int N, int W>
+__device__ __forceinline__ void load_taps(const float *w, int c, float (&t)[W][N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        if constexpr (W == 4) {
+            const float4 y = __ldg(reinterpret_cast<const float4 *>(w) + c + e);
+            t[0][e] = y.x, t[1][e] = y.y, t[2][e] = y.z, t[3][e] = y.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; ++j) t[j][e] = __ldg(w + (size_t)(c + e) * W + j);
+        }
+    }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void load(const T *p, float (&x)[N]) {
+    Vec<T, N>::unpack(*reinterpret_cast<const typename Vec<T, N>::Raw *>(p), x);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store(T *p, const float (&x)[N]) {
+    *reinterpret_cast<typename Vec<T, N>::Raw *>(p) = Vec<T, N>::pack(x);
+}
+template <int N>
+__device__ __forceinline__ void zero(float (&x)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] = 0.f;
+}
+
+// One thread's place: vector `v` of the channels, tokens t0 .. t1-1 of a row.
+struct Strip {
+    int c, row, t0, t1, index, strips;
+};
+template <int N>
+__device__ __forceinline__ bool strip_of(const ConvArgs &a, int len, int per_row, Strip *s) {
+    const int nv = a.C / N;
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const int strip = (int)(i / nv);
+    s->strips = per_row * a.B;
+    if (strip >= s->strips) return false;
+    s->c = (int)(i - (long long)strip * nv) * N;
+    s->index = strip;
+    s->row = strip / per_row;
+    s->t0 = (strip - s->row * per_row) * len;
+    s->t1 = min(s->t0 + len, a.T);
+    return true;
+}
+
+// The inputs before token t of run r, x[t-1] first.
+template <typename T, int N, int W>
+__device__ __forceinline__ void load_past(const ConvArgs &a, const T *x, const Run &r, int t, int c, float (&past)[W - 1][N]) {
+#pragma unroll
+    for (int k = 1; k < W; ++k) {
+        zero<N>(past[k - 1]);
+        if (r.s < 0) continue;
+        if (t - k >= r.start) load<T, N>(x + (t - k) * a.sx.t, past[k - 1]);
+        else if (a.win) load<T, N>(static_cast<const T *>(a.win) + ((size_t)r.s * (W - 1) + (W - 1 + t - r.start - k)) * a.C + c, past[k - 1]);
+    }
+}
+
+// The windows of sequences without tokens are passed on, sequence s by strip s, s + strips, ..
+template <typename T, int N>
+__device__ __forceinline__ void pass_windows(const ConvArgs &a, const Strip &s, int rows, const void *from, void *to) {
+    if (!a.cu || !to) return;
+    for (int q = s.index; q < a.n_seq; q += s.strips) {
+        if (!mx::no_tokens(a.cu, a.T, q)) continue;
+        for (int r = 0; r < rows; ++r) {
+            const size_t at = ((size_t)q * rows + r) * a.C + s.c;
+            float x[N];
+            zero<N>(x);
+            if (from) load<T, N>(static_cast<const T *>(from) + at, x);
+            store<T, N>(static_cast<T *>(to) + at, x);
+        }
+    }
+}
+
+constexpr int kThreads = 128;
+
+// N channels a thread: 16 bytes.
+template <typename T, int N, int W>
+__global__ void __launch_bounds__(kThreads) conv_kernel(ConvArgs a, int len, int per_row) {
+    using Raw = typename Vec<T, N>::Raw;
+    constexpr int U = 4;  // tokens on their way
+    Strip s;
+    if (!strip_of<N>(a, len, per_row, &s)) return;
+    const bool act = a.flags & GDN_SILU;
+    float w[W][N], bias[N], past[W - 1][N];
+    load_taps<N, W>(a.w, s.c, w);
+#pragma unroll
+    for (int e = 0; e < N; ++e) bias[e] = a.bias ? __ldg(a.bias + s.c + e) : 0.f;
+    const T *x = static_cast<const T *>(a.x) + s.row * a.sx.b + s.c;
+    T *y = static_cast<T *>(a.y) + s.row * a.sy.b + s.c;
+    Raw next[U];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (t + u < s.t1) next[u] = __ldg(reinterpret_cast<const Raw *>(x + (t + u) * a.sx.t));
+    };
+    fetch(s.t0);
+    pass_windows<T, N>(a, s, W - 1, a.win, a.win_out);
+    Run r = mx::run_at(a.cu, a.n_seq, a.T, s.row, s.t0);
+    load_past<T, N, W>(a, x, r, s.t0, s.c, past);
+    for (int t = s.t0; t < s.t1; t += U) {
+        Raw now[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) now[u] = next[u];
+        fetch(t + U);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (t + u >= s.t1) break;
+            if (t + u == r.end) {
+                r = mx::run_at(a.cu, a.n_seq, a.T, s.row, t + u);
+                load_past<T, N, W>(a, x, r, t + u, s.c, past);
+            }
+            float v[N], z[N];
+            Vec<T, N>::unpack(now[u], v);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                z[e] = fmaf(w[W - 1][e], v[e], bias[e]);
+#pragma unroll
+                for (int k = 1; k < W; ++k) z[e] = fmaf(w[W - 1 - k][e], past[k - 1][e], z[e]);
+                if (act) z[e] = mx::silu(z[e]);
+                if (r.s < 0) z[e] = 0.f;
+#pragma unroll
+                for (int k = W - 1; k > 1; --k) past[k - 1][e] = past[k - 2][e];
+                past[0][e] = v[e];
+            }
+            __stcs(reinterpret_cast<Raw *>(y + (t + u) * a.sy.t), Vec<T, N>::pack(z));
+            if (a.win_out && r.s >= 0 && t + u + 1 == r.end)
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k)
+                    store<T, N>(static_cast<T *>(a.win_out) + ((size_t)r.s * (W - 1) + (W - 2 - k)) * a.C + s.c, past[k]);
+        }
+    }
+}
+
+// Backward, N channels a thread: 4, as twice as many would leave too few threads
+// resident beside the taps, their gradients, the inputs and the unfinished dx.
+// A strip goes on for the W-1 tokens behind it, whose dz its last dx need; dw and
+// db count its own.  part: [strips][W+1][C].
+template <typename T, int N, int W>
+__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvArgs a, int len, int per_row, float *part) {
+    using Raw = typename Vec<T, N>::Raw;
+    constexpr int U = 4;
+    Strip s;
+    if (!strip_of<N>(a, len, per_row, &s)) return;
+    const bool act = a.flags & GDN_SILU;
+    float w[W][N], bias[N], past[W - 1][N], dw[W][N], db[N];
+    float open[W - 1][N];  // dx so far of tokens t-1, t-2, ..
+    load_taps<N, W>(a.w, s.c, w);
+    zero<N>(db);
+#pragma unroll
+    for (int e = 0; e < N; ++e) bias[e] = a.bias ? __ldg(a.bias + s.c + e) : 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) zero<N>(dw[j]);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) zero<N>(open[j]);
+    const T *x = static_cast<const T *>(a.x) + s.row * a.sx.b + s.c;
+    const T *dy = static_cast<const T *>(a.dy) + s.row * a.sy.b + s.c;
+    T *dx = static_cast<T *>(a.dx) + (size_t)s.row * a.T * a.C + s.c;
+    const int stop = min(s.t1 + W - 1, a.T);
+    Raw nx[U], nd[U];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (t + u < stop) {
+                nx[u] = __ldg(reinterpret_cast<const Raw *>(x + (t + u) * a.sx.t));
+                nd[u] = __ldg(reinterpret_cast<const Raw *>(dy + (t + u) * a.sy.t));
+            }
+    };
+    fetch(s.t0);
+    pass_windows<T, N>(a, s, W - 1, a.dwin_out, a.dwin);
+    Run r = mx::run_at(a.cu, a.n_seq, a.T, s.row, s.t0);
+    load_past<T, N, W>(a, x, r, s.t0, s.c, past);
+    // dx of token t of run r, or of its window's row
+    auto put = [&](int t, const float (&g)[N]) {
+        if (t >= r.start) {
+            if (t >= s.t0 && t < s.t1) __stcs(reinterpret_cast<Raw *>(dx + (size_t)t * a.C), Vec<T, N>::pack(g));
+        } else if (a.dwin && r.start >= s.t0 && r.start < s.t1) {
+            store<T, N>(static_cast<T *>(a.dwin) + ((size_t)r.s * (W - 1) + (W - 1 + t - r.start)) * a.C + s.c, g);
+        }
+    };
+    // what the run's last W-1 inputs get, where it ends before token t
+    auto close = [&](int t) {
+        if (r.s < 0) return;
+#pragma unroll
+        for (int k = 1; k < W; ++k) {
+            if (a.dwin_out) {
+                float g[N];
+                load<T, N>(static_cast<const T *>(a.dwin_out) + ((size_t)r.s * (W - 1) + (W - 1 - k)) * a.C + s.c, g);
+#pragma unroll
+                for (int e = 0; e < N; ++e) open[k - 1][e] += g[e];
+            }
+            put(t - k, open[k - 1]);
+        }
+    };
+    bool done = false;
+    for (int t = s.t0; t < stop && !done; t += U) {
+        Raw cx[U], cd[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) cx[u] = nx[u], cd[u] = nd[u];
+        fetch(t + U);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = t + u;
+            if (i >= stop || done) break;
+            if (i == r.end) {
+                close(i);
+                if (i >= s.t1) {
+                    done = true;
+                    break;
+                }
+                r = mx::run_at(a.cu, a.n_seq, a.T, s.row, i);
+                load_past<T, N, W>(a, x, r, i, s.c, past);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) zero<N>(open[j]);
+            }
+            if (r.s < 0) {
+                if (i < s.t1) __stcs(reinterpret_cast<Raw *>(dx + (size_t)i * a.C), Raw{});
+                continue;
+            }
+            float v[N], g[N], last[N];
+            Vec<T, N>::unpack(cx[u], v);
+            Vec<T, N>::unpack(cd[u], g);
+            const float count = i < s.t1 ? 1.f : 0.f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                if (act) {
+                    float z = fmaf(w[W - 1][e], v[e], bias[e]);
+#pragma unroll
+                    for (int k = 1; k < W; ++k) z = fmaf(w[W - 1 - k][e], past[k - 1][e], z);
+                    g[e] *= mx::silu_slope(z, mx::sigmoid(z));
+                }
+                if (i < s.t1) {
+                    db[e] += g[e];
+                    dw[W - 1][e] = fmaf(g[e], v[e], dw[W - 1][e]);
+#pragma unroll
+                    for (int k = 1; k < W; ++k) dw[W - 1 - k][e] = fmaf(g[e], past[k - 1][e], dw[W - 1 - k][e]);
+                }
+                last[e] = fmaf(w[0][e], g[e], open[W - 2][e]);
+#pragma unroll
+                for (int k = W - 1; k > 1; --k) open[k - 1][e] = fmaf(w[W - k][e], g[e], open[k - 2][e]);
+                open[0][e] = w[W - 1][e] * g[e];
+#pragma unroll
+                for (int k = W - 1; k > 1; --k) past[k - 1][e] = past[k - 2][e];
+                past[0][e] = v[e];
+            }
+            put(i - (W - 1), last);
+        }
+    }
+    if (!done && stop == a.T && (r.end == a.T || r.s >= 0)) close(a.T);
+    float *to = part + (size_t)s.index * (W + 1) * a.C + s.c;
+#pragma unroll
+    for (int j = 0; j < W; ++j) store<float, N>(to + (size_t)j * a.C, dw[j]);
+    store<float, N>(to + (size_t)W * a.C, db);
+}
+
+// dw [C,W] and db [C] from the strips' shares [n][W+1][C], in order: 32 places a
+// CTA, 32 strands of shares, then the strands.
+__global__ void __launch_bounds__(1024) conv_sum_kernel(const float *part, float *dw, float *db, int n, int C, int W) {
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5;
+    const long long all = (long long)(W + 1) * C, i = (long long)blockIdx.x * 32 + lane;
+    float x = 0.f;
+    if (i < all)
+#pragma unroll 4
+        for (int p = strand; p < n; p += 32) x += part[p * all + i];
+    s[strand][lane] = x;
+    __syncthreads();
+    if (strand != 0 || i >= all) return;
+    x = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) x += s[j][lane];
+    const int j = (int)(i / C), c = (int)(i - (long long)j * C);
+    if (j < W) dw[(size_t)c * W + j] = x;
+    else if (db) db[c] = x;
+}
+
+// One token a row: the window's rows are read, shifted and written.
+template <typename T, int N, int W>
+__global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepArgs a) {
+    const int nv = a.C / N;
+    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const int b = (int)(i / nv);
+    if (b >= a.B) return;
+    const int c = (int)(i - (long long)b * nv) * N;
+    T *y = static_cast<T *>(a.y) + (size_t)b * a.C + c;
+    const int slot = a.slots ? a.slots[b] : b;
+    float z[N];
+    if (slot < 0 || slot >= a.n_slots) {  // an idle row
+        zero<N>(z);
+        store<T, N>(y, z);
+        return;
+    }
+    float v[N], past[W - 1][N], w[W][N];
+    const size_t page = (size_t)slot * (W - 1) * a.C + c;
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) load<T, N>(static_cast<const T *>(a.win) + page + (size_t)k * a.C, past[k]);
+    load<T, N>(static_cast<const T *>(a.x) + b * a.sx + c, v);
+    load_taps<N, W>(a.w, c, w);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        z[e] = fmaf(w[W - 1][e], v[e], a.bias ? __ldg(a.bias + c + e) : 0.f);
+#pragma unroll
+        for (int k = W - 2; k >= 0; --k) z[e] = fmaf(w[k][e], past[k][e], z[e]);
+        if (a.flags & GDN_SILU) z[e] = mx::silu(z[e]);
+    }
+    T *out = static_cast<T *>(a.win_out) + page;
+#pragma unroll
+    for (int k = 1; k < W - 1; ++k) store<T, N>(out + (size_t)(k - 1) * a.C, past[k]);
+    store<T, N>(out + (size_t)(W - 2) * a.C, v);
+    store<T, N>(y, z);
+}
+
+// Strips of a row: as many as fill `threads`, of at least 8 tokens.
+struct Cut {
+    int len, per_row;
+};
+Cut cut_rows(int B, int T, int nv, long long threads, int most) {
+    long long strips = threads / nv;
+    if (strips > most) strips = most;
+    long long per_row = strips / B;
+    if (per_row < 1) per_row = 1;
+    long long len = (T + per_row - 1) / per_row;
+    if (len < 8) len = 8;
+    return {(int)len, (int)((T + len - 1) / len)};
+}
+
+template <typename T, int N, int W>
+int fwd(const ConvArgs &a, cudaStream_t stream) {
+    const int nv = a.C / N;
+    const Cut c = cut_rows(a.B, a.T, nv, (long long)mx::resident_ctas<conv_kernel<T, N, W>, kThreads>() * kThreads, 1 << 20);
+    const long long threads = (long long)nv * c.per_row * a.B;
+    conv_kernel<T, N, W><<<(unsigned)((threads + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a, c.len, c.per_row);
+    return mx::launched();
+}
+
+// The shares of dw that a backward makes: at most this many strips, or a strip a row.
+constexpr int kMostStrips = 2048;
+constexpr long long kBwdThreads = 152 * 640;
+Cut bwd_cut(int B, int T, int C) { return cut_rows(B, T, C / 4, kBwdThreads, kMostStrips); }
+
+template <typename T, int W>
+int bwd(const ConvArgs &a, cudaStream_t stream) {
+    constexpr int N = 4;
+    const Cut c = bwd_cut(a.B, a.T, a.C);
+    const long long threads = (long long)(a.C / N) * c.per_row * a.B;
+    float *part = static_cast<float *>(a.ws);
+    conv_bwd_kernel<T, N, W><<<(unsigned)((threads + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a, c.len, c.per_row, part);
+    const int st = mx::launched();
+    if (st != GDN_OK) return st;
+    conv_sum_kernel<<<(unsigned)(((long long)(W + 1) * a.C + 31) / 32), 1024, 0, stream>>>(part, a.dw, a.db, c.per_row * a.B, a.C, W);
+    return mx::launched();
+}
+
+template <typename T, int N, int W>
+int step(const ConvStepArgs &a, cudaStream_t stream) {
+    const long long threads = (long long)(a.C / N) * a.B;
+    conv_step_kernel<T, N, W><<<(unsigned)((threads + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a);
+    return mx::launched();
+}
+
+}  // namespace
+
+int launch_conv_fwd(const ConvArgs &a, cudaStream_t stream) {
+    using B16 = __nv_bfloat16;
+    if (a.dtype == GDN_BF16) return a.W == 2 ? fwd<B16, 8, 2>(a, stream) : a.W == 3 ? fwd<B16, 8, 3>(a, stream) : fwd<B16, 8, 4>(a, stream);
+    return a.W == 2 ? fwd<float, 4, 2>(a, stream) : a.W == 3 ? fwd<float, 4, 3>(a, stream) : fwd<float, 4, 4>(a, stream);
+}
+
+size_t conv_bwd_workspace(int B, int T, int C, int W) {
+    const Cut c = bwd_cut(B, T, C);
+    return sizeof(float) * (size_t)c.per_row * B * (W + 1) * C;
+}
+
+int launch_conv_bwd(const ConvArgs &a, cudaStream_t stream) {
+    using B16 = __nv_bfloat16;
+    if (a.dtype == GDN_BF16) return a.W == 2 ? bwd<B16, 2>(a, stream) : a.W == 3 ? bwd<B16, 3>(a, stream) : bwd<B16, 4>(a, stream);
+    return a.W == 2 ? bwd<float, 2>(a, stream) : a.W == 3 ? bwd<float, 3>(a, stream) : bwd<float, 4>(a, stream);
+}
+
+int launch_conv_step(const ConvStepArgs &a, cudaStream_t stream) {
+    using B16 = __nv_bfloat16;
+    if (a.dtype == GDN_BF16) return a.W == 2 ? step<B16, 8, 2>(a, stream) : a.W == 3 ? step<B16, 8, 3>(a, stream) : step<B16, 8, 4>(a, stream);
+    return a.W == 2 ? step<float, 4, 2>(a, stream) : a.W == 3 ? step<float, 4, 3>(a, stream) : step<float, 4, 4>(a, stream);
+}
+
+}  // namespace gdn

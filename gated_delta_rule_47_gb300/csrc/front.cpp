@@ -17,6 +17,7 @@
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
 #include <ATen/ops/empty_strided.h>
+#include <c10/core/impl/DeviceGuardImplInterface.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -42,6 +43,21 @@ struct Api {
     decltype(&state_pool_fork) fork;
     decltype(&state_pool_compact_workspace_bytes) compact_bytes;
     decltype(&state_pool_compact) compact;
+    decltype(&causal_conv_fwd) conv;
+    decltype(&causal_conv_bwd_workspace_bytes) conv_bytes;
+    decltype(&causal_conv_bwd) conv_back;
+    decltype(&causal_conv_step) conv_step;
+    decltype(&ssm_scan_fwd_workspace_bytes) scan_bytes;
+    decltype(&ssm_scan_fwd) scan;
+    decltype(&ssm_scan_bwd_workspace_bytes) scan_back_bytes;
+    decltype(&ssm_scan_bwd) scan_back;
+    decltype(&ssm_step) scan_step;
+    decltype(&gated_norm_fwd) gated;
+    decltype(&gated_norm_bwd_workspace_bytes) gated_bytes;
+    decltype(&gated_norm_bwd) gated_back;
+    decltype(&block_norm_fwd) block;
+    decltype(&block_norm_bwd_workspace_bytes) block_bytes;
+    decltype(&block_norm_bwd) block_back;
 } api;
 PyObject *current_stream, *fail;  // torch's query, and binding.py's function that raises
 
@@ -391,6 +407,337 @@ PyObject *bwd(PyObject *, PyObject *const *x, Py_ssize_t n) {
     });
 }
 
+// ---- next to a mixer
+
+// The tensors of a call lie on the current device.
+void here(const Tensor &like, std::initializer_list<const Tensor *> others) {
+    need(c10::impl::getDeviceGuardImpl(c10::DeviceType::CUDA)->getDevice() == like.device());
+    for (const Tensor *t : others) need(!t || t->device() == like.device());
+}
+
+// [..,C] with C contiguous and other strides, as the C interface takes them.
+void pitched(const Tensor &t, IntArrayRef shape, at::ScalarType type, long long *out) {
+    need(t.scalar_type() == type && t.sizes() == shape && (t.numel() == 0 || t.stride(-1) == 1 || t.size(-1) == 1));
+    for (int i = 0; i + 1 < t.dim(); ++i) {
+        out[i] = t.size(i) > 1 ? t.stride(i) : 0;
+        need(out[i] >= 0 && out[i] * t.element_size() % 16 == 0);
+    }
+}
+
+struct Rows {
+    int64_t B, T, C, seqs;
+    Rows(const Tensor &x, const Maybe &cu) {
+        need(x.dim() == 3);
+        B = x.size(0), T = x.size(1), C = x.size(2), seqs = B;
+        ints({B, T, C});
+        if (cu) {
+            need(cu.t->dim() == 1 && cu.t->numel() >= 2 && B == 1);
+            dense(cu, cu.t->sizes(), at::kInt);
+            seqs = cu.t->numel() - 1;
+        }
+    }
+};
+int64_t taps(const Tensor &w, const Maybe &bias, int64_t C) {
+    need(w.dim() == 2);
+    dense(w, {C, w.size(1)}, at::kFloat);
+    dense(bias, {C}, at::kFloat);
+    ints({w.size(1)});
+    need(w.size(1) >= 2);
+    return w.size(1);
+}
+Tensor fp32(const Maybe &like) { return like ? at::empty_like(*like.t) : Tensor(); }
+
+// conv(x, weight, bias, initial_window, output_final_window, cu_seqlens, silu): (y, final_window)
+PyObject *conv(PyObject *, PyObject *const *x, Py_ssize_t n) {
+    return guarded(n, 7, [&]() -> PyObject * {
+        const Tensor &in = tensor(x[0]), &w = tensor(x[1]);
+        const Maybe bias(x[2]), win(x[3]), cu(x[5]);
+        const Rows r(in, cu);
+        const auto type = in.scalar_type();
+        const int dt = code(in);
+        const int64_t W = taps(w, bias, r.C);
+        long long st[4];
+        pitched(in, in.sizes(), type, st);
+        dense(win, {r.seqs, W - 1, r.C}, type);
+        here(in, {&w, bias.t, win.t, cu.t});
+        const bool last = truth(x[4]);
+        Tensor y = at::empty(in.sizes(), in.options()), out;
+        if (last) out = at::empty({r.seqs, W - 1, r.C}, in.options());
+        st[2] = r.T * r.C, st[3] = r.C;
+        const int status = api.conv(in.data_ptr(), w.data_ptr<float>(), bias.ptr<float>(), win.ptr(), y.data_ptr(), ptr(out),
+                                    cu.ptr<int>(), st, r.seqs, r.B, r.T, r.C, W, truth(x[6]) ? GDN_SILU : 0, dt, stream_of(in));
+        return good("causal_conv_fwd", status) ? pack({y, out}) : nullptr;
+    });
+}
+
+// conv_back(x, weight, dy, bias, initial_window, dfinal_window, cu_seqlens, silu): (dx, dweight, dbias, dinitial_window)
+PyObject *conv_back(PyObject *, PyObject *const *x, Py_ssize_t n) {
+    return guarded(n, 8, [&]() -> PyObject * {
+        const Tensor &in = tensor(x[0]), &w = tensor(x[1]), &dy = tensor(x[2]);
+        const Maybe bias(x[3]), win(x[4]), dlast(x[5]), cu(x[6]);
+        const Rows r(in, cu);
+        const auto type = in.scalar_type();
+        const int dt = code(in);
+        const int64_t W = taps(w, bias, r.C);
+        long long st[4];
+        pitched(in, in.sizes(), type, st);
+        pitched(dy, in.sizes(), type, st + 2);
+        dense(win, {r.seqs, W - 1, r.C}, type);
+        dense(dlast, {r.seqs, W - 1, r.C}, type);
+        here(in, {&w, &dy, bias.t, win.t, dlast.t, cu.t});
+        const size_t bytes = api.conv_bytes(r.B, r.T, r.C, W);
+        Tensor ws = scratch(bytes, in), dx = at::empty(in.sizes(), in.options()), dw = at::empty_like(w), db = fp32(bias), dwin = fp32(win);
+        const int status = api.conv_back(in.data_ptr(), w.data_ptr<float>(), bias.ptr<float>(), dy.data_ptr(), win.ptr(), dlast.ptr(),
+                                         dx.data_ptr(), dw.data_ptr<float>(), static_cast<float *>(ptr(db)), ptr(dwin), cu.ptr<int>(),
+                                         st, r.seqs, r.B, r.T, r.C, W, truth(x[7]) ? GDN_SILU : 0, dt, ptr(ws), bytes, stream_of(in));
+        return good("causal_conv_bwd", status) ? pack({dx, dw, db, dwin}) : nullptr;
+    });
+}
+
+// A pool's pages of `shape`, and the rows' slots.
+int64_t pages(const Tensor &pool, const Maybe &out, IntArrayRef shape, at::ScalarType type, const Maybe &slots, int64_t B) {
+    need(pool.dim() == 3);
+    const int64_t count = pool.size(0);
+    dense(pool, {count, shape[0], shape[1]}, type);
+    dense(out, pool.sizes(), type);
+    dense(slots, {B}, at::kInt);
+    need(slots || B <= count);
+    ints({B, count});
+    return count;
+}
+
+// conv_step(x, weight, window, bias, slots, window_out, silu): y
+PyObject *conv_step(PyObject *, PyObject *const *x, Py_ssize_t n) {
+    return guarded(n, 7, [&]() -> PyObject * {
+        const Tensor &in = tensor(x[0]), &w = tensor(x[1]), &pool = tensor(x[2]);
+        const Maybe bias(x[3]), slots(x[4]), out(x[5]);
+        need(in.dim() == 2);
+        const int64_t B = in.size(0), C = in.size(1), W = taps(w, bias, C);
+        ints({B, C});
+        const int dt = code(in);
+        long long step;
+        pitched(in, in.sizes(), in.scalar_type(), &step);
+        const int64_t count = pages(pool, out, {W - 1, C}, in.scalar_type(), slots, B);
+        here(in, {&w, &pool, bias.t, slots.t, out.t});
+        Tensor y = at::empty(in.sizes(), in.options());
+        const int status = api.conv_step(in.data_ptr(), w.data_ptr<float>(), bias.ptr<float>(), pool.data_ptr(),
+                                         out ? out.ptr() : pool.data_ptr(), slots.ptr<int>(), y.data_ptr(), step, B, C, W, count,
+                                         truth(x[6]) ? GDN_SILU : 0, dt, stream_of(in));
+        return good("causal_conv_step", status) ? wrap(y) : nullptr;
+    });
+}
+
+// What the scan's two directions share.
+struct Scan : Rows {
+    int64_t N;
+    int dt;
+    unsigned flags;
+    long long st[12];
+    Scan(const Tensor &x, const Tensor &d, const Tensor &A, const Tensor &Bt, const Tensor &Ct, const Maybe &skip, const Maybe &z,
+         const Maybe &bias, const Maybe &s0, const Maybe &cu, PyObject *soft)
+        : Rows(x, cu) {
+        need(A.dim() == 2);
+        N = A.size(1), dt = code(x);
+        ints({N});
+        const auto type = x.scalar_type();
+        dense(A, {C, N}, at::kFloat);
+        pitched(x, {B, T, C}, type, st);
+        pitched(d, {B, T, C}, type, st + 2);
+        pitched(Bt, {B, T, N}, type, st + 4);
+        pitched(Ct, {B, T, N}, type, st + 6);
+        pitched(z ? *z.t : x, {B, T, C}, type, st + 8);
+        dense(skip, {C}, at::kFloat);
+        dense(bias, {C}, at::kFloat);
+        dense(s0, {seqs, C, N}, at::kFloat);
+        here(x, {&d, &A, &Bt, &Ct, skip.t, z.t, bias.t, s0.t, cu.t});
+        flags = truth(soft) ? GDN_DT_SOFTPLUS : 0;
+    }
+};
+
+// scan(x, dt, A, B, C, D, z, dt_bias, initial_state, output_final_state, cu_seqlens, softplus): (y, final_state)
+PyObject *scan(PyObject *, PyObject *const *x, Py_ssize_t n) {
+    return guarded(n, 12, [&]() -> PyObject * {
+        const Tensor &in = tensor(x[0]), &d = tensor(x[1]), &A = tensor(x[2]), &Bt = tensor(x[3]), &Ct = tensor(x[4]);
+        const Maybe skip(x[5]), z(x[6]), bias(x[7]), s0(x[8]), cu(x[10]);
+        Scan p(in, d, A, Bt, Ct, skip, z, bias, s0, cu, x[11]);
+        const bool last = truth(x[9]);
+        const size_t bytes = api.scan_bytes(p.B, p.T, p.C, p.N, p.dt);
+        Tensor ws = scratch(bytes, in), y = at::empty(in.sizes(), in.options()), sf;
+        if (last) sf = at::empty({p.seqs, p.C, p.N}, A.options());
+        p.st[10] = p.T * p.C, p.st[11] = p.C;
+        const int status = api.scan(in.data_ptr(), d.data_ptr(), A.data_ptr<float>(), Bt.data_ptr(), Ct.data_ptr(), skip.ptr<float>(),
+                                    z.ptr(), bias.ptr<float>(), s0.ptr<float>(), y.data_ptr(), static_cast<float *>(ptr(sf)),
+                                    cu.ptr<int>(), p.st, p.seqs, p.B, p.T, p.C, p.N, p.flags, p.dt, ptr(ws), bytes, stream_of(in));
+        return good("ssm_scan_fwd", status) ? pack({y, sf}) : nullptr;
+    });
+}
+
+// scan_back(x, dt, A, B, C, dy, D, z, dt_bias, initial_state, dfinal_state, cu_seqlens, softplus):
+// (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dinitial_state)
+PyObject *scan_back(PyObject *, PyObject *const *x, Py_ssize_t n) {
+    return guarded(n, 13, [&]() -> PyObject * {
+        const Tensor &in = tensor(x[0]), &d = tensor(x[1]), &A = tensor(x[2]), &Bt = tensor(x[3]), &Ct = tensor(x[4]), &dy = tensor(x[5]);
+        const Maybe skip(x[6]), z(x[7]), bias(x[8]), s0(x[9]), dsf(x[10]), cu(x[11]);
+        Scan p(in, d, A, Bt, Ct, skip, z, bias, s0, cu, x[12]);
+        pitched(dy, in.sizes(), in.scalar_type(), p.st + 10);
+        dense(dsf, {p.seqs, p.C, p.N}, at::kFloat);
+        here(in, {&dy, dsf.t});
+        const size_t bytes = api.scan_back_bytes(p.B, p.T, p.C, p.N, p.dt);
+        auto rows = [&](int64_t width) { return at::empty({p.B, p.T, width}, in.options()); };
+        Tensor ws = scratch(bytes, in), dx = rows(p.C), dd = rows(p.C), dB = rows(p.N), dC = rows(p.N), dz, dA = at::empty_like(A);
+        Tensor dskip = fp32(skip), dbias = fp32(bias), ds0 = fp32(s0);
+        if (z) dz = rows(p.C);
+        auto f = [](const Tensor &t) { return static_cast<float *>(ptr(t)); };
+        const int status = api.scan_back(in.data_ptr(), d.data_ptr(), A.data_ptr<float>(), Bt.data_ptr(), Ct.data_ptr(),
+                                         skip.ptr<float>(), z.ptr(), bias.ptr<float>(), s0.ptr<float>(), dy.data_ptr(),
+                                         dsf.ptr<float>(), dx.data_ptr(), dd.data_ptr(), f(dA), dB.data_ptr(), dC.data_ptr(), f(dskip),
+                                         ptr(dz), f(dbias), f(ds0), cu.ptr<int>(), p.st, p.seqs, p.B, p.T, p.C, p.N, p.flags, p.dt,
+                                         ptr(ws), bytes, stream_of(in));
+        return good("ssm_scan_bwd", status) ? pack({dx, dd, dA, dB, dC, dskip, dz, dbias, ds0}) : nullptr;
+    });
+}
+
+// scan_step(x, dt, A, B, C, state, D, z, dt_bias, slots, state_out, softplus): y
+PyObject *scan_step(PyObject *, PyObject *const *x, Py_ssize_t n) {
+    return guarded(n, 12, [&]() -> PyObject * {
+        const Tensor &in = tensor(x[0]), &d = tensor(x[1]), &A = tensor(x[2]), &Bt = tensor(x[3]), &Ct = tensor(x[4]), &pool = tensor(x[5]);
+        const Maybe skip(x[6]), z(x[7]), bias(x[8]), slots(x[9]), out(x[10]);
+        need(in.dim() == 2 && A.dim() == 2);
+        const int64_t B = in.size(0), C = in.size(1), N = A.size(1);
+        ints({B, C, N});
+        const auto type = in.scalar_type();
+        const int dt = code(in);
+        dense(A, {C, N}, at::kFloat);
+        long long st[5];
+        pitched(in, {B, C}, type, st);
+        pitched(d, {B, C}, type, st + 1);
+        pitched(Bt, {B, N}, type, st + 2);
+        pitched(Ct, {B, N}, type, st + 3);
+        pitched(z ? *z.t : in, {B, C}, type, st + 4);
+        dense(skip, {C}, at::kFloat);
+        dense(bias, {C}, at::kFloat);
+        const int64_t count = pages(pool, out, {C, N}, at::kFloat, slots, B);
+        here(in, {&d, &A, &Bt, &Ct, &pool, skip.t, z.t, bias.t, slots.t, out.t});
+        Tensor y = at::empty(in.sizes(), in.options());
+        const int status = api.scan_step(in.data_ptr(), d.data_ptr(), A.data_ptr<float>(), Bt.data_ptr(), Ct.data_ptr(),
+                                         skip.ptr<float>(), z.ptr(), bias.ptr<float>(), pool.data_ptr<float>(),
+                                         out ? out.ptr<float>() : pool.data_ptr<float>(), slots.ptr<int>(), y.data_ptr(), st, B, C, N,
+                                         count, truth(x[11]) ? GDN_DT_SOFTPLUS : 0, dt, stream_of(in));
+        return good("ssm_step", status) ? wrap(y) : nullptr;
+    });
+}
+
+// What the gated norm's two directions share.
+struct Gated {
+    int64_t B, T, H, D;
+    int dt;
+    unsigned flags;
+    long long st[12];
+    Gated(const Tensor &x, const Tensor &gate, const Maybe &w, PyObject *first, PyObject *sigmoid) {
+        need(x.dim() == 4);
+        B = x.size(0), T = x.size(1), H = x.size(2), D = x.size(3), dt = code(x);
+        ints({B, T, H, D});
+        pitched(x, x.sizes(), x.scalar_type(), st);
+        pitched(gate, x.sizes(), x.scalar_type(), st + 3);
+        const bool shared = !w || w.t->dim() == 1;
+        if (shared) dense(w, {D}, at::kFloat);
+        else dense(w, {H, D}, at::kFloat);
+        flags = (truth(first) ? GDN_GATE_FIRST : 0) | (truth(sigmoid) ? GDN_GATE_SIGMOID : 0) | (shared ? GDN_W_SHARED : 0);
+    }
+};
+
+// gated(x, gate, weight, eps, gate_first, sigmoid): y
+PyObject *gated(PyObject *, PyObject *const *x, Py_ssize_t n) {
+    return guarded(n, 6, [&]() -> PyObject * {
+        const Tensor &in = tensor(x[0]), &gate = tensor(x[1]);
+        const Maybe w(x[2]);
+        const Gated p(in, gate, w, x[4], x[5]);
+        here(in, {&gate, w.t});
+        Tensor y = at::empty(in.sizes(), in.options());
+        const int status = api.gated(in.data_ptr(), gate.data_ptr(), w.ptr<float>(), y.data_ptr(), p.st, p.B, p.T, p.H, p.D,
+                                     (float)number(x[3]), p.flags, p.dt, stream_of(in));
+        return good("gated_norm_fwd", status) ? wrap(y) : nullptr;
+    });
+}
+
+// gated_back(dy, x, gate, weight, eps, gate_first, sigmoid): (dx, dgate, dweight)
+PyObject *gated_back(PyObject *, PyObject *const *x, Py_ssize_t n) {
+    return guarded(n, 7, [&]() -> PyObject * {
+        const Tensor &dy = tensor(x[0]), &in = tensor(x[1]), &gate = tensor(x[2]);
+        const Maybe w(x[3]);
+        Gated p(in, gate, w, x[5], x[6]);
+        pitched(dy, in.sizes(), in.scalar_type(), p.st + 6);
+        here(in, {&dy, &gate, w.t});
+        apart(in);  // dx takes its strides
+        const size_t bytes = api.gated_bytes(p.B, p.T, p.H, p.D, p.flags);
+        Tensor ws = scratch(bytes, in), dx = at::empty_like(in), dg = at::empty(in.sizes(), in.options());
+        Tensor dw = p.flags & GDN_W_SHARED ? at::empty({p.D}, in.options().dtype(at::kFloat))
+                                           : at::empty({p.H, p.D}, in.options().dtype(at::kFloat));
+        pitched(dx, in.sizes(), in.scalar_type(), p.st + 9);
+        const int status = api.gated_back(dy.data_ptr(), in.data_ptr(), gate.data_ptr(), w.ptr<float>(), dx.data_ptr(), dg.data_ptr(),
+                                          dw.data_ptr<float>(), p.st, p.B, p.T, p.H, p.D, (float)number(x[4]), p.flags, p.dt, ptr(ws),
+                                          bytes, stream_of(in));
+        return good("gated_norm_bwd", status) ? pack({dx, dg, dw}) : nullptr;
+    });
+}
+
+// What the block norm's two directions share.
+struct Block {
+    int64_t C, rows, groups = 0;
+    int dt;
+    Block(const Tensor &x, const Maybe &w1, const Maybe &s, const Maybe &w2) {
+        need(x.dim() > 0);
+        C = x.size(-1), rows = C ? x.numel() / C : 0, dt = code(x);
+        ints({C});
+        dense(x, x.sizes(), x.scalar_type());
+        dense(w1, {C}, at::kFloat);
+        dense(w2, {C}, at::kFloat);
+        if (s) {
+            need(s.t->dim() == 1 || s.t->dim() == 2);
+            groups = s.t->dim() == 1 ? 1 : s.t->size(0);
+            if (s.t->dim() == 1) dense(s, {C}, at::kFloat);
+            else dense(s, {groups, C}, at::kFloat);
+            ints({groups});
+            need(groups > 0 && rows % groups == 0);
+        }
+    }
+};
+
+// block(x, residual, post_weight, scale, weight, eps): (y, h)
+PyObject *block(PyObject *, PyObject *const *x, Py_ssize_t n) {
+    return guarded(n, 6, [&]() -> PyObject * {
+        const Tensor &in = tensor(x[0]), &res = tensor(x[1]);
+        const Maybe w1(x[2]), s(x[3]), w2(x[4]);
+        const Block p(in, w1, s, w2);
+        dense(res, in.sizes(), in.scalar_type());
+        here(in, {&res, w1.t, s.t, w2.t});
+        Tensor y = at::empty_like(in), h = at::empty_like(in);
+        const int status = api.block(in.data_ptr(), res.data_ptr(), w1.ptr<float>(), s.ptr<float>(), w2.ptr<float>(), y.data_ptr(),
+                                     h.data_ptr(), p.rows, p.C, p.groups, (float)number(x[5]), p.dt, stream_of(in));
+        return good("block_norm_fwd", status) ? pack({y, h}) : nullptr;
+    });
+}
+
+// block_back(dy, dh, x, h, post_weight, scale, weight, eps): (dx, dresidual, dpost_weight, dscale, dweight)
+PyObject *block_back(PyObject *, PyObject *const *x, Py_ssize_t n) {
+    return guarded(n, 8, [&]() -> PyObject * {
+        const Tensor &dy = tensor(x[0]), &in = tensor(x[2]), &h = tensor(x[3]);
+        const Maybe dh(x[1]), w1(x[4]), s(x[5]), w2(x[6]);
+        const Block p(in, w1, s, w2);
+        dense(dy, in.sizes(), in.scalar_type());
+        dense(h, in.sizes(), in.scalar_type());
+        dense(dh, in.sizes(), in.scalar_type());
+        here(in, {&dy, &h, dh.t, w1.t, s.t, w2.t});
+        const size_t bytes = api.block_bytes(p.rows, p.C, p.groups);
+        Tensor ws = scratch(bytes, in), dx = at::empty_like(in), dres = at::empty_like(in), dw1 = fp32(w1), ds = fp32(s), dw2 = fp32(w2);
+        auto f = [](const Tensor &t) { return static_cast<float *>(ptr(t)); };
+        const int status = api.block_back(dy.data_ptr(), dh.ptr(), in.data_ptr(), h.data_ptr(), w1.ptr<float>(), s.ptr<float>(),
+                                          w2.ptr<float>(), dx.data_ptr(), dres.data_ptr(), f(dw1), f(ds), f(dw2), p.rows, p.C, p.groups,
+                                          (float)number(x[7]), p.dt, ptr(ws), bytes, stream_of(in));
+        return good("block_norm_bwd", status) ? pack({dx, dres, dw1, ds, dw2}) : nullptr;
+    });
+}
+
 // init(addresses of the entry points in Api's order, current stream's query, raise)
 PyObject *init(PyObject *, PyObject *args) {
     PyObject *at_;
@@ -420,6 +767,16 @@ PyMethodDef methods[] = {{"init", init, METH_VARARGS, nullptr},
                          {"compact", fast(compact), METH_FASTCALL, nullptr},
                          {"fwd", fast(fwd), METH_FASTCALL, nullptr},
                          {"bwd", fast(bwd), METH_FASTCALL, nullptr},
+                         {"conv", fast(conv), METH_FASTCALL, nullptr},
+                         {"conv_back", fast(conv_back), METH_FASTCALL, nullptr},
+                         {"conv_step", fast(conv_step), METH_FASTCALL, nullptr},
+                         {"scan", fast(scan), METH_FASTCALL, nullptr},
+                         {"scan_back", fast(scan_back), METH_FASTCALL, nullptr},
+                         {"scan_step", fast(scan_step), METH_FASTCALL, nullptr},
+                         {"gated", fast(gated), METH_FASTCALL, nullptr},
+                         {"gated_back", fast(gated_back), METH_FASTCALL, nullptr},
+                         {"block", fast(block), METH_FASTCALL, nullptr},
+                         {"block_back", fast(block_back), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_front", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

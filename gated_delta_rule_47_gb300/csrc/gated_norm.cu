@@ -1,0 +1,333 @@
+// gated_norm.cu -- the norm of a mixer's output by head, with its gate, in front of
+// the output projection; and its backward.
+//
+//   y = w n(x) act(g),  n(u) = u / sqrt(mean u^2 + eps) over a head's D columns,
+//   or with GDN_GATE_FIRST  y = w n(x act(g));   act: SiLU or the sigmoid
+//
+// backward, r = 1 / sqrt(..), u = x or x act(g), t = w dy act(g) or w dy:
+//   du = r (t - n mean(n t)),   dw = sum dy n act(g) or dy n
+//   dg = dy w n act'(g) or du x act'(g),   dx = du or du act(g)
+//
+// One pass: NT threads hold a row's head in registers between its sums and its
+// outputs; the bytes bound it.  A group of threads keeps to one head and walks the
+// tokens, the next row's loads on their way, so that the weights stay in
+// registers, and the head's share of dw does too.
+#include "mixer.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Where a group of NT threads works: head h of tokens first, first + step, ..
+struct Walk {
+    int h, first, step, tid;
+};
+template <int NT>
+__device__ __forceinline__ Walk walk_of(const GatedNormArgs &a, int strips) {
+    const long long slot = (long long)blockIdx.x * (kThreads / NT) + threadIdx.x / NT;
+    const int strip = (int)(slot / a.H);
+    return {(int)(slot - (long long)strip * a.H), strip < strips ? strip : 0x7fffffff, strips, (int)threadIdx.x % NT};
+}
+template <typename T>
+__device__ __forceinline__ T *row_at(T *p, const HeadStrides &s, int b, int t, int h) {
+    return p + b * s.b + t * s.t + h * s.h;
+}
+
+// Sums over the NT threads of a group; where it spans warps, `s` alternates.
+template <int NT, int K>
+__device__ __forceinline__ void group_sum(float (&x)[K], float (*s)[kThreads / 32]) {
+#pragma unroll
+    for (int m = (NT < 32 ? NT : 32) / 2; m; m >>= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) x[k] += __shfl_xor_sync(~0u, x[k], m);
+    if constexpr (NT > 32) {
+        const int warp = threadIdx.x >> 5, first = threadIdx.x / NT * (NT / 32);
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int k = 0; k < K; ++k) s[k][warp] = x[k];
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / NT), "n"(NT) : "memory");
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            x[k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < NT / 32; ++i) x[k] += s[k][first + i];
+        }
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void load_weights(const float *w, int i, bool there, float (&x)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+        float4 y = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (w && there) y = __ldg(reinterpret_cast<const float4 *>(w + i + e));
+        x[e] = y.x, x[e + 1] = y.y, x[e + 2] = y.z, x[e + 3] = y.w;
+    }
+}
+
+// V vectors a thread: vector j of thread t is number j NT + t.
+template <typename T, int NT, int V>
+__global__ void __launch_bounds__(kThreads) gated_kernel(GatedNormArgs a, int strips) {
+    constexpr int N = kWide<T>;
+    using Raw = typename Vec<T, N>::Raw;
+    __shared__ float red[2][1][kThreads / 32];
+    const Walk k = walk_of<NT>(a, strips);
+    const int nv = a.D / N, tokens = a.B * a.T;
+    const bool first = a.flags & GDN_GATE_FIRST, sigmoid = a.flags & GDN_GATE_SIGMOID;
+    float w[V][N];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int i = j * NT + k.tid;
+        load_weights<N>(a.w, ((a.flags & GDN_W_SHARED) ? 0 : k.h * a.D) + i * N, i < nv, w[j]);
+    }
+    Raw nx[V], ng[V];
+    auto fetch = [&](int token) {
+        const int b = token / a.T, t = token - b * a.T;
+        const Raw *x = reinterpret_cast<const Raw *>(row_at(static_cast<const T *>(a.x), a.sx, b, t, k.h));
+        const Raw *g = reinterpret_cast<const Raw *>(row_at(static_cast<const T *>(a.gate), a.sg, b, t, k.h));
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int i = j * NT + k.tid;
+            nx[j] = ng[j] = Raw{};
+            if (token < tokens && i < nv) nx[j] = __ldcs(x + i), ng[j] = __ldcs(g + i);
+        }
+    };
+    // every group of a CTA takes as many turns, so that warps stay whole
+    const int turns = (tokens + strips - 1) / strips;
+    int token = k.first < tokens ? k.first : tokens, buf = 0;
+    fetch(token);
+    for (int turn = 0; turn < turns; ++turn, buf ^= 1) {
+        float x[V][N], act[V][N], ss[1] = {0.f};
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            Vec<T, N>::unpack(nx[j], x[j]);
+            Vec<T, N>::unpack(ng[j], act[j]);
+        }
+        const int now = token;
+        token = token < tokens - k.step ? token + k.step : tokens;
+        fetch(token);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float s = mx::sigmoid(act[j][e]);
+                act[j][e] = sigmoid ? s : act[j][e] * s;
+                if (first) x[j][e] = j * NT + k.tid < nv ? x[j][e] * act[j][e] : 0.f, act[j][e] = 1.f;
+                ss[0] = fmaf(x[j][e], x[j][e], ss[0]);
+            }
+        group_sum<NT, 1>(ss, red[buf]);
+        const float r = rsqrtf(ss[0] / a.D + a.eps);
+        if (now >= tokens) continue;
+        Raw *y = reinterpret_cast<Raw *>(static_cast<T *>(a.y) + ((size_t)now * a.H + k.h) * a.D);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[j][e] *= r * w[j][e] * act[j][e];
+            if (j * NT + k.tid < nv) __stcs(y + j * NT + k.tid, Vec<T, N>::pack(x[j]));
+        }
+    }
+}
+
+// part: with a weight for each head [strips][H][D]; with one for all, a CTA's
+// groups are added up: [gridDim.x][D].
+template <typename T, int NT, int V>
+__global__ void __launch_bounds__(kThreads) gated_bwd_kernel(GatedNormArgs a, int strips, float *part) {
+    constexpr int N = kWide<T>, GROUPS = kThreads / NT;
+    using Raw = typename Vec<T, N>::Raw;
+    __shared__ float red[2][2][kThreads / 32];
+    extern __shared__ __align__(16) float share[];  // [GROUPS][D], where the weight is shared
+    const Walk k = walk_of<NT>(a, strips);
+    const int nv = a.D / N, tokens = a.B * a.T;
+    const bool first = a.flags & GDN_GATE_FIRST, sigmoid = a.flags & GDN_GATE_SIGMOID, shared = a.flags & GDN_W_SHARED;
+    float w[V][N], dw[V][N];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int i = j * NT + k.tid;
+        load_weights<N>(a.w, (shared ? 0 : k.h * a.D) + i * N, i < nv, w[j]);
+#pragma unroll
+        for (int e = 0; e < N; ++e) dw[j][e] = 0.f;
+    }
+    Raw nx[V], ng[V], nd[V];
+    auto fetch = [&](int token) {
+        const int b = token / a.T, t = token - b * a.T;
+        const Raw *x = reinterpret_cast<const Raw *>(row_at(static_cast<const T *>(a.x), a.sx, b, t, k.h));
+        const Raw *g = reinterpret_cast<const Raw *>(row_at(static_cast<const T *>(a.gate), a.sg, b, t, k.h));
+        const Raw *d = reinterpret_cast<const Raw *>(row_at(static_cast<const T *>(a.dy), a.sdy, b, t, k.h));
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int i = j * NT + k.tid;
+            nx[j] = ng[j] = nd[j] = Raw{};
+            if (token < tokens && i < nv) nx[j] = __ldcs(x + i), ng[j] = __ldcs(g + i), nd[j] = __ldcs(d + i);
+        }
+    };
+    const int turns = (tokens + strips - 1) / strips;
+    int token = k.first < tokens ? k.first : tokens, buf = 0;
+    fetch(token);
+    for (int turn = 0; turn < turns; ++turn, buf ^= 1) {
+        Raw px[V], pg[V], pd[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) px[j] = nx[j], pg[j] = ng[j], pd[j] = nd[j];
+        const int now = token;
+        token = token < tokens - k.step ? token + k.step : tokens;
+        fetch(token);
+        float x[V][N], g[V][N], s[V][N], d[V][N], sums[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            Vec<T, N>::unpack(px[j], x[j]);
+            Vec<T, N>::unpack(pg[j], g[j]);
+            Vec<T, N>::unpack(pd[j], d[j]);
+            const bool there = j * NT + k.tid < nv;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                s[j][e] = mx::sigmoid(g[j][e]);
+                const float act = sigmoid ? s[j][e] : g[j][e] * s[j][e];
+                const float u = first ? (there ? x[j][e] * act : 0.f) : x[j][e];
+                const float t = first ? d[j][e] : (there ? d[j][e] * act : 0.f);
+                sums[0] = fmaf(u, u, sums[0]);
+                sums[1] = fmaf(u, t * w[j][e], sums[1]);
+            }
+        }
+        group_sum<NT, 2>(sums, red[buf]);
+        const float r = rsqrtf(sums[0] / a.D + a.eps), m = r * r * (sums[1] / a.D);
+        if (now >= tokens) continue;
+        const int b = now / a.T, t0 = now - b * a.T;
+        Raw *dx = reinterpret_cast<Raw *>(row_at(static_cast<T *>(a.dx), a.sdx, b, t0, k.h));
+        Raw *dg = reinterpret_cast<Raw *>(static_cast<T *>(a.dgate) + ((size_t)now * a.H + k.h) * a.D);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float ox[N], og[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float act = sigmoid ? s[j][e] : g[j][e] * s[j][e];
+                const float slope = sigmoid ? s[j][e] * (1.f - s[j][e]) : mx::silu_slope(g[j][e], s[j][e]);
+                const float u = first ? x[j][e] * act : x[j][e], t = first ? d[j][e] : d[j][e] * act;
+                const float du = r * fmaf(t, w[j][e], -u * m);
+                ox[e] = first ? du * act : du;
+                og[e] = first ? du * x[j][e] * slope : d[j][e] * w[j][e] * (u * r) * slope;
+                dw[j][e] = fmaf(t, u * r, dw[j][e]);
+            }
+            if (j * NT + k.tid < nv) {
+                __stcs(dx + j * NT + k.tid, Vec<T, N>::pack(ox));
+                __stcs(dg + j * NT + k.tid, Vec<T, N>::pack(og));
+            }
+        }
+    }
+    const bool mine = k.first < strips;  // groups past the last strip have nothing
+    float *to = shared ? share + (threadIdx.x / NT) * a.D : part + ((size_t)(mine ? k.first : 0) * a.H + k.h) * a.D;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int i = j * NT + k.tid;
+        if (i < nv && (mine || shared))
+#pragma unroll
+            for (int e = 0; e < N; e += 4)
+                *reinterpret_cast<float4 *>(to + i * N + e) = make_float4(dw[j][e], dw[j][e + 1], dw[j][e + 2], dw[j][e + 3]);
+    }
+    if (!shared) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.D; i += kThreads) {
+        float x = share[i];
+#pragma unroll 4
+        for (int q = 1; q < GROUPS; ++q) x += share[q * a.D + i];
+        part[(size_t)blockIdx.x * a.D + i] = x;
+    }
+}
+
+// out[c] = the sum of part's rows [n][C], in order: 32 columns a CTA, 32 strands of
+// rows, then the strands.
+__global__ void __launch_bounds__(1024) gated_sum_kernel(const float *part, float *out, int n, int C) {
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    float x = 0.f;
+    if (c < C)
+#pragma unroll 4
+        for (int i = strand; i < n; i += 32) x += part[(size_t)i * C + c];
+    s[strand][lane] = x;
+    __syncthreads();
+    if (strand != 0 || c >= C) return;
+    x = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) x += s[j][lane];
+    out[c] = x;
+}
+
+// Threads of a group and vectors a thread, by a head's vectors; and how the tokens
+// of a head are shared out.
+int group_threads(int nv) {
+    int nt = 8;
+    while (nt < 256 && nt < nv) nt *= 2;
+    return nv <= 8 ? 8 : nt;
+}
+struct Cut {
+    int strips, ctas;
+};
+constexpr int kMostCtas = 152 * 4;
+Cut cut_tokens(int B, int T, int H, int groups) {
+    const long long tokens = (long long)B * T;
+    long long strips = (long long)kMostCtas * groups / H;
+    if (strips < 1) strips = 1;
+    if (strips > tokens) strips = tokens;
+    return {(int)strips, (int)((strips * H + groups - 1) / groups)};
+}
+
+template <typename T, int NT, int V>
+int fwd(const GatedNormArgs &a, cudaStream_t stream) {
+    const Cut c = cut_tokens(a.B, a.T, a.H, kThreads / NT);
+    gated_kernel<T, NT, V><<<c.ctas, kThreads, 0, stream>>>(a, c.strips);
+    return mx::launched();
+}
+template <typename T, int NT, int V>
+int bwd(const GatedNormArgs &a, cudaStream_t stream) {
+    constexpr int GROUPS = kThreads / NT;
+    const Cut c = cut_tokens(a.B, a.T, a.H, GROUPS);
+    const bool shared = a.flags & GDN_W_SHARED;
+    float *part = static_cast<float *>(a.ws);
+    const size_t room = shared ? sizeof(float) * GROUPS * a.D : 0;  // at most 32 KB: a group's threads grow with D
+    gated_bwd_kernel<T, NT, V><<<c.ctas, kThreads, room, stream>>>(a, c.strips, part);
+    const int st = mx::launched();
+    if (st != GDN_OK) return st;
+    const int C = shared ? a.D : a.H * a.D;
+    gated_sum_kernel<<<(C + 31) / 32, 1024, 0, stream>>>(part, a.dw, shared ? c.ctas : c.strips, C);
+    return mx::launched();
+}
+
+// A row of up to NT vectors has one a thread, up to 1024 (bf16) or 2048 (fp32) four or eight.
+template <typename T, bool BACK>
+int launch(const GatedNormArgs &a, cudaStream_t stream) {
+    const int nv = a.D / kWide<T>;
+#define GO(NT, V) return BACK ? bwd<T, NT, V>(a, stream) : fwd<T, NT, V>(a, stream)
+    switch (group_threads(nv)) {
+        case 8: GO(8, 1);
+        case 16: GO(16, 1);
+        case 32: GO(32, 1);
+        case 64: GO(64, 1);
+        case 128: GO(128, 1);
+        default:
+            if (nv <= 256) GO(256, 1);
+            if (nv <= 512) GO(256, 2);
+            if (nv <= 1024) GO(256, 4);
+            GO(256, sizeof(T) == 2 ? 4 : 8);
+    }
+#undef GO
+}
+
+}  // namespace
+
+int launch_gated_norm(const GatedNormArgs &a, cudaStream_t stream) {
+    return a.dtype == GDN_BF16 ? launch<__nv_bfloat16, false>(a, stream) : launch<float, false>(a, stream);
+}
+size_t gated_norm_bwd_workspace(int B, int T, int H, int D, unsigned flags) {
+    // the types' groups differ: the larger of both
+    size_t most = 0;
+    for (int n = 4; n <= 8; n += 4) {
+        const Cut c = cut_tokens(B, T, H, kThreads / group_threads(D / n));
+        const size_t rows = (flags & GDN_W_SHARED) ? (size_t)c.ctas : (size_t)c.strips * H;
+        most = rows > most ? rows : most;
+    }
+    return sizeof(float) * most * D;
+}
+int launch_gated_norm_bwd(const GatedNormArgs &a, cudaStream_t stream) {
+    return a.dtype == GDN_BF16 ? launch<__nv_bfloat16, true>(a, stream) : launch<float, true>(a, stream);
+}
+
+}  // namespace gdn

@@ -1,0 +1,742 @@
+// ssm_scan_bwd.cu -- backward of the selective state space scan (ssm.cuh).  With
+// dy' = dy silu(z) and g_t the gradient of h_t:
+//
+//   g_t = C_t dy'_t + exp(D_{t+1} A) g_{t+1},     p_t = g_t exp(D_t A) h_{t-1}
+//   dA = sum_t D_t p_t,  dx_t = D_t sum_n g_t B_t + skip dy'_t,
+//   dD_t = x_t sum_n g_t B_t + sum_n A p_t,       ddt_t = dD_t sigmoid(dt_t + bias)
+//   dB_t = sum_c g_t D_t x_t,  dC_t = sum_c dy'_t h_t,  dz_t = dy_t (C_t.h_t + skip x_t) silu'(z_t)
+//
+// Three launches.  share_kernel walks every chunk forwards from 0 and writes the
+// state before each block of 8 tokens, what the chunk leaves, and what gradient it
+// passes to the chunk before it (through the running product of its decays, so
+// that one exponential serves both).  grad_kernel walks the chunks backwards: a
+// block's states are made anew from the one before it and stay in registers.
+// sum_kernel adds up, in order, what groups of channels give to dB and dC and what
+// chunks give to dA, dskip and dbias.  Three exponentials a (token, channel,
+// state); states every 8 tokens take Di N / 2 bytes a token, written and read once
+// behind the arithmetic.
+//
+// A thread holds 4 channels x 4 states: the sums over states are over N/4 lanes,
+// those over channels over the other lanes, both by halves (each lane passes on
+// what another one keeps).  The other way round (all states of a channel in a
+// thread, as forwards) would need 32 values summed over 32 lanes for dB and dC.
+#include <algorithm>
+#include <atomic>
+
+#include "ssm.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace ssm;
+using mx::Run;
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kBlock = 8;  // tokens between two states in memory
+
+template <typename T, int N>
+struct Shape {
+    static constexpr int L = N / 4;       // lanes of a channel's states
+    static constexpr int G = 32 / L;      // lanes of the channels
+    static constexpr int CH = 4 * G;      // channels a warp
+    static constexpr int V = kWide<T>;
+    static constexpr int RV = CH / V;     // vectors of a token's channels
+    static constexpr int NV = kBlock * RV, VPL = (NV + 31) / 32;  // of a block; of a lane
+    static constexpr int BV = N / V;      // vectors of a token's B
+    static constexpr int NB = kBlock * BV, BPL = (2 * NB + 31) / 32;
+};
+
+// How a row is cut, and where a call's intermediates are.
+struct Plan {
+    int len, chunks;     // tokens of a chunk, a multiple of kBlock
+    int groups, blocks;  // CTAs over the channels; blocks of tokens a row
+    float *left, *back;  // [row][chunk][Di][N]: the state that a chunk leaves, the gradient that it passes on
+    float *steps;        // [row][chunk][Di]: the sum of its steps
+    float *state;        // [row][block][Di][N]: the state before a block, from 0 at the chunk's start
+    float *upto;         // [row][block][Di]: the steps from the chunk's start to the block
+    float *dA, *dD, *db; // [row][chunk][Di][N], [row][chunk][Di] twice
+    float *dBC;          // [group][row][T][2 N]
+};
+
+template <typename T, int N>
+struct Mem {
+    using S = Shape<T, N>;
+    uint4 raw[2][4][S::NV];  // x, dt, dy, z as loaded, twice: one on its way
+    uint4 bc[2][2 * S::NB];
+    float step[kBlock][S::CH], x[kBlock][S::CH], dy[kBlock][S::CH];  // then D's and x's gradients, and y
+    float b[kBlock][N], c[kBlock][N];
+};
+template <typename T, int N>
+struct GradMem : Mem<T, N> {
+    using S = Shape<T, N>;
+    float4 saved[2][5][32];                 // a block's state and steps, as the lanes take them
+    float4 start[4][32];                    // the state that enters the chunk
+    float part[2][kBlock][2 * N];           // a block's dB and dC of this warp
+    float acc[2][S::VPL * S::V][32];        // dskip and dbias of each lane's vectors
+};
+
+__device__ __forceinline__ void copy16(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_done(bool all) {
+    if (all) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else asm volatile("cp.async.wait_group 1;" ::: "memory");
+}
+__device__ __forceinline__ void copies_out() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// A warp's place: channels c0 .., and the thread's four.
+struct Place {
+    int row, chunk, group, t0, t1, c0, c, q, g;
+};
+template <typename T, int N>
+__device__ __forceinline__ Place place_of(const SsmArgs &a, const Plan &p) {
+    using S = Shape<T, N>;
+    Place w;
+    const int lane = threadIdx.x & 31, item = blockIdx.x / p.groups;
+    w.group = blockIdx.x % p.groups;
+    w.row = item / p.chunks, w.chunk = item - w.row * p.chunks;
+    w.t0 = w.chunk * p.len, w.t1 = min(w.t0 + p.len, a.T);
+    w.c0 = (w.group * kWarps + (threadIdx.x >> 5)) * S::CH;
+    w.q = lane % S::L, w.g = lane / S::L;
+    w.c = w.c0 + 4 * w.g;
+    return w;
+}
+
+// Starts the copies of the block of tokens at t.
+template <typename T, int N>
+__device__ __forceinline__ void fetch(const SsmArgs &a, const Place &w, Mem<T, N> &m, int buf, int t) {
+    using S = Shape<T, N>;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < S::VPL; ++i) {
+        const int j = i * 32 + lane, tok = t + j / S::RV, c = w.c0 + j % S::RV * S::V;
+        if (j < S::NV && tok < w.t1 && c < a.Di) {
+            copy16(&m.raw[buf][0][j], static_cast<const T *>(a.x) + w.row * a.sx.b + tok * a.sx.t + c);
+            copy16(&m.raw[buf][1][j], static_cast<const T *>(a.dt) + w.row * a.sdt.b + tok * a.sdt.t + c);
+            copy16(&m.raw[buf][2][j], static_cast<const T *>(a.dy) + w.row * a.sy.b + tok * a.sy.t + c);
+            if (a.z) copy16(&m.raw[buf][3][j], static_cast<const T *>(a.z) + w.row * a.sz.b + tok * a.sz.t + c);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < S::BPL; ++i) {
+        const int j = i * 32 + lane, k = j % S::NB, tok = t + k / S::BV, n = k % S::BV * S::V;
+        if (j < 2 * S::NB && tok < w.t1)
+            copy16(&m.bc[buf][j], j < S::NB ? static_cast<const T *>(a.Bt) + w.row * a.sB.b + tok * a.sB.t + n
+                                            : static_cast<const T *>(a.Ct) + w.row * a.sC.b + tok * a.sC.t + n);
+    }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const uint4 &p, float (&x)[V]) {
+    Vec<T, V>::unpack(p, x);
+}
+template <int V>
+__device__ __forceinline__ void put(float *to, const float (&x)[V]) {
+#pragma unroll
+    for (int e = 0; e < V; e += 4) *reinterpret_cast<float4 *>(to + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+}
+template <int V>
+__device__ __forceinline__ void get(const float *from, float (&x)[V]) {
+#pragma unroll
+    for (int e = 0; e < V; e += 4) {
+        const float4 y = *reinterpret_cast<const float4 *>(from + e);
+        x[e] = y.x, x[e + 1] = y.y, x[e + 2] = y.z, x[e + 3] = y.w;
+    }
+}
+template <int V>
+__device__ __forceinline__ void vector_of(const float *p, int c, float (&x)[V]) {
+#pragma unroll
+    for (int e = 0; e < V; e += 4) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p) y = __ldg(reinterpret_cast<const float4 *>(p + c + e));
+        x[e] = y.x, x[e + 1] = y.y, x[e + 2] = y.z, x[e + 3] = y.w;
+    }
+}
+
+// Steps, x and dy' of a block, and its B and C, in fp32; zeros for tokens of no
+// sequence (bits of `dead`), which then change nothing.
+template <typename T, int N>
+__device__ __forceinline__ void convert(const SsmArgs &a, const Place &w, Mem<T, N> &m, int buf, int t, unsigned dead) {
+    using S = Shape<T, N>;
+    const int lane = threadIdx.x & 31;
+    const bool soft = a.flags & GDN_DT_SOFTPLUS;
+#pragma unroll
+    for (int i = 0; i < S::VPL; ++i) {
+        const int j = i * 32 + lane, tok = j / S::RV, c = j % S::RV * S::V;
+        if (j >= S::NV) break;
+        float x[S::V], d[S::V], g[S::V];
+        if (t + tok < w.t1 && w.c0 + c < a.Di && !(dead >> tok & 1)) {
+            float bias[S::V];
+            vector_of<S::V>(a.bias, w.c0 + c, bias);
+            unpack<T, S::V>(m.raw[buf][0][j], x);
+            unpack<T, S::V>(m.raw[buf][1][j], d);
+            unpack<T, S::V>(m.raw[buf][2][j], g);
+#pragma unroll
+            for (int e = 0; e < S::V; ++e) {
+                d[e] += bias[e];
+                if (soft) d[e] = mx::softplus(d[e]);
+            }
+            if (a.z) {
+                float z[S::V];
+                unpack<T, S::V>(m.raw[buf][3][j], z);
+#pragma unroll
+                for (int e = 0; e < S::V; ++e) g[e] *= mx::silu(z[e]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < S::V; ++e) x[e] = d[e] = g[e] = 0.f;
+        }
+        put<S::V>(&m.x[tok][c], x);
+        put<S::V>(&m.step[tok][c], d);
+        put<S::V>(&m.dy[tok][c], g);
+    }
+#pragma unroll
+    for (int i = 0; i < S::BPL; ++i) {
+        const int j = i * 32 + lane, k = j % S::NB, tok = k / S::BV, n = k % S::BV * S::V;
+        if (j >= 2 * S::NB) break;
+        float x[S::V];
+        unpack<T, S::V>(m.bc[buf][j], x);
+        if (t + tok >= w.t1 || (dead >> tok & 1))
+#pragma unroll
+            for (int e = 0; e < S::V; ++e) x[e] = 0.f;
+        put<S::V>(j < S::NB ? &m.b[tok][n] : &m.c[tok][n], x);
+    }
+}
+
+// Which tokens of a block start a sequence, end one, or are in none (or past the
+// chunk); r: the run of its first token.
+struct Marks {
+    unsigned starts, ends, dead;
+};
+__device__ __forceinline__ Marks marks_of(const SsmArgs &a, const Place &w, int t, Run &r) {
+    if (t < r.start || t >= r.end) r = mx::run_at(a.cu, a.n_seq, a.T, w.row, t);
+    const int n = min(kBlock, w.t1 - t);
+    const unsigned past = 0xffu << n & 0xffu;
+    if (r.end >= t + n) {
+        if (r.s < 0) return {0, 0, 0xffu};
+        return {r.start == t ? 1u : 0u, r.end == t + n ? 1u << (n - 1) : 0u, past};
+    }
+    const int lane = threadIdx.x & 31;
+    Run mine{-1, 0, 0};
+    if (lane < n) mine = mx::run_at(a.cu, a.n_seq, a.T, w.row, t + lane);
+    return {__ballot_sync(~0u, mine.s >= 0 && mine.start == t + lane), __ballot_sync(~0u, mine.s >= 0 && mine.end == t + lane + 1),
+            __ballot_sync(~0u, mine.s < 0) & 0xffu};
+}
+
+// The thread's 4 x 4 of a [Di,N] page, 0 where there is none.
+template <int N>
+__device__ __forceinline__ void load16(const SsmArgs &a, const Place &w, const float *page, F2 (&h)[4][2]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        ulonglong2 v = make_ulonglong2(0, 0);
+        if (page && w.c < a.Di) v = *reinterpret_cast<const ulonglong2 *>(page + (size_t)(w.c + e) * N + 4 * w.q);
+        h[e][0] = v.x, h[e][1] = v.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void store16(const SsmArgs &a, const Place &w, float *page, const F2 (&h)[4][2]) {
+    if (w.c >= a.Di) return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<ulonglong2 *>(page + (size_t)(w.c + e) * N + 4 * w.q) = make_ulonglong2(h[e][0], h[e][1]);
+}
+template <int N>
+__device__ __forceinline__ void load_decays(const SsmArgs &a, const Place &w, F2 (&d)[4][2]) {
+    load16<N>(a, w, a.A, d);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e][0] = mul2(d[e][0], both(mx::kLog2e)), d[e][1] = mul2(d[e][1], both(mx::kLog2e));
+}
+__device__ __forceinline__ void zero16(F2 (&h)[4][2]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e][0] = h[e][1] = 0;
+}
+__device__ __forceinline__ size_t chunk_at(const SsmArgs &a, const Plan &p, int row, int chunk) {
+    return ((size_t)row * p.chunks + chunk) * a.Di;
+}
+
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads, 4) share_kernel(SsmArgs a, Plan p) {
+    using S = Shape<T, N>;
+    extern __shared__ __align__(16) char smem[];
+    Mem<T, N> &m = reinterpret_cast<Mem<T, N> *>(smem)[threadIdx.x >> 5];
+    const Place w = place_of<T, N>(a, p);
+    if (w.c0 >= a.Di) return;  // warps do not wait for one another here
+    fetch<T, N>(a, w, m, 0, w.t0);
+    copies_out();
+    F2 h[4][2], A[4][2], prod[4][2], back[4][2];
+    float total[4] = {0.f, 0.f, 0.f, 0.f};
+    load_decays<N>(a, w, A);
+    zero16(h);
+    zero16(back);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) prod[e][0] = prod[e][1] = both(1.f);
+    const size_t page = (size_t)a.Di * N;
+    Run r = mx::run_at(a.cu, a.n_seq, a.T, w.row, w.t0);
+    // up to where the chunk passes a gradient to the one before
+    const int until = r.s >= 0 && r.start < w.t0 ? min(r.end, w.t1) : w.t0;
+    const int last_of = r.end, seq = r.s;
+    int buf = 0;
+    for (int t = w.t0; t < w.t1; t += kBlock, buf ^= 1) {
+        const bool more = t + kBlock < w.t1;
+        if (more) fetch<T, N>(a, w, m, buf ^ 1, t + kBlock), copies_out();
+        const Marks k = marks_of(a, w, t, r);
+        const size_t at = ((size_t)w.row * p.blocks + t / kBlock) * a.Di;
+        store16<N>(a, w, p.state + at * N, h);
+        if (w.q == 0 && w.c < a.Di) *reinterpret_cast<float4 *>(p.upto + at + w.c) = make_float4(total[0], total[1], total[2], total[3]);
+        copies_done(!more);
+        __syncwarp();
+        convert<T, N>(a, w, m, buf, t, k.dead);
+        __syncwarp();
+#pragma unroll 2
+        for (int u = 0; u < kBlock; ++u) {
+            if (k.starts >> u & 1) {
+                const Run s = mx::run_at(a.cu, a.n_seq, a.T, w.row, t + u);
+                load16<N>(a, w, a.s0 ? a.s0 + s.s * page : nullptr, h);
+            }
+            float d[4], x[4], g[4];
+            get<4>(&m.step[u][4 * w.g], d);
+            get<4>(&m.x[u][4 * w.g], x);
+            get<4>(&m.dy[u][4 * w.g], g);
+            const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(&m.b[u][4 * w.q]);
+            const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(&m.c[u][4 * w.q]);
+            const bool pass = t + u < until;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const F2 in = both(d[e] * x[e]), de = both(d[e]), ge = both(g[e]);
+                total[e] += d[e];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const F2 dec = exp2_2(mul2(de, A[e][i]));
+                    h[e][i] = fma2(dec, h[e][i], mul2(in, i ? b.y : b.x));
+                    if (pass) {
+                        prod[e][i] = mul2(prod[e][i], dec);
+                        back[e][i] = fma2(prod[e][i], mul2(ge, i ? c.y : c.x), back[e][i]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    }
+    if (a.dsf && until > w.t0 && last_of <= w.t1) {  // the sequence ends here: its final state's share
+        F2 s[4][2];
+        load16<N>(a, w, a.dsf + seq * page, s);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) back[e][i] = fma2(prod[e][i], s[e][i], back[e][i]);
+    }
+    const size_t at = chunk_at(a, p, w.row, w.chunk);
+    store16<N>(a, w, p.left + at * N, h);
+    store16<N>(a, w, p.back + at * N, back);
+    if (w.q == 0 && w.c < a.Di) *reinterpret_cast<float4 *>(p.steps + at + w.c) = make_float4(total[0], total[1], total[2], total[3]);
+}
+
+// v[0..K) summed over the lanes that differ in bit m: a lane keeps half of the
+// values (the upper half where its bit is set), or all where there is one.
+template <int K>
+__device__ __forceinline__ void halve(float *v, int m) {
+    if constexpr (K == 1) {
+        v[0] += __shfl_xor_sync(~0u, v[0], m);
+    } else {
+        const bool up = (threadIdx.x & m) != 0;
+#pragma unroll
+        for (int i = 0; i < K / 2; ++i) {
+            const float keep = up ? v[i + K / 2] : v[i], pass = up ? v[i] : v[i + K / 2];
+            v[i] = keep + __shfl_xor_sync(~0u, pass, m);
+        }
+    }
+}
+
+// Sums of four channels' values over the lanes of their states: the lane keeps
+// channel(s) e .. of the four.
+template <int L>
+__device__ __forceinline__ void over_states(float (&v)[4]) {
+    halve<4>(v, 1);
+    if constexpr (L >= 4) halve<2>(v, 2);
+    if constexpr (L >= 8) halve<1>(v, 4);
+}
+template <int L>
+__device__ __forceinline__ void put_channels(float *row, int q, const float (&v)[4]) {
+    const int e = (q & 1) * 2;
+    if constexpr (L == 2) *reinterpret_cast<float2 *>(row + e) = make_float2(v[0], v[1]);
+    else if (q < 4) row[e + (q >> 1 & 1)] = v[0];
+}
+// Sums of dB's and dC's four states over the lanes of the channels.
+template <int N>
+__device__ __forceinline__ void over_channels(float (&v)[8]) {
+    constexpr int L = N / 4;
+    halve<8>(v, L);
+    halve<4>(v, 2 * L);
+    if constexpr (N <= 16) halve<2>(v, 4 * L);
+    if constexpr (N <= 8) halve<1>(v, 8 * L);
+}
+template <int N>
+__device__ __forceinline__ void put_states(float *row, int q, int g, const float (&v)[8]) {
+    float *to = row + (g & 1) * N + 4 * q + (g >> 1 & 1) * 2;
+    if constexpr (N == 32) *reinterpret_cast<float2 *>(to) = make_float2(v[0], v[1]);
+    else if (g < 8) to[g >> 2 & 1] = v[0];
+}
+
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
+    using S = Shape<T, N>;
+    extern __shared__ __align__(16) char smem[];
+    GradMem<T, N> *all = reinterpret_cast<GradMem<T, N> *>(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    GradMem<T, N> &m = all[warp];
+    const Place w = place_of<T, N>(a, p);
+    const size_t page = (size_t)a.Di * N;
+    const bool soft = a.flags & GDN_DT_SOFTPLUS;
+    auto fetch_all = [&](int buf, int t) {
+        fetch<T, N>(a, w, m, buf, t);
+        const size_t at = ((size_t)w.row * p.blocks + t / kBlock) * a.Di + w.c;
+        if (w.c < a.Di) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) copy16(&m.saved[buf][e][lane], p.state + (at + e) * N + 4 * w.q);
+            copy16(&m.saved[buf][4][lane], p.upto + at);
+        }
+        copies_out();
+    };
+    const int last = w.t0 + (w.t1 - 1 - w.t0) / kBlock * kBlock;
+    fetch_all(0, last);
+    F2 A[4][2], g[4][2], dA[4][2];
+    load_decays<N>(a, w, A);
+    zero16(g);
+    zero16(dA);
+#pragma unroll
+    for (int i = 0; i < S::VPL * S::V; ++i) m.acc[0][i][lane] = m.acc[1][i][lane] = 0.f;
+    // sequences without tokens pass their gradient on
+    if (a.cu && a.ds0) {
+        for (int s0 = w.chunk * 32; s0 < a.n_seq; s0 += p.chunks * 32) {
+            const int s = s0 + lane;
+            unsigned e = __ballot_sync(~0u, s < a.n_seq && mx::no_tokens(a.cu, a.T, min(s, a.n_seq - 1)));
+            for (; e; e &= e - 1) {
+                const size_t at = (size_t)(s0 + __ffs(e) - 1) * page;
+                F2 h[4][2];
+                load16<N>(a, w, a.dsf ? a.dsf + at : nullptr, h);
+                store16<N>(a, w, a.ds0 + at, h);
+            }
+        }
+    }
+    // x <- what chunk j gives + its decay x, from the first one named on
+    auto join = [&](const float *from, int j, bool first, F2 (&x)[4][2]) {
+        const size_t at = chunk_at(a, p, w.row, j);
+        F2 v[4][2];
+        load16<N>(a, w, from + at * N, v);
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        if (w.c < a.Di) vector_of<4>(p.steps + at, w.c, d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) x[e][i] = first ? v[e][i] : fma2(exp2_2(mul2(both(d[e]), A[e][i])), x[e][i], v[e][i]);
+    };
+    Run r = mx::run_at(a.cu, a.n_seq, a.T, w.row, w.t0);
+    const int entered = r.s >= 0 && r.start < w.t0 ? r.end : w.t0;  // the entering state matters up to here
+    {
+        F2 h[4][2];
+        zero16(h);
+        if (entered > w.t0) {
+            const int first = min(r.start / p.len, w.chunk - 1);
+            for (int j = first; j < w.chunk; ++j) join(p.left, j, j == first, h);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<ulonglong2 *>(&m.start[e][lane]) = make_ulonglong2(h[e][0], h[e][1]);
+        r = mx::run_at(a.cu, a.n_seq, a.T, w.row, w.t1 - 1);
+        if (r.s >= 0 && r.end > w.t1) {
+            const int end = max((r.end - 1) / p.len, w.chunk + 1);
+            for (int j = end; j > w.chunk; --j) join(p.back, j, j == end, g);
+        }
+    }
+    int buf = 0;
+    for (int t = last; t >= w.t0; t -= kBlock, buf ^= 1) {
+        if (t > w.t0) fetch_all(buf ^ 1, t - kBlock);
+        const Marks k = marks_of(a, w, t, r);
+        copies_done(t == w.t0);
+        __syncwarp();
+        convert<T, N>(a, w, m, buf, t, k.dead);
+        F2 hs[kBlock + 1][4][2];  // before the block, and after each of its tokens
+        {
+            float d[4];
+            get<4>(reinterpret_cast<const float *>(&m.saved[buf][4][lane]), d);
+            const bool there = w.c < a.Di;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&m.saved[buf][e][lane]);
+                hs[0][e][0] = there ? v.x : 0, hs[0][e][1] = there ? v.y : 0;
+                if (there && t < entered) {
+                    const ulonglong2 s = *reinterpret_cast<const ulonglong2 *>(&m.start[e][lane]);
+                    hs[0][e][0] = fma2(exp2_2(mul2(both(d[e]), A[e][0])), s.x, hs[0][e][0]);
+                    hs[0][e][1] = fma2(exp2_2(mul2(both(d[e]), A[e][1])), s.y, hs[0][e][1]);
+                }
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < kBlock; ++u) {
+            float d[4], x[4];
+            get<4>(&m.step[u][4 * w.g], d);
+            get<4>(&m.x[u][4 * w.g], x);
+            const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(&m.b[u][4 * w.q]);
+            if (k.starts >> u & 1) {
+                const Run s = mx::run_at(a.cu, a.n_seq, a.T, w.row, t + u);
+                F2 h0[4][2];
+                load16<N>(a, w, a.s0 ? a.s0 + s.s * page : nullptr, h0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        hs[u + 1][e][i] = fma2(exp2_2(mul2(both(d[e]), A[e][i])), h0[e][i], mul2(both(d[e] * x[e]), i ? b.y : b.x));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        hs[u + 1][e][i] = fma2(exp2_2(mul2(both(d[e]), A[e][i])), hs[u][e][i], mul2(both(d[e] * x[e]), i ? b.y : b.x));
+            }
+        }
+#pragma unroll
+        for (int u = kBlock - 1; u >= 0; --u) {
+            if (k.ends >> u & 1) {
+                const Run s = mx::run_at(a.cu, a.n_seq, a.T, w.row, t + u);
+                load16<N>(a, w, a.dsf ? a.dsf + s.s * page : nullptr, g);
+            }
+            if (k.starts >> u & 1) {  // what came before is the sequence's initial state; the last one's end waits
+                const Run s = mx::run_at(a.cu, a.n_seq, a.T, w.row, t + u);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<ulonglong2 *>(&m.saved[buf][e][lane]) = make_ulonglong2(hs[u][e][0], hs[u][e][1]);
+                load16<N>(a, w, a.s0 ? a.s0 + s.s * page : nullptr, hs[u]);
+            }
+            float d[4], x[4], dy[4], dx[4], ds[4], y[4];
+            get<4>(&m.step[u][4 * w.g], d);
+            get<4>(&m.x[u][4 * w.g], x);
+            get<4>(&m.dy[u][4 * w.g], dy);
+            const ulonglong2 b2 = *reinterpret_cast<const ulonglong2 *>(&m.b[u][4 * w.q]);
+            const ulonglong2 c2 = *reinterpret_cast<const ulonglong2 *>(&m.c[u][4 * w.q]);
+            const F2 b[2] = {b2.x, b2.y}, c[2] = {c2.x, c2.y};
+            F2 dB[2] = {0, 0}, dC[2] = {0, 0};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const F2 de = both(d[e]), ge = both(dy[e]), in = both(d[e] * x[e]);
+                F2 gb = 0, ap = 0, cy = 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    g[e][i] = fma2(c[i], ge, g[e][i]);
+                    dC[i] = fma2(hs[u + 1][e][i], ge, dC[i]);
+                    if (a.z) cy = fma2(hs[u + 1][e][i], c[i], cy);
+                    dB[i] = fma2(g[e][i], in, dB[i]);
+                    gb = fma2(g[e][i], b[i], gb);
+                    const F2 ag = mul2(exp2_2(mul2(de, A[e][i])), g[e][i]), over = mul2(ag, hs[u][e][i]);
+                    dA[e][i] = fma2(over, de, dA[e][i]);
+                    ap = fma2(over, A[e][i], ap);
+                    g[e][i] = ag;
+                }
+                const float s = sum(gb);
+                dx[e] = d[e] * s;
+                ds[e] = fmaf(x[e], s, mx::kLn2 * sum(ap));
+                y[e] = sum(cy);
+            }
+            if (k.starts >> u & 1) {
+                const Run s = mx::run_at(a.cu, a.n_seq, a.T, w.row, t + u);
+                if (a.ds0) store16<N>(a, w, a.ds0 + s.s * page, g);
+                zero16(g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&m.saved[buf][e][lane]);
+                    hs[u][e][0] = v.x, hs[u][e][1] = v.y;
+                }
+            }
+            over_states<S::L>(dx);
+            over_states<S::L>(ds);
+            if (a.z) over_states<S::L>(y);
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) split(dB[i], v[2 * i], v[2 * i + 1]), split(dC[i], v[4 + 2 * i], v[5 + 2 * i]);
+            over_channels<N>(v);
+            __syncwarp();  // the token's inputs have been read by all
+            put_channels<S::L>(&m.x[u][4 * w.g], w.q, dx);
+            put_channels<S::L>(&m.step[u][4 * w.g], w.q, ds);
+            if (a.z) put_channels<S::L>(&m.dy[u][4 * w.g], w.q, y);
+            put_states<N>(m.part[buf][u], w.q, w.g, v);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < S::VPL; ++i) {
+            const int j = i * 32 + lane, tok = j / S::RV, cv = j % S::RV * S::V, c = w.c0 + cv;
+            if (j >= S::NV || t + tok >= w.t1 || c >= a.Di) continue;
+            const size_t at = ((size_t)w.row * a.T + t + tok) * a.Di + c;
+            float dx[S::V], dv[S::V], dz[S::V];
+            if (k.dead >> tok & 1) {
+#pragma unroll
+                for (int e = 0; e < S::V; ++e) dx[e] = dv[e] = dz[e] = 0.f;
+            } else {
+                float x[S::V], dt[S::V], dy[S::V], bias[S::V], skip[S::V];
+                get<S::V>(&m.x[tok][cv], dx);
+                get<S::V>(&m.step[tok][cv], dv);
+                unpack<T, S::V>(m.raw[buf][0][j], x);
+                unpack<T, S::V>(m.raw[buf][1][j], dt);
+                unpack<T, S::V>(m.raw[buf][2][j], dy);
+                vector_of<S::V>(a.bias, c, bias);
+                vector_of<S::V>(a.D, c, skip);
+                if (a.z) {
+                    float z[S::V];
+                    unpack<T, S::V>(m.raw[buf][3][j], z);
+                    get<S::V>(&m.dy[tok][cv], dz);
+#pragma unroll
+                    for (int e = 0; e < S::V; ++e) {
+                        const float s = mx::sigmoid(z[e]);
+                        dz[e] = dy[e] * fmaf(skip[e], x[e], dz[e]) * mx::silu_slope(z[e], s);
+                        dy[e] *= z[e] * s;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < S::V; ++e) {
+                    dx[e] = fmaf(skip[e], dy[e], dx[e]);
+                    if (soft) dv[e] *= mx::sigmoid(dt[e] + bias[e]);
+                    m.acc[0][i * S::V + e][lane] += dy[e] * x[e];
+                    m.acc[1][i * S::V + e][lane] += dv[e];
+                }
+            }
+            using Raw = typename Vec<T, S::V>::Raw;
+            __stcs(reinterpret_cast<Raw *>(static_cast<T *>(a.dx) + at), Vec<T, S::V>::pack(dx));
+            __stcs(reinterpret_cast<Raw *>(static_cast<T *>(a.ddt) + at), Vec<T, S::V>::pack(dv));
+            if (a.z) __stcs(reinterpret_cast<Raw *>(static_cast<T *>(a.dz) + at), Vec<T, S::V>::pack(dz));
+        }
+        // dB and dC of the CTA's channels: the warps take turns at adding the four
+        // shares, and the two buffers need one barrier a block
+        __syncthreads();
+        if (warp == (t / kBlock) % kWarps)
+            for (int i = lane; i < kBlock * 2 * N; i += 32) {
+                const int tok = i / (2 * N), n = i % (2 * N);
+                float x = 0.f;
+#pragma unroll
+                for (int k2 = 0; k2 < kWarps; ++k2) x += all[k2].part[buf][tok][n];
+                if (t + tok < w.t1) p.dBC[(((size_t)w.group * a.B + w.row) * a.T + t + tok) * 2 * N + n] = x;
+            }
+    }
+    const size_t at = chunk_at(a, p, w.row, w.chunk);
+    store16<N>(a, w, p.dA + at * N, dA);
+    __syncwarp();
+    for (int i = lane; i < S::CH; i += 32) {
+        if (w.c0 + i >= a.Di) break;
+        float x = 0.f, y = 0.f;
+        for (int j = i / S::V; j < S::NV; j += S::RV) {
+            x += m.acc[0][j / 32 * S::V + i % S::V][j % 32];
+            y += m.acc[1][j / 32 * S::V + i % S::V][j % 32];
+        }
+        p.dD[at + w.c0 + i] = x;
+        p.db[at + w.c0 + i] = y;
+    }
+}
+
+// dB and dC from the groups' shares, a thread four of a token's values; then dA,
+// dskip and dbias from the chunks'.
+template <typename T, int N>
+__global__ void __launch_bounds__(256) sum_kernel(SsmArgs a, Plan p, int tokens_ctas) {
+    if (blockIdx.x < tokens_ctas) {
+        const long long n = (long long)a.B * a.T * (N / 2), i = (long long)blockIdx.x * 256 + threadIdx.x;
+        if (i >= n) return;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < p.groups; ++k) {
+            const float4 v = __ldcs(reinterpret_cast<const float4 *>(p.dBC) + k * n + i);
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        const long long tok = i / (N / 2);
+        const int at = (int)(i - tok * (N / 2)) * 4;
+        const float out[4] = {s.x, s.y, s.z, s.w};
+        T *to = static_cast<T *>(at < N ? a.dB : a.dC) + tok * N + at % N;
+        *reinterpret_cast<typename Vec<T, 4>::Raw *>(to) = Vec<T, 4>::pack(out);
+        return;
+    }
+    const long long i = (long long)(blockIdx.x - tokens_ctas) * 256 + threadIdx.x, each = (long long)a.Di * N;
+    const int items = a.B * p.chunks;
+    const float *from;
+    float *to;
+    long long step;
+    if (i < each) from = p.dA + i, to = a.dA + i, step = each;
+    else if (i < each + a.Di) from = p.dD + (i - each), to = a.dD ? a.dD + (i - each) : nullptr, step = a.Di;
+    else if (i < each + 2 * a.Di) from = p.db + (i - each - a.Di), to = a.dbias ? a.dbias + (i - each - a.Di) : nullptr, step = a.Di;
+    else return;
+    if (!to) return;
+    float s = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < items; ++k) s += from[k * step];
+    *to = s;
+}
+
+// Two waves of grad_kernel's CTAs: more would join more chunks at the start of
+// each, fewer leave SMs idle.  A chunk has 64 tokens or more.
+constexpr int kResident = 152 * 2;
+int channels(int N) { return kWarps * 4 * (32 / (N / 4)); }
+Plan plan(int B, int T, int Di, int N, float *ws, size_t *bytes) {
+    Plan p{};
+    p.groups = (Di + channels(N) - 1) / channels(N);
+    const long long whole = (long long)B * p.groups;
+    const long long chunks = std::max(1LL, 2LL * kResident / whole);
+    const long long len = std::max(64LL, ((T + chunks - 1) / chunks + kBlock - 1) / kBlock * kBlock);
+    p.len = (int)len;
+    p.chunks = (int)((T + len - 1) / len);
+    p.blocks = (T + kBlock - 1) / kBlock;
+    size_t at = 0;
+    auto take = [&](float **x, size_t n) { *x = ws ? ws + at : nullptr, at += (n + 3) / 4 * 4; };
+    const size_t per_chunk = (size_t)B * p.chunks * Di, per_block = (size_t)B * p.blocks * Di;
+    take(&p.left, per_chunk * N);
+    take(&p.back, per_chunk * N);
+    take(&p.steps, per_chunk);
+    take(&p.state, per_block * N);
+    take(&p.upto, per_block);
+    take(&p.dA, per_chunk * N);
+    take(&p.dD, per_chunk);
+    take(&p.db, per_chunk);
+    take(&p.dBC, (size_t)p.groups * B * T * 2 * N);
+    *bytes = at * sizeof(float);
+    return p;
+}
+
+// Shared memory above 48 KB is asked for once on each device.
+template <auto F>
+bool room(int bytes) {
+    static std::atomic<unsigned long long> done{0};
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return false;
+    const unsigned long long bit = device < 64 ? 1ull << device : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(F, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
+
+template <typename T, int N>
+int bwd(const SsmArgs &a, cudaStream_t stream) {
+    size_t bytes;
+    const Plan p = plan(a.B, a.T, a.Di, N, static_cast<float *>(a.ws), &bytes);
+    constexpr int one = sizeof(Mem<T, N>) * kWarps, two = sizeof(GradMem<T, N>) * kWarps;
+    if (!room<share_kernel<T, N>>(one) || !room<grad_kernel<T, N>>(two)) return GDN_ERR_CUDA;
+    const unsigned ctas = (unsigned)((long long)p.groups * a.B * p.chunks);
+    share_kernel<T, N><<<ctas, kThreads, one, stream>>>(a, p);
+    int st = mx::launched();
+    if (st != GDN_OK) return st;
+    grad_kernel<T, N><<<ctas, kThreads, two, stream>>>(a, p);
+    st = mx::launched();
+    if (st != GDN_OK) return st;
+    const long long tokens = ((long long)a.B * a.T * (N / 2) + 255) / 256, rest = ((long long)a.Di * (N + 2) + 255) / 256;
+    sum_kernel<T, N><<<(unsigned)(tokens + rest), 256, 0, stream>>>(a, p, (int)tokens);
+    return mx::launched();
+}
+
+}  // namespace
+
+size_t ssm_bwd_workspace(int B, int T, int Di, int N, int) {
+    size_t bytes;
+    plan(B, T, Di, N, nullptr, &bytes);
+    return bytes;
+}
+
+int launch_ssm_bwd(const SsmArgs &a, cudaStream_t stream) {
+    using B16 = __nv_bfloat16;
+    if (a.dtype == GDN_BF16) return a.N == 8 ? bwd<B16, 8>(a, stream) : a.N == 16 ? bwd<B16, 16>(a, stream) : bwd<B16, 32>(a, stream);
+    return a.N == 8 ? bwd<float, 8>(a, stream) : a.N == 16 ? bwd<float, 16>(a, stream) : bwd<float, 32>(a, stream);
+}
+
+}  // namespace gdn

@@ -63,6 +63,12 @@ typedef enum {
 #define GDN_CAM_REVERSE 4u /* cam_scan_fwd only: the anti-causal mode        */
 #define GDN_G_PER_HEAD 8u  /* linattn_* and gdn_step: g is [H], one fixed
                               log-decay for each head                        */
+#define GDN_DT_SOFTPLUS 16u  /* ssm_*: steps are softplus(dt + dt_bias)      */
+#define GDN_SILU 32u         /* causal_conv_*: the output goes through SiLU  */
+#define GDN_GATE_FIRST 64u   /* gated_norm_*: the gate comes before the norm */
+#define GDN_GATE_SIGMOID 128u /* gated_norm_*: the gate's activation is the
+                                 sigmoid, not SiLU                           */
+#define GDN_W_SHARED 256u    /* gated_norm_*: one weight [D] for all heads   */
 
 /* Human-readable name of a status code; never NULL. */
 const char *gdn_status_string(int status);
@@ -653,6 +659,175 @@ int state_pool_free(unsigned char *live, int n_slots, const int *slots, int n, v
 size_t state_pool_compact_workspace_bytes(int n_slots);
 int state_pool_compact(void *pool, int layers, int n_slots, long long page_bytes, unsigned char *live, int *remap,
                        int *n_live, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Next to a recurrent layer's mixer: the short convolution in front of it, the
+ * selective state space scan (a mixer with a decay for each channel and state),
+ * the norm by head with its gate behind it, and the norms around a block.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * causal_conv_fwd -- the short causal convolution of each channel:
+ *     z_t = bias + sum_j weight[c,j] x_{t-W+1+j},   y = z, or z / (1 + exp(-z)) with GDN_SILU
+ *
+ *   x, y    [B,T,C] dtype, channels contiguous; y may not alias x
+ *   weight  [C,W] fp32, W 2, 3 or 4; bias [C] fp32 or NULL
+ *   initial_window / final_window [n_seq,W-1,C] dtype or NULL: the inputs before a
+ *           sequence (NULL: zeros), and the last W-1 inputs counted over both; a
+ *           sequence of no tokens passes its window on.  They may not overlap.
+ *   cu_seqlens, n_seq  as in linattn_chunk_fwd: NULL with n_seq = B, or packed
+ *           offsets with B = 1; tokens of no sequence get y = 0
+ *   strides host array of 4 element strides or NULL for contiguous tensors:
+ *           (batch, token) of x, y; not negative and multiples of 16 bytes
+ *           (GDN_ERR_MISALIGNED); y's rows lie apart (GDN_ERR_INVALID_ARG)
+ *   flags   0 or GDN_SILU
+ * C is a multiple of 8 (bf16) or 4 (fp32), n_seq and B up to 65534
+ * (GDN_ERR_UNSUPPORTED).  Arithmetic is fp32, one rounding at the end.
+ */
+int causal_conv_fwd(const void *x, const float *weight, const float *bias, const void *initial_window, void *y,
+                    void *final_window, const int *cu_seqlens, const long long *strides, int n_seq, int B, int T,
+                    int C, int W, unsigned flags, int dtype, void *stream);
+
+/*
+ * causal_conv_bwd -- backward of causal_conv_fwd: with dz = dy or dy silu'(z),
+ *     dx_t = sum_j weight[c,j] dz_{t+W-1-j},  dweight[c,j] = sum_t dz_t x_{t-W+1+j},  dbias = sum_t dz_t
+ *   dy      as y;  dfinal_window [n_seq,W-1,C] dtype or NULL (= zero): what reaches
+ *           the window that a sequence leaves
+ *   dx      [B,T,C] dtype, contiguous; dweight [C,W], dbias [C] fp32 (dbias NULL:
+ *           not wanted); dinitial_window [n_seq,W-1,C] dtype or NULL
+ *   strides 4: (batch, token) of x, dy; workspace of causal_conv_bwd_workspace_bytes
+ * Tokens of no sequence get zeros.  Every sum has a fixed order.
+ */
+size_t causal_conv_bwd_workspace_bytes(int B, int T, int C, int W);
+int causal_conv_bwd(const void *x, const float *weight, const float *bias, const void *dy, const void *initial_window,
+                    const void *dfinal_window, void *dx, float *dweight, float *dbias, void *dinitial_window,
+                    const int *cu_seqlens, const long long *strides, int n_seq, int B, int T, int C, int W,
+                    unsigned flags, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * causal_conv_step -- one token of each of B requests against a pool of windows.
+ *   x [B,C] dtype, rows x_stride elements apart (not negative, a multiple of 16
+ *   bytes); y [B,C] contiguous, not x
+ *   window, window_out [n_slots,W-1,C] dtype; window_out may be window itself
+ *   slots int32 [B] or NULL, as in linattn_step: an idle row gets y = 0
+ */
+int causal_conv_step(const void *x, const float *weight, const float *bias, const void *window, void *window_out,
+                     const int *slots, void *y, long long x_stride, int B, int C, int W, int n_slots, unsigned flags,
+                     int dtype, void *stream);
+
+/*
+ * ssm_scan_fwd -- the selective state space scan over whole prompts, a state of N
+ * numbers for each of Di channels:
+ *     D_t = softplus(dt_t + dt_bias) with GDN_DT_SOFTPLUS, dt_t + dt_bias without
+ *     h_t = exp(D_t A) h_{t-1} + D_t x_t B_t
+ *     y_t = (sum_n C_t h_t + skip x_t) z_t / (1 + exp(-z_t))
+ *
+ *   x, dt, z, y  [B,T,Di] dtype, channels contiguous; z NULL: no gate
+ *   A       [Di,N] fp32 (negative for a decay); Bt, Ct [B,T,N] dtype, for all channels
+ *   skip, dt_bias [Di] fp32 or NULL (no such term)
+ *   initial_state / final_state [n_seq,Di,N] fp32 or NULL; a sequence of no tokens
+ *           passes its state on.  They may not overlap.
+ *   cu_seqlens, n_seq  as in linattn_chunk_fwd; tokens of no sequence get y = 0
+ *   strides host array of 12 element strides or NULL: (batch, token) of x, dt, Bt,
+ *           Ct, z, y; not negative and multiples of 16 bytes; y's rows lie apart
+ *   flags   0 or GDN_DT_SOFTPLUS
+ *   workspace of ssm_scan_fwd_workspace_bytes bytes, 16-byte aligned
+ * N 8, 16 or 32; Di a multiple of 8 (bf16) or 4 (fp32); n_seq, B up to 65534.
+ * States, steps and sums are fp32.  An infinity or NaN stays in its channel and
+ * sequence (in B or C: in its sequence).
+ */
+size_t ssm_scan_fwd_workspace_bytes(int B, int T, int Di, int N, int dtype);
+int ssm_scan_fwd(const void *x, const void *dt, const float *A, const void *Bt, const void *Ct, const float *skip,
+                 const void *z, const float *dt_bias, const float *initial_state, void *y, float *final_state,
+                 const int *cu_seqlens, const long long *strides, int n_seq, int B, int T, int Di, int N,
+                 unsigned flags, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * ssm_scan_bwd -- backward of ssm_scan_fwd: the gradients of all its inputs.
+ *   dy      as y;  dfinal_state [n_seq,Di,N] fp32 or NULL (= zero)
+ *   dx, ddt, dz [B,T,Di], dB, dC [B,T,N] dtype, contiguous (dz NULL without z);
+ *           dA [Di,N], dskip, ddt_bias [Di] fp32 (the latter two NULL: not
+ *           wanted); dinitial_state [n_seq,Di,N] fp32 or NULL
+ *   strides 12: (batch, token) of x, dt, Bt, Ct, z, dy
+ * Tokens of no sequence get zeros.  Every sum has a fixed order.  The workspace
+ * holds a state every 8 tokens: Di N / 2 bytes a token.
+ */
+size_t ssm_scan_bwd_workspace_bytes(int B, int T, int Di, int N, int dtype);
+int ssm_scan_bwd(const void *x, const void *dt, const float *A, const void *Bt, const void *Ct, const float *skip,
+                 const void *z, const float *dt_bias, const float *initial_state, const void *dy,
+                 const float *dfinal_state, void *dx, void *ddt, float *dA, void *dB, void *dC, float *dskip, void *dz,
+                 float *ddt_bias, float *dinitial_state, const int *cu_seqlens, const long long *strides, int n_seq,
+                 int B, int T, int Di, int N, unsigned flags, int dtype, void *workspace, size_t workspace_bytes,
+                 void *stream);
+
+/*
+ * ssm_step -- one token of each of B requests against a pool of states.
+ *   x, dt, z [B,Di], Bt, Ct [B,N] dtype; strides: host array of 5 row strides (x,
+ *   dt, Bt, Ct, z; not negative, multiples of 16 bytes) or NULL for contiguous
+ *   tensors; y [B,Di] contiguous
+ *   state, state_out [n_slots,Di,N] fp32; state_out may be state itself
+ *   slots as in linattn_step: an idle row gets y = 0
+ */
+int ssm_step(const void *x, const void *dt, const float *A, const void *Bt, const void *Ct, const float *skip,
+             const void *z, const float *dt_bias, const float *state, float *state_out, const int *slots, void *y,
+             const long long *strides, int B, int Di, int N, int n_slots, unsigned flags, int dtype, void *stream);
+
+/*
+ * gated_norm_fwd -- the norm of each head's D columns with its gate:
+ *     y = w n(x) act(gate), n(u) = u / sqrt(mean(u^2) + eps)
+ *   or, with GDN_GATE_FIRST, y = w n(x act(gate)); act is SiLU, or the sigmoid
+ *   with GDN_GATE_SIGMOID.
+ *   x, gate [B,T,H,D] dtype, the last dimension contiguous; y contiguous
+ *   weight  [H,D], or [D] with GDN_W_SHARED, fp32; NULL: ones
+ *   strides host array of 6 element strides or NULL: (batch, token, head) of x,
+ *           gate; not negative and multiples of 16 bytes
+ * D a multiple of 8 (bf16) or 4 (fp32) up to 8192; B T H up to 2^31 - 1.
+ */
+int gated_norm_fwd(const void *x, const void *gate, const float *weight, void *y, const long long *strides, int B,
+                   int T, int H, int D, float eps, unsigned flags, int dtype, void *stream);
+
+/*
+ * gated_norm_bwd -- backward of gated_norm_fwd.
+ *   dy      [B,T,H,D] dtype; dx, dgate [B,T,H,D] dtype, dgate contiguous; dweight
+ *           as weight, fp32 (with GDN_W_SHARED the sum over the heads)
+ *   strides 12: (batch, token, head) of x, gate, dy, dx; dx's elements lie apart
+ * dweight is summed in a fixed order.
+ */
+size_t gated_norm_bwd_workspace_bytes(int B, int T, int H, int D, unsigned flags);
+int gated_norm_bwd(const void *dy, const void *x, const void *gate, const float *weight, void *dx, void *dgate,
+                   float *dweight, const long long *strides, int B, int T, int H, int D, float eps, unsigned flags,
+                   int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * block_norm_fwd -- the norm after a block, its scale, the residual's sum and the
+ * norm before the next block:
+ *     h = residual + s n(x) post_weight,  y = n(h) weight,  n(u) = u / sqrt(mean(u^2) + eps)
+ *   x, residual, y, h [rows,C] dtype, contiguous; h may be residual, y may be x
+ *   post_weight, weight [C] fp32 or NULL (ones)
+ *   scale   [groups,C] fp32: s of the rows / groups rows of each group, or NULL
+ *           with groups 0 (ones); groups divides rows
+ * h enters its norm before it is rounded.  C a multiple of 8 (bf16) or 4 (fp32)
+ * up to 8192, groups up to 65535.
+ */
+int block_norm_fwd(const void *x, const void *residual, const float *post_weight, const float *scale,
+                   const float *weight, void *y, void *h, long long rows, int C, int groups, float eps, int dtype,
+                   void *stream);
+
+/*
+ * block_norm_bwd -- backward of block_norm_fwd at the h that it wrote.
+ *   dy      [rows,C] dtype; dh [rows,C] dtype or NULL: the gradient that reaches h
+ *           past the norm
+ *   dx, dresidual [rows,C] dtype; dpost_weight, dweight [C], dscale [groups,C] fp32
+ *           (NULL: not wanted)
+ * dx may be x or dy, dresidual may be dh or h.  Sums have a fixed order.
+ */
+size_t block_norm_bwd_workspace_bytes(long long rows, int C, int groups);
+int block_norm_bwd(const void *dy, const void *dh, const void *x, const void *h, const float *post_weight,
+                   const float *scale, const float *weight, void *dx, void *dresidual, float *dpost_weight,
+                   float *dscale, float *dweight, long long rows, int C, int groups, float eps, int dtype,
+                   void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Reads and clears the device error word of the current device after
