@@ -17,6 +17,7 @@
 namespace gdn {
 namespace {
 
+using mx::F2;
 using mx::Run;
 
 // Weights [C,W] of channels c .. c+N-1.
@@ -97,60 +98,109 @@ __device__ __forceinline__ void pass_windows(const ConvArgs &a, const Strip &s, 
 
 constexpr int kThreads = 128;
 
-// N channels a thread: 16 bytes.
+// N channels of a token as pairs.
+template <typename T, int N>
+__device__ __forceinline__ void unpack2(const typename Vec<T, N>::Raw &p, F2 (&x)[N / 2]) {
+    float v[N];
+    Vec<T, N>::unpack(p, v);
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) x[e] = mx::pair(v[2 * e], v[2 * e + 1]);
+}
+template <typename T, int N>
+__device__ __forceinline__ typename Vec<T, N>::Raw pack2(const F2 (&x)[N / 2]) {
+    float v[N];
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) mx::split(x[e], v[2 * e], v[2 * e + 1]);
+    return Vec<T, N>::pack(v);
+}
+template <int N>
+__device__ __forceinline__ void pairs(const float (&v)[N], F2 (&x)[N / 2]) {
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) x[e] = mx::pair(v[2 * e], v[2 * e + 1]);
+}
+
+// N channels a thread: 16 bytes.  Tokens go in groups of U; a group inside one run
+// has no conditions.  Measured, bf16, W 4, SiLU: FWD_FIGURES
 template <typename T, int N, int W>
-__global__ void __launch_bounds__(kThreads) conv_kernel(ConvArgs a, int len, int per_row) {
+__global__ void __launch_bounds__(kThreads, 4) conv_kernel(ConvArgs a, int len, int per_row) {
     using Raw = typename Vec<T, N>::Raw;
-    constexpr int U = 4;  // tokens on their way
+    constexpr int U = 4, P = N / 2;
     Strip s;
     if (!strip_of<N>(a, len, per_row, &s)) return;
     const bool act = a.flags & GDN_SILU;
-    float w[W][N], bias[N], past[W - 1][N];
-    load_taps<N, W>(a.w, s.c, w);
+    F2 w[W][P], bias[P], past[W - 1][P];
+    {
+        float t[W][N], b[N];
+        load_taps<N, W>(a.w, s.c, t);
 #pragma unroll
-    for (int e = 0; e < N; ++e) bias[e] = a.bias ? __ldg(a.bias + s.c + e) : 0.f;
+        for (int j = 0; j < W; ++j) pairs<N>(t[j], w[j]);
+#pragma unroll
+        for (int e = 0; e < N; ++e) b[e] = a.bias ? __ldg(a.bias + s.c + e) : 0.f;
+        pairs<N>(b, bias);
+    }
     const T *x = static_cast<const T *>(a.x) + s.row * a.sx.b + s.c;
     T *y = static_cast<T *>(a.y) + s.row * a.sy.b + s.c;
     Raw next[U];
     auto fetch = [&](int t) {
+        const T *p = x + t * a.sx.t;
+        if (t + U <= s.t1) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t + u < s.t1) next[u] = __ldg(reinterpret_cast<const Raw *>(x + (t + u) * a.sx.t));
+            for (int u = 0; u < U; ++u, p += a.sx.t) next[u] = __ldg(reinterpret_cast<const Raw *>(p));
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u, p += a.sx.t)
+                if (t + u < s.t1) next[u] = __ldg(reinterpret_cast<const Raw *>(p));
+        }
     };
     fetch(s.t0);
     pass_windows<T, N>(a, s, W - 1, a.win, a.win_out);
     Run r = mx::run_at(a.cu, a.n_seq, a.T, s.row, s.t0);
-    load_past<T, N, W>(a, x, r, s.t0, s.c, past);
+    auto enter = [&](int t) {
+        float p[W - 1][N];
+        load_past<T, N, W>(a, x, r, t, s.c, p);
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) pairs<N>(p[k], past[k]);
+    };
+    enter(s.t0);
+    auto token = [&](const Raw &in, T *to) {
+        F2 v[P], z[P];
+        unpack2<T, N>(in, v);
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+            z[e] = mx::fma2(w[W - 1][e], v[e], bias[e]);
+#pragma unroll
+            for (int k = 1; k < W; ++k) z[e] = mx::fma2(w[W - 1 - k][e], past[k - 1][e], z[e]);
+            if (act) z[e] = mx::mul2(z[e], mx::sigmoid2(z[e]));
+#pragma unroll
+            for (int k = W - 1; k > 1; --k) past[k - 1][e] = past[k - 2][e];
+            past[0][e] = v[e];
+        }
+        __stcs(reinterpret_cast<Raw *>(to), r.s < 0 ? Raw{} : pack2<T, N>(z));
+    };
     for (int t = s.t0; t < s.t1; t += U) {
         Raw now[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) now[u] = next[u];
         fetch(t + U);
+        T *to = y + t * a.sy.t;
+        if (t + U <= s.t1 && t + U < r.end) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < U; ++u, to += a.sy.t) token(now[u], to);
+            continue;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u, to += a.sy.t) {
             if (t + u >= s.t1) break;
             if (t + u == r.end) {
                 r = mx::run_at(a.cu, a.n_seq, a.T, s.row, t + u);
-                load_past<T, N, W>(a, x, r, t + u, s.c, past);
+                enter(t + u);
             }
-            float v[N], z[N];
-            Vec<T, N>::unpack(now[u], v);
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                z[e] = fmaf(w[W - 1][e], v[e], bias[e]);
-#pragma unroll
-                for (int k = 1; k < W; ++k) z[e] = fmaf(w[W - 1 - k][e], past[k - 1][e], z[e]);
-                if (act) z[e] = mx::silu(z[e]);
-                if (r.s < 0) z[e] = 0.f;
-#pragma unroll
-                for (int k = W - 1; k > 1; --k) past[k - 1][e] = past[k - 2][e];
-                past[0][e] = v[e];
-            }
-            __stcs(reinterpret_cast<Raw *>(y + (t + u) * a.sy.t), Vec<T, N>::pack(z));
+            token(now[u], to);
             if (a.win_out && r.s >= 0 && t + u + 1 == r.end)
 #pragma unroll
                 for (int k = 0; k < W - 1; ++k)
-                    store<T, N>(static_cast<T *>(a.win_out) + ((size_t)r.s * (W - 1) + (W - 2 - k)) * a.C + s.c, past[k]);
+                    *reinterpret_cast<Raw *>(static_cast<T *>(a.win_out) + ((size_t)r.s * (W - 1) + (W - 2 - k)) * a.C + s.c) =
+                        pack2<T, N>(past[k]);
         }
     }
 }
@@ -158,47 +208,75 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(ConvArgs a, int len, int
 // Backward, N channels a thread: 4, as twice as many would leave too few threads
 // resident beside the taps, their gradients, the inputs and the unfinished dx.
 // A strip goes on for the W-1 tokens behind it, whose dz its last dx need; dw and
-// db count its own.  part: [strips][W+1][C].
+// db count its own.  part: [strips][W+1][C].  Tokens go in groups as forwards: the
+// conditions of a strip's and a run's ends took three times the arithmetic's
+// instructions.  Measured, bf16, W 4, SiLU: BWD_FIGURES
 template <typename T, int N, int W>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvArgs a, int len, int per_row, float *part) {
+__global__ void __launch_bounds__(kThreads, 4) conv_bwd_kernel(ConvArgs a, int len, int per_row, float *part) {
     using Raw = typename Vec<T, N>::Raw;
-    constexpr int U = 4;
+    constexpr int U = sizeof(T) == 2 ? 4 : 2, P = N / 2;
     Strip s;
     if (!strip_of<N>(a, len, per_row, &s)) return;
     const bool act = a.flags & GDN_SILU;
-    float w[W][N], bias[N], past[W - 1][N], dw[W][N], db[N];
-    float open[W - 1][N];  // dx so far of tokens t-1, t-2, ..
-    load_taps<N, W>(a.w, s.c, w);
-    zero<N>(db);
+    F2 w[W][P], bias[P], past[W - 1][P], dw[W][P], db[P];
+    F2 open[W - 1][P];  // dx so far of tokens t-1, t-2, ..
+    {
+        float t[W][N], b[N];
+        load_taps<N, W>(a.w, s.c, t);
 #pragma unroll
-    for (int e = 0; e < N; ++e) bias[e] = a.bias ? __ldg(a.bias + s.c + e) : 0.f;
+        for (int j = 0; j < W; ++j) pairs<N>(t[j], w[j]);
 #pragma unroll
-    for (int j = 0; j < W; ++j) zero<N>(dw[j]);
+        for (int e = 0; e < N; ++e) b[e] = a.bias ? __ldg(a.bias + s.c + e) : 0.f;
+        pairs<N>(b, bias);
+    }
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) zero<N>(open[j]);
+    for (int e = 0; e < P; ++e) {
+        db[e] = 0;
+#pragma unroll
+        for (int j = 0; j < W; ++j) dw[j][e] = 0;
+    }
     const T *x = static_cast<const T *>(a.x) + s.row * a.sx.b + s.c;
     const T *dy = static_cast<const T *>(a.dy) + s.row * a.sy.b + s.c;
     T *dx = static_cast<T *>(a.dx) + (size_t)s.row * a.T * a.C + s.c;
     const int stop = min(s.t1 + W - 1, a.T);
     Raw nx[U], nd[U];
     auto fetch = [&](int t) {
+        const T *p = x + t * a.sx.t, *d = dy + t * a.sy.t;
+        if (t + U <= stop) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t + u < stop) {
-                nx[u] = __ldg(reinterpret_cast<const Raw *>(x + (t + u) * a.sx.t));
-                nd[u] = __ldg(reinterpret_cast<const Raw *>(dy + (t + u) * a.sy.t));
+            for (int u = 0; u < U; ++u, p += a.sx.t, d += a.sy.t) {
+                nx[u] = __ldg(reinterpret_cast<const Raw *>(p));
+                nd[u] = __ldg(reinterpret_cast<const Raw *>(d));
             }
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u, p += a.sx.t, d += a.sy.t)
+                if (t + u < stop) {
+                    nx[u] = __ldg(reinterpret_cast<const Raw *>(p));
+                    nd[u] = __ldg(reinterpret_cast<const Raw *>(d));
+                }
+        }
     };
     fetch(s.t0);
     pass_windows<T, N>(a, s, W - 1, a.dwin_out, a.dwin);
     Run r = mx::run_at(a.cu, a.n_seq, a.T, s.row, s.t0);
-    load_past<T, N, W>(a, x, r, s.t0, s.c, past);
+    auto enter = [&](int t) {
+        float p[W - 1][N];
+        load_past<T, N, W>(a, x, r, t, s.c, p);
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+            pairs<N>(p[k], past[k]);
+#pragma unroll
+            for (int e = 0; e < P; ++e) open[k][e] = 0;
+        }
+    };
+    enter(s.t0);
     // dx of token t of run r, or of its window's row
-    auto put = [&](int t, const float (&g)[N]) {
+    auto put = [&](int t, const F2 (&g)[P]) {
         if (t >= r.start) {
-            if (t >= s.t0 && t < s.t1) __stcs(reinterpret_cast<Raw *>(dx + (size_t)t * a.C), Vec<T, N>::pack(g));
+            if (t >= s.t0 && t < s.t1) __stcs(reinterpret_cast<Raw *>(dx + (size_t)t * a.C), pack2<T, N>(g));
         } else if (a.dwin && r.start >= s.t0 && r.start < s.t1) {
-            store<T, N>(static_cast<T *>(a.dwin) + ((size_t)r.s * (W - 1) + (W - 1 + t - r.start)) * a.C + s.c, g);
+            *reinterpret_cast<Raw *>(static_cast<T *>(a.dwin) + ((size_t)r.s * (W - 1) + (W - 1 + t - r.start)) * a.C + s.c) = pack2<T, N>(g);
         }
     };
     // what the run's last W-1 inputs get, where it ends before token t
@@ -207,12 +285,41 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvArgs a, int len,
 #pragma unroll
         for (int k = 1; k < W; ++k) {
             if (a.dwin_out) {
-                float g[N];
-                load<T, N>(static_cast<const T *>(a.dwin_out) + ((size_t)r.s * (W - 1) + (W - 1 - k)) * a.C + s.c, g);
+                F2 g[P];
+                unpack2<T, N>(*reinterpret_cast<const Raw *>(static_cast<const T *>(a.dwin_out) +
+                                                             ((size_t)r.s * (W - 1) + (W - 1 - k)) * a.C + s.c), g);
 #pragma unroll
-                for (int e = 0; e < N; ++e) open[k - 1][e] += g[e];
+                for (int e = 0; e < P; ++e) open[k - 1][e] = mx::add2(open[k - 1][e], g[e]);
             }
             put(t - k, open[k - 1]);
+        }
+    };
+    // one token: `last` is what dx of the token W-1 before has got in all; `own`: dw and db count it
+    auto token = [&](const Raw &in, const Raw &grad, bool own, F2 (&last)[P]) {
+        F2 v[P], g[P];
+        unpack2<T, N>(in, v);
+        unpack2<T, N>(grad, g);
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+            if (act) {
+                F2 z = mx::fma2(w[W - 1][e], v[e], bias[e]);
+#pragma unroll
+                for (int k = 1; k < W; ++k) z = mx::fma2(w[W - 1 - k][e], past[k - 1][e], z);
+                g[e] = mx::mul2(g[e], mx::silu_slope2(z, mx::sigmoid2(z)));
+            }
+            if (own) {
+                db[e] = mx::add2(db[e], g[e]);
+                dw[W - 1][e] = mx::fma2(g[e], v[e], dw[W - 1][e]);
+#pragma unroll
+                for (int k = 1; k < W; ++k) dw[W - 1 - k][e] = mx::fma2(g[e], past[k - 1][e], dw[W - 1 - k][e]);
+            }
+            last[e] = mx::fma2(w[0][e], g[e], open[W - 2][e]);
+#pragma unroll
+            for (int k = W - 1; k > 1; --k) open[k - 1][e] = mx::fma2(w[W - k][e], g[e], open[k - 2][e]);
+            open[0][e] = mx::mul2(w[W - 1][e], g[e]);
+#pragma unroll
+            for (int k = W - 1; k > 1; --k) past[k - 1][e] = past[k - 2][e];
+            past[0][e] = v[e];
         }
     };
     bool done = false;
@@ -221,10 +328,22 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvArgs a, int len,
 #pragma unroll
         for (int u = 0; u < U; ++u) cx[u] = nx[u], cd[u] = nd[u];
         fetch(t + U);
+        if (r.s >= 0 && t - (W - 1) >= max(r.start, s.t0) && t + U <= min(r.end, s.t1) && t < r.end) {
+            T *to = dx + (size_t)(t - (W - 1)) * a.C;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = t + u;
-            if (i >= stop || done) break;
+            for (int u = 0; u < U; ++u, to += a.C) {
+                F2 last[P];
+                token(cx[u], cd[u], true, last);
+                __stcs(reinterpret_cast<Raw *>(to), pack2<T, N>(last));
+            }
+            continue;
+        }
+#pragma unroll 1
+        for (int i = t; i < t + U; ++i) {
+            if (i >= stop) break;
+            const Raw vx = cx[0], vd = cd[0];
+#pragma unroll
+            for (int u = 0; u + 1 < U; ++u) cx[u] = cx[u + 1], cd[u] = cd[u + 1];
             if (i == r.end) {
                 close(i);
                 if (i >= s.t1) {
@@ -232,48 +351,22 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvArgs a, int len,
                     break;
                 }
                 r = mx::run_at(a.cu, a.n_seq, a.T, s.row, i);
-                load_past<T, N, W>(a, x, r, i, s.c, past);
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) zero<N>(open[j]);
+                enter(i);
             }
             if (r.s < 0) {
                 if (i < s.t1) __stcs(reinterpret_cast<Raw *>(dx + (size_t)i * a.C), Raw{});
                 continue;
             }
-            float v[N], g[N], last[N];
-            Vec<T, N>::unpack(cx[u], v);
-            Vec<T, N>::unpack(cd[u], g);
-            const float count = i < s.t1 ? 1.f : 0.f;
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                if (act) {
-                    float z = fmaf(w[W - 1][e], v[e], bias[e]);
-#pragma unroll
-                    for (int k = 1; k < W; ++k) z = fmaf(w[W - 1 - k][e], past[k - 1][e], z);
-                    g[e] *= mx::silu_slope(z, mx::sigmoid(z));
-                }
-                if (i < s.t1) {
-                    db[e] += g[e];
-                    dw[W - 1][e] = fmaf(g[e], v[e], dw[W - 1][e]);
-#pragma unroll
-                    for (int k = 1; k < W; ++k) dw[W - 1 - k][e] = fmaf(g[e], past[k - 1][e], dw[W - 1 - k][e]);
-                }
-                last[e] = fmaf(w[0][e], g[e], open[W - 2][e]);
-#pragma unroll
-                for (int k = W - 1; k > 1; --k) open[k - 1][e] = fmaf(w[W - k][e], g[e], open[k - 2][e]);
-                open[0][e] = w[W - 1][e] * g[e];
-#pragma unroll
-                for (int k = W - 1; k > 1; --k) past[k - 1][e] = past[k - 2][e];
-                past[0][e] = v[e];
-            }
+            F2 last[P];
+            token(vx, vd, i < s.t1, last);
             put(i - (W - 1), last);
         }
     }
-    if (!done && stop == a.T && (r.end == a.T || r.s >= 0)) close(a.T);
+    if (!done && stop == a.T) close(a.T);
     float *to = part + (size_t)s.index * (W + 1) * a.C + s.c;
 #pragma unroll
-    for (int j = 0; j < W; ++j) store<float, N>(to + (size_t)j * a.C, dw[j]);
-    store<float, N>(to + (size_t)W * a.C, db);
+    for (int j = 0; j < W; ++j) *reinterpret_cast<typename Vec<float, N>::Raw *>(to + (size_t)j * a.C) = pack2<float, N>(dw[j]);
+    *reinterpret_cast<typename Vec<float, N>::Raw *>(to + (size_t)W * a.C) = pack2<float, N>(db);
 }
 
 // dw [C,W] and db [C] from the strips' shares [n][W+1][C], in order: 32 places a
@@ -297,40 +390,69 @@ __global__ void __launch_bounds__(1024) conv_sum_kernel(const float *part, float
     else if (db) db[c] = x;
 }
 
-// One token a row: the window's rows are read, shifted and written.
-template <typename T, int N, int W>
+// One token a row: the window's rows are read, shifted and written.  R rows a
+// thread, whose taps are read once: with one, the taps were half of what the call
+// read.  STEP_FIGURES
+template <typename T, int N, int W, int R>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepArgs a) {
-    const int nv = a.C / N;
+    using Raw = typename Vec<T, N>::Raw;
+    constexpr int P = N / 2;
+    const int nv = a.C / N, groups = (a.B + R - 1) / R;
     const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const int b = (int)(i / nv);
-    if (b >= a.B) return;
-    const int c = (int)(i - (long long)b * nv) * N;
-    T *y = static_cast<T *>(a.y) + (size_t)b * a.C + c;
-    const int slot = a.slots ? a.slots[b] : b;
-    float z[N];
-    if (slot < 0 || slot >= a.n_slots) {  // an idle row
-        zero<N>(z);
-        store<T, N>(y, z);
-        return;
+    const int b0 = (int)(i / nv);  // rows b0, b0 + groups, ..
+    if (b0 >= groups) return;
+    const int c = (int)(i - (long long)b0 * nv) * N;
+    Raw x[R], past[R][W - 1];
+    int slot[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        const int b = b0 + q * groups;
+        slot[q] = b >= a.B ? -1 : a.slots ? __ldg(a.slots + b) : b;
+        if (slot[q] >= a.n_slots) slot[q] = -1;
     }
-    float v[N], past[W - 1][N], w[W][N];
-    const size_t page = (size_t)slot * (W - 1) * a.C + c;
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) load<T, N>(static_cast<const T *>(a.win) + page + (size_t)k * a.C, past[k]);
-    load<T, N>(static_cast<const T *>(a.x) + b * a.sx + c, v);
-    load_taps<N, W>(a.w, c, w);
+    for (int q = 0; q < R; ++q)
+        if (slot[q] >= 0) {
+            const T *page = static_cast<const T *>(a.win) + (size_t)slot[q] * (W - 1) * a.C + c;
+            x[q] = __ldg(reinterpret_cast<const Raw *>(static_cast<const T *>(a.x) + (b0 + q * groups) * a.sx + c));
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-        z[e] = fmaf(w[W - 1][e], v[e], a.bias ? __ldg(a.bias + c + e) : 0.f);
+            for (int k = 0; k < W - 1; ++k) past[q][k] = __ldcs(reinterpret_cast<const Raw *>(page + (size_t)k * a.C));
+        }
+    float taps[W][N], bs[N];
+    F2 w[W][P], bias[P];
+    load_taps<N, W>(a.w, c, taps);
 #pragma unroll
-        for (int k = W - 2; k >= 0; --k) z[e] = fmaf(w[k][e], past[k][e], z[e]);
-        if (a.flags & GDN_SILU) z[e] = mx::silu(z[e]);
+    for (int j = 0; j < W; ++j) pairs<N>(taps[j], w[j]);
+#pragma unroll
+    for (int e = 0; e < N; ++e) bs[e] = a.bias ? __ldg(a.bias + c + e) : 0.f;
+    pairs<N>(bs, bias);
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        const int b = b0 + q * groups;
+        if (b >= a.B) break;
+        Raw out{};
+        if (slot[q] >= 0) {
+            F2 v[P], z[P];
+            unpack2<T, N>(x[q], v);
+#pragma unroll
+            for (int e = 0; e < P; ++e) z[e] = mx::fma2(w[W - 1][e], v[e], bias[e]);
+#pragma unroll
+            for (int k = W - 2; k >= 0; --k) {
+                unpack2<T, N>(past[q][k], v);
+#pragma unroll
+                for (int e = 0; e < P; ++e) z[e] = mx::fma2(w[k][e], v[e], z[e]);
+            }
+            if (a.flags & GDN_SILU)
+#pragma unroll
+                for (int e = 0; e < P; ++e) z[e] = mx::mul2(z[e], mx::sigmoid2(z[e]));
+            out = pack2<T, N>(z);
+            T *page = static_cast<T *>(a.win_out) + (size_t)slot[q] * (W - 1) * a.C + c;
+#pragma unroll
+            for (int k = 1; k < W - 1; ++k) __stcs(reinterpret_cast<Raw *>(page + (size_t)(k - 1) * a.C), past[q][k]);
+            __stcs(reinterpret_cast<Raw *>(page + (size_t)(W - 2) * a.C), x[q]);
+        }
+        __stcs(reinterpret_cast<Raw *>(static_cast<T *>(a.y) + (size_t)b * a.C + c), out);  // 0 for an idle row
     }
-    T *out = static_cast<T *>(a.win_out) + page;
-#pragma unroll
-    for (int k = 1; k < W - 1; ++k) store<T, N>(out + (size_t)(k - 1) * a.C, past[k]);
-    store<T, N>(out + (size_t)(W - 2) * a.C, v);
-    store<T, N>(y, z);
 }
 
 // Strips of a row: as many as fill `threads`, of at least 8 tokens.
@@ -358,7 +480,7 @@ int fwd(const ConvArgs &a, cudaStream_t stream) {
 
 // The shares of dw that a backward makes: at most this many strips, or a strip a row.
 constexpr int kMostStrips = 2048;
-constexpr long long kBwdThreads = 152 * 640;
+constexpr long long kBwdThreads = 152 * 4 * kThreads;  // resident at once
 Cut bwd_cut(int B, int T, int C) { return cut_rows(B, T, C / 4, kBwdThreads, kMostStrips); }
 
 template <typename T, int W>
@@ -376,8 +498,14 @@ int bwd(const ConvArgs &a, cudaStream_t stream) {
 
 template <typename T, int N, int W>
 int step(const ConvStepArgs &a, cudaStream_t stream) {
-    const long long threads = (long long)(a.C / N) * a.B;
-    conv_step_kernel<T, N, W><<<(unsigned)((threads + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a);
+    const long long vectors = (long long)(a.C / N) * a.B;
+    // four rows a thread where that leaves each SM two CTAs
+    if (vectors >= 4LL * 2 * kThreads * device_sm_count()) {
+        const long long threads = (long long)(a.C / N) * ((a.B + 3) / 4);
+        conv_step_kernel<T, N, W, 4><<<(unsigned)((threads + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a);
+    } else {
+        conv_step_kernel<T, N, W, 1><<<(unsigned)((vectors + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a);
+    }
     return mx::launched();
 }
 

@@ -48,8 +48,14 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// 1 / (1 + exp(-x)).  Where exp(-x) is infinite the quotient is 0.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + exp2_fast(-kLog2e * x)); }
+__device__ __forceinline__ float inverse(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / (1 + exp(-x)); 0 where exp(-x) is infinite.
+__device__ __forceinline__ float sigmoid(float x) { return inverse(1.f + exp2_fast(-kLog2e * x)); }
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 // silu'(x) from sigmoid(x).
 __device__ __forceinline__ float silu_slope(float x, float s) { return s * fmaf(x, 1.f - s, 1.f); }
@@ -74,6 +80,45 @@ __device__ __forceinline__ float softplus(float v) {
     return fmaf(e, log1p_over(e), fmaxf(v, 0.f));
 }
 
+// Two fp32 numbers for one instruction: half the issue slots of single ones at
+// the same rate of operations.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pair(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ F2 both(float x) { return pair(x, x); }
+__device__ __forceinline__ void split(F2 p, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float sum(F2 p) {
+    float a, b;
+    split(p, a, b);
+    return a + b;
+}
+
+// The activations of two at once: the exponentials and reciprocals are single.
+__device__ __forceinline__ F2 sigmoid2(F2 x) {
+    float a, b;
+    split(mul2(x, both(-kLog2e)), a, b);
+    split(add2(pair(exp2_fast(a), exp2_fast(b)), both(1.f)), a, b);
+    return pair(inverse(a), inverse(b));
+}
+__device__ __forceinline__ F2 silu_slope2(F2 x, F2 s) { return mul2(s, fma2(x, fma2(s, both(-1.f), both(1.f)), both(1.f))); }
 // A grid of as many CTAs as the SMs hold at once.
 template <auto F, int NT>
 int resident_ctas() {

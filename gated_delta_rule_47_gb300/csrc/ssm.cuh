@@ -18,36 +18,13 @@
 namespace gdn {
 namespace ssm {
 
-// Two fp32 numbers for one instruction: half the issue slots of single ones at
-// the same rate of operations.
-using F2 = unsigned long long;
-__device__ __forceinline__ F2 pair(float lo, float hi) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ F2 both(float x) { return pair(x, x); }
-__device__ __forceinline__ void split(F2 p, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float sum(F2 p) {
-    float a, b;
-    split(p, a, b);
-    return a + b;
-}
+using mx::F2;
+using mx::both;
+using mx::fma2;
+using mx::mul2;
+using mx::pair;
+using mx::split;
+using mx::sum;
 // 2^x of both.
 __device__ __forceinline__ F2 exp2_2(F2 x) {
     float a, b;

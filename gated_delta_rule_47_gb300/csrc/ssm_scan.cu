@@ -1,7 +1,7 @@
 // ssm_scan.cu -- the selective state space scan over prompts (ssm.cuh), and its
 // single token.
 //
-// A thread holds all N states of its channels (32 states), a warp a block of
+// A thread holds all N states of its channels, a warp a block of
 // consecutive channels; B and C of a token are the same for all of them and come
 // from shared memory, where the warp has put a tile of tokens in fp32.  Warps do
 // not wait for one another.  Exponentials bound it: one instruction of 32 a clock
@@ -21,20 +21,24 @@ using mx::Run;
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTile = 16;  // tokens of B and C in shared memory
 constexpr int kGroup = 4;  // tokens of x, dt and z on their way
+constexpr int kStates = 32, kCtas = 3;
 
 // How a row is cut.
 struct Plan {
     int len, chunks;  // tokens of a chunk, a multiple of kTile; chunks of a row
     int blocks;       // of channels
-    float *state;     // [row][chunk][block][8][32] float4: the state that the chunk leaves from 0
+    float *state;     // [row][chunk][block][V][32] float4: the state that the chunk leaves from 0
     float *steps;     // [row][chunk][block][CH][32]: the sum of its steps
+    bool joined;      // join_kernel has put in `state` what each chunk leaves with all before it
 };
 
 template <int N>
 struct Shape {
-    static constexpr int CH = 32 / N;           // channels a thread
-    static constexpr int P = N / 2;             // pairs of states a channel
-    static constexpr int BLOCK = 32 * CH;       // channels a warp
+    static constexpr int CH = N >= kStates ? 1 : kStates / N;  // channels a thread
+    static constexpr int P = N / 2;                            // pairs of states a channel
+    static constexpr int V = CH * N / 4;                       // vectors of 4 states a thread
+    static constexpr int BLOCK = 32 * CH;                      // channels a warp
+    static constexpr int CTAS = CH * N == 32 ? 3 : kCtas;      // of an SM
 };
 
 // A warp's tile of B (and C): [token][N] fp32, C behind B.
@@ -77,11 +81,17 @@ struct Tile {
 // The steps D of a token's channels from dt as loaded.
 template <int CH>
 __device__ __forceinline__ void steps_of(const float (&dt)[CH], const float (&bias)[CH], bool soft, float (&step)[CH]) {
+    // one by one: an immediate constant is free there, a pair of them is not
 #pragma unroll
     for (int e = 0; e < CH; ++e) {
         const float v = dt[e] + bias[e];
         step[e] = soft ? mx::softplus(v) : v;
     }
+}
+template <int CH>
+__device__ __forceinline__ void gate(const float (&z)[CH], float (&g)[CH]) {
+#pragma unroll
+    for (int e = 0; e < CH; ++e) g[e] = mx::silu(z[e]);
 }
 
 // h <- exp(D A) h + D x B of a token; `bc` points at its B (and C behind), the
@@ -89,9 +99,9 @@ __device__ __forceinline__ void steps_of(const float (&dt)[CH], const float (&bi
 template <int N, int CH, bool OUT>
 __device__ __forceinline__ void advance(F2 (&h)[CH][N / 2], const F2 (&A)[CH][N / 2], const float (&step)[CH], const float (&x)[CH],
                                         const float *bc, float (&y)[CH]) {
-    F2 d[CH], u[CH], acc[CH];
+    F2 d[CH], u[CH], acc[2][CH];
 #pragma unroll
-    for (int e = 0; e < CH; ++e) d[e] = both(step[e]), u[e] = both(step[e] * x[e]), acc[e] = 0;
+    for (int e = 0; e < CH; ++e) d[e] = both(step[e]), u[e] = both(step[e] * x[e]), acc[0][e] = acc[1][e] = 0;
 #pragma unroll
     for (int n = 0; n < N / 2; n += 2) {
         const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(bc + 2 * n);
@@ -103,12 +113,12 @@ __device__ __forceinline__ void advance(F2 (&h)[CH][N / 2], const F2 (&A)[CH][N 
             for (int e = 0; e < CH; ++e) {
                 F2 &s = h[e][n + m];
                 s = fma2(exp2_2(mul2(d[e], A[e][n + m])), s, mul2(u[e], m ? b.y : b.x));
-                if (OUT) acc[e] = fma2(m ? c.y : c.x, s, acc[e]);
+                if (OUT) acc[m][e] = fma2(m ? c.y : c.x, s, acc[m][e]);
             }
     }
     if (OUT)
 #pragma unroll
-        for (int e = 0; e < CH; ++e) y[e] = sum(acc[e]);
+        for (int e = 0; e < CH; ++e) y[e] = sum(mx::add2(acc[0][e], acc[1][e]));
 }
 
 // A thread's states [Di,N] from or to memory, 0 where there are none.
@@ -165,7 +175,7 @@ __device__ __forceinline__ size_t share_at(const Plan &p, int row, int chunk, in
 // What a chunk leaves: from 0, or from the state of a sequence that starts in it
 // and goes on behind it.
 template <typename T, int N>
-__global__ void __launch_bounds__(kThreads, 4) share_kernel(SsmArgs a, Plan p) {
+__global__ void __launch_bounds__(kThreads, Shape<N>::CTAS) share_kernel(SsmArgs a, Plan p) {
     constexpr int CH = Shape<N>::CH, P = Shape<N>::P;
     using Raw = typename Vec<T, CH>::Raw;
     __shared__ __align__(16) float tiles[kWarps][kTile * N];
@@ -187,12 +197,23 @@ __global__ void __launch_bounds__(kThreads, 4) share_kernel(SsmArgs a, Plan p) {
     const T *B = static_cast<const T *>(a.Bt) + w.row * a.sB.b;
     Raw nx[kGroup], nt[kGroup];
     auto fetch = [&](int t) {
+        const T *px = x + t * a.sx.t, *pt = dt + t * a.sdt.t;
+        const bool whole = t + kGroup <= w.t1;
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u)
-            if (t + u < w.t1) {
-                nx[u] = __ldg(reinterpret_cast<const Raw *>(x + (t + u) * a.sx.t));
-                nt[u] = __ldg(reinterpret_cast<const Raw *>(dt + (t + u) * a.sdt.t));
-            }
+        for (int u = 0; u < kGroup; ++u, px += a.sx.t, pt += a.sdt.t)
+            if (whole || t + u < w.t1) nx[u] = __ldg(reinterpret_cast<const Raw *>(px)), nt[u] = __ldg(reinterpret_cast<const Raw *>(pt));
+    };
+    auto step_of = [&](const Raw &vt, float (&step)[CH]) {
+        float dv[CH];
+        Vec<T, CH>::unpack(vt, dv);
+        steps_of<CH>(dv, bias, soft, step);
+    };
+    auto token = [&](const Raw &vx, const float (&step)[CH], const float *b) {
+        float xv[CH], none[CH];
+        Vec<T, CH>::unpack(vx, xv);
+#pragma unroll
+        for (int e = 0; e < CH; ++e) total[e] += step[e];
+        advance<N, CH, false>(h, A, step, xv, b, none);
     };
     Tile<T, N, false> next;
     next.fetch(a, B, nullptr, ts, w.t1);
@@ -208,32 +229,74 @@ __global__ void __launch_bounds__(kThreads, 4) share_kernel(SsmArgs a, Plan p) {
 #pragma unroll
             for (int u = 0; u < kGroup; ++u) cx[u] = nx[u], ct[u] = nt[u];
             fetch(t + g + kGroup);
+            const float *b = tile + g * N;
+            if (t + g + kGroup <= w.t1) {
+                float step[kGroup][CH];  // their chains side by side
 #pragma unroll
-            for (int u = 0; u < kGroup; ++u) {
-                if (t + g + u >= w.t1) break;
-                float xv[CH], dv[CH], step[CH], none[CH];
-                Vec<T, CH>::unpack(cx[u], xv);
-                Vec<T, CH>::unpack(ct[u], dv);
-                steps_of<CH>(dv, bias, soft, step);
+                for (int u = 0; u < kGroup; ++u) step_of(ct[u], step[u]);
 #pragma unroll
-                for (int e = 0; e < CH; ++e) total[e] += step[e];
-                advance<N, CH, false>(h, A, step, xv, tile + (g + u) * N, none);
+                for (int u = 0; u < kGroup; ++u) token(cx[u], step[u], b + u * N);
+            } else {  // the chunk's last tokens
+#pragma unroll 1
+                for (int i = t + g; i < w.t1; ++i, b += N) {
+                    float step[CH];
+                    step_of(ct[0], step);
+                    token(cx[0], step, b);
+#pragma unroll
+                    for (int u = 0; u + 1 < kGroup; ++u) cx[u] = cx[u + 1], ct[u] = ct[u + 1];
+                }
             }
         }
     }
     const size_t at = share_at(p, w.row, w.chunk, w.block);
     const int lane = threadIdx.x & 31;
-    float4 *to = reinterpret_cast<float4 *>(p.state) + at * 8 * 32 + lane;
+    float4 *to = reinterpret_cast<float4 *>(p.state) + at * Shape<N>::V * 32 + lane;
     const F2 *hs = &h[0][0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) *reinterpret_cast<ulonglong2 *>(to + i * 32) = make_ulonglong2(hs[2 * i], hs[2 * i + 1]);
+    for (int i = 0; i < Shape<N>::V; ++i) *reinterpret_cast<ulonglong2 *>(to + i * 32) = make_ulonglong2(hs[2 * i], hs[2 * i + 1]);
 #pragma unroll
     for (int e = 0; e < CH; ++e) p.steps[(at * CH + e) * 32 + lane] = total[e];
 }
 
-template <typename T, int N>
-__global__ void __launch_bounds__(kThreads, 3) scan_kernel(SsmArgs a, Plan p) {
-    constexpr int CH = Shape<N>::CH, P = Shape<N>::P;
+// What the chunks of a row leave, each with those before it of its sequence, in
+// place: a thread 4 of a block's states, the next chunks' loads on their way.  A
+// warp that joins all chunks before its own takes the latency of each.
+template <int N>
+__global__ void __launch_bounds__(32 * Shape<N>::V) join_kernel(SsmArgs a, Plan p) {
+    constexpr int CH = Shape<N>::CH, P = Shape<N>::P, V = Shape<N>::V, AHEAD = 8;
+    const int row = blockIdx.x / p.blocks, block = blockIdx.x - row * p.blocks;
+    const int lane = threadIdx.x & 31, i = threadIdx.x >> 5, e = 2 * i / P, n = 2 * i % P * 2;  // vector i of the lane's
+    const int c = block * Shape<N>::BLOCK + lane * CH + e;
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < a.Di) A = __ldg(reinterpret_cast<const float4 *>(a.A + (size_t)c * N + n));
+    const F2 A0 = mul2(pair(A.x, A.y), both(mx::kLog2e)), A1 = mul2(pair(A.z, A.w), both(mx::kLog2e));
+    ulonglong2 *state = reinterpret_cast<ulonglong2 *>(p.state) + i * 32 + lane;
+    const float *steps = p.steps + e * 32 + lane;
+    F2 h0 = 0, h1 = 0;
+    for (int j0 = 0; j0 + 1 < p.chunks; j0 += AHEAD) {
+        ulonglong2 v[AHEAD];
+        float d[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (j0 + k + 1 < p.chunks) {
+                const size_t at = share_at(p, row, j0 + k, block);
+                v[k] = state[at * V * 32], d[k] = steps[at * CH * 32];
+            }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int j = j0 + k;
+            if (j + 1 >= p.chunks) break;
+            const Run r = mx::run_at(a.cu, a.n_seq, a.T, row, min((j + 1) * p.len, a.T) - 1);
+            if (r.start >= j * p.len) h0 = v[k].x, h1 = v[k].y;
+            else h0 = fma2(exp2_2(mul2(both(d[k]), A0)), h0, v[k].x), h1 = fma2(exp2_2(mul2(both(d[k]), A1)), h1, v[k].y);
+            state[share_at(p, row, j, block) * V * 32] = make_ulonglong2(h0, h1);
+        }
+    }
+}
+
+template <typename T, int N, bool GATE>
+__global__ void __launch_bounds__(kThreads, Shape<N>::CTAS) scan_kernel(SsmArgs a, Plan p) {
+    constexpr int CH = Shape<N>::CH, P = Shape<N>::P, V = Shape<N>::V;
     using Raw = typename Vec<T, CH>::Raw;
     __shared__ __align__(16) float tiles[kWarps][kTile * 2 * N];
     Place w;
@@ -244,17 +307,18 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(SsmArgs a, Plan p) {
     const int c = w.there ? w.c : 0;
     const size_t page = (size_t)a.Di * N;
     const T *x = static_cast<const T *>(a.x) + w.row * a.sx.b + c, *dt = static_cast<const T *>(a.dt) + w.row * a.sdt.b + c;
-    const T *z = a.z ? static_cast<const T *>(a.z) + w.row * a.sz.b + c : nullptr;
+    const T *z = GATE ? static_cast<const T *>(a.z) + w.row * a.sz.b + c : nullptr;
     const T *B = static_cast<const T *>(a.Bt) + w.row * a.sB.b, *C = static_cast<const T *>(a.Ct) + w.row * a.sC.b;
     T *y = static_cast<T *>(a.y) + w.row * a.sy.b + c;
     Raw nx[kGroup], nt[kGroup], nz[kGroup];
     auto fetch = [&](int t) {
+        const T *px = x + t * a.sx.t, *pt = dt + t * a.sdt.t, *pz = z + t * a.sz.t;
+        const bool whole = t + kGroup <= w.t1;
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u)
-            if (t + u < w.t1) {
-                nx[u] = __ldg(reinterpret_cast<const Raw *>(x + (t + u) * a.sx.t));
-                nt[u] = __ldg(reinterpret_cast<const Raw *>(dt + (t + u) * a.sdt.t));
-                if (z) nz[u] = __ldg(reinterpret_cast<const Raw *>(z + (t + u) * a.sz.t));
+        for (int u = 0; u < kGroup; ++u, px += a.sx.t, pt += a.sdt.t, pz += a.sz.t)
+            if (whole || t + u < w.t1) {
+                nx[u] = __ldg(reinterpret_cast<const Raw *>(px)), nt[u] = __ldg(reinterpret_cast<const Raw *>(pt));
+                if (GATE) nz[u] = __ldg(reinterpret_cast<const Raw *>(pz));
             }
     };
     Tile<T, N, true> next;
@@ -284,23 +348,54 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(SsmArgs a, Plan p) {
     auto enter = [&](bool fresh) { load_states<N, CH>(fresh && r.s >= 0 && a.s0 && w.there ? a.s0 + r.s * page : nullptr, c, h); };
     enter(r.start == w.t0);
     if (r.s >= 0 && r.start < w.t0) {  // what the chunks before this one leave
-        const int first = min(r.start / p.len, w.chunk - 1);
-        for (int j = first; j < w.chunk; ++j) {
-            const size_t at = share_at(p, w.row, j, w.block);
-            const ulonglong2 *from = reinterpret_cast<const ulonglong2 *>(p.state) + at * 8 * 32 + lane;
-            F2 d[CH];
-#pragma unroll
-            for (int e = 0; e < CH; ++e) d[e] = both(p.steps[(at * CH + e) * 32 + lane]);
+        if (p.joined) {
+            const ulonglong2 *from = reinterpret_cast<const ulonglong2 *>(p.state) + share_at(p, w.row, w.chunk - 1, w.block) * V * 32 + lane;
             F2 *hs = &h[0][0];
-            const F2 *As = &A[0][0];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < V; ++i) {
                 const ulonglong2 v = from[i * 32];
-                hs[2 * i] = j == first ? v.x : fma2(exp2_2(mul2(d[2 * i / P], As[2 * i])), hs[2 * i], v.x);
-                hs[2 * i + 1] = j == first ? v.y : fma2(exp2_2(mul2(d[(2 * i + 1) / P], As[2 * i + 1])), hs[2 * i + 1], v.y);
+                hs[2 * i] = v.x, hs[2 * i + 1] = v.y;
+            }
+        } else {
+            const int first = min(r.start / p.len, w.chunk - 1);
+            for (int j = first; j < w.chunk; ++j) {
+                const size_t at = share_at(p, w.row, j, w.block);
+                const ulonglong2 *from = reinterpret_cast<const ulonglong2 *>(p.state) + at * V * 32 + lane;
+                F2 d[CH];
+#pragma unroll
+                for (int e = 0; e < CH; ++e) d[e] = both(p.steps[(at * CH + e) * 32 + lane]);
+                F2 *hs = &h[0][0];
+                const F2 *As = &A[0][0];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const ulonglong2 v = from[i * 32];
+                    hs[2 * i] = j == first ? v.x : fma2(exp2_2(mul2(d[2 * i / P], As[2 * i])), hs[2 * i], v.x);
+                    hs[2 * i + 1] = j == first ? v.y : fma2(exp2_2(mul2(d[(2 * i + 1) / P], As[2 * i + 1])), hs[2 * i + 1], v.y);
+                }
             }
         }
     }
+    auto factors_of = [&](const Raw &vt, const Raw &vz, float (&step)[CH], float (&g)[CH]) {
+        float dv[CH];
+        Vec<T, CH>::unpack(vt, dv);
+        steps_of<CH>(dv, bias, soft, step);
+        if (GATE) {
+            float zv[CH];
+            Vec<T, CH>::unpack(vz, zv);
+            gate<CH>(zv, g);
+        }
+    };
+    auto token = [&](const Raw &vx, const float (&step)[CH], const float (&g)[CH], const float *bc, T *to) {
+        float xv[CH], out[CH];
+        Vec<T, CH>::unpack(vx, xv);
+        advance<N, CH, true>(h, A, step, xv, bc, out);
+#pragma unroll
+        for (int e = 0; e < CH; ++e) {
+            out[e] = fmaf(skip[e], xv[e], out[e]);
+            if (GATE) out[e] *= g[e];
+        }
+        if (w.there) __stcs(reinterpret_cast<Raw *>(to), r.s < 0 ? Raw{} : Vec<T, CH>::pack(out));
+    };
     for (int t = w.t0; t < w.t1; t += kTile) {
         __syncwarp();
         next.put(tile);
@@ -312,32 +407,28 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(SsmArgs a, Plan p) {
 #pragma unroll
             for (int u = 0; u < kGroup; ++u) cx[u] = nx[u], ct[u] = nt[u], cz[u] = nz[u];
             fetch(t + g + kGroup);
+            const float *bc = tile + g * 2 * N;
+            T *to = y + (t + g) * a.sy.t;
+            if (t + g + kGroup <= w.t1 && t + g + kGroup <= r.end && t + g < r.end) {
+                float step[kGroup][CH], g[kGroup][CH];  // their chains side by side
 #pragma unroll
-            for (int u = 0; u < kGroup; ++u) {
-                const int i = t + g + u;
-                if (i >= w.t1) break;
-                if (i == r.end) {
-                    if (a.sf && r.s >= 0 && w.there) store_states<N, CH>(a.sf + r.s * page, c, h);
-                    r = mx::run_at(a.cu, a.n_seq, a.T, w.row, i);
-                    enter(true);
+                for (int u = 0; u < kGroup; ++u) factors_of(ct[u], cz[u], step[u], g[u]);
+#pragma unroll
+                for (int u = 0; u < kGroup; ++u, to += a.sy.t) token(cx[u], step[u], g[u], bc + u * 2 * N, to);
+            } else {
+#pragma unroll 1
+                for (int i = t + g; i < w.t1 && i < t + g + kGroup; ++i, bc += 2 * N, to += a.sy.t) {
+                    if (i == r.end) {
+                        if (a.sf && r.s >= 0 && w.there) store_states<N, CH>(a.sf + r.s * page, c, h);
+                        r = mx::run_at(a.cu, a.n_seq, a.T, w.row, i);
+                        enter(true);
+                    }
+                    float step[CH], g[CH];
+                    factors_of(ct[0], cz[0], step, g);
+                    token(cx[0], step, g, bc, to);
+#pragma unroll
+                    for (int u = 0; u + 1 < kGroup; ++u) cx[u] = cx[u + 1], ct[u] = ct[u + 1], cz[u] = cz[u + 1];
                 }
-                float xv[CH], dv[CH], step[CH], out[CH];
-                Vec<T, CH>::unpack(cx[u], xv);
-                Vec<T, CH>::unpack(ct[u], dv);
-                steps_of<CH>(dv, bias, soft, step);
-                advance<N, CH, true>(h, A, step, xv, tile + (g + u) * 2 * N, out);
-#pragma unroll
-                for (int e = 0; e < CH; ++e) out[e] = fmaf(skip[e], xv[e], out[e]);
-                if (z) {
-                    float zv[CH];
-                    Vec<T, CH>::unpack(cz[u], zv);
-#pragma unroll
-                    for (int e = 0; e < CH; ++e) out[e] *= mx::silu(zv[e]);
-                }
-                if (r.s < 0)
-#pragma unroll
-                    for (int e = 0; e < CH; ++e) out[e] = 0.f;
-                if (w.there) __stcs(reinterpret_cast<Raw *>(y + i * a.sy.t), Vec<T, CH>::pack(out));
             }
         }
     }
@@ -347,13 +438,13 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(SsmArgs a, Plan p) {
 // Few warps are cut into more: as many as are resident at once.  A row that fills
 // half of them by itself stays whole, as every exponential of a cut row is taken
 // twice.
-constexpr int kResident = 152 * 3 * kWarps;
+constexpr int kJoin = 8;  // from so many chunks of a row on they are joined by a launch of its own
 template <int N>
 Plan plan(int B, int T, int Di) {
     Plan p{};
     p.blocks = (Di + Shape<N>::BLOCK - 1) / Shape<N>::BLOCK;
-    const long long whole = (long long)B * p.blocks;
-    long long chunks = whole * 2 >= kResident ? 1 : kResident / whole;
+    const long long whole = (long long)B * p.blocks, resident = 152 * Shape<N>::CTAS * kWarps;
+    long long chunks = whole * 2 >= resident ? 1 : resident / whole;
     long long len = ((T + chunks - 1) / chunks + kTile - 1) / kTile * kTile;
     p.len = (int)len;
     p.chunks = (int)((T + len - 1) / len);
@@ -366,60 +457,98 @@ int fwd(const SsmArgs &a, cudaStream_t stream) {
     Plan p = plan<N>(a.B, a.T, a.Di);
     const size_t shares = (size_t)a.B * p.chunks * p.blocks;
     p.state = static_cast<float *>(a.ws);
-    p.steps = p.state + shares * 1024;
+    p.steps = p.state + shares * 128 * Shape<N>::V;
     const long long groups = (p.blocks + kWarps - 1) / kWarps;
     if (p.chunks > 1) {
         share_kernel<T, N><<<(unsigned)(groups * a.B * (p.chunks - 1)), kThreads, 0, stream>>>(a, p);
-        const int st = mx::launched();
+        int st = mx::launched();
         if (st != GDN_OK) return st;
+        p.joined = p.chunks >= kJoin;
+        if (p.joined) {
+            join_kernel<N><<<(unsigned)((long long)a.B * p.blocks), 32 * Shape<N>::V, 0, stream>>>(a, p);
+            st = mx::launched();
+            if (st != GDN_OK) return st;
+        }
     }
-    scan_kernel<T, N><<<(unsigned)(groups * a.B * p.chunks), kThreads, 0, stream>>>(a, p);
+    if (a.z) scan_kernel<T, N, true><<<(unsigned)(groups * a.B * p.chunks), kThreads, 0, stream>>>(a, p);
+    else scan_kernel<T, N, false><<<(unsigned)(groups * a.B * p.chunks), kThreads, 0, stream>>>(a, p);
     return mx::launched();
 }
 
-// One token a row: four states a thread, the N/4 threads of a channel together.
-// The bytes of the states bound it, read and written once.
-constexpr int kStepThreads = 256;
-template <typename T, int N>
+// One token a row: eight states a thread, the N/8 threads of a channel together,
+// R rows a thread, whose A is read once.  The bytes of the states bound it, read
+// and written once; with four states a thread what belongs to the channel (its
+// step, its gate) was worked out four times over and took as long.  STEP_FIGURES
+constexpr int kStepThreads = 128;
+template <typename T, int N, int R>
 __global__ void __launch_bounds__(kStepThreads) step_kernel(SsmStepArgs a) {
-    constexpr int L = N / 4;  // lanes of a channel
-    const int i = blockIdx.x * kStepThreads + threadIdx.x, c = i / L, q = i % L, b = blockIdx.y;
-    const bool there = c < a.Di;
-    const int slot = a.slots ? a.slots[b] : b;
-    T *y = static_cast<T *>(a.y) + (size_t)b * a.Di + c;
-    if (slot < 0 || slot >= a.n_slots) {  // an idle row
-        float none[1] = {0.f};
-        if (there && q == 0) *reinterpret_cast<typename Vec<T, 1>::Raw *>(y) = Vec<T, 1>::pack(none);
-        return;
-    }
-    if (!there) return;
+    constexpr int L = N / 8;  // lanes of a channel, which take its float4 q and q + L
+    const int i = blockIdx.x * kStepThreads + threadIdx.x, c = i / L, q = i % L, groups = (a.B + R - 1) / R;
+    const int b0 = blockIdx.y;  // rows b0, b0 + groups, ..
+    if (c >= a.Di) return;  // a channel's lanes are there or not together
     auto at = [](const void *p, long long i) {
         float v[1];
         Vec<T, 1>::unpack(__ldg(reinterpret_cast<const typename Vec<T, 1>::Raw *>(static_cast<const T *>(p) + i)), v);
         return v[0];
     };
-    const size_t place = ((size_t)slot * a.Di + c) * N + 4 * q;
-    const float4 h = __ldcs(reinterpret_cast<const float4 *>(a.state + place));
-    const float4 A = __ldg(reinterpret_cast<const float4 *>(a.A + (size_t)c * N) + q);
-    float B[4], C[4];
-    Vec<T, 4>::unpack(__ldg(reinterpret_cast<const typename Vec<T, 4>::Raw *>(static_cast<const T *>(a.Bt) + b * a.sB) + q), B);
-    Vec<T, 4>::unpack(__ldg(reinterpret_cast<const typename Vec<T, 4>::Raw *>(static_cast<const T *>(a.Ct) + b * a.sC) + q), C);
-    const float x = at(a.x, b * a.sx + c), v = at(a.dt, b * a.sdt + c) + (a.bias ? __ldg(a.bias + c) : 0.f);
-    const float step = (a.flags & GDN_DT_SOFTPLUS) ? mx::softplus(v) : v, u = step * x, d = step * mx::kLog2e;
-    float4 n;
-    n.x = fmaf(mx::exp2_fast(d * A.x), h.x, u * B[0]), n.y = fmaf(mx::exp2_fast(d * A.y), h.y, u * B[1]);
-    n.z = fmaf(mx::exp2_fast(d * A.z), h.z, u * B[2]), n.w = fmaf(mx::exp2_fast(d * A.w), h.w, u * B[3]);
-    __stcs(reinterpret_cast<float4 *>(a.state_out + place), n);
-    float o = fmaf(C[0], n.x, fmaf(C[1], n.y, fmaf(C[2], n.z, C[3] * n.w)));
-    // a channel's lanes are there or not together
-    const unsigned mask = (L == 8 ? 0xffu : L == 4 ? 0xfu : 0x3u) << ((threadIdx.x & 31) / L * L);
+    auto two = [](const float4 &v, F2 (&x)[2]) { x[0] = pair(v.x, v.y), x[1] = pair(v.z, v.w); };
+    auto four = [](const void *p, long long i, F2 (&x)[2]) {
+        float v[4];
+        Vec<T, 4>::unpack(__ldg(reinterpret_cast<const typename Vec<T, 4>::Raw *>(static_cast<const T *>(p) + i)), v);
+        x[0] = pair(v[0], v[1]), x[1] = pair(v[2], v[3]);
+    };
+    int slot[R];
+    float4 state[R][2];
 #pragma unroll
-    for (int m = 1; m < L; m <<= 1) o += __shfl_xor_sync(mask, o, m);
-    if (q == 0) {
-        if (a.D) o = fmaf(__ldg(a.D + c), x, o);
-        if (a.z) o *= mx::silu(at(a.z, b * a.sz + c));
-        float out[1] = {o};
-        *reinterpret_cast<typename Vec<T, 1>::Raw *>(y) = Vec<T, 1>::pack(out);
+    for (int r = 0; r < R; ++r) {
+        const int b = b0 + r * groups;
+        slot[r] = b >= a.B ? -1 : a.slots ? __ldg(a.slots + b) : b;
+        if (slot[r] >= a.n_slots) slot[r] = -1;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (slot[r] >= 0) {
+            const float4 *page = reinterpret_cast<const float4 *>(a.state + ((size_t)slot[r] * a.Di + c) * N);
+            state[r][0] = __ldcs(page + q), state[r][1] = __ldcs(page + q + L);
+        }
+    F2 A[2][2];
+    two(__ldg(reinterpret_cast<const float4 *>(a.A + (size_t)c * N) + q), A[0]);
+    two(__ldg(reinterpret_cast<const float4 *>(a.A + (size_t)c * N) + q + L), A[1]);
+    const float bias = a.bias ? __ldg(a.bias + c) : 0.f, skip = a.D ? __ldg(a.D + c) : 0.f;
+    const unsigned mask = L == 1 ? 1u << (threadIdx.x & 31) : (L == 2 ? 0x3u : 0xfu) << ((threadIdx.x & 31) / L * L);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int b = b0 + r * groups;
+        if (b >= a.B) break;
+        float out[1] = {0.f};
+        if (slot[r] >= 0) {
+            const float x = at(a.x, b * a.sx + c), v = at(a.dt, b * a.sdt + c) + bias;
+            const float step = (a.flags & GDN_DT_SOFTPLUS) ? mx::softplus(v) : v;
+            const F2 u = both(step * x), d = both(step * mx::kLog2e);
+            F2 o = 0;
+            float4 *page = reinterpret_cast<float4 *>(a.state_out + ((size_t)slot[r] * a.Di + c) * N);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                F2 h[2], B[2], C[2];
+                four(a.Bt, b * a.sB + 4 * (q + k * L), B);
+                four(a.Ct, b * a.sC + 4 * (q + k * L), C);
+                two(state[r][k], h);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    h[m] = fma2(exp2_2(mul2(d, A[k][m])), h[m], mul2(u, B[m]));
+                    o = fma2(C[m], h[m], o);
+                }
+                float4 n;
+                split(h[0], n.x, n.y), split(h[1], n.z, n.w);
+                __stcs(page + q + k * L, n);
+            }
+            out[0] = sum(o);
+#pragma unroll
+            for (int m = 1; m < L; m <<= 1) out[0] += __shfl_xor_sync(mask, out[0], m);
+            out[0] = fmaf(skip, x, out[0]);
+            if (a.z) out[0] *= mx::silu(at(a.z, b * a.sz + c));
+        }
+        if (q == 0) *reinterpret_cast<typename Vec<T, 1>::Raw *>(static_cast<T *>(a.y) + (size_t)b * a.Di + c) = Vec<T, 1>::pack(out);
     }
 }
 
@@ -438,8 +567,10 @@ int step(const SsmStepArgs &a, cudaStream_t stream) {
             p.state = a.state + (size_t)b0 * a.Di * N, p.state_out = a.state_out + (size_t)b0 * a.Di * N;
             p.n_slots = a.n_slots - b0;
         }
-        const long long lanes = (long long)a.Di * (N / 4);
-        step_kernel<T, N><<<dim3((unsigned)((lanes + kStepThreads - 1) / kStepThreads), p.B), kStepThreads, 0, stream>>>(p);
+        const unsigned ctas = (unsigned)(((long long)a.Di * (N / 8) + kStepThreads - 1) / kStepThreads);
+        // four rows a thread where that leaves each SM eight CTAs
+        if ((long long)ctas * p.B >= 4LL * 8 * device_sm_count()) step_kernel<T, N, 4><<<dim3(ctas, (p.B + 3) / 4), kStepThreads, 0, stream>>>(p);
+        else step_kernel<T, N, 1><<<dim3(ctas, p.B), kStepThreads, 0, stream>>>(p);
         const int st = mx::launched();
         if (st != GDN_OK) return st;
     }
@@ -451,7 +582,8 @@ int step(const SsmStepArgs &a, cudaStream_t stream) {
 size_t ssm_fwd_workspace(int B, int T, int Di, int N, int) {
     const Plan p = plan_of(B, T, Di, N);
     if (p.chunks == 1) return 0;
-    return (size_t)B * p.chunks * p.blocks * (1024 + 32 * (32 / N)) * sizeof(float);
+    const int ch = N == 8 ? Shape<8>::CH : N == 16 ? Shape<16>::CH : Shape<32>::CH;
+    return (size_t)B * p.chunks * p.blocks * 32 * ch * (N + 1) * sizeof(float);
 }
 
 int launch_ssm_fwd(const SsmArgs &a, cudaStream_t stream) {
