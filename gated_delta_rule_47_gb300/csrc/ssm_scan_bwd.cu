@@ -16,12 +16,16 @@
 // state); states every 8 tokens take Di N / 2 bytes a token, written and read once
 // behind the arithmetic.
 //
-// A thread holds 4 channels x 4 states: the sums over states are over N/4 lanes,
-// those over channels over the other lanes, both by halves (each lane passes on
-// what another one keeps).  The other way round (all states of a channel in a
-// thread, as forwards) would need 32 values summed over 32 lanes for dB and dC.
+// A thread holds 4 channels x 4 states, as pairs of channels: what belongs to a
+// channel is loaded as a pair, and B and C lie in shared memory twice over.  The
+// sums over a channel's lanes and, for dB and dC, over the channels' go through
+// shared memory, two and four tokens at a time: by shuffles they took 64 and 28
+// instructions a token and warp, so they take 11 and 8.  The other way round (all
+// states of a channel in a thread, as forwards) would need 32 values of a token
+// summed over 32 lanes.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "ssm.cuh"
 
@@ -52,8 +56,8 @@ struct Plan {
     int groups, blocks;  // CTAs over the channels; blocks of tokens a row
     float *left, *back;  // [row][chunk][Di][N]: the state that a chunk leaves, the gradient that it passes on
     float *steps;        // [row][chunk][Di]: the sum of its steps
-    float *state;        // [row][block][Di][N]: the state before a block, from 0 at the chunk's start
-    float *upto;         // [row][block][Di]: the steps from the chunk's start to the block
+    float *state;        // [row][block][warp's channels][4][32] float4: the state before a block, from 0 at the chunk's start
+    float *upto;         // [row][block][warp's channels]: the steps from the chunk's start to the block
     float *dA, *dD, *db; // [row][chunk][Di][N], [row][chunk][Di] twice
     float *dBC;          // [group][row][T][2 N]
 };
@@ -64,15 +68,18 @@ struct Mem {
     uint4 raw[2][4][S::NV];  // x, dt, dy, z as loaded, twice: one on its way
     uint4 bc[2][2 * S::NB];
     float step[kBlock][S::CH], x[kBlock][S::CH], dy[kBlock][S::CH];  // then D's and x's gradients, and y
-    float b[kBlock][N], c[kBlock][N];
+    float b[kBlock][2 * N], c[kBlock][2 * N];                        // every value twice
+    int seq[kBlock];                                                // the sequences that start or end in the block
 };
 template <typename T, int N>
 struct GradMem : Mem<T, N> {
     using S = Shape<T, N>;
-    float4 saved[2][5][32];                 // a block's state and steps, as the lanes take them
-    float4 start[4][32];                    // the state that enters the chunk
-    float part[2][kBlock][2 * N];           // a block's dB and dC of this warp
-    float acc[2][S::VPL * S::V][32];        // dskip and dbias of each lane's vectors
+    float4 saved[5][32];                      // a block's state and steps, as the lanes take them
+    float4 start[4][32];                      // the state that enters the chunk
+    float part[2][kBlock][2 * N];             // a block's dB and dC of this warp
+    float over_states[2][3][S::L][S::CH + 8]; // two tokens' D's and x's gradients and y, of each lane of a channel
+    float over_channels[4][S::G][2 * N + 4];  // four tokens' dB and dC, of each lane of the channels
+    float4 acc[2][S::VPL * S::V / 4][32];     // dskip and dbias of each lane's vectors
 };
 
 __device__ __forceinline__ void copy16(void *to, const void *from) {
@@ -199,7 +206,9 @@ __device__ __forceinline__ void convert(const SsmArgs &a, const Place &w, Mem<T,
         if (t + tok >= w.t1 || (dead >> tok & 1))
 #pragma unroll
             for (int e = 0; e < S::V; ++e) x[e] = 0.f;
-        put<S::V>(j < S::NB ? &m.b[tok][n] : &m.c[tok][n], x);
+        float *to = j < S::NB ? &m.b[tok][2 * n] : &m.c[tok][2 * n];
+#pragma unroll
+        for (int e = 0; e < S::V; e += 2) *reinterpret_cast<float4 *>(to + 2 * e) = make_float4(x[e], x[e], x[e + 1], x[e + 1]);
     }
 }
 
@@ -208,47 +217,84 @@ __device__ __forceinline__ void convert(const SsmArgs &a, const Place &w, Mem<T,
 struct Marks {
     unsigned starts, ends, dead;
 };
-__device__ __forceinline__ Marks marks_of(const SsmArgs &a, const Place &w, int t, Run &r) {
+__device__ __forceinline__ Marks marks_of(const SsmArgs &a, const Place &w, int t, Run &r, int *seq) {
     if (t < r.start || t >= r.end) r = mx::run_at(a.cu, a.n_seq, a.T, w.row, t);
-    const int n = min(kBlock, w.t1 - t);
+    const int n = min(kBlock, w.t1 - t), lane = threadIdx.x & 31;
     const unsigned past = 0xffu << n & 0xffu;
     if (r.end >= t + n) {
+        if (lane < kBlock) seq[lane] = r.s;
         if (r.s < 0) return {0, 0, 0xffu};
         return {r.start == t ? 1u : 0u, r.end == t + n ? 1u << (n - 1) : 0u, past};
     }
-    const int lane = threadIdx.x & 31;
     Run mine{-1, 0, 0};
     if (lane < n) mine = mx::run_at(a.cu, a.n_seq, a.T, w.row, t + lane);
+    if (lane < kBlock) seq[lane] = mine.s;
     return {__ballot_sync(~0u, mine.s >= 0 && mine.start == t + lane), __ballot_sync(~0u, mine.s >= 0 && mine.end == t + lane + 1),
             __ballot_sync(~0u, mine.s < 0) & 0xffu};
 }
 
-// The thread's 4 x 4 of a [Di,N] page, 0 where there is none.
+// A thread's 4 channels x 4 states: [pair of channels][state].
+using Quad = F2[2][4];
+
+// .. of a [Di,N] page, 0 where there is none.
 template <int N>
-__device__ __forceinline__ void load16(const SsmArgs &a, const Place &w, const float *page, F2 (&h)[4][2]) {
+__device__ __forceinline__ void load16(const SsmArgs &a, const Place &w, const float *page, Quad &h) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        ulonglong2 v = make_ulonglong2(0, 0);
-        if (page && w.c < a.Di) v = *reinterpret_cast<const ulonglong2 *>(page + (size_t)(w.c + e) * N + 4 * w.q);
-        h[e][0] = v.x, h[e][1] = v.y;
+    for (int p = 0; p < 2; ++p) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (page && w.c < a.Di) {
+            x = *reinterpret_cast<const float4 *>(page + (size_t)(w.c + 2 * p) * N + 4 * w.q);
+            y = *reinterpret_cast<const float4 *>(page + (size_t)(w.c + 2 * p + 1) * N + 4 * w.q);
+        }
+        h[p][0] = pair(x.x, y.x), h[p][1] = pair(x.y, y.y), h[p][2] = pair(x.z, y.z), h[p][3] = pair(x.w, y.w);
     }
 }
 template <int N>
-__device__ __forceinline__ void store16(const SsmArgs &a, const Place &w, float *page, const F2 (&h)[4][2]) {
+__device__ __forceinline__ void store16(const SsmArgs &a, const Place &w, float *page, const Quad &h) {
     if (w.c >= a.Di) return;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<ulonglong2 *>(page + (size_t)(w.c + e) * N + 4 * w.q) = make_ulonglong2(h[e][0], h[e][1]);
+    for (int p = 0; p < 2; ++p) {
+        float4 x, y;
+        split(h[p][0], x.x, y.x), split(h[p][1], x.y, y.y), split(h[p][2], x.z, y.z), split(h[p][3], x.w, y.w);
+        *reinterpret_cast<float4 *>(page + (size_t)(w.c + 2 * p) * N + 4 * w.q) = x;
+        *reinterpret_cast<float4 *>(page + (size_t)(w.c + 2 * p + 1) * N + 4 * w.q) = y;
+    }
 }
+// Vector e of the quad, as it lies in a block's saved state.
+__device__ __forceinline__ ulonglong2 quad_vector(const Quad &h, int e) { return make_ulonglong2(h[e >> 1][2 * (e & 1)], h[e >> 1][2 * (e & 1) + 1]); }
+__device__ __forceinline__ void set_vector(Quad &h, int e, const ulonglong2 &v) { h[e >> 1][2 * (e & 1)] = v.x, h[e >> 1][2 * (e & 1) + 1] = v.y; }
+
+// Four channels' values of a token, as pairs; four states', each twice.
+__device__ __forceinline__ void channels(const float *p, F2 (&x)[2]) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(p);
+    x[0] = v.x, x[1] = v.y;
+}
+__device__ __forceinline__ void states(const float *p, F2 (&x)[4]) {
+    const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(p), v = *reinterpret_cast<const ulonglong2 *>(p + 4);
+    x[0] = u.x, x[1] = u.y, x[2] = v.x, x[3] = v.y;
+}
+// h <- exp(D A) h + D x B of one token, from `from`.
+__device__ __forceinline__ void advance(const Quad &from, Quad &h, const Quad &A, const F2 (&d)[2], const F2 (&u)[2], const F2 (&b)[4]) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) h[p][n] = fma2(exp2_2(mul2(d[p], A[p][n])), from[p][n], mul2(u[p], b[n]));
+}
+
 template <int N>
-__device__ __forceinline__ void load_decays(const SsmArgs &a, const Place &w, F2 (&d)[4][2]) {
+__device__ __forceinline__ void load_decays(const SsmArgs &a, const Place &w, Quad &d) {
     load16<N>(a, w, a.A, d);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) d[e][0] = mul2(d[e][0], both(mx::kLog2e)), d[e][1] = mul2(d[e][1], both(mx::kLog2e));
+    for (int i = 0; i < 8; ++i) d[i >> 2][i & 3] = mul2(d[i >> 2][i & 3], both(mx::kLog2e));
 }
-__device__ __forceinline__ void zero16(F2 (&h)[4][2]) {
+__device__ __forceinline__ void zero16(Quad &h) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) h[e][0] = h[e][1] = 0;
+    for (int i = 0; i < 8; ++i) h[i >> 2][i & 3] = 0;
+}
+// Where a block's saved state and steps are, of this warp's channels.
+template <typename T, int N>
+__device__ __forceinline__ size_t saved_at(const SsmArgs &a, const Plan &p, const Place &w, int t) {
+    return ((size_t)w.row * p.blocks + t / kBlock) * (p.groups * kWarps) + w.c0 / Shape<T, N>::CH;
 }
 __device__ __forceinline__ size_t chunk_at(const SsmArgs &a, const Plan &p, int row, int chunk) {
     return ((size_t)row * p.chunks + chunk) * a.Di;
@@ -263,13 +309,14 @@ __global__ void __launch_bounds__(kThreads, 4) share_kernel(SsmArgs a, Plan p) {
     if (w.c0 >= a.Di) return;  // warps do not wait for one another here
     fetch<T, N>(a, w, m, 0, w.t0);
     copies_out();
-    F2 h[4][2], A[4][2], prod[4][2], back[4][2];
-    float total[4] = {0.f, 0.f, 0.f, 0.f};
+    const int lane = threadIdx.x & 31;
+    Quad h, A, prod, back;
+    F2 total[2] = {0, 0};
     load_decays<N>(a, w, A);
     zero16(h);
     zero16(back);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) prod[e][0] = prod[e][1] = both(1.f);
+    for (int i = 0; i < 8; ++i) prod[i >> 2][i & 3] = both(1.f);
     const size_t page = (size_t)a.Di * N;
     Run r = mx::run_at(a.cu, a.n_seq, a.T, w.row, w.t0);
     // up to where the chunk passes a gradient to the one before
@@ -279,102 +326,69 @@ __global__ void __launch_bounds__(kThreads, 4) share_kernel(SsmArgs a, Plan p) {
     for (int t = w.t0; t < w.t1; t += kBlock, buf ^= 1) {
         const bool more = t + kBlock < w.t1;
         if (more) fetch<T, N>(a, w, m, buf ^ 1, t + kBlock), copies_out();
-        const Marks k = marks_of(a, w, t, r);
-        const size_t at = ((size_t)w.row * p.blocks + t / kBlock) * a.Di;
-        store16<N>(a, w, p.state + at * N, h);
-        if (w.q == 0 && w.c < a.Di) *reinterpret_cast<float4 *>(p.upto + at + w.c) = make_float4(total[0], total[1], total[2], total[3]);
+        const Marks k = marks_of(a, w, t, r, m.seq);
+        const size_t at = saved_at<T, N>(a, p, w, t);
+        ulonglong2 *to = reinterpret_cast<ulonglong2 *>(p.state) + at * 128 + lane;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) to[e * 32] = quad_vector(h, e);
+        if (w.q == 0) *reinterpret_cast<ulonglong2 *>(p.upto + at * S::CH + 4 * w.g) = make_ulonglong2(total[0], total[1]);
         copies_done(!more);
         __syncwarp();
         convert<T, N>(a, w, m, buf, t, k.dead);
         __syncwarp();
-#pragma unroll 2
-        for (int u = 0; u < kBlock; ++u) {
-            if (k.starts >> u & 1) {
-                const Run s = mx::run_at(a.cu, a.n_seq, a.T, w.row, t + u);
-                load16<N>(a, w, a.s0 ? a.s0 + s.s * page : nullptr, h);
+        auto token = [&](int u, bool pass) {
+            F2 d[2], x[2], b[4];
+            channels(&m.step[u][4 * w.g], d);
+            channels(&m.x[u][4 * w.g], x);
+            states(&m.b[u][8 * w.q], b);
+            const F2 in[2] = {mul2(d[0], x[0]), mul2(d[1], x[1])};
+            total[0] = mx::add2(total[0], d[0]), total[1] = mx::add2(total[1], d[1]);
+            if (!pass) {
+                advance(h, h, A, d, in, b);
+                return;
             }
-            float d[4], x[4], g[4];
-            get<4>(&m.step[u][4 * w.g], d);
-            get<4>(&m.x[u][4 * w.g], x);
-            get<4>(&m.dy[u][4 * w.g], g);
-            const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(&m.b[u][4 * w.q]);
-            const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(&m.c[u][4 * w.q]);
-            const bool pass = t + u < until;
+            F2 g[2], c[4];
+            channels(&m.dy[u][4 * w.g], g);
+            states(&m.c[u][8 * w.q], c);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const F2 in = both(d[e] * x[e]), de = both(d[e]), ge = both(g[e]);
-                total[e] += d[e];
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const F2 dec = exp2_2(mul2(de, A[e][i]));
-                    h[e][i] = fma2(dec, h[e][i], mul2(in, i ? b.y : b.x));
-                    if (pass) {
-                        prod[e][i] = mul2(prod[e][i], dec);
-                        back[e][i] = fma2(prod[e][i], mul2(ge, i ? c.y : c.x), back[e][i]);
-                    }
+                for (int n = 0; n < 4; ++n) {
+                    const F2 dec = exp2_2(mul2(d[i], A[i][n]));
+                    h[i][n] = fma2(dec, h[i][n], mul2(in[i], b[n]));
+                    prod[i][n] = mul2(prod[i][n], dec);
+                    back[i][n] = fma2(prod[i][n], mul2(g[i], c[n]), back[i][n]);
                 }
+        };
+        if (k.starts == 0 && (t + kBlock <= until || t >= until)) {
+            const bool pass = t < until;
+            if (pass) {
+#pragma unroll 2
+                for (int u = 0; u < kBlock; ++u) token(u, true);
+            } else {
+#pragma unroll 2
+                for (int u = 0; u < kBlock; ++u) token(u, false);
+            }
+        } else {
+#pragma unroll 1
+            for (int u = 0; u < kBlock; ++u) {
+                if (k.starts >> u & 1) load16<N>(a, w, a.s0 ? a.s0 + m.seq[u] * page : nullptr, h);
+                if (t + u < until) token(u, true);
+                else token(u, false);
             }
         }
         __syncwarp();
     }
     if (a.dsf && until > w.t0 && last_of <= w.t1) {  // the sequence ends here: its final state's share
-        F2 s[4][2];
+        Quad s;
         load16<N>(a, w, a.dsf + seq * page, s);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) back[e][i] = fma2(prod[e][i], s[e][i], back[e][i]);
+        for (int i = 0; i < 8; ++i) back[i >> 2][i & 3] = fma2(prod[i >> 2][i & 3], s[i >> 2][i & 3], back[i >> 2][i & 3]);
     }
     const size_t at = chunk_at(a, p, w.row, w.chunk);
     store16<N>(a, w, p.left + at * N, h);
     store16<N>(a, w, p.back + at * N, back);
-    if (w.q == 0 && w.c < a.Di) *reinterpret_cast<float4 *>(p.steps + at + w.c) = make_float4(total[0], total[1], total[2], total[3]);
-}
-
-// v[0..K) summed over the lanes that differ in bit m: a lane keeps half of the
-// values (the upper half where its bit is set), or all where there is one.
-template <int K>
-__device__ __forceinline__ void halve(float *v, int m) {
-    if constexpr (K == 1) {
-        v[0] += __shfl_xor_sync(~0u, v[0], m);
-    } else {
-        const bool up = (threadIdx.x & m) != 0;
-#pragma unroll
-        for (int i = 0; i < K / 2; ++i) {
-            const float keep = up ? v[i + K / 2] : v[i], pass = up ? v[i] : v[i + K / 2];
-            v[i] = keep + __shfl_xor_sync(~0u, pass, m);
-        }
-    }
-}
-
-// Sums of four channels' values over the lanes of their states: the lane keeps
-// channel(s) e .. of the four.
-template <int L>
-__device__ __forceinline__ void over_states(float (&v)[4]) {
-    halve<4>(v, 1);
-    if constexpr (L >= 4) halve<2>(v, 2);
-    if constexpr (L >= 8) halve<1>(v, 4);
-}
-template <int L>
-__device__ __forceinline__ void put_channels(float *row, int q, const float (&v)[4]) {
-    const int e = (q & 1) * 2;
-    if constexpr (L == 2) *reinterpret_cast<float2 *>(row + e) = make_float2(v[0], v[1]);
-    else if (q < 4) row[e + (q >> 1 & 1)] = v[0];
-}
-// Sums of dB's and dC's four states over the lanes of the channels.
-template <int N>
-__device__ __forceinline__ void over_channels(float (&v)[8]) {
-    constexpr int L = N / 4;
-    halve<8>(v, L);
-    halve<4>(v, 2 * L);
-    if constexpr (N <= 16) halve<2>(v, 4 * L);
-    if constexpr (N <= 8) halve<1>(v, 8 * L);
-}
-template <int N>
-__device__ __forceinline__ void put_states(float *row, int q, int g, const float (&v)[8]) {
-    float *to = row + (g & 1) * N + 4 * q + (g >> 1 & 1) * 2;
-    if constexpr (N == 32) *reinterpret_cast<float2 *>(to) = make_float2(v[0], v[1]);
-    else if (g < 8) to[g >> 2 & 1] = v[0];
+    if (w.q == 0 && w.c < a.Di) *reinterpret_cast<ulonglong2 *>(p.steps + at + w.c) = make_ulonglong2(total[0], total[1]);
 }
 
 template <typename T, int N>
@@ -387,24 +401,26 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
     const Place w = place_of<T, N>(a, p);
     const size_t page = (size_t)a.Di * N;
     const bool soft = a.flags & GDN_DT_SOFTPLUS;
-    auto fetch_all = [&](int buf, int t) {
-        fetch<T, N>(a, w, m, buf, t);
-        const size_t at = ((size_t)w.row * p.blocks + t / kBlock) * a.Di + w.c;
-        if (w.c < a.Di) {
+    // the copies of a block's saved state: a lane's are its own
+    auto fetch_saved = [&](int t) {
+        if (w.c0 < a.Di) {
+            const size_t at = saved_at<T, N>(a, p, w, t);
+            const float4 *from = reinterpret_cast<const float4 *>(p.state) + at * 128 + lane;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) copy16(&m.saved[buf][e][lane], p.state + (at + e) * N + 4 * w.q);
-            copy16(&m.saved[buf][4][lane], p.upto + at);
+            for (int e = 0; e < 4; ++e) copy16(&m.saved[e][lane], from + e * 32);
+            copy16(&m.saved[4][lane], p.upto + at * S::CH + 4 * w.g);
         }
-        copies_out();
     };
     const int last = w.t0 + (w.t1 - 1 - w.t0) / kBlock * kBlock;
-    fetch_all(0, last);
-    F2 A[4][2], g[4][2], dA[4][2];
+    fetch<T, N>(a, w, m, 0, last);
+    fetch_saved(last);
+    copies_out();
+    Quad A, g, dA;
     load_decays<N>(a, w, A);
     zero16(g);
     zero16(dA);
 #pragma unroll
-    for (int i = 0; i < S::VPL * S::V; ++i) m.acc[0][i][lane] = m.acc[1][i][lane] = 0.f;
+    for (int i = 0; i < S::VPL * S::V / 4; ++i) m.acc[0][i][lane] = m.acc[1][i][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
     // sequences without tokens pass their gradient on
     if (a.cu && a.ds0) {
         for (int s0 = w.chunk * 32; s0 < a.n_seq; s0 += p.chunks * 32) {
@@ -412,35 +428,35 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
             unsigned e = __ballot_sync(~0u, s < a.n_seq && mx::no_tokens(a.cu, a.T, min(s, a.n_seq - 1)));
             for (; e; e &= e - 1) {
                 const size_t at = (size_t)(s0 + __ffs(e) - 1) * page;
-                F2 h[4][2];
+                Quad h;
                 load16<N>(a, w, a.dsf ? a.dsf + at : nullptr, h);
                 store16<N>(a, w, a.ds0 + at, h);
             }
         }
     }
     // x <- what chunk j gives + its decay x, from the first one named on
-    auto join = [&](const float *from, int j, bool first, F2 (&x)[4][2]) {
+    auto join = [&](const float *from, int j, bool first, Quad &x) {
         const size_t at = chunk_at(a, p, w.row, j);
-        F2 v[4][2];
+        Quad v;
         load16<N>(a, w, from + at * N, v);
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        if (w.c < a.Di) vector_of<4>(p.steps + at, w.c, d);
+        F2 d[2] = {0, 0};
+        if (w.c < a.Di) channels(p.steps + at + w.c, d);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) x[e][i] = first ? v[e][i] : fma2(exp2_2(mul2(both(d[e]), A[e][i])), x[e][i], v[e][i]);
+            for (int n = 0; n < 4; ++n) x[i][n] = first ? v[i][n] : fma2(exp2_2(mul2(d[i], A[i][n])), x[i][n], v[i][n]);
     };
     Run r = mx::run_at(a.cu, a.n_seq, a.T, w.row, w.t0);
     const int entered = r.s >= 0 && r.start < w.t0 ? r.end : w.t0;  // the entering state matters up to here
     {
-        F2 h[4][2];
+        Quad h;
         zero16(h);
         if (entered > w.t0) {
             const int first = min(r.start / p.len, w.chunk - 1);
             for (int j = first; j < w.chunk; ++j) join(p.left, j, j == first, h);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) *reinterpret_cast<ulonglong2 *>(&m.start[e][lane]) = make_ulonglong2(h[e][0], h[e][1]);
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<ulonglong2 *>(&m.start[e][lane]) = quad_vector(h, e);
         r = mx::run_at(a.cu, a.n_seq, a.T, w.row, w.t1 - 1);
         if (r.s >= 0 && r.end > w.t1) {
             const int end = max((r.end - 1) / p.len, w.chunk + 1);
@@ -449,116 +465,134 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
     }
     int buf = 0;
     for (int t = last; t >= w.t0; t -= kBlock, buf ^= 1) {
-        if (t > w.t0) fetch_all(buf ^ 1, t - kBlock);
-        const Marks k = marks_of(a, w, t, r);
-        copies_done(t == w.t0);
+        copies_done(true);
+        const Marks k = marks_of(a, w, t, r, m.seq);
         __syncwarp();
+        if (t > w.t0) fetch<T, N>(a, w, m, buf ^ 1, t - kBlock);
         convert<T, N>(a, w, m, buf, t, k.dead);
-        F2 hs[kBlock + 1][4][2];  // before the block, and after each of its tokens
+        Quad h0;  // before the block
         {
-            float d[4];
-            get<4>(reinterpret_cast<const float *>(&m.saved[buf][4][lane]), d);
             const bool there = w.c < a.Di;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&m.saved[buf][e][lane]);
-                hs[0][e][0] = there ? v.x : 0, hs[0][e][1] = there ? v.y : 0;
-                if (there && t < entered) {
-                    const ulonglong2 s = *reinterpret_cast<const ulonglong2 *>(&m.start[e][lane]);
-                    hs[0][e][0] = fma2(exp2_2(mul2(both(d[e]), A[e][0])), s.x, hs[0][e][0]);
-                    hs[0][e][1] = fma2(exp2_2(mul2(both(d[e]), A[e][1])), s.y, hs[0][e][1]);
-                }
+            for (int e = 0; e < 4; ++e)
+                set_vector(h0, e, there ? *reinterpret_cast<const ulonglong2 *>(&m.saved[e][lane]) : make_ulonglong2(0, 0));
+            if (there && t < entered) {
+                F2 d[2];
+                Quad s;
+                channels(reinterpret_cast<const float *>(&m.saved[4][lane]), d);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) set_vector(s, e, *reinterpret_cast<const ulonglong2 *>(&m.start[e][lane]));
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) h0[i][n] = fma2(exp2_2(mul2(d[i], A[i][n])), s[i][n], h0[i][n]);
             }
         }
+        if (t > w.t0) fetch_saved(t - kBlock);
+        copies_out();
         __syncwarp();
+        // the block, with or without sequences that start or end in it
+        auto block = [&](auto marked) {
+            constexpr bool MARKED = decltype(marked)::value;  // few blocks: their states go through local memory
+            constexpr int UNROLL = MARKED ? 1 : kBlock;
+            Quad hs[kBlock + 1];  // before the block, and after each of its tokens
 #pragma unroll
-        for (int u = 0; u < kBlock; ++u) {
-            float d[4], x[4];
-            get<4>(&m.step[u][4 * w.g], d);
-            get<4>(&m.x[u][4 * w.g], x);
-            const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(&m.b[u][4 * w.q]);
-            if (k.starts >> u & 1) {
-                const Run s = mx::run_at(a.cu, a.n_seq, a.T, w.row, t + u);
-                F2 h0[4][2];
-                load16<N>(a, w, a.s0 ? a.s0 + s.s * page : nullptr, h0);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        hs[u + 1][e][i] = fma2(exp2_2(mul2(both(d[e]), A[e][i])), h0[e][i], mul2(both(d[e] * x[e]), i ? b.y : b.x));
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        hs[u + 1][e][i] = fma2(exp2_2(mul2(both(d[e]), A[e][i])), hs[u][e][i], mul2(both(d[e] * x[e]), i ? b.y : b.x));
-            }
-        }
-#pragma unroll
-        for (int u = kBlock - 1; u >= 0; --u) {
-            if (k.ends >> u & 1) {
-                const Run s = mx::run_at(a.cu, a.n_seq, a.T, w.row, t + u);
-                load16<N>(a, w, a.dsf ? a.dsf + s.s * page : nullptr, g);
-            }
-            if (k.starts >> u & 1) {  // what came before is the sequence's initial state; the last one's end waits
-                const Run s = mx::run_at(a.cu, a.n_seq, a.T, w.row, t + u);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    *reinterpret_cast<ulonglong2 *>(&m.saved[buf][e][lane]) = make_ulonglong2(hs[u][e][0], hs[u][e][1]);
-                load16<N>(a, w, a.s0 ? a.s0 + s.s * page : nullptr, hs[u]);
-            }
-            float d[4], x[4], dy[4], dx[4], ds[4], y[4];
-            get<4>(&m.step[u][4 * w.g], d);
-            get<4>(&m.x[u][4 * w.g], x);
-            get<4>(&m.dy[u][4 * w.g], dy);
-            const ulonglong2 b2 = *reinterpret_cast<const ulonglong2 *>(&m.b[u][4 * w.q]);
-            const ulonglong2 c2 = *reinterpret_cast<const ulonglong2 *>(&m.c[u][4 * w.q]);
-            const F2 b[2] = {b2.x, b2.y}, c[2] = {c2.x, c2.y};
-            F2 dB[2] = {0, 0}, dC[2] = {0, 0};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const F2 de = both(d[e]), ge = both(dy[e]), in = both(d[e] * x[e]);
-                F2 gb = 0, ap = 0, cy = 0;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    g[e][i] = fma2(c[i], ge, g[e][i]);
-                    dC[i] = fma2(hs[u + 1][e][i], ge, dC[i]);
-                    if (a.z) cy = fma2(hs[u + 1][e][i], c[i], cy);
-                    dB[i] = fma2(g[e][i], in, dB[i]);
-                    gb = fma2(g[e][i], b[i], gb);
-                    const F2 ag = mul2(exp2_2(mul2(de, A[e][i])), g[e][i]), over = mul2(ag, hs[u][e][i]);
-                    dA[e][i] = fma2(over, de, dA[e][i]);
-                    ap = fma2(over, A[e][i], ap);
-                    g[e][i] = ag;
-                }
-                const float s = sum(gb);
-                dx[e] = d[e] * s;
-                ds[e] = fmaf(x[e], s, mx::kLn2 * sum(ap));
-                y[e] = sum(cy);
-            }
-            if (k.starts >> u & 1) {
-                const Run s = mx::run_at(a.cu, a.n_seq, a.T, w.row, t + u);
-                if (a.ds0) store16<N>(a, w, a.ds0 + s.s * page, g);
-                zero16(g);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&m.saved[buf][e][lane]);
-                    hs[u][e][0] = v.x, hs[u][e][1] = v.y;
+            for (int i = 0; i < 8; ++i) hs[0][i >> 2][i & 3] = h0[i >> 2][i & 3];
+#pragma unroll UNROLL
+            for (int u = 0; u < kBlock; ++u) {
+                F2 d[2], x[2], b[4];
+                channels(&m.step[u][4 * w.g], d);
+                channels(&m.x[u][4 * w.g], x);
+                states(&m.b[u][8 * w.q], b);
+                const F2 in[2] = {mul2(d[0], x[0]), mul2(d[1], x[1])};
+                if (MARKED && (k.starts >> u & 1)) {
+                    Quad first;
+                    load16<N>(a, w, a.s0 ? a.s0 + m.seq[u] * page : nullptr, first);
+                    advance(first, hs[u + 1], A, d, in, b);
+                } else {
+                    advance(hs[u], hs[u + 1], A, d, in, b);
                 }
             }
-            over_states<S::L>(dx);
-            over_states<S::L>(ds);
-            if (a.z) over_states<S::L>(y);
-            float v[8];
+#pragma unroll UNROLL
+            for (int u = kBlock - 1; u >= 0; --u) {
+                if (MARKED && (k.ends >> u & 1)) load16<N>(a, w, a.dsf ? a.dsf + m.seq[u] * page : nullptr, g);
+                F2 d[2], x[2], dy[2], b[4], c[4], dx[2], ds[2], y[2];
+                channels(&m.step[u][4 * w.g], d);
+                channels(&m.x[u][4 * w.g], x);
+                channels(&m.dy[u][4 * w.g], dy);
+                states(&m.b[u][8 * w.q], b);
+                states(&m.c[u][8 * w.q], c);
+                F2 dB[4], dC[4];
+                auto token = [&](const Quad &before) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) split(dB[i], v[2 * i], v[2 * i + 1]), split(dC[i], v[4 + 2 * i], v[5 + 2 * i]);
-            over_channels<N>(v);
-            __syncwarp();  // the token's inputs have been read by all
-            put_channels<S::L>(&m.x[u][4 * w.g], w.q, dx);
-            put_channels<S::L>(&m.step[u][4 * w.g], w.q, ds);
-            if (a.z) put_channels<S::L>(&m.dy[u][4 * w.g], w.q, y);
-            put_states<N>(m.part[buf][u], w.q, w.g, v);
-        }
+                    for (int i = 0; i < 2; ++i) {
+                        const F2 in = mul2(d[i], x[i]);
+                        F2 gb, ap, cy;
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            g[i][n] = fma2(c[n], dy[i], g[i][n]);
+                            dC[n] = i ? fma2(hs[u + 1][i][n], dy[i], dC[n]) : mul2(hs[u + 1][i][n], dy[i]);
+                            dB[n] = i ? fma2(g[i][n], in, dB[n]) : mul2(g[i][n], in);
+                            if (a.z) cy = n ? fma2(hs[u + 1][i][n], c[n], cy) : mul2(hs[u + 1][i][n], c[n]);
+                            gb = n ? fma2(g[i][n], b[n], gb) : mul2(g[i][n], b[n]);
+                            g[i][n] = mul2(exp2_2(mul2(d[i], A[i][n])), g[i][n]);
+                            const F2 passed = mul2(g[i][n], before[i][n]);
+                            dA[i][n] = fma2(passed, d[i], dA[i][n]);
+                            ap = n ? fma2(passed, A[i][n], ap) : mul2(passed, A[i][n]);
+                        }
+                        dx[i] = mul2(d[i], gb);
+                        ds[i] = fma2(x[i], gb, mul2(ap, both(mx::kLn2)));
+                        y[i] = cy;
+                    }
+                };
+                if (MARKED && (k.starts >> u & 1)) {  // what came before is the sequence's initial state
+                    Quad first;
+                    load16<N>(a, w, a.s0 ? a.s0 + m.seq[u] * page : nullptr, first);
+                    token(first);
+                    if (a.ds0) store16<N>(a, w, a.ds0 + m.seq[u] * page, g);
+                    zero16(g);
+                } else {
+                    token(hs[u]);
+                }
+                auto put = [&](int what, const F2 (&v)[2]) {
+                    *reinterpret_cast<ulonglong2 *>(&m.over_states[u & 1][what][w.q][4 * w.g]) = make_ulonglong2(v[0], v[1]);
+                };
+                put(0, ds);
+                put(1, dx);
+                if (a.z) put(2, y);
+                float *row = m.over_channels[u & 3][w.g];
+                *reinterpret_cast<float4 *>(row + 4 * w.q) = make_float4(sum(dB[0]), sum(dB[1]), sum(dB[2]), sum(dB[3]));
+                *reinterpret_cast<float4 *>(row + N + 4 * w.q) = make_float4(sum(dC[0]), sum(dC[1]), sum(dC[2]), sum(dC[3]));
+                if ((u & 1) != 0) continue;
+                __syncwarp();
+                const int kinds = a.z ? 3 : 2;  // over step, x and dy of the two tokens, which all lanes have read
+                for (int i = lane; i < kinds * S::CH / 2; i += 32) {
+                    const int what = i / (S::CH / 2), tok = i % (S::CH / 2) / (S::CH / 4), c4 = i % (S::CH / 4) * 4;
+                    F2 p0 = 0, p1 = 0;
+#pragma unroll
+                    for (int q = 0; q < S::L; ++q) {
+                        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&m.over_states[tok][what][q][c4]);
+                        p0 = mx::add2(p0, v.x), p1 = mx::add2(p1, v.y);
+                    }
+                    *reinterpret_cast<ulonglong2 *>(&m.step[0][0] + (what * kBlock + u + tok) * S::CH + c4) = make_ulonglong2(p0, p1);
+                }
+                if ((u & 3) == 0)
+#pragma unroll
+                    for (int i = lane; i < 2 * N; i += 32) {
+                        const int tok = i / (N / 2), n = i % (N / 2) * 4;
+                        F2 p0 = 0, p1 = 0;
+#pragma unroll
+                        for (int q = 0; q < S::G; ++q) {
+                            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&m.over_channels[tok][q][n]);
+                            p0 = mx::add2(p0, v.x), p1 = mx::add2(p1, v.y);
+                        }
+                        *reinterpret_cast<ulonglong2 *>(&m.part[buf][u + tok][n]) = make_ulonglong2(p0, p1);
+                    }
+                __syncwarp();
+            }
+        };
+        if (k.starts | k.ends) block(std::true_type{});
+        else block(std::false_type{});
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < S::VPL; ++i) {
@@ -593,8 +627,13 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
                 for (int e = 0; e < S::V; ++e) {
                     dx[e] = fmaf(skip[e], dy[e], dx[e]);
                     if (soft) dv[e] *= mx::sigmoid(dt[e] + bias[e]);
-                    m.acc[0][i * S::V + e][lane] += dy[e] * x[e];
-                    m.acc[1][i * S::V + e][lane] += dv[e];
+                }
+#pragma unroll
+                for (int e = 0; e < S::V; e += 4) {
+                    float4 &p = m.acc[0][(i * S::V + e) / 4][lane], &q = m.acc[1][(i * S::V + e) / 4][lane];
+                    p.x = fmaf(dy[e], x[e], p.x), p.y = fmaf(dy[e + 1], x[e + 1], p.y);
+                    p.z = fmaf(dy[e + 2], x[e + 2], p.z), p.w = fmaf(dy[e + 3], x[e + 3], p.w);
+                    q.x += dv[e], q.y += dv[e + 1], q.z += dv[e + 2], q.w += dv[e + 3];
                 }
             }
             using Raw = typename Vec<T, S::V>::Raw;
@@ -621,8 +660,9 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
         if (w.c0 + i >= a.Di) break;
         float x = 0.f, y = 0.f;
         for (int j = i / S::V; j < S::NV; j += S::RV) {
-            x += m.acc[0][j / 32 * S::V + i % S::V][j % 32];
-            y += m.acc[1][j / 32 * S::V + i % S::V][j % 32];
+            const int v = j / 32 * S::V + i % S::V;
+            x += reinterpret_cast<const float *>(&m.acc[0][v / 4][j % 32])[v % 4];
+            y += reinterpret_cast<const float *>(&m.acc[1][v / 4][j % 32])[v % 4];
         }
         p.dD[at + w.c0 + i] = x;
         p.db[at + w.c0 + i] = y;
@@ -680,7 +720,8 @@ Plan plan(int B, int T, int Di, int N, float *ws, size_t *bytes) {
     p.blocks = (T + kBlock - 1) / kBlock;
     size_t at = 0;
     auto take = [&](float **x, size_t n) { *x = ws ? ws + at : nullptr, at += (n + 3) / 4 * 4; };
-    const size_t per_chunk = (size_t)B * p.chunks * Di, per_block = (size_t)B * p.blocks * Di;
+    // a block's places are of whole warps
+    const size_t per_chunk = (size_t)B * p.chunks * Di, per_block = (size_t)B * p.blocks * p.groups * channels(N);
     take(&p.left, per_chunk * N);
     take(&p.back, per_chunk * N);
     take(&p.steps, per_chunk);
