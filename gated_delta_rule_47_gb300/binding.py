@@ -1162,7 +1162,7 @@ def _written(t, name, shape, dtype):
 
 
 def _apart(a, b, names):
-    """An output that a call reads the input of after it has begun to write."""
+    """A call reads b after it has begun to write a: they may not share memory."""
     if a is not None and b is not None and a.numel() and b.numel():
         span = lambda t: t.data_ptr() + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()  # noqa: E731
         if a.data_ptr() < span(b) and b.data_ptr() < span(a):
@@ -1281,6 +1281,8 @@ def causal_conv_step(x, weight, window, bias=None, slots=None, window_out=None, 
         window_out = window
     elif window_out is not window:
         _dense(window_out, "window_out", window.shape, x.dtype)
+        if window_out.data_ptr() != window.data_ptr():
+            _apart(window_out, window, "window and window_out")
     _same_device(x, weight, window, bias, slots, window_out, y)
     with _device(x, stream):
         if y is None:
@@ -1412,6 +1414,8 @@ def ssm_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, slots=None, st
         state_out = state
     elif state_out is not state:
         _dense(state_out, "state_out", state.shape, torch.float32)
+        if state_out.data_ptr() != state.data_ptr():
+            _apart(state_out, state, "state and state_out")
     _same_device(x, dt, A, B, C, state, D, z, dt_bias, slots, state_out, y)
     with _device(x, stream):
         if y is None:
@@ -1468,9 +1472,9 @@ def gated_norm_fwd(x, gate, weight=None, eps=1e-6, gate_first=False, sigmoid=Fal
 
 
 def gated_norm_bwd(dy, x, gate, weight=None, eps=1e-6, gate_first=False, sigmoid=False, workspace=None, stream=None):
-    """Backward of gated_norm_fwd: (dx, dgate, dweight).  dx has x's strides where
-    those leave every element a place of its own; dweight is fp32 in weight's shape
-    ([D], the sum over the heads, without one)."""
+    """Backward of gated_norm_fwd: (dx, dgate, dweight).  dx is dense, its dimensions
+    in x's order; dgate is contiguous; dweight is fp32 in weight's shape ([D], the
+    sum over the heads, without one)."""
     if workspace is None and stream is None:
         r = (_front or _quick()).gated_back(dy, x, gate, weight, eps, gate_first, sigmoid)
         if r is not NotImplemented:

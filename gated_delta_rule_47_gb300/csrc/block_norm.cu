@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(1024) block_sum_kernel(BlockNormArgs a, const 
         if (a.ds) a.ds[(size_t)g * a.C + c] = y * (a.w1 ? a.w1[c] : 1.f);
     };
     auto add = [&](int g, int first, int step, float &x, float &y) {
-#pragma unroll 4
+#pragma unroll 8
         for (int i = first; i < per; i += step) {
             const float *p = part + ((size_t)g * per + i) * 2 * a.C + c;
             x += p[0], y += p[a.C];

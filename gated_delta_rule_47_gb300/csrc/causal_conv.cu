@@ -19,6 +19,8 @@ namespace {
 
 using mx::F2;
 using mx::Run;
+using mx::pack2;
+using mx::unpack2;
 
 // Weights [C,W] of channels c .. c+N-1.
 template <int N, int W>
@@ -98,21 +100,6 @@ __device__ __forceinline__ void pass_windows(const ConvArgs &a, const Strip &s, 
 
 constexpr int kThreads = 128;
 
-// N channels of a token as pairs.
-template <typename T, int N>
-__device__ __forceinline__ void unpack2(const typename Vec<T, N>::Raw &p, F2 (&x)[N / 2]) {
-    float v[N];
-    Vec<T, N>::unpack(p, v);
-#pragma unroll
-    for (int e = 0; e < N / 2; ++e) x[e] = mx::pair(v[2 * e], v[2 * e + 1]);
-}
-template <typename T, int N>
-__device__ __forceinline__ typename Vec<T, N>::Raw pack2(const F2 (&x)[N / 2]) {
-    float v[N];
-#pragma unroll
-    for (int e = 0; e < N / 2; ++e) mx::split(x[e], v[2 * e], v[2 * e + 1]);
-    return Vec<T, N>::pack(v);
-}
 template <int N>
 __device__ __forceinline__ void pairs(const float (&v)[N], F2 (&x)[N / 2]) {
 #pragma unroll
@@ -122,9 +109,9 @@ __device__ __forceinline__ void pairs(const float (&v)[N], F2 (&x)[N / 2]) {
 // N channels a thread: 16 bytes.  Tokens go in groups of U; a group inside one run
 // has no conditions.  Measured, bf16, W 4, SiLU: FWD_FIGURES
 template <typename T, int N, int W>
-__global__ void __launch_bounds__(kThreads, 4) conv_kernel(ConvArgs a, int len, int per_row) {
+__global__ void __launch_bounds__(kThreads, 3) conv_kernel(ConvArgs a, int len, int per_row) {
     using Raw = typename Vec<T, N>::Raw;
-    constexpr int U = 4, P = N / 2;
+    constexpr int U = sizeof(T) == 2 ? 8 : 4, P = N / 2;
     Strip s;
     if (!strip_of<N>(a, len, per_row, &s)) return;
     const bool act = a.flags & GDN_SILU;
@@ -212,9 +199,9 @@ __global__ void __launch_bounds__(kThreads, 4) conv_kernel(ConvArgs a, int len, 
 // conditions of a strip's and a run's ends took three times the arithmetic's
 // instructions.  Measured, bf16, W 4, SiLU: BWD_FIGURES
 template <typename T, int N, int W>
-__global__ void __launch_bounds__(kThreads, 4) conv_bwd_kernel(ConvArgs a, int len, int per_row, float *part) {
+__global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ConvArgs a, int len, int per_row, float *part) {
     using Raw = typename Vec<T, N>::Raw;
-    constexpr int U = sizeof(T) == 2 ? 4 : 2, P = N / 2;
+    constexpr int U = sizeof(T) == 2 ? 8 : 2, P = N / 2;
     Strip s;
     if (!strip_of<N>(a, len, per_row, &s)) return;
     const bool act = a.flags & GDN_SILU;
@@ -369,22 +356,12 @@ __global__ void __launch_bounds__(kThreads, 4) conv_bwd_kernel(ConvArgs a, int l
     *reinterpret_cast<typename Vec<float, N>::Raw *>(to + (size_t)W * a.C) = pack2<float, N>(db);
 }
 
-// dw [C,W] and db [C] from the strips' shares [n][W+1][C], in order: 32 places a
-// CTA, 32 strands of shares, then the strands.
-__global__ void __launch_bounds__(1024) conv_sum_kernel(const float *part, float *dw, float *db, int n, int C, int W) {
-    __shared__ float s[32][33];
-    const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5;
-    const long long all = (long long)(W + 1) * C, i = (long long)blockIdx.x * 32 + lane;
-    float x = 0.f;
-    if (i < all)
-#pragma unroll 4
-        for (int p = strand; p < n; p += 32) x += part[p * all + i];
-    s[strand][lane] = x;
-    __syncthreads();
-    if (strand != 0 || i >= all) return;
-    x = 0.f;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) x += s[j][lane];
+// dw [C,W] and db [C] from the strips' shares [n][W+1][C].
+template <int STRANDS>
+__global__ void __launch_bounds__(32 * STRANDS) conv_sum_kernel(const float *part, float *dw, float *db, int n, int C, int W) {
+    const long long all = (long long)(W + 1) * C, i = (long long)blockIdx.x * 32 + (threadIdx.x & 31);
+    const float x = mx::column_sum<STRANDS>(part, n, all, i);
+    if (threadIdx.x >= 32 || i >= all) return;
     const int j = (int)(i / C), c = (int)(i - (long long)j * C);
     if (j < W) dw[(size_t)c * W + j] = x;
     else if (db) db[c] = x;
@@ -480,7 +457,7 @@ int fwd(const ConvArgs &a, cudaStream_t stream) {
 
 // The shares of dw that a backward makes: at most this many strips, or a strip a row.
 constexpr int kMostStrips = 2048;
-constexpr long long kBwdThreads = 152 * 4 * kThreads;  // resident at once
+constexpr long long kBwdThreads = 152 * 3 * kThreads;  // resident at once
 Cut bwd_cut(int B, int T, int C) { return cut_rows(B, T, C / 4, kBwdThreads, kMostStrips); }
 
 template <typename T, int W>
@@ -492,7 +469,10 @@ int bwd(const ConvArgs &a, cudaStream_t stream) {
     conv_bwd_kernel<T, N, W><<<(unsigned)((threads + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a, c.len, c.per_row, part);
     const int st = mx::launched();
     if (st != GDN_OK) return st;
-    conv_sum_kernel<<<(unsigned)(((long long)(W + 1) * a.C + 31) / 32), 1024, 0, stream>>>(part, a.dw, a.db, c.per_row * a.B, a.C, W);
+    const unsigned ctas = (unsigned)(((long long)(W + 1) * a.C + 31) / 32);
+    const int n = c.per_row * a.B;
+    if (n <= 256) conv_sum_kernel<8><<<ctas, 256, 0, stream>>>(part, a.dw, a.db, n, a.C, W);
+    else conv_sum_kernel<32><<<ctas, 1024, 0, stream>>>(part, a.dw, a.db, n, a.C, W);
     return mx::launched();
 }
 

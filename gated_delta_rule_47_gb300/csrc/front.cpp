@@ -500,6 +500,11 @@ int64_t pages(const Tensor &pool, const Maybe &out, IntArrayRef shape, at::Scala
     const int64_t count = pool.size(0);
     dense(pool, {count, shape[0], shape[1]}, type);
     dense(out, pool.sizes(), type);
+    if (out && out.ptr() != pool.data_ptr()) {  // in place, or apart
+        const char *p = static_cast<const char *>(pool.data_ptr()), *q = static_cast<const char *>(out.ptr());
+        const int64_t bytes = pool.numel() * pool.element_size();
+        need(p + bytes <= q || q + bytes <= p);
+    }
     dense(slots, {B}, at::kInt);
     need(slots || B <= count);
     ints({B, count});

@@ -56,30 +56,34 @@ __device__ __forceinline__ void group_sum(float (&x)[K], float (*s)[kThreads / 3
     }
 }
 
-template <int N>
-__device__ __forceinline__ void load_weights(const float *w, int i, bool there, float (&x)[N]) {
-#pragma unroll
-    for (int e = 0; e < N; e += 4) {
-        float4 y = make_float4(1.f, 1.f, 1.f, 1.f);
-        if (w && there) y = __ldg(reinterpret_cast<const float4 *>(w + i + e));
-        x[e] = y.x, x[e + 1] = y.y, x[e + 2] = y.z, x[e + 3] = y.w;
-    }
-}
+using mx::F2;
 
-// V vectors a thread: vector j of thread t is number j NT + t.
-template <typename T, int NT, int V>
+// The gate's activation and its slope, of pairs: act = s m and slope = s ((1 - s) m
+// + k) with s the sigmoid; SiLU has m = gate and k = 1, the sigmoid m = 1 and k = 0.
+struct Act {
+    F2 k, rest;
+    __device__ __forceinline__ explicit Act(bool sigmoid) : k(mx::both(sigmoid ? 0.f : 1.f)), rest(mx::both(sigmoid ? 1.f : 0.f)) {}
+    __device__ __forceinline__ F2 factor(F2 gate) const { return mx::fma2(gate, k, rest); }
+    __device__ __forceinline__ F2 slope(F2 s, F2 m) const {
+        return mx::mul2(s, mx::fma2(mx::fma2(s, mx::both(-1.f), mx::both(1.f)), m, k));
+    }
+};
+
+// V vectors a thread: vector j of thread t is number j NT + t; what a row lacks is 0
+// and stays so.  Measured: FWD_FIGURES
+template <typename T, int NT, int V, bool FIRST>
 __global__ void __launch_bounds__(kThreads) gated_kernel(GatedNormArgs a, int strips) {
-    constexpr int N = kWide<T>;
+    constexpr int N = kWide<T>, P = N / 2;
     using Raw = typename Vec<T, N>::Raw;
     __shared__ float red[2][1][kThreads / 32];
     const Walk k = walk_of<NT>(a, strips);
     const int nv = a.D / N, tokens = a.B * a.T;
-    const bool first = a.flags & GDN_GATE_FIRST, sigmoid = a.flags & GDN_GATE_SIGMOID;
-    float w[V][N];
+    const Act act(a.flags & GDN_GATE_SIGMOID);
+    F2 w[V][P];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int i = j * NT + k.tid;
-        load_weights<N>(a.w, ((a.flags & GDN_W_SHARED) ? 0 : k.h * a.D) + i * N, i < nv, w[j]);
+        mx::weights2<N>(a.w + ((a.flags & GDN_W_SHARED) ? 0 : k.h * a.D) + i * N, a.w && i < nv, w[j]);
     }
     Raw nx[V], ng[V];
     auto fetch = [&](int token) {
@@ -98,11 +102,11 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedNormArgs a, int st
     int token = k.first < tokens ? k.first : tokens, buf = 0;
     fetch(token);
     for (int turn = 0; turn < turns; ++turn, buf ^= 1) {
-        float x[V][N], act[V][N], ss[1] = {0.f};
+        F2 x[V][P], g[V][P], s2 = 0;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            Vec<T, N>::unpack(nx[j], x[j]);
-            Vec<T, N>::unpack(ng[j], act[j]);
+            mx::unpack2<T, N>(nx[j], x[j]);
+            mx::unpack2<T, N>(ng[j], g[j]);
         }
         const int now = token;
         token = token < tokens - k.step ? token + k.step : tokens;
@@ -110,43 +114,47 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedNormArgs a, int st
 #pragma unroll
         for (int j = 0; j < V; ++j)
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float s = mx::sigmoid(act[j][e]);
-                act[j][e] = sigmoid ? s : act[j][e] * s;
-                if (first) x[j][e] = j * NT + k.tid < nv ? x[j][e] * act[j][e] : 0.f, act[j][e] = 1.f;
-                ss[0] = fmaf(x[j][e], x[j][e], ss[0]);
+            for (int e = 0; e < P; ++e) {
+                g[j][e] = mx::mul2(mx::sigmoid2(g[j][e]), act.factor(g[j][e]));
+                if (FIRST) x[j][e] = mx::mul2(x[j][e], g[j][e]);
+                s2 = mx::fma2(x[j][e], x[j][e], s2);
             }
+        float ss[1] = {mx::sum(s2)};
         group_sum<NT, 1>(ss, red[buf]);
-        const float r = rsqrtf(ss[0] / a.D + a.eps);
+        const F2 r = mx::both(rsqrtf(ss[0] / a.D + a.eps));
         if (now >= tokens) continue;
         Raw *y = reinterpret_cast<Raw *>(static_cast<T *>(a.y) + ((size_t)now * a.H + k.h) * a.D);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
 #pragma unroll
-            for (int e = 0; e < N; ++e) x[j][e] *= r * w[j][e] * act[j][e];
-            if (j * NT + k.tid < nv) __stcs(y + j * NT + k.tid, Vec<T, N>::pack(x[j]));
+            for (int e = 0; e < P; ++e) {
+                x[j][e] = mx::mul2(x[j][e], mx::mul2(r, w[j][e]));
+                if (!FIRST) x[j][e] = mx::mul2(x[j][e], g[j][e]);
+            }
+            if (j * NT + k.tid < nv) __stcs(y + j * NT + k.tid, mx::pack2<T, N>(x[j]));
         }
     }
 }
 
 // part: with a weight for each head [strips][H][D]; with one for all, a CTA's
-// groups are added up: [gridDim.x][D].
-template <typename T, int NT, int V>
-__global__ void __launch_bounds__(kThreads) gated_bwd_kernel(GatedNormArgs a, int strips, float *part) {
-    constexpr int N = kWide<T>, GROUPS = kThreads / NT;
+// groups are added up: [gridDim.x][D].  Measured: BWD_FIGURES
+template <typename T, int NT, int V, bool FIRST>
+__global__ void __launch_bounds__(kThreads, V == 1 ? 2 : 1) gated_bwd_kernel(GatedNormArgs a, int strips, float *part) {
+    constexpr int N = kWide<T>, P = N / 2, GROUPS = kThreads / NT;
     using Raw = typename Vec<T, N>::Raw;
     __shared__ float red[2][2][kThreads / 32];
     extern __shared__ __align__(16) float share[];  // [GROUPS][D], where the weight is shared
     const Walk k = walk_of<NT>(a, strips);
     const int nv = a.D / N, tokens = a.B * a.T;
-    const bool first = a.flags & GDN_GATE_FIRST, sigmoid = a.flags & GDN_GATE_SIGMOID, shared = a.flags & GDN_W_SHARED;
-    float w[V][N], dw[V][N];
+    const bool shared = a.flags & GDN_W_SHARED;
+    const Act act(a.flags & GDN_GATE_SIGMOID);
+    F2 w[V][P], dw[V][P];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int i = j * NT + k.tid;
-        load_weights<N>(a.w, (shared ? 0 : k.h * a.D) + i * N, i < nv, w[j]);
+        mx::weights2<N>(a.w + (shared ? 0 : k.h * a.D) + i * N, a.w && i < nv, w[j]);
 #pragma unroll
-        for (int e = 0; e < N; ++e) dw[j][e] = 0.f;
+        for (int e = 0; e < P; ++e) dw[j][e] = 0;
     }
     Raw nx[V], ng[V], nd[V];
     auto fetch = [&](int token) {
@@ -165,51 +173,50 @@ __global__ void __launch_bounds__(kThreads) gated_bwd_kernel(GatedNormArgs a, in
     int token = k.first < tokens ? k.first : tokens, buf = 0;
     fetch(token);
     for (int turn = 0; turn < turns; ++turn, buf ^= 1) {
-        Raw px[V], pg[V], pd[V];
+        F2 x[V][P], m[V][P], s[V][P], d[V][P], s2 = 0, p2 = 0;  // m: the activation's factor
 #pragma unroll
-        for (int j = 0; j < V; ++j) px[j] = nx[j], pg[j] = ng[j], pd[j] = nd[j];
+        for (int j = 0; j < V; ++j) {
+            mx::unpack2<T, N>(nx[j], x[j]);
+            mx::unpack2<T, N>(ng[j], s[j]);
+            mx::unpack2<T, N>(nd[j], d[j]);
+        }
         const int now = token;
         token = token < tokens - k.step ? token + k.step : tokens;
         fetch(token);
-        float x[V][N], g[V][N], s[V][N], d[V][N], sums[2] = {0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            Vec<T, N>::unpack(px[j], x[j]);
-            Vec<T, N>::unpack(pg[j], g[j]);
-            Vec<T, N>::unpack(pd[j], d[j]);
-            const bool there = j * NT + k.tid < nv;
+        for (int j = 0; j < V; ++j)
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                s[j][e] = mx::sigmoid(g[j][e]);
-                const float act = sigmoid ? s[j][e] : g[j][e] * s[j][e];
-                const float u = first ? (there ? x[j][e] * act : 0.f) : x[j][e];
-                const float t = first ? d[j][e] : (there ? d[j][e] * act : 0.f);
-                sums[0] = fmaf(u, u, sums[0]);
-                sums[1] = fmaf(u, t * w[j][e], sums[1]);
+            for (int e = 0; e < P; ++e) {
+                m[j][e] = act.factor(s[j][e]);
+                s[j][e] = mx::sigmoid2(s[j][e]);
+                const F2 f = mx::mul2(s[j][e], m[j][e]);
+                const F2 u = FIRST ? mx::mul2(x[j][e], f) : x[j][e], t = FIRST ? d[j][e] : mx::mul2(d[j][e], f);
+                s2 = mx::fma2(u, u, s2);
+                p2 = mx::fma2(u, mx::mul2(t, w[j][e]), p2);
             }
-        }
+        float sums[2] = {mx::sum(s2), mx::sum(p2)};
         group_sum<NT, 2>(sums, red[buf]);
-        const float r = rsqrtf(sums[0] / a.D + a.eps), m = r * r * (sums[1] / a.D);
+        const float r1 = rsqrtf(sums[0] / a.D + a.eps);
+        const F2 r = mx::both(r1), mean = mx::both(-r1 * r1 * (sums[1] / a.D));
         if (now >= tokens) continue;
         const int b = now / a.T, t0 = now - b * a.T;
         Raw *dx = reinterpret_cast<Raw *>(row_at(static_cast<T *>(a.dx), a.sdx, b, t0, k.h));
         Raw *dg = reinterpret_cast<Raw *>(static_cast<T *>(a.dgate) + ((size_t)now * a.H + k.h) * a.D);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            float ox[N], og[N];
+            F2 ox[P], og[P];
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float act = sigmoid ? s[j][e] : g[j][e] * s[j][e];
-                const float slope = sigmoid ? s[j][e] * (1.f - s[j][e]) : mx::silu_slope(g[j][e], s[j][e]);
-                const float u = first ? x[j][e] * act : x[j][e], t = first ? d[j][e] : d[j][e] * act;
-                const float du = r * fmaf(t, w[j][e], -u * m);
-                ox[e] = first ? du * act : du;
-                og[e] = first ? du * x[j][e] * slope : d[j][e] * w[j][e] * (u * r) * slope;
-                dw[j][e] = fmaf(t, u * r, dw[j][e]);
+            for (int e = 0; e < P; ++e) {
+                const F2 f = mx::mul2(s[j][e], m[j][e]), slope = act.slope(s[j][e], m[j][e]);
+                const F2 u = FIRST ? mx::mul2(x[j][e], f) : x[j][e], t = FIRST ? d[j][e] : mx::mul2(d[j][e], f);
+                const F2 du = mx::mul2(r, mx::fma2(u, mean, mx::mul2(t, w[j][e]))), n = mx::mul2(u, r);
+                ox[e] = FIRST ? mx::mul2(du, f) : du;
+                og[e] = mx::mul2(slope, FIRST ? mx::mul2(du, x[j][e]) : mx::mul2(n, mx::mul2(d[j][e], w[j][e])));
+                dw[j][e] = mx::fma2(t, n, dw[j][e]);
             }
             if (j * NT + k.tid < nv) {
-                __stcs(dx + j * NT + k.tid, Vec<T, N>::pack(ox));
-                __stcs(dg + j * NT + k.tid, Vec<T, N>::pack(og));
+                __stcs(dx + j * NT + k.tid, mx::pack2<T, N>(ox));
+                __stcs(dg + j * NT + k.tid, mx::pack2<T, N>(og));
             }
         }
     }
@@ -220,8 +227,7 @@ __global__ void __launch_bounds__(kThreads) gated_bwd_kernel(GatedNormArgs a, in
         const int i = j * NT + k.tid;
         if (i < nv && (mine || shared))
 #pragma unroll
-            for (int e = 0; e < N; e += 4)
-                *reinterpret_cast<float4 *>(to + i * N + e) = make_float4(dw[j][e], dw[j][e + 1], dw[j][e + 2], dw[j][e + 3]);
+            for (int e = 0; e < P; e += 2) *reinterpret_cast<ulonglong2 *>(to + i * N + 2 * e) = make_ulonglong2(dw[j][e], dw[j][e + 1]);
     }
     if (!shared) return;
     __syncthreads();
@@ -233,22 +239,10 @@ __global__ void __launch_bounds__(kThreads) gated_bwd_kernel(GatedNormArgs a, in
     }
 }
 
-// out[c] = the sum of part's rows [n][C], in order: 32 columns a CTA, 32 strands of
-// rows, then the strands.
 __global__ void __launch_bounds__(1024) gated_sum_kernel(const float *part, float *out, int n, int C) {
-    __shared__ float s[32][33];
-    const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-    float x = 0.f;
-    if (c < C)
-#pragma unroll 4
-        for (int i = strand; i < n; i += 32) x += part[(size_t)i * C + c];
-    s[strand][lane] = x;
-    __syncthreads();
-    if (strand != 0 || c >= C) return;
-    x = 0.f;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) x += s[j][lane];
-    out[c] = x;
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31);
+    const float x = mx::column_sum<32>(part, n, C, c);
+    if (threadIdx.x < 32 && c < C) out[c] = x;
 }
 
 // Threads of a group and vectors a thread, by a head's vectors; and how the tokens
@@ -261,29 +255,30 @@ int group_threads(int nv) {
 struct Cut {
     int strips, ctas;
 };
-constexpr int kMostCtas = 152 * 4;
-Cut cut_tokens(int B, int T, int H, int groups) {
+constexpr int kMostCtas = 152 * 3;  // of a backward, whose workspace holds their sums
+Cut cut_tokens(int B, int T, int H, int groups, int most) {
     const long long tokens = (long long)B * T;
-    long long strips = (long long)kMostCtas * groups / H;
+    long long strips = (long long)most * groups / H;
     if (strips < 1) strips = 1;
     if (strips > tokens) strips = tokens;
     return {(int)strips, (int)((strips * H + groups - 1) / groups)};
 }
 
-template <typename T, int NT, int V>
+template <typename T, int NT, int V, bool FIRST>
 int fwd(const GatedNormArgs &a, cudaStream_t stream) {
-    const Cut c = cut_tokens(a.B, a.T, a.H, kThreads / NT);
-    gated_kernel<T, NT, V><<<c.ctas, kThreads, 0, stream>>>(a, c.strips);
+    const Cut c = cut_tokens(a.B, a.T, a.H, kThreads / NT, mx::resident_ctas<gated_kernel<T, NT, V, FIRST>, kThreads>());
+    gated_kernel<T, NT, V, FIRST><<<c.ctas, kThreads, 0, stream>>>(a, c.strips);
     return mx::launched();
 }
-template <typename T, int NT, int V>
+template <typename T, int NT, int V, bool FIRST>
 int bwd(const GatedNormArgs &a, cudaStream_t stream) {
     constexpr int GROUPS = kThreads / NT;
-    const Cut c = cut_tokens(a.B, a.T, a.H, GROUPS);
+    const int fit = mx::resident_ctas<gated_bwd_kernel<T, NT, V, FIRST>, kThreads>();
+    const Cut c = cut_tokens(a.B, a.T, a.H, GROUPS, fit < kMostCtas ? fit : kMostCtas);
     const bool shared = a.flags & GDN_W_SHARED;
     float *part = static_cast<float *>(a.ws);
     const size_t room = shared ? sizeof(float) * GROUPS * a.D : 0;  // at most 32 KB: a group's threads grow with D
-    gated_bwd_kernel<T, NT, V><<<c.ctas, kThreads, room, stream>>>(a, c.strips, part);
+    gated_bwd_kernel<T, NT, V, FIRST><<<c.ctas, kThreads, room, stream>>>(a, c.strips, part);
     const int st = mx::launched();
     if (st != GDN_OK) return st;
     const int C = shared ? a.D : a.H * a.D;
@@ -295,7 +290,9 @@ int bwd(const GatedNormArgs &a, cudaStream_t stream) {
 template <typename T, bool BACK>
 int launch(const GatedNormArgs &a, cudaStream_t stream) {
     const int nv = a.D / kWide<T>;
-#define GO(NT, V) return BACK ? bwd<T, NT, V>(a, stream) : fwd<T, NT, V>(a, stream)
+#define GO(NT, V)                                                                                        \
+    return a.flags & GDN_GATE_FIRST ? (BACK ? bwd<T, NT, V, true>(a, stream) : fwd<T, NT, V, true>(a, stream)) \
+                                    : (BACK ? bwd<T, NT, V, false>(a, stream) : fwd<T, NT, V, false>(a, stream))
     switch (group_threads(nv)) {
         case 8: GO(8, 1);
         case 16: GO(16, 1);
@@ -320,7 +317,7 @@ size_t gated_norm_bwd_workspace(int B, int T, int H, int D, unsigned flags) {
     // the types' groups differ: the larger of both
     size_t most = 0;
     for (int n = 4; n <= 8; n += 4) {
-        const Cut c = cut_tokens(B, T, H, kThreads / group_threads(D / n));
+        const Cut c = cut_tokens(B, T, H, kThreads / group_threads(D / n), kMostCtas);
         const size_t rows = (flags & GDN_W_SHARED) ? (size_t)c.ctas : (size_t)c.strips * H;
         most = rows > most ? rows : most;
     }

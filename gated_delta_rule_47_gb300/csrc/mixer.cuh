@@ -119,6 +119,51 @@ __device__ __forceinline__ F2 sigmoid2(F2 x) {
     return pair(inverse(a), inverse(b));
 }
 __device__ __forceinline__ F2 silu_slope2(F2 x, F2 s) { return mul2(s, fma2(x, fma2(s, both(-1.f), both(1.f)), both(1.f))); }
+// N elements as pairs.
+template <typename T, int N>
+__device__ __forceinline__ void unpack2(const typename Vec<T, N>::Raw &p, F2 (&x)[N / 2]) {
+    float v[N];
+    Vec<T, N>::unpack(p, v);
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) x[e] = pair(v[2 * e], v[2 * e + 1]);
+}
+template <typename T, int N>
+__device__ __forceinline__ typename Vec<T, N>::Raw pack2(const F2 (&x)[N / 2]) {
+    float v[N];
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) split(x[e], v[2 * e], v[2 * e + 1]);
+    return Vec<T, N>::pack(v);
+}
+// N fp32 weights from w on as pairs, 1 where there are none.
+template <int N>
+__device__ __forceinline__ void weights2(const float *w, bool there, F2 (&x)[N / 2]) {
+#pragma unroll
+    for (int e = 0; e < N / 2; e += 2) {
+        float4 y = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (there) y = __ldg(reinterpret_cast<const float4 *>(w + 2 * e));
+        x[e] = pair(y.x, y.y), x[e + 1] = pair(y.z, y.w);
+    }
+}
+
+// The sum of column c of part's rows [n][C], in order: 32 columns a CTA, its
+// strands of rows, then the strands; the first strand's threads get it.
+template <int STRANDS>
+__device__ __forceinline__ float column_sum(const float *part, int n, long long C, long long c) {
+    __shared__ float s[STRANDS][33];
+    const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5;
+    float x = 0.f;
+    if (c < C)
+#pragma unroll 8
+        for (int i = strand; i < n; i += STRANDS) x += part[i * C + c];
+    s[strand][lane] = x;
+    __syncthreads();
+    x = 0.f;
+    if (strand == 0)
+#pragma unroll
+        for (int j = 0; j < STRANDS; ++j) x += s[j][lane];
+    return x;
+}
+
 // A grid of as many CTAs as the SMs hold at once.
 template <auto F, int NT>
 int resident_ctas() {

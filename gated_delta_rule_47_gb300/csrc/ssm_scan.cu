@@ -9,6 +9,7 @@
 // walks each chunk but the last from 0, then every chunk starts from what the
 // chunks before it leave, so that each exponential is taken twice.
 #include <algorithm>
+#include <type_traits>
 
 #include "ssm.cuh"
 
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, Shape<N>::CTAS) scan_kernel(SsmArgs 
 // Few warps are cut into more: as many as are resident at once.  A row that fills
 // half of them by itself stays whole, as every exponential of a cut row is taken
 // twice.
-constexpr int kJoin = 8;  // from so many chunks of a row on they are joined by a launch of its own
+constexpr int kJoin = 16;  // from so many chunks of a row on they are joined by a launch of its own
 template <int N>
 Plan plan(int B, int T, int Di) {
     Plan p{};
@@ -486,30 +487,43 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(SsmStepArgs a) {
     const int i = blockIdx.x * kStepThreads + threadIdx.x, c = i / L, q = i % L, groups = (a.B + R - 1) / R;
     const int b0 = blockIdx.y;  // rows b0, b0 + groups, ..
     if (c >= a.Di) return;  // a channel's lanes are there or not together
-    auto at = [](const void *p, long long i) {
+    using One = typename Vec<T, 1>::Raw;
+    using Four = typename Vec<T, 4>::Raw;
+    auto load = [](const void *p, long long i, auto *to) {
+        using Raw = std::remove_pointer_t<decltype(to)>;
+        *to = __ldg(reinterpret_cast<const Raw *>(static_cast<const T *>(p) + i));
+    };
+    auto one = [](const One &p) {
         float v[1];
-        Vec<T, 1>::unpack(__ldg(reinterpret_cast<const typename Vec<T, 1>::Raw *>(static_cast<const T *>(p) + i)), v);
+        Vec<T, 1>::unpack(p, v);
         return v[0];
     };
     auto two = [](const float4 &v, F2 (&x)[2]) { x[0] = pair(v.x, v.y), x[1] = pair(v.z, v.w); };
-    auto four = [](const void *p, long long i, F2 (&x)[2]) {
-        float v[4];
-        Vec<T, 4>::unpack(__ldg(reinterpret_cast<const typename Vec<T, 4>::Raw *>(static_cast<const T *>(p) + i)), v);
-        x[0] = pair(v[0], v[1]), x[1] = pair(v[2], v[3]);
-    };
     int slot[R];
-    float4 state[R][2];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int b = b0 + r * groups;
         slot[r] = b >= a.B ? -1 : a.slots ? __ldg(a.slots + b) : b;
         if (slot[r] >= a.n_slots) slot[r] = -1;
     }
+    // all of the rows' loads before any of their arithmetic
+    float4 state[R][2];
+    One x[R], dt[R], z[R];
+    Four B[R][2], C[R][2];
 #pragma unroll
     for (int r = 0; r < R; ++r)
         if (slot[r] >= 0) {
+            const int b = b0 + r * groups;
             const float4 *page = reinterpret_cast<const float4 *>(a.state + ((size_t)slot[r] * a.Di + c) * N);
             state[r][0] = __ldcs(page + q), state[r][1] = __ldcs(page + q + L);
+            load(a.x, b * a.sx + c, &x[r]);
+            load(a.dt, b * a.sdt + c, &dt[r]);
+            if (a.z) load(a.z, b * a.sz + c, &z[r]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                load(a.Bt, b * a.sB + 4 * (q + k * L), &B[r][k]);
+                load(a.Ct, b * a.sC + 4 * (q + k * L), &C[r][k]);
+            }
         }
     F2 A[2][2];
     two(__ldg(reinterpret_cast<const float4 *>(a.A + (size_t)c * N) + q), A[0]);
@@ -522,21 +536,21 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(SsmStepArgs a) {
         if (b >= a.B) break;
         float out[1] = {0.f};
         if (slot[r] >= 0) {
-            const float x = at(a.x, b * a.sx + c), v = at(a.dt, b * a.sdt + c) + bias;
+            const float xv = one(x[r]), v = one(dt[r]) + bias;
             const float step = (a.flags & GDN_DT_SOFTPLUS) ? mx::softplus(v) : v;
-            const F2 u = both(step * x), d = both(step * mx::kLog2e);
+            const F2 u = both(step * xv), d = both(step * mx::kLog2e);
             F2 o = 0;
             float4 *page = reinterpret_cast<float4 *>(a.state_out + ((size_t)slot[r] * a.Di + c) * N);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                F2 h[2], B[2], C[2];
-                four(a.Bt, b * a.sB + 4 * (q + k * L), B);
-                four(a.Ct, b * a.sC + 4 * (q + k * L), C);
+                F2 h[2], bs[2], cs[2];
+                mx::unpack2<T, 4>(B[r][k], bs);
+                mx::unpack2<T, 4>(C[r][k], cs);
                 two(state[r][k], h);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    h[m] = fma2(exp2_2(mul2(d, A[k][m])), h[m], mul2(u, B[m]));
-                    o = fma2(C[m], h[m], o);
+                    h[m] = fma2(exp2_2(mul2(d, A[k][m])), h[m], mul2(u, bs[m]));
+                    o = fma2(cs[m], h[m], o);
                 }
                 float4 n;
                 split(h[0], n.x, n.y), split(h[1], n.z, n.w);
@@ -545,10 +559,10 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(SsmStepArgs a) {
             out[0] = sum(o);
 #pragma unroll
             for (int m = 1; m < L; m <<= 1) out[0] += __shfl_xor_sync(mask, out[0], m);
-            out[0] = fmaf(skip, x, out[0]);
-            if (a.z) out[0] *= mx::silu(at(a.z, b * a.sz + c));
+            out[0] = fmaf(skip, xv, out[0]);
+            if (a.z) out[0] *= mx::silu(one(z[r]));
         }
-        if (q == 0) *reinterpret_cast<typename Vec<T, 1>::Raw *>(static_cast<T *>(a.y) + (size_t)b * a.Di + c) = Vec<T, 1>::pack(out);
+        if (q == 0) *reinterpret_cast<One *>(static_cast<T *>(a.y) + (size_t)b * a.Di + c) = Vec<T, 1>::pack(out);
     }
 }
 
@@ -568,8 +582,8 @@ int step(const SsmStepArgs &a, cudaStream_t stream) {
             p.n_slots = a.n_slots - b0;
         }
         const unsigned ctas = (unsigned)(((long long)a.Di * (N / 8) + kStepThreads - 1) / kStepThreads);
-        // four rows a thread where that leaves each SM eight CTAs
-        if ((long long)ctas * p.B >= 4LL * 8 * device_sm_count()) step_kernel<T, N, 4><<<dim3(ctas, (p.B + 3) / 4), kStepThreads, 0, stream>>>(p);
+        // two rows a thread where that leaves each SM eight CTAs; four were slower (256 rows of 2048 channels: 22 us against 16)
+        if ((long long)ctas * p.B >= 2LL * 8 * device_sm_count()) step_kernel<T, N, 2><<<dim3(ctas, (p.B + 1) / 2), kStepThreads, 0, stream>>>(p);
         else step_kernel<T, N, 1><<<dim3(ctas, p.B), kStepThreads, 0, stream>>>(p);
         const int st = mx::launched();
         if (st != GDN_OK) return st;

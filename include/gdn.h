@@ -710,8 +710,10 @@ int causal_conv_bwd(const void *x, const float *weight, const float *bias, const
  * causal_conv_step -- one token of each of B requests against a pool of windows.
  *   x [B,C] dtype, rows x_stride elements apart (not negative, a multiple of 16
  *   bytes); y [B,C] contiguous, not x
- *   window, window_out [n_slots,W-1,C] dtype; window_out may be window itself
- *   slots int32 [B] or NULL, as in linattn_step: an idle row gets y = 0
+ *   window, window_out [n_slots,W-1,C] dtype; window_out may be window itself, but
+ *   not overlap it otherwise
+ *   slots int32 [B] or NULL, as in linattn_step: an idle row gets y = 0, and rows
+ *   may not share a page
  */
 int causal_conv_step(const void *x, const float *weight, const float *bias, const void *window, void *window_out,
                      const int *slots, void *y, long long x_stride, int B, int C, int W, int n_slots, unsigned flags,
@@ -767,8 +769,9 @@ int ssm_scan_bwd(const void *x, const void *dt, const float *A, const void *Bt, 
  *   x, dt, z [B,Di], Bt, Ct [B,N] dtype; strides: host array of 5 row strides (x,
  *   dt, Bt, Ct, z; not negative, multiples of 16 bytes) or NULL for contiguous
  *   tensors; y [B,Di] contiguous
- *   state, state_out [n_slots,Di,N] fp32; state_out may be state itself
- *   slots as in linattn_step: an idle row gets y = 0
+ *   state, state_out [n_slots,Di,N] fp32; state_out may be state itself, but not
+ *           overlap it otherwise
+ *   slots as in linattn_step: an idle row gets y = 0, and rows may not share a page
  */
 int ssm_step(const void *x, const void *dt, const float *A, const void *Bt, const void *Ct, const float *skip,
              const void *z, const float *dt_bias, const float *state, float *state_out, const int *slots, void *y,
