@@ -152,7 +152,6 @@ static_assert(2 * WB_PER_GROUP <= 32, "WY barriers fit their 256 bytes");
 
 // Per-chunk vectors of one WY pipeline.
 struct Misc {
-    alignas(16) unsigned long long tag[2];  // ring mode: the ready tag being published
     float beta[64];   // beta of each row (0 past the end)
     float gam[64];    // within-chunk cumulative log-decay
     float n[64];      // 1/||k_s|| with GDN_QK_L2NORM, else 1
@@ -820,17 +819,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (flat && shipper)
                 for (int i = 0; i < kMaxRingHeads; ++i) ms->ccache[i] = 0u;
             int pend = -1, pend_tag = 0;  // ring mode, shipper: slot and tag still to publish
-            // Publishing a slot: once its copies are complete, the ready tag goes
-            // out as one more bulk copy (16 B from shared memory), which costs the
-            // thread far less than a release store.
+            // Publishing a slot: once its copies are complete, the ready tag is
+            // released.  As one more bulk copy behind theirs it cost the thread 1.1K
+            // cycles less, but nothing orders the two for another SM: half of the
+            // launches at B4 H16 T4096 gave a head's tokens from a stale slot.
             auto publish = [&]() {
                 if (pend >= 0) {
-                    tma_store_wait_all<0>();  // the slot's bytes, and the previous tag, are written
-                    ms->tag[0] = ((unsigned long long)p.epoch << 32) | (unsigned)pend_tag;
-                    ms->tag[1] = 0ull;
-                    fence_proxy_async_smem();
-                    bulk_store_global(p.ready + 2 * pend, ms->tag, 16);
-                    tma_store_commit();
+                    tma_store_wait_all<0>();  // the slot's bytes are written
+                    fence_proxy_async_global();
+                    st_release_gpu(p.ready + 2 * pend, ((unsigned long long)p.epoch << 32) | (unsigned)pend_tag);
                     pend = -1;
                 }
             };
