@@ -162,7 +162,7 @@ struct Misc {
     float qp[2][64];  // partial q_t^2 sums over the two key-dim halves
     int safe;         // 1 if |gam_t - gam_0| <= 80 for all rows (factorised exponentials)
     unsigned ccache[80];  // ring mode: chunks each head's scan CTA was last seen to have taken out
-    float pad[107];
+    float pad[111];
 };
 static_assert(sizeof(Misc) == 3072, "Misc layout");
 
