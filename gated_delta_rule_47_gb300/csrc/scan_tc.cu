@@ -1412,9 +1412,9 @@ int launch_ring(const ScanArgs &a, TcParams p, const CUtensorMap &mK, const CUte
     p.ring = ws;
     p.ready = reinterpret_cast<unsigned long long *>(ws + (size_t)BH * kRing * kShipBytes);
     p.cons = p.ready + (size_t)BH * kRing * 2;
-    unsigned e = ++g_epoch;
-    if (e == 0) e = ++g_epoch;
-    p.epoch = e;
+    // From 0xffc00000 on, short of 0xffffffff: what a workspace held before (small
+    // whole numbers such as offsets, values, bytes of one kind) has no such words.
+    p.epoch = 0xffc00000u + (++g_epoch) % 0x3fffffu;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3((unsigned)(BH + nwy));

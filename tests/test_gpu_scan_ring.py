@@ -30,3 +30,20 @@ def test_equal_launches_give_equal_bits(name, idle):
             torch.cuda.synchronize()
         differ += (f(d["q"], d["k"], d["v"], d["beta"], d["g"], chunk=w.chunk)[0] != first).any()
     assert int(differ) == 0 and binding.device_error() == 0
+
+
+def test_whole_numbers_in_the_workspace_are_no_tags():
+    """A workspace that held pairs of small whole numbers (offsets, lengths beside sequence numbers): none of
+    them counts as a tag, whichever number of launches the process has made."""
+    gen = torch.Generator().manual_seed(3)
+    q, k = (torch.nn.functional.normalize(torch.randn(1, 2, 640, 128, generator=gen), dim=-1).bfloat16().cuda() for _ in range(2))
+    v = torch.randn(1, 2, 640, 128, generator=gen).bfloat16().cuda()
+    beta, g = torch.rand(1, 2, 640, generator=gen).bfloat16().cuda(), -torch.rand(1, 2, 640, generator=gen).cuda() / 16
+    ws = torch.zeros(binding.workspace_bytes(1, 2, 640, 128, 128), dtype=torch.uint8, device="cuda")
+    first = binding.gdn_chunk_fwd(q, k, v, beta, g, workspace=ws)[0].clone()
+    room = ws[: ws.numel() // 8 * 8].view(torch.int32).view(-1, 2)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for n in range(3000):
+        room[:, 0], room[:, 1] = 1000, 3000  # the launch of that number would take every slot for filled
+        differ += (binding.gdn_chunk_fwd(q, k, v, beta, g, workspace=ws)[0] != first).any()
+    assert int(differ) == 0 and binding.device_error() == 0
