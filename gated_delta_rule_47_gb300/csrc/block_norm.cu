@@ -289,7 +289,9 @@ int per_group(long long rows, int groups, int most) {
     const long long each = rows / g, per = most / g;
     return (int)(per < 1 ? 1 : per < each ? per : each);
 }
-constexpr int kMostBwd = 152 * 4;  // what a backward's workspace holds the sums of
+// CTAs of a backward, whose workspace holds their sums: narrow rows have few threads
+// a CTA (30230 x 88: 38 us with four CTAs an SM, NARROW_FIGURES).
+int most_bwd(int C) { return 152 * (C <= 512 ? 12 : C <= 1024 ? 8 : 4); }
 
 template <typename T, int NT, int V, bool BACK>
 int go(const BlockNormArgs &a, cudaStream_t stream) {
@@ -300,7 +302,7 @@ int go(const BlockNormArgs &a, cudaStream_t stream) {
         return mx::launched();
     } else {
         const int fit = mx::resident_ctas<block_bwd_kernel<T, NT, V>, NT>();
-        const int per = per_group(a.rows, a.groups, fit < kMostBwd ? fit : kMostBwd);
+        const int most = most_bwd(a.C), per = per_group(a.rows, a.groups, fit < most ? fit : most);
         float *part = static_cast<float *>(a.ws);
         block_bwd_kernel<T, NT, V><<<groups * per, NT, 0, stream>>>(a, per, part);
         const int st = mx::launched();
@@ -329,7 +331,7 @@ int launch_block_norm(const BlockNormArgs &a, cudaStream_t stream) {
     return a.dtype == GDN_BF16 ? launch<__nv_bfloat16, false>(a, stream) : launch<float, false>(a, stream);
 }
 size_t block_norm_bwd_workspace(long long rows, int C, int groups) {
-    return sizeof(float) * 2 * C * (size_t)(groups ? groups : 1) * per_group(rows, groups, kMostBwd);
+    return sizeof(float) * 2 * C * (size_t)(groups ? groups : 1) * per_group(rows, groups, most_bwd(C));
 }
 int launch_block_norm_bwd(const BlockNormArgs &a, cudaStream_t stream) {
     return a.dtype == GDN_BF16 ? launch<__nv_bfloat16, true>(a, stream) : launch<float, true>(a, stream);

@@ -9,6 +9,7 @@
 // walks each chunk but the last from 0, then every chunk starts from what the
 // chunks before it leave, so that each exponential is taken twice.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "ssm.cuh"
@@ -159,11 +160,11 @@ struct Place {
 };
 template <int N>
 __device__ __forceinline__ bool place_of(const SsmArgs &a, const Plan &p, int chunks, Place *w) {
-    const int groups = (p.blocks + kWarps - 1) / kWarps;
-    const int g = blockIdx.x % groups, item = blockIdx.x / groups;
-    w->block = g * kWarps + (threadIdx.x >> 5);
-    w->row = item / chunks, w->chunk = item - w->row * chunks;
-    if (w->block >= p.blocks) return false;
+    const long long i = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const long long item = i / p.blocks;
+    w->block = (int)(i - item * p.blocks);
+    w->row = (int)(item / chunks), w->chunk = (int)(item - (long long)w->row * chunks);
+    if (w->row >= a.B) return false;
     w->c = w->block * Shape<N>::BLOCK + (threadIdx.x & 31) * Shape<N>::CH;
     w->there = w->c < a.Di;
     w->t0 = w->chunk * p.len, w->t1 = min(w->t0 + p.len, a.T);
@@ -274,7 +275,9 @@ __global__ void __launch_bounds__(32 * Shape<N>::V) join_kernel(SsmArgs a, Plan 
     ulonglong2 *state = reinterpret_cast<ulonglong2 *>(p.state) + i * 32 + lane;
     const float *steps = p.steps + e * 32 + lane;
     F2 h0 = 0, h1 = 0;
+    int starts = 0;  // where the run at the end of chunk j + lane starts, for each 32 chunks
     for (int j0 = 0; j0 + 1 < p.chunks; j0 += AHEAD) {
+        if (j0 % 32 == 0) starts = mx::run_at(a.cu, a.n_seq, a.T, row, (int)min((long long)(j0 + lane + 1) * p.len, (long long)a.T) - 1).start;
         ulonglong2 v[AHEAD];
         float d[AHEAD];
 #pragma unroll
@@ -287,8 +290,7 @@ __global__ void __launch_bounds__(32 * Shape<N>::V) join_kernel(SsmArgs a, Plan 
         for (int k = 0; k < AHEAD; ++k) {
             const int j = j0 + k;
             if (j + 1 >= p.chunks) break;
-            const Run r = mx::run_at(a.cu, a.n_seq, a.T, row, min((j + 1) * p.len, a.T) - 1);
-            if (r.start >= j * p.len) h0 = v[k].x, h1 = v[k].y;
+            if (__shfl_sync(~0u, starts, j % 32) >= j * p.len) h0 = v[k].x, h1 = v[k].y;
             else h0 = fma2(exp2_2(mul2(both(d[k]), A0)), h0, v[k].x), h1 = fma2(exp2_2(mul2(both(d[k]), A1)), h1, v[k].y);
             state[share_at(p, row, j, block) * V * 32] = make_ulonglong2(h0, h1);
         }
@@ -438,17 +440,19 @@ __global__ void __launch_bounds__(kThreads, Shape<N>::CTAS) scan_kernel(SsmArgs 
 
 // Few warps are cut into more: as many as are resident at once.  A row that fills
 // half of them by itself stays whole, as every exponential of a cut row is taken
-// twice.
+// twice.  A chunk has sqrt(T) tokens or more: joining a chunk takes a launch about
+// as long as walking one more token (40 channels of 18531 tokens: 442 us in 1158
+// chunks, JOIN_FIGURES).
 constexpr int kJoin = 16;  // from so many chunks of a row on they are joined by a launch of its own
 template <int N>
 Plan plan(int B, int T, int Di) {
     Plan p{};
     p.blocks = (Di + Shape<N>::BLOCK - 1) / Shape<N>::BLOCK;
     const long long whole = (long long)B * p.blocks, resident = 152 * Shape<N>::CTAS * kWarps;
-    long long chunks = whole * 2 >= resident ? 1 : resident / whole;
-    long long len = ((T + chunks - 1) / chunks + kTile - 1) / kTile * kTile;
-    p.len = (int)len;
-    p.chunks = (int)((T + len - 1) / len);
+    const long long chunks = whole * 2 >= resident ? 1 : resident / whole;
+    const long long len = std::max((T + chunks - 1) / chunks, (long long)std::sqrt((double)T));
+    p.len = (int)((len + kTile - 1) / kTile * kTile);
+    p.chunks = (T + p.len - 1) / p.len;
     return p;
 }
 Plan plan_of(int B, int T, int Di, int N) { return N == 8 ? plan<8>(B, T, Di) : N == 16 ? plan<16>(B, T, Di) : plan<32>(B, T, Di); }
@@ -459,9 +463,9 @@ int fwd(const SsmArgs &a, cudaStream_t stream) {
     const size_t shares = (size_t)a.B * p.chunks * p.blocks;
     p.state = static_cast<float *>(a.ws);
     p.steps = p.state + shares * 128 * Shape<N>::V;
-    const long long groups = (p.blocks + kWarps - 1) / kWarps;
+    auto ctas = [&](int chunks) { return (unsigned)(((long long)a.B * chunks * p.blocks + kWarps - 1) / kWarps); };
     if (p.chunks > 1) {
-        share_kernel<T, N><<<(unsigned)(groups * a.B * (p.chunks - 1)), kThreads, 0, stream>>>(a, p);
+        share_kernel<T, N><<<ctas(p.chunks - 1), kThreads, 0, stream>>>(a, p);
         int st = mx::launched();
         if (st != GDN_OK) return st;
         p.joined = p.chunks >= kJoin;
@@ -471,8 +475,8 @@ int fwd(const SsmArgs &a, cudaStream_t stream) {
             if (st != GDN_OK) return st;
         }
     }
-    if (a.z) scan_kernel<T, N, true><<<(unsigned)(groups * a.B * p.chunks), kThreads, 0, stream>>>(a, p);
-    else scan_kernel<T, N, false><<<(unsigned)(groups * a.B * p.chunks), kThreads, 0, stream>>>(a, p);
+    if (a.z) scan_kernel<T, N, true><<<ctas(p.chunks), kThreads, 0, stream>>>(a, p);
+    else scan_kernel<T, N, false><<<ctas(p.chunks), kThreads, 0, stream>>>(a, p);
     return mx::launched();
 }
 

@@ -19,12 +19,13 @@
 // A thread holds 4 channels x 4 states, as pairs of channels: what belongs to a
 // channel is loaded as a pair, and B and C lie in shared memory twice over.  The
 // sums over a channel's lanes and, for dB and dC, over the channels' go through
-// shared memory, two and four tokens at a time: by shuffles they took 64 and 28
+// shared memory, two or four tokens at a time: by shuffles they took 64 and 28
 // instructions a token and warp, so they take 11 and 8.  The other way round (all
 // states of a channel in a thread, as forwards) would need 32 values of a token
 // summed over 32 lanes.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "ssm.cuh"
@@ -47,6 +48,7 @@ struct Shape {
     static constexpr int RV = CH / V;     // vectors of a token's channels
     static constexpr int NV = kBlock * RV, VPL = (NV + 31) / 32;  // of a block; of a lane
     static constexpr int BV = N / V;      // vectors of a token's B
+    static constexpr int SLOTS = N == 16 ? 4 : 2;  // tokens whose dB and dC are summed over channels at once
     static constexpr int NB = kBlock * BV, BPL = (2 * NB + 31) / 32;
 };
 
@@ -78,7 +80,7 @@ struct GradMem : Mem<T, N> {
     float4 start[4][32];                      // the state that enters the chunk
     float part[2][kBlock][2 * N];             // a block's dB and dC of this warp
     float over_states[2][3][S::L][S::CH + 8]; // two tokens' D's and x's gradients and y, of each lane of a channel
-    float over_channels[4][S::G][2 * N + 4];  // four tokens' dB and dC, of each lane of the channels
+    float over_channels[S::SLOTS][S::G][2 * N + 4];  // some tokens' dB and dC, of each lane of the channels
     float4 acc[2][S::VPL * S::V / 4][32];     // dskip and dbias of each lane's vectors
 };
 
@@ -434,17 +436,29 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
             }
         }
     }
-    // x <- what chunk j gives + its decay x, from the first one named on
-    auto join = [&](const float *from, int j, bool first, Quad &x) {
-        const size_t at = chunk_at(a, p, w.row, j);
-        Quad v;
-        load16<N>(a, w, from + at * N, v);
-        F2 d[2] = {0, 0};
-        if (w.c < a.Di) channels(p.steps + at + w.c, d);
+    // x <- what chunk j gives + its decay x, for n chunks from j on in steps of `step`;
+    // four chunks' loads at a time
+    auto join = [&](const float *from, int j, int step, int n, Quad &x) {
+        for (int i0 = 0; i0 < n; i0 += 4) {
+            Quad v[4];
+            F2 d[4][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+            for (int k = 0; k < 4; ++k)
+                if (i0 + k < n) {
+                    const size_t at = chunk_at(a, p, w.row, j + (i0 + k) * step);
+                    load16<N>(a, w, from + at * N, v[k]);
+                    d[k][0] = d[k][1] = 0;
+                    if (w.c < a.Di) channels(p.steps + at + w.c, d[k]);
+                }
 #pragma unroll
-            for (int n = 0; n < 4; ++n) x[i][n] = first ? v[i][n] : fma2(exp2_2(mul2(d[i], A[i][n])), x[i][n], v[i][n]);
+            for (int k = 0; k < 4; ++k)
+                if (i0 + k < n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            x[i][q] = i0 + k == 0 ? v[k][i][q] : fma2(exp2_2(mul2(d[k][i], A[i][q])), x[i][q], v[k][i][q]);
+        }
     };
     Run r = mx::run_at(a.cu, a.n_seq, a.T, w.row, w.t0);
     const int entered = r.s >= 0 && r.start < w.t0 ? r.end : w.t0;  // the entering state matters up to here
@@ -453,14 +467,14 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
         zero16(h);
         if (entered > w.t0) {
             const int first = min(r.start / p.len, w.chunk - 1);
-            for (int j = first; j < w.chunk; ++j) join(p.left, j, j == first, h);
+            join(p.left, first, 1, w.chunk - first, h);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) *reinterpret_cast<ulonglong2 *>(&m.start[e][lane]) = quad_vector(h, e);
         r = mx::run_at(a.cu, a.n_seq, a.T, w.row, w.t1 - 1);
         if (r.s >= 0 && r.end > w.t1) {
             const int end = max((r.end - 1) / p.len, w.chunk + 1);
-            for (int j = end; j > w.chunk; --j) join(p.back, j, j == end, g);
+            join(p.back, end, -1, end - w.chunk, g);
         }
     }
     int buf = 0;
@@ -560,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
                 put(0, ds);
                 put(1, dx);
                 if (a.z) put(2, y);
-                float *row = m.over_channels[u & 3][w.g];
+                float *row = m.over_channels[u % S::SLOTS][w.g];
                 *reinterpret_cast<float4 *>(row + 4 * w.q) = make_float4(sum(dB[0]), sum(dB[1]), sum(dB[2]), sum(dB[3]));
                 *reinterpret_cast<float4 *>(row + N + 4 * w.q) = make_float4(sum(dC[0]), sum(dC[1]), sum(dC[2]), sum(dC[3]));
                 if ((u & 1) != 0) continue;
@@ -576,9 +590,9 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
                     }
                     *reinterpret_cast<ulonglong2 *>(&m.step[0][0] + (what * kBlock + u + tok) * S::CH + c4) = make_ulonglong2(p0, p1);
                 }
-                if ((u & 3) == 0)
+                if (u % S::SLOTS == 0)
 #pragma unroll
-                    for (int i = lane; i < 2 * N; i += 32) {
+                    for (int i = lane; i < S::SLOTS * N / 2; i += 32) {
                         const int tok = i / (N / 2), n = i % (N / 2) * 4;
                         F2 p0 = 0, p1 = 0;
 #pragma unroll
@@ -705,18 +719,35 @@ __global__ void __launch_bounds__(256) sum_kernel(SsmArgs a, Plan p, int tokens_
     *to = s;
 }
 
-// Two waves of grad_kernel's CTAs: more would join more chunks at the start of
-// each, fewer leave SMs idle.  A chunk has 64 tokens or more.
-constexpr int kResident = 152 * 2;
+// CTAs of grad_kernel on an SM, by its shared memory (228 KB, 1 KB of it for each).
+template <typename T, int N>
+constexpr int kPerSm = 2 * (sizeof(GradMem<T, N>) * kWarps + 1024) <= 228 * 1024 ? 2 : 1;
+int per_sm(int N, int dtype) {
+    using B16 = __nv_bfloat16;
+    if (dtype == GDN_BF16) return N == 8 ? kPerSm<B16, 8> : N == 16 ? kPerSm<B16, 16> : kPerSm<B16, 32>;
+    return N == 8 ? kPerSm<float, 8> : N == 16 ? kPerSm<float, 16> : kPerSm<float, 32>;
+}
 int channels(int N) { return kWarps * 4 * (32 / (N / 4)); }
-Plan plan(int B, int T, int Di, int N, float *ws, size_t *bytes) {
+
+// The chunks' length: what a wave of grad_kernel's CTAs takes is about its tokens
+// and half a token's time for each chunk of the row, which it joins at its start.
+// Candidates are what fills up to four waves, and lengths a quarter apart.
+Plan plan(int B, int T, int Di, int N, int dtype, float *ws, size_t *bytes) {
     Plan p{};
     p.groups = (Di + channels(N) - 1) / channels(N);
-    const long long whole = (long long)B * p.groups;
-    const long long chunks = std::max(1LL, 2LL * kResident / whole);
-    const long long len = std::max(64LL, ((T + chunks - 1) / chunks + kBlock - 1) / kBlock * kBlock);
-    p.len = (int)len;
-    p.chunks = (int)((T + len - 1) / len);
+    const long long whole = (long long)B * p.groups, resident = 152LL * per_sm(N, dtype);
+    double best = 0.;
+    auto consider = [&](long long tokens) {
+        const long long len = std::min((std::max(tokens, 1LL) + kBlock - 1) / kBlock * kBlock, ((long long)T + kBlock - 1) / kBlock * kBlock);
+        const long long chunks = (T + len - 1) / len, waves = (whole * chunks + resident - 1) / resident;
+        const double cost = (double)waves * ((double)len + 0.5 * (double)chunks);
+        if (p.len == 0 || cost < best) best = cost, p.len = (int)len, p.chunks = (int)chunks;
+    };
+    for (int w = 1; w <= 4; ++w) {
+        const long long chunks = std::max(1LL, w * resident / whole);
+        consider((T + chunks - 1) / chunks);
+    }
+    for (long long len = kBlock; len < T; len += std::max((long long)kBlock, len / 4)) consider(len);
     p.blocks = (T + kBlock - 1) / kBlock;
     size_t at = 0;
     auto take = [&](float **x, size_t n) { *x = ws ? ws + at : nullptr, at += (n + 3) / 4 * 4; };
@@ -751,7 +782,7 @@ bool room(int bytes) {
 template <typename T, int N>
 int bwd(const SsmArgs &a, cudaStream_t stream) {
     size_t bytes;
-    const Plan p = plan(a.B, a.T, a.Di, N, static_cast<float *>(a.ws), &bytes);
+    const Plan p = plan(a.B, a.T, a.Di, N, a.dtype, static_cast<float *>(a.ws), &bytes);
     constexpr int one = sizeof(Mem<T, N>) * kWarps, two = sizeof(GradMem<T, N>) * kWarps;
     if (!room<share_kernel<T, N>>(one) || !room<grad_kernel<T, N>>(two)) return GDN_ERR_CUDA;
     const unsigned ctas = (unsigned)((long long)p.groups * a.B * p.chunks);
@@ -768,9 +799,9 @@ int bwd(const SsmArgs &a, cudaStream_t stream) {
 
 }  // namespace
 
-size_t ssm_bwd_workspace(int B, int T, int Di, int N, int) {
+size_t ssm_bwd_workspace(int B, int T, int Di, int N, int dtype) {
     size_t bytes;
-    plan(B, T, Di, N, nullptr, &bytes);
+    plan(B, T, Di, N, dtype, nullptr, &bytes);
     return bytes;
 }
 
