@@ -813,16 +813,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t rf_par = 0;  // thread 0: parity of the next RECV_FREE phase, bit 2 * head + slot
             bool ship_ok = true;
             // The thread that ships: thread 0 into the cluster; in ring mode lane 0
-            // of warp 5, which is idle while warps 0 and 1 form the chunk's factors
+            // of warp 5, which is idle while warps 0 and 1 invert the diagonal blocks
             // and publishes the previous shipment then.
             const bool shipper = flat ? wt == 160 : wt == 0;
             if (flat && shipper)
                 for (int i = 0; i < kMaxRingHeads; ++i) ms->ccache[i] = 0u;
             int pend = -1, pend_tag = 0;  // ring mode, shipper: slot and tag still to publish
             // Publishing a slot: once its copies are complete, the ready tag is
-            // released.  As one more bulk copy behind theirs it cost the thread 1.1K
-            // cycles less, but nothing orders the two for another SM: half of the
-            // launches at B4 H16 T4096 gave a head's tokens from a stale slot.
+            // released, which takes the thread about 1.1K cycles: B4 H16 T4096 0.176 ms
+            // while the factors are formed, 0.162 in the longer time of the inverses.
+            // As one more bulk copy behind theirs it takes less (0.160), but nothing
+            // orders the two for another SM: half of the launches gave a head's tokens
+            // from a stale slot.
             auto publish = [&]() {
                 if (pend >= 0) {
                     tma_store_wait_all<0>();  // the slot's bytes are written
@@ -911,8 +913,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ms->ea[wt] = __expf(gi - g0);
                     vec[V_SEF + wt] = __expf(gl - gi) * ni;
                     vec[V_QS + wt] = wt < NQ ? __expf(ms->gam[wt * R + R - 1]) * mi : 0.f;
-                } else if (flat && shipper) {
-                    publish();  // the previous chunk's ring slot, while warps 0-1 form the factors
                 }
                 named_bar(bar_id, 256);
                 if (wt == 0) GDN_TR(c, 35 + 16 * g);
@@ -1010,6 +1010,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = j + 1; i < 16; ++i) pp[i] += AF[(16 * db + i) * kAS + 16 * db + j] * xs[j];
                     }
+                } else if (flat && shipper) {
+                    publish();  // the previous chunk's ring slot, while warps 0-1 invert the diagonal blocks
                 }
                 named_bar(bar_id, 256);
                 if (wt == 0) GDN_TR(c, 37 + 16 * g);
