@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedNormArgs a, int st
         }
     };
     // every group of a CTA takes as many turns, so that warps stay whole
-    const int turns = (tokens + strips - 1) / strips;
+    const int turns = (tokens - 1) / strips + 1;
     int token = k.first < tokens ? k.first : tokens, buf = 0;
     fetch(token);
     for (int turn = 0; turn < turns; ++turn, buf ^= 1) {
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 2 : 1) gated_bwd_kernel(Gat
             if (token < tokens && i < nv) nx[j] = __ldcs(x + i), ng[j] = __ldcs(g + i), nd[j] = __ldcs(d + i);
         }
     };
-    const int turns = (tokens + strips - 1) / strips;
+    const int turns = (tokens - 1) / strips + 1;
     int token = k.first < tokens ? k.first : tokens, buf = 0;
     fetch(token);
     for (int turn = 0; turn < turns; ++turn, buf ^= 1) {

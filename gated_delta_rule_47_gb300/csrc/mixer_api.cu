@@ -272,6 +272,7 @@ int check_gated(int B, int T, int H, int D, float eps, unsigned flags, int dtype
     if (B < 0 || T < 0 || H < 0 || D < 0 || !(eps >= 0.f) || bad_type(dtype)) return GDN_ERR_INVALID_ARG;
     if (flags & ~(GDN_GATE_FIRST | GDN_GATE_SIGMOID | GDN_W_SHARED)) return GDN_ERR_INVALID_ARG;
     if (D % wide(dtype) != 0 || D > 8192) return GDN_ERR_UNSUPPORTED;
+    if ((long long)H * D > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
     // in two steps: the product of three ints may pass 64 bits
     if ((long long)B * T > 0x7fffffffLL || (long long)B * T * H > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;

@@ -786,7 +786,7 @@ int ssm_step(const void *x, const void *dt, const float *A, const void *Bt, cons
  *   weight  [H,D], or [D] with GDN_W_SHARED, fp32; NULL: ones
  *   strides host array of 6 element strides or NULL: (batch, token, head) of x,
  *           gate; not negative and multiples of 16 bytes
- * D a multiple of 8 (bf16) or 4 (fp32) up to 8192; B T H up to 2^31 - 1.
+ * D a multiple of 8 (bf16) or 4 (fp32) up to 8192; B T H and H D up to 2^31 - 1.
  */
 int gated_norm_fwd(const void *x, const void *gate, const float *weight, void *y, const long long *strides, int B,
                    int T, int H, int D, float eps, unsigned flags, int dtype, void *stream);

@@ -128,6 +128,26 @@ def test_caller_workspaces():
     assert all(torch.equal(p, q) for p, q in zip(a[:3], b[:3]))
 
 
+def test_many_chunks_and_what_a_workspace_held():
+    """Packed sequences over more chunks than are joined in place, ends at chunks' ends among them, in a workspace full
+    of NaN: shares that no sequence carries on are never read."""
+    for cu in ([0, 256, 4000, 4001, 9000], [700, 1024, 2048, 8000, 8500], [0, 9000, 9000, 9000, 9000]):
+        s = scan_inputs(1, 9000, 16, 16, "f32", 2, n_seq=4)
+        offsets = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        for f, name in ((forward, "ssm_scan_fwd_workspace_bytes"), (backward, "ssm_scan_bwd_workspace_bytes")):
+            ws = torch.full((binding._bytes(name, 1, 9000, 16, 16, binding.GDN_F32),), 255, dtype=torch.uint8, device="cuda")
+            a, b = f(s, offsets), f(s, offsets, workspace=ws)
+            a, b = (list(t.values()) if isinstance(t, dict) else t for t in (a, b))
+            assert all(torch.equal(p, q) and bool(p.isfinite().all()) for p, q in zip(a, b))
+            # each sequence by itself
+            if f is forward:
+                for i, (t0, t1) in enumerate(zip(cu, cu[1:])):
+                    one = {n: t[:, t0:t1] if n in ("x", "dt", "B", "C", "z") else t for n, t in s.items()}
+                    y, last = forward(dict(one, s0=s["s0"][i: i + 1]))
+                    assert float((y - a[0][:, t0:t1]).abs().max() if t1 > t0 else 0) <= 9000 * 2.0 ** -22 * float(a[0].abs().max())
+                    assert float((last[0] - a[1][i]).abs().max()) <= 9000 * 2.0 ** -22 * float(a[1].abs().max())
+
+
 def test_many_sequences():
     """Thousands of short and empty sequences in one row."""
     gen = torch.Generator().manual_seed(1)

@@ -120,7 +120,7 @@ def test_norm_checks(lib):
 
     for f, n in ((gated, 6), (gated_back, 12)):
         assert f(x=None) == 1 and f(g=None) == 1 and f(eps=-1.0) == 1 and f(eps=float("nan")) == 1 and f(flags=2) == 1
-        assert f(D=20) == 2 and f(D=16384) == 2 and f(B=1 << 20, T=1 << 20) == 2 and f(g=FAKE + 8) == 3
+        assert f(D=20) == 2 and f(D=16384) == 2 and f(B=1 << 20, T=1 << 20) == 2 and f(T=1, H=1 << 20, D=8192) == 2 and f(g=FAKE + 8) == 3
         assert f(st=strides(*[4] * n)) == 3 and f(st=strides(*[-64] * n)) == 1
     assert gated(T=0) == 0
     assert gated_back() == 4 and gated_back(dw=None) == 1
