@@ -7,17 +7,18 @@
 //   dB_t = sum_c g_t D_t x_t,  dC_t = sum_c dy'_t h_t,  dz_t = dy_t (C_t.h_t + skip x_t) silu'(z_t)
 //
 // Three launches.  share_kernel walks every chunk forwards from 0 and writes the
-// state before each block of 8 tokens, what the chunk leaves, and what gradient it
+// state before every 4 tokens, what the chunk leaves, and what gradient it
 // passes to the chunk before it (through the running product of its decays, so
-// that one exponential serves both).  grad_kernel walks the chunks backwards: a
-// block's states are made anew from the one before it and stay in registers.
+// that one exponential serves both).  grad_kernel walks the chunks backwards: four
+// tokens' states are made anew from the one before them and stay in registers.
 // sum_kernel adds up, in order, what groups of channels give to dB and dC and what
 // chunks give to dA, dskip and dbias.  Three exponentials a (token, channel,
-// state); states every 8 tokens take Di N / 2 bytes a token, written and read once
-// behind the arithmetic.
-// Measured, bf16, 4 x 4096 x 2048 x 16 with a gate: 1,062 us, of them share_kernel
-// 235 and grad_kernel about 800.  Instructions bound it, not bytes (0.47 GB and 0.54
-// of states, 160 us): 24 for a warp's 32 tokens x channels x states in grad_kernel,
+// state); states every 4 tokens take Di N bytes a token, written and read once behind
+// the arithmetic.  Every 8 took half of that and 7% longer: 64 registers more, of
+// which some went through memory, and twice the code to fetch.
+// Measured, bf16, 4 x 4096 x 2048 x 16 with a gate: 986 us, of them share_kernel
+// 235 and grad_kernel about 800.  Instructions bound it, not bytes (0.47 GB and 1.07
+// of states, 230 us): 24 for a warp's 32 tokens x channels x states in grad_kernel,
 // at 39% of the issue slots, as its states in registers leave room for 8 warps an SM.
 //
 // A thread holds 4 channels x 4 states, as pairs of channels: what belongs to a
@@ -41,7 +42,8 @@ using namespace ssm;
 using mx::Run;
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kBlock = 8;  // tokens between two states in memory
+constexpr int kBlock = 8;  // tokens that are fetched and converted at once
+constexpr int kHalf = 4;   // tokens between two states in memory
 
 template <typename T, int N>
 struct Shape {
@@ -59,11 +61,11 @@ struct Shape {
 // How a row is cut, and where a call's intermediates are.
 struct Plan {
     int len, chunks;     // tokens of a chunk, a multiple of kBlock
-    int groups, blocks;  // CTAs over the channels; blocks of tokens a row
+    int groups, halves;  // CTAs over the channels; half blocks of tokens a row
     float *left, *back;  // [row][chunk][Di][N]: the state that a chunk leaves, the gradient that it passes on
     float *steps;        // [row][chunk][Di]: the sum of its steps
-    float *state;        // [row][block][warp's channels][4][32] float4: the state before a block, from 0 at the chunk's start
-    float *upto;         // [row][block][warp's channels]: the steps from the chunk's start to the block
+    float *state;        // [row][half block][warp's channels][4][32] float4: the state before it, from 0 at the chunk's start
+    float *upto;         // [row][half block][warp's channels]: the steps from the chunk's start to it
     float *dA, *dD, *db; // [row][chunk][Di][N], [row][chunk][Di] twice
     float *dBC;          // [group][row][T][2 N]
 };
@@ -80,7 +82,7 @@ struct Mem {
 template <typename T, int N>
 struct GradMem : Mem<T, N> {
     using S = Shape<T, N>;
-    float4 saved[5][32];                      // a block's state and steps, as the lanes take them
+    float4 saved[5][32];                      // a half block's state and steps, as the lanes take them
     float4 start[4][32];                      // the state that enters the chunk
     float part[2][kBlock][2 * N];             // a block's dB and dC of this warp
     float over_states[2][3][S::L][S::CH + 8]; // two tokens' D's and x's gradients and y, of each lane of a channel
@@ -297,10 +299,10 @@ __device__ __forceinline__ void zero16(Quad &h) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i >> 2][i & 3] = 0;
 }
-// Where a block's saved state and steps are, of this warp's channels.
+// Where a half block's saved state and steps are, of this warp's channels.
 template <typename T, int N>
 __device__ __forceinline__ size_t saved_at(const SsmArgs &a, const Plan &p, const Place &w, int t) {
-    return ((size_t)w.row * p.blocks + t / kBlock) * (p.groups * kWarps) + w.c0 / Shape<T, N>::CH;
+    return ((size_t)w.row * p.halves + t / kHalf) * (p.groups * kWarps) + w.c0 / Shape<T, N>::CH;
 }
 __device__ __forceinline__ size_t chunk_at(const SsmArgs &a, const Plan &p, int row, int chunk) {
     return ((size_t)row * p.chunks + chunk) * a.Di;
@@ -333,11 +335,13 @@ __global__ void __launch_bounds__(kThreads, 4) share_kernel(SsmArgs a, Plan p) {
         const bool more = t + kBlock < w.t1;
         if (more) fetch<T, N>(a, w, m, buf ^ 1, t + kBlock), copies_out();
         const Marks k = marks_of(a, w, t, r, m.seq);
-        const size_t at = saved_at<T, N>(a, p, w, t);
-        ulonglong2 *to = reinterpret_cast<ulonglong2 *>(p.state) + at * 128 + lane;
+        auto save = [&](int u) {
+            const size_t at = saved_at<T, N>(a, p, w, t + u);
+            ulonglong2 *to = reinterpret_cast<ulonglong2 *>(p.state) + at * 128 + lane;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) to[e * 32] = quad_vector(h, e);
-        if (w.q == 0) *reinterpret_cast<ulonglong2 *>(p.upto + at * S::CH + 4 * w.g) = make_ulonglong2(total[0], total[1]);
+            for (int e = 0; e < 4; ++e) to[e * 32] = quad_vector(h, e);
+            if (w.q == 0) *reinterpret_cast<ulonglong2 *>(p.upto + at * S::CH + 4 * w.g) = make_ulonglong2(total[0], total[1]);
+        };
         copies_done(!more);
         __syncwarp();
         convert<T, N>(a, w, m, buf, t, k.dead);
@@ -368,16 +372,21 @@ __global__ void __launch_bounds__(kThreads, 4) share_kernel(SsmArgs a, Plan p) {
         };
         if (k.starts == 0 && (t + kBlock <= until || t >= until)) {
             const bool pass = t < until;
-            if (pass) {
-#pragma unroll 2
-                for (int u = 0; u < kBlock; ++u) token(u, true);
-            } else {
-#pragma unroll 2
-                for (int u = 0; u < kBlock; ++u) token(u, false);
+#pragma unroll 1
+            for (int v = 0; v < kBlock; v += kHalf) {
+                save(v);
+                if (pass) {
+#pragma unroll 4
+                    for (int u = v; u < v + kHalf; ++u) token(u, true);
+                } else {
+#pragma unroll 4
+                    for (int u = v; u < v + kHalf; ++u) token(u, false);
+                }
             }
         } else {
 #pragma unroll 1
             for (int u = 0; u < kBlock; ++u) {
+                if (u % kHalf == 0) save(u);
                 if (k.starts >> u & 1) load16<N>(a, w, a.s0 ? a.s0 + m.seq[u] * page : nullptr, h);
                 if (t + u < until) token(u, true);
                 else token(u, false);
@@ -407,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
     const Place w = place_of<T, N>(a, p);
     const size_t page = (size_t)a.Di * N;
     const bool soft = a.flags & GDN_DT_SOFTPLUS;
-    // the copies of a block's saved state: a lane's are its own
+    // the copies of a half block's saved state: a lane's are its own
     auto fetch_saved = [&](int t) {
         if (w.c0 < a.Di) {
             const size_t at = saved_at<T, N>(a, p, w, t);
@@ -419,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
     };
     const int last = w.t0 + (w.t1 - 1 - w.t0) / kBlock * kBlock;
     fetch<T, N>(a, w, m, 0, last);
-    fetch_saved(last);
+    fetch_saved(last + kHalf);
     copies_out();
     Quad A, g, dA;
     load_decays<N>(a, w, A);
@@ -488,129 +497,135 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
         __syncwarp();
         if (t > w.t0) fetch<T, N>(a, w, m, buf ^ 1, t - kBlock);
         convert<T, N>(a, w, m, buf, t, k.dead);
-        Quad h0;  // before the block
-        {
-            const bool there = w.c < a.Di;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                set_vector(h0, e, there ? *reinterpret_cast<const ulonglong2 *>(&m.saved[e][lane]) : make_ulonglong2(0, 0));
-            if (there && t < entered) {
-                F2 d[2];
-                Quad s;
-                channels(reinterpret_cast<const float *>(&m.saved[4][lane]), d);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) set_vector(s, e, *reinterpret_cast<const ulonglong2 *>(&m.start[e][lane]));
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) h0[i][n] = fma2(exp2_2(mul2(d[i], A[i][n])), s[i][n], h0[i][n]);
-            }
-        }
-        if (t > w.t0) fetch_saved(t - kBlock);
-        copies_out();
         __syncwarp();
-        // the block, with or without sequences that start or end in it
-        auto block = [&](auto marked) {
-            constexpr bool MARKED = decltype(marked)::value;  // few blocks: their states go through local memory
-            constexpr int UNROLL = MARKED ? 1 : kBlock;
-            Quad hs[kBlock + 1];  // before the block, and after each of its tokens
+#pragma unroll 1
+        for (int half = kBlock - kHalf; half >= 0; half -= kHalf) {
+            if (half == 0) copies_done(true);
+            Quad h0;  // before the half block
+            {
+                const bool there = w.c < a.Di;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) hs[0][i >> 2][i & 3] = h0[i >> 2][i & 3];
-#pragma unroll UNROLL
-            for (int u = 0; u < kBlock; ++u) {
-                F2 d[2], x[2], b[4];
-                channels(&m.step[u][4 * w.g], d);
-                channels(&m.x[u][4 * w.g], x);
-                states(&m.b[u][8 * w.q], b);
-                const F2 in[2] = {mul2(d[0], x[0]), mul2(d[1], x[1])};
-                if (MARKED && (k.starts >> u & 1)) {
-                    Quad first;
-                    load16<N>(a, w, a.s0 ? a.s0 + m.seq[u] * page : nullptr, first);
-                    advance(first, hs[u + 1], A, d, in, b);
-                } else {
-                    advance(hs[u], hs[u + 1], A, d, in, b);
+                for (int e = 0; e < 4; ++e)
+                    set_vector(h0, e, there ? *reinterpret_cast<const ulonglong2 *>(&m.saved[e][lane]) : make_ulonglong2(0, 0));
+                if (there && t + half < entered) {
+                    F2 d[2];
+                    Quad s;
+                    channels(reinterpret_cast<const float *>(&m.saved[4][lane]), d);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) set_vector(s, e, *reinterpret_cast<const ulonglong2 *>(&m.start[e][lane]));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) h0[i][n] = fma2(exp2_2(mul2(d[i], A[i][n])), s[i][n], h0[i][n]);
                 }
             }
+            if (t + half > w.t0) fetch_saved(t + half - kHalf);
+            copies_out();
+            // the half block, with or without sequences that start or end in it
+            auto block = [&](auto marked) {
+                constexpr bool MARKED = decltype(marked)::value;  // few blocks: their states go through local memory
+                constexpr int UNROLL = MARKED ? 1 : kHalf;
+                Quad hs[kHalf + 1];  // before the half block, and after each of its tokens
+#pragma unroll
+                for (int i = 0; i < 8; ++i) hs[0][i >> 2][i & 3] = h0[i >> 2][i & 3];
 #pragma unroll UNROLL
-            for (int u = kBlock - 1; u >= 0; --u) {
-                if (MARKED && (k.ends >> u & 1)) load16<N>(a, w, a.dsf ? a.dsf + m.seq[u] * page : nullptr, g);
-                F2 d[2], x[2], dy[2], b[4], c[4], dx[2], ds[2], y[2];
-                channels(&m.step[u][4 * w.g], d);
-                channels(&m.x[u][4 * w.g], x);
-                channels(&m.dy[u][4 * w.g], dy);
-                states(&m.b[u][8 * w.q], b);
-                states(&m.c[u][8 * w.q], c);
-                F2 dB[4], dC[4];
-                auto token = [&](const Quad &before) {
+                for (int u = 0; u < kHalf; ++u) {
+                    const int v = half + u;
+                    F2 d[2], x[2], b[4];
+                    channels(&m.step[v][4 * w.g], d);
+                    channels(&m.x[v][4 * w.g], x);
+                    states(&m.b[v][8 * w.q], b);
+                    const F2 in[2] = {mul2(d[0], x[0]), mul2(d[1], x[1])};
+                    if (MARKED && (k.starts >> v & 1)) {
+                        Quad first;
+                        load16<N>(a, w, a.s0 ? a.s0 + m.seq[v] * page : nullptr, first);
+                        advance(first, hs[u + 1], A, d, in, b);
+                    } else {
+                        advance(hs[u], hs[u + 1], A, d, in, b);
+                    }
+                }
+#pragma unroll UNROLL
+                for (int u = kHalf - 1; u >= 0; --u) {
+                    const int v = half + u;
+                    if (MARKED && (k.ends >> v & 1)) load16<N>(a, w, a.dsf ? a.dsf + m.seq[v] * page : nullptr, g);
+                    F2 d[2], x[2], dy[2], b[4], c[4], dx[2], ds[2], y[2];
+                    channels(&m.step[v][4 * w.g], d);
+                    channels(&m.x[v][4 * w.g], x);
+                    channels(&m.dy[v][4 * w.g], dy);
+                    states(&m.b[v][8 * w.q], b);
+                    states(&m.c[v][8 * w.q], c);
+                    F2 dB[4], dC[4];
+                    auto token = [&](const Quad &before) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const F2 in = mul2(d[i], x[i]);
-                        F2 gb, ap, cy;
+                        for (int i = 0; i < 2; ++i) {
+                            const F2 in = mul2(d[i], x[i]);
+                            F2 gb, ap, cy;
 #pragma unroll
-                        for (int n = 0; n < 4; ++n) {
-                            g[i][n] = fma2(c[n], dy[i], g[i][n]);
-                            dC[n] = i ? fma2(hs[u + 1][i][n], dy[i], dC[n]) : mul2(hs[u + 1][i][n], dy[i]);
-                            dB[n] = i ? fma2(g[i][n], in, dB[n]) : mul2(g[i][n], in);
-                            if (a.z) cy = n ? fma2(hs[u + 1][i][n], c[n], cy) : mul2(hs[u + 1][i][n], c[n]);
-                            gb = n ? fma2(g[i][n], b[n], gb) : mul2(g[i][n], b[n]);
-                            g[i][n] = mul2(exp2_2(mul2(d[i], A[i][n])), g[i][n]);
-                            const F2 passed = mul2(g[i][n], before[i][n]);
-                            dA[i][n] = fma2(passed, d[i], dA[i][n]);
-                            ap = n ? fma2(passed, A[i][n], ap) : mul2(passed, A[i][n]);
+                            for (int n = 0; n < 4; ++n) {
+                                g[i][n] = fma2(c[n], dy[i], g[i][n]);
+                                dC[n] = i ? fma2(hs[u + 1][i][n], dy[i], dC[n]) : mul2(hs[u + 1][i][n], dy[i]);
+                                dB[n] = i ? fma2(g[i][n], in, dB[n]) : mul2(g[i][n], in);
+                                if (a.z) cy = n ? fma2(hs[u + 1][i][n], c[n], cy) : mul2(hs[u + 1][i][n], c[n]);
+                                gb = n ? fma2(g[i][n], b[n], gb) : mul2(g[i][n], b[n]);
+                                g[i][n] = mul2(exp2_2(mul2(d[i], A[i][n])), g[i][n]);
+                                const F2 passed = mul2(g[i][n], before[i][n]);
+                                dA[i][n] = fma2(passed, d[i], dA[i][n]);
+                                ap = n ? fma2(passed, A[i][n], ap) : mul2(passed, A[i][n]);
+                            }
+                            dx[i] = mul2(d[i], gb);
+                            ds[i] = fma2(x[i], gb, mul2(ap, both(mx::kLn2)));
+                            y[i] = cy;
                         }
-                        dx[i] = mul2(d[i], gb);
-                        ds[i] = fma2(x[i], gb, mul2(ap, both(mx::kLn2)));
-                        y[i] = cy;
+                    };
+                    if (MARKED && (k.starts >> v & 1)) {  // what came before is the sequence's initial state
+                        Quad first;
+                        load16<N>(a, w, a.s0 ? a.s0 + m.seq[v] * page : nullptr, first);
+                        token(first);
+                        if (a.ds0) store16<N>(a, w, a.ds0 + m.seq[v] * page, g);
+                        zero16(g);
+                    } else {
+                        token(hs[u]);
                     }
-                };
-                if (MARKED && (k.starts >> u & 1)) {  // what came before is the sequence's initial state
-                    Quad first;
-                    load16<N>(a, w, a.s0 ? a.s0 + m.seq[u] * page : nullptr, first);
-                    token(first);
-                    if (a.ds0) store16<N>(a, w, a.ds0 + m.seq[u] * page, g);
-                    zero16(g);
-                } else {
-                    token(hs[u]);
-                }
-                auto put = [&](int what, const F2 (&v)[2]) {
-                    *reinterpret_cast<ulonglong2 *>(&m.over_states[u & 1][what][w.q][4 * w.g]) = make_ulonglong2(v[0], v[1]);
-                };
-                put(0, ds);
-                put(1, dx);
-                if (a.z) put(2, y);
-                float *row = m.over_channels[u % S::SLOTS][w.g];
-                *reinterpret_cast<float4 *>(row + 4 * w.q) = make_float4(sum(dB[0]), sum(dB[1]), sum(dB[2]), sum(dB[3]));
-                *reinterpret_cast<float4 *>(row + N + 4 * w.q) = make_float4(sum(dC[0]), sum(dC[1]), sum(dC[2]), sum(dC[3]));
-                if ((u & 1) != 0) continue;
-                __syncwarp();
-                const int kinds = a.z ? 3 : 2;  // over step, x and dy of the two tokens, which all lanes have read
-                for (int i = lane; i < kinds * S::CH / 2; i += 32) {
-                    const int what = i / (S::CH / 2), tok = i % (S::CH / 2) / (S::CH / 4), c4 = i % (S::CH / 4) * 4;
-                    F2 p0 = 0, p1 = 0;
-#pragma unroll
-                    for (int q = 0; q < S::L; ++q) {
-                        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&m.over_states[tok][what][q][c4]);
-                        p0 = mx::add2(p0, v.x), p1 = mx::add2(p1, v.y);
-                    }
-                    *reinterpret_cast<ulonglong2 *>(&m.step[0][0] + (what * kBlock + u + tok) * S::CH + c4) = make_ulonglong2(p0, p1);
-                }
-                if (u % S::SLOTS == 0)
-#pragma unroll
-                    for (int i = lane; i < S::SLOTS * N / 2; i += 32) {
-                        const int tok = i / (N / 2), n = i % (N / 2) * 4;
+                    auto put = [&](int what, const F2 (&v)[2]) {
+                        *reinterpret_cast<ulonglong2 *>(&m.over_states[u & 1][what][w.q][4 * w.g]) = make_ulonglong2(v[0], v[1]);
+                    };
+                    put(0, ds);
+                    put(1, dx);
+                    if (a.z) put(2, y);
+                    float *row = m.over_channels[u % S::SLOTS][w.g];
+                    *reinterpret_cast<float4 *>(row + 4 * w.q) = make_float4(sum(dB[0]), sum(dB[1]), sum(dB[2]), sum(dB[3]));
+                    *reinterpret_cast<float4 *>(row + N + 4 * w.q) = make_float4(sum(dC[0]), sum(dC[1]), sum(dC[2]), sum(dC[3]));
+                    if ((u & 1) != 0) continue;
+                    __syncwarp();
+                    const int kinds = a.z ? 3 : 2;  // over step, x and dy of the two tokens, which all lanes have read
+                    for (int i = lane; i < kinds * S::CH / 2; i += 32) {
+                        const int what = i / (S::CH / 2), tok = i % (S::CH / 2) / (S::CH / 4), c4 = i % (S::CH / 4) * 4;
                         F2 p0 = 0, p1 = 0;
 #pragma unroll
-                        for (int q = 0; q < S::G; ++q) {
-                            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&m.over_channels[tok][q][n]);
+                        for (int q = 0; q < S::L; ++q) {
+                            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&m.over_states[tok][what][q][c4]);
                             p0 = mx::add2(p0, v.x), p1 = mx::add2(p1, v.y);
                         }
-                        *reinterpret_cast<ulonglong2 *>(&m.part[buf][u + tok][n]) = make_ulonglong2(p0, p1);
+                        *reinterpret_cast<ulonglong2 *>(&m.step[0][0] + (what * kBlock + v + tok) * S::CH + c4) = make_ulonglong2(p0, p1);
                     }
-                __syncwarp();
-            }
-        };
-        if (k.starts | k.ends) block(std::true_type{});
-        else block(std::false_type{});
+                    if (u % S::SLOTS == 0)
+#pragma unroll
+                        for (int i = lane; i < S::SLOTS * N / 2; i += 32) {
+                            const int tok = i / (N / 2), n = i % (N / 2) * 4;
+                            F2 p0 = 0, p1 = 0;
+#pragma unroll
+                            for (int q = 0; q < S::G; ++q) {
+                                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&m.over_channels[tok][q][n]);
+                                p0 = mx::add2(p0, v.x), p1 = mx::add2(p1, v.y);
+                            }
+                            *reinterpret_cast<ulonglong2 *>(&m.part[buf][v + tok][n]) = make_ulonglong2(p0, p1);
+                        }
+                    __syncwarp();
+                }
+            };
+            if (k.starts | k.ends) block(std::true_type{});
+            else block(std::false_type{});
+        }
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < S::VPL; ++i) {
@@ -752,16 +767,16 @@ Plan plan(int B, int T, int Di, int N, int dtype, float *ws, size_t *bytes) {
         consider((T + chunks - 1) / chunks);
     }
     for (long long len = kBlock; len < T; len += std::max((long long)kBlock, len / 4)) consider(len);
-    p.blocks = (T + kBlock - 1) / kBlock;
+    p.halves = (T + kBlock - 1) / kBlock * (kBlock / kHalf);
     size_t at = 0;
     auto take = [&](float **x, size_t n) { *x = ws ? ws + at : nullptr, at += (n + 3) / 4 * 4; };
-    // a block's places are of whole warps
-    const size_t per_chunk = (size_t)B * p.chunks * Di, per_block = (size_t)B * p.blocks * p.groups * channels(N);
+    // a half block's places are of whole warps
+    const size_t per_chunk = (size_t)B * p.chunks * Di, per_half = (size_t)B * p.halves * p.groups * channels(N);
     take(&p.left, per_chunk * N);
     take(&p.back, per_chunk * N);
     take(&p.steps, per_chunk);
-    take(&p.state, per_block * N);
-    take(&p.upto, per_block);
+    take(&p.state, per_half * N);
+    take(&p.upto, per_half);
     take(&p.dA, per_chunk * N);
     take(&p.dD, per_chunk);
     take(&p.db, per_chunk);
