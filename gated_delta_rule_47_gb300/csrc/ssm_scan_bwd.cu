@@ -16,10 +16,10 @@
 // state); states every 4 tokens take Di N bytes a token, written and read once behind
 // the arithmetic.  Every 8 took half of that and 7% longer: 64 registers more, of
 // which some went through memory, and twice the code to fetch.
-// Measured, bf16, 4 x 4096 x 2048 x 16 with a gate: 986 us, of them share_kernel
-// 235 and grad_kernel about 800.  Instructions bound it, not bytes (0.47 GB and 1.07
-// of states, 230 us): 24 for a warp's 32 tokens x channels x states in grad_kernel,
-// at 39% of the issue slots, as its states in registers leave room for 8 warps an SM.
+// Measured, bf16, 4 x 4096 x 2048 x 16 with a gate: 925 us, of them share_kernel
+// 240 and grad_kernel about 660.  Instructions bound it, not bytes (0.47 GB and 1.07
+// of states, 230 us): 21 for a warp's 32 tokens x channels x states in grad_kernel,
+// at 41% of the issue slots, as its states in registers leave room for 8 warps an SM.
 //
 // A thread holds 4 channels x 4 states, as pairs of channels: what belongs to a
 // channel is loaded as a pair, and B and C lie in shared memory twice over.  The
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 4) share_kernel(SsmArgs a, Plan p) {
     if (w.q == 0 && w.c < a.Di) *reinterpret_cast<ulonglong2 *>(p.steps + at + w.c) = make_ulonglong2(total[0], total[1]);
 }
 
-template <typename T, int N>
+template <typename T, int N, bool GATE>
 __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
     using S = Shape<T, N>;
     extern __shared__ __align__(16) char smem[];
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
                                 g[i][n] = fma2(c[n], dy[i], g[i][n]);
                                 dC[n] = i ? fma2(hs[u + 1][i][n], dy[i], dC[n]) : mul2(hs[u + 1][i][n], dy[i]);
                                 dB[n] = i ? fma2(g[i][n], in, dB[n]) : mul2(g[i][n], in);
-                                if (a.z) cy = n ? fma2(hs[u + 1][i][n], c[n], cy) : mul2(hs[u + 1][i][n], c[n]);
+                                if (GATE) cy = n ? fma2(hs[u + 1][i][n], c[n], cy) : mul2(hs[u + 1][i][n], c[n]);
                                 gb = n ? fma2(g[i][n], b[n], gb) : mul2(g[i][n], b[n]);
                                 g[i][n] = mul2(exp2_2(mul2(d[i], A[i][n])), g[i][n]);
                                 const F2 passed = mul2(g[i][n], before[i][n]);
@@ -591,14 +591,17 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
                     };
                     put(0, ds);
                     put(1, dx);
-                    if (a.z) put(2, y);
+                    if (GATE) put(2, y);
                     float *row = m.over_channels[u % S::SLOTS][w.g];
                     *reinterpret_cast<float4 *>(row + 4 * w.q) = make_float4(sum(dB[0]), sum(dB[1]), sum(dB[2]), sum(dB[3]));
                     *reinterpret_cast<float4 *>(row + N + 4 * w.q) = make_float4(sum(dC[0]), sum(dC[1]), sum(dC[2]), sum(dC[3]));
                     if ((u & 1) != 0) continue;
                     __syncwarp();
-                    const int kinds = a.z ? 3 : 2;  // over step, x and dy of the two tokens, which all lanes have read
-                    for (int i = lane; i < kinds * S::CH / 2; i += 32) {
+                    constexpr int kinds = GATE ? 3 : 2;  // over step, x and dy of the two tokens, which all lanes have read
+#pragma unroll
+                    for (int i0 = 0; i0 < kinds * S::CH / 2; i0 += 32) {
+                        const int i = i0 + lane;
+                        if (i >= kinds * S::CH / 2) break;
                         const int what = i / (S::CH / 2), tok = i % (S::CH / 2) / (S::CH / 4), c4 = i % (S::CH / 4) * 4;
                         F2 p0 = 0, p1 = 0;
 #pragma unroll
@@ -645,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
                 unpack<T, S::V>(m.raw[buf][2][j], dy);
                 vector_of<S::V>(a.bias, c, bias);
                 vector_of<S::V>(a.D, c, skip);
-                if (a.z) {
+                if (GATE) {
                     float z[S::V];
                     unpack<T, S::V>(m.raw[buf][3][j], z);
                     get<S::V>(&m.dy[tok][cv], dz);
@@ -672,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
             using Raw = typename Vec<T, S::V>::Raw;
             __stcs(reinterpret_cast<Raw *>(static_cast<T *>(a.dx) + at), Vec<T, S::V>::pack(dx));
             __stcs(reinterpret_cast<Raw *>(static_cast<T *>(a.ddt) + at), Vec<T, S::V>::pack(dv));
-            if (a.z) __stcs(reinterpret_cast<Raw *>(static_cast<T *>(a.dz) + at), Vec<T, S::V>::pack(dz));
+            if (GATE) __stcs(reinterpret_cast<Raw *>(static_cast<T *>(a.dz) + at), Vec<T, S::V>::pack(dz));
         }
         // dB and dC of the CTA's channels: the warps take turns at adding the four
         // shares, and the two buffers need one barrier a block
@@ -803,12 +806,13 @@ int bwd(const SsmArgs &a, cudaStream_t stream) {
     size_t bytes;
     const Plan p = plan(a.B, a.T, a.Di, N, a.dtype, static_cast<float *>(a.ws), &bytes);
     constexpr int one = sizeof(Mem<T, N>) * kWarps, two = sizeof(GradMem<T, N>) * kWarps;
-    if (!room<share_kernel<T, N>>(one) || !room<grad_kernel<T, N>>(two)) return GDN_ERR_CUDA;
+    if (!room<share_kernel<T, N>>(one) || !room<grad_kernel<T, N, false>>(two) || !room<grad_kernel<T, N, true>>(two)) return GDN_ERR_CUDA;
     const unsigned ctas = (unsigned)((long long)p.groups * a.B * p.chunks);
     share_kernel<T, N><<<ctas, kThreads, one, stream>>>(a, p);
     int st = mx::launched();
     if (st != GDN_OK) return st;
-    grad_kernel<T, N><<<ctas, kThreads, two, stream>>>(a, p);
+    if (a.z) grad_kernel<T, N, true><<<ctas, kThreads, two, stream>>>(a, p);
+    else grad_kernel<T, N, false><<<ctas, kThreads, two, stream>>>(a, p);
     st = mx::launched();
     if (st != GDN_OK) return st;
     const long long tokens = ((long long)a.B * a.T * (N / 2) + 255) / 256, rest = ((long long)a.Di * (N + 2) + 255) / 256;
