@@ -16,8 +16,8 @@
 // state); states every 4 tokens take Di N bytes a token, written and read once behind
 // the arithmetic.  Every 8 took half of that and 7% longer: 64 registers more, of
 // which some went through memory, and twice the code to fetch.
-// Measured, bf16, 4 x 4096 x 2048 x 16 with a gate: 925 us, of them share_kernel
-// 240 and grad_kernel about 660.  Instructions bound it, not bytes (0.47 GB and 1.07
+// Measured, bf16, 4 x 4096 x 2048 x 16 with a gate: 897 us, of them share_kernel
+// 235 and grad_kernel about 640.  Instructions bound it, not bytes (0.47 GB and 1.07
 // of states, 230 us): 21 for a warp's 32 tokens x channels x states in grad_kernel,
 // at 41% of the issue slots, as its states in registers leave room for 8 warps an SM.
 //
@@ -50,10 +50,13 @@ struct Shape {
     static constexpr int L = N / 4;       // lanes of a channel's states
     static constexpr int G = 32 / L;      // lanes of the channels
     static constexpr int CH = 4 * G;      // channels a warp
+    static constexpr int ROW = CH + 4;    // of them in shared memory: the lanes of a quarter warp, 32 bytes each of two tokens, meet in no bank
     static constexpr int V = kWide<T>;
     static constexpr int RV = CH / V;     // vectors of a token's channels
     static constexpr int NV = kBlock * RV, VPL = (NV + 31) / 32;  // of a block; of a lane
     static constexpr int BV = N / V;      // vectors of a token's B
+    // dB's and dC's halves trade places in rows that would meet in a bank
+    static __device__ __forceinline__ int swap(int g) { return N == 16 ? (g & 1) * 16 : N == 8 ? (g >> 1 & 1) * 8 : 0; }
     static constexpr int SLOTS = N == 16 ? 4 : 2;  // tokens whose dB and dC are summed over channels at once
     static constexpr int NB = kBlock * BV, BPL = (2 * NB + 31) / 32;
 };
@@ -75,7 +78,7 @@ struct Mem {
     using S = Shape<T, N>;
     uint4 raw[2][4][S::NV];  // x, dt, dy, z as loaded, twice: one on its way
     uint4 bc[2][2 * S::NB];
-    float step[kBlock][S::CH], x[kBlock][S::CH], dy[kBlock][S::CH];  // then D's and x's gradients, and y
+    float step[kBlock][S::ROW], x[kBlock][S::ROW], dy[kBlock][S::ROW];  // then D's and x's gradients, and y
     float b[kBlock][2 * N], c[kBlock][2 * N];                        // every value twice
     int seq[kBlock];                                                // the sequences that start or end in the block
 };
@@ -86,7 +89,7 @@ struct GradMem : Mem<T, N> {
     float4 start[4][32];                      // the state that enters the chunk
     float part[2][kBlock][2 * N];             // a block's dB and dC of this warp
     float over_states[2][3][S::L][S::CH + 8]; // two tokens' D's and x's gradients and y, of each lane of a channel
-    float over_channels[S::SLOTS][S::G][2 * N + 4];  // some tokens' dB and dC, of each lane of the channels
+    float over_channels[S::SLOTS][S::G][2 * N];  // some tokens' dB and dC, of each lane of the channels; swizzled
     float4 acc[2][S::VPL * S::V / 4][32];     // dskip and dbias of each lane's vectors
 };
 
@@ -205,18 +208,17 @@ __device__ __forceinline__ void convert(const SsmArgs &a, const Place &w, Mem<T,
         put<S::V>(&m.step[tok][c], d);
         put<S::V>(&m.dy[tok][c], g);
     }
+    // two values a lane, so that the doubled ones of a quarter warp lie side by side
+    constexpr int PAIRS = kBlock * N / 2;
+    using Two = typename Vec<T, 2>::Raw;
 #pragma unroll
-    for (int i = 0; i < S::BPL; ++i) {
-        const int j = i * 32 + lane, k = j % S::NB, tok = k / S::BV, n = k % S::BV * S::V;
-        if (j >= 2 * S::NB) break;
-        float x[S::V];
-        unpack<T, S::V>(m.bc[buf][j], x);
-        if (t + tok >= w.t1 || (dead >> tok & 1))
-#pragma unroll
-            for (int e = 0; e < S::V; ++e) x[e] = 0.f;
-        float *to = j < S::NB ? &m.b[tok][2 * n] : &m.c[tok][2 * n];
-#pragma unroll
-        for (int e = 0; e < S::V; e += 2) *reinterpret_cast<float4 *>(to + 2 * e) = make_float4(x[e], x[e], x[e + 1], x[e + 1]);
+    for (int i = 0; i < 2 * PAIRS; i += 32) {
+        const int j = i + lane, k = j % PAIRS, tok = k / (N / 2), n = k % (N / 2) * 2;
+        float x[2];
+        Vec<T, 2>::unpack(reinterpret_cast<const Two *>(m.bc[buf])[j], x);
+        if (t + tok >= w.t1 || (dead >> tok & 1)) x[0] = x[1] = 0.f;
+        float *to = j < PAIRS ? &m.b[tok][2 * n] : &m.c[tok][2 * n];
+        *reinterpret_cast<float4 *>(to) = make_float4(x[0], x[0], x[1], x[1]);
     }
 }
 
@@ -593,8 +595,8 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
                     put(1, dx);
                     if (GATE) put(2, y);
                     float *row = m.over_channels[u % S::SLOTS][w.g];
-                    *reinterpret_cast<float4 *>(row + 4 * w.q) = make_float4(sum(dB[0]), sum(dB[1]), sum(dB[2]), sum(dB[3]));
-                    *reinterpret_cast<float4 *>(row + N + 4 * w.q) = make_float4(sum(dC[0]), sum(dC[1]), sum(dC[2]), sum(dC[3]));
+                    *reinterpret_cast<float4 *>(row + (4 * w.q ^ S::swap(w.g))) = make_float4(sum(dB[0]), sum(dB[1]), sum(dB[2]), sum(dB[3]));
+                    *reinterpret_cast<float4 *>(row + (N + 4 * w.q ^ S::swap(w.g))) = make_float4(sum(dC[0]), sum(dC[1]), sum(dC[2]), sum(dC[3]));
                     if ((u & 1) != 0) continue;
                     __syncwarp();
                     constexpr int kinds = GATE ? 3 : 2;  // over step, x and dy of the two tokens, which all lanes have read
@@ -609,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
                             const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&m.over_states[tok][what][q][c4]);
                             p0 = mx::add2(p0, v.x), p1 = mx::add2(p1, v.y);
                         }
-                        *reinterpret_cast<ulonglong2 *>(&m.step[0][0] + (what * kBlock + v + tok) * S::CH + c4) = make_ulonglong2(p0, p1);
+                        *reinterpret_cast<ulonglong2 *>(&m.step[0][0] + (what * kBlock + v + tok) * S::ROW + c4) = make_ulonglong2(p0, p1);
                     }
                     if (u % S::SLOTS == 0)
 #pragma unroll
@@ -618,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
                             F2 p0 = 0, p1 = 0;
 #pragma unroll
                             for (int q = 0; q < S::G; ++q) {
-                                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&m.over_channels[tok][q][n]);
+                                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&m.over_channels[tok][q][n ^ S::swap(q)]);
                                 p0 = mx::add2(p0, v.x), p1 = mx::add2(p1, v.y);
                             }
                             *reinterpret_cast<ulonglong2 *>(&m.part[buf][v + tok][n]) = make_ulonglong2(p0, p1);
