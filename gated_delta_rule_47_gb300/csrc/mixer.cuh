@@ -62,17 +62,17 @@ __device__ __forceinline__ float silu_slope(float x, float s) { return s * fmaf(
 
 // log(1 + e) / e for e in 0..1, by interpolation in Chebyshev's points: to 1.3e-7.
 // lg2 would take twice an ex2's time and lose the value of small e against 1.
+// Coefficient i, the highest power's first.
+__device__ __forceinline__ float log1p_coefficient(int i) {
+    const float c[10] = {-0.00317605701f, 0.0195425283f, -0.0563736148f, 0.105436236f, -0.152696669f,
+                         0.196632743f, -0.249516159f, 0.333297104f, -0.499998927f, 1.f};
+    return c[i];
+}
 __device__ __forceinline__ float log1p_over(float e) {
-    float p = -0.00317605701f;
-    p = fmaf(p, e, 0.0195425283f);
-    p = fmaf(p, e, -0.0563736148f);
-    p = fmaf(p, e, 0.105436236f);
-    p = fmaf(p, e, -0.152696669f);
-    p = fmaf(p, e, 0.196632743f);
-    p = fmaf(p, e, -0.249516159f);
-    p = fmaf(p, e, 0.333297104f);
-    p = fmaf(p, e, -0.499998927f);
-    return fmaf(p, e, 1.f);
+    float p = log1p_coefficient(0);
+#pragma unroll
+    for (int i = 1; i < 10; ++i) p = fmaf(p, e, log1p_coefficient(i));
+    return p;
 }
 // log(1 + exp(v)) = max(v, 0) + log(1 + exp(-|v|)).
 __device__ __forceinline__ float softplus(float v) {
@@ -112,12 +112,22 @@ __device__ __forceinline__ float sum(F2 p) {
 }
 
 // The activations of two at once: the exponentials and reciprocals are single.
+__device__ __forceinline__ F2 softplus2(F2 v) {
+    float a, b;
+    split(v, a, b);
+    const F2 e = pair(exp2_fast(-kLog2e * fabsf(a)), exp2_fast(-kLog2e * fabsf(b)));
+    F2 p = both(log1p_coefficient(0));
+#pragma unroll
+    for (int i = 1; i < 10; ++i) p = fma2(p, e, both(log1p_coefficient(i)));
+    return fma2(e, p, pair(fmaxf(a, 0.f), fmaxf(b, 0.f)));
+}
 __device__ __forceinline__ F2 sigmoid2(F2 x) {
     float a, b;
     split(mul2(x, both(-kLog2e)), a, b);
     split(add2(pair(exp2_fast(a), exp2_fast(b)), both(1.f)), a, b);
     return pair(inverse(a), inverse(b));
 }
+__device__ __forceinline__ F2 silu2(F2 x) { return mul2(x, sigmoid2(x)); }
 __device__ __forceinline__ F2 silu_slope2(F2 x, F2 s) { return mul2(s, fma2(x, fma2(s, both(-1.f), both(1.f)), both(1.f))); }
 // N elements as pairs.
 template <typename T, int N>

@@ -85,14 +85,18 @@ struct Tile {
     }
 };
 
-// The steps D of a token's channels from dt as loaded.
+// The steps D of a token's channels from dt as loaded, two at once where there are.
 template <int CH>
 __device__ __forceinline__ void steps_of(const float (&dt)[CH], const float (&bias)[CH], bool soft, float (&step)[CH]) {
-    // one by one: an immediate constant is free there, a pair of them is not
+    if constexpr (CH == 1) {
+        const float v = dt[0] + bias[0];
+        step[0] = soft ? mx::softplus(v) : v;
+    } else {
 #pragma unroll
-    for (int e = 0; e < CH; ++e) {
-        const float v = dt[e] + bias[e];
-        step[e] = soft ? mx::softplus(v) : v;
+        for (int e = 0; e < CH; e += 2) {
+            const F2 v = mx::add2(pair(dt[e], dt[e + 1]), pair(bias[e], bias[e + 1]));
+            split(soft ? mx::softplus2(v) : v, step[e], step[e + 1]);
+        }
     }
 }
 template <int CH>

@@ -190,15 +190,15 @@ __device__ __forceinline__ void convert(const SsmArgs &a, const Place &w, Mem<T,
             unpack<T, S::V>(m.raw[buf][1][j], d);
             unpack<T, S::V>(m.raw[buf][2][j], g);
 #pragma unroll
-            for (int e = 0; e < S::V; ++e) {
-                d[e] += bias[e];
-                if (soft) d[e] = mx::softplus(d[e]);
+            for (int e = 0; e < S::V; e += 2) {
+                const F2 v = mx::add2(pair(d[e], d[e + 1]), pair(bias[e], bias[e + 1]));
+                split(soft ? mx::softplus2(v) : v, d[e], d[e + 1]);
             }
             if (a.z) {
                 float z[S::V];
                 unpack<T, S::V>(m.raw[buf][3][j], z);
 #pragma unroll
-                for (int e = 0; e < S::V; ++e) g[e] *= mx::silu(z[e]);
+                for (int e = 0; e < S::V; e += 2) split(mul2(pair(g[e], g[e + 1]), mx::silu2(pair(z[e], z[e + 1]))), g[e], g[e + 1]);
             }
         } else {
 #pragma unroll
@@ -650,28 +650,31 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
                 unpack<T, S::V>(m.raw[buf][2][j], dy);
                 vector_of<S::V>(a.bias, c, bias);
                 vector_of<S::V>(a.D, c, skip);
+                float z[S::V];
                 if (GATE) {
-                    float z[S::V];
                     unpack<T, S::V>(m.raw[buf][3][j], z);
                     get<S::V>(&m.dy[tok][cv], dz);
-#pragma unroll
-                    for (int e = 0; e < S::V; ++e) {
-                        const float s = mx::sigmoid(z[e]);
-                        dz[e] = dy[e] * fmaf(skip[e], x[e], dz[e]) * mx::silu_slope(z[e], s);
-                        dy[e] *= z[e] * s;
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < S::V; ++e) {
-                    dx[e] = fmaf(skip[e], dy[e], dx[e]);
-                    if (soft) dv[e] *= mx::sigmoid(dt[e] + bias[e]);
                 }
 #pragma unroll
                 for (int e = 0; e < S::V; e += 4) {
-                    float4 &p = m.acc[0][(i * S::V + e) / 4][lane], &q = m.acc[1][(i * S::V + e) / 4][lane];
-                    p.x = fmaf(dy[e], x[e], p.x), p.y = fmaf(dy[e + 1], x[e + 1], p.y);
-                    p.z = fmaf(dy[e + 2], x[e + 2], p.z), p.w = fmaf(dy[e + 3], x[e + 3], p.w);
-                    q.x += dv[e], q.y += dv[e + 1], q.z += dv[e + 2], q.w += dv[e + 3];
+                    ulonglong2 &p = reinterpret_cast<ulonglong2 &>(m.acc[0][(i * S::V + e) / 4][lane]);
+                    ulonglong2 &q = reinterpret_cast<ulonglong2 &>(m.acc[1][(i * S::V + e) / 4][lane]);
+#pragma unroll
+                    for (int f = e; f < e + 4; f += 2) {  // two at once
+                        const F2 x2 = pair(x[f], x[f + 1]), skip2 = pair(skip[f], skip[f + 1]);
+                        F2 dy2 = pair(dy[f], dy[f + 1]), dv2 = pair(dv[f], dv[f + 1]);
+                        if (GATE) {
+                            const F2 z2 = pair(z[f], z[f + 1]), s = mx::sigmoid2(z2);
+                            const F2 out = mul2(dy2, fma2(skip2, x2, pair(dz[f], dz[f + 1])));
+                            split(mul2(out, mx::silu_slope2(z2, s)), dz[f], dz[f + 1]);
+                            dy2 = mul2(dy2, mul2(z2, s));
+                        }
+                        split(fma2(skip2, dy2, pair(dx[f], dx[f + 1])), dx[f], dx[f + 1]);
+                        if (soft) dv2 = mul2(dv2, mx::sigmoid2(mx::add2(pair(dt[f], dt[f + 1]), pair(bias[f], bias[f + 1]))));
+                        split(dv2, dv[f], dv[f + 1]);
+                        F2 &pf = f == e ? p.x : p.y, &qf = f == e ? q.x : q.y;
+                        pf = fma2(dy2, x2, pf), qf = mx::add2(qf, dv2);
+                    }
                 }
             }
             using Raw = typename Vec<T, S::V>::Raw;
