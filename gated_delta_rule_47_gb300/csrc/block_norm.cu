@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(NT) block_kernel(BlockNormArgs a, int per) {
 // part: [CTA][2][C], the sums of dy h r2 and of dres x r1.
 template <typename T, int NT, int V>
 __global__ void __launch_bounds__(NT) block_bwd_kernel(BlockNormArgs a, int per, float *part) {
+    mx::let_follow();
     constexpr int N = kWide<T>;
     using Raw = typename Vec<T, N>::Raw;
     __shared__ float red[2][3][32];
@@ -234,6 +235,7 @@ __global__ void __launch_bounds__(NT) block_bwd_kernel(BlockNormArgs a, int per,
 // The three gradients of columns, from the CTAs' sums, in order: 32 columns a CTA,
 // 32 strands of shares or of groups.
 __global__ void __launch_bounds__(1024) block_sum_kernel(BlockNormArgs a, const float *part, int groups, int per) {
+    mx::follow_on();
     __shared__ float s[2][32][33];
     const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float dw1 = 0.f, dw2 = 0.f;
@@ -308,7 +310,7 @@ int go(const BlockNormArgs &a, cudaStream_t stream) {
         block_bwd_kernel<T, NT, V><<<groups * per, NT, 0, stream>>>(a, per, part);
         const int st = mx::launched();
         if (st != GDN_OK) return st;
-        block_sum_kernel<<<(a.C + 31) / 32, 1024, 0, stream>>>(a, part, groups, per);
+        mx::follow(block_sum_kernel, (a.C + 31) / 32, 1024, 0, stream, a, part, groups, per);
         return mx::launched();
     }
 }

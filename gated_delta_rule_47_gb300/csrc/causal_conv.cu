@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, 3) conv_kernel(ConvArgs a, int len, 
 // TB/s; 278 with the conditions at every token, 129 with four tokens on their way).
 template <typename T, int N, int W>
 __global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ConvArgs a, int len, int per_row, float *part) {
+    mx::let_follow();
     using Raw = typename Vec<T, N>::Raw;
     constexpr int U = sizeof(T) == 2 ? 8 : 2, P = N / 2;
     Strip s;
@@ -363,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ConvArgs a, int l
 template <int STRANDS>
 __global__ void __launch_bounds__(32 * STRANDS) conv_sum_kernel(const float *part, float *dw, float *db, int n, int C, int W) {
     const long long all = (long long)(W + 1) * C, i = (long long)blockIdx.x * 32 + (threadIdx.x & 31);
+    mx::follow_on();
     const float x = mx::column_sum<STRANDS>(part, n, all, i);
     if (threadIdx.x >= 32 || i >= all) return;
     const int j = (int)(i / C), c = (int)(i - (long long)j * C);
@@ -474,8 +476,8 @@ int bwd(const ConvArgs &a, cudaStream_t stream) {
     if (st != GDN_OK) return st;
     const unsigned ctas = (unsigned)(((long long)(W + 1) * a.C + 31) / 32);
     const int n = c.per_row * a.B;
-    if (n <= 256) conv_sum_kernel<8><<<ctas, 256, 0, stream>>>(part, a.dw, a.db, n, a.C, W);
-    else conv_sum_kernel<32><<<ctas, 1024, 0, stream>>>(part, a.dw, a.db, n, a.C, W);
+    if (n <= 256) mx::follow(conv_sum_kernel<8>, ctas, 256, 0, stream, part, a.dw, a.db, n, a.C, W);
+    else mx::follow(conv_sum_kernel<32>, ctas, 1024, 0, stream, part, a.dw, a.db, n, a.C, W);
     return mx::launched();
 }
 

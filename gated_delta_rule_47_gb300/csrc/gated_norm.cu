@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(kThreads) gated_kernel(GatedNormArgs a, int st
 // arithmetic 77.  Another row on its way made no difference.
 template <typename T, int NT, int V, bool FIRST>
 __global__ void __launch_bounds__(kThreads, V == 1 ? 2 : 1) gated_bwd_kernel(GatedNormArgs a, int strips, float *part) {
+    mx::let_follow();
     constexpr int N = kWide<T>, P = N / 2, GROUPS = kThreads / NT;
     using Raw = typename Vec<T, N>::Raw;
     __shared__ float red[2][2][kThreads / 32];
@@ -244,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 2 : 1) gated_bwd_kernel(Gat
 
 __global__ void __launch_bounds__(1024) gated_sum_kernel(const float *part, float *out, int n, int C) {
     const int c = blockIdx.x * 32 + (threadIdx.x & 31);
+    mx::follow_on();
     const float x = mx::column_sum<32>(part, n, C, c);
     if (threadIdx.x < 32 && c < C) out[c] = x;
 }
@@ -285,7 +287,7 @@ int bwd(const GatedNormArgs &a, cudaStream_t stream) {
     const int st = mx::launched();
     if (st != GDN_OK) return st;
     const int C = shared ? a.D : a.H * a.D;
-    gated_sum_kernel<<<(C + 31) / 32, 1024, 0, stream>>>(part, a.dw, shared ? c.ctas : c.strips, C);
+    mx::follow(gated_sum_kernel, (C + 31) / 32, 1024, 0, stream, part, a.dw, shared ? c.ctas : c.strips, C);
     return mx::launched();
 }
 

@@ -185,6 +185,22 @@ int resident_ctas() {
     return n;
 }
 
+// A kernel that is launched with `follow` may begin as soon as every CTA of the one
+// before it in the stream has called let_follow(); it calls follow_on() before it
+// reads or writes what that one, or work before that one, writes or reads.
+__device__ __forceinline__ void let_follow() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void follow_on() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+void follow(void (*kernel)(P...), unsigned ctas, int threads, int smem, cudaStream_t stream, const A &...args) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3(ctas), config.blockDim = dim3(threads), config.dynamicSmemBytes = smem, config.stream = stream;
+    config.attrs = &early, config.numAttrs = 1;
+    cudaLaunchKernelEx(&config, kernel, args...);  // a failure is the last error, as that of <<<>>>
+}
+
 inline int launched() {
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
     note_launch();

@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, Shape<N>::CTAS) share_kernel(SsmArgs
     constexpr int CH = Shape<N>::CH, P = Shape<N>::P;
     using Raw = typename Vec<T, CH>::Raw;
     __shared__ __align__(16) float tiles[kWarps][kTile * N];
+    mx::let_follow();
     Place w;
     if (!place_of<N>(a, p, p.chunks - 1, &w)) return;
     const Run r = mx::run_at(a.cu, a.n_seq, a.T, w.row, w.t1 - 1);
@@ -281,6 +282,8 @@ __global__ void __launch_bounds__(32 * Shape<N>::V) join_kernel(SsmArgs a, Plan 
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < a.Di) A = __ldg(reinterpret_cast<const float4 *>(a.A + (size_t)c * N + n));
     const F2 A0 = mul2(pair(A.x, A.y), both(mx::kLog2e)), A1 = mul2(pair(A.z, A.w), both(mx::kLog2e));
+    mx::let_follow();
+    mx::follow_on();
     ulonglong2 *state = reinterpret_cast<ulonglong2 *>(p.state) + i * 32 + lane;
     const float *steps = p.steps + e * 32 + lane;
     F2 h0 = 0, h1 = 0;
@@ -344,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, Shape<N>::CTAS) scan_kernel(SsmArgs 
         bias[e] = a.bias ? __ldg(a.bias + c + e) : 0.f;
         skip[e] = a.D ? __ldg(a.D + c + e) : 0.f;
     }
+    mx::follow_on();
     // sequences without tokens pass their state on
     if (a.cu && a.sf) {
         for (int s0 = w.chunk * 32; s0 < a.n_seq; s0 += p.chunks * 32) {
@@ -479,13 +483,14 @@ int fwd(const SsmArgs &a, cudaStream_t stream) {
         if (st != GDN_OK) return st;
         p.joined = p.chunks >= kJoin;
         if (p.joined) {
-            join_kernel<N><<<(unsigned)((long long)a.B * p.blocks), 32 * Shape<N>::V, 0, stream>>>(a, p);
+            mx::follow(join_kernel<N>, (unsigned)((long long)a.B * p.blocks), 32 * Shape<N>::V, 0, stream, a, p);
             st = mx::launched();
             if (st != GDN_OK) return st;
         }
     }
-    if (a.z) scan_kernel<T, N, true><<<ctas(p.chunks), kThreads, 0, stream>>>(a, p);
-    else scan_kernel<T, N, false><<<ctas(p.chunks), kThreads, 0, stream>>>(a, p);
+    const auto kernel = a.z ? scan_kernel<T, N, true> : scan_kernel<T, N, false>;
+    if (p.chunks > 1) mx::follow(kernel, ctas(p.chunks), kThreads, 0, stream, a, p);
+    else kernel<<<ctas(p.chunks), kThreads, 0, stream>>>(a, p);
     return mx::launched();
 }
 

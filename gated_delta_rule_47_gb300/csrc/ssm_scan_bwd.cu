@@ -315,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 4) share_kernel(SsmArgs a, Plan p) {
     using S = Shape<T, N>;
     extern __shared__ __align__(16) char smem[];
     Mem<T, N> &m = reinterpret_cast<Mem<T, N> *>(smem)[threadIdx.x >> 5];
+    mx::let_follow();
     const Place w = place_of<T, N>(a, p);
     if (w.c0 >= a.Di) return;  // warps do not wait for one another here
     fetch<T, N>(a, w, m, 0, w.t0);
@@ -429,7 +430,9 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
         }
     };
     const int last = w.t0 + (w.t1 - 1 - w.t0) / kBlock * kBlock;
+    mx::let_follow();
     fetch<T, N>(a, w, m, 0, last);
+    mx::follow_on();
     fetch_saved(last + kHalf);
     copies_out();
     Quad A, g, dA;
@@ -714,6 +717,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
 // dskip and dbias from the chunks'.
 template <typename T, int N>
 __global__ void __launch_bounds__(256) sum_kernel(SsmArgs a, Plan p, int tokens_ctas) {
+    mx::follow_on();
     if (blockIdx.x < tokens_ctas) {
         const long long n = (long long)a.B * a.T * (N / 2), i = (long long)blockIdx.x * 256 + threadIdx.x;
         if (i >= n) return;
@@ -816,12 +820,11 @@ int bwd(const SsmArgs &a, cudaStream_t stream) {
     share_kernel<T, N><<<ctas, kThreads, one, stream>>>(a, p);
     int st = mx::launched();
     if (st != GDN_OK) return st;
-    if (a.z) grad_kernel<T, N, true><<<ctas, kThreads, two, stream>>>(a, p);
-    else grad_kernel<T, N, false><<<ctas, kThreads, two, stream>>>(a, p);
+    mx::follow(a.z ? grad_kernel<T, N, true> : grad_kernel<T, N, false>, ctas, kThreads, two, stream, a, p);
     st = mx::launched();
     if (st != GDN_OK) return st;
     const long long tokens = ((long long)a.B * a.T * (N / 2) + 255) / 256, rest = ((long long)a.Di * (N + 2) + 255) / 256;
-    sum_kernel<T, N><<<(unsigned)(tokens + rest), 256, 0, stream>>>(a, p, (int)tokens);
+    mx::follow(sum_kernel<T, N>, (unsigned)(tokens + rest), 256, 0, stream, a, p, (int)tokens);
     return mx::launched();
 }
 
