@@ -5,14 +5,17 @@
 // consecutive channels; B and C of a token are the same for all of them and come
 // from shared memory, where the warp has put a tile of tokens in fp32.  Warps do
 // not wait for one another.  Exponentials bound it from below, one instruction of
-// 32 a clock and SM; as it stands the issue does: 6.7 instructions a token, channel
+// 32 a clock and SM; as it stands the issue does: 6.4 instructions a token, channel
 // and state for a warp's 32 (4.2 in share_kernel), of them one exponential and 2
-// packed multiply-adds, at 58% of the issue slots of 12 warps an SM, which is what
-// the registers allow.  Few rows and channels are cut into chunks of tokens:
-// share_kernel walks each chunk but the last from 0, then every chunk starts from
-// what the chunks before it leave, so that each exponential is taken twice.
-// Measured, bf16, 16 states, gate: 32 x 1024 x 2048 whole 393 us, 1 x 32760 x 2048
-// cut into 57 chunks 517 (exponentials alone 110 and 220), 4 x 4096 x 2048 275.
+// packed multiply-adds, at 59% of the issue slots of 12 warps an SM, which is what
+// the registers allow.  (Channels' states over four lanes, 20 warps an SM: 686 us
+// for 498, by the shared memory through which their steps and sums go.)  Few rows
+// and channels are cut into chunks of tokens: share_kernel walks each chunk but the
+// last from 0, then every chunk starts from what the chunks before it leave, so
+// that each exponential is taken twice.
+// Measured, bf16, 16 states, gate: 32 x 1024 x 2048 whole 387 us, 1 x 32760 x 2048
+// cut into 57 chunks 498 (exponentials alone 110 and 220), 4 x 4096 x 2048 262,
+// 1 x 130 x 2048 12 (9 one after another).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -29,6 +32,7 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTile = 16;  // tokens of B and C in shared memory
 constexpr int kGroup = 4;  // tokens of x, dt and z on their way
 constexpr int kStates = 32, kCtas = 3;
+constexpr long long kResident = 152 * kCtas * kWarps;  // warps
 
 // How a row is cut.
 struct Plan {
@@ -39,13 +43,13 @@ struct Plan {
     bool joined;      // join_kernel has put in `state` what each chunk leaves with all before it
 };
 
-template <int N>
+constexpr int channels_of(int N) { return N >= kStates ? 1 : kStates / N; }  // a thread, where there are many
+
+template <int N, int CH>
 struct Shape {
-    static constexpr int CH = N >= kStates ? 1 : kStates / N;  // channels a thread
     static constexpr int P = N / 2;                            // pairs of states a channel
     static constexpr int V = CH * N / 4;                       // vectors of 4 states a thread
     static constexpr int BLOCK = 32 * CH;                      // channels a warp
-    static constexpr int CTAS = CH * N == 32 ? 3 : kCtas;      // of an SM
 };
 
 // A warp's tile of B (and C): [token][N] fp32, C behind B.
@@ -167,14 +171,14 @@ struct Place {
     int block, chunk, row, c, t0, t1;
     bool there;  // the thread's channels exist
 };
-template <int N>
+template <int N, int CH>
 __device__ __forceinline__ bool place_of(const SsmArgs &a, const Plan &p, int chunks, Place *w) {
     const long long i = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
     const long long item = i / p.blocks;
     w->block = (int)(i - item * p.blocks);
     w->row = (int)(item / chunks), w->chunk = (int)(item - (long long)w->row * chunks);
     if (w->row >= a.B) return false;
-    w->c = w->block * Shape<N>::BLOCK + (threadIdx.x & 31) * Shape<N>::CH;
+    w->c = w->block * Shape<N, CH>::BLOCK + (threadIdx.x & 31) * CH;
     w->there = w->c < a.Di;
     w->t0 = w->chunk * p.len, w->t1 = min(w->t0 + p.len, a.T);
     return true;
@@ -185,14 +189,14 @@ __device__ __forceinline__ size_t share_at(const Plan &p, int row, int chunk, in
 
 // What a chunk leaves: from 0, or from the state of a sequence that starts in it
 // and goes on behind it.
-template <typename T, int N>
-__global__ void __launch_bounds__(kThreads, Shape<N>::CTAS) share_kernel(SsmArgs a, Plan p) {
-    constexpr int CH = Shape<N>::CH, P = Shape<N>::P;
+template <typename T, int N, int CH>
+__global__ void __launch_bounds__(kThreads, kCtas) share_kernel(SsmArgs a, Plan p) {
+    constexpr int P = Shape<N, CH>::P;
     using Raw = typename Vec<T, CH>::Raw;
     __shared__ __align__(16) float tiles[kWarps][kTile * N];
     mx::let_follow();
     Place w;
-    if (!place_of<N>(a, p, p.chunks - 1, &w)) return;
+    if (!place_of<N, CH>(a, p, p.chunks - 1, &w)) return;
     const Run r = mx::run_at(a.cu, a.n_seq, a.T, w.row, w.t1 - 1);
     if (r.s < 0 || r.end <= w.t1) return;  // no sequence goes on behind the chunk
     const int ts = max(w.t0, r.start);
@@ -262,10 +266,10 @@ __global__ void __launch_bounds__(kThreads, Shape<N>::CTAS) share_kernel(SsmArgs
     }
     const size_t at = share_at(p, w.row, w.chunk, w.block);
     const int lane = threadIdx.x & 31;
-    float4 *to = reinterpret_cast<float4 *>(p.state) + at * Shape<N>::V * 32 + lane;
+    float4 *to = reinterpret_cast<float4 *>(p.state) + at * Shape<N, CH>::V * 32 + lane;
     const F2 *hs = &h[0][0];
 #pragma unroll
-    for (int i = 0; i < Shape<N>::V; ++i) *reinterpret_cast<ulonglong2 *>(to + i * 32) = make_ulonglong2(hs[2 * i], hs[2 * i + 1]);
+    for (int i = 0; i < Shape<N, CH>::V; ++i) *reinterpret_cast<ulonglong2 *>(to + i * 32) = make_ulonglong2(hs[2 * i], hs[2 * i + 1]);
 #pragma unroll
     for (int e = 0; e < CH; ++e) p.steps[(at * CH + e) * 32 + lane] = total[e];
 }
@@ -273,12 +277,12 @@ __global__ void __launch_bounds__(kThreads, Shape<N>::CTAS) share_kernel(SsmArgs
 // What the chunks of a row leave, each with those before it of its sequence, in
 // place: a thread 4 of a block's states, the next chunks' loads on their way.  A
 // warp that joins all chunks before its own takes the latency of each.
-template <int N>
-__global__ void __launch_bounds__(32 * Shape<N>::V) join_kernel(SsmArgs a, Plan p) {
-    constexpr int CH = Shape<N>::CH, P = Shape<N>::P, V = Shape<N>::V, AHEAD = 8;
+template <int N, int CH>
+__global__ void __launch_bounds__(32 * Shape<N, CH>::V) join_kernel(SsmArgs a, Plan p) {
+    constexpr int P = Shape<N, CH>::P, V = Shape<N, CH>::V, AHEAD = 8;
     const int row = blockIdx.x / p.blocks, block = blockIdx.x - row * p.blocks;
     const int lane = threadIdx.x & 31, i = threadIdx.x >> 5, e = 2 * i / P, n = 2 * i % P * 2;  // vector i of the lane's
-    const int c = block * Shape<N>::BLOCK + lane * CH + e;
+    const int c = block * Shape<N, CH>::BLOCK + lane * CH + e;
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < a.Di) A = __ldg(reinterpret_cast<const float4 *>(a.A + (size_t)c * N + n));
     const F2 A0 = mul2(pair(A.x, A.y), both(mx::kLog2e)), A1 = mul2(pair(A.z, A.w), both(mx::kLog2e));
@@ -309,13 +313,13 @@ __global__ void __launch_bounds__(32 * Shape<N>::V) join_kernel(SsmArgs a, Plan 
     }
 }
 
-template <typename T, int N, bool GATE>
-__global__ void __launch_bounds__(kThreads, Shape<N>::CTAS) scan_kernel(SsmArgs a, Plan p) {
-    constexpr int CH = Shape<N>::CH, P = Shape<N>::P, V = Shape<N>::V;
+template <typename T, int N, int CH, bool GATE>
+__global__ void __launch_bounds__(kThreads, kCtas) scan_kernel(SsmArgs a, Plan p) {
+    constexpr int P = Shape<N, CH>::P, V = Shape<N, CH>::V;
     using Raw = typename Vec<T, CH>::Raw;
     __shared__ __align__(16) float tiles[kWarps][kTile * 2 * N];
     Place w;
-    if (!place_of<N>(a, p, p.chunks, &w)) return;
+    if (!place_of<N, CH>(a, p, p.chunks, &w)) return;
     const bool soft = a.flags & GDN_DT_SOFTPLUS;
     const int lane = threadIdx.x & 31;
     float *tile = tiles[threadIdx.x >> 5];
@@ -457,41 +461,67 @@ __global__ void __launch_bounds__(kThreads, Shape<N>::CTAS) scan_kernel(SsmArgs 
 // as long as walking one more token (40 channels of 18531 tokens: 442 us in 1158
 // chunks, 98 in 129).
 constexpr int kJoin = 16;  // from so many chunks of a row on they are joined by a launch of its own
-template <int N>
+template <int N, int CH>
 Plan plan(int B, int T, int Di) {
     Plan p{};
-    p.blocks = (Di + Shape<N>::BLOCK - 1) / Shape<N>::BLOCK;
-    const long long whole = (long long)B * p.blocks, resident = 152 * Shape<N>::CTAS * kWarps;
-    const long long chunks = whole * 2 >= resident ? 1 : resident / whole;
+    p.blocks = (Di + Shape<N, CH>::BLOCK - 1) / Shape<N, CH>::BLOCK;
+    const long long whole = (long long)B * p.blocks;
+    const long long chunks = whole * 2 >= kResident ? 1 : kResident / whole;
     const long long len = std::max((T + chunks - 1) / chunks, (long long)std::sqrt((double)T));
     p.len = (int)((len + kTile - 1) / kTile * kTile);
     p.chunks = (T + p.len - 1) / p.len;
     return p;
 }
-Plan plan_of(int B, int T, int Di, int N) { return N == 8 ? plan<8>(B, T, Di) : N == 16 ? plan<16>(B, T, Di) : plan<32>(B, T, Di); }
+// A call that does not fill the SMs takes as long as a warp's tokens, which half as
+// many channels a warp shorten: up to seven eighths of the warps that fit, if so
+// many more fit at once.  Full, it is slower by what B and C from shared memory
+// cost.  Measured, bf16, 2048 channels of 16 states, one channel a thread against
+// two: 130 tokens 9.0 and 13.6 us, 500 17.0 and 20.3, 2048 45.7 and 52.6, 4096 (full)
+// 82.9 and 79.9; 32 rows of 1024 (2048 warps where 1824 fit) 455 and 385.
+template <int N>
+bool thin(int B, int T, int Di) {
+    constexpr int CH = channels_of(N), HALF = CH > 1 ? CH / 2 : 1;
+    const Plan p = plan<N, CH>(B, T, Di), q = plan<N, HALF>(B, T, Di);
+    return CH > 1 && (long long)B * p.chunks * p.blocks * 8 <= 7 * kResident && (long long)B * q.chunks * q.blocks <= kResident;
+}
+template <int N, int CH>
+size_t shares(int B, int T, int Di) {
+    const Plan p = plan<N, CH>(B, T, Di);
+    return p.chunks == 1 ? 0 : (size_t)B * p.chunks * p.blocks * 32 * CH * (N + 1) * sizeof(float);
+}
+template <int N>
+size_t workspace(int B, int T, int Di) {
+    constexpr int CH = channels_of(N), HALF = CH > 1 ? CH / 2 : 1;
+    return thin<N>(B, T, Di) ? shares<N, HALF>(B, T, Di) : shares<N, CH>(B, T, Di);
+}
 
-template <typename T, int N>
-int fwd(const SsmArgs &a, cudaStream_t stream) {
-    Plan p = plan<N>(a.B, a.T, a.Di);
-    const size_t shares = (size_t)a.B * p.chunks * p.blocks;
+template <typename T, int N, int CH>
+int fwd_with(const SsmArgs &a, cudaStream_t stream) {
+    Plan p = plan<N, CH>(a.B, a.T, a.Di);
+    const size_t n = (size_t)a.B * p.chunks * p.blocks;
     p.state = static_cast<float *>(a.ws);
-    p.steps = p.state + shares * 128 * Shape<N>::V;
+    p.steps = p.state + n * 128 * Shape<N, CH>::V;
     auto ctas = [&](int chunks) { return (unsigned)(((long long)a.B * chunks * p.blocks + kWarps - 1) / kWarps); };
     if (p.chunks > 1) {
-        share_kernel<T, N><<<ctas(p.chunks - 1), kThreads, 0, stream>>>(a, p);
+        share_kernel<T, N, CH><<<ctas(p.chunks - 1), kThreads, 0, stream>>>(a, p);
         int st = mx::launched();
         if (st != GDN_OK) return st;
         p.joined = p.chunks >= kJoin;
         if (p.joined) {
-            mx::follow(join_kernel<N>, (unsigned)((long long)a.B * p.blocks), 32 * Shape<N>::V, 0, stream, a, p);
+            mx::follow(join_kernel<N, CH>, (unsigned)((long long)a.B * p.blocks), 32 * Shape<N, CH>::V, 0, stream, a, p);
             st = mx::launched();
             if (st != GDN_OK) return st;
         }
     }
-    const auto kernel = a.z ? scan_kernel<T, N, true> : scan_kernel<T, N, false>;
+    const auto kernel = a.z ? scan_kernel<T, N, CH, true> : scan_kernel<T, N, CH, false>;
     if (p.chunks > 1) mx::follow(kernel, ctas(p.chunks), kThreads, 0, stream, a, p);
     else kernel<<<ctas(p.chunks), kThreads, 0, stream>>>(a, p);
     return mx::launched();
+}
+template <typename T, int N>
+int fwd(const SsmArgs &a, cudaStream_t stream) {
+    constexpr int CH = channels_of(N), HALF = CH > 1 ? CH / 2 : 1;
+    return thin<N>(a.B, a.T, a.Di) ? fwd_with<T, N, HALF>(a, stream) : fwd_with<T, N, CH>(a, stream);
 }
 
 // One token a row: eight states a thread, the N/8 threads of a channel together,
@@ -613,10 +643,7 @@ int step(const SsmStepArgs &a, cudaStream_t stream) {
 }  // namespace
 
 size_t ssm_fwd_workspace(int B, int T, int Di, int N, int) {
-    const Plan p = plan_of(B, T, Di, N);
-    if (p.chunks == 1) return 0;
-    const int ch = N == 8 ? Shape<8>::CH : N == 16 ? Shape<16>::CH : Shape<32>::CH;
-    return (size_t)B * p.chunks * p.blocks * 32 * ch * (N + 1) * sizeof(float);
+    return N == 8 ? workspace<8>(B, T, Di) : N == 16 ? workspace<16>(B, T, Di) : workspace<32>(B, T, Di);
 }
 
 int launch_ssm_fwd(const SsmArgs &a, cudaStream_t stream) {

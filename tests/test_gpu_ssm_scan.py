@@ -144,6 +144,18 @@ def test_slices_of_projections(dtype):
     assert torch.equal(y, forward(d)[0]) and float(room[..., :32].min()) == 7.0 and float(room[..., 80:].max()) == 7.0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,Di,N", [(64, 16, 2048, 16), (28, 64, 2040, 16), (3, 608, 2048, 16), (56, 40, 2040, 8), (30, 17, 1000, 32)])
+def test_full_machine(B, T, Di, N, dtype):
+    """Rows and channels that fill the SMs: whole rows, rows of two chunks, of more chunks than are joined in place."""
+    d = inputs(B, T, Di, N, dtype, T)
+    wide = {n: ref.wide(d[n]) for n in NAMES}
+    want, last = ref.scan(*wide.values())
+    y, state = forward(d)
+    close(y, want, dtype, max(1e-4, T * 2.0 ** -22))
+    close(state, last, "f32", max(1e-4, T * 2.0 ** -22))
+
+
 @pytest.mark.parametrize("B,T,Di", [(1, 5000, 64), (2, 1500, 256), (20, 300, 2048)])
 def test_long_rows(B, T, Di):
     """Cut rows against the same rows in parts: states carry on, and so do their gradients."""
