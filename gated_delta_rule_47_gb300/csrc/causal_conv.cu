@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 3) conv_kernel(ConvArgs a, int len, 
 // A strip goes on for the W-1 tokens behind it, whose dz its last dx need; dw and
 // db count its own.  part: [strips][W+1][C].  Tokens go in groups as forwards: the
 // conditions of a strip's and a run's ends took three times the arithmetic's
-// instructions.  Measured, bf16, W 4, SiLU: 4 x 4096 x 6144 123 us (604 MB at 4.9
+// instructions.  Measured, bf16, W 4, SiLU: 4 x 4096 x 6144 121 us (604 MB at 5.0
 // TB/s; 278 with the conditions at every token, 129 with four tokens on their way).
 template <typename T, int N, int W>
 __global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ConvArgs a, int len, int per_row, float *part) {

@@ -16,10 +16,12 @@
 // state); states every 4 tokens take Di N bytes a token, written and read once behind
 // the arithmetic.  Every 8 took half of that and 7% longer: 64 registers more, of
 // which some went through memory, and twice the code to fetch.
-// Measured, bf16, 4 x 4096 x 2048 x 16 with a gate: 897 us, of them share_kernel
-// 235 and grad_kernel about 640.  Instructions bound it, not bytes (0.47 GB and 1.07
+// Measured, bf16, 4 x 4096 x 2048 x 16 with a gate: 879 us, of them share_kernel
+// 235 and grad_kernel about 630.  Instructions bound it, not bytes (0.47 GB and 1.07
 // of states, 230 us): 21 for a warp's 32 tokens x channels x states in grad_kernel,
-// at 41% of the issue slots, as its states in registers leave room for 8 warps an SM.
+// at 43% of the issue slots of 8 warps an SM, which is what shared memory leaves room
+// for.  (12 warps, with 168 registers and one block of 4 tokens at a time, spilled and
+// waited for its loads: 1,104 us.)
 //
 // A thread holds 4 channels x 4 states, as pairs of channels: what belongs to a
 // channel is loaded as a pair, and B and C lie in shared memory twice over.  The

@@ -754,7 +754,7 @@ int ssm_scan_fwd(const void *x, const void *dt, const float *A, const void *Bt, 
  *           wanted); dinitial_state [n_seq,Di,N] fp32 or NULL
  *   strides 12: (batch, token) of x, dt, Bt, Ct, z, dy
  * Tokens of no sequence get zeros.  Every sum has a fixed order.  The workspace
- * holds a state every 8 tokens: Di N / 2 bytes a token.
+ * holds a state every 4 tokens: Di N bytes a token.
  */
 size_t ssm_scan_bwd_workspace_bytes(int B, int T, int Di, int N, int dtype);
 int ssm_scan_bwd(const void *x, const void *dt, const float *A, const void *Bt, const void *Ct, const float *skip,
