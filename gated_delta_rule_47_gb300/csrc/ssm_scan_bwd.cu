@@ -52,14 +52,18 @@ struct Shape {
     static constexpr int L = N / 4;       // lanes of a channel's states
     static constexpr int G = 32 / L;      // lanes of the channels
     static constexpr int CH = 4 * G;      // channels a warp
-    static constexpr int ROW = CH + 4;    // of them in shared memory: the lanes of a quarter warp, 32 bytes each of two tokens, meet in no bank
     static constexpr int V = kWide<T>;
+    // a token's channels in shared memory: lanes of 32 bytes, of two tokens in a quarter warp, meet in no bank
+    static constexpr int ROW = CH + (V == 8 ? 4 : 0);
     static constexpr int RV = CH / V;     // vectors of a token's channels
     static constexpr int NV = kBlock * RV, VPL = (NV + 31) / 32;  // of a block; of a lane
     static constexpr int BV = N / V;      // vectors of a token's B
     // dB's and dC's halves trade places in rows that would meet in a bank
     static __device__ __forceinline__ int swap(int g) { return N == 16 ? (g & 1) * 16 : N == 8 ? (g >> 1 & 1) * 8 : 0; }
-    static constexpr int SLOTS = N == 16 ? 4 : 2;  // tokens whose dB and dC are summed over channels at once
+    // tokens that are summed at once over the states' lanes, and over the channels' (dB and dC): of fp32 rows fewer, so
+    // that two CTAs fit on an SM (2 x 4096 x 2048 x 16 647 -> 518 us, 1999 x 512 59 -> 62)
+    static constexpr int TOK = sizeof(T) == 2 ? 2 : 1;
+    static constexpr int SLOTS = sizeof(T) == 2 && N == 16 ? 4 : 2;
     static constexpr int NB = kBlock * BV, BPL = (2 * NB + 31) / 32;
 };
 
@@ -90,7 +94,7 @@ struct GradMem : Mem<T, N> {
     float4 saved[5][32];                      // a half block's state and steps, as the lanes take them
     float4 start[4][32];                      // the state that enters the chunk
     float part[2][kBlock][2 * N];             // a block's dB and dC of this warp
-    float over_states[2][3][S::L][S::CH + 8]; // two tokens' D's and x's gradients and y, of each lane of a channel
+    float over_states[S::TOK][3][S::L][S::CH + 8];  // some tokens' D's and x's gradients and y, of each lane of a channel
     float over_channels[S::SLOTS][S::G][2 * N];  // some tokens' dB and dC, of each lane of the channels; swizzled
     float4 acc[2][S::VPL * S::V / 4][32];     // dskip and dbias of each lane's vectors
 };
@@ -594,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
                         token(hs[u]);
                     }
                     auto put = [&](int what, const F2 (&v)[2]) {
-                        *reinterpret_cast<ulonglong2 *>(&m.over_states[u & 1][what][w.q][4 * w.g]) = make_ulonglong2(v[0], v[1]);
+                        *reinterpret_cast<ulonglong2 *>(&m.over_states[u % S::TOK][what][w.q][4 * w.g]) = make_ulonglong2(v[0], v[1]);
                     };
                     put(0, ds);
                     put(1, dx);
@@ -602,14 +606,15 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
                     float *row = m.over_channels[u % S::SLOTS][w.g];
                     *reinterpret_cast<float4 *>(row + (4 * w.q ^ S::swap(w.g))) = make_float4(sum(dB[0]), sum(dB[1]), sum(dB[2]), sum(dB[3]));
                     *reinterpret_cast<float4 *>(row + (N + 4 * w.q ^ S::swap(w.g))) = make_float4(sum(dC[0]), sum(dC[1]), sum(dC[2]), sum(dC[3]));
-                    if ((u & 1) != 0) continue;
+                    if (u % S::TOK != 0) continue;
                     __syncwarp();
-                    constexpr int kinds = GATE ? 3 : 2;  // over step, x and dy of the two tokens, which all lanes have read
+                    // over step, x and dy of the tokens, which all lanes have read
+                    constexpr int each = S::TOK * S::CH / 4, items = (GATE ? 3 : 2) * each;
 #pragma unroll
-                    for (int i0 = 0; i0 < kinds * S::CH / 2; i0 += 32) {
+                    for (int i0 = 0; i0 < items; i0 += 32) {
                         const int i = i0 + lane;
-                        if (i >= kinds * S::CH / 2) break;
-                        const int what = i / (S::CH / 2), tok = i % (S::CH / 2) / (S::CH / 4), c4 = i % (S::CH / 4) * 4;
+                        if (i >= items) break;
+                        const int what = i / each, tok = i % each / (S::CH / 4), c4 = i % (S::CH / 4) * 4;
                         F2 p0 = 0, p1 = 0;
 #pragma unroll
                         for (int q = 0; q < S::L; ++q) {
