@@ -148,6 +148,29 @@ def test_many_chunks_and_what_a_workspace_held():
                     assert float((last[0] - a[1][i]).abs().max()) <= 9000 * 2.0 ** -22 * float(a[1].abs().max())
 
 
+@pytest.mark.parametrize("T,Di", [(130, 256), (700, 2048)])
+def test_calls_feed_one_another(T, Di):
+    """Each call reads what the one before it wrote, in the same workspace and without a wait of the host in between: a
+    call's kernels, which begin while the one before ends, wait for what they read."""
+    def walk(wait):
+        s = scan_inputs(1, T, Di, 16, "f32", 4)
+        kept = []
+        for _ in range(12):
+            y, last = forward(s)
+            if wait:
+                torch.cuda.synchronize()
+            s = dict(s, x=y, s0=last)
+            got = backward(s)
+            if wait:
+                torch.cuda.synchronize()
+            s = dict(s, x=y / y.abs().amax(), dy=got["x"] / got["x"].abs().amax().clamp_min(1e-30))
+            kept += [y, last, *got.values()]
+        torch.cuda.synchronize()
+        return kept
+    for a, b in zip(walk(True), walk(False)):
+        assert torch.equal(a, b)
+
+
 def test_many_sequences():
     """Thousands of short and empty sequences in one row."""
     gen = torch.Generator().manual_seed(1)
