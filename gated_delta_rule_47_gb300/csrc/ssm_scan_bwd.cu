@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
             }
             if (t + half > w.t0) fetch_saved(t + half - kHalf);
             copies_out();
-            // the half block, with or without sequences that start or end in it
+            // the half block, with or without sequences that start or end in it or tokens of none
             auto block = [&](auto marked) {
                 constexpr bool MARKED = decltype(marked)::value;  // few blocks: their states go through local memory
                 constexpr int UNROLL = MARKED ? 1 : kHalf;
@@ -542,6 +542,10 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
 #pragma unroll UNROLL
                 for (int u = 0; u < kHalf; ++u) {
                     const int v = half + u;
+                    if (MARKED && (k.dead >> v & 1)) {  // no state of a sequence before it passes here: it may be infinite
+                        zero16(hs[u + 1]);
+                        continue;
+                    }
                     F2 d[2], x[2], b[4];
                     channels(&m.step[v][4 * w.g], d);
                     channels(&m.x[v][4 * w.g], x);
@@ -588,7 +592,12 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
                             y[i] = cy;
                         }
                     };
-                    if (MARKED && (k.starts >> v & 1)) {  // what came before is the sequence's initial state
+                    if (MARKED && (k.dead >> v & 1)) {
+                        zero16(g);
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) dB[n] = dC[n] = 0;
+                        dx[0] = dx[1] = ds[0] = ds[1] = y[0] = y[1] = 0;
+                    } else if (MARKED && (k.starts >> v & 1)) {  // what came before is the sequence's initial state
                         Quad first;
                         load16<N>(a, w, a.s0 ? a.s0 + m.seq[v] * page : nullptr, first);
                         token(first);
@@ -638,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(SsmArgs a, Plan p) {
                     __syncwarp();
                 }
             };
-            if (k.starts | k.ends) block(std::true_type{});
+            if (k.starts | k.ends | k.dead) block(std::true_type{});
             else block(std::false_type{});
         }
         __syncwarp();
