@@ -243,8 +243,8 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 2 : 1) gated_bwd_kernel(Gat
     }
 }
 
-__global__ void __launch_bounds__(1024) gated_sum_kernel(const float *part, float *out, int n, int C) {
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31);
+__global__ void __launch_bounds__(1024) gated_sum_kernel(const float *part, float *out, int n, long long C) {
+    const long long c = (long long)blockIdx.x * 32 + (threadIdx.x & 31);
     mx::follow_on();
     const float x = mx::column_sum<32>(part, n, C, c);
     if (threadIdx.x < 32 && c < C) out[c] = x;
@@ -286,8 +286,8 @@ int bwd(const GatedNormArgs &a, cudaStream_t stream) {
     gated_bwd_kernel<T, NT, V, FIRST><<<c.ctas, kThreads, room, stream>>>(a, c.strips, part);
     const int st = mx::launched();
     if (st != GDN_OK) return st;
-    const int C = shared ? a.D : a.H * a.D;
-    mx::follow(gated_sum_kernel, (C + 31) / 32, 1024, 0, stream, part, a.dw, shared ? c.ctas : c.strips, C);
+    const long long C = shared ? a.D : (long long)a.H * a.D;  // up to 2^31 - 1
+    mx::follow(gated_sum_kernel, (unsigned)((C + 31) / 32), 1024, 0, stream, part, a.dw, shared ? c.ctas : c.strips, C);
     return mx::launched();
 }
 
