@@ -53,6 +53,7 @@
 #include <mutex>
 
 #include "gdn_internal.h"
+#include "ring_tag.h"
 #include "tc_util.cuh"
 
 namespace gdn {
@@ -184,9 +185,9 @@ struct TcParams {
     // c % kRing of the head's ring in global memory instead of a cluster copy.
     int flat;
     uint8_t *ring;                // [BH][kRing] slots of kShipBytes
-    unsigned long long *ready;    // [BH][kRing] x 16 B: epoch << 32 | (chunk + 1) of the slot's contents
-    unsigned long long *cons;     // [BH]: epoch << 32 | chunks the scan CTA has taken out of its ring
-    unsigned epoch;               // tag of this launch, never 0
+    unsigned long long *ready;    // [BH][kRing] x 16 B: key + chunk + 1 of the slot's contents
+    unsigned long long *cons;     // [BH]: key + chunks the scan CTA has taken out of its ring
+    unsigned long long key;       // of this launch (ring_tag.h)
 };
 
 constexpr unsigned long long kCleanupNs = 200000000ull;  // 0.2 s for draining on the way out
@@ -211,22 +212,22 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, unsigne
 }
 
 // Bounded wait, like wait_bar, until *flag (written by another CTA with a
-// release store) holds this launch's epoch in its high word and at least
-// `need` in its low word.  Gives up early once any CTA has reported an error.
-__device__ __forceinline__ bool wait_tag(const unsigned long long *flag, unsigned epoch, unsigned need,
+// release store) holds this launch's key plus a count of least .. most.  Gives
+// up early once any CTA has reported an error.
+__device__ __forceinline__ bool wait_tag(const unsigned long long *flag, unsigned long long key, unsigned least, unsigned most,
                                          unsigned long long timeout_ns, volatile int *abort_flag, unsigned code,
                                          unsigned *seen = nullptr) {
     unsigned long long v = ld_acquire_gpu(flag);
-    if ((unsigned)(v >> 32) == epoch && (unsigned)v >= need) {
-        if (seen) *seen = (unsigned)v;
+    if (ring_word_in(v, key + least, key + most)) {
+        if (seen) *seen = (unsigned)(v - key);
         return true;
     }
     const uint64_t t0 = global_timer_ns();
     while (true) {
         __nanosleep(100);
         v = ld_acquire_gpu(flag);
-        if ((unsigned)(v >> 32) == epoch && (unsigned)v >= need) {
-            if (seen) *seen = (unsigned)v;
+        if (ring_word_in(v, key + least, key + most)) {
+            if (seen) *seen = (unsigned)(v - key);
             return true;
         }
         if (*abort_flag || *reinterpret_cast<volatile unsigned *>(&g_tc_error) != 0u) {
@@ -447,14 +448,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // once its WY pipeline has published it (checked ahead, while the
                 // slot is still in use) and the receive slot is free, then report
                 // the chunks taken out so that their ring slots can be refilled
-                const unsigned long long tagc = (unsigned long long)p.epoch << 32;
                 int armed[2] = {0, 0};
                 int c = 0;
                 for (; c < NT; ++c) {
                     const int b = c & 1;
                     const size_t slot = (size_t)bh * kRing + c % kRing;
                     GDN_TR(c, 11);
-                    if (!wait_tag(p.ready + 2 * slot, p.epoch, (unsigned)(c + 1), tmo, abort_flag, 256u)) break;
+                    if (!wait_tag(p.ready + 2 * slot, p.key, c + 1, c + 1, tmo, abort_flag, 256u)) break;
                     GDN_TR(c, 12);
                     fence_proxy_async_global();
                     if (c >= 2 && !wait_bar(&bars[SB_SLOT_DONE0 + b], ((c - 2) >> 1) & 1, tmo, abort_flag, 16u)) break;
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive_expect_tx(&bars[SB_RECV0 + b], kShipBytes);
                     bulk_load_global(sm + S_RECV0 + b * RS, p.ring + slot * kShipBytes, kShipBytes, &bars[SB_RECV0 + b]);
                     armed[b]++;
-                    if (c >= 2) st_release_gpu(p.cons + bh, tagc | (unsigned)(c - 1));  // chunks 0 .. c-2 are out
+                    if (c >= 2) st_release_gpu(p.cons + bh, p.key + (unsigned)(c - 1));  // chunks 0 .. c-2 are out
                 }
                 for (int b = 0; b < 2; ++b)
                     if (armed[b]) mbar_wait(&bars[SB_RECV0 + b], (armed[b] - 1) & 1, kCleanupNs);
@@ -470,8 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // Every chunk of this head has been published and taken out, so
                     // nothing reads or writes its tags again in this launch: zero
                     // them, so that the next launch on this workspace starts from
-                    // clean tags even when it carries the same epoch (a replayed
-                    // CUDA graph freezes the epoch it was captured with).
+                    // clean tags even when it carries the same key (a replayed
+                    // CUDA graph freezes the key it was captured with).
                     for (int s = 0; s < kRing; ++s) p.ready[2 * ((size_t)bh * kRing + s)] = 0ull;
                     p.cons[bh] = 0ull;
                 }
@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (pend >= 0) {
                     tma_store_wait_all<0>();  // the slot's bytes are written
                     fence_proxy_async_global();
-                    st_release_gpu(p.ready + 2 * pend, ((unsigned long long)p.epoch << 32) | (unsigned)pend_tag);
+                    st_release_gpu(p.ready + 2 * pend, p.key + (unsigned)pend_tag);
                     pend = -1;
                 }
             };
@@ -1202,7 +1202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const unsigned need = (unsigned)(c - kRing + 1);
                     if (c >= kRing && ms->ccache[ibh] < need) {
                         unsigned seen = 0;
-                        ship_ok = wait_tag(p.cons + ibh, p.epoch, need, tmo, abort_flag, 512u, &seen);
+                        ship_ok = wait_tag(p.cons + ibh, p.key, need, (unsigned)p.NT, tmo, abort_flag, 512u, &seen);
                         if (ship_ok) ms->ccache[ibh] = seen;
                     }
                     GDN_TR(c, 47 + 16 * g);
@@ -1380,13 +1380,14 @@ constexpr size_t ring_bytes(int BH) {
 // Scratch of the allocation-free entry point: the ring of up to kNoAllocHeads
 // heads (13.1 MB on every GPU that loads the library, until the process
 // exits).  It is zero when the module loads and is never cleared: each tag in
-// it carries the launch that wrote it, so one call's leftovers are never read
-// as another's.
+// it carries the key of the launch that wrote it (ring_tag.h), so one call's
+// leftovers are not read as another's, but for those of a call that gave up and
+// was captured in a graph whose replay carries the same key.
 constexpr int kNoAllocHeads = 64;
 constexpr size_t kNoAllocBytes = ring_bytes(kNoAllocHeads);
 static __device__ __align__(256) uint8_t g_noalloc_scratch[kNoAllocBytes];
 
-std::atomic<unsigned> g_epoch{0};
+std::atomic<unsigned long long> g_launches{0};
 
 // Launches the ring mode if it applies (no forced cluster shape, few enough
 // heads, a 16-byte aligned workspace of ring_bytes); returns -1 if it does not.
@@ -1414,9 +1415,7 @@ int launch_ring(const ScanArgs &a, TcParams p, const CUtensorMap &mK, const CUte
     p.ring = ws;
     p.ready = reinterpret_cast<unsigned long long *>(ws + (size_t)BH * kRing * kShipBytes);
     p.cons = p.ready + (size_t)BH * kRing * 2;
-    // From 0xffc00000 on, short of 0xffffffff: what a workspace held before (small
-    // whole numbers such as offsets, values, bytes of one kind) has no such words.
-    p.epoch = 0xffc00000u + (++g_epoch) % 0x3fffffu;
+    p.key = ring_key(++g_launches);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3((unsigned)(BH + nwy));
@@ -1457,7 +1456,7 @@ int launch_r(const ScanArgs &a, cudaStream_t stream) {
     p.flat = 0;
     p.ring = nullptr;
     p.ready = p.cons = nullptr;
-    p.epoch = 0;
+    p.key = 0;
     auto kern = gdn_tc_kernel<R>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) != cudaSuccess ||
         cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)

@@ -112,9 +112,10 @@ size_t gdn_chunk_fwd_workspace_bytes(int B, int H, int T, int r, int Dk, int Dv,
  *           contents need no initialisation and are not meaningful after
  *           the call; calls that may overlap on the GPU need separate
  *           workspaces.  A call that completes leaves the ring's tags zeroed,
- *           so a workspace may be reused by launches that carry the same tag
- *           epoch (replays of one captured CUDA graph); after a call that
- *           ended in GDN_ERR_TIMEOUT, zero the workspace before such reuse.
+ *           so a workspace may be reused by launches that carry the same key
+ *           in their tags (replays of one captured CUDA graph); after a replay
+ *           that ended in GDN_ERR_TIMEOUT, zero the workspace before the next.
+ *           Other launches need no such clearing: their keys differ.
  *           A smaller workspace is GDN_ERR_WORKSPACE; one that is not
  *           16-byte aligned makes the call run without the ring.
  * T = 0 or B*H = 0 is valid and enqueues nothing (final_state, if given,
@@ -146,6 +147,8 @@ int gdn_chunk_fwd(const void *q, const void *k, const void *v, const void *beta,
  * capture.  All calls share the one array, which keeps the last call's
  * contents; nothing in it has to start at zero (every tag it holds names the
  * launch that wrote it, and a call that completes zeroes the tags it used).
+ * A graph whose replay of this call ended in GDN_ERR_TIMEOUT is captured anew
+ * before it runs again: a replay carries the tags of the one before.
  * Two calls that overlap on the GPU, on different streams, race on it:
  * serialise them.
  */
