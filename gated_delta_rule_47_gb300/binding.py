@@ -1355,7 +1355,7 @@ def ssm_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, initial_state
     [sequences,Di,N] fp32.  Returns (dx, ddt, dA, dB, dC, dD, dz, ddt_bias,
     dinitial_state), contiguous: those of tensors in their type, dA, dD, ddt_bias and
     dinitial_state in fp32; None for inputs that are not given.  The workspace, if
-    not given, takes Di N / 2 bytes a token and more."""
+    not given, takes Di N bytes a token and more."""
     if workspace is None and stream is None:
         r = (_front or _quick()).scan_back(x, dt, A, B, C, dy, D, z, dt_bias, initial_state, dfinal_state, cu_seqlens, softplus)
         if r is not NotImplemented:
