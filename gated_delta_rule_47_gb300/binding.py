@@ -18,6 +18,7 @@ import ctypes
 import functools
 import importlib.machinery
 import importlib.util
+import math
 import os
 import threading
 
@@ -1161,11 +1162,19 @@ def _written(t, name, shape, dtype):
         raise ValueError(f"{name}'s elements share memory")
 
 
+def _side_by_side(a, b):
+    """Whether the rows of a and b (their last dimensions) are columns of one buffer's
+    rows: all begin at one of two places in what their strides are multiples of."""
+    every = math.gcd(*(s * t.element_size() for t in (a, b) for n, s in zip(t.shape[:-1], t.stride()) if n > 1))
+    wide = lambda t: t.shape[-1] * t.element_size()  # noqa: E731
+    return every > 0 and wide(a) <= (b.data_ptr() - a.data_ptr()) % every <= every - wide(b)
+
+
 def _apart(a, b, names):
     """A call reads b after it has begun to write a: they may not share memory."""
     if a is not None and b is not None and a.numel() and b.numel():
         span = lambda t: t.data_ptr() + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()  # noqa: E731
-        if a.data_ptr() < span(b) and b.data_ptr() < span(a):
+        if a.data_ptr() < span(b) and b.data_ptr() < span(a) and not _side_by_side(a, b):
             raise ValueError(f"{names} share memory")
 
 
