@@ -1210,6 +1210,7 @@ def causal_conv_fwd(x, weight, bias=None, initial_window=None, output_final_wind
         else:
             _written(y, "y", (B, T, C), x.dtype)
             _apart(y, x, "x and y")
+            _apart(y, initial_window, "initial_window and y")
         win = torch.empty(n_seq, W - 1, C, dtype=x.dtype, device=x.device) if output_final_window else None
         st = load().causal_conv_fwd(x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(initial_window), y.data_ptr(),
                                     _addr(win), _addr(cu_seqlens), _pitches(x, y), n_seq, B, T, C, W,
@@ -1298,7 +1299,8 @@ def causal_conv_step(x, weight, window, bias=None, slots=None, window_out=None, 
             y = torch.empty(B, C, dtype=x.dtype, device=x.device)
         else:
             _dense(y, "y", (B, C), x.dtype)
-            _apart(y, x, "x and y")
+            for t, name in ((x, "x"), (window, "window"), (window_out, "window_out")):
+                _apart(y, t, f"{name} and y")
         st = load().causal_conv_step(x.data_ptr(), weight.data_ptr(), _addr(bias), window.data_ptr(), window_out.data_ptr(),
                                      _addr(slots), y.data_ptr(), step, B, C, W, n, GDN_SILU if silu else 0, code,
                                      _at(stream, x))
@@ -1343,7 +1345,7 @@ def ssm_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, initial_state=Non
             y = torch.empty(rows, T, Di, dtype=x.dtype, device=x.device)
         else:
             _written(y, "y", (rows, T, Di), x.dtype)
-            for t, name in ((x, "x"), (dt, "dt"), (B, "B"), (C, "C"), (z, "z")):
+            for t, name in ((x, "x"), (dt, "dt"), (B, "B"), (C, "C"), (z, "z"), (initial_state, "initial_state")):
                 _apart(y, t, f"{name} and y")
         sf = torch.empty(n_seq, Di, N, dtype=torch.float32, device=x.device) if output_final_state else None
         if workspace is None:
@@ -1431,7 +1433,7 @@ def ssm_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, slots=None, st
             y = torch.empty(rows, Di, dtype=dtype, device=x.device)
         else:
             _dense(y, "y", (rows, Di), dtype)
-            for t, name in ((x, "x"), (dt, "dt"), (B, "B"), (C, "C"), (z, "z")):
+            for t, name in ((x, "x"), (dt, "dt"), (B, "B"), (C, "C"), (z, "z"), (state, "state"), (state_out, "state_out")):
                 _apart(y, t, f"{name} and y")
         st = load().ssm_step(x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _addr(D), _addr(z),
                              _addr(dt_bias), state.data_ptr(), state_out.data_ptr(), _addr(slots), y.data_ptr(),

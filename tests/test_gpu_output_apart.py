@@ -34,3 +34,20 @@ def test_columns_of_one_buffer():
     x, y = beside(s["x"], 64)
     got = forward(dict(s, x=x), y=y)
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(x, s["x"])
+
+
+def test_over_what_is_read():
+    d = conv_inputs(2, 3, 64, 4, "bf16", 1)
+    refused = lambda: pytest.raises(ValueError, match="share memory")  # noqa: E731
+    with refused():
+        binding.causal_conv_fwd(d["x"], d["w"], initial_window=d["win"], y=d["win"])
+    for w, out in ((d["win"], None), (d["dwin"], d["win"])):
+        with refused():
+            binding.causal_conv_step(d["x"][:, 0], d["w"], w, window_out=out, y=d["win"].view(6, 64)[2:4])
+    s = scan_inputs(2, 16, 64, 16, "f32", 2)
+    with refused():
+        forward(s, y=s["s0"].view(2, 16, 64))
+    row = [s["x"][:, 0], s["dt"][:, 0], s["A"], s["B"][:, 0], s["C"][:, 0]]
+    for state, out in ((s["s0"], None), (s["dsf"], s["s0"])):
+        with refused():
+            binding.ssm_step(*row, state, state_out=out, y=s["s0"].view(32, 64)[3:5])
