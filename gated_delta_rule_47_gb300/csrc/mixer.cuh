@@ -188,7 +188,7 @@ int resident_ctas() {
 // A kernel that is launched with `follow` may begin as soon as every CTA of the one
 // before it in the stream has called let_follow(); it calls follow_on() before it
 // reads or writes what that one, or work before that one, writes or reads.  Measured:
-// 2 us a call of two or three kernels (130 tokens' scan 18.4 to 16.4).
+// 2 us a call of two or three kernels (scan of 1999 x 512 fp32, backward, 61.6 to 59.4).
 __device__ __forceinline__ void let_follow() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void follow_on() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <typename... P, typename... A>

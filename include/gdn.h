@@ -741,7 +741,9 @@ int causal_conv_step(const void *x, const float *weight, const float *bias, cons
  *   workspace of ssm_scan_fwd_workspace_bytes bytes, 16-byte aligned
  * N 8, 16 or 32; Di a multiple of 8 (bf16) or 4 (fp32); n_seq, B up to 65534.
  * States, steps and sums are fp32.  An infinity or NaN stays in its channel and
- * sequence (in B or C: in its sequence).
+ * sequence (in B or C: in its sequence).  Rows are cut into chunks, which the
+ * products of their decays join: where D_t A is positive over so many tokens that
+ * such a product passes fp32's range, results are not finite even if the state is 0.
  */
 size_t ssm_scan_fwd_workspace_bytes(int B, int T, int Di, int N, int dtype);
 int ssm_scan_fwd(const void *x, const void *dt, const float *A, const void *Bt, const void *Ct, const float *skip,
